@@ -4,6 +4,7 @@
 #include <cstring>
 
 #include "../../include/kq.h"
+#include "kq_cache.h"
 #include "kq_internal.h"
 
 namespace kq {
@@ -340,6 +341,163 @@ kq_status kq_moe_ffn(const kq_moe_ffn_weights* w, const int32_t* expert_ids, con
   return cuda_status(e);
 }
 
+static bool cache_dtype(int d) { return d == KQ_BF16 || d == KQ_F8E4M3; }
+static bool float_dtype(int d) { return d == KQ_F32 || d == KQ_BF16; }
+static bool good_scale(float s) { return s > 0.0f && s <= 3.402823466e38f; }
+// a byte stride that is not negative and keeps 16-byte alignment
+static bool stride16(int64_t elements, int size) {
+  return elements >= 0 && elements < (int64_t(1) << 56) && elements * size % 16 == 0;
+}
+
+static kq_status check_cache(const kq_kv_cache* c) {
+  if (!c) return KQ_ERR_ARG;
+  if (!cache_dtype(c->dtype) || c->n_kv_heads <= 0 || c->n_pages < 0 || c->page_size <= 0) return KQ_ERR_ARG;
+  if (!good_scale(c->k_scale) || !good_scale(c->v_scale)) return KQ_ERR_ARG;
+  if (c->page_size > 1024 || (c->page_size & (c->page_size - 1)) || !head_dim_supported(c->head_dim) ||
+      c->n_kv_heads > 65536 || c->n_pages > INT32_MAX)
+    return KQ_ERR_UNSUPPORTED;
+  if (c->n_pages > 0 && (!c->k || !c->v)) return KQ_ERR_ARG;
+  const int es = c->dtype == KQ_BF16 ? 2 : 1;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !stride16(c->page_stride, es) || !stride16(c->slot_stride, es) ||
+      !stride16(c->head_stride, es))
+    return KQ_ERR_ALIGN;
+  return KQ_OK;
+}
+
+static int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
+kq_status kq_kv_append(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
+                       const int32_t* seq_lens, int64_t B, int64_t T, const void* q, const void* k, const void* v,
+                       int x_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t n_q_heads,
+                       const kq_rope* rope, void* q_out, int q_out_dtype, kq_stream_t stream) {
+  const kq_status cs = check_cache(cache);
+  if (cs != KQ_OK) return cs;
+  if (!rope || !float_dtype(x_dtype) || !float_dtype(q_out_dtype)) return KQ_ERR_ARG;
+  if (max_pages < 0 || B < 0 || T < 0 || n_q_heads <= 0 || rope->n_positions < 0 || rope->rot_dim < 0) return KQ_ERR_ARG;
+  if (rope->rot_dim % 8 || rope->rot_dim > cache->head_dim) return KQ_ERR_SHAPE;
+  if (B == 0 || T == 0) return KQ_OK;
+  const int64_t heads = int64_t(n_q_heads) + 2 * int64_t(cache->n_kv_heads);
+  if (B > INT32_MAX || T > INT32_MAX || B * T > INT32_MAX / heads) return KQ_ERR_UNSUPPORTED;
+  if (!seq_lens || !q || !k || !v || !q_out || (max_pages > 0 && !page_table) || (rope->rot_dim > 0 && !rope->cos_sin))
+    return KQ_ERR_ARG;
+  const int xs = x_dtype == KQ_BF16 ? 2 : 4;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(page_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(rope->q_norm, 16) || !aligned(rope->k_norm, 16) ||
+      !aligned(rope->cos_sin, 16) || !stride16(q_stride, xs) || !stride16(k_stride, xs) || !stride16(v_stride, xs))
+    return KQ_ERR_ALIGN;
+  AppendArgs a;
+  a.c = *cache;
+  a.rope = *rope;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = q_out;
+  a.B = static_cast<int>(B);
+  a.T = static_cast<int>(T);
+  a.Hq = n_q_heads;
+  a.page_shift = log2_of(cache->page_size);
+  a.err = device_error_ptr();
+  cudaError_t e = launch_kv_append(a, x_dtype == KQ_BF16, q_out_dtype == KQ_BF16, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_status(e);
+}
+
+static kq_status check_attn(const kq_kv_cache* cache, int64_t B, int64_t T, int32_t n_q_heads) {
+  const kq_status cs = check_cache(cache);
+  if (cs != KQ_OK) return cs;
+  if (B < 0 || T < 0 || n_q_heads <= 0 || n_q_heads % cache->n_kv_heads) return KQ_ERR_ARG;
+  if (B > 4096 || T > 16 || n_q_heads / cache->n_kv_heads > 16) return KQ_ERR_UNSUPPORTED;
+  return KQ_OK;
+}
+
+size_t kq_attn_workspace_size(const kq_kv_cache* cache, int64_t B, int64_t T, int32_t n_q_heads) {
+  if (check_attn(cache, B, T, n_q_heads) != KQ_OK) return 0;
+  return attn_workspace_bytes(cache->head_dim, cache->n_kv_heads, B, T, n_q_heads);
+}
+
+kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
+                         const int32_t* seq_lens, int64_t B, int64_t T, const void* q, int q_dtype, int64_t q_stride,
+                         int32_t n_q_heads, float scale, float softcap, int32_t window, void* out, void* workspace,
+                         size_t workspace_bytes, kq_stream_t stream) {
+  const kq_status cs = check_attn(cache, B, T, n_q_heads);
+  if (cs != KQ_OK) return cs;
+  if (!float_dtype(q_dtype) || max_pages < 0 || window < 0 || !(softcap >= 0.0f) || scale != scale) return KQ_ERR_ARG;
+  if (B == 0 || T == 0) return KQ_OK;
+  if (max_pages > INT32_MAX) return KQ_ERR_UNSUPPORTED;
+  if (!seq_lens || !q || !out || (max_pages > 0 && !page_table)) return KQ_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
+      !stride16(q_stride, q_dtype == KQ_BF16 ? 2 : 4))
+    return KQ_ERR_ALIGN;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < attn_workspace_bytes(cache->head_dim, cache->n_kv_heads, B, T, n_q_heads))
+    return KQ_ERR_WORKSPACE;
+  AttnArgs a;
+  a.c = *cache;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.scale = scale;
+  a.softcap = softcap;
+  a.window = window;
+  a.B = static_cast<int>(B);
+  a.T = static_cast<int>(T);
+  a.Hq = n_q_heads;
+  a.G = n_q_heads / cache->n_kv_heads;
+  a.page_shift = log2_of(cache->page_size);
+  a.ws = workspace;
+  a.err = device_error_ptr();
+  cudaError_t e = launch_attn(a, q_dtype == KQ_BF16, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_status(e);
+}
+
+size_t kq_sample_workspace_size(int64_t M, int64_t V) {
+  if (M < 0 || V < 1 || M > INT32_MAX || V > (1 << 20)) return 0;
+  return sample_workspace_bytes(M, V);
+}
+
+kq_status kq_sample(const void* logits, int dtype, int64_t row_stride, int64_t M, int64_t V, const float* u,
+                    const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                    int32_t* ids, float* probs, void* workspace, size_t workspace_bytes, kq_stream_t stream) {
+  if (!float_dtype(dtype) || M < 0 || V < 0 || row_stride < 0) return KQ_ERR_ARG;
+  if (V < 1 || V > (1 << 20) || M > INT32_MAX) return KQ_ERR_UNSUPPORTED;
+  if (M == 0) return KQ_OK;
+  if (!logits || !u || !ids) return KQ_ERR_ARG;
+  if (!aligned(logits, dtype == KQ_BF16 ? 2 : 4) || !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
+      !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(ids, 4) || !aligned(probs, 4))
+    return KQ_ERR_ALIGN;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < sample_workspace_bytes(M, V)) return KQ_ERR_WORKSPACE;
+  SampleArgs a;
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.temperature = temperature;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.u = u;
+  a.top_k = top_k;
+  a.ids = ids;
+  a.probs = probs;
+  a.ws = workspace;
+  a.M = static_cast<int>(M);
+  a.V = static_cast<int>(V);
+  cudaError_t e = launch_sample(a, dtype == KQ_BF16, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_status(e);
+}
+
 kq_status kq_selftest_wait(int kind, int* observed_code, kq_stream_t stream) {
   if ((kind != 0 && kind != 1) || !observed_code) return KQ_ERR_ARG;
   return cuda_status(run_selftest_wait(kind, observed_code, reinterpret_cast<cudaStream_t>(stream)));
@@ -382,7 +540,7 @@ const char* kq_status_string(kq_status s) {
     case KQ_ERR_ARG: return "invalid argument";
     case KQ_ERR_TYPE: return "unknown block type";
     case KQ_ERR_SHAPE: return "unsupported shape (K must be a multiple of 32; dequant n a multiple of 256)";
-    case KQ_ERR_UNSUPPORTED: return "unsupported size (M must be 1..16, top_k 1..32)";
+    case KQ_ERR_UNSUPPORTED: return "size outside this call's limits (products: M 1..16, top_k 1..32)";
     case KQ_ERR_ALIGN: return "misaligned pointer";
     case KQ_ERR_CUDA: return "CUDA error";
     case KQ_ERR_WORKSPACE: return "workspace missing or too small";

@@ -1,0 +1,170 @@
+// kq_append.cu -- what stands between a layer's q|k|v products and its
+// attention, in one launch: RMS norms of q and k per head, the rotation by
+// position, q out, and k and v into the sequences' cache pages.
+//
+//   y = x / sqrt(mean(x^2) + eps) * (w + off)             (q and k, optional)
+//   (a, b) -> (a c - b s, b c + a s)                      (q and k, first rot_dim values)
+//
+// with c, s read from a table of cos | sin per position: the angles of long
+// contexts (positions of 10^5 and more, scaled frequencies) lose their digits
+// in fp32 products, so they are made once, by the caller, in 64 bits.
+//
+// Everything is fp32 up to one rounding into q_out or the cache; an 8-bit
+// cache stores x / scale, saturated at e4m3's largest value 448 (a NaN stays
+// a NaN).
+//
+// Bound: memory (and at one token, the chain of dependent loads length ->
+// page id -> store).  A row of D values is D / 8 lanes' work: each lane holds
+// two vectors of four values that are each other's rotation partners (i and
+// i + rot/2, or adjacent pairs when interleaved), so the rotation needs no
+// exchange between lanes and the norm one shuffle sum over the row's lanes.
+#include "kq_cache.h"
+
+namespace kq {
+namespace {
+
+constexpr int ATH = 256;  // threads per CTA
+
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+}
+__device__ __forceinline__ void store4(__nv_fp8_e4m3* p, float4 v) {
+  const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v.x, v.y), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v.z, v.w), __NV_SATFINITE, __NV_E4M3);
+  *reinterpret_cast<uint32_t*>(p) = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+__device__ __forceinline__ float sq4(float4 v) { return v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w; }
+__device__ __forceinline__ float4 scale4(float4 v, float s, float4 w, float off) {
+  return make_float4(v.x * s * (w.x + off), v.y * s * (w.y + off), v.z * s * (w.z + off), v.w * s * (w.w + off));
+}
+
+// X: q, k, v; O: q_out; C: the cache.  LG = D / 8 lanes hold one row.
+template <class X, class O, class C, int LG>
+__global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int D = 8 * LG;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int Hkv = a.c.n_kv_heads, H = a.Hq + 2 * Hkv;
+  const uint32_t rows = static_cast<uint32_t>(a.B) * a.T * H;
+  const int l = threadIdx.x % LG;
+  const int rot = a.rope.rot_dim, rl = rot / 8;
+  // the row's two vectors of this lane
+  int e0, e1;
+  if (l >= rl || a.rope.interleaved) {
+    e0 = 8 * l;
+    e1 = e0 + 4;
+  } else {
+    e0 = 4 * l;
+    e1 = rot / 2 + 4 * l;
+  }
+  // every lane of a warp runs the same number of rounds (the norm's shuffles)
+  const uint32_t step = gridDim.x * (ATH / LG);
+  for (uint32_t r0 = blockIdx.x * (ATH / LG); r0 < rows; r0 += step) {
+    const uint32_t r = r0 + threadIdx.x / LG;
+    const bool in = r < rows;
+    const uint32_t tok = in ? r / H : 0;
+    const int h = in ? static_cast<int>(r - tok * H) : 0;
+    const int b = tok / a.T, t = tok - b * a.T;
+    const int kind = h < a.Hq ? 0 : (h < a.Hq + Hkv ? 1 : 2);  // q, k, v
+    const int hk = kind == 0 ? h : h - a.Hq - (kind == 2 ? Hkv : 0);
+    const X* src = kind == 0   ? static_cast<const X*>(a.q) + tok * a.q_stride
+                   : kind == 1 ? static_cast<const X*>(a.k) + tok * a.k_stride
+                               : static_cast<const X*>(a.v) + tok * a.v_stride;
+    src += static_cast<int64_t>(hk) * D;
+    float4 x0 = make_float4(0, 0, 0, 0), x1 = x0;
+    if (in) {
+      x0 = load4(src + e0);
+      x1 = load4(src + e1);
+    }
+    const int pos = in ? __ldg(a.seq_lens + b) - a.T + t : -1;
+    bool ok = pos >= 0;
+    if (ok && rot > 0 && pos >= a.rope.n_positions) {
+      if (l == 0) record_error(a.err, DEV_ERR_POSITION);
+      ok = false;
+    }
+    const float* nw = kind == 0 ? a.rope.q_norm : kind == 1 ? a.rope.k_norm : nullptr;
+    float ss = sq4(x0) + sq4(x1);
+#pragma unroll
+    for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    if (nw) {
+      const float s = rsqrtf(ss * (1.0f / D) + a.rope.eps);
+      x0 = scale4(x0, s, load4(nw + e0), a.rope.norm_offset);
+      x1 = scale4(x1, s, load4(nw + e1), a.rope.norm_offset);
+    }
+    if (kind != 2 && l < rl && ok) {
+      const float* cs = a.rope.cos_sin + static_cast<int64_t>(pos) * rot + 4 * l;
+      const float4 c = load4(cs), s = load4(cs + rot / 2);
+      if (a.rope.interleaved) {  // pairs (x0.x, x0.y), (x0.z, x0.w), (x1.x, x1.y), (x1.z, x1.w)
+        const float4 p = x0, q = x1;
+        x0 = make_float4(p.x * c.x - p.y * s.x, p.y * c.x + p.x * s.x, p.z * c.y - p.w * s.y, p.w * c.y + p.z * s.y);
+        x1 = make_float4(q.x * c.z - q.y * s.z, q.y * c.z + q.x * s.z, q.z * c.w - q.w * s.w, q.w * c.w + q.z * s.w);
+      } else {
+        const float4 p = x0, q = x1;
+        x0 = make_float4(p.x * c.x - q.x * s.x, p.y * c.y - q.y * s.y, p.z * c.z - q.z * s.z, p.w * c.w - q.w * s.w);
+        x1 = make_float4(q.x * c.x + p.x * s.x, q.y * c.y + p.y * s.y, q.z * c.z + p.z * s.z, q.w * c.w + p.w * s.w);
+      }
+    }
+    if (!in) continue;
+    if (kind == 0) {
+      if (!ok) x0 = x1 = make_float4(0, 0, 0, 0);
+      O* dst = static_cast<O*>(a.q_out) + static_cast<int64_t>(r - tok * 2 * Hkv) * D;
+      store4(dst + e0, x0);
+      store4(dst + e1, x1);
+    } else if (ok) {
+      const int64_t pi = pos >> a.page_shift;
+      const int page = pi < a.max_pages ? __ldg(a.page_table + b * a.max_pages + pi) : -1;
+      if (page < 0 || page >= a.c.n_pages) {
+        if (l == 0) record_error(a.err, DEV_ERR_PAGE);
+        continue;
+      }
+      C* dst = static_cast<C*>(kind == 1 ? a.c.k : a.c.v) + page * a.c.page_stride +
+               (pos & (a.c.page_size - 1)) * a.c.slot_stride + hk * a.c.head_stride;
+      const float sc = kind == 1 ? a.c.k_scale : a.c.v_scale;
+      if (sc != 1.0f) {
+        x0 = make_float4(x0.x / sc, x0.y / sc, x0.z / sc, x0.w / sc);
+        x1 = make_float4(x1.x / sc, x1.y / sc, x1.z / sc, x1.w / sc);
+      }
+      store4(dst + e0, x0);
+      store4(dst + e1, x1);
+    }
+  }
+}
+
+template <class X, class O, class C>
+cudaError_t launch_d(const AppendArgs& a, cudaStream_t st) {
+  const int D = a.c.head_dim;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T * (a.Hq + 2 * a.c.n_kv_heads);
+  const int rpc = ATH / (D / 8);
+  const int64_t want = (rows + rpc - 1) / rpc, most = static_cast<int64_t>(num_sms()) * (2048 / ATH);
+  const dim3 grid(static_cast<unsigned>(want < most ? want : most)), block(ATH);
+  switch (D) {
+    case 64: return launch_pdl(append_kernel<X, O, C, 8>, grid, block, 0, st, a);
+    case 128: return launch_pdl(append_kernel<X, O, C, 16>, grid, block, 0, st, a);
+    default: return launch_pdl(append_kernel<X, O, C, 32>, grid, block, 0, st, a);
+  }
+}
+template <class X, class O>
+cudaError_t launch_c(const AppendArgs& a, cudaStream_t st) {
+  return a.c.dtype == KQ_BF16 ? launch_d<X, O, __nv_bfloat16>(a, st) : launch_d<X, O, __nv_fp8_e4m3>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendArgs& a, int x_bf16, int out_bf16, cudaStream_t st) {
+  if (x_bf16) return out_bf16 ? launch_c<__nv_bfloat16, __nv_bfloat16>(a, st) : launch_c<__nv_bfloat16, float>(a, st);
+  return out_bf16 ? launch_c<float, __nv_bfloat16>(a, st) : launch_c<float, float>(a, st);
+}
+
+}  // namespace kq

@@ -16,7 +16,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libkq.so")
 
 KQ_Q4_K, KQ_Q5_K, KQ_Q6_K, KQ_IA4 = 1, 2, 3, 4
-KQ_F32, KQ_BF16 = 0, 1
+KQ_F32, KQ_BF16, KQ_F8E4M3 = 0, 1, 2
 KQ_ACT_SILU, KQ_ACT_GELU_TANH = 0, 1
 KQ_OK = 0
 STATUS = {0: "KQ_OK", -1: "KQ_ERR_ARG", -2: "KQ_ERR_TYPE", -3: "KQ_ERR_SHAPE", -4: "KQ_ERR_UNSUPPORTED",
@@ -46,6 +46,13 @@ SIGNATURES = {
     "kq_moe_ffn": (_I, [_P, _P, _P, _P, _I, _P, _I64, _I64, ctypes.c_int32, _P, _SZ, _P]),
     "kq_moe_matvec_noalloc": (_I, [_I, _P, ctypes.c_int32, _P, _P, _P, _I, _I, _P, _I64, _I64, _I64,
                                    ctypes.c_int32, _P]),
+    "kq_kv_append": (_I, [_P, _P, _I64, _P, _I64, _I64, _P, _P, _P, _I, _I64, _I64, _I64, ctypes.c_int32, _P, _P, _I,
+                          _P]),
+    "kq_attn_workspace_size": (_SZ, [_P, _I64, _I64, ctypes.c_int32]),
+    "kq_attn_decode": (_I, [_P, _P, _I64, _P, _I64, _I64, _P, _I, _I64, ctypes.c_int32, ctypes.c_float,
+                            ctypes.c_float, ctypes.c_int32, _P, _P, _SZ, _P]),
+    "kq_sample_workspace_size": (_SZ, [_I64, _I64]),
+    "kq_sample": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "kq_device_error": (_I, [ctypes.POINTER(ctypes.c_int), _I]),
     "kq_last_cuda_error": (_I, []),
     "kq_status_string": (ctypes.c_char_p, [_I]),
@@ -375,3 +382,200 @@ def dequant_bf16(qtype: int, blocks: torch.Tensor, n: int) -> torch.Tensor:
     out = torch.empty(n, dtype=torch.bfloat16, device=blocks.device)
     kq_dequant_bf16(qtype, blocks, out, n)
     return out
+
+
+# ---------------------------------------------------------------------------
+# The paged key-value cache, its writer and its reader, and the sampler.
+# ---------------------------------------------------------------------------
+
+class KqKvCache(ctypes.Structure):
+    """struct kq_kv_cache of include/kq.h."""
+    _fields_ = [("dtype", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class KqRope(ctypes.Structure):
+    """struct kq_rope of include/kq.h."""
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("norm_offset", ctypes.c_float), ("cos_sin", ctypes.c_void_p), ("n_positions", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+_CACHE_TYPES = {torch.bfloat16: KQ_BF16, torch.float8_e4m3fn: KQ_F8E4M3}
+
+
+class KVCache:
+    """A layer's cache: k and v [n_pages, page_size, n_kv_heads, head_dim], bfloat16 or float8_e4m3fn (stored values
+    times k_scale, v_scale), of any strides but a contiguous last dimension (a permuted view gives another order of
+    slots and heads).  Holds both tensors."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v: alike, [n_pages, page_size, n_kv_heads, head_dim], last dimension contiguous")
+        if k.dtype not in _CACHE_TYPES:
+            raise TypeError("a cache is bfloat16 or float8_e4m3fn")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, float(k_scale), float(v_scale)
+        n_pages, page, heads, dim = k.shape
+        self.struct = KqKvCache(_CACHE_TYPES[k.dtype], heads, dim, page, n_pages, k.stride(0), k.stride(1), k.stride(2),
+                                _ptr(k), _ptr(v), self.k_scale, self.v_scale)
+        self._ref = ctypes.addressof(self.struct)
+
+
+class RopeNorm:
+    """What kv_append does to q and k (struct kq_rope): norm weights [head_dim] fp32 or None, and cos_sin
+    [n_positions, rot_dim] fp32 (see rope_table) or None for no rotation.  Holds the tensors."""
+
+    def __init__(self, cos_sin=None, interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6,
+                 norm_offset: float = 0.0):
+        for w in (cos_sin, q_norm, k_norm):
+            if w is not None and (w.dtype != torch.float32 or not w.is_contiguous()):
+                raise TypeError("cos_sin, q_norm and k_norm are contiguous float32")
+        self.cos_sin, self.q_norm, self.k_norm = cos_sin, q_norm, k_norm
+        n, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+        self.struct = KqRope(_ptr(q_norm), _ptr(k_norm), eps, norm_offset, _ptr(cos_sin), n, rot, int(interleaved))
+        self._ref = ctypes.addressof(self.struct)
+
+
+def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, factor: float = 1.0, trained: int = 0,
+               low: float = 1.0, high: float = 4.0, amplitude: float = 1.0, device="cuda") -> torch.Tensor:
+    """cos | sin [n_positions, rot_dim] fp32 for RopeNorm, computed in 64 bits: pair i turns by base^(-2i/rot_dim) per
+    position.  factor > 1 stretches positions: all pairs alike (trained = 0), or, given the context length the model
+    was trained on, the pairs that turn at most `low` times over it, none that turn at least `high` times, and a
+    linear blend between.  amplitude multiplies the table."""
+    freq = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    if factor != 1.0:
+        keep = torch.zeros_like(freq)
+        if trained:
+            turns = trained * freq / (2 * torch.pi)
+            keep = ((turns - low) / (high - low)).clamp(0.0, 1.0)
+        freq = freq * keep + freq / factor * (1.0 - keep)
+    a = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * freq
+    return (torch.cat([a.cos(), a.sin()], 1) * amplitude).float()
+
+
+def kq_kv_append(cache, page_table, max_pages, seq_lens, B, T, q, k, v, x_dtype, q_stride, k_stride, v_stride, n_q_heads,
+                 rope, q_out, q_out_dtype, stream=None):
+    _check("kq_kv_append", lib().kq_kv_append(cache, _ptr(page_table), max_pages, _ptr(seq_lens), B, T, _ptr(q), _ptr(k),
+                                              _ptr(v), x_dtype, q_stride, k_stride, v_stride, n_q_heads, rope,
+                                              _ptr(q_out), q_out_dtype, _stream(stream)))
+
+
+def kq_attn_workspace_size(cache, B, T, n_q_heads) -> int:
+    return lib().kq_attn_workspace_size(cache, B, T, n_q_heads)
+
+
+def kq_attn_decode(cache, page_table, max_pages, seq_lens, B, T, q, q_dtype, q_stride, n_q_heads, scale, softcap, window,
+                   out, workspace, workspace_bytes, stream=None):
+    _check("kq_attn_decode", lib().kq_attn_decode(cache, _ptr(page_table), max_pages, _ptr(seq_lens), B, T, _ptr(q),
+                                                  q_dtype, q_stride, n_q_heads, scale, softcap, window, _ptr(out),
+                                                  _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def kq_sample_workspace_size(M, V) -> int:
+    return lib().kq_sample_workspace_size(M, V)
+
+
+def kq_sample(logits, dtype, row_stride, M, V, u, temperature, top_k, top_p, min_p, ids, probs, workspace,
+              workspace_bytes, stream=None):
+    _check("kq_sample", lib().kq_sample(_ptr(logits), dtype, row_stride, M, V, _ptr(u), _ptr(temperature), _ptr(top_k),
+                                        _ptr(top_p), _ptr(min_p), _ptr(ids), _ptr(probs), _ptr(workspace),
+                                        workspace_bytes, _stream(stream)))
+
+
+def _rows(name: str, x: torch.Tensor, B: int, T: int, D: int):
+    """The heads and the row stride of x [B, T, heads, D]: heads contiguous, rows at one stride."""
+    if x.dim() != 4 or x.shape[0] != B or x.shape[1] != T or x.shape[3] != D:
+        raise ValueError(f"{name}: [{B}, {T}, heads, {D}], not {list(x.shape)}")
+    s0, s1, s2, s3 = x.stride()
+    if (s3 != 1 or (s2 != D and x.shape[2] > 1) or (B > 1 and T > 1 and s0 != T * s1)):
+        raise ValueError(f"{name}: heads contiguous, tokens at one stride")
+    return x.shape[2], (s1 if T > 1 else s0 if B > 1 else x.shape[2] * D)
+
+
+def _int32(name: str, t: torch.Tensor, *shape):
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 {list(shape)}")
+
+
+def kv_append(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+              v: torch.Tensor, rope: RopeNorm, q_out: torch.Tensor | None = None, q_out_dtype=torch.bfloat16,
+              stream=None) -> torch.Tensor:
+    """kq_kv_append for q [B, T, n_q_heads, head_dim], k and v [B, T, n_kv_heads, head_dim] (views of one fused buffer
+    will do), page_table [B, max_pages] and seq_lens [B] int32; returns q_out."""
+    B, T, c = q.shape[0], q.shape[1], cache.struct
+    D = c.head_dim
+    (Hq, qs), (Hk, ks), (Hv, vs) = _rows("q", q, B, T, D), _rows("k", k, B, T, D), _rows("v", v, B, T, D)
+    if Hk != c.n_kv_heads or Hv != c.n_kv_heads or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("k and v: the cache's heads, of q's type")
+    for w in (rope.q_norm, rope.k_norm):
+        if w is not None and w.numel() != D:
+            raise ValueError("norm weights: [head_dim]")
+    _int32("page_table", page_table, B, page_table.shape[-1])
+    _int32("seq_lens", seq_lens, B)
+    if q_out is None:
+        q_out = torch.empty((B, T, Hq, D), dtype=q_out_dtype, device=q.device)
+    elif q_out.shape != q.shape or not q_out.is_contiguous():
+        raise ValueError("q_out: contiguous, of q's shape")
+    kq_kv_append(cache._ref, page_table, page_table.shape[1], seq_lens, B, T, q, k, v, x_dtype_of(q), qs, ks, vs, Hq,
+                 rope._ref, q_out, x_dtype_of(q_out), stream)
+    return q_out
+
+
+def attn_workspace(cache: KVCache, B: int, T: int, n_q_heads: int) -> torch.Tensor:
+    """A zero-filled workspace tensor for attn_decode."""
+    n = kq_attn_workspace_size(cache._ref, B, T, n_q_heads)
+    if n == 0:
+        raise KQError("kq_attn_workspace_size", -4)
+    return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)
+
+
+def attn_decode(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor,
+                workspace: torch.Tensor, scale: float | None = None, softcap: float = 0.0, window: int = 0,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kq_attn_decode for q [B, T, n_q_heads, head_dim]; scale None: head_dim^-0.5.  Returns out, of q's type."""
+    B, T = q.shape[0], q.shape[1]
+    D = cache.struct.head_dim
+    Hq, qs = _rows("q", q, B, T, D)
+    _int32("page_table", page_table, B, page_table.shape[-1])
+    _int32("seq_lens", seq_lens, B)
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out: contiguous, of q's shape and type")
+    kq_attn_decode(cache._ref, page_table, page_table.shape[1], seq_lens, B, T, q, x_dtype_of(q), qs, Hq,
+                   D ** -0.5 if scale is None else scale, softcap, window, out, workspace,
+                   workspace.numel() * workspace.element_size(), stream)
+    return out
+
+
+def sample_workspace(M: int, V: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace tensor for sample."""
+    n = kq_sample_workspace_size(M, V)
+    if n == 0:
+        raise KQError("kq_sample_workspace_size", -4)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None, workspace=None,
+           ids=None, probs=None, stream=None):
+    """kq_sample for logits [M, V] (rows contiguous) and u [M]; temperature, top_p, min_p [M] fp32 and top_k [M] int32,
+    or None.  Returns (ids int32 [M], probs fp32 [M])."""
+    M, V = logits.shape
+    if logits.stride(1) != 1 and V > 1:
+        raise ValueError("logits: each row contiguous")
+    for name, t, dt in (("u", u, torch.float32), ("temperature", temperature, torch.float32),
+                        ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32),
+                        ("ids", ids, torch.int32), ("probs", probs, torch.float32)):
+        if t is not None and (t.dtype != dt or t.shape != (M,) or not t.is_contiguous()):
+            raise ValueError(f"{name}: contiguous {dt} [{M}]")
+    if workspace is None:
+        workspace = sample_workspace(M, V, logits.device)
+    if ids is None:
+        ids = torch.empty(M, dtype=torch.int32, device=logits.device)
+    if probs is None:
+        probs = torch.empty(M, dtype=torch.float32, device=logits.device)
+    kq_sample(logits, x_dtype_of(logits), logits.stride(0), M, V, u, temperature, top_k, top_p, min_p, ids, probs,
+              workspace, workspace.numel() * workspace.element_size(), stream)
+    return ids, probs

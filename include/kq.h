@@ -72,7 +72,7 @@ extern "C" {
 typedef struct CUstream_st *kq_stream_t; /* same type as cudaStream_t */
 
 typedef enum { KQ_Q4_K = 1, KQ_Q5_K = 2, KQ_Q6_K = 3, KQ_IA4 = 4 } kq_type;
-typedef enum { KQ_F32 = 0, KQ_BF16 = 1 } kq_dtype;
+typedef enum { KQ_F32 = 0, KQ_BF16 = 1, KQ_F8E4M3 = 2 } kq_dtype; /* KQ_F8E4M3: key-value caches only */
 
 typedef int kq_status;
 #define KQ_OK 0
@@ -394,6 +394,144 @@ kq_status kq_moe_ffn_offsets(int64_t H, int64_t F, int64_t SH, int64_t M, int32_
 kq_status kq_moe_ffn(const kq_moe_ffn_weights *w, const int32_t *expert_ids, const float *gate_w, const void *x,
                      int x_dtype, float *y, int64_t H, int64_t M, int32_t top_k, void *workspace,
                      size_t workspace_bytes, kq_stream_t stream);
+
+/*
+ * The rest of a decode step around the quantized products: a paged key-value
+ * cache with its writer (kq_kv_append) and its reader (kq_attn_decode), and the
+ * choice of the token from the LM head's logits (kq_sample).  The pages name
+ * these steps ("GGUF in transformers", "Reusing ggml's Metal kernels":
+ * normalization and attention; "ANE Fieldfare" README, "Speculative decoding":
+ * sampling, verify blocks of up to 16 tokens) and give no formulas; the ones
+ * below are this library's reading.
+ *
+ * The cache.  Two pools of n_pages pages, one of keys, one of values, with
+ * page_size token slots each (a power of two, at most 1024); the strides count
+ * elements and hold for both pools: element d of head h of slot s of page p is
+ * at p*page_stride + s*slot_stride + h*head_stride + d.  Any order of slots
+ * and heads can be had this way.  dtype KQ_BF16, or KQ_F8E4M3: a stored value
+ * stands for itself times k_scale (v_scale); both scales are finite and > 0.
+ * head_dim 64, 128 or 256.  Pools 16-byte aligned, strides multiples of 16
+ * bytes (strides may be 0 or overlap only where the sizes they step over are 1).
+ *
+ * Sequences.  page_table [B][max_pages] int32: page i of a sequence holds its
+ * positions i*page_size .. (i+1)*page_size - 1.  seq_lens [B] int32: the
+ * sequences' lengths, the T newest tokens included, so token t of the T is at
+ * position seq_lens[b] - T + t; where that is negative the token is padding.
+ * Table entries past a sequence's length are not read.  A length past the
+ * table (max_pages*page_size) and a page id outside [0, n_pages) never fault:
+ * they are recorded in the device error word (kq_device_error), and what that
+ * sequence gets is unspecified.
+ */
+typedef struct kq_kv_cache {
+  int32_t dtype;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int64_t n_pages;
+  int64_t page_stride, slot_stride, head_stride;
+  void *k, *v;
+  float k_scale, v_scale;
+} kq_kv_cache;
+
+/*
+ * What is done to q and k before the cache and the attention.
+ *   q_norm, k_norm  [head_dim] fp32 or NULL (no norm): each head's values become
+ *                   x / sqrt(mean(x^2) + eps) * (norm + norm_offset); offset 1
+ *                   for zero-centred weights.
+ *   cos_sin         [n_positions][rot_dim] fp32: per position rot_dim/2 cosines,
+ *                   then rot_dim/2 sines, scaled for long contexts or not as
+ *                   the model wants (the caller makes it once, in 64 bits).
+ *   rot_dim         values of each head that rotate, from the first; a multiple
+ *                   of 8, at most head_dim; 0: none (cos_sin may be NULL).
+ *   interleaved     0: value i rotates with i + rot_dim/2; 1: 2i with 2i + 1.
+ * The norm precedes the rotation (a, b) -> (a cos - b sin, b cos + a sin).
+ * cos_sin, q_norm and k_norm 16-byte aligned.
+ */
+typedef struct kq_rope {
+  const float *q_norm, *k_norm;
+  float eps, norm_offset;
+  const float *cos_sin;
+  int64_t n_positions;
+  int32_t rot_dim;
+  int32_t interleaved;
+} kq_rope;
+
+/*
+ * Norms, rotation and the write into the cache, of T new tokens of each of B
+ * sequences, in one launch:
+ *   q [B*T] rows of n_q_heads*head_dim values, k and v of n_kv_heads*head_dim;
+ *   token i's row starts i*q_stride (k_stride, v_stride) elements in, so one
+ *   buffer of fused rows serves.  x_dtype KQ_F32 or KQ_BF16 (all three).
+ *   q_out [B*T][n_q_heads][head_dim], q_out_dtype KQ_F32 or KQ_BF16.
+ * k and v go to their positions' slots; v as it is, in the cache's type.  All
+ * arithmetic is fp32, rounded once on its way out (KQ_F8E4M3: x / scale, to
+ * nearest, saturated at +-448).  A padding token's q_out is 0 and nothing is
+ * stored for it; so too where a position is outside [0, n_positions) with
+ * rot_dim > 0, which is recorded in the device error word.  Two tokens must
+ * not share a slot (sequences that share a page have to be past it).
+ * q, k, v, q_out 16-byte aligned, row strides multiples of 16 bytes.
+ * T >= 0 of any size (prompts too), B*T*(n_q_heads + 2*n_kv_heads) < 2^31.
+ */
+kq_status kq_kv_append(const kq_kv_cache *cache, const int32_t *page_table, int64_t max_pages,
+                       const int32_t *seq_lens, int64_t B, int64_t T, const void *q, const void *k, const void *v,
+                       int x_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t n_q_heads,
+                       const kq_rope *rope, void *q_out, int q_out_dtype, kq_stream_t stream);
+
+/*
+ * Attention of the newest T tokens (1..16) of each sequence over its cache:
+ *   s_j = scale * q.k_j, with softcap > 0: softcap * tanh(s_j / softcap)
+ *   out = sum_j softmax(s)_j v_j
+ * where the token at position p sees positions j <= p, with window > 0 only
+ * j > p - window.  n_q_heads a multiple of n_kv_heads, at most 16 times it:
+ * query head h reads head h / (n_q_heads / n_kv_heads).  A token that sees
+ * nothing (padding, an empty sequence) gets zeros.  What lies in slots that no
+ * token sees has no influence, NaN and infinities included; a slot that only
+ * some of the T tokens see has none on the others.
+ *   q   [B*T] rows of n_q_heads*head_dim, q_stride elements apart, q_dtype KQ_F32 or KQ_BF16
+ *   out [B*T][n_q_heads][head_dim] of q_dtype
+ * Scores, softmax and sums are fp32, and so are the partial results that
+ * split sequences are joined from; the order of the sums depends on the
+ * arguments, the lengths and the device's SM count only: repeated calls give
+ * identical outputs.
+ * workspace: kq_attn_workspace_size bytes, 256-byte aligned, zero-filled once
+ * before first use (its counters are zero again after every call); one call at
+ * a time per workspace.  q and out 16-byte aligned, q_stride a multiple of 16
+ * bytes.  B <= 4096 (else KQ_ERR_UNSUPPORTED).
+ */
+size_t kq_attn_workspace_size(const kq_kv_cache *cache, int64_t B, int64_t T, int32_t n_q_heads);
+
+kq_status kq_attn_decode(const kq_kv_cache *cache, const int32_t *page_table, int64_t max_pages,
+                         const int32_t *seq_lens, int64_t B, int64_t T, const void *q, int q_dtype, int64_t q_stride,
+                         int32_t n_q_heads, float scale, float softcap, int32_t window, void *out, void *workspace,
+                         size_t workspace_bytes, kq_stream_t stream);
+
+/*
+ * The next token of each of M rows of V logits, from a uniform number per row.
+ *   logits [M] rows of V values, row_stride elements apart, KQ_F32 or KQ_BF16
+ *   u      [M] fp32 in [0, 1)
+ *   temperature, top_p, min_p [M] fp32 and top_k [M] int32, each NULL for off
+ * With l_max the row's largest logit, the words in descending order of their
+ * logits (equal logits by ascending index; a NaN counts as -inf):
+ *   w_i = exp((l_i - l_max) / temperature)     (+inf: the infinite ones share)
+ *   top_k > 0:  the first top_k words stay
+ *   top_p < 1:  of those, the words with less than top_p of their sum before them
+ *   min_p > 0:  of those, the words with w_i >= min_p
+ * the first word always stays, and the token is the first whose running sum
+ * of the kept weights exceeds u times their sum.  temperature not above 0
+ * takes the first word (the largest logit).
+ *   ids    [M] int32; -1 where a row has no logit above -inf
+ *   probs  [M] fp32 or NULL: the token's share of the kept weights (0 for -1)
+ * Weights are fp32 exponentials summed exactly, in units of 2^-40 of the
+ * largest: the result depends on the arguments alone.
+ * V in 1..2^20 (else KQ_ERR_UNSUPPORTED).  workspace: kq_sample_workspace_size
+ * bytes, 256-byte aligned, zero-filled once before first use; one call at a
+ * time per workspace.  logits 4-byte (KQ_F32) or 2-byte aligned.
+ */
+size_t kq_sample_workspace_size(int64_t M, int64_t V);
+
+kq_status kq_sample(const void *logits, int dtype, int64_t row_stride, int64_t M, int64_t V, const float *u,
+                    const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                    int32_t *ids, float *probs, void *workspace, size_t workspace_bytes, kq_stream_t stream);
 
 /*
  * Read the device error word (KQ_OK when clean); with clear != 0 also reset

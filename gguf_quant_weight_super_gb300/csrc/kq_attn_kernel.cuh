@@ -1,0 +1,711 @@
+// kq_attn_kernel.cuh -- attention of the newest T tokens of each sequence over
+// its paged cache (instantiated per cache type in kq_attn_bf16.cu and
+// kq_attn_f8.cu, launched by kq_attn.cu):
+//   s_j = scale q.k_j  or  softcap tanh(scale q.k_j / softcap)
+//   o   = sum_j 2^(s_j log2 e - m) v_j / sum_j 2^(s_j log2 e - m)
+// over the positions j that the token sees, in one pass with a running
+// maximum m and running sums (the sums are scaled down when m grows).
+//
+// Bound: the cache is read once and every key and value serves the T*G query
+// rows of its head only, so up to about 64 rows the bytes bound it.  Hence
+//  * the rows of a head (T tokens x G heads) share what is loaded: they are
+//    the M of the matrix instructions, 16 or 32 per pass over the cache;
+//  * each warp streams its own sub-tiles of 16 positions through its own ring
+//    of asynchronous 16-byte copies (any page size, order of slots and
+//    alignment of lengths: a row is one token of one head) and keeps its own
+//    m and sums, so no barrier interrupts the loads; the four warps' sums
+//    join once per segment.  Rows are padded by 16 bytes in shared memory, so
+//    that the 8-row matrix loads touch every bank once;
+//  * all tiles of 64 positions of all (sequence, head, row tile) items are one
+//    line, cut evenly into one contiguous range per CTA, whatever the
+//    lengths.  An item inside one range is finished there; for one that spans
+//    ranges the CTAs leave their sums in the workspace, and the last to
+//    arrive joins them in the ranges' order (so the result does not depend on
+//    which one that is).
+//
+// Precision: products enter the matrix instructions exactly or in parts.
+// bf16 cache: bf16 q as it is, fp32 q as three bf16 parts (all 24 bits); the
+// weights 2^(..) as two parts (2^-17) for bf16 q and three for fp32 q.  e4m3
+// cache: its values are fp16 values, so fp16 instructions serve; q is scaled
+// by a power of two per row into fp16's range (bf16: one part; fp32: two, 22
+// bits), weights are two parts.  Accumulation is fp32.
+//
+// Values that no row sees are never loaded (zeros take their place).  One that
+// some rows of the block see and others do not would reach the others as
+// 0 * NaN if it is not finite: a warp whose sums are not all finite runs its
+// part again, taking those values out of the product and adding each to the
+// rows that see it.
+#pragma once
+
+#include "kq_cache.h"
+
+namespace kq {
+namespace attn {
+
+constexpr int NW = 4;            // warps per CTA
+constexpr int NTH = NW * 32;
+constexpr int WT = 16;           // positions per warp sub-tile
+constexpr int TK = NW * WT;      // positions per tile
+
+template <class Q, class C, int D, int MT>
+struct Cfg {
+  static constexpr bool F8 = sizeof(C) == 1, QF32 = sizeof(Q) == 4;
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int NQ = F8 ? (QF32 ? 2 : 1) : (QF32 ? 3 : 1);  // parts of q
+  static constexpr int NP = F8 ? 2 : (QF32 ? 3 : 2);               // parts of the weights
+  static constexpr int RB = D * static_cast<int>(sizeof(C)) + 16;  // bytes of a cache row in shared memory
+  static constexpr int SUB = WT * RB, STAGE = 2 * SUB;
+  static constexpr int QB = 2 * D + 16;  // bytes of a q row in shared memory
+  static constexpr int QBYTES = NQ * ROWS * QB;
+  static constexpr int HDR = (ROWS * (3 + 2 * NW) * 4 + 127) / 128 * 128;  // row scales, joined and warps' statistics
+  static constexpr int FIXED = HDR + QBYTES;
+  // two CTAs per SM where a ring of at least two stages fits beside q in half of the shared memory (the rest is the
+  // line of tiles' index, 8 bytes per sequence)
+  static constexpr int HALF = 110 * 1024, FULL = 192 * 1024;
+  static constexpr bool TWO = FIXED + 2 * NW * STAGE <= HALF;
+  static constexpr int FIT = ((TWO ? HALF : FULL) - FIXED) / (NW * STAGE);
+  static constexpr int S = FIT < 6 ? FIT : 6;  // ring stages
+  static constexpr int CPS = TWO ? 2 : 1;
+  static constexpr int SMEM = FIXED + S * NW * STAGE;
+  static_assert(S >= 2 && S * STAGE >= ROWS * D * 4, "the warps' sums take the ring's place");
+};
+
+struct Params {
+  AttnArgs a;
+  int RT;          // row tiles per (sequence, head)
+  float* part;     // [2 * grid][ROWS][D] sums, then [2 * grid][ROWS][2] maximum and weight sum
+  float* part_ml;
+  int* count;      // [items] arrivals
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two values as packed 16-bit ones (lo in the low half), and back.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  else return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+// e4m3 values of the low two bytes as two fp16 (exact).
+__device__ __forceinline__ uint32_t f8_pair(uint32_t v) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float q_value(float v) { return v; }
+__device__ __forceinline__ float q_value(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+__device__ __forceinline__ void put2(__nv_bfloat16* p, float x, float y) {
+  *reinterpret_cast<uint32_t*>(p) = pack2<false>(x, y);
+}
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+
+// One segment: tiles [t0, t1) of one item, for one warp.
+struct Seg {
+  const int32_t* table;  // the sequence's pages
+  int64_t head_off;      // elements
+  int len, first;        // positions [first, len) can be seen by some row
+  int t0, t1;
+};
+
+template <class Q, class C, int D, int MT>
+struct Warp {
+  using K = Cfg<Q, C, D, MT>;
+  float o[MT][D / 8][4];
+  float m[MT][2], l[MT][2];  // maximum (in log2 units) and this lane's part of the weight sum, of rows lane/4 and + 8
+
+  // The copies of one sub-tile: K rows, then V rows.  `page`: this lane's row's page id (row lane & 15).
+  static __device__ __forceinline__ void issue(const Params& p, const Seg& g, uint32_t stage, int base, int page, int lane) {
+    const AttnArgs& a = p.a;
+    const int j = base + (lane & 15);
+    bool on = j >= g.first && j < g.len;
+    if (on && (page < 0 || page >= a.c.n_pages)) {
+      record_error(a.err, DEV_ERR_PAGE);
+      on = false;
+    }
+    const int64_t off = on ? (page * a.c.page_stride + (j & (a.c.page_size - 1)) * a.c.slot_stride + g.head_off) *
+                                 static_cast<int64_t>(sizeof(C))
+                           : -1;
+    constexpr int CH = D * static_cast<int>(sizeof(C)) / 16;  // 16-byte chunks per row
+#pragma unroll
+    for (int i = 0; i < CH / 2; ++i) {
+      const int c = i * 32 + lane, row = c / CH, col = c % CH;
+      const int64_t ro = __shfl_sync(0xFFFFFFFFu, off, row);
+      const bool ok = ro >= 0;
+      const int64_t src = (ok ? ro : 0) + col * 16;
+      const uint32_t dst = stage + row * K::RB + col * 16;
+      copy16(dst, static_cast<const uint8_t*>(a.c.k) + src, ok);
+      copy16(dst + K::SUB, static_cast<const uint8_t*>(a.c.v) + src, ok);
+    }
+  }
+  static __device__ __forceinline__ int page_of(const Params& p, const Seg& g, int base, int lane) {
+    const int j = base + (lane & 15);
+    return j >= g.first && j < g.len ? __ldg(g.table + (j >> p.a.page_shift)) : 0;
+  }
+
+  // Scores, weights and sums of one sub-tile in shared memory.  pos[mt][i]: the position of the token of row 16 mt +
+  // lane/4 + 8 i; qs[mt][i]: that row's factor from the raw product to log2 units (or to the cap's argument).
+  template <bool CAREFUL>
+  __device__ __forceinline__ void tile(const Params& p, const Seg& g, uint32_t stage, uint8_t* vrow, uint32_t qaddr, int base,
+                                       const int (&pos)[MT][2], const float (&qs)[MT][2], bool all, int lane) {
+    const AttnArgs& a = p.a;
+    float s[MT][2][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.0f;
+    // ---- scores
+    const uint32_t kaddr = stage + ((lane >> 4) * 8 + (lane & 7)) * K::RB + ((lane >> 3) & 1) * 16;
+    const uint32_t qa = qaddr + (lane & 15) * K::QB + (lane >> 4) * 16;
+    auto step = [&](int kk, uint32_t b00, uint32_t b01, uint32_t b10, uint32_t b11) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int t = 0; t < K::NQ; ++t) {
+          uint32_t aq[4];
+          ldsm4(aq, qa + (t * K::ROWS + 16 * mt) * K::QB + kk * 32);
+          mma<K::F8>(s[mt][0], aq, b00, b01);
+          mma<K::F8>(s[mt][1], aq, b10, b11);
+        }
+    };
+    if constexpr (K::F8) {
+#pragma unroll
+      for (int k2 = 0; k2 < D / 32; ++k2) {
+        uint32_t r[4];  // positions 0-7: dims 0-15, 16-31; positions 8-15 likewise
+        ldsm4(r, kaddr + k2 * 32);
+        step(2 * k2, f8_pair(r[0]), f8_pair(r[0] >> 16), f8_pair(r[2]), f8_pair(r[2] >> 16));
+        step(2 * k2 + 1, f8_pair(r[1]), f8_pair(r[1] >> 16), f8_pair(r[3]), f8_pair(r[3] >> 16));
+      }
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t r[4];
+        ldsm4(r, kaddr + kk * 32);
+        step(kk, r[0], r[1], r[2], r[3]);
+      }
+    }
+    // ---- weights
+    const int jq = base + 2 * (lane & 3);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[mt][n][e] * qs[mt][e >> 1];
+          if (a.softcap > 0.0f) x = a.softcap * 1.4426950408889634f * tanhf(x);
+          s[mt][n][e] = x;
+        }
+      if (!all) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = jq + 8 * n + (e & 1), ps = pos[mt][e >> 1];
+            if (!(j <= ps && (a.window == 0 || j > ps - a.window))) s[mt][n][e] = -INFINITY;
+          }
+      }
+      float mx[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mx[i] = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
+        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
+        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 2));
+        mx[i] = fmaxf(mx[i], m[mt][i]);
+      }
+      if (__any_sync(0xFFFFFFFFu, mx[0] != m[mt][0] || mx[1] != m[mt][1])) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float c = mx[i] == m[mt][i] ? 1.0f : ex2(m[mt][i] - mx[i]);
+          l[mt][i] *= c;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            o[mt][n][2 * i] *= c;
+            o[mt][n][2 * i + 1] *= c;
+          }
+          m[mt][i] = mx[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mm = m[mt][i] == -INFINITY ? 0.0f : m[mt][i];  // nothing seen yet: the weights are 0
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float w = ex2(s[mt][n][2 * i + e] - mm);
+            s[mt][n][2 * i + e] = w;
+            l[mt][i] += w;
+          }
+      }
+    }
+    if constexpr (CAREFUL) take_out(p, vrow, base, s, pos, lane);
+    // ---- sums
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      uint32_t w[K::NP][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {  // rows lane/4 and + 8 of positions 0-7, then 8-15
+        float x = s[mt][r >> 1][2 * (r & 1)], y = s[mt][r >> 1][2 * (r & 1) + 1];
+#pragma unroll
+        for (int t = 0; t < K::NP; ++t) {
+          w[t][r] = pack2<K::F8>(x, y);
+          const float2 b = unpack2<K::F8>(w[t][r]);
+          x -= b.x;
+          y -= b.y;
+        }
+      }
+      const uint32_t vaddr = stage + K::SUB + (lane & 15) * K::RB + (lane >> 4) * 16;
+      if constexpr (K::F8) {
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) {
+          uint32_t r[4];  // dims 0-15: positions 0-7, 8-15; dims 16-31 likewise
+          ldsm4t(r, vaddr + n * 32);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t b0 = __byte_perm(r[2 * h], 0, 0x3120), b1 = __byte_perm(r[2 * h + 1], 0, 0x3120);
+            const uint32_t e0 = f8_pair(b0), e1 = f8_pair(b1), d0 = f8_pair(b0 >> 16), d1 = f8_pair(b1 >> 16);
+#pragma unroll
+            for (int t = 0; t < K::NP; ++t) {
+              mma<true>(o[mt][4 * n + 2 * h], w[t], e0, e1);      // even dims
+              mma<true>(o[mt][4 * n + 2 * h + 1], w[t], d0, d1);  // odd dims
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t r[4];
+          ldsm4t(r, vaddr + n * 32);
+#pragma unroll
+          for (int t = 0; t < K::NP; ++t) {
+            mma<false>(o[mt][2 * n], w[t], r[0], r[1]);
+            mma<false>(o[mt][2 * n + 1], w[t], r[2], r[3]);
+          }
+        }
+      }
+    }
+  }
+
+  // The dimension of accumulator o[.][n][e] (e & 1 within the pair).
+  static __device__ __forceinline__ int dim_of(int n, int e, int lane) {
+    if constexpr (K::F8) return 16 * (n >> 1) + 4 * (lane & 3) + 2 * (e & 1) + (n & 1);
+    return 8 * n + 2 * (lane & 3) + (e & 1);
+  }
+  static __device__ __forceinline__ float value_at(const uint8_t* row, int d) {
+    if constexpr (K::F8) return static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(row)[d]);
+    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[d]);
+  }
+  // Adds the values that are not finite to the rows that see them, and puts zeros in their place.
+  __device__ __noinline__ void take_out(const Params& p, uint8_t* vrow, int base, const float (&s)[MT][2][4],
+                                        const int (&pos)[MT][2], int lane) {
+    for (int jj = 0; jj < WT; ++jj) {
+      const int j = base + jj, from = (lane & ~3) | ((jj & 7) >> 1);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float a0 = jj & 8 ? s[mt][1][2 * i] : s[mt][0][2 * i];
+          const float a1 = jj & 8 ? s[mt][1][2 * i + 1] : s[mt][0][2 * i + 1];
+          const float w = __shfl_sync(0xFFFFFFFFu, jj & 1 ? a1 : a0, from);
+          const bool sees = j <= pos[mt][i] && (p.a.window == 0 || j > pos[mt][i] - p.a.window);
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float v = value_at(vrow + jj * K::RB, dim_of(n, e, lane));
+              if (sees && !finite(v)) o[mt][n][2 * i + e] += w * v;
+            }
+        }
+    }
+    __syncwarp();
+    for (int x = lane; x < WT * D; x += 32) {
+      uint8_t* row = vrow + (x / D) * K::RB;
+      if (!finite(value_at(row, x % D))) {
+        if constexpr (K::F8) row[x % D] = 0;
+        else reinterpret_cast<uint16_t*>(row)[x % D] = 0;
+      }
+    }
+    __syncwarp();
+  }
+
+  // A warp's share of a segment: sub-tile `warp` of each tile.
+  template <bool CAREFUL>
+  __device__ __forceinline__ void run(const Params& p, const Seg& g, uint8_t* ring, uint32_t qaddr, const int (&pos)[MT][2],
+                                      const float (&qs)[MT][2], int warp, int lane) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) { m[mt][i] = -INFINITY; l[mt][i] = 0.0f; }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.0f;
+    }
+    const uint32_t rs = smem_u32(ring);
+    const int n = g.t1 - g.t0, b0 = g.t0 * TK + warp * WT;
+    int page = page_of(p, g, b0, lane);
+#pragma unroll
+    for (int i = 0; i < K::S; ++i) {
+      const int next = i + 1 < n ? page_of(p, g, b0 + (i + 1) * TK, lane) : 0;
+      if (i < n) issue(p, g, rs + i * K::STAGE, b0 + i * TK, page, lane);
+      copy_commit();
+      page = next;
+    }
+    // a sub-tile in [all_lo, all_hi] is seen by every row in full
+    const int all_lo = p.a.window > 0 ? g.len - p.a.window : 0, all_hi = g.len - p.a.T;
+    int slot = 0;
+    for (int i = 0; i < n; ++i) {
+      const int base = b0 + i * TK;
+      copy_wait<K::S - 1>();
+      __syncwarp();
+      const int next = i + K::S + 1 < n ? page_of(p, g, base + (K::S + 1) * TK, lane) : 0;
+      if (base < g.len && base + WT > g.first)
+        tile<CAREFUL>(p, g, rs + slot * K::STAGE, ring + slot * K::STAGE + K::SUB, qaddr, base, pos, qs,
+                      base >= all_lo && base + WT - 1 <= all_hi, lane);
+      __syncwarp();
+      if (i + K::S < n) issue(p, g, rs + slot * K::STAGE, base + K::S * TK, page, lane);
+      copy_commit();
+      page = next;
+      slot = slot + 1 == K::S ? 0 : slot + 1;
+    }
+    copy_wait<0>();
+    __syncwarp();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[mt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][i], 1);
+        l[mt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][i], 2);
+      }
+  }
+  __device__ __forceinline__ bool all_finite() const {
+    float x = 0.0f;  // a product with 0 keeps NaN and makes it of an infinity
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x = fmaf(o[mt][n][e], 0.0f, x);
+    return __all_sync(0xFFFFFFFFu, x == 0.0f);
+  }
+};
+
+// q rows of an item as 16-bit parts in shared memory; rscale: each row's power of two (e4m3 cache).
+template <class Q, class C, int D, int MT>
+__device__ __forceinline__ void stage_q(const Params& p, uint8_t* qsm, float* rscale, int b, int hk, int r0, int warp, int lane) {
+  using K = Cfg<Q, C, D, MT>;
+  const AttnArgs& a = p.a;
+  const int R = a.T * a.G;
+  for (int r = warp; r < K::ROWS; r += NW) {
+    float x[D / 32];
+    const int row = r0 + r;
+    if (row < R) {
+      const int t = row / a.G, h = hk * a.G + row - t * a.G;
+      const Q* src = static_cast<const Q*>(a.q) + (static_cast<int64_t>(b) * a.T + t) * a.q_stride + static_cast<int64_t>(h) * D;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) x[i] = q_value(src[lane + 32 * i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) x[i] = 0.0f;
+    }
+    float back = 1.0f;
+    if constexpr (K::F8) {
+      float mx = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) mx = fmaxf(mx, fabsf(x[i]));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+      // largest value into [2^13, 2^14); the factor and its inverse stay normal numbers
+      const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const float f = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+      back = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) x[i] *= f;
+    }
+    if (lane == 0) rscale[r] = back;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int d = lane + 32 * i;
+      // e4m3: four neighbouring dims come in one register, so a k-step's slots hold them in this order
+      const int c = d & 15, slot = K::F8 ? (d & ~15) + ((c >> 2) * 2 + (c & 1)) + ((c & 2) ? 8 : 0) : d;
+      float v = x[i];
+#pragma unroll
+      for (int t = 0; t < K::NQ; ++t) {
+        const uint32_t w = pack2<K::F8>(v, 0.0f);
+        *reinterpret_cast<uint16_t*>(qsm + (t * K::ROWS + r) * K::QB + 2 * slot) = static_cast<uint16_t>(w);
+        v -= unpack2<K::F8>(w).x;
+      }
+    }
+  }
+}
+
+template <class Q, class C, int D, int MT>
+__global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, MT>::CPS)) attn_kernel(const __grid_constant__ Params p) {
+  using K = Cfg<Q, C, D, MT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_scan[NTH];
+  __shared__ int s_last;
+  float* rscale = reinterpret_cast<float*>(smem);  // [ROWS]
+  float* s_m = rscale + K::ROWS;                   // [ROWS] joined maximum
+  float* s_i = s_m + K::ROWS;                      // [ROWS] 1 / weight sum
+  float* w_ml = s_i + K::ROWS;                     // [NW][ROWS][2] each warp's maximum and weight sum
+  uint8_t* qsm = smem + K::HDR;
+  uint8_t* ring = smem + K::FIXED;
+  const AttnArgs& a = p.a;
+  int64_t* prefix = reinterpret_cast<int64_t*>(ring + K::S * NW * K::STAGE);  // [B + 1] tiles before each sequence
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- the line of tiles (every sequence has at least one, so that its rows are written)
+  const int64_t room = a.max_pages << a.page_shift;
+  auto length = [&](int b, bool tell) {
+    const int n = __ldg(a.seq_lens + b);
+    if (n > room) {
+      if (tell) record_error(a.err, DEV_ERR_PAGE);
+      return static_cast<int>(room);
+    }
+    return max(n, 0);
+  };
+  auto first_of = [&](int len) { return a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0; };
+  auto tiles_of = [&](int len) { return max(1, (len + TK - 1) / TK - first_of(len) / TK); };
+  const int per = (a.B + NTH - 1) / NTH;
+  {
+    const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
+    int64_t n = 0;
+    for (int b = b0; b < b1; ++b) n += tiles_of(length(b, blockIdx.x == 0));
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - n;
+    for (int w = 0; w < warp; ++w) before += s_scan[w];
+    for (int b = b0; b < b1; ++b) {
+      prefix[b] = before;
+      before += tiles_of(length(b, false));
+      if (b == a.B - 1) prefix[a.B] = before;
+    }
+    __syncthreads();
+  }
+  const int64_t HR = static_cast<int64_t>(a.c.n_kv_heads) * p.RT;
+  const int64_t total = prefix[a.B] * HR;
+  const int64_t nc = total < gridDim.x ? total : gridDim.x, c = blockIdx.x;
+  if (c >= nc) return;
+  const int64_t lo = c * total / nc, hi = (c + 1) * total / nc;
+
+  for (int64_t u = lo; u < hi;) {
+    int b = 0;  // the last sequence that starts at or before u
+    for (int w = 1 << (31 - __clz(a.B)); w > 0; w >>= 1)
+      if (b + w < a.B && prefix[b + w] * HR <= u) b += w;
+    const int nt = static_cast<int>(prefix[b + 1] - prefix[b]);
+    const int64_t in = u - prefix[b] * HR;
+    const int hr = static_cast<int>(in / nt), hk = hr / p.RT, rt = hr - hk * p.RT;
+    const int64_t i0 = prefix[b] * HR + static_cast<int64_t>(hr) * nt, i1 = i0 + nt;  // the item
+    const int64_t end = i1 < hi ? i1 : hi;
+    Seg g;
+    g.len = length(b, false);
+    g.first = first_of(g.len);
+    g.table = a.page_table + b * a.max_pages;
+    g.head_off = hk * a.c.head_stride;
+    g.t0 = static_cast<int>(u - i0) + g.first / TK;
+    g.t1 = static_cast<int>(end - i0) + g.first / TK;
+    const int r0 = rt * K::ROWS, R = min(K::ROWS, a.T * a.G - r0);
+
+    stage_q<Q, C, D, MT>(p, qsm, rscale, b, hk, r0, warp, lane);
+    __syncthreads();
+    int pos[MT][2];
+    float qs[MT][2];
+    const float f = a.scale * a.c.k_scale * (a.softcap > 0.0f ? 1.0f / a.softcap : 1.4426950408889634f);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 16 * mt + (lane >> 2) + 8 * i;
+        pos[mt][i] = g.len - a.T + min((r0 + r) / a.G, a.T - 1);
+        qs[mt][i] = f * rscale[r];
+      }
+    Warp<Q, C, D, MT> w;
+    uint8_t* mine = ring + warp * (K::S * K::STAGE);
+    w.template run<false>(p, g, mine, smem_u32(qsm), pos, qs, warp, lane);
+    if (!w.all_finite()) {
+      Warp<Q, C, D, MT> again;  // an object of its own: the call in it keeps this one out of registers
+      again.template run<true>(p, g, mine, smem_u32(qsm), pos, qs, warp, lane);
+      w = again;
+    }
+
+    // ---- the warps' sums, side by side in the ring's place
+    float* so = reinterpret_cast<float*>(mine);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 16 * mt + (lane >> 2) + 8 * i;
+        if ((lane & 3) == 0) {
+          w_ml[(warp * K::ROWS + r) * 2] = w.m[mt][i];
+          w_ml[(warp * K::ROWS + r) * 2 + 1] = w.l[mt][i];
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          if constexpr (K::F8) {
+            if (n & 1) continue;
+            *reinterpret_cast<float4*>(so + r * D + 16 * (n >> 1) + 4 * (lane & 3)) =
+                make_float4(w.o[mt][n][2 * i], w.o[mt][n + 1][2 * i], w.o[mt][n][2 * i + 1], w.o[mt][n + 1][2 * i + 1]);
+          } else {
+            *reinterpret_cast<float2*>(so + r * D + 8 * n + 2 * (lane & 3)) = make_float2(w.o[mt][n][2 * i], w.o[mt][n][2 * i + 1]);
+          }
+        }
+      }
+    __syncthreads();
+    const bool whole = u == i0 && end == i1;
+    const int slot = static_cast<int>(2 * c + (lo >= i0 ? 1 : 0));  // the range starts in this item (1), or before it (0)
+    auto write = [&](int r, int d, float x, float y, float inv) {
+      const int row = r0 + r, t = row / a.G, h = hk * a.G + row - t * a.G;
+      put2(static_cast<Q*>(a.out) + ((static_cast<int64_t>(b) * a.T + t) * a.Hq + h) * D + d, x * inv, y * inv);
+    };
+    for (int x = threadIdx.x; x < R * (D / 2); x += NTH) {
+      const int r = x / (D / 2), d = 2 * (x % (D / 2));
+      float mm = -INFINITY, ll = 0.0f, ox = 0.0f, oy = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) mm = fmaxf(mm, w_ml[(k * K::ROWS + r) * 2]);
+      const float ms = mm == -INFINITY ? 0.0f : mm;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) {
+        const float e = ex2(w_ml[(k * K::ROWS + r) * 2] - ms);
+        const float2 v = *reinterpret_cast<const float2*>(ring + k * (K::S * K::STAGE) + (r * D + d) * 4);
+        ll += w_ml[(k * K::ROWS + r) * 2 + 1] * e;
+        ox += v.x * e;
+        oy += v.y * e;
+      }
+      if (whole) {
+        write(r, d, ox, oy, ll == 0.0f ? 0.0f : a.c.v_scale / ll);
+      } else {
+        *reinterpret_cast<float2*>(p.part + (static_cast<int64_t>(slot) * K::ROWS + r) * D + d) = make_float2(ox, oy);
+        if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * K::ROWS + r) * 2) = make_float2(mm, ll);
+      }
+    }
+    if (!whole) {
+      // ---- the last CTA of the item to arrive joins the ranges' sums
+      const int64_t ca = ((i0 + 1) * nc - 1) / total, cb = (i1 * nc - 1) / total;  // first and last range
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        int* cnt = p.count + (static_cast<int64_t>(b) * HR + hr);
+        const int got = atomicAdd(cnt, 1);
+        s_last = got == static_cast<int>(cb - ca);
+        if (s_last) *cnt = 0;
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        auto slot_of = [&](int64_t k) { return 2 * k + (k * total / nc >= i0 ? 1 : 0); };
+        for (int r = warp; r < R; r += NW) {
+          float mm = -INFINITY, ll = 0.0f;
+          for (int64_t k = ca + lane; k <= cb; k += 32)
+            mm = fmaxf(mm, __ldcg(p.part_ml + (slot_of(k) * K::ROWS + r) * 2));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+          const float ms = mm == -INFINITY ? 0.0f : mm;
+          for (int64_t k = ca + lane; k <= cb; k += 32) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (slot_of(k) * K::ROWS + r) * 2));
+            ll += v.y * ex2(v.x - ms);
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o);
+          if (lane == 0) {
+            s_m[r] = ms;
+            s_i[r] = ll == 0.0f ? 0.0f : a.c.v_scale / ll;
+          }
+        }
+        __syncthreads();
+        for (int x = threadIdx.x; x < R * (D / 2); x += NTH) {
+          const int r = x / (D / 2), d = 2 * (x % (D / 2));
+          float ox = 0.0f, oy = 0.0f;
+#pragma unroll 4
+          for (int64_t k = ca; k <= cb; ++k) {
+            const int64_t s = slot_of(k) * K::ROWS + r;
+            const float e = ex2(__ldcg(p.part_ml + s * 2) - s_m[r]);
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part + s * D + d));
+            ox += v.x * e;
+            oy += v.y * e;
+          }
+          write(r, d, ox, oy, s_i[r]);
+        }
+      }
+    }
+    __syncthreads();
+    u = end;
+  }
+}
+
+template <class Q, class C, int D, int MT>
+cudaError_t launch_one(const Params& p, cudaStream_t st) {
+  using K = Cfg<Q, C, D, MT>;
+  const size_t smem = K::SMEM + 8 * (static_cast<size_t>(p.a.B) + 1);
+  static int set[64] = {0};  // shared memory allowed so far, per device
+  const int dev = current_device_id();
+  if (set[dev] < static_cast<int>(smem)) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_kernel<Q, C, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    set[dev] = static_cast<int>(smem);
+  }
+  return launch_pdl(attn_kernel<Q, C, D, MT>, dim3(num_sms() * K::CPS), dim3(NTH), smem, st, p);
+}
+
+}  // namespace attn
+
+// One translation unit per cache type (rows: query rows per pass, 16 or 32).
+cudaError_t launch_attn_bf16(const attn::Params& p, int q_bf16, int rows, cudaStream_t st);
+cudaError_t launch_attn_f8(const attn::Params& p, int q_bf16, int rows, cudaStream_t st);
+
+}  // namespace kq

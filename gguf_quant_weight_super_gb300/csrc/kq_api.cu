@@ -465,7 +465,7 @@ kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, in
 }
 
 size_t kq_sample_workspace_size(int64_t M, int64_t V) {
-  if (M < 0 || V < 1 || M > INT32_MAX || V > (1 << 20)) return 0;
+  if (M < 0 || V < 1 || M > (1 << 24) || V > (1 << 20)) return 0;
   return sample_workspace_bytes(M, V);
 }
 
@@ -473,7 +473,7 @@ kq_status kq_sample(const void* logits, int dtype, int64_t row_stride, int64_t M
                     const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                     int32_t* ids, float* probs, void* workspace, size_t workspace_bytes, kq_stream_t stream) {
   if (!float_dtype(dtype) || M < 0 || V < 0 || row_stride < 0) return KQ_ERR_ARG;
-  if (V < 1 || V > (1 << 20) || M > INT32_MAX) return KQ_ERR_UNSUPPORTED;
+  if (V < 1 || V > (1 << 20) || M > (1 << 24)) return KQ_ERR_UNSUPPORTED;
   if (M == 0) return KQ_OK;
   if (!logits || !u || !ids) return KQ_ERR_ARG;
   if (!aligned(logits, dtype == KQ_BF16 ? 2 : 4) || !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||

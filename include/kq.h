@@ -523,7 +523,7 @@ kq_status kq_attn_decode(const kq_kv_cache *cache, const int32_t *page_table, in
  *   probs  [M] fp32 or NULL: the token's share of the kept weights (0 for -1)
  * Weights are fp32 exponentials summed exactly, in units of 2^-40 of the
  * largest: the result depends on the arguments alone.
- * V in 1..2^20 (else KQ_ERR_UNSUPPORTED).  workspace: kq_sample_workspace_size
+ * V in 1..2^20, M up to 2^24 (else KQ_ERR_UNSUPPORTED).  workspace: kq_sample_workspace_size
  * bytes, 256-byte aligned, zero-filled once before first use; one call at a
  * time per workspace.  logits 4-byte (KQ_F32) or 2-byte aligned.
  */

@@ -13,18 +13,21 @@
 // Bound: each logit is read once from memory (bytes), and behind that a chain
 // of dependent steps per row (latency).  A row is a cluster of up to 8 CTAs.
 //  * One pass finds each thread's largest logit, and from the threads' largest
-//    ones a threshold with at least as many words above it as the row needs
-//    (top_k of them, else 64); the few words above it are listed.  No CTA
-//    waits for another up to here.  Only a row without top_k takes a second
-//    pass (from L2): its total weight.
+//    ones a threshold with about as many words above it as the row needs
+//    (top_k of them, else 1024 in all).  While the CTAs exchange their largest
+//    logits each works out its threshold.
+//  * The words above it are listed; a row without top_k sums its total weight
+//    in the same second pass (from L2), others only look again where a thread's
+//    largest logit is above the threshold.
 //  * The first CTA sorts the lists and makes the cuts and the choice on the
-//    sorted prefix.  Words it lists are complete above the highest threshold,
-//    so whatever falls inside is final.
+//    sorted words.  They are complete above the highest of the CTAs'
+//    thresholds, so what falls inside is final.
 //  * A row whose cut or token falls outside (flat distributions, large top_k)
-//    goes on with histograms of counts and weights over the whole row, 1024
-//    bins at a time, until the words of the bin that holds the answer fit the
-//    list; equal logits are told apart by index as further digits of the
-//    sorting key.
+//    goes on with histograms over the whole row: counts by the distance to the
+//    largest logit, which bound the running weights and so bracket the bin
+//    that holds the answer; exact weights in 1024 finer bins of the bracket;
+//    where even such a bin has more words than the list, 1024 bins of the next
+//    digits of the words' sorting key at a time, the index being the last.
 #include "kq_cache.h"
 
 namespace kq {
@@ -32,18 +35,23 @@ namespace {
 
 constexpr int STH = 512;      // threads per CTA
 constexpr int SW = STH / 32;
-constexpr int CAND = 1024;    // words a CTA lists
-constexpr int LIST = 2048;    // words the first CTA sorts
-constexpr int BINS = 1024;
-constexpr int TOPK_FAST = 256;  // top_k up to here by thresholds (of 512 threads' largest logits)
+constexpr int CAND = 2048;    // words a CTA lists
+constexpr int LIST = 2048;    // words the first CTA works on
+constexpr int BINS = 1024;    // two per thread
+constexpr int WANT = 1024;    // words to list in all for a row without top_k
+constexpr int TOPK_FAST = 1024;  // top_k up to here by thresholds
 constexpr float kSpan = 29.0f;  // exp(-29) < 2^-41: words this far below the largest weigh nothing
 constexpr int kIdxBits = 20;
 
-struct Cmd {  // from the first CTA to the others
-  int done;
-  int bin0, shift;  // the words looked at: of level-0 bin `bin0` (-1: all), with the key digits above shift + 10 of `pre`
-  unsigned long long pre;
-  int gather;       // list the words of digit `pre >> shift` (level 0: of bin0)
+// Which words the cluster looks at next, and what for: from the first CTA to the others.
+enum : int { kCount, kWeigh, kDigits, kGather, kStop };
+struct Cmd {
+  int what;
+  int bin_lo, bin_hi;      // level-0 bins of the bracket
+  float fine;              // finer bins per level-0 bin
+  int at;                  // the finer bin (kDigits, kGather)
+  int shift;               // kDigits: by the key's 10 bits above shift; kGather: of the key's digits above shift
+  unsigned long long pre;  // those digits
 };
 
 struct Smem {
@@ -55,11 +63,11 @@ struct Smem {
   float red_f[SW];
   unsigned long long mass;      // this CTA's sum
   unsigned long long tau;       // its threshold, as the largest sorting key that is listed for sure
-  int ncand, nlist, overflow;
+  int ncand, nlist, done;
   float bmax;
   Cmd cmd;
-  unsigned long long found_cv, found_before;  // locate()'s answer
-  int pick, pick_c;
+  unsigned long long found_cv, found_before;  // the word at which a running sum passes, and the sum before it
+  int pick, pick_lo, pick_c, pick_n;
   unsigned long long pick_m;
 };
 
@@ -79,32 +87,41 @@ __device__ __forceinline__ void each4(const __nv_bfloat16*, uint4 v, int i, F f)
   f(i + 4, bf16_lo(v.z)), f(i + 5, bf16_hi(v.z)), f(i + 6, bf16_lo(v.w)), f(i + 7, bf16_hi(v.w));
 }
 
-// f(index, logit) for every word of this CTA's share of the row: 16-byte chunks by address, single loads where a chunk
-// reaches past the row.
-template <class X, class F>
-__device__ __forceinline__ void each_word(const X* row, int V, int rank, int CS, F f) {
-  constexpr int E = 16 / static_cast<int>(sizeof(X)), U = 4;
+// Every word of this CTA's share of the row: chunk(index, 16 bytes) for whole chunks by address, U of them in flight per
+// thread (U = 0: none), and word(index, logit) for the up to 14 words outside whole chunks.
+template <int U, class X, class FC, class FW>
+__device__ __forceinline__ void each_chunk(const X* row, int V, int rank, int CS, FC chunk, FW word) {
+  constexpr int E = 16 / static_cast<int>(sizeof(X));
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(X)) % E);
-  const int n = (V + off + E - 1) / E, step = CS * STH;
-  for (int c0 = rank * STH + static_cast<int>(threadIdx.x); c0 < n; c0 += U * step) {
-    uint4 v[U];
-    bool full[U];
+  const int head = off ? min(V, E - off) : 0, chunks = (V - head) / E, tail = V - head - chunks * E;
+  const uint4* body = reinterpret_cast<const uint4*>(row + head);
+  const int step = CS * STH;
+#pragma unroll 1
+  for (int c = rank * STH + static_cast<int>(threadIdx.x); U > 0 && c < chunks; c += U * step) {
+    uint4 v[U > 0 ? U : 1];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int i = (c0 + k * step) * E - off;
-      full[k] = i >= 0 && i + E <= V;
-      if (full[k]) v[k] = __ldg(reinterpret_cast<const uint4*>(row + i));
-    }
+    for (int k = 0; k < U; ++k)
+      if (c + k * step < chunks) v[k] = __ldg(body + c + k * step);
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int i = (c0 + k * step) * E - off;
-      if (full[k]) {
-        each4(row, v[k], i, f);
-      } else if (c0 + k * step < n) {
-        for (int j = max(i, 0); j < min(i + E, V); ++j) f(j, one(row + j));
-      }
-    }
+    for (int k = 0; k < U; ++k)
+      if (c + k * step < chunks) chunk(head + (c + k * step) * E, v[k]);
   }
+  if (rank == 0 && static_cast<int>(threadIdx.x) < head + tail) {
+    const int t = threadIdx.x, i = t < head ? t : V - 1 - (t - head);
+    word(i, one(row + i));
+  }
+}
+// The same, word(index, logit) for all of them.
+template <int U, class X, class F>
+__device__ __forceinline__ void each_word(const X* row, int V, int rank, int CS, F word) {
+  each_chunk<U>(row, V, rank, CS, [&](int i, uint4 v) { each4(row, v, i, word); }, word);
+}
+__device__ __forceinline__ float largest(const float*, uint4 v) {
+  return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+__device__ __forceinline__ float largest(const __nv_bfloat16*, uint4 v) {
+  const float x = fmaxf(fmaxf(bf16_lo(v.x), bf16_hi(v.x)), fmaxf(bf16_lo(v.y), bf16_hi(v.y)));
+  return fmaxf(x, fmaxf(fmaxf(bf16_lo(v.z), bf16_hi(v.z)), fmaxf(bf16_lo(v.w), bf16_hi(v.w))));
 }
 
 // Words compare by their sorting key, ascending: the logit's bits in an order that compares as integers, inverted, then
@@ -127,7 +144,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 struct Row {
   float lmax, c;  // c = log2(e) / temperature
-  float zs;       // level-0 bins per unit of logit
+  float zs;       // level-0 bins per unit of logit (exp(-1/zs) per bin, whatever the temperature)
   __device__ __forceinline__ float weight(float l) const { return l == lmax ? 1.0f : ex2((l - lmax) * c); }
   // the weight in units of 2^-40 as 2^20 hi + lo, |lo| <= 2^19 (adding 1.5 * 2^23 rounds to an integer)
   __device__ __forceinline__ void parts(float l, int& hi, int& lo) const {
@@ -141,8 +158,11 @@ struct Row {
     parts(l, hi, lo);
     return static_cast<unsigned long long>((static_cast<long long>(hi) << 20) + lo);
   }
-  __device__ __forceinline__ int bin(float l) const {
-    return l == lmax ? 0 : static_cast<int>(fminf((lmax - l) * zs, static_cast<float>(BINS - 1)));
+  // the distance to the largest logit in level-0 bins
+  __device__ __forceinline__ float depth(float l) const { return l == lmax ? 0.0f : fminf((lmax - l) * zs, BINS - 1.0f); }
+  __device__ __forceinline__ int bin(float l) const { return static_cast<int>(depth(l)); }
+  __device__ __forceinline__ int fine_bin(float depth, const Cmd& c) const {
+    return static_cast<int>(fminf((depth - c.bin_lo) * c.fine, BINS - 1.0f));
   }
 };
 
@@ -178,21 +198,26 @@ __device__ __forceinline__ void block_scan(Smem& s, unsigned long long& m, int& 
   m = im;
   c = ic;
 }
-// Sorts s.list[0, n) ascending, n <= LIST.
-__device__ void sort_list(Smem& s, int n) {
-  int size = 2;
+// Sorts s.list[0, n) ascending, n <= LIST.  A warp's 32 threads compare within the same 64 places while the stride is 32
+// or less: only wider steps need the whole block's barrier.
+__device__ __noinline__ void sort_list(Smem& s, int n) {
+  int size = 64;
   while (size < n) size <<= 1;
   for (int i = n + threadIdx.x; i < size; i += STH) s.list[i] = ~0ull;
   __syncthreads();
-  for (int k = 2; k <= size; k <<= 1)
+  for (int k = 2; k <= size; k <<= 1) {
     for (int j = k >> 1; j > 0; j >>= 1) {
       for (int t = threadIdx.x; t < size / 2; t += STH) {
         const int i = 2 * t - (t & (j - 1)), x = i + j;  // i has bit j clear
         const unsigned long long a = s.list[i], b = s.list[x];
         if ((a > b) == ((i & k) == 0)) { s.list[i] = b; s.list[x] = a; }
       }
-      __syncthreads();
+      if (j > 32) __syncthreads();
+      else __syncwarp();
     }
+    if (k >= 64) __syncthreads();  // the next step is a wide one
+  }
+  __syncthreads();
 }
 
 // ---- another CTA's shared memory
@@ -219,40 +244,40 @@ __device__ __forceinline__ int peer_add(uint32_t addr, int v) {
   return r;
 }
 
-// The four words of the sorted list that thread t holds, and what lies before them.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The four words of the sorted list that thread t holds, and the weight before them.
 struct Held {
-  unsigned long long cv[LIST / STH], w[LIST / STH], before;
-  int n;
+  unsigned long long w[LIST / STH], before;
 };
 __device__ __forceinline__ Held hold(Smem& s, const Row& r, int n) {
   Held h;
-  unsigned long long m = 0;
+  h.before = 0;
   int c = 0;
-  h.n = 0;
 #pragma unroll
   for (int i = 0; i < LIST / STH; ++i) {
     const int j = static_cast<int>(threadIdx.x) * (LIST / STH) + i;
-    h.cv[i] = j < n ? s.list[j] : 0;
-    h.w[i] = j < n ? r.units(logit_of(h.cv[i])) : 0;
-    m += h.w[i];
-    h.n += j < n;
+    h.w[i] = j < n ? r.units(logit_of(s.list[j])) : 0;
+    h.before += h.w[i];
   }
-  block_scan(s, m, c);
-  h.before = m;
+  block_scan(s, h.before, c);
   return h;
 }
-// The held word at which the running sum passes x: s.found_cv, s.found_before and s.pick (its place, else -1).
-__device__ __forceinline__ bool pass_at(Smem& s, const Held& h, unsigned long long base, unsigned long long x) {
+// The held word at which the running sum, from base on, passes x (by_count: the x-th of the list): found_cv, found_before;
+// false where there is none.
+__device__ __forceinline__ bool pass_at(Smem& s, const Held& h, unsigned long long base, unsigned long long x, bool by_count) {
   __syncthreads();
   if (threadIdx.x == 0) s.pick = -1;
   __syncthreads();
   unsigned long long c = base + h.before;
 #pragma unroll
   for (int i = 0; i < LIST / STH; ++i) {
-    if (c <= x && x < c + h.w[i]) {
-      s.found_cv = h.cv[i];
+    const int j = static_cast<int>(threadIdx.x) * (LIST / STH) + i;
+    if (by_count ? static_cast<unsigned long long>(j) == x && h.w[i] > 0 : c <= x && x < c + h.w[i]) {
+      s.found_cv = s.list[j];
       s.found_before = c;
-      s.pick = static_cast<int>(threadIdx.x) * (LIST / STH) + i;
+      s.pick = j;
     }
     c += h.w[i];
   }
@@ -260,126 +285,374 @@ __device__ __forceinline__ bool pass_at(Smem& s, const Held& h, unsigned long lo
   return s.pick >= 0;
 }
 
-// Over the whole row, every CTA of the cluster: the word at which the running sum of weights (by_count: of words)
-// passes x; found_cv and found_before (the weight before it) in the first CTA, false there when there is none.
-template <class X>
-__device__ bool locate(Smem& s, const X* row, int V, int rank, int CS, const Row& r, unsigned long long x, bool by_count) {
-  unsigned long long base_m = 0, base_c = 0;
-  if (threadIdx.x == 0 && rank == 0) {
-    s.cmd.bin0 = -1;
-    s.cmd.shift = 0;
-    s.cmd.pre = 0;
-    s.cmd.gather = 0;
+// The running sums that the last kept word passes for top_p (kept: the words with less than p * total before them) and
+// that the token passes for u, as integers: f * total exactly, f being a 64-bit fraction.
+__device__ __forceinline__ unsigned long long fraction(float f) {  // 0 <= f < 1
+  const uint32_t b = __float_as_uint(f);
+  const int sh = static_cast<int>(b >> 23) - 86;
+  const unsigned long long man = (b & 0x7FFFFFu) | 0x800000u;
+  return sh >= 0 ? man << sh : sh > -24 ? man >> -sh : 0;
+}
+__device__ __forceinline__ unsigned long long nucleus(float p, unsigned long long total) {
+  if (!(p > 0.0f)) return 0;
+  const unsigned long long f = fraction(p), hi = __umul64hi(f, total);
+  return f * total != 0 || hi == 0 ? hi : hi - 1;
+}
+__device__ __forceinline__ unsigned long long share(float u, unsigned long long total) {
+  if (!(u > 0.0f)) return 0;
+  return u < 1.0f ? __umul64hi(fraction(u), total) : total - 1;
+}
+__device__ __forceinline__ void write_row(const SampleArgs& a, int m, const Row& r, unsigned long long cv,
+                                          unsigned long long total) {
+  a.ids[m] = static_cast<int>(cv & ((1u << kIdxBits) - 1));
+  if (a.probs) a.probs[m] = __ull2float_rn(r.units(logit_of(cv))) / __ull2float_rn(total);
+}
+
+// The cuts and the choice on n <= 128 listed words, by one warp: s.list[0, n) in any order, four words per lane.  total: the
+// row's weight where k is 0.  Returns whether the answer lies in the list (found_cv and the kept weight in `total`, in
+// every lane).
+__device__ __forceinline__ bool choose_in_warp(Smem& s, const Row& r, int n, bool complete, int k, float p, float mp, float u,
+                                               unsigned long long& total, unsigned long long& cv_out) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31;
+  unsigned long long v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = 4 * lane + e < n ? s.list[4 * lane + e] : ~0ull;
+  // bitonic over place 4 lane + e
+#pragma unroll
+  for (int k2 = 2; k2 <= 128; k2 <<= 1) {
+#pragma unroll
+    for (int j = k2 >> 1; j >= 4; j >>= 1) {
+      const bool low = (lane & (j >> 2)) == 0, up = k2 == 128 || ((4 * lane) & k2) == 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const unsigned long long o = __shfl_xor_sync(kAll, v[e], j >> 2);
+        v[e] = (v[e] < o) == (low == up) ? v[e] : o;
+      }
+    }
+#pragma unroll
+    for (int j = k2 >> 1 < 2 ? k2 >> 1 : 2; j > 0; j >>= 1)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!(e & j)) {
+          const bool up = k2 == 128 || ((4 * lane + e) & k2) == 0;
+          const unsigned long long x = v[e], y = v[e | j];
+          if ((x > y) == up) { v[e] = y; v[e | j] = x; }
+        }
   }
+  unsigned long long w[4], before = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    w[e] = 4 * lane + e < n ? r.units(logit_of(v[e])) : 0;
+    before += w[e];
+  }
+  const unsigned long long mine = before;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long t = __shfl_up_sync(kAll, before, o);
+    if (lane >= o) before += t;
+  }
+  const unsigned long long sum = __shfl_sync(kAll, before, 31);
+  before -= mine;
+  // the word at which the running sum passes x, and the sum with it
+  auto pass = [&](unsigned long long x, unsigned long long& cv, unsigned long long& with) {
+    unsigned long long c = before;
+    bool here = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (c <= x && x < c + w[e]) { here = true; cv = v[e]; with = c + w[e]; }
+      c += w[e];
+    }
+    const uint32_t who = __ballot_sync(kAll, here);
+    if (!who) return false;
+    cv = __shfl_sync(kAll, cv, __ffs(who) - 1);
+    with = __shfl_sync(kAll, with, __ffs(who) - 1);
+    return true;
+  };
+  unsigned long long cv = 0, with = 0;
+  if (k > 0) {
+    if (k > n && !complete) return false;
+    unsigned long long t = before;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (4 * lane + e < k) t += w[e];
+    total = k >= n ? sum : __shfl_sync(kAll, t, (k - 1) >> 2);
+  }
+  if (p < 1.0f) {
+    if (!pass(nucleus(p, total), cv, with)) return false;
+    total = min(total, with);
+  }
+  if (mp > 0.0f) {
+    unsigned long long t = 0;
+    bool below = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool in = 4 * lane + e < n;
+      if (in && r.weight(logit_of(v[e])) >= fminf(mp, 1.0f)) t += w[e];
+      else below |= in;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kAll, t, o);
+    if (__any_sync(kAll, below) || complete) total = min(total, t);
+    else if (k == 0 && !(p < 1.0f)) return false;  // the cut lies past the list
+  }
+  return pass(share(u, total), cv_out, with);
+}
+
+// This CTA's sum of the weights that `take` takes, into s.mass.  also(index, chunk): what else is done with each chunk.
+template <class X, class F, class G>
+__device__ __forceinline__ void sum_where(Smem& s, const X* row, int V, int rank, int CS, const Row& r, F take, G also) {
+  uint32_t hi = 0;  // a thread has at most 2^11 words (2^20 of a row, 512 threads)
+  int lo = 0;
+  auto word = [&](int i, float l) {
+    int h, g;
+    r.parts(l, h, g);
+    if (take(i, l)) { hi += h; lo += g; }
+  };
+  each_chunk<sizeof(X) == 4 ? 4 : 2>(
+      row, V, rank, CS,
+      [&](int i, uint4 v) {
+        also(i, v);
+        each4(row, v, i, word);
+      },
+      word);
+  const unsigned long long t = block_sum(s, static_cast<unsigned long long>((static_cast<long long>(hi) << 20) + lo));
+  if (threadIdx.x == 0) s.mass = t;
+}
+// Lists the words of a chunk (a single word: of a chunk of others at -inf) from `cut` up.
+template <class X>
+__device__ __noinline__ void list_chunk(Smem& s, const X* row, int i, uint4 v, float cut) {
+  each4(row, v, i, [&](int j, float l) {
+    if (l >= cut && l > -INFINITY) {
+      const int at = atomicAdd(&s.ncand, 1);
+      if (at < CAND) s.cand[at] = sort_key(l, j);
+    }
+  });
+}
+
+__device__ __forceinline__ unsigned long long cluster_mass(Smem& s, int CS) {
+  unsigned long long t = 0;
+  for (int q = 0; q < CS; ++q) t += peer64(at_rank(&s.mass, q));
+  return t;
+}
+
+// ---- the whole-row path
+
+// A histogram's two bins of this thread, and what lies before them.
+struct Bins {
+  unsigned long long m[2], pm;
+  int c[2], pc;
+};
+// Weights are up to 2^40: three sums of 14 bits each, of at most 2^18 words.
+__device__ __forceinline__ void add_weight(Smem& s, int d, unsigned long long w) {
+  const uint32_t l0 = static_cast<uint32_t>(w) & 0x3FFFu, l1 = static_cast<uint32_t>(w >> 14) & 0x3FFFu,
+                 l2 = static_cast<uint32_t>(w >> 28);
+  if (l0) atomicAdd(&s.limb[0][d], l0);
+  if (l1) atomicAdd(&s.limb[1][d], l1);
+  if (l2) atomicAdd(&s.limb[2][d], l2);
+}
+// The sum of the cluster's histograms.
+__device__ __forceinline__ Bins read_bins(Smem& s, int CS, bool weights) {
+  Bins h;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) { h.m[e] = 0; h.c[e] = 0; }
+#pragma unroll 2
+  for (int k = 0; k < CS; ++k)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int b = 2 * threadIdx.x + e;
+      h.c[e] += static_cast<int>(peer32(at_rank(&s.count[b], k)));
+      if (weights)
+        h.m[e] += static_cast<unsigned long long>(peer32(at_rank(&s.limb[0][b], k))) +
+                  (static_cast<unsigned long long>(peer32(at_rank(&s.limb[1][b], k))) << 14) +
+                  (static_cast<unsigned long long>(peer32(at_rank(&s.limb[2][b], k))) << 28);
+    }
+  h.pm = h.m[0] + h.m[1];
+  h.pc = h.c[0] + h.c[1];
+  block_scan(s, h.pm, h.pc);
+  return h;
+}
+// The bin in which the running sum of weights (by_count: of words), from base on, passes x: s.pick (-1: none), s.pick_m
+// and s.pick_c before it, s.pick_n words in it.
+__device__ __forceinline__ void pick_bin(Smem& s, const Bins& h, unsigned long long base_m, int base_c,
+                                         unsigned long long x, bool by_count) {
+  __syncthreads();
+  if (threadIdx.x == 0) s.pick = -1;
+  __syncthreads();
+  unsigned long long m = base_m + h.pm;
+  int c = base_c + h.pc;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const unsigned long long before = by_count ? c : m, in = by_count ? h.c[e] : h.m[e];
+    if (before <= x && x < before + in) {
+      s.pick = 2 * threadIdx.x + e;
+      s.pick_m = m;
+      s.pick_c = c;
+      s.pick_n = h.c[e];
+    }
+    m += h.m[e];
+    c += h.c[e];
+  }
+  __syncthreads();
+}
+// The bins that can hold the word at which the running weight passes x, from the counts alone: a word of bin b weighs
+// between exp(-(b + 1) d) and exp(-b d), d = kSpan / BINS; the margin covers the rounding of all of it.
+__device__ __forceinline__ void bracket(Smem& s, const Bins& h, unsigned long long x) {
+  unsigned long long up[2], low[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float b = static_cast<float>(2 * threadIdx.x + e), c = static_cast<float>(h.c[e]) * 1099511627776.0f;
+    constexpr float d = kSpan / BINS * 1.4426950408889634f;
+    up[e] = static_cast<unsigned long long>(ceilf(c * fminf(ex2(-b * d) * 1.0001f, 1.0f))) + h.c[e];
+    low[e] = static_cast<unsigned long long>(c * ex2(-(b + 1.0f) * d) * 0.9999f);
+    low[e] -= low[e] < static_cast<unsigned long long>(h.c[e]) ? low[e] : h.c[e];  // units are rounded, too
+    if (2 * threadIdx.x + e == BINS - 1) low[e] = 0;  // also what lies deeper
+  }
+  unsigned long long pu = up[0] + up[1], pl = low[0] + low[1];
+  int none = 0;
+  block_scan(s, pu, none);
+  block_scan(s, pl, none);
+  __syncthreads();
+  if (threadIdx.x == 0) { s.pick_lo = BINS - 1; s.pick = BINS - 1; }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int b = 2 * threadIdx.x + e;
+    if (pu <= x && x < pu + up[e]) s.pick_lo = b;
+    if (pl <= x && x < pl + low[e]) s.pick = b;
+    pu += up[e];
+    pl += low[e];
+  }
+  __syncthreads();
+}
+
+// Over the whole row, every CTA of the cluster: the word at which the running sum of weights (by_count: of words that
+// weigh anything) passes x; found_cv and, by weight, found_before in the first CTA, false there when there is none.  h0:
+// the row's counts by level-0 bin, made by the first call (have = false).
+template <class X>
+__device__ __noinline__ bool locate(Smem& s, const X* row, int V, int rank, int CS, const Row& r_in, unsigned long long x,
+                                    bool by_count, Bins& h0, bool have) {
+  const Row r = r_in;  // a copy that no store can change
+  constexpr int UL = sizeof(X) == 4 ? 4 : 2;
+  unsigned long long base_m = 0;
+  int base_c = 0;
   bool found = true;
+  auto start = [&] {  // the counts are known: the bracket, or the bin itself
+    if (by_count) {
+      pick_bin(s, h0, 0, 0, x, true);
+      found = s.pick >= 0;
+      if (found) base_c = s.pick_c;
+      if (threadIdx.x == 0) s.pick_lo = s.pick;
+      __syncthreads();
+    } else {
+      bracket(s, h0, x);
+    }
+    if (threadIdx.x == 0) {
+      s.cmd.bin_lo = s.pick_lo;
+      s.cmd.bin_hi = s.pick;
+      s.cmd.fine = static_cast<float>(BINS) / static_cast<float>(s.pick - s.pick_lo + 1);
+      s.cmd.what = found ? kWeigh : kStop;
+    }
+    __syncthreads();
+  };
+  auto narrow = [&](const Bins& h, int shift, unsigned long long pre, bool digits) {
+    pick_bin(s, h, base_m, base_c, x, by_count);
+    found = s.pick >= 0;
+    if (found) { base_m = s.pick_m; base_c = s.pick_c; }
+    if (threadIdx.x == 0) {
+      const bool fits = s.pick_n <= LIST;
+      if (digits)
+        s.cmd.pre = (shift + 10 < 52 ? pre >> (shift + 10) << (shift + 10) : 0) | (static_cast<unsigned long long>(s.pick) << shift);
+      else
+        s.cmd.at = s.pick;
+      s.cmd.shift = digits ? (fits ? shift : shift - 10) : (fits ? 64 : 42);
+      s.cmd.what = !found ? kStop : fits ? kGather : kDigits;
+    }
+    __syncthreads();
+  };
+  if (rank == 0) {
+    if (threadIdx.x == 0) s.cmd.what = kCount;
+    if (have) start();
+  }
   for (;;) {
     if (threadIdx.x == 0) s.nlist = 0;
     cluster_sync();  // the command is written, the first CTA's list is empty, and it is done with the histograms
-    for (int i = threadIdx.x; i < BINS; i += STH) { s.count[i] = 0; s.limb[0][i] = 0; s.limb[1][i] = 0; s.limb[2][i] = 0; }
-    __syncthreads();
-    const int bin0 = static_cast<int>(peer32(at_rank(&s.cmd.bin0, 0)));
-    const int shift = static_cast<int>(peer32(at_rank(&s.cmd.shift, 0)));
-    const int gather = static_cast<int>(peer32(at_rank(&s.cmd.gather, 0)));
-    const unsigned long long pre = peer64(at_rank(&s.cmd.pre, 0));
-    if (gather == 2) {
+    Cmd c;
+    c.what = static_cast<int>(peer32(at_rank(&s.cmd.what, 0)));
+    c.bin_lo = static_cast<int>(peer32(at_rank(&s.cmd.bin_lo, 0)));
+    c.bin_hi = static_cast<int>(peer32(at_rank(&s.cmd.bin_hi, 0)));
+    c.fine = __uint_as_float(peer32(at_rank(&s.cmd.fine, 0)));
+    c.at = static_cast<int>(peer32(at_rank(&s.cmd.at, 0)));
+    c.shift = static_cast<int>(peer32(at_rank(&s.cmd.shift, 0)));
+    c.pre = peer64(at_rank(&s.cmd.pre, 0));
+    if (c.what == kStop) {
       cluster_sync();  // every CTA has read the command
       break;
     }
-    const uint32_t list0 = at_rank(s.list, 0), nlist0 = at_rank(&s.nlist, 0);
-    each_word(row, V, rank, CS, [&](int i, float l) {
-      if (!(l > -INFINITY)) return;
-      const unsigned long long w = r.units(l);
-      if (w == 0) return;
-      const int b = r.bin(l);
-      int d = b;
-      if (bin0 >= 0) {
-        if (b != bin0) return;
-        const unsigned long long cv = sort_key(l, i);
-        if (gather) {
-          if (shift < 64 && (cv >> shift) != (pre >> shift)) return;
+    for (int i = threadIdx.x; i < BINS; i += STH) { s.count[i] = 0; s.limb[0][i] = 0; s.limb[1][i] = 0; s.limb[2][i] = 0; }
+    __syncthreads();
+    if (c.what == kCount) {
+      each_word<UL>(row, V, rank, CS, [&](int, float l) {
+        int h, g;
+        r.parts(l, h, g);
+        if (l > -INFINITY && (h | g)) atomicAdd(&s.count[r.bin(l)], 1u);
+      });
+    } else if (c.what == kWeigh) {
+      uint32_t hi = 0;
+      int lo = 0;
+      each_word<UL>(row, V, rank, CS, [&](int, float l) {
+        if (!(l > -INFINITY)) return;
+        const float z = r.depth(l);
+        const int b = static_cast<int>(z);
+        if (b > c.bin_hi) return;
+        int h, g;
+        r.parts(l, h, g);
+        if (b < c.bin_lo) {
+          hi += h;
+          lo += g;
+        } else if (h | g) {
+          const int d = r.fine_bin(z, c);
+          atomicAdd(&s.count[d], 1u);
+          add_weight(s, d, static_cast<unsigned long long>((static_cast<long long>(h) << 20) + g));
+        }
+      });
+      const unsigned long long t = block_sum(s, static_cast<unsigned long long>((static_cast<long long>(hi) << 20) + lo));
+      if (threadIdx.x == 0) s.mass = t;
+    } else {
+      const uint32_t list0 = at_rank(s.list, 0), nlist0 = at_rank(&s.nlist, 0);
+      each_word<UL>(row, V, rank, CS, [&](int i, float l) {
+        if (!(l > -INFINITY)) return;
+        const float z = r.depth(l);
+        const int b = static_cast<int>(z);
+        if (b < c.bin_lo || b > c.bin_hi || r.fine_bin(z, c) != c.at) return;
+        const unsigned long long cv = sort_key(l, i), w = r.units(l);
+        if (w == 0) return;
+        if (c.what == kGather) {
+          if (c.shift < 64 && (cv >> c.shift) != (c.pre >> c.shift)) return;
           const int at = peer_add(nlist0, 1);
           if (at < LIST) peer_store64(list0 + 8 * at, cv);
-          return;
+        } else {
+          if (c.shift + 10 < 52 && (cv >> (c.shift + 10)) != (c.pre >> (c.shift + 10))) return;
+          const int d = static_cast<int>(cv >> c.shift) & (BINS - 1);
+          atomicAdd(&s.count[d], 1u);
+          add_weight(s, d, w);
         }
-        if (shift + 10 < 52 && (cv >> (shift + 10)) != (pre >> (shift + 10))) return;
-        d = static_cast<int>(cv >> shift) & (BINS - 1);
-      }
-      atomicAdd(&s.count[d], 1u);
-      atomicAdd(&s.limb[0][d], static_cast<uint32_t>(w) & 0x3FFFu);
-      atomicAdd(&s.limb[1][d], static_cast<uint32_t>(w >> 14) & 0x3FFFu);
-      atomicAdd(&s.limb[2][d], static_cast<uint32_t>(w >> 28));
-    });
+      });
+    }
     cluster_sync();
     if (rank != 0) continue;
-    if (gather) {
+    if (c.what == kGather) {
       const int n = min(s.nlist, LIST);
       sort_list(s, n);
-      if (by_count) {  // the place in the list is known
-        const int at = static_cast<int>(x - base_c);
-        const Held h = hold(s, r, n);
-        unsigned long long c = base_m + h.before;
-#pragma unroll
-        for (int i = 0; i < LIST / STH; ++i) {
-          if (static_cast<int>(threadIdx.x) * (LIST / STH) + i == at) { s.found_cv = h.cv[i]; s.found_before = c; }
-          c += h.w[i];
-        }
-        __syncthreads();
-      } else {
-        pass_at(s, hold(s, r, n), base_m, x);
-      }
-      if (threadIdx.x == 0) s.cmd.gather = 2;
-      continue;
+      pass_at(s, hold(s, r, n), base_m, by_count ? x - base_c : x, by_count);
+      if (threadIdx.x == 0) s.cmd.what = kStop;
+    } else if (c.what == kCount) {
+      h0 = read_bins(s, CS, false);
+      start();
+    } else {
+      if (c.what == kWeigh && !by_count) base_m = cluster_mass(s, CS);
+      narrow(read_bins(s, CS, true), c.shift, c.pre, c.what == kDigits);
     }
-    // the cluster's histogram: two neighbouring bins per thread
-    unsigned long long m[2] = {0, 0};
-    int c[2] = {0, 0};
-    for (int k = 0; k < CS; ++k)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int b = 2 * threadIdx.x + e;
-        c[e] += static_cast<int>(peer32(at_rank(&s.count[b], k)));
-        m[e] += static_cast<unsigned long long>(peer32(at_rank(&s.limb[0][b], k))) +
-                (static_cast<unsigned long long>(peer32(at_rank(&s.limb[1][b], k))) << 14) +
-                (static_cast<unsigned long long>(peer32(at_rank(&s.limb[2][b], k))) << 28);
-      }
-    unsigned long long pm = m[0] + m[1];
-    int pc = c[0] + c[1];
-    block_scan(s, pm, pc);
-    __syncthreads();
-    if (threadIdx.x == 0) s.pick = -1;
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const unsigned long long before = by_count ? base_c + pc : base_m + pm, in = by_count ? c[e] : m[e];
-      if (before <= x && x < before + in) {
-        s.pick = 2 * threadIdx.x + e;
-        s.pick_m = base_m + pm;
-        s.pick_c = static_cast<int>(base_c) + pc;
-        s.nlist = c[e];
-      }
-      pm += m[e];
-      pc += c[e];
-    }
-    __syncthreads();
-    const int pick = s.pick, in_bin = s.nlist;
-    if (pick >= 0) { base_m = s.pick_m; base_c = s.pick_c; }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      if (pick < 0) {
-        s.cmd.gather = 2;
-      } else if (bin0 < 0) {
-        s.cmd.bin0 = pick;
-        s.cmd.shift = in_bin <= LIST ? 64 : 42;
-        s.cmd.gather = in_bin <= LIST;
-      } else {
-        const unsigned long long p = (shift + 10 < 52 ? pre >> (shift + 10) << (shift + 10) : 0) |
-                                     (static_cast<unsigned long long>(pick) << shift);
-        s.cmd.pre = p;
-        s.cmd.gather = in_bin <= LIST;
-        if (in_bin > LIST) s.cmd.shift = shift - 10;
-      }
-    }
-    found = pick >= 0;
     __syncthreads();
   }
   return found;
@@ -396,31 +669,40 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
   const X* row = static_cast<const X*>(a.logits) + m * a.row_stride;
   float temp = a.temperature ? __ldg(a.temperature + m) : 1.0f;
   int k = a.top_k ? __ldg(a.top_k + m) : 0;
+  const float p = a.top_p ? __ldg(a.top_p + m) : 1.0f, mp = a.min_p ? __ldg(a.min_p + m) : 0.0f;
+  const float u = __ldg(a.u + m);
+
+  // ---- each thread's largest logit, and the CTA's
+  for (int i = tid; i < BINS; i += STH) s.count[i] = 0;
+  float mine = -INFINITY;
+  each_chunk<8>(
+      row, V, rank, CS, [&](int, uint4 v) { mine = fmaxf(mine, largest(row, v)); },
+      [&](int, float l) { mine = fmaxf(mine, l); });
+  float mx = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+  if (lane == 0) s.red_f[warp] = mx;
+  if (tid == 0) { s.ncand = 0; s.done = 0; s.pick = BINS; }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < SW; ++i) mx = fmaxf(mx, s.red_f[i]);
+  if (tid == 0) s.bmax = mx;
+  cluster_arrive();
+
+  // ---- meanwhile the threshold: the smallest of the threads' largest logits in the first bins that hold enough of them
   if (!(temp > 0.0f)) {  // the largest logit
     temp = 1.0f;
     k = 1;
   }
   if (k < 0 || k >= V) k = 0;
-  const float p = a.top_p ? __ldg(a.top_p + m) : 1.0f, mp = a.min_p ? __ldg(a.min_p + m) : 0.0f;
-  const float u = __ldg(a.u + m);
-
-  // ---- this CTA's words above its threshold
-  if (tid == 0) { s.ncand = 0; s.overflow = 0; s.tau = 0; s.cmd.done = 0; }
-  for (int i = tid; i < BINS; i += STH) s.count[i] = 0;
-  float mine = -INFINITY;
-  each_word(row, V, rank, CS, [&](int, float l) { mine = fmaxf(mine, l); });
-  float mx = mine;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-  if (lane == 0) s.red_f[warp] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < SW; ++i) mx = fmaxf(mx, s.red_f[i]);
+  const bool by_top_k = k > 0 && k <= TOPK_FAST;
   Row r;
   r.lmax = mx;
   r.c = 1.4426950408889634f / temp;
   r.zs = static_cast<float>(BINS) / kSpan / temp;
-  const int want = k > 0 && k <= TOPK_FAST ? max(k, 16) : 64;
+  // with n words above the threshold spread over the threads at random, 1 - exp(-n / threads) of them have one
+  const float per = static_cast<float>(by_top_k ? k + k / 4 + 32 : WANT) / static_cast<float>(CS);
+  const int want = max(8, static_cast<int>(STH * (1.0f - __expf(-fminf(per, 1200.0f) / STH))));
   const bool some = mine > -INFINITY && (mine == mx || (mx - mine) * r.zs < static_cast<float>(BINS));
   const int bin = some ? r.bin(mine) : BINS;
   if (some) atomicAdd(&s.count[bin], 1u);
@@ -430,191 +712,231 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
     const int c0 = s.count[2 * tid], c1 = s.count[2 * tid + 1];
     int before = c0 + c1;
     block_scan(s, none, before);
-    if (tid == 0) s.pick = BINS;  // all of them: the list is complete
-    __syncthreads();
     if (before < want && before + c0 >= want) s.pick = 2 * tid;
     else if (before + c0 < want && before + c0 + c1 >= want) s.pick = 2 * tid + 1;
-    __syncthreads();
   }
-  const int last = s.pick;
-  // the threshold: the smallest of the threads' largest logits in the bins up to `last`, or what weighs anything
-  float cut = INFINITY;
-  if (last < BINS) {
-    if (some && bin <= last) cut = mine;
+  __syncthreads();
+  const int last = s.pick;  // BINS: there are not enough; then all that weighs anything is listed
+  float cut = some && bin <= last ? mine : INFINITY;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) cut = fminf(cut, __shfl_xor_sync(0xFFFFFFFFu, cut, o));
-    if (lane == 0) s.red_f[warp] = cut;
-    __syncthreads();
+  for (int o = 16; o > 0; o >>= 1) cut = fminf(cut, __shfl_xor_sync(0xFFFFFFFFu, cut, o));
+  if (lane == 0) s.red_f[warp] = cut;
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < SW; ++i) cut = fminf(cut, s.red_f[i]);
-    if (tid == 0) s.tau = sort_key(cut, V - 1);
-  } else {
-    cut = mx - kSpan * temp;
-    if (tid == 0) s.tau = ~0ull;
+  for (int i = 0; i < SW; ++i) cut = fminf(cut, s.red_f[i]);
+  if (last == BINS) cut = mx - kSpan * temp;
+  if (tid == 0) s.tau = last == BINS ? ~0ull : sort_key(cut, V - 1);
+  cluster_wait();
+  {
+    const float other = lane < CS ? __uint_as_float(peer32(at_rank(&s.bmax, lane))) : -INFINITY;
+    mx = fmaxf(mx, other);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    mx = __shfl_sync(0xFFFFFFFFu, mx, 0);
   }
-  if (mine > -INFINITY && mine >= cut)
-    each_word(row, V, rank, CS, [&](int i, float l) {
-      if (l >= cut && l > -INFINITY) {
-        const int at = atomicAdd(&s.ncand, 1);
-        if (at < CAND) s.cand[at] = sort_key(l, i);
-        else s.overflow = 1;
-      }
-    });
-  if (tid == 0) s.bmax = mx;
-  cluster_sync();
-
-  // ---- the row's largest logit; its total weight where top_k does not bound it
-  for (int q = 0; q < CS; ++q) mx = fmaxf(mx, __uint_as_float(peer32(at_rank(&s.bmax, q))));
   r.lmax = mx;
-  if (mx == -INFINITY) {  // no word is left
-    if (rank == 0 && tid == 0) {
-      a.ids[m] = -1;
-      if (a.probs) a.probs[m] = 0.0f;
+
+  // ---- the words above the threshold; the row's total weight where top_k does not bound it
+  auto list = [&](int i, uint4 v) {
+    if (largest(row, v) >= cut) list_chunk(s, row, i, v, cut);
+  };
+  auto list_one = [&](int i, float l) {
+    if (l >= cut && l > -INFINITY) {
+      const int at = atomicAdd(&s.ncand, 1);
+      if (at < CAND) s.cand[at] = sort_key(l, i);
     }
-    cluster_sync();
-    return;
+  };
+  if (by_top_k) {
+    if (mine >= cut) each_chunk<4>(row, V, rank, CS, list, list_one);
+  } else {
+    sum_where(
+        s, row, V, rank, CS, r,
+        [&](int, float l) { return l > -INFINITY; }, list);
+    each_chunk<0>(row, V, rank, CS, list, list_one);
   }
-  auto sum_where = [&](auto take) {  // over the CTA's words
-    uint32_t hi = 0;  // a thread has at most 2^11 words (2^20 of a row, 512 threads)
-    int lo = 0;
-    each_word(row, V, rank, CS, [&](int, float l) {
-      int h, g;
-      r.parts(l, h, g);
-      if (take(l)) { hi += h; lo += g; }
-    });
-    const unsigned long long t =
-        block_sum(s, static_cast<unsigned long long>((static_cast<long long>(hi) << 20) + lo));
-    if (tid == 0) s.mass = t;
-  };
-  auto cluster_mass = [&] {
-    unsigned long long t = 0;
-    for (int q = 0; q < CS; ++q) t += peer64(at_rank(&s.mass, q));
-    return t;
-  };
-  unsigned long long total = 0;  // of the words kept
-  if (k == 0 || k > TOPK_FAST) sum_where([](float l) { return l > -INFINITY; });
   cluster_sync();
 
   // ---- the cuts and the choice on the listed words, in the first CTA
+  unsigned long long total = 0;  // weight of the words kept
   if (rank == 0) {
-    unsigned long long tau = ~0ull;
-    bool good = true;
-    for (int q = 0; q < CS; ++q) {
-      const unsigned long long t = peer64(at_rank(&s.tau, q));
-      tau = t < tau ? t : tau;
-      good = good && !peer32(at_rank(&s.overflow, q));
-    }
     if (tid == 0) s.nlist = 0;
+    unsigned long long tau = lane < CS ? peer64(at_rank(&s.tau, lane)) : ~0ull;
+    const int listed = lane < CS ? static_cast<int>(peer32(at_rank(&s.ncand, lane))) : 0;
+    unsigned long long sum = lane < CS && !by_top_k ? peer64(at_rank(&s.mass, lane)) : 0;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      tau = min(tau, __shfl_xor_sync(0xFFFFFFFFu, tau, o));
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    }
+    tau = __shfl_sync(0xFFFFFFFFu, tau, 0);
+    sum = __shfl_sync(0xFFFFFFFFu, sum, 0);
+    const bool fits = __all_sync(0xFFFFFFFFu, listed <= CAND);
+    const bool complete = tau == ~0ull;  // the list holds every word that weighs anything
+    const int q = warp % CS;             // SW / CS warps fetch each list
+    const int nq = min(__shfl_sync(0xFFFFFFFFu, listed, q), CAND);
     __syncthreads();
-    for (int q = 0; q < CS; ++q) {
-      const int n = min(static_cast<int>(peer32(at_rank(&s.ncand, q))), CAND);
-      const uint32_t from = at_rank(s.cand, q);
-      for (int i = tid; i < n; i += STH) {
-        const unsigned long long cv = peer64(from + 8 * i);
-        if (cv <= tau) {
-          const int at = atomicAdd(&s.nlist, 1);
-          if (at < LIST) s.list[at] = cv;
-        }
+    const uint32_t from = at_rank(s.cand, q);
+    for (int i = (warp / CS) * 32 + lane; i < nq; i += SW / CS * 32) {
+      const unsigned long long cv = peer64(from + 8 * i);
+      if (cv <= tau) {
+        const int at = atomicAdd(&s.nlist, 1);
+        if (at < LIST) s.list[at] = cv;
       }
     }
     __syncthreads();
     const int n = s.nlist;
-    good = good && n <= LIST && (k <= TOPK_FAST);
-    if (good) {
-      const bool complete = tau == ~0ull;  // the list holds every word that weighs anything
-      sort_list(s, n);
-      Held h = hold(s, r, n);
-      if (k > 0) {  // the words past the first k weigh nothing from here on
-        good = complete || k <= n;
-        unsigned long long t = 0;
+    bool good = fits && n <= LIST && n > 0 && (k == 0 || by_top_k);
+    if (mx == -INFINITY) {  // no word is left
+      if (tid == 0) {
+        a.ids[m] = -1;
+        if (a.probs) a.probs[m] = 0.0f;
+        s.done = 1;
+      }
+    } else if (good) {
+      // first on the (at most 128) words nearest to the largest: by halving, a depth with 64 to 128 words above it
+      constexpr int FEW = 128;
+      int few = n;
+      if (n > FEW && k <= FEW) {
+        unsigned long long cv[LIST / STH];
+        float z[LIST / STH];
 #pragma unroll
         for (int i = 0; i < LIST / STH; ++i) {
-          if (tid * (LIST / STH) + i >= k) h.w[i] = 0;
-          t += h.w[i];
+          const int j = tid + i * STH;
+          cv[i] = j < n ? s.list[j] : ~0ull;
+          z[i] = j < n ? r.depth(logit_of(cv[i])) : 4.0f * BINS;
         }
-        total = block_sum(s, t);
-      } else {
-        total = cluster_mass();
-      }
-      if (good && p < 1.0f) {
-        const double want_m = static_cast<double>(p) * static_cast<double>(total);
-        unsigned long long x = want_m > 1.0 ? static_cast<unsigned long long>(ceil(want_m)) - 1 : 0;
-        if (x >= total) x = total - 1;
-        good = pass_at(s, h, 0, x);
-        if (good) total = s.found_before + r.units(logit_of(s.found_cv));
-      }
-      if (good && mp > 0.0f) {
-        unsigned long long t = 0;
-        int below = 0;  // some listed word is below min_p: the cut is inside the list
+        float lo = 0.0f, hi = static_cast<float>(BINS);
+        for (int step = 0; step < 14; ++step) {
+          const float mid = 0.5f * (lo + hi);
+          int c = 0;
 #pragma unroll
-        for (int i = 0; i < LIST / STH; ++i) {
-          if (tid * (LIST / STH) + i >= n) continue;
-          const float w = r.weight(logit_of(h.cv[i]));
-          if (w >= fminf(mp, 1.0f)) t += h.w[i];
-          else below = 1;
+          for (int i = 0; i < LIST / STH; ++i) {
+            const uint32_t in = __ballot_sync(0xFFFFFFFFu, z[i] <= mid);
+            c += __popc(in);
+          }
+          if (lane == 0) s.scan_c[warp] = c;
+          __syncthreads();
+          c = lane < SW ? s.scan_c[lane] : 0;
+          c = __reduce_add_sync(0xFFFFFFFFu, c);
+          __syncthreads();
+          few = c;
+          if (c > FEW) hi = mid;
+          else if (c < max(k, FEW / 2)) lo = mid;
+          else { lo = mid; break; }
         }
-        below = __syncthreads_or(below);
-        t = block_sum(s, t);
-        if (below || complete) total = t < total ? t : total;
-        else good = k > 0 || p < 1.0f;  // the cut lies past the list, and past the other cut where there is one
+        if (few <= FEW && few >= max(k, 1)) {
+          // they go first: every word is in a register
+          if (tid == 0) s.nlist = 0;
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < LIST / STH; ++i)
+            if (z[i] <= lo) s.list[atomicAdd(&s.nlist, 1)] = cv[i];
+          if (tid == 0) s.pick = few;
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < LIST / STH; ++i)
+            if (z[i] > lo && cv[i] != ~0ull) s.list[atomicAdd(&s.pick, 1)] = cv[i];
+        } else {
+          few = n;
+        }
+        __syncthreads();
       }
-      if (good) {
-        const double uw = static_cast<double>(u) * static_cast<double>(total);
-        unsigned long long x = uw > 0.0 ? static_cast<unsigned long long>(uw) : 0;
-        if (x >= total) x = total - 1;
-        good = pass_at(s, h, 0, x);
+      total = sum;
+      bool found = false;
+      if (few <= FEW) {
+        if (warp == 0) {
+          unsigned long long cv = 0, kept = total;
+          found = choose_in_warp(s, r, few, complete && few == n, k, p, mp, u, kept, cv);
+          if (found && lane == 0) {
+            write_row(a, m, r, cv, kept);
+            s.done = 1;
+          }
+        }
+        found = __syncthreads_or(found);
+      }
+      if (!found && n > FEW) {
+        sort_list(s, n);
+        const Held h = hold(s, r, n);
+        if (k > 0) {
+          if (pass_at(s, h, 0, static_cast<unsigned long long>(k) - 1, true)) {
+            total = s.found_before + r.units(logit_of(s.found_cv));
+          } else {  // fewer weigh anything: all of them, if they are listed
+            good = complete || k <= n;
+            unsigned long long t = 0;
+#pragma unroll
+            for (int i = 0; i < LIST / STH; ++i) t += h.w[i];
+            total = block_sum(s, t);
+          }
+        }
+        if (good && p < 1.0f) {
+          good = pass_at(s, h, 0, nucleus(p, total), false);
+          if (good) total = min(total, s.found_before + r.units(logit_of(s.found_cv)));
+        }
+        if (good && mp > 0.0f) {
+          unsigned long long t = 0;
+          int below = 0;  // some listed word is below min_p: the cut is inside the list
+#pragma unroll
+          for (int i = 0; i < LIST / STH; ++i) {
+            const int j = tid * (LIST / STH) + i;
+            if (j < n && r.weight(logit_of(s.list[j])) >= fminf(mp, 1.0f)) t += h.w[i];
+            else below |= j < n;
+          }
+          below = __syncthreads_or(below);
+          t = block_sum(s, t);
+          if (below || complete) total = min(total, t);
+          else good = k > 0 || p < 1.0f;  // the cut lies past the list, and past the other cut where there is one
+        }
+        if (good) good = pass_at(s, h, 0, share(u, total), false);
         if (good && tid == 0) {
-          a.ids[m] = static_cast<int>(s.found_cv & ((1u << kIdxBits) - 1));
-          if (a.probs)
-            a.probs[m] = static_cast<float>(static_cast<double>(r.units(logit_of(s.found_cv))) / static_cast<double>(total));
+          write_row(a, m, r, s.found_cv, total);
+          s.done = 1;
         }
       }
     }
-    if (tid == 0) s.cmd.done = good;
   }
   cluster_sync();
-  const bool done = peer32(at_rank(&s.cmd.done, 0)) != 0;
-  total = cluster_mass();
+  const bool done = peer32(at_rank(&s.done, 0)) != 0;
   cluster_sync();
   if (done) return;
 
   // ---- the same cuts over the whole row
+  Bins h0;
+  bool have = false;
+  auto none = [](int, uint4) {};
+  if (by_top_k) {
+    sum_where(s, row, V, rank, CS, r, [](int, float l) { return l > -INFINITY; }, none);
+    cluster_sync();
+  }
+  total = cluster_mass(s, CS);
+  cluster_sync();
   if (k > 0) {
-    if (k <= TOPK_FAST) {
-      sum_where([](float l) { return l > -INFINITY; });
+    const bool some_k = locate(s, row, V, rank, CS, r, static_cast<unsigned long long>(k) - 1, true, h0, have);
+    have = true;
+    if (rank == 0 && tid == 0) s.pick = some_k;
+    cluster_sync();
+    const bool cut_k = peer32(at_rank(&s.pick, 0)) != 0;  // else fewer words weigh anything
+    const unsigned long long kth = peer64(at_rank(&s.found_cv, 0));
+    cluster_sync();
+    if (cut_k) {
+      sum_where(s, row, V, rank, CS, r, [&](int i, float l) { return l > -INFINITY && sort_key(l, i) <= kth; }, none);
       cluster_sync();
-      total = cluster_mass();
+      total = cluster_mass(s, CS);
+      cluster_sync();
     }
-    if (locate(s, row, V, rank, CS, r, static_cast<unsigned long long>(k) - 1, true) && rank == 0)
-      total = s.found_before + r.units(logit_of(s.found_cv));
   }
   if (p < 1.0f) {
-    const double want_m = static_cast<double>(p) * static_cast<double>(total);
-    unsigned long long x = want_m > 1.0 ? static_cast<unsigned long long>(ceil(want_m)) - 1 : 0;
-    if (x >= total) x = total - 1;
-    locate(s, row, V, rank, CS, r, x, false);
-    if (rank == 0) {
-      const unsigned long long t = s.found_before + r.units(logit_of(s.found_cv));
-      total = t < total ? t : total;
-    }
+    locate(s, row, V, rank, CS, r, nucleus(p, total), false, h0, have);
+    have = true;
+    if (rank == 0) total = min(total, s.found_before + r.units(logit_of(s.found_cv)));
   }
   if (mp > 0.0f) {
+    sum_where(s, row, V, rank, CS, r, [&](int, float l) { return l > -INFINITY && r.weight(l) >= fminf(mp, 1.0f); }, none);
     cluster_sync();
-    sum_where([&](float l) { return l > -INFINITY && r.weight(l) >= fminf(mp, 1.0f); });
+    total = min(total, cluster_mass(s, CS));
     cluster_sync();
-    const unsigned long long t = cluster_mass();
-    total = t < total ? t : total;
   }
-  const double uw = static_cast<double>(u) * static_cast<double>(total);
-  unsigned long long x = uw > 0.0 ? static_cast<unsigned long long>(uw) : 0;
-  if (x >= total) x = total - 1;
-  locate(s, row, V, rank, CS, r, x, false);
-  if (rank == 0 && tid == 0) {
-    a.ids[m] = static_cast<int>(s.found_cv & ((1u << kIdxBits) - 1));
-    if (a.probs)
-      a.probs[m] = static_cast<float>(static_cast<double>(r.units(logit_of(s.found_cv))) / static_cast<double>(total));
-  }
-  cluster_sync();
+  locate(s, row, V, rank, CS, r, share(u, total), false, h0, have);
+  if (rank == 0 && tid == 0) write_row(a, m, r, s.found_cv, total);
 }
 
 }  // namespace
@@ -627,6 +949,14 @@ cudaError_t launch_sample(const SampleArgs& a, int bf16, cudaStream_t st) {
   int CS = 1;
   while (CS < 8 && static_cast<int64_t>(a.M) * CS * 2 <= 4 * num_sms() && a.V / (CS * 2) >= 4096) CS *= 2;
   while (CS < 8 && a.V / CS > (1 << 18)) CS *= 2;
+  auto* kernel = bf16 ? sample_kernel<__nv_bfloat16> : sample_kernel<float>;
+  static bool smem_set[64][2] = {{false}};
+  bool& set = smem_set[current_device_id()][bf16 ? 1 : 0];
+  if (!set) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
+    if (e != cudaSuccess) return e;
+    set = true;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.M) * CS);
   cfg.blockDim = dim3(STH);
@@ -641,8 +971,7 @@ cudaError_t launch_sample(const SampleArgs& a, int bf16, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return bf16 ? cudaLaunchKernelEx(&cfg, sample_kernel<__nv_bfloat16>, a, CS)
-              : cudaLaunchKernelEx(&cfg, sample_kernel<float>, a, CS);
+  return cudaLaunchKernelEx(&cfg, kernel, a, CS);
 }
 
 }  // namespace kq

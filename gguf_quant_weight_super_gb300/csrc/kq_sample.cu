@@ -38,7 +38,8 @@ constexpr int SW = STH / 32;
 constexpr int CAND = 2048;    // words a CTA lists
 constexpr int LIST = 2048;    // words the first CTA works on
 constexpr int BINS = 1024;    // two per thread
-constexpr int WANT = 1024;    // words to list in all for a row without top_k
+constexpr int WANT = 1280;    // words to list in all for a row without top_k
+constexpr int FEW = 64;       // words that one warp decides on
 constexpr int TOPK_FAST = 1024;  // top_k up to here by thresholds
 constexpr float kSpan = 29.0f;  // exp(-29) < 2^-41: words this far below the largest weigh nothing
 constexpr int kIdxBits = 20;
@@ -58,12 +59,13 @@ struct Smem {
   uint32_t count[BINS], limb[3][BINS];
   unsigned long long list[LIST];
   unsigned long long cand[CAND];
+  unsigned long long few[FEW];
   unsigned long long scan_m[SW], red_m[SW];
-  int scan_c[SW];
+  int scan_c[2 * SW];
   float red_f[SW];
   unsigned long long mass;      // this CTA's sum
   unsigned long long tau;       // its threshold, as the largest sorting key that is listed for sure
-  int ncand, nlist, done;
+  int ncand, nlist, nfew, done;
   float bmax;
   Cmd cmd;
   unsigned long long found_cv, found_before;  // the word at which a running sum passes, and the sum before it
@@ -308,95 +310,83 @@ __device__ __forceinline__ void write_row(const SampleArgs& a, int m, const Row&
   if (a.probs) a.probs[m] = __ull2float_rn(r.units(logit_of(cv))) / __ull2float_rn(total);
 }
 
-// The cuts and the choice on n <= 128 listed words, by one warp: s.list[0, n) in any order, four words per lane.  total: the
-// row's weight where k is 0.  Returns whether the answer lies in the list (found_cv and the kept weight in `total`, in
-// every lane).
-__device__ __forceinline__ bool choose_in_warp(Smem& s, const Row& r, int n, bool complete, int k, float p, float mp, float u,
-                                               unsigned long long& total, unsigned long long& cv_out) {
+// A place in a list for each lane that is `on` (every lane of the warp calls it).
+__device__ __forceinline__ int push_at(int* counter, bool on) {
+  const uint32_t who = __ballot_sync(0xFFFFFFFFu, on);
+  const int lane = threadIdx.x & 31;
+  int base = 0;
+  if (lane == 0 && who) base = atomicAdd(counter, __popc(who));
+  return __shfl_sync(0xFFFFFFFFu, base, 0) + __popc(who & ((1u << lane) - 1u));
+}
+
+// The cuts and the choice on n <= FEW listed words, by one warp: v[0, n) in any order, two words per lane.  total: the
+// row's weight where k is 0.  Returns whether the answer lies in the list; then cv_out and the kept weight in `total`.
+// Runs once per row: loops stay rolled, since what it costs is fetching its code.
+__device__ __noinline__ bool choose_in_warp(const unsigned long long* list, const Row r, int n, bool complete, int k, float p,
+                                            float mp, float u, unsigned long long& total, unsigned long long& cv_out) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31;
-  unsigned long long v[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = 4 * lane + e < n ? s.list[4 * lane + e] : ~0ull;
-  // bitonic over place 4 lane + e
-#pragma unroll
-  for (int k2 = 2; k2 <= 128; k2 <<= 1) {
-#pragma unroll
-    for (int j = k2 >> 1; j >= 4; j >>= 1) {
-      const bool low = (lane & (j >> 2)) == 0, up = k2 == 128 || ((4 * lane) & k2) == 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const unsigned long long o = __shfl_xor_sync(kAll, v[e], j >> 2);
-        v[e] = (v[e] < o) == (low == up) ? v[e] : o;
-      }
+  unsigned long long v0 = lane < n ? list[lane] : ~0ull, v1 = lane + 32 < n ? list[lane + 32] : ~0ull;
+  // bitonic over places lane and lane + 32
+#pragma unroll 1
+  for (int k2 = 2; k2 <= 32; k2 <<= 1)
+#pragma unroll 1
+    for (int j = k2 >> 1; j > 0; j >>= 1) {
+      const unsigned long long o0 = __shfl_xor_sync(kAll, v0, j), o1 = __shfl_xor_sync(kAll, v1, j);
+      const bool least = ((lane & j) == 0) == ((lane & k2) == 0);  // k2 = 32: the lower half ascends, the upper descends
+      v0 = (v0 < o0) == least ? v0 : o0;
+      v1 = (v1 < o1) == (k2 == 32 ? (lane & j) != 0 : least) ? v1 : o1;
     }
-#pragma unroll
-    for (int j = k2 >> 1 < 2 ? k2 >> 1 : 2; j > 0; j >>= 1)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (!(e & j)) {
-          const bool up = k2 == 128 || ((4 * lane + e) & k2) == 0;
-          const unsigned long long x = v[e], y = v[e | j];
-          if ((x > y) == up) { v[e] = y; v[e | j] = x; }
-        }
+  if (v0 > v1) { const unsigned long long x = v0; v0 = v1; v1 = x; }
+#pragma unroll 1
+  for (int j = 16; j > 0; j >>= 1) {
+    const unsigned long long o0 = __shfl_xor_sync(kAll, v0, j), o1 = __shfl_xor_sync(kAll, v1, j);
+    const bool least = (lane & j) == 0;
+    v0 = (v0 < o0) == least ? v0 : o0;
+    v1 = (v1 < o1) == least ? v1 : o1;
   }
-  unsigned long long w[4], before = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    w[e] = 4 * lane + e < n ? r.units(logit_of(v[e])) : 0;
-    before += w[e];
-  }
-  const unsigned long long mine = before;
-#pragma unroll
+  const unsigned long long w0 = lane < n ? r.units(logit_of(v0)) : 0, w1 = lane + 32 < n ? r.units(logit_of(v1)) : 0;
+  unsigned long long c0 = w0, c1 = w1;  // running sums with the word
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long t = __shfl_up_sync(kAll, before, o);
-    if (lane >= o) before += t;
+    const unsigned long long t0 = __shfl_up_sync(kAll, c0, o), t1 = __shfl_up_sync(kAll, c1, o);
+    if (lane >= o) { c0 += t0; c1 += t1; }
   }
-  const unsigned long long sum = __shfl_sync(kAll, before, 31);
-  before -= mine;
-  // the word at which the running sum passes x, and the sum with it
-  auto pass = [&](unsigned long long x, unsigned long long& cv, unsigned long long& with) {
-    unsigned long long c = before;
-    bool here = false;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (c <= x && x < c + w[e]) { here = true; cv = v[e]; with = c + w[e]; }
-      c += w[e];
-    }
-    const uint32_t who = __ballot_sync(kAll, here);
-    if (!who) return false;
-    cv = __shfl_sync(kAll, cv, __ffs(who) - 1);
-    with = __shfl_sync(kAll, with, __ffs(who) - 1);
-    return true;
+  c1 += __shfl_sync(kAll, c0, 31);
+  const unsigned long long sum = __shfl_sync(kAll, c1, 31);
+  // the place of the word at which the running sum passes x, 64: none
+  auto pass = [&](unsigned long long x) {
+    const uint32_t a = __ballot_sync(kAll, x < c0), b = __ballot_sync(kAll, x < c1);
+    return a ? __ffs(a) - 1 : b ? 31 + __ffs(b) : 64;
   };
-  unsigned long long cv = 0, with = 0;
+  auto with = [&](int at) { return __shfl_sync(kAll, at < 32 ? c0 : c1, at & 31); };
   if (k > 0) {
     if (k > n && !complete) return false;
-    unsigned long long t = before;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (4 * lane + e < k) t += w[e];
-    total = k >= n ? sum : __shfl_sync(kAll, t, (k - 1) >> 2);
+    total = k >= n ? sum : with(k - 1);
   }
+  bool bounded = k > 0;  // the kept words end inside the list
   if (p < 1.0f) {
-    if (!pass(nucleus(p, total), cv, with)) return false;
-    total = min(total, with);
+    const int at = pass(nucleus(p, total));
+    if (at < 64) {
+      total = min(total, with(at));
+      bounded = true;
+    }
   }
   if (mp > 0.0f) {
-    unsigned long long t = 0;
-    bool below = false;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool in = 4 * lane + e < n;
-      if (in && r.weight(logit_of(v[e])) >= fminf(mp, 1.0f)) t += w[e];
-      else below |= in;
+    const float least = fminf(mp, 1.0f);
+    const int in = __popc(__ballot_sync(kAll, lane < n && r.weight(logit_of(v0)) >= least)) +
+                   __popc(__ballot_sync(kAll, lane + 32 < n && r.weight(logit_of(v1)) >= least));
+    if (in < n || complete) {
+      total = min(total, with(max(in, 1) - 1));
+      bounded = true;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kAll, t, o);
-    if (__any_sync(kAll, below) || complete) total = min(total, t);
-    else if (k == 0 && !(p < 1.0f)) return false;  // the cut lies past the list
   }
-  return pass(share(u, total), cv_out, with);
+  // a nucleus that ends past the list is only harmless if another cut ends inside, and no cut at all only for u inside
+  if (!bounded && (p < 1.0f || mp > 0.0f)) return false;
+  const int at = pass(share(u, total));
+  if (at >= 64) return false;
+  cv_out = __shfl_sync(kAll, at < 32 ? v0 : v1, at & 31);
+  return true;
 }
 
 // This CTA's sum of the weights that `take` takes, into s.mass.  also(index, chunk): what else is done with each chunk.
@@ -419,13 +409,17 @@ __device__ __forceinline__ void sum_where(Smem& s, const X* row, int V, int rank
   const unsigned long long t = block_sum(s, static_cast<unsigned long long>((static_cast<long long>(hi) << 20) + lo));
   if (threadIdx.x == 0) s.mass = t;
 }
-// Lists the words of a chunk (a single word: of a chunk of others at -inf) from `cut` up.
+// Lists the words of a chunk from `cut` up.
 template <class X>
 __device__ __noinline__ void list_chunk(Smem& s, const X* row, int i, uint4 v, float cut) {
+  int n = 0;
+  each4(row, v, i, [&](int, float l) { n += l >= cut && l > -INFINITY; });
+  if (n == 0) return;
+  int at = atomicAdd(&s.ncand, n);
   each4(row, v, i, [&](int j, float l) {
     if (l >= cut && l > -INFINITY) {
-      const int at = atomicAdd(&s.ncand, 1);
       if (at < CAND) s.cand[at] = sort_key(l, j);
+      ++at;
     }
   });
 }
@@ -658,8 +652,77 @@ __device__ __noinline__ bool locate(Smem& s, const X* row, int V, int rank, int 
   return found;
 }
 
+// The cuts and the choice over the whole row, every CTA of the cluster.
 template <class X>
-__global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ SampleArgs a, int CS) {
+__device__ __noinline__ void whole_row(Smem& s, const SampleArgs& a, const X* row, int m, int rank, int CS, const Row r, int k,
+                                       float p, float mp, float u) {
+  const int V = a.V;
+  Bins h0;
+  bool have = false;
+  auto none = [](int, uint4) {};
+  sum_where(s, row, V, rank, CS, r, [](int, float l) { return l > -INFINITY; }, none);
+  cluster_sync();
+  unsigned long long total = cluster_mass(s, CS);  // of the words kept
+  cluster_sync();
+  if (k > 0) {
+    const bool some_k = locate(s, row, V, rank, CS, r, static_cast<unsigned long long>(k) - 1, true, h0, have);
+    have = true;
+    if (rank == 0 && threadIdx.x == 0) s.pick = some_k;
+    cluster_sync();
+    const bool cut_k = peer32(at_rank(&s.pick, 0)) != 0;  // else fewer words weigh anything
+    const unsigned long long kth = peer64(at_rank(&s.found_cv, 0));
+    cluster_sync();
+    if (cut_k) {
+      sum_where(s, row, V, rank, CS, r, [&](int i, float l) { return l > -INFINITY && sort_key(l, i) <= kth; }, none);
+      cluster_sync();
+      total = cluster_mass(s, CS);
+      cluster_sync();
+    }
+  }
+  if (p < 1.0f) {
+    locate(s, row, V, rank, CS, r, nucleus(p, total), false, h0, have);
+    have = true;
+    if (rank == 0) total = min(total, s.found_before + r.units(logit_of(s.found_cv)));
+  }
+  if (mp > 0.0f) {
+    const float least = fminf(mp, 1.0f);
+    sum_where(s, row, V, rank, CS, r, [&](int, float l) { return l > -INFINITY && r.weight(l) >= least; }, none);
+    cluster_sync();
+    total = min(total, cluster_mass(s, CS));
+    cluster_sync();
+  }
+  locate(s, row, V, rank, CS, r, share(u, total), false, h0, have);
+  if (rank == 0 && threadIdx.x == 0) write_row(a, m, r, s.found_cv, total);
+}
+
+// A row's settings: temperature not above 0 is the first word; k = 0: no top_k.
+__device__ __forceinline__ void settings(const SampleArgs& a, int m, float& temp, int& k, float& p, float& mp, float& u) {
+  temp = a.temperature ? __ldg(a.temperature + m) : 1.0f;
+  k = a.top_k ? __ldg(a.top_k + m) : 0;
+  p = a.top_p ? __ldg(a.top_p + m) : 1.0f;
+  mp = a.min_p ? __ldg(a.min_p + m) : 0.0f;
+  u = __ldg(a.u + m);
+  if (!(temp > 0.0f)) {
+    temp = 1.0f;
+    k = 1;
+  }
+  if (k < 0 || k >= a.V) k = 0;
+}
+__device__ __forceinline__ Row row_of(float lmax, float temp) {
+  Row r;
+  r.lmax = lmax;
+  r.c = 1.4426950408889634f / temp;
+  r.zs = static_cast<float>(BINS) / kSpan / temp;
+  return r;
+}
+
+// Rows left to the tail kernel: count, CTAs that have left it, and the rows (null: none are left).
+struct Tail {
+  int *count, *left, *rows;
+};
+
+template <class X>
+__global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ SampleArgs a, int CS, Tail tail) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>(smem_raw);
   pdl_wait();
@@ -667,10 +730,9 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int m = blockIdx.x / CS, rank = blockIdx.x - m * CS, V = a.V;
   const X* row = static_cast<const X*>(a.logits) + m * a.row_stride;
-  float temp = a.temperature ? __ldg(a.temperature + m) : 1.0f;
-  int k = a.top_k ? __ldg(a.top_k + m) : 0;
-  const float p = a.top_p ? __ldg(a.top_p + m) : 1.0f, mp = a.min_p ? __ldg(a.min_p + m) : 0.0f;
-  const float u = __ldg(a.u + m);
+  float temp, p, mp, u;
+  int k;
+  settings(a, m, temp, k, p, mp, u);
 
   // ---- each thread's largest logit, and the CTA's
   for (int i = tid; i < BINS; i += STH) s.count[i] = 0;
@@ -690,16 +752,8 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
   cluster_arrive();
 
   // ---- meanwhile the threshold: the smallest of the threads' largest logits in the first bins that hold enough of them
-  if (!(temp > 0.0f)) {  // the largest logit
-    temp = 1.0f;
-    k = 1;
-  }
-  if (k < 0 || k >= V) k = 0;
   const bool by_top_k = k > 0 && k <= TOPK_FAST;
-  Row r;
-  r.lmax = mx;
-  r.c = 1.4426950408889634f / temp;
-  r.zs = static_cast<float>(BINS) / kSpan / temp;
+  Row r = row_of(mx, temp);
   // with n words above the threshold spread over the threads at random, 1 - exp(-n / threads) of them have one
   const float per = static_cast<float>(by_top_k ? k + k / 4 + 32 : WANT) / static_cast<float>(CS);
   const int want = max(8, static_cast<int>(STH * (1.0f - __expf(-fminf(per, 1200.0f) / STH))));
@@ -776,12 +830,11 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
     const int nq = min(__shfl_sync(0xFFFFFFFFu, listed, q), CAND);
     __syncthreads();
     const uint32_t from = at_rank(s.cand, q);
-    for (int i = (warp / CS) * 32 + lane; i < nq; i += SW / CS * 32) {
-      const unsigned long long cv = peer64(from + 8 * i);
-      if (cv <= tau) {
-        const int at = atomicAdd(&s.nlist, 1);
-        if (at < LIST) s.list[at] = cv;
-      }
+    for (int i0 = (warp / CS) * 32; i0 < nq; i0 += SW / CS * 32) {
+      const unsigned long long cv = i0 + lane < nq ? peer64(from + 8 * (i0 + lane)) : ~0ull;
+      const bool on = cv <= tau && i0 + lane < nq;
+      const int at = push_at(&s.nlist, on);
+      if (on && at < LIST) s.list[at] = cv;
     }
     __syncthreads();
     const int n = s.nlist;
@@ -793,9 +846,9 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
         s.done = 1;
       }
     } else if (good) {
-      // first on the (at most 128) words nearest to the largest: by halving, a depth with 64 to 128 words above it
-      constexpr int FEW = 128;
+      // first on the few words nearest to the largest: by halving, a depth with 32 to 64 words above it
       int few = n;
+      const unsigned long long* from_list = s.list;
       if (n > FEW && k <= FEW) {
         unsigned long long cv[LIST / STH];
         float z[LIST / STH];
@@ -805,37 +858,31 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
           cv[i] = j < n ? s.list[j] : ~0ull;
           z[i] = j < n ? r.depth(logit_of(cv[i])) : 4.0f * BINS;
         }
+        if (tid == 0) s.nfew = 0;
         float lo = 0.0f, hi = static_cast<float>(BINS);
+#pragma unroll 1
         for (int step = 0; step < 14; ++step) {
           const float mid = 0.5f * (lo + hi);
           int c = 0;
 #pragma unroll
-          for (int i = 0; i < LIST / STH; ++i) {
-            const uint32_t in = __ballot_sync(0xFFFFFFFFu, z[i] <= mid);
-            c += __popc(in);
+          for (int i = 0; i < LIST / STH; ++i) c += __popc(__ballot_sync(0xFFFFFFFFu, z[i] <= mid));
+          if (lane == 0) s.scan_c[(step & 1) * SW + warp] = c;
+          __syncthreads();
+          few = __reduce_add_sync(0xFFFFFFFFu, lane < SW ? s.scan_c[(step & 1) * SW + lane] : 0);
+          if (few > FEW) {
+            hi = mid;
+          } else {
+            lo = mid;
+            if (few >= max(k, FEW / 2)) break;
           }
-          if (lane == 0) s.scan_c[warp] = c;
-          __syncthreads();
-          c = lane < SW ? s.scan_c[lane] : 0;
-          c = __reduce_add_sync(0xFFFFFFFFu, c);
-          __syncthreads();
-          few = c;
-          if (c > FEW) hi = mid;
-          else if (c < max(k, FEW / 2)) lo = mid;
-          else { lo = mid; break; }
         }
         if (few <= FEW && few >= max(k, 1)) {
-          // they go first: every word is in a register
-          if (tid == 0) s.nlist = 0;
-          __syncthreads();
 #pragma unroll
-          for (int i = 0; i < LIST / STH; ++i)
-            if (z[i] <= lo) s.list[atomicAdd(&s.nlist, 1)] = cv[i];
-          if (tid == 0) s.pick = few;
-          __syncthreads();
-#pragma unroll
-          for (int i = 0; i < LIST / STH; ++i)
-            if (z[i] > lo && cv[i] != ~0ull) s.list[atomicAdd(&s.pick, 1)] = cv[i];
+          for (int i = 0; i < LIST / STH; ++i) {
+            const int at = push_at(&s.nfew, z[i] <= lo);
+            if (z[i] <= lo) s.few[at] = cv[i];
+          }
+          from_list = s.few;
         } else {
           few = n;
         }
@@ -846,7 +893,7 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
       if (few <= FEW) {
         if (warp == 0) {
           unsigned long long cv = 0, kept = total;
-          found = choose_in_warp(s, r, few, complete && few == n, k, p, mp, u, kept, cv);
+          found = choose_in_warp(from_list, r, few, complete && few == n, k, p, mp, u, kept, cv);
           if (found && lane == 0) {
             write_row(a, m, r, cv, kept);
             s.done = 1;
@@ -868,13 +915,14 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
             total = block_sum(s, t);
           }
         }
-        if (good && p < 1.0f) {
-          good = pass_at(s, h, 0, nucleus(p, total), false);
-          if (good) total = min(total, s.found_before + r.units(logit_of(s.found_cv)));
+        bool bounded = k > 0;  // the kept words end inside the list
+        if (good && p < 1.0f && pass_at(s, h, 0, nucleus(p, total), false)) {
+          total = min(total, s.found_before + r.units(logit_of(s.found_cv)));
+          bounded = true;
         }
         if (good && mp > 0.0f) {
           unsigned long long t = 0;
-          int below = 0;  // some listed word is below min_p: the cut is inside the list
+          int below = 0;  // some listed word is below min_p
 #pragma unroll
           for (int i = 0; i < LIST / STH; ++i) {
             const int j = tid * (LIST / STH) + i;
@@ -883,9 +931,13 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
           }
           below = __syncthreads_or(below);
           t = block_sum(s, t);
-          if (below || complete) total = min(total, t);
-          else good = k > 0 || p < 1.0f;  // the cut lies past the list, and past the other cut where there is one
+          if (below || complete) {
+            total = min(total, t);
+            bounded = true;
+          }
         }
+        // a nucleus that ends past the list is only harmless if another cut ends inside
+        good = good && (bounded || !(p < 1.0f || mp > 0.0f));
         if (good) good = pass_at(s, h, 0, share(u, total), false);
         if (good && tid == 0) {
           write_row(a, m, r, s.found_cv, total);
@@ -899,64 +951,75 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
   cluster_sync();
   if (done) return;
 
-  // ---- the same cuts over the whole row
-  Bins h0;
-  bool have = false;
-  auto none = [](int, uint4) {};
-  if (by_top_k) {
-    sum_where(s, row, V, rank, CS, r, [](int, float l) { return l > -INFINITY; }, none);
+  if (tail.rows) {  // left to the clusters of eight that follow
+    if (rank == 0 && tid == 0) tail.rows[atomicAdd(tail.count, 1)] = m;
+    return;
+  }
+  whole_row(s, a, row, m, rank, CS, r, k, p, mp, u);
+}
+
+// The rows that sample_kernel left, by clusters of eight CTAs in turn; the last CTA to leave clears the count.
+template <class X>
+__global__ void __launch_bounds__(STH, 2) tail_kernel(const __grid_constant__ SampleArgs a, Tail tail) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>(smem_raw);
+  const int rank = blockIdx.x % 8, tid = threadIdx.x;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int n = __ldcg(tail.count);
+  for (int i = blockIdx.x / 8; i < n; i += gridDim.x / 8) {
+    const int m = __ldcg(tail.rows + i);
+    const X* row = static_cast<const X*>(a.logits) + m * a.row_stride;
+    float temp, p, mp, u;
+    int k;
+    settings(a, m, temp, k, p, mp, u);
+    float mx = -INFINITY;
+    each_chunk<8>(
+        row, a.V, rank, 8, [&](int, uint4 v) { mx = fmaxf(mx, largest(row, v)); }, [&](int, float l) { mx = fmaxf(mx, l); });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    if ((tid & 31) == 0) s.red_f[tid >> 5] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < SW; ++w) mx = fmaxf(mx, s.red_f[w]);
+    if (tid == 0) s.bmax = mx;
+    cluster_sync();
+    for (int q = 0; q < 8; ++q) mx = fmaxf(mx, __uint_as_float(peer32(at_rank(&s.bmax, q))));
+    whole_row(s, a, row, m, rank, 8, row_of(mx, temp), k, p, mp, u);
     cluster_sync();
   }
-  total = cluster_mass(s, CS);
-  cluster_sync();
-  if (k > 0) {
-    const bool some_k = locate(s, row, V, rank, CS, r, static_cast<unsigned long long>(k) - 1, true, h0, have);
-    have = true;
-    if (rank == 0 && tid == 0) s.pick = some_k;
-    cluster_sync();
-    const bool cut_k = peer32(at_rank(&s.pick, 0)) != 0;  // else fewer words weigh anything
-    const unsigned long long kth = peer64(at_rank(&s.found_cv, 0));
-    cluster_sync();
-    if (cut_k) {
-      sum_where(s, row, V, rank, CS, r, [&](int i, float l) { return l > -INFINITY && sort_key(l, i) <= kth; }, none);
-      cluster_sync();
-      total = cluster_mass(s, CS);
-      cluster_sync();
+  if (tid == 0) {
+    __threadfence();
+    if (atomicAdd(tail.left, 1) == static_cast<int>(gridDim.x) - 1) {
+      *tail.count = 0;
+      *tail.left = 0;
     }
   }
-  if (p < 1.0f) {
-    locate(s, row, V, rank, CS, r, nucleus(p, total), false, h0, have);
-    have = true;
-    if (rank == 0) total = min(total, s.found_before + r.units(logit_of(s.found_cv)));
-  }
-  if (mp > 0.0f) {
-    sum_where(s, row, V, rank, CS, r, [&](int, float l) { return l > -INFINITY && r.weight(l) >= fminf(mp, 1.0f); }, none);
-    cluster_sync();
-    total = min(total, cluster_mass(s, CS));
-    cluster_sync();
-  }
-  locate(s, row, V, rank, CS, r, share(u, total), false, h0, have);
-  if (rank == 0 && tid == 0) write_row(a, m, r, s.found_cv, total);
 }
 
 }  // namespace
 
-size_t sample_workspace_bytes(int64_t, int64_t) { return 256; }
+// The workspace: the tail's counters (zero between calls) and its rows.
+size_t sample_workspace_bytes(int64_t M, int64_t) { return (256 + static_cast<size_t>(M) * sizeof(int) + 255) / 256 * 256; }
 
-cudaError_t launch_sample(const SampleArgs& a, int bf16, cudaStream_t st) {
-  // CTAs per row: as many as fill the device's four CTAs per SM (a row in fewer, larger shares once the rows do), with
-  // at least 4096 words each, and at most 2^18, the histograms' room.
-  int CS = 1;
-  while (CS < 8 && static_cast<int64_t>(a.M) * CS * 2 <= 4 * num_sms() && a.V / (CS * 2) >= 4096) CS *= 2;
-  while (CS < 8 && a.V / CS > (1 << 18)) CS *= 2;
-  auto* kernel = bf16 ? sample_kernel<__nv_bfloat16> : sample_kernel<float>;
-  static bool smem_set[64][2] = {{false}};
-  bool& set = smem_set[current_device_id()][bf16 ? 1 : 0];
+namespace {
+template <class X>
+cudaError_t launch_x(const SampleArgs& a, cudaStream_t st) {
+  static bool smem_set[64] = {false};
+  bool& set = smem_set[current_device_id()];
   if (!set) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
+    cudaError_t e = cudaFuncSetAttribute(sample_kernel<X>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(tail_kernel<X>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
     if (e != cudaSuccess) return e;
     set = true;
   }
+  // CTAs per row: as many as fill the device (a row in fewer, larger shares once the rows do), with at least 4096 words
+  // each, and at most 2^18, the histograms' room.
+  const int sms = num_sms();
+  int CS = 1;
+  while (CS < 8 && static_cast<int64_t>(a.M) * CS * 2 <= 4 * sms && a.V / (CS * 2) >= 4096) CS *= 2;
+  while (CS < 8 && a.V / CS > (1 << 18)) CS *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.M) * CS);
   cfg.blockDim = dim3(STH);
@@ -971,7 +1034,27 @@ cudaError_t launch_sample(const SampleArgs& a, int bf16, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, CS);
+  // A row that needs the whole-row path keeps its few CTAs busy long after the others are done: where a row has fewer
+  // than eight of them and enough words, those rows are left to a second launch.
+  Tail tail = {nullptr, nullptr, nullptr};
+  const bool second = CS < 8 && a.V >= 32768;
+  if (second) {
+    tail.count = static_cast<int*>(a.ws);
+    tail.left = tail.count + 1;
+    tail.rows = tail.count + 64;
+  }
+  cudaError_t e = cudaLaunchKernelEx(&cfg, sample_kernel<X>, a, CS, tail);
+  if (e == cudaSuccess && second) {
+    cfg.gridDim = dim3(sms / 8 * 8 > 0 ? sms / 8 * 8 : 8);
+    attr[1].val.clusterDim.x = 8;
+    e = cudaLaunchKernelEx(&cfg, tail_kernel<X>, a, tail);
+  }
+  return e;
+}
+}  // namespace
+
+cudaError_t launch_sample(const SampleArgs& a, int bf16, cudaStream_t st) {
+  return bf16 ? launch_x<__nv_bfloat16>(a, st) : launch_x<float>(a, st);
 }
 
 }  // namespace kq

@@ -238,3 +238,24 @@ def test_sample_in_a_graph_and_on_another_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(ids, want) and torch.equal(probs, wp)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_sample_many_rows_some_flat(dtype):
+    """More rows than the device has clusters of eight: the rows whose answer lies deep in a flat distribution, or whose
+    top_k is large, are worked on apart from the others.  Twice on one workspace."""
+    M, V = 160, 40001
+    x = logits(M, V, 10, dtype, sd=1.0)
+    x[::7] = torch.randn((len(range(0, M, 7)), V), generator=torch.Generator().manual_seed(1)).cuda().to(dtype) * 0.5
+    x[3::40] = 1.0                                      # all equal
+    x[5::40, 20:] = float("-inf")
+    k = [[0, 20, 0, 1500, 30000][m % 5] for m in range(M)]
+    p = [1.0 if m % 3 == 0 else ("mid", [3, 700, 9000][m % 3]) for m in range(M)]
+    check(x, [[1.0, 0.7, 2.0][m % 3] for m in range(M)], k, p, [0.3 * (m % 11 == 0) for m in range(M)],
+          [[2, 15000, 600, 39000][m % 4] for m in range(M)])
+
+
+@pytest.mark.parametrize("V", [300000, 1 << 20])
+def test_sample_large_vocabularies(V):
+    x = logits(3, V, 11)
+    check(x, [1.0, 2.5, 0.8], [0, 0, 50], [("mid", 12), 1.0, ("mid", 20)], [0.0, 0.0, 0.0], [9, 300, 5])

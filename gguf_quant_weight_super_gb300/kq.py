@@ -140,6 +140,8 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
+        if torch.cuda.is_initialized():  # the current stream's handle without a Stream object around it
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -421,6 +423,7 @@ class KVCache:
         self.struct = KqKvCache(_CACHE_TYPES[k.dtype], heads, dim, page, n_pages, k.stride(0), k.stride(1), k.stride(2),
                                 _ptr(k), _ptr(v), self.k_scale, self.v_scale)
         self._ref = ctypes.addressof(self.struct)
+        self.n_kv_heads, self.head_dim = heads, dim
 
 
 class RopeNorm:
@@ -436,6 +439,10 @@ class RopeNorm:
         n, rot = cos_sin.shape if cos_sin is not None else (0, 0)
         self.struct = KqRope(_ptr(q_norm), _ptr(k_norm), eps, norm_offset, _ptr(cos_sin), n, rot, int(interleaved))
         self._ref = ctypes.addressof(self.struct)
+        dims = {w.numel() for w in (q_norm, k_norm) if w is not None}
+        if len(dims) > 1:
+            raise ValueError("norm weights: [head_dim]")
+        self.norm_dim = dims.pop() if dims else 0
 
 
 def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, factor: float = 1.0, trained: int = 0,
@@ -484,19 +491,39 @@ def kq_sample(logits, dtype, row_stride, M, V, u, temperature, top_k, top_p, min
                                         workspace_bytes, _stream(stream)))
 
 
+# The calls below are made once per layer and token, where a Python call's own time counts: each tensor is looked at once.
+
+_DTYPE_CODE = {torch.float32: KQ_F32, torch.bfloat16: KQ_BF16}
+
+
 def _rows(name: str, x: torch.Tensor, B: int, T: int, D: int):
     """The heads and the row stride of x [B, T, heads, D]: heads contiguous, rows at one stride."""
-    if x.dim() != 4 or x.shape[0] != B or x.shape[1] != T or x.shape[3] != D:
-        raise ValueError(f"{name}: [{B}, {T}, heads, {D}], not {list(x.shape)}")
+    shape = x.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != D:
+        raise ValueError(f"{name}: [{B}, {T}, heads, {D}], not {list(shape)}")
     s0, s1, s2, s3 = x.stride()
-    if (s3 != 1 or (s2 != D and x.shape[2] > 1) or (B > 1 and T > 1 and s0 != T * s1)):
+    heads = shape[2]
+    if s3 != 1 or (s2 != D and heads > 1) or (s0 != T * s1 and B > 1 and T > 1):
         raise ValueError(f"{name}: heads contiguous, tokens at one stride")
-    return x.shape[2], (s1 if T > 1 else s0 if B > 1 else x.shape[2] * D)
+    return heads, (s1 if T > 1 else s0 if B > 1 else heads * D)
 
 
-def _int32(name: str, t: torch.Tensor, *shape):
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous int32 {list(shape)}")
+def _vector(name: str, t: torch.Tensor, dtype, shape) -> int:
+    """The address of a contiguous device tensor of the given type and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {list(shape)}")
+    if not t.is_cuda:
+        raise ValueError("libkq takes device tensors only")
+    return t.data_ptr()
+
+
+def _floats(x: torch.Tensor) -> int:
+    code = _DTYPE_CODE.get(x.dtype)
+    if code is None:
+        raise TypeError("float32 or bfloat16")
+    if not x.is_cuda:
+        raise ValueError("libkq takes device tensors only")
+    return code
 
 
 def kv_append(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -504,22 +531,25 @@ def kv_append(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, 
               stream=None) -> torch.Tensor:
     """kq_kv_append for q [B, T, n_q_heads, head_dim], k and v [B, T, n_kv_heads, head_dim] (views of one fused buffer
     will do), page_table [B, max_pages] and seq_lens [B] int32; returns q_out."""
-    B, T, c = q.shape[0], q.shape[1], cache.struct
-    D = c.head_dim
+    B, T = q.shape[:2]
+    D, heads = cache.head_dim, cache.n_kv_heads
     (Hq, qs), (Hk, ks), (Hv, vs) = _rows("q", q, B, T, D), _rows("k", k, B, T, D), _rows("v", v, B, T, D)
-    if Hk != c.n_kv_heads or Hv != c.n_kv_heads or k.dtype != q.dtype or v.dtype != q.dtype:
+    x_dtype = _floats(q)
+    if Hk != heads or Hv != heads or _floats(k) != x_dtype or _floats(v) != x_dtype:
         raise ValueError("k and v: the cache's heads, of q's type")
-    for w in (rope.q_norm, rope.k_norm):
-        if w is not None and w.numel() != D:
-            raise ValueError("norm weights: [head_dim]")
-    _int32("page_table", page_table, B, page_table.shape[-1])
-    _int32("seq_lens", seq_lens, B)
+    if rope.norm_dim not in (0, D):
+        raise ValueError("norm weights: [head_dim]")
+    W = page_table.shape[-1]
     if q_out is None:
         q_out = torch.empty((B, T, Hq, D), dtype=q_out_dtype, device=q.device)
     elif q_out.shape != q.shape or not q_out.is_contiguous():
         raise ValueError("q_out: contiguous, of q's shape")
-    kq_kv_append(cache._ref, page_table, page_table.shape[1], seq_lens, B, T, q, k, v, x_dtype_of(q), qs, ks, vs, Hq,
-                 rope._ref, q_out, x_dtype_of(q_out), stream)
+    status = lib().kq_kv_append(cache._ref, _vector("page_table", page_table, torch.int32, (B, W)), W,
+                                _vector("seq_lens", seq_lens, torch.int32, (B,)), B, T, q.data_ptr(), k.data_ptr(),
+                                v.data_ptr(), x_dtype, qs, ks, vs, Hq, rope._ref, q_out.data_ptr(), _floats(q_out),
+                                _stream(stream))
+    if status:
+        raise KQError("kq_kv_append", status)
     return q_out
 
 
@@ -535,18 +565,20 @@ def attn_decode(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor
                 workspace: torch.Tensor, scale: float | None = None, softcap: float = 0.0, window: int = 0,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """kq_attn_decode for q [B, T, n_q_heads, head_dim]; scale None: head_dim^-0.5.  Returns out, of q's type."""
-    B, T = q.shape[0], q.shape[1]
-    D = cache.struct.head_dim
+    B, T = q.shape[:2]
+    D = cache.head_dim
     Hq, qs = _rows("q", q, B, T, D)
-    _int32("page_table", page_table, B, page_table.shape[-1])
-    _int32("seq_lens", seq_lens, B)
+    W = page_table.shape[-1]
     if out is None:
         out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-        raise ValueError("out: contiguous, of q's shape and type")
-    kq_attn_decode(cache._ref, page_table, page_table.shape[1], seq_lens, B, T, q, x_dtype_of(q), qs, Hq,
-                   D ** -0.5 if scale is None else scale, softcap, window, out, workspace,
-                   workspace.numel() * workspace.element_size(), stream)
+    status = lib().kq_attn_decode(cache._ref, _vector("page_table", page_table, torch.int32, (B, W)), W,
+                                  _vector("seq_lens", seq_lens, torch.int32, (B,)), B, T, q.data_ptr(), _floats(q), qs, Hq,
+                                  D ** -0.5 if scale is None else scale, softcap, window,
+                                  _vector("out", out, q.dtype, q.shape),
+                                  _vector("workspace", workspace, torch.uint8, workspace.shape), workspace.numel(),
+                                  _stream(stream))
+    if status:
+        raise KQError("kq_attn_decode", status)
     return out
 
 
@@ -562,20 +594,27 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
            ids=None, probs=None, stream=None):
     """kq_sample for logits [M, V] (rows contiguous) and u [M]; temperature, top_p, min_p [M] fp32 and top_k [M] int32,
     or None.  Returns (ids int32 [M], probs fp32 [M])."""
-    M, V = logits.shape
-    if logits.stride(1) != 1 and V > 1:
+    shape = logits.shape
+    M, V = shape
+    row = shape[:1]
+    f32, i32 = torch.float32, torch.int32
+    stride, one = logits.stride()
+    if one != 1 and V > 1:
         raise ValueError("logits: each row contiguous")
-    for name, t, dt in (("u", u, torch.float32), ("temperature", temperature, torch.float32),
-                        ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32),
-                        ("ids", ids, torch.int32), ("probs", probs, torch.float32)):
-        if t is not None and (t.dtype != dt or t.shape != (M,) or not t.is_contiguous()):
-            raise ValueError(f"{name}: contiguous {dt} [{M}]")
+    if ids is None:
+        ids = torch.empty(M, dtype=i32, device=logits.device)
+    if probs is None:
+        probs = torch.empty(M, dtype=f32, device=logits.device)
     if workspace is None:
         workspace = sample_workspace(M, V, logits.device)
-    if ids is None:
-        ids = torch.empty(M, dtype=torch.int32, device=logits.device)
-    if probs is None:
-        probs = torch.empty(M, dtype=torch.float32, device=logits.device)
-    kq_sample(logits, x_dtype_of(logits), logits.stride(0), M, V, u, temperature, top_k, top_p, min_p, ids, probs,
-              workspace, workspace.numel() * workspace.element_size(), stream)
+    status = lib().kq_sample(logits.data_ptr(), _floats(logits), stride, M, V, _vector("u", u, f32, row),
+                             None if temperature is None else _vector("temperature", temperature, f32, row),
+                             None if top_k is None else _vector("top_k", top_k, i32, row),
+                             None if top_p is None else _vector("top_p", top_p, f32, row),
+                             None if min_p is None else _vector("min_p", min_p, f32, row),
+                             _vector("ids", ids, i32, row), _vector("probs", probs, f32, row),
+                             _vector("workspace", workspace, torch.uint8, workspace.shape), workspace.numel(),
+                             _stream(stream))
+    if status:
+        raise KQError("kq_sample", status)
     return ids, probs

@@ -18,7 +18,9 @@
 //    that the 8-row matrix loads touch every bank once;
 //  * all tiles of 64 positions of all (sequence, head, row tile) items are one
 //    line, cut evenly into one contiguous range per CTA, whatever the
-//    lengths.  An item inside one range is finished there; for one that spans
+//    lengths (each item counts three tiles more than it has, what starting and
+//    ending it costs: a batch of 24 ragged sequences, among them one of a
+//    single position, took 115 us without).  An item inside one range is finished there; for one that spans
 //    ranges the CTAs leave their sums in the workspace, and the last to
 //    arrive joins them in the ranges' order (so the result does not depend on
 //    which one that is).
@@ -46,6 +48,7 @@ constexpr int NW = 4;            // warps per CTA
 constexpr int NTH = NW * 32;
 constexpr int WT = 16;           // positions per warp sub-tile
 constexpr int TK = NW * WT;      // positions per tile
+constexpr int START = 3;         // tiles' time that an item costs besides its tiles
 
 template <class Q, class C, int D, int MT>
 struct Cfg {
@@ -57,7 +60,7 @@ struct Cfg {
   static constexpr int SUB = WT * RB, STAGE = 2 * SUB;
   static constexpr int QB = 2 * D + 16;  // bytes of a q row in shared memory
   static constexpr int QBYTES = NQ * ROWS * QB;
-  static constexpr int HDR = (ROWS * (3 + 2 * NW) * 4 + 127) / 128 * 128;  // row scales, joined and warps' statistics
+  static constexpr int HDR = (ROWS * (2 + 2 * NW) * 4 + 127) / 128 * 128;  // row scales, the join's and the warps' statistics
   static constexpr int FIXED = HDR + QBYTES;
   // two CTAs per SM where a ring of at least two stages fits beside q in half of the shared memory (the rest is the
   // line of tiles' index, 8 bytes per sequence)
@@ -135,11 +138,14 @@ __device__ __forceinline__ uint32_t f8_pair(uint32_t v) {
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ float q_value(float v) { return v; }
-__device__ __forceinline__ float q_value(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void put2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
-__device__ __forceinline__ void put2(__nv_bfloat16* p, float x, float y) {
-  *reinterpret_cast<uint32_t*>(p) = pack2<false>(x, y);
+__device__ __forceinline__ void put4(float* p, float4 v, float f) {
+  *reinterpret_cast<float4*>(p) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+}
+__device__ __forceinline__ void put4(__nv_bfloat16* p, float4 v, float f) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2<false>(v.x * f, v.y * f), pack2<false>(v.z * f, v.w * f));
+}
+__device__ __forceinline__ void add4(float4& a, float f, float4 v) {
+  a = make_float4(fmaf(f, v.x, a.x), fmaf(f, v.y, a.y), fmaf(f, v.z, a.z), fmaf(f, v.w, a.w));
 }
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
 
@@ -436,50 +442,69 @@ struct Warp {
   }
 };
 
-// q rows of an item as 16-bit parts in shared memory; rscale: each row's power of two (e4m3 cache).
+__device__ __forceinline__ float4 load_q(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 load_q(const __nv_bfloat16* p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  const float2 a = unpack2<false>(u.x), b = unpack2<false>(u.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// q rows of an item as 16-bit parts in shared memory; rscale: each row's power of two (e4m3 cache).  A row is D / 4 lanes'
+// work (D = 256: two rounds of a warp); a warp's rows are all loaded before the first is used.
 template <class Q, class C, int D, int MT>
 __device__ __forceinline__ void stage_q(const Params& p, uint8_t* qsm, float* rscale, int b, int hk, int r0, int warp, int lane) {
   using K = Cfg<Q, C, D, MT>;
+  constexpr int LR = D < 128 ? D / 4 : 32, PR = D / 4 / LR;  // lanes per row, vectors per lane
+  constexpr int RW = 32 / LR, N = K::ROWS / (NW * RW);       // rows at a time per warp, times
   const AttnArgs& a = p.a;
   const int R = a.T * a.G;
-  for (int r = warp; r < K::ROWS; r += NW) {
-    float x[D / 32];
-    const int row = r0 + r;
+  float4 x[N][PR];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int row = r0 + (n * NW + warp) * RW + lane / LR;
     if (row < R) {
       const int t = row / a.G, h = hk * a.G + row - t * a.G;
       const Q* src = static_cast<const Q*>(a.q) + (static_cast<int64_t>(b) * a.T + t) * a.q_stride + static_cast<int64_t>(h) * D;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) x[i] = q_value(src[lane + 32 * i]);
+      for (int i = 0; i < PR; ++i) x[n][i] = load_q(src + 4 * (lane % LR + i * LR));
     } else {
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) x[i] = 0.0f;
+      for (int i = 0; i < PR; ++i) x[n][i] = make_float4(0, 0, 0, 0);
     }
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int r = (n * NW + warp) * RW + lane / LR;
     float back = 1.0f;
     if constexpr (K::F8) {
       float mx = 0.0f;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) mx = fmaxf(mx, fabsf(x[i]));
+      for (int i = 0; i < PR; ++i)
+        mx = fmaxf(fmaxf(fmaxf(mx, fabsf(x[n][i].x)), fabsf(x[n][i].y)), fmaxf(fabsf(x[n][i].z), fabsf(x[n][i].w)));
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+      for (int d = LR / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
       // largest value into [2^13, 2^14); the factor and its inverse stay normal numbers
       const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
       const float f = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
       back = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) x[i] *= f;
+      for (int i = 0; i < PR; ++i) x[n][i] = make_float4(x[n][i].x * f, x[n][i].y * f, x[n][i].z * f, x[n][i].w * f);
     }
-    if (lane == 0) rscale[r] = back;
+    if (lane % LR == 0) rscale[r] = back;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int d = lane + 32 * i;
+    for (int i = 0; i < PR; ++i) {
+      const int d = 4 * (lane % LR + i * LR);
       // e4m3: four neighbouring dims come in one register, so a k-step's slots hold them in this order
-      const int c = d & 15, slot = K::F8 ? (d & ~15) + ((c >> 2) * 2 + (c & 1)) + ((c & 2) ? 8 : 0) : d;
-      float v = x[i];
+      const int s0 = K::F8 ? (d & ~15) + (d & 15) / 2 : d, s1 = K::F8 ? s0 + 8 : d + 2;
+      float4 v = x[n][i];
 #pragma unroll
       for (int t = 0; t < K::NQ; ++t) {
-        const uint32_t w = pack2<K::F8>(v, 0.0f);
-        *reinterpret_cast<uint16_t*>(qsm + (t * K::ROWS + r) * K::QB + 2 * slot) = static_cast<uint16_t>(w);
-        v -= unpack2<K::F8>(w).x;
+        uint8_t* row = qsm + (t * K::ROWS + r) * K::QB;
+        const uint32_t w0 = pack2<K::F8>(v.x, v.y), w1 = pack2<K::F8>(v.z, v.w);
+        *reinterpret_cast<uint32_t*>(row + 2 * s0) = w0;
+        *reinterpret_cast<uint32_t*>(row + 2 * s1) = w1;
+        const float2 b0 = unpack2<K::F8>(w0), b1 = unpack2<K::F8>(w1);
+        v = make_float4(v.x - b0.x, v.y - b0.y, v.z - b1.x, v.w - b1.y);
       }
     }
   }
@@ -492,8 +517,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, MT>::CPS)) attn_kernel(cons
   __shared__ int64_t s_scan[NTH];
   __shared__ int s_last;
   float* rscale = reinterpret_cast<float*>(smem);  // [ROWS]
-  float* s_m = rscale + K::ROWS;                   // [ROWS] joined maximum
-  float* s_i = s_m + K::ROWS;                      // [ROWS] 1 / weight sum
+  float* s_i = rscale + K::ROWS;                   // [ROWS] the join's 1 / weight sum
   float* w_ml = s_i + K::ROWS;                     // [NW][ROWS][2] each warp's maximum and weight sum
   uint8_t* qsm = smem + K::HDR;
   uint8_t* ring = smem + K::FIXED;
@@ -503,7 +527,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, MT>::CPS)) attn_kernel(cons
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the line of tiles (every sequence has at least one, so that its rows are written)
+  // ---- the line of tiles (an empty sequence has a unit, too, so that its rows are written)
   const int64_t room = a.max_pages << a.page_shift;
   auto length = [&](int b, bool tell) {
     const int n = __ldg(a.seq_lens + b);
@@ -514,7 +538,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, MT>::CPS)) attn_kernel(cons
     return max(n, 0);
   };
   auto first_of = [&](int len) { return a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0; };
-  auto tiles_of = [&](int len) { return max(1, (len + TK - 1) / TK - first_of(len) / TK); };
+  auto tiles_of = [&](int len) { return len > 0 ? START + (len + TK - 1) / TK - first_of(len) / TK : 1; };
   const int per = (a.B + NTH - 1) / NTH;
   {
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
@@ -550,16 +574,31 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, MT>::CPS)) attn_kernel(cons
     const int nt = static_cast<int>(prefix[b + 1] - prefix[b]);
     const int64_t in = u - prefix[b] * HR;
     const int hr = static_cast<int>(in / nt), hk = hr / p.RT, rt = hr - hk * p.RT;
-    const int64_t i0 = prefix[b] * HR + static_cast<int64_t>(hr) * nt, i1 = i0 + nt;  // the item
-    const int64_t end = i1 < hi ? i1 : hi;
     Seg g;
     g.len = length(b, false);
+    const int64_t i1 = prefix[b] * HR + static_cast<int64_t>(hr + 1) * nt;  // the item's end
+    const int64_t i0 = g.len > 0 ? i1 - nt + START : i1 - 1;                // its first tile
+    const int64_t end = i1 < hi ? i1 : hi;
+    if (u < i0) u = i0;
+    if (u >= end) {  // none of its tiles is in this range
+      u = end;
+      continue;
+    }
+    const int r0 = rt * K::ROWS, R = min(K::ROWS, a.T * a.G - r0);
+    auto write = [&](int r, int d, float4 v, float inv) {
+      const int row = r0 + r, t = row / a.G, h = hk * a.G + row - t * a.G;
+      put4(static_cast<Q*>(a.out) + ((static_cast<int64_t>(b) * a.T + t) * a.Hq + h) * D + d, v, inv);
+    };
+    if (g.len == 0) {
+      for (int x = threadIdx.x; x < R * (D / 4); x += NTH) write(x / (D / 4), 4 * (x % (D / 4)), make_float4(0, 0, 0, 0), 0.0f);
+      u = end;
+      continue;
+    }
     g.first = first_of(g.len);
     g.table = a.page_table + b * a.max_pages;
     g.head_off = hk * a.c.head_stride;
     g.t0 = static_cast<int>(u - i0) + g.first / TK;
     g.t1 = static_cast<int>(end - i0) + g.first / TK;
-    const int r0 = rt * K::ROWS, R = min(K::ROWS, a.T * a.G - r0);
 
     stage_q<Q, C, D, MT>(p, qsm, rscale, b, hk, r0, warp, lane);
     __syncthreads();
@@ -607,78 +646,73 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, MT>::CPS)) attn_kernel(cons
       }
     __syncthreads();
     const bool whole = u == i0 && end == i1;
-    const int slot = static_cast<int>(2 * c + (lo >= i0 ? 1 : 0));  // the range starts in this item (1), or before it (0)
-    auto write = [&](int r, int d, float x, float y, float inv) {
-      const int row = r0 + r, t = row / a.G, h = hk * a.G + row - t * a.G;
-      put2(static_cast<Q*>(a.out) + ((static_cast<int64_t>(b) * a.T + t) * a.Hq + h) * D + d, x * inv, y * inv);
-    };
-    for (int x = threadIdx.x; x < R * (D / 2); x += NTH) {
-      const int r = x / (D / 2), d = 2 * (x % (D / 2));
-      float mm = -INFINITY, ll = 0.0f, ox = 0.0f, oy = 0.0f;
+    const int slot = static_cast<int>(2 * c + (lo >= i0 ? 1 : 0));  // the range starts in these tiles (1), or before them
+    for (int x = threadIdx.x; x < R * (D / 4); x += NTH) {
+      const int r = x / (D / 4), d = 4 * (x % (D / 4));
+      float mm = -INFINITY, ll = 0.0f;
+      float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll
       for (int k = 0; k < NW; ++k) mm = fmaxf(mm, w_ml[(k * K::ROWS + r) * 2]);
       const float ms = mm == -INFINITY ? 0.0f : mm;
 #pragma unroll
       for (int k = 0; k < NW; ++k) {
         const float e = ex2(w_ml[(k * K::ROWS + r) * 2] - ms);
-        const float2 v = *reinterpret_cast<const float2*>(ring + k * (K::S * K::STAGE) + (r * D + d) * 4);
         ll += w_ml[(k * K::ROWS + r) * 2 + 1] * e;
-        ox += v.x * e;
-        oy += v.y * e;
+        add4(acc, e, *reinterpret_cast<const float4*>(ring + k * (K::S * K::STAGE) + (r * D + d) * 4));
       }
       if (whole) {
-        write(r, d, ox, oy, ll == 0.0f ? 0.0f : a.c.v_scale / ll);
+        write(r, d, acc, ll == 0.0f ? 0.0f : a.c.v_scale / ll);
       } else {
-        *reinterpret_cast<float2*>(p.part + (static_cast<int64_t>(slot) * K::ROWS + r) * D + d) = make_float2(ox, oy);
+        *reinterpret_cast<float4*>(p.part + (static_cast<int64_t>(slot) * K::ROWS + r) * D + d) = acc;
         if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * K::ROWS + r) * 2) = make_float2(mm, ll);
       }
     }
     if (!whole) {
       // ---- the last CTA of the item to arrive joins the ranges' sums
-      const int64_t ca = ((i0 + 1) * nc - 1) / total, cb = (i1 * nc - 1) / total;  // first and last range
+      const int ca = static_cast<int>(((i0 + 1) * nc - 1) / total), cb = static_cast<int>((i1 * nc - 1) / total);
+      const int parts = cb - ca + 1;  // the item's tiles lie in ranges ca .. cb
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
         int* cnt = p.count + (static_cast<int64_t>(b) * HR + hr);
-        const int got = atomicAdd(cnt, 1);
-        s_last = got == static_cast<int>(cb - ca);
+        s_last = atomicAdd(cnt, 1) == parts - 1;
         if (s_last) *cnt = 0;
       }
       __syncthreads();
       if (s_last) {
         __threadfence();
-        auto slot_of = [&](int64_t k) { return 2 * k + (k * total / nc >= i0 ? 1 : 0); };
+        // every range but the first starts in the item's tiles
+        const int slot0 = 2 * ca + (static_cast<int64_t>(ca) * total / nc >= i0 ? 1 : 0);
+        auto slot_of = [&](int k) { return k == 0 ? slot0 : 2 * (ca + k) + 1; };
+        float* factor = reinterpret_cast<float*>(ring);  // [parts][R]
         for (int r = warp; r < R; r += NW) {
           float mm = -INFINITY, ll = 0.0f;
-          for (int64_t k = ca + lane; k <= cb; k += 32)
-            mm = fmaxf(mm, __ldcg(p.part_ml + (slot_of(k) * K::ROWS + r) * 2));
+          for (int k = lane; k < parts; k += 32) {
+            const float x = __ldcg(p.part_ml + (static_cast<int64_t>(slot_of(k)) * K::ROWS + r) * 2);
+            factor[k * R + r] = x;
+            mm = fmaxf(mm, x);
+          }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
           const float ms = mm == -INFINITY ? 0.0f : mm;
-          for (int64_t k = ca + lane; k <= cb; k += 32) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (slot_of(k) * K::ROWS + r) * 2));
-            ll += v.y * ex2(v.x - ms);
+          for (int k = lane; k < parts; k += 32) {
+            const float e = ex2(factor[k * R + r] - ms);
+            factor[k * R + r] = e;
+            ll += e * __ldcg(p.part_ml + (static_cast<int64_t>(slot_of(k)) * K::ROWS + r) * 2 + 1);
           }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o);
-          if (lane == 0) {
-            s_m[r] = ms;
-            s_i[r] = ll == 0.0f ? 0.0f : a.c.v_scale / ll;
-          }
+          if (lane == 0) s_i[r] = ll == 0.0f ? 0.0f : a.c.v_scale / ll;
         }
         __syncthreads();
-        for (int x = threadIdx.x; x < R * (D / 2); x += NTH) {
-          const int r = x / (D / 2), d = 2 * (x % (D / 2));
-          float ox = 0.0f, oy = 0.0f;
-#pragma unroll 4
-          for (int64_t k = ca; k <= cb; ++k) {
-            const int64_t s = slot_of(k) * K::ROWS + r;
-            const float e = ex2(__ldcg(p.part_ml + s * 2) - s_m[r]);
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part + s * D + d));
-            ox += v.x * e;
-            oy += v.y * e;
-          }
-          write(r, d, ox, oy, s_i[r]);
+        for (int x = threadIdx.x; x < R * (D / 4); x += NTH) {
+          const int r = x / (D / 4), d = 4 * (x % (D / 4));
+          float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+          for (int k = 0; k < parts; ++k)
+            add4(acc, factor[k * R + r],
+                 __ldcg(reinterpret_cast<const float4*>(p.part + (static_cast<int64_t>(slot_of(k)) * K::ROWS + r) * D + d)));
+          write(r, d, acc, s_i[r]);
         }
       }
     }

@@ -8,10 +8,9 @@ using namespace attn;
 
 namespace {
 
-// Query rows per pass over the cache: all T*G in one pass of 16 or 32; more
-// rows take several passes (heads of 256 values: 16 at a time, whose sums
-// already fill the registers).
-int rows_per_pass(int head_dim, int rows) { return rows <= 16 || head_dim > 128 ? 16 : 32; }
+// Query rows per pass over the cache: all T*G in one pass of 8, 16 or 32; more rows take several passes (heads of 256
+// values: 16 at a time, whose sums already fill the registers).
+int rows_per_pass(int head_dim, int rows) { return rows <= 8 ? 8 : rows <= 16 || head_dim > 128 ? 16 : 32; }
 
 struct Layout {
   int rows, RT;
@@ -46,7 +45,8 @@ cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st) {
   p.count = reinterpret_cast<int*>(ws + L.count_off);
   p.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
   p.part = reinterpret_cast<float*>(ws + L.part_off);
-  return a.c.dtype == KQ_BF16 ? launch_attn_bf16(p, q_bf16, L.rows, st) : launch_attn_f8(p, q_bf16, L.rows, st);
+  if (a.c.dtype == KQ_BF16) return q_bf16 ? launch_attn_bf16_bf16(p, L.rows, st) : launch_attn_bf16_f32(p, L.rows, st);
+  return q_bf16 ? launch_attn_f8_bf16(p, L.rows, st) : launch_attn_f8_f32(p, L.rows, st);
 }
 
 }  // namespace kq

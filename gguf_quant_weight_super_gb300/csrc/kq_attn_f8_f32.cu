@@ -1,0 +1,10 @@
+// kq_attn_f8_f32.cu -- the attention kernel's instantiations for e4m3 caches and fp32 queries.
+#include "kq_attn_kernel.cuh"
+
+namespace kq {
+
+cudaError_t launch_attn_f8_f32(const attn::Params& p, int rows, cudaStream_t st) {
+  return attn::launch_kind<float, __nv_fp8_e4m3>(p, rows, st);
+}
+
+}  // namespace kq

@@ -1,6 +1,6 @@
 // kq_attn_kernel.cuh -- attention of the newest T tokens of each sequence over
-// its paged cache (instantiated per cache type in kq_attn_bf16.cu and
-// kq_attn_f8.cu, launched by kq_attn.cu):
+// its paged cache (instantiated per cache and query type in
+// kq_attn_<cache>_<query>.cu, launched by kq_attn.cu):
 //   s_j = scale q.k_j  or  softcap tanh(scale q.k_j / softcap)
 //   o   = sum_j 2^(s_j log2 e - m) v_j / sum_j 2^(s_j log2 e - m)
 // over the positions j that the token sees, in one pass with a running
@@ -8,8 +8,12 @@
 //
 // Bound: the cache is read once and every key and value serves the T*G query
 // rows of its head only, so up to about 64 rows the bytes bound it.  Hence
-//  * the rows of a head (T tokens x G heads) share what is loaded: they are
-//    the M of the matrix instructions, 16 or 32 per pass over the cache;
+//  * the rows of a head (T tokens x G heads) share what is loaded.  They are
+//    the N of the matrix instructions, 8 to 32 per pass over the cache, and
+//    positions (scores) and values' dims (sums) the M: S^T = K q^T, then
+//    o^T += V^T w^T.  With rows as M, 16 of them would be the least, while
+//    most decode steps have 8 or fewer; the weights go from one product's
+//    result to the next one's operand by 8 x 8 transposes between lanes;
 //  * each warp streams its own sub-tiles of 16 positions through its own ring
 //    of asynchronous 16-byte copies (any page size, order of slots and
 //    alignment of lengths: a row is one token of one head) and keeps its own
@@ -50,10 +54,10 @@ constexpr int WT = 16;           // positions per warp sub-tile
 constexpr int TK = NW * WT;      // positions per tile
 constexpr int START = 3;         // tiles' time that an item costs besides its tiles
 
-template <class Q, class C, int D, int MT>
+template <class Q, class C, int D, int NT>
 struct Cfg {
   static constexpr bool F8 = sizeof(C) == 1, QF32 = sizeof(Q) == 4;
-  static constexpr int ROWS = 16 * MT;
+  static constexpr int ROWS = 8 * NT;
   static constexpr int NQ = F8 ? (QF32 ? 2 : 1) : (QF32 ? 3 : 1);  // parts of q
   static constexpr int NP = F8 ? 2 : (QF32 ? 3 : 2);               // parts of the weights
   static constexpr int RB = D * static_cast<int>(sizeof(C)) + 16;  // bytes of a cache row in shared memory
@@ -70,7 +74,9 @@ struct Cfg {
   static constexpr int S = FIT < 6 ? FIT : 6;  // ring stages
   static constexpr int CPS = TWO ? 2 : 1;
   static constexpr int SMEM = FIXED + S * NW * STAGE;
-  static_assert(S >= 2 && S * STAGE >= ROWS * D * 4, "the warps' sums take the ring's place");
+  static constexpr bool QREG = NT * NQ * (D / 8) <= 32;  // q's operands stay in registers
+  static constexpr int OB = (D + 4) * 4;                 // bytes of a row of the warps' sums in shared memory
+  static_assert(S >= 2 && S * STAGE >= ROWS * OB, "the warps' sums take the ring's place");
 };
 
 struct Params {
@@ -92,6 +98,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// An 8 x 8 tile of 16-bit values held as matrix operands are (row lane / 4, columns 2 (lane & 3) and + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -157,11 +169,13 @@ struct Seg {
   int t0, t1;
 };
 
-template <class Q, class C, int D, int MT>
+template <class Q, class C, int D, int NT>
 struct Warp {
-  using K = Cfg<Q, C, D, MT>;
-  float o[MT][D / 8][4];
-  float m[MT][2], l[MT][2];  // maximum (in log2 units) and this lane's part of the weight sum, of rows lane/4 and + 8
+  using K = Cfg<Q, C, D, NT>;
+  // o[n][d]: dims 16 d + ... (M) of rows 8 n + ... (N): registers 0, 1 of the lane's first dim, 2, 3 of its second, for rows
+  // 8 n + 2 (lane & 3) and + 1
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];  // those rows' maximum (in log2 units) and this lane's part of the weight sum
 
   // The copies of one sub-tile: K rows, then V rows.  `page`: this lane's row's page id (row lane & 15).
   static __device__ __forceinline__ void issue(const Params& p, const Seg& g, uint32_t stage, int base, int page, int lane) {
@@ -191,181 +205,177 @@ struct Warp {
     const int j = base + (lane & 15);
     return j >= g.first && j < g.len ? __ldg(g.table + (j >> p.a.page_shift)) : 0;
   }
+  // q's operand of k-steps 2 k2 and 2 k2 + 1 for rows 8 n .. 8 n + 7, part t
+  static __device__ __forceinline__ void load_q4(uint32_t (&r)[4], uint32_t qaddr, int t, int n, int k2, int lane) {
+    ldsm4(r, qaddr + (t * K::ROWS + 8 * n + (lane & 7)) * K::QB + (lane >> 3) * 16 + k2 * 64);
+  }
 
-  // Scores, weights and sums of one sub-tile in shared memory.  pos[mt][i]: the position of the token of row 16 mt +
-  // lane/4 + 8 i; qs[mt][i]: that row's factor from the raw product to log2 units (or to the cap's argument).
+  // Scores, weights and sums of one sub-tile in shared memory.  pos[n][e]: the position of the token of row 8 n +
+  // 2 (lane & 3) + e; qs[n][e]: that row's factor from the raw product to log2 units (or to the cap's argument).
   template <bool CAREFUL>
-  __device__ __forceinline__ void tile(const Params& p, const Seg& g, uint32_t stage, uint8_t* vrow, uint32_t qaddr, int base,
-                                       const int (&pos)[MT][2], const float (&qs)[MT][2], bool all, int lane) {
+  __device__ __forceinline__ void tile(const Params& p, const Seg& g, uint32_t stage, uint8_t* vrow, uint32_t qaddr,
+                                       const uint32_t (&qreg)[K::QREG ? NT * K::NQ * (D / 32) : 1][4], int base,
+                                       const int (&pos)[NT][2], const float (&qs)[NT][2], bool all, int lane) {
     const AttnArgs& a = p.a;
-    float s[MT][2][4];
+    float s[NT][4];  // positions base + lane / 4 (0, 1) and + 8 (2, 3)
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
     // ---- scores
-    const uint32_t kaddr = stage + ((lane >> 4) * 8 + (lane & 7)) * K::RB + ((lane >> 3) & 1) * 16;
-    const uint32_t qa = qaddr + (lane & 15) * K::QB + (lane >> 4) * 16;
-    auto step = [&](int kk, uint32_t b00, uint32_t b01, uint32_t b10, uint32_t b11) {
+    const uint32_t kaddr = stage + (lane & 15) * K::RB + (lane >> 4) * 16;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+    for (int k2 = 0; k2 < D / 32; ++k2) {
+      uint32_t ka[2][4];
+      if constexpr (K::F8) {
+        uint32_t r[4];  // dims 0-15: positions 0-7, 8-15; dims 16-31 likewise
+        ldsm4(r, kaddr + k2 * 32);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ka[h][0] = f8_pair(r[2 * h]);
+          ka[h][1] = f8_pair(r[2 * h + 1]);
+          ka[h][2] = f8_pair(r[2 * h] >> 16);
+          ka[h][3] = f8_pair(r[2 * h + 1] >> 16);
+        }
+      } else {
+        ldsm4(ka[0], kaddr + k2 * 64);
+        ldsm4(ka[1], kaddr + k2 * 64 + 32);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int t = 0; t < K::NQ; ++t) {
-          uint32_t aq[4];
-          ldsm4(aq, qa + (t * K::ROWS + 16 * mt) * K::QB + kk * 32);
-          mma<K::F8>(s[mt][0], aq, b00, b01);
-          mma<K::F8>(s[mt][1], aq, b10, b11);
+          if constexpr (K::QREG) {
+            const uint32_t(&b)[4] = qreg[(n * K::NQ + t) * (D / 32) + k2];
+            mma<K::F8>(s[n], ka[0], b[0], b[1]);
+            mma<K::F8>(s[n], ka[1], b[2], b[3]);
+          } else {
+            uint32_t b[4];
+            load_q4(b, qaddr, t, n, k2, lane);
+            mma<K::F8>(s[n], ka[0], b[0], b[1]);
+            mma<K::F8>(s[n], ka[1], b[2], b[3]);
+          }
         }
-    };
-    if constexpr (K::F8) {
-#pragma unroll
-      for (int k2 = 0; k2 < D / 32; ++k2) {
-        uint32_t r[4];  // positions 0-7: dims 0-15, 16-31; positions 8-15 likewise
-        ldsm4(r, kaddr + k2 * 32);
-        step(2 * k2, f8_pair(r[0]), f8_pair(r[0] >> 16), f8_pair(r[2]), f8_pair(r[2] >> 16));
-        step(2 * k2 + 1, f8_pair(r[1]), f8_pair(r[1] >> 16), f8_pair(r[3]), f8_pair(r[3] >> 16));
-      }
-    } else {
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t r[4];
-        ldsm4(r, kaddr + kk * 32);
-        step(kk, r[0], r[1], r[2], r[3]);
-      }
     }
     // ---- weights
-    const int jq = base + 2 * (lane & 3);
+    const int j0 = base + (lane >> 2);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int e = 0; e < 4; ++e) s[n][e] *= qs[n][e & 1];
+      if (a.softcap > 0.0f) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[mt][n][e] * qs[mt][e >> 1];
-          if (a.softcap > 0.0f) x = a.softcap * 1.4426950408889634f * tanhf(x);
-          s[mt][n][e] = x;
-        }
+        for (int e = 0; e < 4; ++e) s[n][e] = a.softcap * 1.4426950408889634f * tanhf(s[n][e]);
+      }
       if (!all) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = jq + 8 * n + (e & 1), ps = pos[mt][e >> 1];
-            if (!(j <= ps && (a.window == 0 || j > ps - a.window))) s[mt][n][e] = -INFINITY;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + 8 * (e >> 1), ps = pos[n][e & 1];
+          if (!(j <= ps && (a.window == 0 || j > ps - a.window))) s[n][e] = -INFINITY;
+        }
       }
       float mx[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mx[i] = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 2));
-        mx[i] = fmaxf(mx[i], m[mt][i]);
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(s[n][e], s[n][2 + e]);
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 4));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 8));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 16));
+        mx[e] = fmaxf(mx[e], m[n][e]);
       }
-      if (__any_sync(0xFFFFFFFFu, mx[0] != m[mt][0] || mx[1] != m[mt][1])) {
+      if (__any_sync(0xFFFFFFFFu, mx[0] != m[n][0] || mx[1] != m[n][1])) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float c = mx[i] == m[mt][i] ? 1.0f : ex2(m[mt][i] - mx[i]);
-          l[mt][i] *= c;
+        for (int e = 0; e < 2; ++e) {
+          const float c = mx[e] == m[n][e] ? 1.0f : ex2(m[n][e] - mx[e]);
+          l[n][e] *= c;
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            o[mt][n][2 * i] *= c;
-            o[mt][n][2 * i + 1] *= c;
+          for (int d = 0; d < D / 16; ++d) {
+            o[n][d][e] *= c;
+            o[n][d][2 + e] *= c;
           }
-          m[mt][i] = mx[i];
+          m[n][e] = mx[e];
         }
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float mm = m[mt][i] == -INFINITY ? 0.0f : m[mt][i];  // nothing seen yet: the weights are 0
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float w = ex2(s[mt][n][2 * i + e] - mm);
-            s[mt][n][2 * i + e] = w;
-            l[mt][i] += w;
-          }
+      for (int e = 0; e < 2; ++e) {
+        const float mm = m[n][e] == -INFINITY ? 0.0f : m[n][e];  // nothing seen yet: the weights are 0
+        s[n][e] = ex2(s[n][e] - mm);
+        s[n][2 + e] = ex2(s[n][2 + e] - mm);
+        l[n][e] += s[n][e] + s[n][2 + e];
       }
     }
     if constexpr (CAREFUL) take_out(p, vrow, base, s, pos, lane);
     // ---- sums
+    uint32_t w[NT][K::NP][2];  // positions 0-7 and 8-15, as the second operand
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      uint32_t w[K::NP][4];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {  // rows lane/4 and + 8 of positions 0-7, then 8-15
-        float x = s[mt][r >> 1][2 * (r & 1)], y = s[mt][r >> 1][2 * (r & 1) + 1];
+      for (int h = 0; h < 2; ++h) {
+        float x = s[n][2 * h], y = s[n][2 * h + 1];
 #pragma unroll
         for (int t = 0; t < K::NP; ++t) {
-          w[t][r] = pack2<K::F8>(x, y);
-          const float2 b = unpack2<K::F8>(w[t][r]);
+          const uint32_t v = pack2<K::F8>(x, y);
+          const float2 b = unpack2<K::F8>(v);
           x -= b.x;
           y -= b.y;
+          w[n][t][h] = transpose8(v);
         }
       }
+    if constexpr (K::F8) {
       const uint32_t vaddr = stage + K::SUB + (lane & 15) * K::RB + (lane >> 4) * 16;
-      if constexpr (K::F8) {
 #pragma unroll
-        for (int n = 0; n < D / 32; ++n) {
-          uint32_t r[4];  // dims 0-15: positions 0-7, 8-15; dims 16-31 likewise
-          ldsm4t(r, vaddr + n * 32);
+      for (int d2 = 0; d2 < D / 32; ++d2) {
+        uint32_t r[4];  // dims 0-15: positions 0-7, 8-15; dims 16-31 likewise
+        ldsm4t(r, vaddr + d2 * 32);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t b0 = __byte_perm(r[2 * h], 0, 0x3120), b1 = __byte_perm(r[2 * h + 1], 0, 0x3120);
-            const uint32_t e0 = f8_pair(b0), e1 = f8_pair(b1), d0 = f8_pair(b0 >> 16), d1 = f8_pair(b1 >> 16);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t b0 = __byte_perm(r[2 * h], 0, 0x3120), b1 = __byte_perm(r[2 * h + 1], 0, 0x3120);
+          const uint32_t va[4] = {f8_pair(b0), f8_pair(b0 >> 16), f8_pair(b1), f8_pair(b1 >> 16)};  // even dims, odd dims
 #pragma unroll
-            for (int t = 0; t < K::NP; ++t) {
-              mma<true>(o[mt][4 * n + 2 * h], w[t], e0, e1);      // even dims
-              mma<true>(o[mt][4 * n + 2 * h + 1], w[t], d0, d1);  // odd dims
-            }
-          }
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int t = 0; t < K::NP; ++t) mma<true>(o[n][2 * d2 + h], va, w[n][t][0], w[n][t][1]);
         }
-      } else {
+      }
+    } else {
+      const uint32_t vaddr = stage + K::SUB + ((lane & 7) + (lane >> 4) * 8) * K::RB + ((lane >> 3) & 1) * 16;
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t r[4];
-          ldsm4t(r, vaddr + n * 32);
+      for (int d = 0; d < D / 16; ++d) {
+        uint32_t va[4];
+        ldsm4t(va, vaddr + d * 32);
 #pragma unroll
-          for (int t = 0; t < K::NP; ++t) {
-            mma<false>(o[mt][2 * n], w[t], r[0], r[1]);
-            mma<false>(o[mt][2 * n + 1], w[t], r[2], r[3]);
-          }
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int t = 0; t < K::NP; ++t) mma<false>(o[n][d], va, w[n][t][0], w[n][t][1]);
       }
     }
   }
 
-  // The dimension of accumulator o[.][n][e] (e & 1 within the pair).
-  static __device__ __forceinline__ int dim_of(int n, int e, int lane) {
-    if constexpr (K::F8) return 16 * (n >> 1) + 4 * (lane & 3) + 2 * (e & 1) + (n & 1);
-    return 8 * n + 2 * (lane & 3) + (e & 1);
+  // The dim of accumulator o[.][d][2 h + e].
+  static __device__ __forceinline__ int dim_of(int d, int h, int lane) {
+    return 16 * d + (K::F8 ? 2 * (lane >> 2) + h : (lane >> 2) + 8 * h);
   }
   static __device__ __forceinline__ float value_at(const uint8_t* row, int d) {
     if constexpr (K::F8) return static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(row)[d]);
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[d]);
   }
   // Adds the values that are not finite to the rows that see them, and puts zeros in their place.
-  __device__ __noinline__ void take_out(const Params& p, uint8_t* vrow, int base, const float (&s)[MT][2][4],
-                                        const int (&pos)[MT][2], int lane) {
+  __device__ __noinline__ void take_out(const Params& p, uint8_t* vrow, int base, const float (&s)[NT][4],
+                                        const int (&pos)[NT][2], int lane) {
     for (int jj = 0; jj < WT; ++jj) {
-      const int j = base + jj, from = (lane & ~3) | ((jj & 7) >> 1);
+      const int j = base + jj, from = (jj & 7) * 4 + (lane & 3);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float a0 = jj & 8 ? s[mt][1][2 * i] : s[mt][0][2 * i];
-          const float a1 = jj & 8 ? s[mt][1][2 * i + 1] : s[mt][0][2 * i + 1];
-          const float w = __shfl_sync(0xFFFFFFFFu, jj & 1 ? a1 : a0, from);
-          const bool sees = j <= pos[mt][i] && (p.a.window == 0 || j > pos[mt][i] - p.a.window);
+        for (int e = 0; e < 2; ++e) {
+          const float w = __shfl_sync(0xFFFFFFFFu, jj & 8 ? s[n][2 + e] : s[n][e], from);
+          const bool sees = j <= pos[n][e] && (p.a.window == 0 || j > pos[n][e] - p.a.window);
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n)
+          for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float v = value_at(vrow + jj * K::RB, dim_of(n, e, lane));
-              if (sees && !finite(v)) o[mt][n][2 * i + e] += w * v;
+            for (int h = 0; h < 2; ++h) {
+              const float v = value_at(vrow + jj * K::RB, dim_of(d, h, lane));
+              if (sees && !finite(v)) o[n][d][2 * h + e] += w * v;
             }
         }
     }
@@ -382,16 +392,16 @@ struct Warp {
 
   // A warp's share of a segment: sub-tile `warp` of each tile.
   template <bool CAREFUL>
-  __device__ __forceinline__ void run(const Params& p, const Seg& g, uint8_t* ring, uint32_t qaddr, const int (&pos)[MT][2],
-                                      const float (&qs)[MT][2], int warp, int lane) {
+  __device__ __forceinline__ void run(const Params& p, const Seg& g, uint8_t* ring, uint32_t qaddr, const int (&pos)[NT][2],
+                                      const float (&qs)[NT][2], int warp, int lane) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) { m[mt][i] = -INFINITY; l[mt][i] = 0.0f; }
+      for (int e = 0; e < 2; ++e) { m[n][e] = -INFINITY; l[n][e] = 0.0f; }
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
+      for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) o[n][d][e] = 0.0f;
     }
     const uint32_t rs = smem_u32(ring);
     const int n = g.t1 - g.t0, b0 = g.t0 * TK + warp * WT;
@@ -403,6 +413,15 @@ struct Warp {
       copy_commit();
       page = next;
     }
+    uint32_t qreg[K::QREG ? NT * K::NQ * (D / 32) : 1][4];
+    if constexpr (K::QREG) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int t = 0; t < K::NQ; ++t)
+#pragma unroll
+          for (int k2 = 0; k2 < D / 32; ++k2) load_q4(qreg[(i * K::NQ + t) * (D / 32) + k2], qaddr, t, i, k2, lane);
+    }
     // a sub-tile in [all_lo, all_hi] is seen by every row in full
     const int all_lo = p.a.window > 0 ? g.len - p.a.window : 0, all_hi = g.len - p.a.T;
     int slot = 0;
@@ -412,7 +431,7 @@ struct Warp {
       __syncwarp();
       const int next = i + K::S + 1 < n ? page_of(p, g, base + (K::S + 1) * TK, lane) : 0;
       if (base < g.len && base + WT > g.first)
-        tile<CAREFUL>(p, g, rs + slot * K::STAGE, ring + slot * K::STAGE + K::SUB, qaddr, base, pos, qs,
+        tile<CAREFUL>(p, g, rs + slot * K::STAGE, ring + slot * K::STAGE + K::SUB, qaddr, qreg, base, pos, qs,
                       base >= all_lo && base + WT - 1 <= all_hi, lane);
       __syncwarp();
       if (i + K::S < n) issue(p, g, rs + slot * K::STAGE, base + K::S * TK, page, lane);
@@ -423,21 +442,22 @@ struct Warp {
     copy_wait<0>();
     __syncwarp();
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[mt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][i], 1);
-        l[mt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][i], 2);
+      for (int e = 0; e < 2; ++e) {
+        l[i][e] += __shfl_xor_sync(0xFFFFFFFFu, l[i][e], 4);
+        l[i][e] += __shfl_xor_sync(0xFFFFFFFFu, l[i][e], 8);
+        l[i][e] += __shfl_xor_sync(0xFFFFFFFFu, l[i][e], 16);
       }
   }
   __device__ __forceinline__ bool all_finite() const {
     float x = 0.0f;  // a product with 0 keeps NaN and makes it of an infinity
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
+      for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x = fmaf(o[mt][n][e], 0.0f, x);
+        for (int e = 0; e < 4; ++e) x = fmaf(o[n][d][e], 0.0f, x);
     return __all_sync(0xFFFFFFFFu, x == 0.0f);
   }
 };
@@ -451,11 +471,11 @@ __device__ __forceinline__ float4 load_q(const __nv_bfloat16* p) {
 
 // q rows of an item as 16-bit parts in shared memory; rscale: each row's power of two (e4m3 cache).  A row is D / 4 lanes'
 // work (D = 256: two rounds of a warp); a warp's rows are all loaded before the first is used.
-template <class Q, class C, int D, int MT>
+template <class Q, class C, int D, int NT>
 __device__ __forceinline__ void stage_q(const Params& p, uint8_t* qsm, float* rscale, int b, int hk, int r0, int warp, int lane) {
-  using K = Cfg<Q, C, D, MT>;
+  using K = Cfg<Q, C, D, NT>;
   constexpr int LR = D < 128 ? D / 4 : 32, PR = D / 4 / LR;  // lanes per row, vectors per lane
-  constexpr int RW = 32 / LR, N = K::ROWS / (NW * RW);       // rows at a time per warp, times
+  constexpr int RW = 32 / LR, N = (K::ROWS + NW * RW - 1) / (NW * RW);  // rows at a time per warp, times
   const AttnArgs& a = p.a;
   const int R = a.T * a.G;
   float4 x[N][PR];
@@ -510,9 +530,9 @@ __device__ __forceinline__ void stage_q(const Params& p, uint8_t* qsm, float* rs
   }
 }
 
-template <class Q, class C, int D, int MT>
-__global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, MT>::CPS)) attn_kernel(const __grid_constant__ Params p) {
-  using K = Cfg<Q, C, D, MT>;
+template <class Q, class C, int D, int NT>
+__global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(const __grid_constant__ Params p) {
+  using K = Cfg<Q, C, D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_scan[NTH];
   __shared__ int s_last;
@@ -600,47 +620,46 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, MT>::CPS)) attn_kernel(cons
     g.t0 = static_cast<int>(u - i0) + g.first / TK;
     g.t1 = static_cast<int>(end - i0) + g.first / TK;
 
-    stage_q<Q, C, D, MT>(p, qsm, rscale, b, hk, r0, warp, lane);
+    stage_q<Q, C, D, NT>(p, qsm, rscale, b, hk, r0, warp, lane);
     __syncthreads();
-    int pos[MT][2];
-    float qs[MT][2];
+    int pos[NT][2];
+    float qs[NT][2];
     const float f = a.scale * a.c.k_scale * (a.softcap > 0.0f ? 1.0f / a.softcap : 1.4426950408889634f);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 16 * mt + (lane >> 2) + 8 * i;
-        pos[mt][i] = g.len - a.T + min((r0 + r) / a.G, a.T - 1);
-        qs[mt][i] = f * rscale[r];
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * (lane & 3) + e;
+        pos[n][e] = g.len - a.T + min((r0 + r) / a.G, a.T - 1);
+        qs[n][e] = f * rscale[r];
       }
-    Warp<Q, C, D, MT> w;
+    Warp<Q, C, D, NT> w;
     uint8_t* mine = ring + warp * (K::S * K::STAGE);
     w.template run<false>(p, g, mine, smem_u32(qsm), pos, qs, warp, lane);
     if (!w.all_finite()) {
-      Warp<Q, C, D, MT> again;  // an object of its own: the call in it keeps this one out of registers
+      Warp<Q, C, D, NT> again;  // an object of its own: the call in it keeps this one out of registers
       again.template run<true>(p, g, mine, smem_u32(qsm), pos, qs, warp, lane);
       w = again;
     }
 
     // ---- the warps' sums, side by side in the ring's place
-    float* so = reinterpret_cast<float*>(mine);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 16 * mt + (lane >> 2) + 8 * i;
-        if ((lane & 3) == 0) {
-          w_ml[(warp * K::ROWS + r) * 2] = w.m[mt][i];
-          w_ml[(warp * K::ROWS + r) * 2 + 1] = w.l[mt][i];
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * (lane & 3) + e;
+        if (lane < 4) {
+          w_ml[(warp * K::ROWS + r) * 2] = w.m[n][e];
+          w_ml[(warp * K::ROWS + r) * 2 + 1] = w.l[n][e];
         }
+        float* so = reinterpret_cast<float*>(mine + r * K::OB);
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
+        for (int d = 0; d < D / 16; ++d) {
           if constexpr (K::F8) {
-            if (n & 1) continue;
-            *reinterpret_cast<float4*>(so + r * D + 16 * (n >> 1) + 4 * (lane & 3)) =
-                make_float4(w.o[mt][n][2 * i], w.o[mt][n + 1][2 * i], w.o[mt][n][2 * i + 1], w.o[mt][n + 1][2 * i + 1]);
+            *reinterpret_cast<float2*>(so + w.dim_of(d, 0, lane)) = make_float2(w.o[n][d][e], w.o[n][d][2 + e]);
           } else {
-            *reinterpret_cast<float2*>(so + r * D + 8 * n + 2 * (lane & 3)) = make_float2(w.o[mt][n][2 * i], w.o[mt][n][2 * i + 1]);
+            so[w.dim_of(d, 0, lane)] = w.o[n][d][e];
+            so[w.dim_of(d, 1, lane)] = w.o[n][d][2 + e];
           }
         }
       }
@@ -658,7 +677,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, MT>::CPS)) attn_kernel(cons
       for (int k = 0; k < NW; ++k) {
         const float e = ex2(w_ml[(k * K::ROWS + r) * 2] - ms);
         ll += w_ml[(k * K::ROWS + r) * 2 + 1] * e;
-        add4(acc, e, *reinterpret_cast<const float4*>(ring + k * (K::S * K::STAGE) + (r * D + d) * 4));
+        add4(acc, e, *reinterpret_cast<const float4*>(ring + k * (K::S * K::STAGE) + r * K::OB + d * 4));
       }
       if (whole) {
         write(r, d, acc, ll == 0.0f ? 0.0f : a.c.v_scale / ll);
@@ -721,25 +740,41 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, MT>::CPS)) attn_kernel(cons
   }
 }
 
-template <class Q, class C, int D, int MT>
+template <class Q, class C, int D, int NT>
 cudaError_t launch_one(const Params& p, cudaStream_t st) {
-  using K = Cfg<Q, C, D, MT>;
+  using K = Cfg<Q, C, D, NT>;
   const size_t smem = K::SMEM + 8 * (static_cast<size_t>(p.a.B) + 1);
   static int set[64] = {0};  // shared memory allowed so far, per device
   const int dev = current_device_id();
   if (set[dev] < static_cast<int>(smem)) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_kernel<Q, C, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(attn_kernel<Q, C, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     set[dev] = static_cast<int>(smem);
   }
-  return launch_pdl(attn_kernel<Q, C, D, MT>, dim3(num_sms() * K::CPS), dim3(NTH), smem, st, p);
+  return launch_pdl(attn_kernel<Q, C, D, NT>, dim3(num_sms() * K::CPS), dim3(NTH), smem, st, p);
+}
+
+template <class Q, class C>
+cudaError_t launch_kind(const Params& p, int rows, cudaStream_t st) {
+  switch (p.a.c.head_dim * 100 + rows) {
+    case 6408: return launch_one<Q, C, 64, 1>(p, st);
+    case 6416: return launch_one<Q, C, 64, 2>(p, st);
+    case 6432: return launch_one<Q, C, 64, 4>(p, st);
+    case 12808: return launch_one<Q, C, 128, 1>(p, st);
+    case 12816: return launch_one<Q, C, 128, 2>(p, st);
+    case 12832: return launch_one<Q, C, 128, 4>(p, st);
+    case 25608: return launch_one<Q, C, 256, 1>(p, st);
+    default: return launch_one<Q, C, 256, 2>(p, st);
+  }
 }
 
 }  // namespace attn
 
-// One translation unit per cache type (rows: query rows per pass, 16 or 32).
-cudaError_t launch_attn_bf16(const attn::Params& p, int q_bf16, int rows, cudaStream_t st);
-cudaError_t launch_attn_f8(const attn::Params& p, int q_bf16, int rows, cudaStream_t st);
+// One translation unit per cache and query type (rows: query rows per pass, 8, 16 or 32).
+cudaError_t launch_attn_bf16_bf16(const attn::Params& p, int rows, cudaStream_t st);
+cudaError_t launch_attn_bf16_f32(const attn::Params& p, int rows, cudaStream_t st);
+cudaError_t launch_attn_f8_bf16(const attn::Params& p, int rows, cudaStream_t st);
+cudaError_t launch_attn_f8_f32(const attn::Params& p, int rows, cudaStream_t st);
 
 }  // namespace kq

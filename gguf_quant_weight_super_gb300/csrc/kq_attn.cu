@@ -21,7 +21,7 @@ Layout layout(int head_dim, int Hkv, int64_t B, int64_t T, int Hq) {
   const int R = static_cast<int>(T) * (Hq / Hkv);
   L.rows = rows_per_pass(head_dim, R);
   L.RT = R > 0 ? (R + L.rows - 1) / L.rows : 1;
-  const size_t slots = 2 * static_cast<size_t>(num_sms()) * 2;  // two parts per CTA, at most two CTAs per SM
+  const size_t slots = 2 * static_cast<size_t>(num_sms()) * 3;  // two parts per CTA, at most three CTAs per SM
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   L.count_off = 0;
   L.ml_off = up(static_cast<size_t>(B) * Hkv * L.RT * sizeof(int));

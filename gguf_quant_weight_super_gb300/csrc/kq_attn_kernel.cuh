@@ -66,13 +66,12 @@ struct Cfg {
   static constexpr int QBYTES = NQ * ROWS * QB;
   static constexpr int HDR = (ROWS * (2 + 2 * NW) * 4 + 127) / 128 * 128;  // row scales, the join's and the warps' statistics
   static constexpr int FIXED = HDR + QBYTES;
-  // two CTAs per SM where a ring of at least two stages fits beside q in half of the shared memory (the rest is the
-  // line of tiles' index, 8 bytes per sequence)
-  static constexpr int HALF = 110 * 1024, FULL = 192 * 1024;
-  static constexpr bool TWO = FIXED + 2 * NW * STAGE <= HALF;
-  static constexpr int FIT = ((TWO ? HALF : FULL) - FIXED) / (NW * STAGE);
-  static constexpr int S = FIT < 6 ? FIT : 6;  // ring stages
-  static constexpr int CPS = TWO ? 2 : 1;
+  // CTAs per SM: three where the sums take few registers, two where a ring of at least two stages fits beside q in half of
+  // the shared memory (what is left of it is the line of tiles' index, 8 bytes per sequence), else one
+  static constexpr int budget(int ctas) { return (ctas == 3 ? 73 : ctas == 2 ? 110 : 192) * 1024; }
+  static constexpr int stages(int ctas) { return (budget(ctas) - FIXED) / (NW * STAGE); }
+  static constexpr int CPS = NT * D <= 128 && stages(3) >= 2 ? 3 : stages(2) >= 2 ? 2 : 1;
+  static constexpr int S = stages(CPS) < 6 ? stages(CPS) : 6;  // ring stages
   static constexpr int SMEM = FIXED + S * NW * STAGE;
   static constexpr bool QREG = NT * NQ * (D / 8) <= 32;  // q's operands stay in registers
   static constexpr int OB = (D + 4) * 4;                 // bytes of a row of the warps' sums in shared memory
@@ -180,6 +179,27 @@ struct Warp {
   // The copies of one sub-tile: K rows, then V rows.  `page`: this lane's row's page id (row lane & 15).
   static __device__ __forceinline__ void issue(const Params& p, const Seg& g, uint32_t stage, int base, int page, int lane) {
     const AttnArgs& a = p.a;
+    constexpr int CH = D * static_cast<int>(sizeof(C)) / 16;  // 16-byte chunks per row
+    if (base >= g.first && base + WT <= g.len && a.c.page_size >= WT && static_cast<unsigned>(page) < a.c.n_pages) {
+      // 16 whole rows of one page, at one stride
+      const int64_t row = a.c.slot_stride * static_cast<int64_t>(sizeof(C));
+      int64_t src = (page * a.c.page_stride + g.head_off) * static_cast<int64_t>(sizeof(C)) +
+                    ((base & (a.c.page_size - 1)) + lane / CH) * row + lane % CH * 16;
+      uint32_t dst = stage + lane / CH * K::RB + lane % CH * 16;
+#pragma unroll
+      for (int i = 0; i < CH / 2; ++i) {
+        copy16(dst, static_cast<const uint8_t*>(a.c.k) + src, true);
+        copy16(dst + K::SUB, static_cast<const uint8_t*>(a.c.v) + src, true);
+        src += 32 / CH * row;
+        dst += 32 / CH * K::RB;
+      }
+    } else {
+      issue_rows(p, g, stage, base, page, lane);
+    }
+  }
+  static __device__ __noinline__ void issue_rows(const Params& p, const Seg& g, uint32_t stage, int base, int page, int lane) {
+    const AttnArgs& a = p.a;
+    constexpr int CH = D * static_cast<int>(sizeof(C)) / 16;
     const int j = base + (lane & 15);
     bool on = j >= g.first && j < g.len;
     if (on && (page < 0 || page >= a.c.n_pages)) {
@@ -189,8 +209,7 @@ struct Warp {
     const int64_t off = on ? (page * a.c.page_stride + (j & (a.c.page_size - 1)) * a.c.slot_stride + g.head_off) *
                                  static_cast<int64_t>(sizeof(C))
                            : -1;
-    constexpr int CH = D * static_cast<int>(sizeof(C)) / 16;  // 16-byte chunks per row
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < CH / 2; ++i) {
       const int c = i * 32 + lane, row = c / CH, col = c % CH;
       const int64_t ro = __shfl_sync(0xFFFFFFFFu, off, row);

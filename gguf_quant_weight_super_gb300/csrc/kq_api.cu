@@ -460,6 +460,7 @@ kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, in
   a.ws = workspace;
   a.err = device_error_ptr();
   cudaError_t e = launch_attn(a, q_dtype == KQ_BF16, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return KQ_ERR_UNSUPPORTED;
   if (e == cudaSuccess) e = cudaGetLastError();
   return cuda_status(e);
 }

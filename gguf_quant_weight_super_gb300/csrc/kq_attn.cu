@@ -38,6 +38,9 @@ size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t B, int64_t T, int Hq)
 
 cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st) {
   const Layout L = layout(a.c.head_dim, a.c.n_kv_heads, a.B, a.T, a.Hq);
+  // the line of tiles is counted in 31 bits
+  const int64_t tiles = ((a.max_pages << a.page_shift) + TK - 1) / TK + START + 1;
+  if (tiles * a.B > INT32_MAX / (a.c.n_kv_heads * L.RT)) return cudaErrorNotSupported;
   Params p;
   p.a = a;
   p.RT = L.RT;

@@ -67,7 +67,7 @@ struct Cfg {
   static constexpr int HDR = (ROWS * (2 + 2 * NW) * 4 + 127) / 128 * 128;  // row scales, the join's and the warps' statistics
   static constexpr int FIXED = HDR + QBYTES;
   // CTAs per SM: three where the sums take few registers, two where a ring of at least two stages fits beside q in half of
-  // the shared memory (what is left of it is the line of tiles' index, 8 bytes per sequence), else one
+  // the shared memory (what is left of it is the line of tiles' index, 4 bytes per sequence), else one
   static constexpr int budget(int ctas) { return (ctas == 3 ? 73 : ctas == 2 ? 110 : 192) * 1024; }
   static constexpr int stages(int ctas) { return (budget(ctas) - FIXED) / (NW * STAGE); }
   static constexpr int CPS = NT * D <= 128 && stages(3) >= 2 ? 3 : stages(2) >= 2 ? 2 : 1;
@@ -553,7 +553,7 @@ template <class Q, class C, int D, int NT>
 __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(const __grid_constant__ Params p) {
   using K = Cfg<Q, C, D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_scan[NTH];
+  __shared__ int s_scan[NW];
   __shared__ int s_last;
   float* rscale = reinterpret_cast<float*>(smem);  // [ROWS]
   float* s_i = rscale + K::ROWS;                   // [ROWS] the join's 1 / weight sum
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
   uint8_t* qsm = smem + K::HDR;
   uint8_t* ring = smem + K::FIXED;
   const AttnArgs& a = p.a;
-  int64_t* prefix = reinterpret_cast<int64_t*>(ring + K::S * NW * K::STAGE);  // [B + 1] tiles before each sequence
+  int* prefix = reinterpret_cast<int*>(ring + K::S * NW * K::STAGE);  // [B + 1] tiles before each sequence
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
@@ -581,17 +581,17 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
   const int per = (a.B + NTH - 1) / NTH;
   {
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
-    int64_t n = 0;
+    int n = 0;
     for (int b = b0; b < b1; ++b) n += tiles_of(length(b, blockIdx.x == 0));
-    int64_t incl = n;
+    int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      const int t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += t;
     }
     if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
-    int64_t before = incl - n;
+    int before = incl - n;
     for (int w = 0; w < warp; ++w) before += s_scan[w];
     for (int b = b0; b < b1; ++b) {
       prefix[b] = before;
@@ -600,24 +600,26 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
     }
     __syncthreads();
   }
-  const int64_t HR = static_cast<int64_t>(a.c.n_kv_heads) * p.RT;
-  const int64_t total = prefix[a.B] * HR;
-  const int64_t nc = total < gridDim.x ? total : gridDim.x, c = blockIdx.x;
-  if (c >= nc) return;
-  const int64_t lo = c * total / nc, hi = (c + 1) * total / nc;
+  const int HR = a.c.n_kv_heads * p.RT;  // the host has seen to it that the line's units fit 31 bits
+  const int total = prefix[a.B] * HR;
+  const int nc = min(total, static_cast<int>(gridDim.x));
+  if (static_cast<int>(blockIdx.x) >= nc) return;
+  // ranges 0 .. nc - 1: `more` of share + 1 units, then of share
+  const int share = total / nc, more = total - share * nc;
+  auto bound = [&](int k) { return k * share + min(k, more); };
+  auto range_of = [&](int u) { return u < more * (share + 1) ? u / (share + 1) : more + (u - more * (share + 1)) / share; };
 
-  for (int64_t u = lo; u < hi;) {
+  const int range = blockIdx.x, lo = bound(range), hi = bound(range + 1);
+  for (int u = lo; u < hi;) {
     int b = 0;  // the last sequence that starts at or before u
     for (int w = 1 << (31 - __clz(a.B)); w > 0; w >>= 1)
       if (b + w < a.B && prefix[b + w] * HR <= u) b += w;
-    const int nt = static_cast<int>(prefix[b + 1] - prefix[b]);
-    const int64_t in = u - prefix[b] * HR;
-    const int hr = static_cast<int>(in / nt), hk = hr / p.RT, rt = hr - hk * p.RT;
+    const int nt = prefix[b + 1] - prefix[b], hr = (u - prefix[b] * HR) / nt, hk = hr / p.RT, rt = hr - hk * p.RT;
     Seg g;
     g.len = length(b, false);
-    const int64_t i1 = prefix[b] * HR + static_cast<int64_t>(hr + 1) * nt;  // the item's end
-    const int64_t i0 = g.len > 0 ? i1 - nt + START : i1 - 1;                // its first tile
-    const int64_t end = i1 < hi ? i1 : hi;
+    const int i1 = prefix[b] * HR + (hr + 1) * nt;            // the item's end
+    const int i0 = g.len > 0 ? i1 - nt + START : i1 - 1;      // its first tile
+    const int end = min(i1, hi);
     if (u < i0) u = i0;
     if (u >= end) {  // none of its tiles is in this range
       u = end;
@@ -636,8 +638,8 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
     g.first = first_of(g.len);
     g.table = a.page_table + b * a.max_pages;
     g.head_off = hk * a.c.head_stride;
-    g.t0 = static_cast<int>(u - i0) + g.first / TK;
-    g.t1 = static_cast<int>(end - i0) + g.first / TK;
+    g.t0 = u - i0 + g.first / TK;
+    g.t1 = end - i0 + g.first / TK;
 
     stage_q<Q, C, D, NT>(p, qsm, rscale, b, hk, r0, warp, lane);
     __syncthreads();
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
       }
     __syncthreads();
     const bool whole = u == i0 && end == i1;
-    const int slot = static_cast<int>(2 * c + (lo >= i0 ? 1 : 0));  // the range starts in these tiles (1), or before them
+    const int slot = 2 * range + (lo >= i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
     for (int x = threadIdx.x; x < R * (D / 4); x += NTH) {
       const int r = x / (D / 4), d = 4 * (x % (D / 4));
       float mm = -INFINITY, ll = 0.0f;
@@ -707,12 +709,12 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
     }
     if (!whole) {
       // ---- the last CTA of the item to arrive joins the ranges' sums
-      const int ca = static_cast<int>(((i0 + 1) * nc - 1) / total), cb = static_cast<int>((i1 * nc - 1) / total);
+      const int ca = range_of(i0), cb = range_of(i1 - 1);
       const int parts = cb - ca + 1;  // the item's tiles lie in ranges ca .. cb
-      __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
-        int* cnt = p.count + (static_cast<int64_t>(b) * HR + hr);
+        __threadfence();  // after the barrier: orders the whole block's stores before the arrival
+        int* cnt = p.count + (b * HR + hr);
         s_last = atomicAdd(cnt, 1) == parts - 1;
         if (s_last) *cnt = 0;
       }
@@ -720,37 +722,53 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
       if (s_last) {
         __threadfence();
         // every range but the first starts in the item's tiles
-        const int slot0 = 2 * ca + (static_cast<int64_t>(ca) * total / nc >= i0 ? 1 : 0);
+        const int slot0 = 2 * ca + (bound(ca) >= i0 ? 1 : 0);
         auto slot_of = [&](int k) { return k == 0 ? slot0 : 2 * (ca + k) + 1; };
-        float* factor = reinterpret_cast<float*>(ring);  // [parts][R]
-        for (int r = warp; r < R; r += NW) {
-          float mm = -INFINITY, ll = 0.0f;
-          for (int k = lane; k < parts; k += 32) {
-            const float x = __ldcg(p.part_ml + (static_cast<int64_t>(slot_of(k)) * K::ROWS + r) * 2);
-            factor[k * R + r] = x;
-            mm = fmaxf(mm, x);
-          }
+        float* factor = reinterpret_cast<float*>(ring);  // [parts][rows], as many rows at a time as fit
+        const int fit = min(R, K::S * NW * K::STAGE / 4 / parts);
+        for (int rb = 0; rb < R; rb += fit) {
+          const int rows = min(fit, R - rb);
+          for (int r = warp; r < rows; r += NW) {
+            float mm = -INFINITY, ll = 0.0f;
+            for (int k = lane; k < parts; k += 32) {
+              const float x = __ldcg(p.part_ml + (static_cast<int64_t>(slot_of(k)) * K::ROWS + rb + r) * 2);
+              factor[k * rows + r] = x;
+              mm = fmaxf(mm, x);
+            }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
-          const float ms = mm == -INFINITY ? 0.0f : mm;
-          for (int k = lane; k < parts; k += 32) {
-            const float e = ex2(factor[k * R + r] - ms);
-            factor[k * R + r] = e;
-            ll += e * __ldcg(p.part_ml + (static_cast<int64_t>(slot_of(k)) * K::ROWS + r) * 2 + 1);
-          }
+            for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+            const float ms = mm == -INFINITY ? 0.0f : mm;
+            for (int k = lane; k < parts; k += 32) {
+              const float e = ex2(factor[k * rows + r] - ms);
+              factor[k * rows + r] = e;
+              ll += e * __ldcg(p.part_ml + (static_cast<int64_t>(slot_of(k)) * K::ROWS + rb + r) * 2 + 1);
+            }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o);
-          if (lane == 0) s_i[r] = ll == 0.0f ? 0.0f : a.c.v_scale / ll;
-        }
-        __syncthreads();
-        for (int x = threadIdx.x; x < R * (D / 4); x += NTH) {
-          const int r = x / (D / 4), d = 4 * (x % (D / 4));
-          float4 acc = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-          for (int k = 0; k < parts; ++k)
-            add4(acc, factor[k * R + r],
-                 __ldcg(reinterpret_cast<const float4*>(p.part + (static_cast<int64_t>(slot_of(k)) * K::ROWS + r) * D + d)));
-          write(r, d, acc, s_i[r]);
+            for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o);
+            if (lane == 0) s_i[r] = ll == 0.0f ? 0.0f : a.c.v_scale / ll;
+          }
+          __syncthreads();
+          constexpr int XU = 2;  // vectors at a time per thread, of four parts: their loads are in flight together
+          for (int x0 = threadIdx.x; x0 < rows * (D / 4); x0 += XU * NTH) {
+            float4 acc[XU];
+#pragma unroll
+            for (int i = 0; i < XU; ++i) acc[i] = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int k = 0; k < parts; ++k) {
+              const float4* part = reinterpret_cast<const float4*>(p.part + (static_cast<int64_t>(slot_of(k)) * K::ROWS + rb) * D);
+#pragma unroll
+              for (int i = 0; i < XU; ++i) {
+                const int x = x0 + i * NTH;
+                if (x < rows * (D / 4)) add4(acc[i], factor[k * rows + x / (D / 4)], __ldcg(part + x));
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < XU; ++i) {
+              const int x = x0 + i * NTH;
+              if (x < rows * (D / 4)) write(rb + x / (D / 4), 4 * (x % (D / 4)), acc[i], s_i[x / (D / 4)]);
+            }
+          }
+          __syncthreads();
         }
       }
     }
@@ -762,7 +780,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
 template <class Q, class C, int D, int NT>
 cudaError_t launch_one(const Params& p, cudaStream_t st) {
   using K = Cfg<Q, C, D, NT>;
-  const size_t smem = K::SMEM + 8 * (static_cast<size_t>(p.a.B) + 1);
+  const size_t smem = K::SMEM + 4 * (static_cast<size_t>(p.a.B) + 1);
   static int set[64] = {0};  // shared memory allowed so far, per device
   const int dev = current_device_id();
   if (set[dev] < static_cast<int>(smem)) {

@@ -489,3 +489,10 @@ def test_append_then_attend_is_a_decode_loop():
                 o = (p / p.sum()) @ vv[:, h // 2]
                 sv = (p / p.sum()) @ np.abs(vv[:, h // 2])
                 assert np.all(np.abs(f64(outs[i].float())[b, 0, h] - o) <= 2.0 ** -8 * np.abs(o) + 2.0 ** -14 * sv)
+
+
+@pytest.mark.parametrize("T,G,dtype", [(1, 1, BF16), (16, 2, BF16), (8, 4, F8)])
+def test_attn_one_head_over_every_range(T, G, dtype):
+    """One head's long cache: all the device's CTAs, and the left-over ranges, hold a part of the same item."""
+    P = Paged([150001], 1, 64, 64, dtype, seed=29)
+    check_attn(P, rand_q(1, T, G, 64, BF16, 30))

@@ -18,6 +18,10 @@
 // two vectors of four values that are each other's rotation partners (i and
 // i + rot/2, or adjacent pairs when interleaved), so the rotation needs no
 // exchange between lanes and the norm one shuffle sum over the row's lanes.
+// A CTA works on one token: each group of lanes takes up to four of its heads,
+// whose loads are all in flight together, and reads the token's cosines and
+// sines once for them.  With few tokens a group takes one head, so that the
+// rows spread over more SMs.
 #include "kq_cache.h"
 
 namespace kq {
@@ -50,14 +54,17 @@ __device__ __forceinline__ float4 scale4(float4 v, float s, float4 w, float off)
   return make_float4(v.x * s * (w.x + off), v.y * s * (w.y + off), v.z * s * (w.z + off), v.w * s * (w.w + off));
 }
 
-// X: q, k, v; O: q_out; C: the cache.  LG = D / 8 lanes hold one row.
-template <class X, class O, class C, int LG>
+// X: q, k, v; O: q_out; C: the cache.  LG = D / 8 lanes hold one row; U rows per group of lanes.
+template <class X, class O, class C, int LG, int U>
 __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int D = 8 * LG;
+  constexpr int D = 8 * LG, NG = ATH / LG;
   pdl_wait();
   pdl_launch_dependents();
   const int Hkv = a.c.n_kv_heads, H = a.Hq + 2 * Hkv;
-  const uint32_t rows = static_cast<uint32_t>(a.B) * a.T * H;
+  const uint32_t per = (H + NG * U - 1) / (NG * U);  // CTAs per token
+  const uint32_t tok = blockIdx.x / per;
+  const int h0 = static_cast<int>(blockIdx.x - tok * per) * (NG * U) + static_cast<int>(threadIdx.x) / LG;
+  const int b = tok / a.T, t = tok - b * a.T;
   const int l = threadIdx.x % LG;
   const int rot = a.rope.rot_dim, rl = rot / 8;
   // the row's two vectors of this lane
@@ -69,95 +76,109 @@ __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ App
     e0 = 4 * l;
     e1 = rot / 2 + 4 * l;
   }
-  // every lane of a warp runs the same number of rounds (the norm's shuffles)
-  const uint32_t step = gridDim.x * (ATH / LG);
-  for (uint32_t r0 = blockIdx.x * (ATH / LG); r0 < rows; r0 += step) {
-    const uint32_t r = r0 + threadIdx.x / LG;
-    const bool in = r < rows;
-    const uint32_t tok = in ? r / H : 0;
-    const int h = in ? static_cast<int>(r - tok * H) : 0;
-    const int b = tok / a.T, t = tok - b * a.T;
-    const int kind = h < a.Hq ? 0 : (h < a.Hq + Hkv ? 1 : 2);  // q, k, v
-    const int hk = kind == 0 ? h : h - a.Hq - (kind == 2 ? Hkv : 0);
-    const X* src = kind == 0   ? static_cast<const X*>(a.q) + tok * a.q_stride
-                   : kind == 1 ? static_cast<const X*>(a.k) + tok * a.k_stride
-                               : static_cast<const X*>(a.v) + tok * a.v_stride;
-    src += static_cast<int64_t>(hk) * D;
-    float4 x0 = make_float4(0, 0, 0, 0), x1 = x0;
-    if (in) {
-      x0 = load4(src + e0);
-      x1 = load4(src + e1);
+  // head h: q, then k, then v
+  float4 x0[U], x1[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int h = h0 + i * NG;
+    x0[i] = x1[i] = make_float4(0, 0, 0, 0);
+    if (h < H) {
+      const X* src = h < a.Hq ? static_cast<const X*>(a.q) + tok * a.q_stride + static_cast<int64_t>(h) * D
+                     : h < a.Hq + Hkv
+                         ? static_cast<const X*>(a.k) + tok * a.k_stride + static_cast<int64_t>(h - a.Hq) * D
+                         : static_cast<const X*>(a.v) + tok * a.v_stride + static_cast<int64_t>(h - a.Hq - Hkv) * D;
+      x0[i] = load4(src + e0);
+      x1[i] = load4(src + e1);
     }
-    const int pos = in ? __ldg(a.seq_lens + b) - a.T + t : -1;
-    bool ok = pos >= 0;
-    if (ok && rot > 0 && pos >= a.rope.n_positions) {
-      if (l == 0) record_error(a.err, DEV_ERR_POSITION);
-      ok = false;
+  }
+  const int pos = __ldg(a.seq_lens + b) - a.T + t;
+  bool ok = pos >= 0;
+  if (ok && rot > 0 && pos >= a.rope.n_positions) {
+    if (threadIdx.x == 0) record_error(a.err, DEV_ERR_POSITION);
+    ok = false;
+  }
+  int page = -1;
+  float4 c = make_float4(1, 1, 1, 1), s = make_float4(0, 0, 0, 0);
+  if (ok) {
+    const int64_t pi = pos >> a.page_shift;
+    if (pi < a.max_pages) page = __ldg(a.page_table + b * a.max_pages + pi);
+    if (l < rl) {
+      const float* cs = a.rope.cos_sin + static_cast<int64_t>(pos) * rot + 4 * l;
+      c = load4(cs);
+      s = load4(cs + rot / 2);
     }
-    const float* nw = kind == 0 ? a.rope.q_norm : kind == 1 ? a.rope.k_norm : nullptr;
-    float ss = sq4(x0) + sq4(x1);
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int h = h0 + i * NG;
+    const bool isq = h < a.Hq, isk = !isq && h < a.Hq + Hkv;
+    const float* nw = isq ? a.rope.q_norm : isk ? a.rope.k_norm : nullptr;
+    float ss = sq4(x0[i]) + sq4(x1[i]);
 #pragma unroll
     for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     if (nw) {
-      const float s = rsqrtf(ss * (1.0f / D) + a.rope.eps);
-      x0 = scale4(x0, s, load4(nw + e0), a.rope.norm_offset);
-      x1 = scale4(x1, s, load4(nw + e1), a.rope.norm_offset);
+      const float f = rsqrtf(ss * (1.0f / D) + a.rope.eps);
+      x0[i] = scale4(x0[i], f, load4(nw + e0), a.rope.norm_offset);
+      x1[i] = scale4(x1[i], f, load4(nw + e1), a.rope.norm_offset);
     }
-    if (kind != 2 && l < rl && ok) {
-      const float* cs = a.rope.cos_sin + static_cast<int64_t>(pos) * rot + 4 * l;
-      const float4 c = load4(cs), s = load4(cs + rot / 2);
-      if (a.rope.interleaved) {  // pairs (x0.x, x0.y), (x0.z, x0.w), (x1.x, x1.y), (x1.z, x1.w)
-        const float4 p = x0, q = x1;
-        x0 = make_float4(p.x * c.x - p.y * s.x, p.y * c.x + p.x * s.x, p.z * c.y - p.w * s.y, p.w * c.y + p.z * s.y);
-        x1 = make_float4(q.x * c.z - q.y * s.z, q.y * c.z + q.x * s.z, q.z * c.w - q.w * s.w, q.w * c.w + q.z * s.w);
+    if ((isq || isk) && l < rl && ok) {
+      const float4 p = x0[i], q = x1[i];
+      if (a.rope.interleaved) {  // pairs (p.x, p.y), (p.z, p.w), (q.x, q.y), (q.z, q.w)
+        x0[i] = make_float4(p.x * c.x - p.y * s.x, p.y * c.x + p.x * s.x, p.z * c.y - p.w * s.y, p.w * c.y + p.z * s.y);
+        x1[i] = make_float4(q.x * c.z - q.y * s.z, q.y * c.z + q.x * s.z, q.z * c.w - q.w * s.w, q.w * c.w + q.z * s.w);
       } else {
-        const float4 p = x0, q = x1;
-        x0 = make_float4(p.x * c.x - q.x * s.x, p.y * c.y - q.y * s.y, p.z * c.z - q.z * s.z, p.w * c.w - q.w * s.w);
-        x1 = make_float4(q.x * c.x + p.x * s.x, q.y * c.y + p.y * s.y, q.z * c.z + p.z * s.z, q.w * c.w + p.w * s.w);
+        x0[i] = make_float4(p.x * c.x - q.x * s.x, p.y * c.y - q.y * s.y, p.z * c.z - q.z * s.z, p.w * c.w - q.w * s.w);
+        x1[i] = make_float4(q.x * c.x + p.x * s.x, q.y * c.y + p.y * s.y, q.z * c.z + p.z * s.z, q.w * c.w + p.w * s.w);
       }
     }
-    if (!in) continue;
-    if (kind == 0) {
-      if (!ok) x0 = x1 = make_float4(0, 0, 0, 0);
-      O* dst = static_cast<O*>(a.q_out) + static_cast<int64_t>(r - tok * 2 * Hkv) * D;
-      store4(dst + e0, x0);
-      store4(dst + e1, x1);
+    if (h >= H) continue;
+    if (isq) {
+      if (!ok) x0[i] = x1[i] = make_float4(0, 0, 0, 0);
+      O* dst = static_cast<O*>(a.q_out) + (static_cast<int64_t>(tok) * a.Hq + h) * D;
+      store4(dst + e0, x0[i]);
+      store4(dst + e1, x1[i]);
     } else if (ok) {
-      const int64_t pi = pos >> a.page_shift;
-      const int page = pi < a.max_pages ? __ldg(a.page_table + b * a.max_pages + pi) : -1;
       if (page < 0 || page >= a.c.n_pages) {
         if (l == 0) record_error(a.err, DEV_ERR_PAGE);
         continue;
       }
-      C* dst = static_cast<C*>(kind == 1 ? a.c.k : a.c.v) + page * a.c.page_stride +
+      const int hk = isk ? h - a.Hq : h - a.Hq - Hkv;
+      C* dst = static_cast<C*>(isk ? a.c.k : a.c.v) + page * a.c.page_stride +
                (pos & (a.c.page_size - 1)) * a.c.slot_stride + hk * a.c.head_stride;
-      const float sc = kind == 1 ? a.c.k_scale : a.c.v_scale;
+      const float sc = isk ? a.c.k_scale : a.c.v_scale;
       if (sc != 1.0f) {
-        x0 = make_float4(x0.x / sc, x0.y / sc, x0.z / sc, x0.w / sc);
-        x1 = make_float4(x1.x / sc, x1.y / sc, x1.z / sc, x1.w / sc);
+        x0[i] = make_float4(x0[i].x / sc, x0[i].y / sc, x0[i].z / sc, x0[i].w / sc);
+        x1[i] = make_float4(x1[i].x / sc, x1[i].y / sc, x1[i].z / sc, x1[i].w / sc);
       }
-      store4(dst + e0, x0);
-      store4(dst + e1, x1);
+      store4(dst + e0, x0[i]);
+      store4(dst + e1, x1[i]);
     }
   }
 }
 
-template <class X, class O, class C>
+template <class X, class O, class C, int LG>
 cudaError_t launch_d(const AppendArgs& a, cudaStream_t st) {
-  const int D = a.c.head_dim;
-  const int64_t rows = static_cast<int64_t>(a.B) * a.T * (a.Hq + 2 * a.c.n_kv_heads);
-  const int rpc = ATH / (D / 8);
-  const int64_t want = (rows + rpc - 1) / rpc, most = static_cast<int64_t>(num_sms()) * (2048 / ATH);
-  const dim3 grid(static_cast<unsigned>(want < most ? want : most)), block(ATH);
-  switch (D) {
-    case 64: return launch_pdl(append_kernel<X, O, C, 8>, grid, block, 0, st, a);
-    case 128: return launch_pdl(append_kernel<X, O, C, 16>, grid, block, 0, st, a);
-    default: return launch_pdl(append_kernel<X, O, C, 32>, grid, block, 0, st, a);
+  constexpr int NG = ATH / LG;
+  const int H = a.Hq + 2 * a.c.n_kv_heads;
+  const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
+  // four heads per group once that still fills the device's eight CTAs per SM
+  const int64_t four = tokens * ((H + 4 * NG - 1) / (4 * NG)), one = tokens * ((H + NG - 1) / NG);
+  if (four >= 8 * num_sms())
+    return launch_pdl(append_kernel<X, O, C, LG, 4>, dim3(static_cast<unsigned>(four)), dim3(ATH), 0, st, a);
+  return launch_pdl(append_kernel<X, O, C, LG, 1>, dim3(static_cast<unsigned>(one)), dim3(ATH), 0, st, a);
+}
+
+template <class X, class O, class C>
+cudaError_t launch_dim(const AppendArgs& a, cudaStream_t st) {
+  switch (a.c.head_dim) {
+    case 64: return launch_d<X, O, C, 8>(a, st);
+    case 128: return launch_d<X, O, C, 16>(a, st);
+    default: return launch_d<X, O, C, 32>(a, st);
   }
 }
 template <class X, class O>
 cudaError_t launch_c(const AppendArgs& a, cudaStream_t st) {
-  return a.c.dtype == KQ_BF16 ? launch_d<X, O, __nv_bfloat16>(a, st) : launch_d<X, O, __nv_fp8_e4m3>(a, st);
+  return a.c.dtype == KQ_BF16 ? launch_dim<X, O, __nv_bfloat16>(a, st) : launch_dim<X, O, __nv_fp8_e4m3>(a, st);
 }
 
 }  // namespace

@@ -18,7 +18,7 @@
 // two vectors of four values that are each other's rotation partners (i and
 // i + rot/2, or adjacent pairs when interleaved), so the rotation needs no
 // exchange between lanes and the norm one shuffle sum over the row's lanes.
-// A CTA works on one token: each group of lanes takes up to four of its heads,
+// A CTA works on one token: each group of lanes takes up to three of its heads,
 // whose loads are all in flight together, and reads the token's cosines and
 // sines once for them.  With few tokens a group takes one head, so that the
 // rows spread over more SMs.
@@ -27,7 +27,8 @@
 namespace kq {
 namespace {
 
-constexpr int ATH = 256;  // threads per CTA
+constexpr int ATH = 128;  // threads per CTA
+constexpr int ROWS = 3;   // rows per group of lanes at a time
 
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
@@ -161,10 +162,10 @@ cudaError_t launch_d(const AppendArgs& a, cudaStream_t st) {
   constexpr int NG = ATH / LG;
   const int H = a.Hq + 2 * a.c.n_kv_heads;
   const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
-  // four heads per group once that still fills the device's eight CTAs per SM
-  const int64_t four = tokens * ((H + 4 * NG - 1) / (4 * NG)), one = tokens * ((H + NG - 1) / NG);
-  if (four >= 8 * num_sms())
-    return launch_pdl(append_kernel<X, O, C, LG, 4>, dim3(static_cast<unsigned>(four)), dim3(ATH), 0, st, a);
+  // several heads per group once that still fills the device (8 CTAs per SM)
+  const int64_t few = tokens * ((H + ROWS * NG - 1) / (ROWS * NG)), one = tokens * ((H + NG - 1) / NG);
+  if (few >= 8 * num_sms())
+    return launch_pdl(append_kernel<X, O, C, LG, ROWS>, dim3(static_cast<unsigned>(few)), dim3(ATH), 0, st, a);
   return launch_pdl(append_kernel<X, O, C, LG, 1>, dim3(static_cast<unsigned>(one)), dim3(ATH), 0, st, a);
 }
 

@@ -59,13 +59,12 @@ struct Smem {
   uint32_t count[BINS], limb[3][BINS];
   unsigned long long list[LIST];
   unsigned long long cand[CAND];
-  unsigned long long few[FEW];
   unsigned long long scan_m[SW], red_m[SW];
-  int scan_c[2 * SW];
+  int scan_c[SW];
   float red_f[SW];
   unsigned long long mass;      // this CTA's sum
   unsigned long long tau;       // its threshold, as the largest sorting key that is listed for sure
-  int ncand, nlist, nfew, done;
+  int ncand, nlist, done;
   float bmax;
   Cmd cmd;
   unsigned long long found_cv, found_before;  // the word at which a running sum passes, and the sum before it
@@ -200,9 +199,57 @@ __device__ __forceinline__ void block_scan(Smem& s, unsigned long long& m, int& 
   m = im;
   c = ic;
 }
-// Sorts s.list[0, n) ascending, n <= LIST.  A warp's 32 threads compare within the same 64 places while the stride is 32
-// or less: only wider steps need the whole block's barrier.
-__device__ __noinline__ void sort_list(Smem& s, int n) {
+// Sorts s.list[0, n) ascending, n <= LIST.  By counting: the words' depths, stretched over the bins, nearly sort them
+// (a few words per bin), and inside a bin each word counts those before it.  Where a bin holds many (equal logits):
+// bitonic, a warp's 32 threads comparing within the same 64 places while the stride is 32 or less, so that only wider
+// steps need the whole block's barrier.  Takes s.cand and s.count as scratch.
+__device__ __noinline__ void sort_list(Smem& s, const Row r, int n) {
+  constexpr int PER = LIST / STH, MANY = 48;
+  unsigned long long cv[PER];
+  float z[PER], deepest = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int j = static_cast<int>(threadIdx.x) + i * STH;
+    cv[i] = j < n ? s.list[j] : ~0ull;
+    z[i] = j < n ? r.depth(logit_of(cv[i])) : 0.0f;
+    deepest = fmaxf(deepest, z[i]);
+  }
+  deepest = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(deepest)));  // not negative
+  if ((threadIdx.x & 31) == 0) s.red_f[threadIdx.x >> 5] = deepest;
+  s.count[2 * threadIdx.x] = s.count[2 * threadIdx.x + 1] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < SW; ++i) deepest = fmaxf(deepest, s.red_f[i]);
+  const float f = deepest > 0.0f ? (BINS - 1) / deepest : 0.0f;
+  int at[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (cv[i] != ~0ull) at[i] = atomicAdd(&s.count[static_cast<int>(fminf(z[i] * f, BINS - 1.0f))], 1);
+  __syncthreads();
+  const int c0 = s.count[2 * threadIdx.x], c1 = s.count[2 * threadIdx.x + 1];
+  if (!__syncthreads_or(max(c0, c1) > MANY)) {
+    unsigned long long none = 0;
+    int before = c0 + c1;
+    block_scan(s, none, before);
+    s.count[2 * threadIdx.x] = before;
+    s.count[2 * threadIdx.x + 1] = before + c0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (cv[i] != ~0ull) s.cand[s.count[static_cast<int>(fminf(z[i] * f, BINS - 1.0f))] + at[i]] = cv[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (cv[i] == ~0ull) continue;
+      const int b = static_cast<int>(fminf(z[i] * f, BINS - 1.0f));
+      const int from = s.count[b], to = b + 1 < BINS ? s.count[b + 1] : n;
+      int place = from;
+      for (int j = from; j < to; ++j) place += s.cand[j] < cv[i];
+      s.list[place] = cv[i];
+    }
+    __syncthreads();
+    return;
+  }
   int size = 64;
   while (size < n) size <<= 1;
   for (int i = n + threadIdx.x; i < size; i += STH) s.list[i] = ~0ull;
@@ -637,7 +684,7 @@ __device__ __noinline__ bool locate(Smem& s, const X* row, int V, int rank, int 
     if (rank != 0) continue;
     if (c.what == kGather) {
       const int n = min(s.nlist, LIST);
-      sort_list(s, n);
+      sort_list(s, r, n);
       pass_at(s, hold(s, r, n), base_m, by_count ? x - base_c : x, by_count);
       if (threadIdx.x == 0) s.cmd.what = kStop;
     } else if (c.what == kCount) {
@@ -652,18 +699,20 @@ __device__ __noinline__ bool locate(Smem& s, const X* row, int V, int rank, int 
   return found;
 }
 
-// The cuts and the choice over the whole row, every CTA of the cluster.
+// The cuts and the choice over the whole row, every CTA of the cluster.  total: the row's weight, 0 if it is not known.
 template <class X>
-__device__ __noinline__ void whole_row(Smem& s, const SampleArgs& a, const X* row, int m, int rank, int CS, const Row r, int k,
-                                       float p, float mp, float u) {
+__device__ __noinline__ void whole_row(Smem& s, const SampleArgs& a, const X* row, int m, int rank, int CS, const Row r,
+                                       unsigned long long total, int k, float p, float mp, float u) {
   const int V = a.V;
   Bins h0;
   bool have = false;
   auto none = [](int, uint4) {};
-  sum_where(s, row, V, rank, CS, r, [](int, float l) { return l > -INFINITY; }, none);
-  cluster_sync();
-  unsigned long long total = cluster_mass(s, CS);  // of the words kept
-  cluster_sync();
+  if (total == 0) {
+    sum_where(s, row, V, rank, CS, r, [](int, float l) { return l > -INFINITY; }, none);
+    cluster_sync();
+    total = cluster_mass(s, CS);
+    cluster_sync();
+  }
   if (k > 0) {
     const bool some_k = locate(s, row, V, rank, CS, r, static_cast<unsigned long long>(k) - 1, true, h0, have);
     have = true;
@@ -717,8 +766,14 @@ __device__ __forceinline__ Row row_of(float lmax, float temp) {
 }
 
 // Rows left to the tail kernel: count, CTAs that have left it, and the rows (null: none are left).
+struct Left {
+  int m;
+  float lmax;
+  unsigned long long total;  // the row's weight; 0: not known yet
+};
 struct Tail {
-  int *count, *left, *rows;
+  int *count, *left;
+  Left* rows;
 };
 
 template <class X>
@@ -811,12 +866,12 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
   cluster_sync();
 
   // ---- the cuts and the choice on the listed words, in the first CTA
-  unsigned long long total = 0;  // weight of the words kept
+  unsigned long long sum = 0;  // the row's weight, where it is known
   if (rank == 0) {
     if (tid == 0) s.nlist = 0;
     unsigned long long tau = lane < CS ? peer64(at_rank(&s.tau, lane)) : ~0ull;
     const int listed = lane < CS ? static_cast<int>(peer32(at_rank(&s.ncand, lane))) : 0;
-    unsigned long long sum = lane < CS && !by_top_k ? peer64(at_rank(&s.mass, lane)) : 0;
+    if (lane < CS && !by_top_k) sum = peer64(at_rank(&s.mass, lane));
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) {
       tau = min(tau, __shfl_xor_sync(0xFFFFFFFFu, tau, o));
@@ -846,63 +901,17 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
         s.done = 1;
       }
     } else if (good) {
-      // first on the few words nearest to the largest: by halving, a depth with 32 to 64 words above it
-      int few = n;
-      const unsigned long long* from_list = s.list;
-      if (n > FEW && k <= FEW) {
-        unsigned long long cv[LIST / STH];
-        float z[LIST / STH];
-#pragma unroll
-        for (int i = 0; i < LIST / STH; ++i) {
-          const int j = tid + i * STH;
-          cv[i] = j < n ? s.list[j] : ~0ull;
-          z[i] = j < n ? r.depth(logit_of(cv[i])) : 4.0f * BINS;
-        }
-        if (tid == 0) s.nfew = 0;
-        float lo = 0.0f, hi = static_cast<float>(BINS);
-#pragma unroll 1
-        for (int step = 0; step < 14; ++step) {
-          const float mid = 0.5f * (lo + hi);
-          int c = 0;
-#pragma unroll
-          for (int i = 0; i < LIST / STH; ++i) c += __popc(__ballot_sync(0xFFFFFFFFu, z[i] <= mid));
-          if (lane == 0) s.scan_c[(step & 1) * SW + warp] = c;
-          __syncthreads();
-          few = __reduce_add_sync(0xFFFFFFFFu, lane < SW ? s.scan_c[(step & 1) * SW + lane] : 0);
-          if (few > FEW) {
-            hi = mid;
-          } else {
-            lo = mid;
-            if (few >= max(k, FEW / 2)) break;
-          }
-        }
-        if (few <= FEW && few >= max(k, 1)) {
-#pragma unroll
-          for (int i = 0; i < LIST / STH; ++i) {
-            const int at = push_at(&s.nfew, z[i] <= lo);
-            if (z[i] <= lo) s.few[at] = cv[i];
-          }
-          from_list = s.few;
-        } else {
-          few = n;
-        }
-        __syncthreads();
-      }
-      total = sum;
-      bool found = false;
-      if (few <= FEW) {
+      unsigned long long total = sum;  // weight of the words kept
+      if (n <= FEW) {
         if (warp == 0) {
           unsigned long long cv = 0, kept = total;
-          found = choose_in_warp(from_list, r, few, complete && few == n, k, p, mp, u, kept, cv);
-          if (found && lane == 0) {
+          if (choose_in_warp(s.list, r, n, complete, k, p, mp, u, kept, cv) && lane == 0) {
             write_row(a, m, r, cv, kept);
             s.done = 1;
           }
         }
-        found = __syncthreads_or(found);
-      }
-      if (!found && n > FEW) {
-        sort_list(s, n);
+      } else {
+        sort_list(s, r, n);
         const Held h = hold(s, r, n);
         if (k > 0) {
           if (pass_at(s, h, 0, static_cast<unsigned long long>(k) - 1, true)) {
@@ -952,10 +961,10 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
   if (done) return;
 
   if (tail.rows) {  // left to the clusters of eight that follow
-    if (rank == 0 && tid == 0) tail.rows[atomicAdd(tail.count, 1)] = m;
+    if (rank == 0 && tid == 0) tail.rows[atomicAdd(tail.count, 1)] = Left{m, r.lmax, sum};
     return;
   }
-  whole_row(s, a, row, m, rank, CS, r, k, p, mp, u);
+  whole_row(s, a, row, m, rank, CS, r, by_top_k ? 0 : cluster_mass(s, CS), k, p, mp, u);
 }
 
 // The rows that sample_kernel left, by clusters of eight CTAs in turn; the last CTA to leave clears the count.
@@ -968,24 +977,13 @@ __global__ void __launch_bounds__(STH, 2) tail_kernel(const __grid_constant__ Sa
   pdl_launch_dependents();
   const int n = __ldcg(tail.count);
   for (int i = blockIdx.x / 8; i < n; i += gridDim.x / 8) {
-    const int m = __ldcg(tail.rows + i);
+    const Left todo = tail.rows[i];
+    const int m = todo.m;
     const X* row = static_cast<const X*>(a.logits) + m * a.row_stride;
     float temp, p, mp, u;
     int k;
     settings(a, m, temp, k, p, mp, u);
-    float mx = -INFINITY;
-    each_chunk<8>(
-        row, a.V, rank, 8, [&](int, uint4 v) { mx = fmaxf(mx, largest(row, v)); }, [&](int, float l) { mx = fmaxf(mx, l); });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    if ((tid & 31) == 0) s.red_f[tid >> 5] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < SW; ++w) mx = fmaxf(mx, s.red_f[w]);
-    if (tid == 0) s.bmax = mx;
-    cluster_sync();
-    for (int q = 0; q < 8; ++q) mx = fmaxf(mx, __uint_as_float(peer32(at_rank(&s.bmax, q))));
-    whole_row(s, a, row, m, rank, 8, row_of(mx, temp), k, p, mp, u);
+    whole_row(s, a, row, m, rank, 8, row_of(todo.lmax, temp), todo.total, k, p, mp, u);
     cluster_sync();
   }
   if (tid == 0) {
@@ -1000,7 +998,7 @@ __global__ void __launch_bounds__(STH, 2) tail_kernel(const __grid_constant__ Sa
 }  // namespace
 
 // The workspace: the tail's counters (zero between calls) and its rows.
-size_t sample_workspace_bytes(int64_t M, int64_t) { return (256 + static_cast<size_t>(M) * sizeof(int) + 255) / 256 * 256; }
+size_t sample_workspace_bytes(int64_t M, int64_t) { return (256 + static_cast<size_t>(M) * sizeof(Left) + 255) / 256 * 256; }
 
 namespace {
 template <class X>
@@ -1041,7 +1039,7 @@ cudaError_t launch_x(const SampleArgs& a, cudaStream_t st) {
   if (second) {
     tail.count = static_cast<int*>(a.ws);
     tail.left = tail.count + 1;
-    tail.rows = tail.count + 64;
+    tail.rows = reinterpret_cast<Left*>(tail.count + 64);
   }
   cudaError_t e = cudaLaunchKernelEx(&cfg, sample_kernel<X>, a, CS, tail);
   if (e == cudaSuccess && second) {

@@ -14,7 +14,7 @@
 // of dependent steps per row (latency).  A row is a cluster of up to 8 CTAs.
 //  * One pass finds each thread's largest logit, and from the threads' largest
 //    ones a threshold with about as many words above it as the row needs
-//    (top_k of them, else 1024 in all).  While the CTAs exchange their largest
+//    (top_k of them, else 512 in all).  While the CTAs exchange their largest
 //    logits each works out its threshold.
 //  * The words above it are listed; a row without top_k sums its total weight
 //    in the same second pass (from L2), others only look again where a thread's
@@ -23,11 +23,11 @@
 //    sorted words.  They are complete above the highest of the CTAs'
 //    thresholds, so what falls inside is final.
 //  * A row whose cut or token falls outside (flat distributions, large top_k)
-//    goes on with histograms over the whole row: counts by the distance to the
-//    largest logit, which bound the running weights and so bracket the bin
-//    that holds the answer; exact weights in 1024 finer bins of the bracket;
-//    where even such a bin has more words than the list, 1024 bins of the next
-//    digits of the words' sorting key at a time, the index being the last.
+//    goes on with a histogram of the whole row: counts and weights in 1024 bins
+//    of the distance to the largest logit.  The words of the bin that holds an
+//    answer are listed and sorted; where a bin has more words than the list,
+//    1024 bins of the next digits of their sorting key at a time, the index
+//    being the last.
 #include "kq_cache.h"
 
 namespace kq {
@@ -38,19 +38,17 @@ constexpr int SW = STH / 32;
 constexpr int CAND = 2048;    // words a CTA lists
 constexpr int LIST = 2048;    // words the first CTA works on
 constexpr int BINS = 1024;    // two per thread
-constexpr int WANT = 1280;    // words to list in all for a row without top_k
+constexpr int WANT = 512;    // words to list in all for a row without top_k
 constexpr int FEW = 64;       // words that one warp decides on
 constexpr int TOPK_FAST = 1024;  // top_k up to here by thresholds
 constexpr float kSpan = 29.0f;  // exp(-29) < 2^-41: words this far below the largest weigh nothing
 constexpr int kIdxBits = 20;
 
 // Which words the cluster looks at next, and what for: from the first CTA to the others.
-enum : int { kCount, kWeigh, kDigits, kGather, kStop };
+enum : int { kAll, kDigits, kGather, kStop };
 struct Cmd {
   int what;
-  int bin_lo, bin_hi;      // level-0 bins of the bracket
-  float fine;              // finer bins per level-0 bin
-  int at;                  // the finer bin (kDigits, kGather)
+  int bin;                 // kDigits, kGather: the bin of all words
   int shift;               // kDigits: by the key's 10 bits above shift; kGather: of the key's digits above shift
   unsigned long long pre;  // those digits
 };
@@ -68,7 +66,7 @@ struct Smem {
   float bmax;
   Cmd cmd;
   unsigned long long found_cv, found_before;  // the word at which a running sum passes, and the sum before it
-  int pick, pick_lo, pick_c, pick_n;
+  int pick, pick_c, pick_n;
   unsigned long long pick_m;
 };
 
@@ -145,7 +143,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 struct Row {
   float lmax, c;  // c = log2(e) / temperature
-  float zs;       // level-0 bins per unit of logit (exp(-1/zs) per bin, whatever the temperature)
+  float zs;       // bins per unit of logit: kSpan over all of them, whatever the temperature
   __device__ __forceinline__ float weight(float l) const { return l == lmax ? 1.0f : ex2((l - lmax) * c); }
   // the weight in units of 2^-40 as 2^20 hi + lo, |lo| <= 2^19 (adding 1.5 * 2^23 rounds to an integer)
   __device__ __forceinline__ void parts(float l, int& hi, int& lo) const {
@@ -159,12 +157,9 @@ struct Row {
     parts(l, hi, lo);
     return static_cast<unsigned long long>((static_cast<long long>(hi) << 20) + lo);
   }
-  // the distance to the largest logit in level-0 bins
+  // the distance to the largest logit in bins
   __device__ __forceinline__ float depth(float l) const { return l == lmax ? 0.0f : fminf((lmax - l) * zs, BINS - 1.0f); }
   __device__ __forceinline__ int bin(float l) const { return static_cast<int>(depth(l)); }
-  __device__ __forceinline__ int fine_bin(float depth, const Cmd& c) const {
-    return static_cast<int>(fminf((depth - c.bin_lo) * c.fine, BINS - 1.0f));
-  }
 };
 
 // ---- block-wide helpers (every thread calls them)
@@ -204,7 +199,7 @@ __device__ __forceinline__ void block_scan(Smem& s, unsigned long long& m, int& 
 // bitonic, a warp's 32 threads comparing within the same 64 places while the stride is 32 or less, so that only wider
 // steps need the whole block's barrier.  Takes s.cand and s.count as scratch.
 __device__ __noinline__ void sort_list(Smem& s, const Row r, int n) {
-  constexpr int PER = LIST / STH, MANY = 48;
+  constexpr int PER = LIST / STH, MANY = 160;
   unsigned long long cv[PER];
   float z[PER], deepest = 0.0f;
 #pragma unroll
@@ -446,7 +441,7 @@ __device__ __forceinline__ void sum_where(Smem& s, const X* row, int V, int rank
     r.parts(l, h, g);
     if (take(i, l)) { hi += h; lo += g; }
   };
-  each_chunk<sizeof(X) == 4 ? 4 : 2>(
+  each_chunk<4>(
       row, V, rank, CS,
       [&](int i, uint4 v) {
         also(i, v);
@@ -493,7 +488,7 @@ __device__ __forceinline__ void add_weight(Smem& s, int d, unsigned long long w)
   if (l2) atomicAdd(&s.limb[2][d], l2);
 }
 // The sum of the cluster's histograms.
-__device__ __forceinline__ Bins read_bins(Smem& s, int CS, bool weights) {
+__device__ __forceinline__ Bins read_bins(Smem& s, int CS) {
   Bins h;
 #pragma unroll
   for (int e = 0; e < 2; ++e) { h.m[e] = 0; h.c[e] = 0; }
@@ -503,10 +498,9 @@ __device__ __forceinline__ Bins read_bins(Smem& s, int CS, bool weights) {
     for (int e = 0; e < 2; ++e) {
       const int b = 2 * threadIdx.x + e;
       h.c[e] += static_cast<int>(peer32(at_rank(&s.count[b], k)));
-      if (weights)
-        h.m[e] += static_cast<unsigned long long>(peer32(at_rank(&s.limb[0][b], k))) +
-                  (static_cast<unsigned long long>(peer32(at_rank(&s.limb[1][b], k))) << 14) +
-                  (static_cast<unsigned long long>(peer32(at_rank(&s.limb[2][b], k))) << 28);
+      h.m[e] += static_cast<unsigned long long>(peer32(at_rank(&s.limb[0][b], k))) +
+                (static_cast<unsigned long long>(peer32(at_rank(&s.limb[1][b], k))) << 14) +
+                (static_cast<unsigned long long>(peer32(at_rank(&s.limb[2][b], k))) << 28);
     }
   h.pm = h.m[0] + h.m[1];
   h.pc = h.c[0] + h.c[1];
@@ -536,40 +530,9 @@ __device__ __forceinline__ void pick_bin(Smem& s, const Bins& h, unsigned long l
   }
   __syncthreads();
 }
-// The bins that can hold the word at which the running weight passes x, from the counts alone: a word of bin b weighs
-// between exp(-(b + 1) d) and exp(-b d), d = kSpan / BINS; the margin covers the rounding of all of it.
-__device__ __forceinline__ void bracket(Smem& s, const Bins& h, unsigned long long x) {
-  unsigned long long up[2], low[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const float b = static_cast<float>(2 * threadIdx.x + e), c = static_cast<float>(h.c[e]) * 1099511627776.0f;
-    constexpr float d = kSpan / BINS * 1.4426950408889634f;
-    up[e] = static_cast<unsigned long long>(ceilf(c * fminf(ex2(-b * d) * 1.0001f, 1.0f))) + h.c[e];
-    low[e] = static_cast<unsigned long long>(c * ex2(-(b + 1.0f) * d) * 0.9999f);
-    low[e] -= low[e] < static_cast<unsigned long long>(h.c[e]) ? low[e] : h.c[e];  // units are rounded, too
-    if (2 * threadIdx.x + e == BINS - 1) low[e] = 0;  // also what lies deeper
-  }
-  unsigned long long pu = up[0] + up[1], pl = low[0] + low[1];
-  int none = 0;
-  block_scan(s, pu, none);
-  block_scan(s, pl, none);
-  __syncthreads();
-  if (threadIdx.x == 0) { s.pick_lo = BINS - 1; s.pick = BINS - 1; }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int b = 2 * threadIdx.x + e;
-    if (pu <= x && x < pu + up[e]) s.pick_lo = b;
-    if (pl <= x && x < pl + low[e]) s.pick = b;
-    pu += up[e];
-    pl += low[e];
-  }
-  __syncthreads();
-}
-
 // Over the whole row, every CTA of the cluster: the word at which the running sum of weights (by_count: of words that
 // weigh anything) passes x; found_cv and, by weight, found_before in the first CTA, false there when there is none.  h0:
-// the row's counts by level-0 bin, made by the first call (have = false).
+// the histogram of all words, made by the first call (have = false).
 template <class X>
 __device__ __noinline__ bool locate(Smem& s, const X* row, int V, int rank, int CS, const Row& r_in, unsigned long long x,
                                     bool by_count, Bins& h0, bool have) {
@@ -578,103 +541,63 @@ __device__ __noinline__ bool locate(Smem& s, const X* row, int V, int rank, int 
   unsigned long long base_m = 0;
   int base_c = 0;
   bool found = true;
-  auto start = [&] {  // the counts are known: the bracket, or the bin itself
-    if (by_count) {
-      pick_bin(s, h0, 0, 0, x, true);
-      found = s.pick >= 0;
-      if (found) base_c = s.pick_c;
-      if (threadIdx.x == 0) s.pick_lo = s.pick;
-      __syncthreads();
-    } else {
-      bracket(s, h0, x);
-    }
-    if (threadIdx.x == 0) {
-      s.cmd.bin_lo = s.pick_lo;
-      s.cmd.bin_hi = s.pick;
-      s.cmd.fine = static_cast<float>(BINS) / static_cast<float>(s.pick - s.pick_lo + 1);
-      s.cmd.what = found ? kWeigh : kStop;
-    }
-    __syncthreads();
-  };
-  auto narrow = [&](const Bins& h, int shift, unsigned long long pre, bool digits) {
+  auto narrow = [&](const Bins& h, int what, int shift, unsigned long long pre) {
     pick_bin(s, h, base_m, base_c, x, by_count);
     found = s.pick >= 0;
     if (found) { base_m = s.pick_m; base_c = s.pick_c; }
     if (threadIdx.x == 0) {
       const bool fits = s.pick_n <= LIST;
-      if (digits)
+      if (what == kAll) {
+        s.cmd.bin = s.pick;
+        s.cmd.shift = fits ? 64 : 42;
+      } else {
         s.cmd.pre = (shift + 10 < 52 ? pre >> (shift + 10) << (shift + 10) : 0) | (static_cast<unsigned long long>(s.pick) << shift);
-      else
-        s.cmd.at = s.pick;
-      s.cmd.shift = digits ? (fits ? shift : shift - 10) : (fits ? 64 : 42);
+        s.cmd.shift = fits ? shift : shift - 10;
+      }
       s.cmd.what = !found ? kStop : fits ? kGather : kDigits;
     }
     __syncthreads();
   };
   if (rank == 0) {
-    if (threadIdx.x == 0) s.cmd.what = kCount;
-    if (have) start();
+    if (have) narrow(h0, kAll, 0, 0);
+    else if (threadIdx.x == 0) s.cmd.what = kAll;
   }
   for (;;) {
     if (threadIdx.x == 0) s.nlist = 0;
     cluster_sync();  // the command is written, the first CTA's list is empty, and it is done with the histograms
-    Cmd c;
-    c.what = static_cast<int>(peer32(at_rank(&s.cmd.what, 0)));
-    c.bin_lo = static_cast<int>(peer32(at_rank(&s.cmd.bin_lo, 0)));
-    c.bin_hi = static_cast<int>(peer32(at_rank(&s.cmd.bin_hi, 0)));
-    c.fine = __uint_as_float(peer32(at_rank(&s.cmd.fine, 0)));
-    c.at = static_cast<int>(peer32(at_rank(&s.cmd.at, 0)));
-    c.shift = static_cast<int>(peer32(at_rank(&s.cmd.shift, 0)));
-    c.pre = peer64(at_rank(&s.cmd.pre, 0));
-    if (c.what == kStop) {
+    const int what = static_cast<int>(peer32(at_rank(&s.cmd.what, 0))), bin = static_cast<int>(peer32(at_rank(&s.cmd.bin, 0)));
+    const int shift = static_cast<int>(peer32(at_rank(&s.cmd.shift, 0)));
+    const unsigned long long pre = peer64(at_rank(&s.cmd.pre, 0));
+    if (what == kStop) {
       cluster_sync();  // every CTA has read the command
       break;
     }
-    for (int i = threadIdx.x; i < BINS; i += STH) { s.count[i] = 0; s.limb[0][i] = 0; s.limb[1][i] = 0; s.limb[2][i] = 0; }
-    __syncthreads();
-    if (c.what == kCount) {
+    if (what != kGather) {
+      for (int i = threadIdx.x; i < BINS; i += STH) { s.count[i] = 0; s.limb[0][i] = 0; s.limb[1][i] = 0; s.limb[2][i] = 0; }
+      __syncthreads();
+    }
+    if (what == kAll) {
       each_word<UL>(row, V, rank, CS, [&](int, float l) {
         int h, g;
         r.parts(l, h, g);
-        if (l > -INFINITY && (h | g)) atomicAdd(&s.count[r.bin(l)], 1u);
+        if (!(l > -INFINITY) || !(h | g)) return;
+        const int d = r.bin(l);
+        atomicAdd(&s.count[d], 1u);
+        add_weight(s, d, static_cast<unsigned long long>((static_cast<long long>(h) << 20) + g));
       });
-    } else if (c.what == kWeigh) {
-      uint32_t hi = 0;
-      int lo = 0;
-      each_word<UL>(row, V, rank, CS, [&](int, float l) {
-        if (!(l > -INFINITY)) return;
-        const float z = r.depth(l);
-        const int b = static_cast<int>(z);
-        if (b > c.bin_hi) return;
-        int h, g;
-        r.parts(l, h, g);
-        if (b < c.bin_lo) {
-          hi += h;
-          lo += g;
-        } else if (h | g) {
-          const int d = r.fine_bin(z, c);
-          atomicAdd(&s.count[d], 1u);
-          add_weight(s, d, static_cast<unsigned long long>((static_cast<long long>(h) << 20) + g));
-        }
-      });
-      const unsigned long long t = block_sum(s, static_cast<unsigned long long>((static_cast<long long>(hi) << 20) + lo));
-      if (threadIdx.x == 0) s.mass = t;
     } else {
       const uint32_t list0 = at_rank(s.list, 0), nlist0 = at_rank(&s.nlist, 0);
       each_word<UL>(row, V, rank, CS, [&](int i, float l) {
-        if (!(l > -INFINITY)) return;
-        const float z = r.depth(l);
-        const int b = static_cast<int>(z);
-        if (b < c.bin_lo || b > c.bin_hi || r.fine_bin(z, c) != c.at) return;
+        if (!(l > -INFINITY) || r.bin(l) != bin) return;
         const unsigned long long cv = sort_key(l, i), w = r.units(l);
         if (w == 0) return;
-        if (c.what == kGather) {
-          if (c.shift < 64 && (cv >> c.shift) != (c.pre >> c.shift)) return;
+        if (what == kGather) {
+          if (shift < 64 && (cv >> shift) != (pre >> shift)) return;
           const int at = peer_add(nlist0, 1);
           if (at < LIST) peer_store64(list0 + 8 * at, cv);
         } else {
-          if (c.shift + 10 < 52 && (cv >> (c.shift + 10)) != (c.pre >> (c.shift + 10))) return;
-          const int d = static_cast<int>(cv >> c.shift) & (BINS - 1);
+          if (shift + 10 < 52 && (cv >> (shift + 10)) != (pre >> (shift + 10))) return;
+          const int d = static_cast<int>(cv >> shift) & (BINS - 1);
           atomicAdd(&s.count[d], 1u);
           add_weight(s, d, w);
         }
@@ -682,17 +605,15 @@ __device__ __noinline__ bool locate(Smem& s, const X* row, int V, int rank, int 
     }
     cluster_sync();
     if (rank != 0) continue;
-    if (c.what == kGather) {
+    if (what == kGather) {
       const int n = min(s.nlist, LIST);
       sort_list(s, r, n);
       pass_at(s, hold(s, r, n), base_m, by_count ? x - base_c : x, by_count);
       if (threadIdx.x == 0) s.cmd.what = kStop;
-    } else if (c.what == kCount) {
-      h0 = read_bins(s, CS, false);
-      start();
     } else {
-      if (c.what == kWeigh && !by_count) base_m = cluster_mass(s, CS);
-      narrow(read_bins(s, CS, true), c.shift, c.pre, c.what == kDigits);
+      const Bins h = read_bins(s, CS);
+      if (what == kAll) h0 = h;
+      narrow(h, what, shift, pre);
     }
     __syncthreads();
   }
@@ -1012,11 +933,11 @@ cudaError_t launch_x(const SampleArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set = true;
   }
-  // CTAs per row: as many as fill the device (a row in fewer, larger shares once the rows do), with at least 4096 words
+  // CTAs per row: as many as the device holds at once, two per SM, with at least 4096 words
   // each, and at most 2^18, the histograms' room.
   const int sms = num_sms();
   int CS = 1;
-  while (CS < 8 && static_cast<int64_t>(a.M) * CS * 2 <= 4 * sms && a.V / (CS * 2) >= 4096) CS *= 2;
+  while (CS < 8 && static_cast<int64_t>(a.M) * CS * 2 <= 2 * sms && a.V / (CS * 2) >= 4096) CS *= 2;
   while (CS < 8 && a.V / CS > (1 << 18)) CS *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.M) * CS);

@@ -34,7 +34,10 @@
 // weights 2^(..) as two parts (2^-17) for bf16 q and three for fp32 q.  e4m3
 // cache: its values are fp16 values, so fp16 instructions serve; q is scaled
 // by a power of two per row into fp16's range (bf16: one part; fp32: two, 22
-// bits), weights are two parts.  Accumulation is fp32.
+// bits), weights are two parts.  Accumulation is fp32; the matrix instructions
+// cut what they add to an accumulator instead of rounding it, which over the
+// hundreds of steps of a long range grows to 2^-16, so with fp32 q each step's
+// product is added by rounding fp32 additions.
 //
 // Values that no row sees are never loaded (zeros take their place).  One that
 // some rows of the block see and others do not would reach the others as
@@ -261,20 +264,27 @@ struct Warp {
         ldsm4(ka[1], kaddr + k2 * 64 + 32);
       }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float(&acc)[4] = K::QF32 ? part : s[n];
 #pragma unroll
         for (int t = 0; t < K::NQ; ++t) {
           if constexpr (K::QREG) {
             const uint32_t(&b)[4] = qreg[(n * K::NQ + t) * (D / 32) + k2];
-            mma<K::F8>(s[n], ka[0], b[0], b[1]);
-            mma<K::F8>(s[n], ka[1], b[2], b[3]);
+            mma<K::F8>(acc, ka[0], b[0], b[1]);
+            mma<K::F8>(acc, ka[1], b[2], b[3]);
           } else {
             uint32_t b[4];
             load_q4(b, qaddr, t, n, k2, lane);
-            mma<K::F8>(s[n], ka[0], b[0], b[1]);
-            mma<K::F8>(s[n], ka[1], b[2], b[3]);
+            mma<K::F8>(acc, ka[0], b[0], b[1]);
+            mma<K::F8>(acc, ka[1], b[2], b[3]);
           }
         }
+        if constexpr (K::QF32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] += part[e];
+        }
+      }
     }
     // ---- weights
     const int j0 = base + (lane >> 2);
@@ -351,9 +361,7 @@ struct Warp {
           const uint32_t b0 = __byte_perm(r[2 * h], 0, 0x3120), b1 = __byte_perm(r[2 * h + 1], 0, 0x3120);
           const uint32_t va[4] = {f8_pair(b0), f8_pair(b0 >> 16), f8_pair(b1), f8_pair(b1 >> 16)};  // even dims, odd dims
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int t = 0; t < K::NP; ++t) mma<true>(o[n][2 * d2 + h], va, w[n][t][0], w[n][t][1]);
+          for (int n = 0; n < NT; ++n) add_product(o[n][2 * d2 + h], va, w[n]);
         }
       }
     } else {
@@ -363,10 +371,21 @@ struct Warp {
         uint32_t va[4];
         ldsm4t(va, vaddr + d * 32);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int t = 0; t < K::NP; ++t) mma<false>(o[n][d], va, w[n][t][0], w[n][t][1]);
+        for (int n = 0; n < NT; ++n) add_product(o[n][d], va, w[n]);
       }
+    }
+  }
+
+  static __device__ __forceinline__ void add_product(float (&o)[4], const uint32_t (&va)[4], const uint32_t (&w)[K::NP][2]) {
+    if constexpr (K::QF32) {
+      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int t = 0; t < K::NP; ++t) mma<K::F8>(part, va, w[t][0], w[t][1]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += part[e];
+    } else {
+#pragma unroll
+      for (int t = 0; t < K::NP; ++t) mma<K::F8>(o, va, w[t][0], w[t][1]);
     }
   }
 

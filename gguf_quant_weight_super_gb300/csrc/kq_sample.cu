@@ -732,7 +732,8 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
   Row r = row_of(mx, temp);
   // with n words above the threshold spread over the threads at random, 1 - exp(-n / threads) of them have one
   const float per = static_cast<float>(by_top_k ? k + k / 4 + 32 : WANT) / static_cast<float>(CS);
-  const int want = max(8, static_cast<int>(STH * (1.0f - __expf(-fminf(per, 1200.0f) / STH))));
+  // (the CTA with the highest threshold has at least `want` words above it: small top_k are met for certain)
+  const int want = max(by_top_k ? min(k, 128) : 8, static_cast<int>(STH * (1.0f - __expf(-fminf(per, 1200.0f) / STH))));
   const bool some = mine > -INFINITY && (mine == mx || (mx - mine) * r.zs < static_cast<float>(BINS));
   const int bin = some ? r.bin(mine) : BINS;
   if (some) atomicAdd(&s.count[bin], 1u);

@@ -491,39 +491,36 @@ def kq_sample(logits, dtype, row_stride, M, V, u, temperature, top_k, top_p, min
                                         workspace_bytes, _stream(stream)))
 
 
-# The calls below are made once per layer and token, where a Python call's own time counts: each tensor is looked at once.
+# The calls below are made once per layer and token, where a Python call's own time counts: each property of a tensor is
+# looked up once, in line.
 
 _DTYPE_CODE = {torch.float32: KQ_F32, torch.bfloat16: KQ_BF16}
+_f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
+
+
+def _row_stride(name: str, x: torch.Tensor, B: int, T: int, heads: int, D: int) -> int:
+    """The row stride of x [B, T, heads, D]: heads contiguous, rows at one stride."""
+    s0, s1, s2, s3 = x.stride()
+    if s3 != 1 or (s2 != D and heads > 1) or (s0 != T * s1 and B > 1 and T > 1):
+        raise ValueError(f"{name}: heads contiguous, tokens at one stride")
+    return s1 if T > 1 else s0 if B > 1 else heads * D
 
 
 def _rows(name: str, x: torch.Tensor, B: int, T: int, D: int):
-    """The heads and the row stride of x [B, T, heads, D]: heads contiguous, rows at one stride."""
+    """The heads and the row stride of x [B, T, heads, D]."""
     shape = x.shape
     if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != D:
         raise ValueError(f"{name}: [{B}, {T}, heads, {D}], not {list(shape)}")
-    s0, s1, s2, s3 = x.stride()
-    heads = shape[2]
-    if s3 != 1 or (s2 != D and heads > 1) or (s0 != T * s1 and B > 1 and T > 1):
-        raise ValueError(f"{name}: heads contiguous, tokens at one stride")
-    return heads, (s1 if T > 1 else s0 if B > 1 else heads * D)
+    return shape[2], _row_stride(name, x, B, T, shape[2], D)
 
 
-def _vector(name: str, t: torch.Tensor, dtype, shape) -> int:
-    """The address of a contiguous device tensor of the given type and shape."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous {dtype} {list(shape)}")
-    if not t.is_cuda:
-        raise ValueError("libkq takes device tensors only")
-    return t.data_ptr()
+def _host():
+    return ValueError("libkq takes device tensors only")
 
 
-def _floats(x: torch.Tensor) -> int:
-    code = _DTYPE_CODE.get(x.dtype)
-    if code is None:
-        raise TypeError("float32 or bfloat16")
-    if not x.is_cuda:
-        raise ValueError("libkq takes device tensors only")
-    return code
+def _here():
+    """The current device's current stream (a device tensor is at hand, so CUDA is up)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def kv_append(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -531,23 +528,35 @@ def kv_append(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, 
               stream=None) -> torch.Tensor:
     """kq_kv_append for q [B, T, n_q_heads, head_dim], k and v [B, T, n_kv_heads, head_dim] (views of one fused buffer
     will do), page_table [B, max_pages] and seq_lens [B] int32; returns q_out."""
-    B, T = q.shape[:2]
-    D, heads = cache.head_dim, cache.n_kv_heads
-    (Hq, qs), (Hk, ks), (Hv, vs) = _rows("q", q, B, T, D), _rows("k", k, B, T, D), _rows("v", v, B, T, D)
-    x_dtype = _floats(q)
-    if Hk != heads or Hv != heads or _floats(k) != x_dtype or _floats(v) != x_dtype:
-        raise ValueError("k and v: the cache's heads, of q's type")
-    if rope.norm_dim not in (0, D):
+    shape, kv_shape, D, heads, dtype = q.shape, k.shape, cache.head_dim, cache.n_kv_heads, q.dtype
+    if len(shape) != 4 or shape[3] != D:
+        raise ValueError(f"q: [B, T, heads, {D}], not {list(shape)}")
+    B, T, Hq, _ = shape
+    if kv_shape != (B, T, heads, D) or v.shape != kv_shape or k.dtype is not dtype or v.dtype is not dtype:
+        raise ValueError(f"k and v: [{B}, {T}, {heads}, {D}], of q's type")
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
+        raise TypeError("q, k and v are float32 or bfloat16")
+    if rope.norm_dim != 0 and rope.norm_dim != D:
         raise ValueError("norm weights: [head_dim]")
-    W = page_table.shape[-1]
     if q_out is None:
-        q_out = torch.empty((B, T, Hq, D), dtype=q_out_dtype, device=q.device)
-    elif q_out.shape != q.shape or not q_out.is_contiguous():
+        q_out = torch.empty(shape, dtype=q_out_dtype, device=q.device)
+    elif q_out.shape != shape or not q_out.is_contiguous():
         raise ValueError("q_out: contiguous, of q's shape")
-    status = lib().kq_kv_append(cache._ref, _vector("page_table", page_table, torch.int32, (B, W)), W,
-                                _vector("seq_lens", seq_lens, torch.int32, (B,)), B, T, q.data_ptr(), k.data_ptr(),
-                                v.data_ptr(), x_dtype, qs, ks, vs, Hq, rope._ref, q_out.data_ptr(), _floats(q_out),
-                                _stream(stream))
+    out_code = _DTYPE_CODE.get(q_out.dtype)
+    if out_code is None:
+        raise TypeError("q_out is float32 or bfloat16")
+    W = page_table.shape[-1]
+    if page_table.dtype is not _i32 or page_table.shape != (B, W) or not page_table.is_contiguous():
+        raise ValueError(f"page_table: contiguous int32 [{B}, max_pages]")
+    if seq_lens.dtype is not _i32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
+        raise ValueError(f"seq_lens: contiguous int32 [{B}]")
+    if not (q.is_cuda and k.is_cuda and v.is_cuda and q_out.is_cuda and page_table.is_cuda and seq_lens.is_cuda):
+        raise _host()
+    status = (_lib or lib()).kq_kv_append(
+        cache._ref, page_table.data_ptr(), W, seq_lens.data_ptr(), B, T, q.data_ptr(), k.data_ptr(), v.data_ptr(), code,
+        _row_stride("q", q, B, T, Hq, D), _row_stride("k", k, B, T, heads, D), _row_stride("v", v, B, T, heads, D), Hq,
+        rope._ref, q_out.data_ptr(), out_code, _here() if stream is None else _stream(stream))
     if status:
         raise KQError("kq_kv_append", status)
     return q_out
@@ -565,18 +574,30 @@ def attn_decode(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor
                 workspace: torch.Tensor, scale: float | None = None, softcap: float = 0.0, window: int = 0,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """kq_attn_decode for q [B, T, n_q_heads, head_dim]; scale None: head_dim^-0.5.  Returns out, of q's type."""
-    B, T = q.shape[:2]
-    D = cache.head_dim
-    Hq, qs = _rows("q", q, B, T, D)
-    W = page_table.shape[-1]
+    shape, D, dtype = q.shape, cache.head_dim, q.dtype
+    if len(shape) != 4 or shape[3] != D:
+        raise ValueError(f"q: [B, T, heads, {D}], not {list(shape)}")
+    B, T, Hq, _ = shape
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
+        raise TypeError("q is float32 or bfloat16")
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device)
-    status = lib().kq_attn_decode(cache._ref, _vector("page_table", page_table, torch.int32, (B, W)), W,
-                                  _vector("seq_lens", seq_lens, torch.int32, (B,)), B, T, q.data_ptr(), _floats(q), qs, Hq,
-                                  D ** -0.5 if scale is None else scale, softcap, window,
-                                  _vector("out", out, q.dtype, q.shape),
-                                  _vector("workspace", workspace, torch.uint8, workspace.shape), workspace.numel(),
-                                  _stream(stream))
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
+        raise ValueError("out: contiguous, of q's shape and type")
+    W = page_table.shape[-1]
+    if page_table.dtype is not _i32 or page_table.shape != (B, W) or not page_table.is_contiguous():
+        raise ValueError(f"page_table: contiguous int32 [{B}, max_pages]")
+    if seq_lens.dtype is not _i32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
+        raise ValueError(f"seq_lens: contiguous int32 [{B}]")
+    if workspace.dtype is not _u8 or not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous uint8")
+    if not (q.is_cuda and out.is_cuda and page_table.is_cuda and seq_lens.is_cuda and workspace.is_cuda):
+        raise _host()
+    status = (_lib or lib()).kq_attn_decode(
+        cache._ref, page_table.data_ptr(), W, seq_lens.data_ptr(), B, T, q.data_ptr(), code,
+        _row_stride("q", q, B, T, Hq, D), Hq, D ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _here() if stream is None else _stream(stream))
     if status:
         raise KQError("kq_attn_decode", status)
     return out
@@ -597,24 +618,34 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     shape = logits.shape
     M, V = shape
     row = shape[:1]
-    f32, i32 = torch.float32, torch.int32
+    code = _DTYPE_CODE.get(logits.dtype)
+    if code is None:
+        raise TypeError("logits are float32 or bfloat16")
     stride, one = logits.stride()
     if one != 1 and V > 1:
         raise ValueError("logits: each row contiguous")
-    if ids is None:
-        ids = torch.empty(M, dtype=i32, device=logits.device)
-    if probs is None:
-        probs = torch.empty(M, dtype=f32, device=logits.device)
     if workspace is None:
         workspace = sample_workspace(M, V, logits.device)
-    status = lib().kq_sample(logits.data_ptr(), _floats(logits), stride, M, V, _vector("u", u, f32, row),
-                             None if temperature is None else _vector("temperature", temperature, f32, row),
-                             None if top_k is None else _vector("top_k", top_k, i32, row),
-                             None if top_p is None else _vector("top_p", top_p, f32, row),
-                             None if min_p is None else _vector("min_p", min_p, f32, row),
-                             _vector("ids", ids, i32, row), _vector("probs", probs, f32, row),
-                             _vector("workspace", workspace, torch.uint8, workspace.shape), workspace.numel(),
-                             _stream(stream))
+    elif workspace.dtype is not _u8 or not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous uint8")
+    if ids is None:
+        ids = torch.empty(M, dtype=_i32, device=logits.device)
+    if probs is None:
+        probs = torch.empty(M, dtype=_f32, device=logits.device)
+    cuda = logits.is_cuda and workspace.is_cuda
+    at = []
+    for t, dtype in ((u, _f32), (temperature, _f32), (top_k, _i32), (top_p, _f32), (min_p, _f32), (ids, _i32), (probs, _f32)):
+        if t is None:
+            at.append(None)
+            continue
+        if t.dtype is not dtype or t.shape != row or not t.is_contiguous():
+            raise ValueError(f"u, temperature, top_p, min_p, probs: contiguous float32 [{M}]; top_k, ids: int32")
+        cuda = cuda and t.is_cuda
+        at.append(t.data_ptr())
+    if not cuda:
+        raise _host()
+    status = (_lib or lib()).kq_sample(logits.data_ptr(), code, stride, M, V, *at, workspace.data_ptr(), workspace.numel(),
+                                       _here() if stream is None else _stream(stream))
     if status:
         raise KQError("kq_sample", status)
     return ids, probs

@@ -496,3 +496,16 @@ def test_attn_one_head_over_every_range(T, G, dtype):
     """One head's long cache: all the device's CTAs, and the left-over ranges, hold a part of the same item."""
     P = Paged([150001], 1, 64, 64, dtype, seed=29)
     check_attn(P, rand_q(1, T, G, 64, BF16, 30))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F8])
+def test_attn_fp32_long_sums_keep_their_digits(dtype):
+    """Values of one sign over a long cache: every step adds to the same sum.  fp32 q and out keep 2^-19 (the weights'
+    parts 2^-20, a few rounded additions per step of sums that are joined from short ones)."""
+    P = Paged([40000], 1, 64, 64, dtype, seed=31)
+    P.v.copy_((P.v.float().nan_to_num(0.0).abs() + 0.5).to(dtype))
+    q = rand_q(1, 1, 2, 64, F32, 32, mul=0.5)
+    out = kq.attn_decode(P.cache, P.table, P.seq_lens, q, kq.attn_workspace(P.cache, 1, 1, 2))
+    torch.cuda.synchronize()
+    ref, _, _ = attn_ref(P, q, 64 ** -0.5, 0.0, 0)
+    assert np.max(np.abs(f64(out) / ref - 1)) <= 2.0 ** -19

@@ -18,10 +18,9 @@
 // two vectors of four values that are each other's rotation partners (i and
 // i + rot/2, or adjacent pairs when interleaved), so the rotation needs no
 // exchange between lanes and the norm one shuffle sum over the row's lanes.
-// A CTA works on one token: each group of lanes takes up to three of its heads,
-// whose loads are all in flight together, and reads the token's cosines and
-// sines once for them.  With few tokens a group takes one head, so that the
-// rows spread over more SMs.
+// Each group of lanes takes three heads of a token, whose loads are all in
+// flight together, and reads the token's cosines and sines once for them.  With
+// few tokens a group takes one head, so that the rows spread over more SMs.
 #include "kq_cache.h"
 
 namespace kq {
@@ -62,9 +61,10 @@ __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ App
   pdl_wait();
   pdl_launch_dependents();
   const int Hkv = a.c.n_kv_heads, H = a.Hq + 2 * Hkv;
-  const uint32_t per = (H + NG * U - 1) / (NG * U);  // CTAs per token
-  const uint32_t tok = blockIdx.x / per;
-  const int h0 = static_cast<int>(blockIdx.x - tok * per) * (NG * U) + static_cast<int>(threadIdx.x) / LG;
+  const uint32_t per = (H + U - 1) / U;  // groups per token
+  const uint32_t grp = blockIdx.x * NG + threadIdx.x / LG, all = static_cast<uint32_t>(a.B) * a.T * per;
+  const uint32_t tok = min(grp, all - 1) / per;  // groups past the last: its token, no head
+  const int h0 = grp < all ? static_cast<int>(grp - tok * per) * U : H;
   const int b = tok / a.T, t = tok - b * a.T;
   const int l = threadIdx.x % LG;
   const int rot = a.rope.rot_dim, rl = rot / 8;
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ App
   float4 x0[U], x1[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int h = h0 + i * NG;
+    const int h = h0 + i;
     x0[i] = x1[i] = make_float4(0, 0, 0, 0);
     if (h < H) {
       const X* src = h < a.Hq ? static_cast<const X*>(a.q) + tok * a.q_stride + static_cast<int64_t>(h) * D
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ App
   const int pos = __ldg(a.seq_lens + b) - a.T + t;
   bool ok = pos >= 0;
   if (ok && rot > 0 && pos >= a.rope.n_positions) {
-    if (threadIdx.x == 0) record_error(a.err, DEV_ERR_POSITION);
+    if (l == 0) record_error(a.err, DEV_ERR_POSITION);
     ok = false;
   }
   int page = -1;
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ App
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int h = h0 + i * NG;
+    const int h = h0 + i;
     const bool isq = h < a.Hq, isk = !isq && h < a.Hq + Hkv;
     const float* nw = isq ? a.rope.q_norm : isk ? a.rope.k_norm : nullptr;
     float ss = sq4(x0[i]) + sq4(x1[i]);
@@ -163,7 +163,7 @@ cudaError_t launch_d(const AppendArgs& a, cudaStream_t st) {
   const int H = a.Hq + 2 * a.c.n_kv_heads;
   const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
   // several heads per group once that still fills the device (8 CTAs per SM)
-  const int64_t few = tokens * ((H + ROWS * NG - 1) / (ROWS * NG)), one = tokens * ((H + NG - 1) / NG);
+  const int64_t few = (tokens * ((H + ROWS - 1) / ROWS) + NG - 1) / NG, one = (tokens * H + NG - 1) / NG;
   if (few >= 8 * num_sms())
     return launch_pdl(append_kernel<X, O, C, LG, ROWS>, dim3(static_cast<unsigned>(few)), dim3(ATH), 0, st, a);
   return launch_pdl(append_kernel<X, O, C, LG, 1>, dim3(static_cast<unsigned>(one)), dim3(ATH), 0, st, a);

@@ -183,18 +183,23 @@ struct Warp {
   static __device__ __forceinline__ void issue(const Params& p, const Seg& g, uint32_t stage, int base, int page, int lane) {
     const AttnArgs& a = p.a;
     constexpr int CH = D * static_cast<int>(sizeof(C)) / 16;  // 16-byte chunks per row
-    if (base >= g.first && base + WT <= g.len && a.c.page_size >= WT && static_cast<unsigned>(page) < a.c.n_pages) {
-      // 16 whole rows of one page, at one stride
+    if (base >= g.first && base + WT <= g.len && a.c.page_size >= WT / 2 &&
+        __all_sync(0xFFFFFFFFu, static_cast<unsigned>(page) < a.c.n_pages)) {
+      // two times eight whole rows of one page, at one stride
       const int64_t row = a.c.slot_stride * static_cast<int64_t>(sizeof(C));
-      int64_t src = (page * a.c.page_stride + g.head_off) * static_cast<int64_t>(sizeof(C)) +
-                    ((base & (a.c.page_size - 1)) + lane / CH) * row + lane % CH * 16;
       uint32_t dst = stage + lane / CH * K::RB + lane % CH * 16;
 #pragma unroll
-      for (int i = 0; i < CH / 2; ++i) {
-        copy16(dst, static_cast<const uint8_t*>(a.c.k) + src, true);
-        copy16(dst + K::SUB, static_cast<const uint8_t*>(a.c.v) + src, true);
-        src += 32 / CH * row;
-        dst += 32 / CH * K::RB;
+      for (int h = 0; h < 2; ++h) {
+        const int pg = __shfl_sync(0xFFFFFFFFu, page, 8 * h);
+        int64_t src = (pg * a.c.page_stride + g.head_off) * static_cast<int64_t>(sizeof(C)) +
+                      (((base + 8 * h) & (a.c.page_size - 1)) + lane / CH) * row + lane % CH * 16;
+#pragma unroll
+        for (int i = 0; i < CH / 4; ++i) {
+          copy16(dst, static_cast<const uint8_t*>(a.c.k) + src, true);
+          copy16(dst + K::SUB, static_cast<const uint8_t*>(a.c.v) + src, true);
+          src += 32 / CH * row;
+          dst += 32 / CH * K::RB;
+        }
       }
     } else {
       issue_rows(p, g, stage, base, page, lane);
@@ -573,6 +578,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
   using K = Cfg<Q, C, D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_scan[NW];
+  __shared__ __align__(16) float s_sum[NW * 2 * 32 * 4];
   __shared__ int s_last;
   float* rscale = reinterpret_cast<float*>(smem);  // [ROWS]
   float* s_i = rscale + K::ROWS;                   // [ROWS] the join's 1 / weight sum
@@ -767,24 +773,43 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
             if (lane == 0) s_i[r] = ll == 0.0f ? 0.0f : a.c.v_scale / ll;
           }
           __syncthreads();
-          constexpr int XU = 2;  // vectors at a time per thread, of four parts: their loads are in flight together
-          for (int x0 = threadIdx.x; x0 < rows * (D / 4); x0 += XU * NTH) {
+          // Vectors of the rows, XU at a time per lane, over the parts, four in flight.  Few parts: every warp takes all of
+          // them for its vectors; many: each warp a quarter of them for all vectors, joined in shared memory.
+          constexpr int XU = 2;
+          const int vecs = rows * (D / 4), groups = parts > 8 ? NW : 1, warps = NW / groups;
+          float4* sum = reinterpret_cast<float4*>(s_sum);
+          for (int x1 = 0; x1 < vecs; x1 += warps * 32 * XU) {
+            const int x0 = x1 + (groups == 1 ? warp * 32 : 0) + lane;
             float4 acc[XU];
 #pragma unroll
             for (int i = 0; i < XU; ++i) acc[i] = make_float4(0, 0, 0, 0);
 #pragma unroll 4
-            for (int k = 0; k < parts; ++k) {
+            for (int k = groups == 1 ? 0 : warp; k < parts; k += groups) {
               const float4* part = reinterpret_cast<const float4*>(p.part + (static_cast<int64_t>(slot_of(k)) * K::ROWS + rb) * D);
 #pragma unroll
               for (int i = 0; i < XU; ++i) {
-                const int x = x0 + i * NTH;
-                if (x < rows * (D / 4)) add4(acc[i], factor[k * rows + x / (D / 4)], __ldcg(part + x));
+                const int x = x0 + i * warps * 32;
+                if (x < vecs) add4(acc[i], factor[k * rows + x / (D / 4)], __ldcg(part + x));
               }
             }
+            if (groups > 1) {
 #pragma unroll
-            for (int i = 0; i < XU; ++i) {
-              const int x = x0 + i * NTH;
-              if (x < rows * (D / 4)) write(rb + x / (D / 4), 4 * (x % (D / 4)), acc[i], s_i[x / (D / 4)]);
+              for (int i = 0; i < XU; ++i) sum[(warp * XU + i) * 32 + lane] = acc[i];
+              __syncthreads();
+              if (warp < XU) {
+                acc[0] = sum[warp * 32 + lane];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) add4(acc[0], 1.0f, sum[(w * XU + warp) * 32 + lane]);
+                const int x = x0 + warp * 32;
+                if (x < vecs) write(rb + x / (D / 4), 4 * (x % (D / 4)), acc[0], s_i[x / (D / 4)]);
+              }
+              __syncthreads();
+            } else {
+#pragma unroll
+              for (int i = 0; i < XU; ++i) {
+                const int x = x0 + i * warps * 32;
+                if (x < vecs) write(rb + x / (D / 4), 4 * (x % (D / 4)), acc[i], s_i[x / (D / 4)]);
+              }
             }
           }
           __syncthreads();

@@ -573,12 +573,186 @@ __device__ __forceinline__ void stage_q(const Params& p, uint8_t* qsm, float* rs
   }
 }
 
+// ---- the line of tiles
+
+// A sequence's length as its table allows, and the first position that some of its tokens sees.
+__device__ __forceinline__ int length_of(const AttnArgs& a, int b, bool tell) {
+  const int n = __ldg(a.seq_lens + b);
+  const int64_t room = a.max_pages << a.page_shift;
+  if (n > room) {
+    if (tell) record_error(a.err, DEV_ERR_PAGE);
+    return static_cast<int>(room);
+  }
+  return max(n, 0);
+}
+__device__ __forceinline__ int first_of(const AttnArgs& a, int len) {
+  return a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0;
+}
+// Units of the line that one item of the sequence takes (an empty sequence has one, so that its rows are written).
+__device__ __forceinline__ int units_of(const AttnArgs& a, int len, int start) {
+  return len > 0 ? start + (len + TK - 1) / TK - first_of(a, len) / TK : 1;
+}
+
+// prefix [B + 1]: units (per head and row tile) before each sequence.  Threads 0 .. NTH - 1 work, every thread of the
+// block calls.
+__device__ __forceinline__ void build_prefix(const AttnArgs& a, int start, int* prefix, int* s_scan) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (a.B + NTH - 1) / NTH;
+  const int b0 = tid < NTH ? min(a.B, tid * per) : a.B, b1 = tid < NTH ? min(a.B, b0 + per) : a.B;
+  int n = 0;
+  for (int b = b0; b < b1; ++b) n += units_of(a, length_of(a, b, blockIdx.x == 0), start);
+  int incl = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31 && tid < NTH) s_scan[warp] = incl;
+  __syncthreads();
+  int before = incl - n;
+  for (int w = 0; w < warp && w < NW; ++w) before += s_scan[w];
+  for (int b = b0; b < b1; ++b) {
+    prefix[b] = before;
+    before += units_of(a, length_of(a, b, false), start);
+    if (b == a.B - 1) prefix[a.B] = before;
+  }
+  __syncthreads();
+}
+
+// The line and its cut: ranges 0 .. nc - 1, `more` of share + 1 units, then of share.
+struct Line {
+  const int* prefix;
+  int HR, nc, share, more;  // heads x row tiles of a sequence; ranges
+  __device__ __forceinline__ Line(const AttnArgs& a, int RT, const int* pre) : prefix(pre) {
+    HR = a.c.n_kv_heads * RT;  // the host has seen to it that the line's units fit 31 bits
+    const int total = prefix[a.B] * HR;
+    nc = min(total, static_cast<int>(gridDim.x));
+    share = total / nc;
+    more = total - share * nc;
+  }
+  __device__ __forceinline__ int bound(int k) const { return k * share + min(k, more); }
+  __device__ __forceinline__ int range_of(int u) const {
+    return u < more * (share + 1) ? u / (share + 1) : more + (u - more * (share + 1)) / share;
+  }
+};
+// The item that unit u is of: its tiles are units [i0, i1).
+struct Item {
+  int b, hr, hk, rt, len, i0, i1;
+  __device__ __forceinline__ Item(const AttnArgs& a, const Line& line, int RT, int start, int u) {
+    b = 0;  // the last sequence that starts at or before u
+    for (int w = 1 << (31 - __clz(a.B)); w > 0; w >>= 1)
+      if (b + w < a.B && line.prefix[b + w] * line.HR <= u) b += w;
+    const int nt = line.prefix[b + 1] - line.prefix[b];
+    hr = (u - line.prefix[b] * line.HR) / nt;
+    hk = hr / RT;
+    rt = hr - hk * RT;
+    len = length_of(a, b, false);
+    i1 = line.prefix[b] * line.HR + (hr + 1) * nt;
+    i0 = len > 0 ? i1 - nt + start : i1 - 1;
+  }
+};
+
+// The last CTA to arrive with its part of an item joins the ranges' sums: NTH threads (tid) call with their part stored,
+// sync being their barrier.  scratch: `room` bytes of shared memory; s_sum, s_i, s_last: shared.  write(r, d, sum, factor).
+template <int D, int ROWS, class Sync, class Write>
+__device__ __forceinline__ void join_parts(const Params& p, const Line& line, const Item& it, int R, int tid, float* factor, int room,
+                                           float* s_sum, float* s_i, int* s_last, Sync sync, Write write) {
+  const int warp = tid >> 5, lane = tid & 31;
+  const int ca = line.range_of(it.i0), cb = line.range_of(it.i1 - 1);
+  const int parts = cb - ca + 1;  // the item's tiles lie in ranges ca .. cb
+  sync();
+  if (tid == 0) {
+    __threadfence();  // after the barrier: orders the whole block's stores before the arrival
+    int* cnt = p.count + (it.b * line.HR + it.hr);
+    *s_last = atomicAdd(cnt, 1) == parts - 1;
+    if (*s_last) *cnt = 0;
+  }
+  sync();
+  if (!*s_last) return;
+  __threadfence();
+  // every range but the first starts in the item's tiles
+  const int slot0 = 2 * ca + (line.bound(ca) >= it.i0 ? 1 : 0);
+  auto slot_of = [&](int k) { return k == 0 ? slot0 : 2 * (ca + k) + 1; };
+  const int fit = min(R, room / 4 / parts);  // factor: [parts][rows], as many rows at a time as fit
+  for (int rb = 0; rb < R; rb += fit) {
+    const int rows = min(fit, R - rb);
+    // a row's parts are spread over as many lanes as they need, so that a warp takes several rows at a time
+    const int span = parts >= 32 ? 32 : 1 << (32 - __clz(parts - 1)), k0 = lane & (span - 1);
+    for (int r1 = warp * (32 / span); r1 < rows; r1 += NW * (32 / span)) {
+      const int r = r1 + lane / span;
+      float mm = -INFINITY, ll = 0.0f;
+      if (r < rows)
+        for (int k = k0; k < parts; k += span) {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (static_cast<int64_t>(slot_of(k)) * ROWS + rb + r) * 2));
+          factor[k * rows + r] = x.x;
+          mm = fmaxf(mm, x.x);
+          if (parts <= 32) ll = x.y;
+        }
+      for (int o = span / 2; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+      const float ms = mm == -INFINITY ? 0.0f : mm;
+      if (r < rows) {
+        const float first = ll;
+        ll = 0.0f;
+        for (int k = k0; k < parts; k += span) {
+          const float e = ex2(factor[k * rows + r] - ms);
+          factor[k * rows + r] = e;
+          ll += e * (parts <= 32 ? first : __ldcg(p.part_ml + (static_cast<int64_t>(slot_of(k)) * ROWS + rb + r) * 2 + 1));
+        }
+      }
+      for (int o = span / 2; o > 0; o >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o);
+      if (r < rows && k0 == 0) s_i[r] = ll == 0.0f ? 0.0f : p.a.c.v_scale / ll;
+    }
+    sync();
+    // Vectors of the rows, four at a time per lane, over the parts, two in flight.  Few parts: every warp takes all of them
+    // for its vectors; many: each warp a quarter of them for all vectors, joined in shared memory.
+    constexpr int XU = 4;
+    const int vecs = rows * (D / 4), groups = parts > 8 ? NW : 1, warps = NW / groups;
+    float4* sum = reinterpret_cast<float4*>(s_sum);
+    for (int x1 = 0; x1 < vecs; x1 += warps * 32 * XU) {
+      const int x0 = x1 + (groups == 1 ? warp * 32 : 0) + lane;
+      float4 acc[XU];
+#pragma unroll
+      for (int i = 0; i < XU; ++i) acc[i] = make_float4(0, 0, 0, 0);
+#pragma unroll 2
+      for (int k = groups == 1 ? 0 : warp; k < parts; k += groups) {
+        const float4* part = reinterpret_cast<const float4*>(p.part + (static_cast<int64_t>(slot_of(k)) * ROWS + rb) * D);
+#pragma unroll
+        for (int i = 0; i < XU; ++i) {
+          const int x = x0 + i * warps * 32;
+          if (x < vecs) add4(acc[i], factor[k * rows + x / (D / 4)], __ldcg(part + x));
+        }
+      }
+      if (groups > 1) {
+#pragma unroll
+        for (int i = 0; i < XU; ++i) sum[(warp * XU + i) * 32 + lane] = acc[i];
+        sync();
+        if (warp < XU) {
+          acc[0] = sum[warp * 32 + lane];
+#pragma unroll
+          for (int w = 1; w < NW; ++w) add4(acc[0], 1.0f, sum[(w * XU + warp) * 32 + lane]);
+          const int x = x0 + warp * 32;
+          if (x < vecs) write(rb + x / (D / 4), 4 * (x % (D / 4)), acc[0], s_i[x / (D / 4)]);
+        }
+        sync();
+      } else {
+#pragma unroll
+        for (int i = 0; i < XU; ++i) {
+          const int x = x0 + i * warps * 32;
+          if (x < vecs) write(rb + x / (D / 4), 4 * (x % (D / 4)), acc[i], s_i[x / (D / 4)]);
+        }
+      }
+    }
+    sync();
+  }
+}
+constexpr int JOIN_SUMS = NW * 4 * 32 * 4;  // floats of s_sum
+
 template <class Q, class C, int D, int NT>
 __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(const __grid_constant__ Params p) {
   using K = Cfg<Q, C, D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_scan[NW];
-  __shared__ __align__(16) float s_sum[NW * 2 * 32 * 4];
+  __shared__ __align__(16) float s_sum[JOIN_SUMS];
   __shared__ int s_last;
   float* rscale = reinterpret_cast<float*>(smem);  // [ROWS]
   float* s_i = rscale + K::ROWS;                   // [ROWS] the join's 1 / weight sum
@@ -591,82 +765,38 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the line of tiles (an empty sequence has a unit, too, so that its rows are written)
-  const int64_t room = a.max_pages << a.page_shift;
-  auto length = [&](int b, bool tell) {
-    const int n = __ldg(a.seq_lens + b);
-    if (n > room) {
-      if (tell) record_error(a.err, DEV_ERR_PAGE);
-      return static_cast<int>(room);
-    }
-    return max(n, 0);
-  };
-  auto first_of = [&](int len) { return a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0; };
-  auto tiles_of = [&](int len) { return len > 0 ? START + (len + TK - 1) / TK - first_of(len) / TK : 1; };
-  const int per = (a.B + NTH - 1) / NTH;
-  {
-    const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
-    int n = 0;
-    for (int b = b0; b < b1; ++b) n += tiles_of(length(b, blockIdx.x == 0));
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    int before = incl - n;
-    for (int w = 0; w < warp; ++w) before += s_scan[w];
-    for (int b = b0; b < b1; ++b) {
-      prefix[b] = before;
-      before += tiles_of(length(b, false));
-      if (b == a.B - 1) prefix[a.B] = before;
-    }
-    __syncthreads();
-  }
-  const int HR = a.c.n_kv_heads * p.RT;  // the host has seen to it that the line's units fit 31 bits
-  const int total = prefix[a.B] * HR;
-  const int nc = min(total, static_cast<int>(gridDim.x));
-  if (static_cast<int>(blockIdx.x) >= nc) return;
-  // ranges 0 .. nc - 1: `more` of share + 1 units, then of share
-  const int share = total / nc, more = total - share * nc;
-  auto bound = [&](int k) { return k * share + min(k, more); };
-  auto range_of = [&](int u) { return u < more * (share + 1) ? u / (share + 1) : more + (u - more * (share + 1)) / share; };
-
-  const int range = blockIdx.x, lo = bound(range), hi = bound(range + 1);
+  build_prefix(a, START, prefix, s_scan);
+  const Line line(a, p.RT, prefix);
+  const int range = blockIdx.x;
+  if (range >= line.nc) return;
+  const int lo = line.bound(range), hi = line.bound(range + 1);
   for (int u = lo; u < hi;) {
-    int b = 0;  // the last sequence that starts at or before u
-    for (int w = 1 << (31 - __clz(a.B)); w > 0; w >>= 1)
-      if (b + w < a.B && prefix[b + w] * HR <= u) b += w;
-    const int nt = prefix[b + 1] - prefix[b], hr = (u - prefix[b] * HR) / nt, hk = hr / p.RT, rt = hr - hk * p.RT;
-    Seg g;
-    g.len = length(b, false);
-    const int i1 = prefix[b] * HR + (hr + 1) * nt;            // the item's end
-    const int i0 = g.len > 0 ? i1 - nt + START : i1 - 1;      // its first tile
-    const int end = min(i1, hi);
-    if (u < i0) u = i0;
+    const Item it(a, line, p.RT, START, u);
+    const int end = min(it.i1, hi);
+    if (u < it.i0) u = it.i0;
     if (u >= end) {  // none of its tiles is in this range
       u = end;
       continue;
     }
-    const int r0 = rt * K::ROWS, R = min(K::ROWS, a.T * a.G - r0);
+    const int r0 = it.rt * K::ROWS, R = min(K::ROWS, a.T * a.G - r0);
     auto write = [&](int r, int d, float4 v, float inv) {
-      const int row = r0 + r, t = row / a.G, h = hk * a.G + row - t * a.G;
-      put4(static_cast<Q*>(a.out) + ((static_cast<int64_t>(b) * a.T + t) * a.Hq + h) * D + d, v, inv);
+      const int row = r0 + r, t = row / a.G, h = it.hk * a.G + row - t * a.G;
+      put4(static_cast<Q*>(a.out) + ((static_cast<int64_t>(it.b) * a.T + t) * a.Hq + h) * D + d, v, inv);
     };
-    if (g.len == 0) {
+    if (it.len == 0) {
       for (int x = threadIdx.x; x < R * (D / 4); x += NTH) write(x / (D / 4), 4 * (x % (D / 4)), make_float4(0, 0, 0, 0), 0.0f);
       u = end;
       continue;
     }
-    g.first = first_of(g.len);
-    g.table = a.page_table + b * a.max_pages;
-    g.head_off = hk * a.c.head_stride;
-    g.t0 = u - i0 + g.first / TK;
-    g.t1 = end - i0 + g.first / TK;
+    Seg g;
+    g.len = it.len;
+    g.first = first_of(a, it.len);
+    g.table = a.page_table + it.b * a.max_pages;
+    g.head_off = it.hk * a.c.head_stride;
+    g.t0 = u - it.i0 + g.first / TK;
+    g.t1 = end - it.i0 + g.first / TK;
 
-    stage_q<Q, C, D, NT>(p, qsm, rscale, b, hk, r0, warp, lane);
+    stage_q<Q, C, D, NT>(p, qsm, rscale, it.b, it.hk, r0, warp, lane);
     __syncthreads();
     int pos[NT][2];
     float qs[NT][2];
@@ -710,8 +840,8 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
         }
       }
     __syncthreads();
-    const bool whole = u == i0 && end == i1;
-    const int slot = 2 * range + (lo >= i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
+    const bool whole = u == it.i0 && end == it.i1;
+    const int slot = 2 * range + (lo >= it.i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
     for (int x = threadIdx.x; x < R * (D / 4); x += NTH) {
       const int r = x / (D / 4), d = 4 * (x % (D / 4));
       float mm = -INFINITY, ll = 0.0f;
@@ -732,90 +862,9 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
         if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * K::ROWS + r) * 2) = make_float2(mm, ll);
       }
     }
-    if (!whole) {
-      // ---- the last CTA of the item to arrive joins the ranges' sums
-      const int ca = range_of(i0), cb = range_of(i1 - 1);
-      const int parts = cb - ca + 1;  // the item's tiles lie in ranges ca .. cb
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        __threadfence();  // after the barrier: orders the whole block's stores before the arrival
-        int* cnt = p.count + (b * HR + hr);
-        s_last = atomicAdd(cnt, 1) == parts - 1;
-        if (s_last) *cnt = 0;
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        // every range but the first starts in the item's tiles
-        const int slot0 = 2 * ca + (bound(ca) >= i0 ? 1 : 0);
-        auto slot_of = [&](int k) { return k == 0 ? slot0 : 2 * (ca + k) + 1; };
-        float* factor = reinterpret_cast<float*>(ring);  // [parts][rows], as many rows at a time as fit
-        const int fit = min(R, K::S * NW * K::STAGE / 4 / parts);
-        for (int rb = 0; rb < R; rb += fit) {
-          const int rows = min(fit, R - rb);
-          for (int r = warp; r < rows; r += NW) {
-            float mm = -INFINITY, ll = 0.0f;
-            for (int k = lane; k < parts; k += 32) {
-              const float x = __ldcg(p.part_ml + (static_cast<int64_t>(slot_of(k)) * K::ROWS + rb + r) * 2);
-              factor[k * rows + r] = x;
-              mm = fmaxf(mm, x);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
-            const float ms = mm == -INFINITY ? 0.0f : mm;
-            for (int k = lane; k < parts; k += 32) {
-              const float e = ex2(factor[k * rows + r] - ms);
-              factor[k * rows + r] = e;
-              ll += e * __ldcg(p.part_ml + (static_cast<int64_t>(slot_of(k)) * K::ROWS + rb + r) * 2 + 1);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o);
-            if (lane == 0) s_i[r] = ll == 0.0f ? 0.0f : a.c.v_scale / ll;
-          }
-          __syncthreads();
-          // Vectors of the rows, XU at a time per lane, over the parts, four in flight.  Few parts: every warp takes all of
-          // them for its vectors; many: each warp a quarter of them for all vectors, joined in shared memory.
-          constexpr int XU = 2;
-          const int vecs = rows * (D / 4), groups = parts > 8 ? NW : 1, warps = NW / groups;
-          float4* sum = reinterpret_cast<float4*>(s_sum);
-          for (int x1 = 0; x1 < vecs; x1 += warps * 32 * XU) {
-            const int x0 = x1 + (groups == 1 ? warp * 32 : 0) + lane;
-            float4 acc[XU];
-#pragma unroll
-            for (int i = 0; i < XU; ++i) acc[i] = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-            for (int k = groups == 1 ? 0 : warp; k < parts; k += groups) {
-              const float4* part = reinterpret_cast<const float4*>(p.part + (static_cast<int64_t>(slot_of(k)) * K::ROWS + rb) * D);
-#pragma unroll
-              for (int i = 0; i < XU; ++i) {
-                const int x = x0 + i * warps * 32;
-                if (x < vecs) add4(acc[i], factor[k * rows + x / (D / 4)], __ldcg(part + x));
-              }
-            }
-            if (groups > 1) {
-#pragma unroll
-              for (int i = 0; i < XU; ++i) sum[(warp * XU + i) * 32 + lane] = acc[i];
-              __syncthreads();
-              if (warp < XU) {
-                acc[0] = sum[warp * 32 + lane];
-#pragma unroll
-                for (int w = 1; w < NW; ++w) add4(acc[0], 1.0f, sum[(w * XU + warp) * 32 + lane]);
-                const int x = x0 + warp * 32;
-                if (x < vecs) write(rb + x / (D / 4), 4 * (x % (D / 4)), acc[0], s_i[x / (D / 4)]);
-              }
-              __syncthreads();
-            } else {
-#pragma unroll
-              for (int i = 0; i < XU; ++i) {
-                const int x = x0 + i * warps * 32;
-                if (x < vecs) write(rb + x / (D / 4), 4 * (x % (D / 4)), acc[i], s_i[x / (D / 4)]);
-              }
-            }
-          }
-          __syncthreads();
-        }
-      }
-    }
+    if (!whole)
+      join_parts<D, K::ROWS>(p, line, it, R, threadIdx.x, reinterpret_cast<float*>(ring), K::S * NW * K::STAGE, s_sum, s_i, &s_last,
+                             [] { __syncthreads(); }, write);
     __syncthreads();
     u = end;
   }
@@ -851,6 +900,10 @@ cudaError_t launch_kind(const Params& p, int rows, cudaStream_t st) {
 }
 
 }  // namespace attn
+
+// More than 16 rows, bf16 q and cache, heads of 64 or 128 values (kq_attn_wide.cu).
+constexpr int kWideRows = 128;
+cudaError_t launch_attn_wide(const attn::Params& p, cudaStream_t st);
 
 // One translation unit per cache and query type (rows: query rows per pass, 8, 16 or 32).
 cudaError_t launch_attn_bf16_bf16(const attn::Params& p, int rows, cudaStream_t st);

@@ -39,6 +39,14 @@
 // hundreds of steps of a long range grows to 2^-16, so with fp32 q each step's
 // product is added by rounding fp32 additions.
 //
+// Measured on one GB300, calls in a graph: 4 x 131071 positions, 32 heads on 8
+// of 128, bf16, 316-322 us (6.4 TB/s, 94% of the copy rate); 24 sequences of 0
+// to 9001 positions, 71-76 us (5.2-5.5 TB/s: the slower fifth of the SMs ends
+// an eighth later, and an even cut cannot know them); one of 1000 positions,
+// 9.1 us, a chain of length, page, row, sum, partial sums and their join; 16
+// sequences in an e4m3 cache, heads of 256, fp32 q, window 4096, cap, 34 us
+// (3.9 TB/s: two CTAs per SM of 255 registers, and 4 us of joins).
+//
 // Values that no row sees are never loaded (zeros take their place).  One that
 // some rows of the block see and others do not would reach the others as
 // 0 * NaN if it is not finite: a warp whose sums are not all finite runs its

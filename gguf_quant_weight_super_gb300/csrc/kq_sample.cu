@@ -28,6 +28,12 @@
 //    answer are listed and sorted; where a bin has more words than the list,
 //    1024 bins of the next digits of their sorting key at a time, the index
 //    being the last.
+// Measured on one GB300, calls in a graph: one row of 151936 (fp32, top-k 20)
+// 12 us: 1.3 for the first pass, 4 for threshold and lists, 1 for fetching
+// them, 4 for the choice, most of it fetching code that runs once; 16 rows of
+// 262144 (nucleus and min-p) 20 us, of which 6 for the total weight; 256 bf16
+// rows of mixed settings 92 us: 52 for all of them and 40 for the one to four
+// flat ones that are left to the tail.
 #include "kq_cache.h"
 
 namespace kq {

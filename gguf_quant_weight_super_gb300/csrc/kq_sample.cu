@@ -200,12 +200,25 @@ __device__ __forceinline__ void block_scan(Smem& s, unsigned long long& m, int& 
   m = im;
   c = ic;
 }
-// Sorts s.list[0, n) ascending, n <= LIST.  By counting: the words' depths, stretched over the bins, nearly sort them
-// (a few words per bin), and inside a bin each word counts those before it.  Where a bin holds many (equal logits):
-// bitonic, a warp's 32 threads comparing within the same 64 places while the stride is 32 or less, so that only wider
-// steps need the whole block's barrier.  Takes s.cand and s.count as scratch.
+// Sorts s.list[0, n) ascending, n <= LIST.  Up to 320 words: each counts those before it.  More: the words'
+// depths, stretched over the bins, nearly sort them (a few words per bin), and inside a bin each word counts those before
+// it.  Where a bin holds many (equal logits): bitonic, a warp's 32 threads comparing within the same 64 places while the
+// stride is 32 or less, so that only wider steps need the whole block's barrier.  Takes s.cand and s.count as scratch.
 __device__ __noinline__ void sort_list(Smem& s, const Row r, int n) {
-  constexpr int PER = LIST / STH, MANY = 160;
+  constexpr int PER = LIST / STH, MANY = 160, MOST = 320;
+  if (n <= MOST) {
+    const int t = threadIdx.x;
+    const unsigned long long mine = t < n ? s.list[t] : 0;
+    int place = 0;
+    if (t < n) {
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) place += s.list[j] < mine;
+    }
+    __syncthreads();
+    if (t < n) s.list[place] = mine;
+    __syncthreads();
+    return;
+  }
   unsigned long long cv[PER];
   float z[PER], deepest = 0.0f;
 #pragma unroll
@@ -367,31 +380,31 @@ __device__ __forceinline__ int push_at(int* counter, bool on) {
   return __shfl_sync(0xFFFFFFFFu, base, 0) + __popc(who & ((1u << lane) - 1u));
 }
 
-// The cuts and the choice on n <= FEW listed words, by one warp: v[0, n) in any order, two words per lane.  total: the
-// row's weight where k is 0.  Returns whether the answer lies in the list; then cv_out and the kept weight in `total`.
+// The cuts and the choice on n <= FEW listed words, by one warp, two words per lane.  total: the row's weight where k is 0.  Returns whether the answer lies in the list; then cv_out and the kept weight in `total`.
 // Runs once per row: loops stay rolled, since what it costs is fetching its code.
-__device__ __noinline__ bool choose_in_warp(const unsigned long long* list, const Row r, int n, bool complete, int k, float p,
-                                            float mp, float u, unsigned long long& total, unsigned long long& cv_out) {
+__device__ __noinline__ bool choose_in_warp(const unsigned long long* list, bool sorted, const Row r, int n, bool complete, int k,
+                                            float p, float mp, float u, unsigned long long& total, unsigned long long& cv_out) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31;
   unsigned long long v0 = lane < n ? list[lane] : ~0ull, v1 = lane + 32 < n ? list[lane + 32] : ~0ull;
-  // bitonic over places lane and lane + 32
+  if (!sorted) {  // bitonic over places lane and lane + 32
 #pragma unroll 1
-  for (int k2 = 2; k2 <= 32; k2 <<= 1)
+    for (int k2 = 2; k2 <= 32; k2 <<= 1)
 #pragma unroll 1
-    for (int j = k2 >> 1; j > 0; j >>= 1) {
+      for (int j = k2 >> 1; j > 0; j >>= 1) {
+        const unsigned long long o0 = __shfl_xor_sync(kAll, v0, j), o1 = __shfl_xor_sync(kAll, v1, j);
+        const bool least = ((lane & j) == 0) == ((lane & k2) == 0);  // k2 = 32: the lower half ascends, the upper descends
+        v0 = (v0 < o0) == least ? v0 : o0;
+        v1 = (v1 < o1) == (k2 == 32 ? (lane & j) != 0 : least) ? v1 : o1;
+      }
+    if (v0 > v1) { const unsigned long long x = v0; v0 = v1; v1 = x; }
+#pragma unroll 1
+    for (int j = 16; j > 0; j >>= 1) {
       const unsigned long long o0 = __shfl_xor_sync(kAll, v0, j), o1 = __shfl_xor_sync(kAll, v1, j);
-      const bool least = ((lane & j) == 0) == ((lane & k2) == 0);  // k2 = 32: the lower half ascends, the upper descends
+      const bool least = (lane & j) == 0;
       v0 = (v0 < o0) == least ? v0 : o0;
-      v1 = (v1 < o1) == (k2 == 32 ? (lane & j) != 0 : least) ? v1 : o1;
+      v1 = (v1 < o1) == least ? v1 : o1;
     }
-  if (v0 > v1) { const unsigned long long x = v0; v0 = v1; v1 = x; }
-#pragma unroll 1
-  for (int j = 16; j > 0; j >>= 1) {
-    const unsigned long long o0 = __shfl_xor_sync(kAll, v0, j), o1 = __shfl_xor_sync(kAll, v1, j);
-    const bool least = (lane & j) == 0;
-    v0 = (v0 < o0) == least ? v0 : o0;
-    v1 = (v1 < o1) == least ? v1 : o1;
   }
   const unsigned long long w0 = lane < n ? r.units(logit_of(v0)) : 0, w1 = lane + 32 < n ? r.units(logit_of(v1)) : 0;
   unsigned long long c0 = w0, c1 = w1;  // running sums with the word
@@ -830,16 +843,18 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
       }
     } else if (good) {
       unsigned long long total = sum;  // weight of the words kept
-      if (n <= FEW) {
-        if (warp == 0) {
-          unsigned long long cv = 0, kept = total;
-          if (choose_in_warp(s.list, r, n, complete, k, p, mp, u, kept, cv) && lane == 0) {
-            write_row(a, m, r, cv, kept);
-            s.done = 1;
-          }
+      // first the likeliest words by one warp, then all of the list by the block
+      if (n > FEW) sort_list(s, r, n);
+      bool found = false;
+      if (warp == 0) {
+        unsigned long long cv = 0, kept = total;
+        found = choose_in_warp(s.list, n > FEW, r, min(n, FEW), complete && n <= FEW, k, p, mp, u, kept, cv);
+        if (found && lane == 0) {
+          write_row(a, m, r, cv, kept);
+          s.done = 1;
         }
-      } else {
-        sort_list(s, r, n);
+      }
+      if (n > FEW && !__syncthreads_or(found)) {
         const Held h = hold(s, r, n);
         if (k > 0) {
           if (pass_at(s, h, 0, static_cast<unsigned long long>(k) - 1, true)) {

@@ -514,13 +514,17 @@ def _rows(name: str, x: torch.Tensor, B: int, T: int, D: int):
     return shape[2], _row_stride(name, x, B, T, shape[2], D)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent from builds without CUDA, as _cuda_getDevice
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _host():
     return ValueError("libkq takes device tensors only")
 
 
 def _here():
     """The current device's current stream (a device tensor is at hand, so CUDA is up)."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _raw_stream(_device())
 
 
 def kv_append(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -546,8 +550,8 @@ def kv_append(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, 
     out_code = _DTYPE_CODE.get(q_out.dtype)
     if out_code is None:
         raise TypeError("q_out is float32 or bfloat16")
-    W = page_table.shape[-1]
-    if page_table.dtype is not _i32 or page_table.shape != (B, W) or not page_table.is_contiguous():
+    rows, W = page_table.shape
+    if page_table.dtype is not _i32 or rows != B or not page_table.is_contiguous():
         raise ValueError(f"page_table: contiguous int32 [{B}, max_pages]")
     if seq_lens.dtype is not _i32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
         raise ValueError(f"seq_lens: contiguous int32 [{B}]")
@@ -555,7 +559,9 @@ def kv_append(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, 
         raise _host()
     status = (_lib or lib()).kq_kv_append(
         cache._ref, page_table.data_ptr(), W, seq_lens.data_ptr(), B, T, q.data_ptr(), k.data_ptr(), v.data_ptr(), code,
-        _row_stride("q", q, B, T, Hq, D), _row_stride("k", k, B, T, heads, D), _row_stride("v", v, B, T, heads, D), Hq,
+        Hq * D if q.is_contiguous() else _row_stride("q", q, B, T, Hq, D),
+        heads * D if k.is_contiguous() else _row_stride("k", k, B, T, heads, D),
+        heads * D if v.is_contiguous() else _row_stride("v", v, B, T, heads, D), Hq,
         rope._ref, q_out.data_ptr(), out_code, _here() if stream is None else _stream(stream))
     if status:
         raise KQError("kq_kv_append", status)
@@ -585,8 +591,8 @@ def attn_decode(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor
         out = torch.empty(shape, dtype=dtype, device=q.device)
     elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
         raise ValueError("out: contiguous, of q's shape and type")
-    W = page_table.shape[-1]
-    if page_table.dtype is not _i32 or page_table.shape != (B, W) or not page_table.is_contiguous():
+    rows, W = page_table.shape
+    if page_table.dtype is not _i32 or rows != B or not page_table.is_contiguous():
         raise ValueError(f"page_table: contiguous int32 [{B}, max_pages]")
     if seq_lens.dtype is not _i32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
         raise ValueError(f"seq_lens: contiguous int32 [{B}]")
@@ -596,7 +602,7 @@ def attn_decode(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor
         raise _host()
     status = (_lib or lib()).kq_attn_decode(
         cache._ref, page_table.data_ptr(), W, seq_lens.data_ptr(), B, T, q.data_ptr(), code,
-        _row_stride("q", q, B, T, Hq, D), Hq, D ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
+        Hq * D if q.is_contiguous() else _row_stride("q", q, B, T, Hq, D), Hq, D ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
         workspace.data_ptr(), workspace.numel(), _here() if stream is None else _stream(stream))
     if status:
         raise KQError("kq_attn_decode", status)

@@ -51,7 +51,7 @@ constexpr float kSpan = 29.0f;  // exp(-29) < 2^-41: words this far below the la
 constexpr int kIdxBits = 20;
 
 // Which words the cluster looks at next, and what for: from the first CTA to the others.
-enum : int { kAll, kDigits, kGather, kStop };
+enum : int { kAll, kDigits, kGather, kNone };
 struct Cmd {
   int what;
   int bin;                 // kDigits, kGather: the bin of all words
@@ -61,6 +61,8 @@ struct Cmd {
 
 struct Smem {
   uint32_t count[BINS], limb[3][BINS];
+  unsigned long long all_m[BINS];  // the whole row's histogram, in the first CTA
+  uint32_t all_c[BINS];
   unsigned long long list[LIST];
   unsigned long long cand[CAND];
   unsigned long long scan_m[SW], red_m[SW];
@@ -68,7 +70,7 @@ struct Smem {
   float red_f[SW];
   unsigned long long mass;      // this CTA's sum
   unsigned long long tau;       // its threshold, as the largest sorting key that is listed for sure
-  int ncand, nlist, done;
+  int ncand, nhit, nlist, listed, done;
   float bmax;
   Cmd cmd;
   unsigned long long found_cv, found_before;  // the word at which a running sum passes, and the sum before it
@@ -124,9 +126,10 @@ __device__ __forceinline__ void each_word(const X* row, int V, int rank, int CS,
 __device__ __forceinline__ float largest(const float*, uint4 v) {
   return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
 }
-__device__ __forceinline__ float largest(const __nv_bfloat16*, uint4 v) {
-  const float x = fmaxf(fmaxf(bf16_lo(v.x), bf16_hi(v.x)), fmaxf(bf16_lo(v.y), bf16_hi(v.y)));
-  return fmaxf(x, fmaxf(fmaxf(bf16_lo(v.z), bf16_hi(v.z)), fmaxf(bf16_lo(v.w), bf16_hi(v.w))));
+__device__ __forceinline__ float largest(const __nv_bfloat16*, uint4 v) {  // NaN counts for nothing
+  auto pair = [](uint32_t x) { return *reinterpret_cast<__nv_bfloat162*>(&x); };
+  const __nv_bfloat162 x = __hmax2(__hmax2(pair(v.x), pair(v.y)), __hmax2(pair(v.z), pair(v.w)));
+  return fmaxf(__low2float(x), __high2float(x));
 }
 
 // Words compare by their sorting key, ascending: the logit's bits in an order that compares as integers, inverted, then
@@ -196,7 +199,9 @@ __device__ __forceinline__ void block_scan(Smem& s, unsigned long long& m, int& 
   __syncthreads();
   im -= m;
   ic -= c;
-  for (int w = 0; w < warp; ++w) { im += s.scan_m[w]; ic += s.scan_c[w]; }
+#pragma unroll
+  for (int w = 0; w < SW - 1; ++w)
+    if (w < warp) { im += s.scan_m[w]; ic += s.scan_c[w]; }
   m = im;
   c = ic;
 }
@@ -300,6 +305,9 @@ __device__ __forceinline__ unsigned long long peer64(uint32_t addr) {
 }
 __device__ __forceinline__ void peer_store64(uint32_t addr, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void peer_store32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ int peer_add(uint32_t addr, int v) {
   int r;
@@ -470,6 +478,64 @@ __device__ __forceinline__ void sum_where(Smem& s, const X* row, int V, int rank
   const unsigned long long t = block_sum(s, static_cast<unsigned long long>((static_cast<long long>(hi) << 20) + lo));
   if (threadIdx.x == 0) s.mass = t;
 }
+// The same for all words, two at a time: half the instructions, which bound it where a CTA has a whole row.  The largest
+// logit and the scale are finite.
+struct F2 {
+  unsigned long long v;
+  __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ explicit F2(float a) : F2(a, a) {}
+  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(a.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return a;
+}
+template <class F>
+__device__ __forceinline__ void each_pair(const float*, uint4 v, F f) {
+  f(__uint_as_float(v.x), __uint_as_float(v.y)), f(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+template <class F>
+__device__ __forceinline__ void each_pair(const __nv_bfloat16*, uint4 v, F f) {
+  f(bf16_lo(v.x), bf16_hi(v.x)), f(bf16_lo(v.y), bf16_hi(v.y)), f(bf16_lo(v.z), bf16_hi(v.z)), f(bf16_lo(v.w), bf16_hi(v.w));
+}
+template <class X, class G>
+__device__ __forceinline__ void sum_all(Smem& s, const X* row, int V, int rank, int CS, const Row& r, G also) {
+  uint32_t hi = 0, lo = 0, pairs = 0;
+  const F2 less(-r.lmax), c(r.c), unit(1048576.0f), magic(12582912.0f), minus(-1.0f);
+  each_chunk<sizeof(X)>(
+      row, V, rank, CS,
+      [&](int i, uint4 v) {
+        also(i, v);
+        each_pair(row, v, [&](float a, float b) {
+          ((F2(a, b) + less) * c).get(a, b);
+          const F2 w(fmaxf(ex2(a), 0.0f), fmaxf(ex2(b), 0.0f));  // a NaN weighs nothing
+          const F2 h = fma2(w, unit, magic), l = fma2(fma2(w, unit, fma2(h, minus, magic)), unit, magic);
+          h.get(a, b);
+          hi += __float_as_uint(a) + __float_as_uint(b);
+          l.get(a, b);
+          lo += __float_as_uint(a) + __float_as_uint(b);
+          ++pairs;
+        });
+      },
+      [&](int, float l) {
+        int h, g;
+        r.parts(l, h, g);
+        if (l > -INFINITY) { hi += h; lo += g; }
+      });
+  hi -= pairs * 0x96800000u;
+  lo -= pairs * 0x96800000u;
+  const unsigned long long t =
+      block_sum(s, static_cast<unsigned long long>((static_cast<long long>(hi) << 20) + static_cast<int>(lo)));
+  if (threadIdx.x == 0) s.mass = t;
+}
 // Lists the words of a chunk from `cut` up.
 template <class X>
 __device__ __noinline__ void list_chunk(Smem& s, const X* row, int i, uint4 v, float cut) {
@@ -506,21 +572,45 @@ __device__ __forceinline__ void add_weight(Smem& s, int d, unsigned long long w)
   if (l1) atomicAdd(&s.limb[1][d], l1);
   if (l2) atomicAdd(&s.limb[2][d], l2);
 }
-// The sum of the cluster's histograms.
-__device__ __forceinline__ Bins read_bins(Smem& s, int CS) {
+// The sum of the cluster's histograms, into the first CTA's `to` (weights) and `to_n` (words).  Each CTA sums its share of the bins: one that
+// read all of them from the others (128 KB) took 8 us.
+__device__ __forceinline__ void share_bins(Smem& s, unsigned long long* to, uint32_t* to_n, int rank, int CS) {
+  const int share = BINS / CS, each = max(1, CS / 2);  // CTAs are read by `each` groups of threads
+  for (int i = threadIdx.x; i < share * each; i += STH) {
+    const int b = rank * share + i % share;
+    unsigned long long m = 0, c = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int q = i / share * 2 + k;
+      if (q < CS) {
+        c += peer32(at_rank(&s.count[b], q));
+        m += static_cast<unsigned long long>(peer32(at_rank(&s.limb[0][b], q))) +
+             (static_cast<unsigned long long>(peer32(at_rank(&s.limb[1][b], q))) << 14) +
+             (static_cast<unsigned long long>(peer32(at_rank(&s.limb[2][b], q))) << 28);
+      }
+    }
+    s.cand[i] = m;
+    s.cand[BINS + i] = c;
+  }
+  __syncthreads();
+  const uint32_t to_m = at_rank(to, 0), to_c = at_rank(to_n, 0);
+  for (int i = threadIdx.x; i < share; i += STH) {
+    unsigned long long m = 0, c = 0;
+    for (int k = 0; k < each; ++k) {
+      m += s.cand[k * share + i];
+      c += s.cand[BINS + k * share + i];
+    }
+    peer_store64(to_m + 8 * (rank * share + i), m);
+    peer_store32(to_c + 4 * (rank * share + i), static_cast<uint32_t>(c));
+  }
+}
+__device__ __forceinline__ Bins read_bins(Smem& s, const unsigned long long* m, const uint32_t* c) {
   Bins h;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) { h.m[e] = 0; h.c[e] = 0; }
-#pragma unroll 2
-  for (int k = 0; k < CS; ++k)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int b = 2 * threadIdx.x + e;
-      h.c[e] += static_cast<int>(peer32(at_rank(&s.count[b], k)));
-      h.m[e] += static_cast<unsigned long long>(peer32(at_rank(&s.limb[0][b], k))) +
-                (static_cast<unsigned long long>(peer32(at_rank(&s.limb[1][b], k))) << 14) +
-                (static_cast<unsigned long long>(peer32(at_rank(&s.limb[2][b], k))) << 28);
-    }
+  for (int e = 0; e < 2; ++e) {
+    h.m[e] = m[2 * threadIdx.x + e];
+    h.c[e] = static_cast<int>(c[2 * threadIdx.x + e]);
+  }
   h.pm = h.m[0] + h.m[1];
   h.pc = h.c[0] + h.c[1];
   block_scan(s, h.pm, h.pc);
@@ -549,138 +639,222 @@ __device__ __forceinline__ void pick_bin(Smem& s, const Bins& h, unsigned long l
   }
   __syncthreads();
 }
-// Over the whole row, every CTA of the cluster: the word at which the running sum of weights (by_count: of words that
-// weigh anything) passes x; found_cv and, by weight, found_before in the first CTA, false there when there is none.  h0:
-// the histogram of all words, made by the first call (have = false).
+// The word of s.list[0, n), in any order, at which the running sum, from base on, passes x, as by pick_bin: found_cv and
+// found_before.  The range of the keys that are left is cut into 1024 bins and one of them picked, until at most 32 words
+// are left for one warp.  The keys of bf16 logits are taken without the 16 bits that all have alike, and those of indices
+// without the bits above V's: the list has few different logits then, and bins by logit alone would hold hundreds of words,
+// whose additions wait for one another (9 us in place of 4 for 2048 words).
 template <class X>
-__device__ __noinline__ bool locate(Smem& s, const X* row, int V, int rank, int CS, const Row& r_in, unsigned long long x,
-                                    bool by_count, Bins& h0, bool have) {
-  const Row r = r_in;  // a copy that no store can change
-  constexpr int UL = sizeof(X) == 4 ? 4 : 2;
-  unsigned long long base_m = 0;
-  int base_c = 0;
-  bool found = true;
-  auto narrow = [&](const Bins& h, int what, int shift, unsigned long long pre) {
-    pick_bin(s, h, base_m, base_c, x, by_count);
-    found = s.pick >= 0;
-    if (found) { base_m = s.pick_m; base_c = s.pick_c; }
-    if (threadIdx.x == 0) {
-      const bool fits = s.pick_n <= LIST;
-      if (what == kAll) {
-        s.cmd.bin = s.pick;
-        s.cmd.shift = fits ? 64 : 42;
-      } else {
-        s.cmd.pre = (shift + 10 < 52 ? pre >> (shift + 10) << (shift + 10) : 0) | (static_cast<unsigned long long>(s.pick) << shift);
-        s.cmd.shift = fits ? shift : shift - 10;
-      }
-      s.cmd.what = !found ? kStop : fits ? kGather : kDigits;
-    }
-    __syncthreads();
+__device__ __forceinline__ void pass_in_list(Smem& s, const Row r, int V, int n, unsigned long long base_m, int base_c,
+                                          unsigned long long x, bool by_count) {
+  constexpr int PER = LIST / STH, kSame = sizeof(X) == 2 ? 16 : 0;
+  const int bits = 32 - __clz(V);
+  auto place = [&](unsigned long long cv) {
+    return (cv >> (kIdxBits + kSame) << bits) | (cv & ((1u << kIdxBits) - 1));
   };
-  if (rank == 0) {
-    if (have) narrow(h0, kAll, 0, 0);
-    else if (threadIdx.x == 0) s.cmd.what = kAll;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned long long at[PER], w[PER];  // ~0: not among those left
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int j = static_cast<int>(threadIdx.x) + i * STH;
+    at[i] = j < n ? place(s.list[j]) : ~0ull;
+    w[i] = j < n ? r.units(logit_of(s.list[j])) : 0;
   }
-  for (;;) {
-    if (threadIdx.x == 0) s.nlist = 0;
-    cluster_sync();  // the command is written, the first CTA's list is empty, and it is done with the histograms
-    const int what = static_cast<int>(peer32(at_rank(&s.cmd.what, 0))), bin = static_cast<int>(peer32(at_rank(&s.cmd.bin, 0)));
-    const int shift = static_cast<int>(peer32(at_rank(&s.cmd.shift, 0)));
-    const unsigned long long pre = peer64(at_rank(&s.cmd.pre, 0));
-    if (what == kStop) {
-      cluster_sync();  // every CTA has read the command
-      break;
+  while (n > 32) {
+    unsigned long long least = ~0ull, most = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      least = min(least, at[i]);
+      if (at[i] != ~0ull) most = max(most, at[i]);
     }
-    if (what != kGather) {
-      for (int i = threadIdx.x; i < BINS; i += STH) { s.count[i] = 0; s.limb[0][i] = 0; s.limb[1][i] = 0; s.limb[2][i] = 0; }
-      __syncthreads();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+      most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
     }
-    if (what == kAll) {
-      each_word<UL>(row, V, rank, CS, [&](int, float l) {
-        int h, g;
-        r.parts(l, h, g);
-        if (!(l > -INFINITY) || !(h | g)) return;
-        const int d = r.bin(l);
+    if (lane == 0) { s.red_m[warp] = least; s.scan_m[warp] = most; }
+    for (int i = threadIdx.x; i < BINS; i += STH) { s.count[i] = 0; s.limb[0][i] = 0; s.limb[1][i] = 0; }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < SW; ++i) { least = min(least, s.red_m[i]); most = max(most, s.scan_m[i]); }
+    const int shift = max(0, 54 - __clzll(static_cast<long long>(most - least)));  // most - least in 1024 steps
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (at[i] != ~0ull) {
+        const int d = static_cast<int>((at[i] - least) >> shift);
         atomicAdd(&s.count[d], 1u);
-        add_weight(s, d, static_cast<unsigned long long>((static_cast<long long>(h) << 20) + g));
-      });
-    } else {
-      const uint32_t list0 = at_rank(s.list, 0), nlist0 = at_rank(&s.nlist, 0);
-      each_word<UL>(row, V, rank, CS, [&](int i, float l) {
-        if (!(l > -INFINITY) || r.bin(l) != bin) return;
-        const unsigned long long cv = sort_key(l, i), w = r.units(l);
-        if (w == 0) return;
-        if (what == kGather) {
-          if (shift < 64 && (cv >> shift) != (pre >> shift)) return;
-          const int at = peer_add(nlist0, 1);
-          if (at < LIST) peer_store64(list0 + 8 * at, cv);
-        } else {
-          if (shift + 10 < 52 && (cv >> (shift + 10)) != (pre >> (shift + 10))) return;
-          const int d = static_cast<int>(cv >> shift) & (BINS - 1);
-          atomicAdd(&s.count[d], 1u);
-          add_weight(s, d, w);
-        }
-      });
+        atomicAdd(&s.limb[0][d], static_cast<uint32_t>(w[i]) & 0xFFFFFu);  // at most 2048 of them: below 2^31
+        atomicAdd(&s.limb[1][d], static_cast<uint32_t>(w[i] >> 20));
+      }
+    __syncthreads();
+    Bins h;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int b = 2 * threadIdx.x + e;
+      h.c[e] = s.count[b];
+      h.m[e] = (static_cast<unsigned long long>(s.limb[1][b]) << 20) + s.limb[0][b];
     }
-    cluster_sync();
-    if (rank != 0) continue;
-    if (what == kGather) {
-      const int n = min(s.nlist, LIST);
-      sort_list(s, r, n);
-      pass_at(s, hold(s, r, n), base_m, by_count ? x - base_c : x, by_count);
-      if (threadIdx.x == 0) s.cmd.what = kStop;
-    } else {
-      const Bins h = read_bins(s, CS);
-      if (what == kAll) h0 = h;
-      narrow(h, what, shift, pre);
-    }
+    h.pm = h.m[0] + h.m[1];
+    h.pc = h.c[0] + h.c[1];
+    block_scan(s, h.pm, h.pc);
+    pick_bin(s, h, base_m, base_c, x, by_count);
+    const int pick = s.pick;
+    if (pick < 0) return;  // none
+    base_m = s.pick_m;
+    base_c = s.pick_c;
+    n = s.pick_n;  // each bin is narrower than all of them by 2^10: six rounds at most
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (at[i] != ~0ull && static_cast<int>((at[i] - least) >> shift) != pick) at[i] = ~0ull;
     __syncthreads();
   }
-  return found;
+  if (threadIdx.x == 0) s.pick_n = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (at[i] != ~0ull) s.cand[atomicAdd(&s.pick_n, 1)] = s.list[static_cast<int>(threadIdx.x) + i * STH];
+  __syncthreads();
+  if (warp == 0) {
+    const unsigned long long mine = lane < n ? s.cand[lane] : ~0ull, has = lane < n ? r.units(logit_of(mine)) : 0;
+    unsigned long long before = base_m, count = base_c;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const unsigned long long o = __shfl_sync(0xFFFFFFFFu, mine, i), ow = __shfl_sync(0xFFFFFFFFu, has, i);
+      if (o < mine) { before += ow; ++count; }
+    }
+    if (lane < n && (by_count ? count == x : before <= x && x < before + has)) {
+      s.found_cv = mine;
+      s.found_before = before;
+    }
+  }
+  __syncthreads();
+}
+// The weight of the words down to the one with the key `last` that weigh at least `least`, every CTA of the cluster.
+template <class X>
+__device__ __noinline__ void sum_cut(Smem& s, const X* row, int V, int rank, int CS, const Row r, unsigned long long last,
+                                     float least) {
+  sum_where(
+      s, row, V, rank, CS, r,
+      [&](int i, float l) { return l > -INFINITY && sort_key(l, i) <= last && r.weight(l) >= least; }, [](int, uint4) {});
 }
 
 // The cuts and the choice over the whole row, every CTA of the cluster.  total: the row's weight, 0 if it is not known.
+// Up to three words are looked for, one after the other: the top_k-th, the last of the nucleus, the token.  Each is found
+// as the word at which the running sum of weights (for the top_k-th: of words that weigh anything) passes x: first its bin
+// in the histogram of the whole row, which is made once, then among the words of that bin.  What is kept across the
+// cluster's barriers is in registers or shared memory: each of them empties the cache that local memory is read through.
 template <class X>
-__device__ __noinline__ void whole_row(Smem& s, const SampleArgs& a, const X* row, int m, int rank, int CS, const Row r,
+__device__ __noinline__ void whole_row(Smem& s, const SampleArgs& a, const X* row, int m, int rank, int CS, const Row r_in,
                                        unsigned long long total, int k, float p, float mp, float u) {
+  const Row r = r_in;  // a copy that no store can change
+  constexpr int UL = 1;
+  enum : int { kCount, kNucleus, kToken };
   const int V = a.V;
-  Bins h0;
-  bool have = false;
-  auto none = [](int, uint4) {};
-  if (total == 0) {
-    sum_where(s, row, V, rank, CS, r, [](int, float l) { return l > -INFINITY; }, none);
+  auto cut_total = [&](unsigned long long last, float least) {
+    sum_cut(s, row, V, rank, CS, r, last, least);
     cluster_sync();
-    total = cluster_mass(s, CS);
+    const unsigned long long t = cluster_mass(s, CS);
     cluster_sync();
-  }
-  if (k > 0) {
-    const bool some_k = locate(s, row, V, rank, CS, r, static_cast<unsigned long long>(k) - 1, true, h0, have);
-    have = true;
-    if (rank == 0 && threadIdx.x == 0) s.pick = some_k;
-    cluster_sync();
-    const bool cut_k = peer32(at_rank(&s.pick, 0)) != 0;  // else fewer words weigh anything
-    const unsigned long long kth = peer64(at_rank(&s.found_cv, 0));
-    cluster_sync();
-    if (cut_k) {
-      sum_where(s, row, V, rank, CS, r, [&](int i, float l) { return l > -INFINITY && sort_key(l, i) <= kth; }, none);
+    return t;
+  };
+  if (total == 0) total = cut_total(~0ull, 0.0f);
+  bool have = false;  // the histogram of the whole row
+#pragma unroll 1
+  for (int step = k > 0 ? kCount : p < 1.0f ? kNucleus : kToken;;) {
+    if (step == kToken && mp > 0.0f) total = min(total, cut_total(~0ull, fminf(mp, 1.0f)));
+    const bool by_count = step == kCount;
+    const unsigned long long x = by_count ? static_cast<unsigned long long>(k) - 1 : step == kNucleus ? nucleus(p, total) : share(u, total);
+    unsigned long long base_m = 0, pre = 0;  // before the words that are left, in the first CTA
+    int base_c = 0, what = kAll, shift = 0, bin = 0;
+    auto sums = [&] { return what == kAll ? s.all_m : s.list; };  // of digits: where nothing is listed yet
+    auto counts = [&] { return what == kAll ? s.all_c : reinterpret_cast<uint32_t*>(s.list + BINS); };
+#pragma unroll 1
+    for (;;) {
+      if (have) {
+        if (rank == 0) {
+          pick_bin(s, read_bins(s, sums(), counts()), base_m, base_c, x, by_count);
+          if (s.pick >= 0) { base_m = s.pick_m; base_c = s.pick_c; }
+          if (threadIdx.x == 0) {
+            const bool fits = s.pick_n <= LIST;
+            if (what == kAll) {
+              s.cmd.bin = s.pick;
+              s.cmd.shift = fits ? 64 : 42;
+            } else {
+              s.cmd.pre = (shift + 10 < 52 ? pre >> (shift + 10) << (shift + 10) : 0) | (static_cast<unsigned long long>(s.pick) << shift);
+              s.cmd.shift = fits ? shift : shift - 10;
+            }
+            s.cmd.what = s.pick < 0 ? kNone : fits ? kGather : kDigits;
+            s.nlist = 0;
+          }
+        }
+        if (threadIdx.x == 0) s.ncand = 0;
+        cluster_sync();  // the command is written, and the first CTA's list is empty
+        what = static_cast<int>(peer32(at_rank(&s.cmd.what, 0)));
+        bin = static_cast<int>(peer32(at_rank(&s.cmd.bin, 0)));
+        shift = static_cast<int>(peer32(at_rank(&s.cmd.shift, 0)));
+        pre = peer64(at_rank(&s.cmd.pre, 0));
+        if (what == kNone) {
+          cluster_sync();  // every CTA has read the command
+          break;
+        }
+      }
+      if (what != kGather) {
+        for (int i = threadIdx.x; i < BINS; i += STH) { s.count[i] = 0; s.limb[0][i] = 0; s.limb[1][i] = 0; s.limb[2][i] = 0; }
+        __syncthreads();
+      }
+      if (what == kAll) {
+        each_word<UL>(row, V, rank, CS, [&](int, float l) {
+          int h, g;
+          r.parts(l, h, g);
+          if (!(l > -INFINITY) || !(h | g)) return;
+          const int d = r.bin(l);
+          atomicAdd(&s.count[d], 1u);
+          add_weight(s, d, static_cast<unsigned long long>((static_cast<long long>(h) << 20) + g));
+        });
+      } else {
+        each_word<UL>(row, V, rank, CS, [&](int i, float l) {
+          if (!(l > -INFINITY) || r.bin(l) != bin) return;
+          const unsigned long long cv = sort_key(l, i), w = r.units(l);
+          if (w == 0) return;
+          if (what == kGather) {
+            if (shift < 64 && (cv >> shift) != (pre >> shift)) return;
+            s.cand[min(atomicAdd(&s.ncand, 1), CAND - 1)] = cv;  // at most LIST of all the CTAs
+          } else {
+            if (shift + 10 < 52 && (cv >> (shift + 10)) != (pre >> (shift + 10))) return;
+            const int d = static_cast<int>(cv >> shift) & (BINS - 1);
+            atomicAdd(&s.count[d], 1u);
+            add_weight(s, d, w);
+          }
+        });
+      }
+      if (what == kGather) {
+        __syncthreads();
+        const int n = min(s.ncand, CAND);
+        if (threadIdx.x == 0) s.listed = peer_add(at_rank(&s.nlist, 0), n);
+        __syncthreads();
+        const uint32_t to = at_rank(s.list, 0);
+        for (int i = threadIdx.x; i < n; i += STH)
+          if (s.listed + i < LIST) peer_store64(to + 8 * (s.listed + i), s.cand[i]);
+        cluster_sync();
+        if (rank == 0) pass_in_list<X>(s, r, V, min(s.nlist, LIST), base_m, base_c, x, by_count);
+        break;
+      }
       cluster_sync();
-      total = cluster_mass(s, CS);
+      share_bins(s, sums(), counts(), rank, CS);
       cluster_sync();
+      have = true;
     }
+    if (step == kToken) break;
+    if (step == kCount) {
+      cluster_sync();
+      const unsigned long long kth = peer64(at_rank(&s.found_cv, 0));
+      cluster_sync();
+      if (what != kNone) total = cut_total(kth, 0.0f);  // else fewer words weigh anything
+    } else if (rank == 0) {
+      total = min(total, s.found_before + r.units(logit_of(s.found_cv)));
+    }
+    step = by_count && p < 1.0f ? kNucleus : kToken;
   }
-  if (p < 1.0f) {
-    locate(s, row, V, rank, CS, r, nucleus(p, total), false, h0, have);
-    have = true;
-    if (rank == 0) total = min(total, s.found_before + r.units(logit_of(s.found_cv)));
-  }
-  if (mp > 0.0f) {
-    const float least = fminf(mp, 1.0f);
-    sum_where(s, row, V, rank, CS, r, [&](int, float l) { return l > -INFINITY && r.weight(l) >= least; }, none);
-    cluster_sync();
-    total = min(total, cluster_mass(s, CS));
-    cluster_sync();
-  }
-  locate(s, row, V, rank, CS, r, share(u, total), false, h0, have);
   if (rank == 0 && threadIdx.x == 0) write_row(a, m, r, s.found_cv, total);
 }
 
@@ -739,7 +913,7 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
   if (lane == 0) s.red_f[warp] = mx;
-  if (tid == 0) { s.ncand = 0; s.done = 0; s.pick = BINS; }
+  if (tid == 0) { s.ncand = 0; s.nhit = 0; s.nlist = 0; s.done = 0; s.pick = BINS; }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < SW; ++i) mx = fmaxf(mx, s.red_f[i]);
@@ -787,23 +961,56 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
   r.lmax = mx;
 
   // ---- the words above the threshold; the row's total weight where top_k does not bound it
-  auto list = [&](int i, uint4 v) {
-    if (largest(row, v) >= cut) list_chunk(s, row, i, v, cut);
+  // Chunks with a word above it are noted, then all threads look at the noted ones: a warp would go through its few hits
+  // one by one where it found them.
+  int* hits = reinterpret_cast<int*>(s.list);
+  constexpr int HITS = 2 * LIST;
+  auto hit = [&](int i, uint4 v) {
+    const float x = largest(row, v);
+    if (x >= cut && x > -INFINITY) {
+      const int at = atomicAdd(&s.nhit, 1);
+      if (at < HITS) hits[at] = i;
+    }
   };
-  auto list_one = [&](int i, float l) {
+  if (by_top_k) {
+    // the chunks of the threads whose largest logit is above the threshold, shared out over all threads: a few loads each,
+    // where those threads alone would go through all of theirs again
+    const bool on = mine >= cut && mine > -INFINITY;
+    const int at = push_at(&s.nlist, on);
+    if (on) s.count[at] = tid;
+    __syncthreads();
+    constexpr int E = 16 / static_cast<int>(sizeof(X)), U = 4;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(X)) % E), head = off ? min(V, E - off) : 0;
+    const int chunks = (V - head) / E, step = CS * STH, n = max(s.nlist, 1), groups = STH / n, group = tid / n;
+    const uint4* body = reinterpret_cast<const uint4*>(row + head);
+    // thread h of a group takes every groups-th chunk of the h-th of those threads
+    const int from = rank * STH + static_cast<int>(s.count[tid - group * n]);
+#pragma unroll 1
+    for (int c = from + group * step; group < groups && s.nlist > 0 && c < chunks; c += U * groups * step) {
+      uint4 v[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (c + i * groups * step < chunks) v[i] = __ldg(body + c + i * groups * step);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (c + i * groups * step < chunks) hit(head + (c + i * groups * step) * E, v[i]);
+    }
+  } else if (mx < INFINITY && r.c < INFINITY) {
+    sum_all(s, row, V, rank, CS, r, hit);
+  } else {
+    sum_where(s, row, V, rank, CS, r, [&](int, float l) { return l > -INFINITY; }, hit);
+  }
+  __syncthreads();
+  const int nh = s.nhit;
+  for (int i = tid; i < min(nh, HITS); i += STH)
+    list_chunk(s, row, hits[i], __ldg(reinterpret_cast<const uint4*>(row + hits[i])), cut);
+  if (nh > HITS && tid == 0) atomicAdd(&s.ncand, CAND + 1);  // too many
+  each_chunk<0>(row, V, rank, CS, [](int, uint4) {}, [&](int i, float l) {
     if (l >= cut && l > -INFINITY) {
       const int at = atomicAdd(&s.ncand, 1);
       if (at < CAND) s.cand[at] = sort_key(l, i);
     }
-  };
-  if (by_top_k) {
-    if (mine >= cut) each_chunk<4>(row, V, rank, CS, list, list_one);
-  } else {
-    sum_where(
-        s, row, V, rank, CS, r,
-        [&](int, float l) { return l > -INFINITY; }, list);
-    each_chunk<0>(row, V, rank, CS, list, list_one);
-  }
+  });
   cluster_sync();
 
   // ---- the cuts and the choice on the listed words, in the first CTA

@@ -16,24 +16,26 @@
 //    ones a threshold with about as many words above it as the row needs
 //    (top_k of them, else 512 in all).  While the CTAs exchange their largest
 //    logits each works out its threshold.
-//  * The words above it are listed; a row without top_k sums its total weight
-//    in the same second pass (from L2), others only look again where a thread's
-//    largest logit is above the threshold.
+//  * The words above it are listed, in two steps: chunks of 16 bytes that hold
+//    one are noted, then every thread looks at a noted one (a warp that lists
+//    what few of its lanes found, where they found it, took 26 us in place of 8
+//    for top_k = 1000 in one CTA).  A row without top_k sums its total weight in
+//    the same second pass (from L2), others only look again at the chunks of the
+//    threads whose largest logit is above the threshold.
 //  * The first CTA sorts the lists and makes the cuts and the choice on the
 //    sorted words.  They are complete above the highest of the CTAs'
 //    thresholds, so what falls inside is final.
 //  * A row whose cut or token falls outside (flat distributions, large top_k)
 //    goes on with a histogram of the whole row: counts and weights in 1024 bins
 //    of the distance to the largest logit.  The words of the bin that holds an
-//    answer are listed and sorted; where a bin has more words than the list,
-//    1024 bins of the next digits of their sorting key at a time, the index
-//    being the last.
+//    answer are listed and the word picked among them; where a bin has more
+//    words than the list, 1024 bins of the next digits of their sorting key at a
+//    time, the index being the last.
 // Measured on one GB300, calls in a graph: one row of 151936 (fp32, top-k 20)
-// 12 us: 1.3 for the first pass, 4 for threshold and lists, 1 for fetching
-// them, 4 for the choice, most of it fetching code that runs once; 16 rows of
-// 262144 (nucleus and min-p) 20 us, of which 6 for the total weight; 256 bf16
-// rows of mixed settings 92 us: 52 for all of them and 40 for the one to four
-// flat ones that are left to the tail.
+// 9.6 us: 1.0 for the first pass, 3.8 for threshold and lists, 1 for fetching
+// them, 2.8 for the choice; 16 rows of 262144 (nucleus and min-p) 17.0 us, of
+// which 4.5 for the total weight; 256 bf16 rows of mixed settings 66 us: 35 for
+// all of them and 28 for the one to four flat ones that are left to the tail.
 #include "kq_cache.h"
 
 namespace kq {
@@ -60,7 +62,7 @@ struct Cmd {
 };
 
 struct Smem {
-  uint32_t count[BINS], limb[3][BINS];
+  uint32_t count[BINS], limb[2][BINS];
   unsigned long long all_m[BINS];  // the whole row's histogram, in the first CTA
   uint32_t all_c[BINS];
   unsigned long long list[LIST];
@@ -76,6 +78,8 @@ struct Smem {
   unsigned long long found_cv, found_before;  // the word at which a running sum passes, and the sum before it
   int pick, pick_c, pick_n;
   unsigned long long pick_m;
+  unsigned long long total, x, base_m;  // whole_row's: the weight kept, what the running sum has to pass, the sum before
+  int base_c;
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
@@ -118,10 +122,24 @@ __device__ __forceinline__ void each_chunk(const X* row, int V, int rank, int CS
     word(i, one(row + i));
   }
 }
-// The same, word(index, logit) for all of them.
-template <int U, class X, class F>
+// The same, word(index, logit) for all of them, one chunk at a time with the next one in flight: for long bodies, of which
+// several copies cost more to fetch than they save.
+template <class X, class F>
 __device__ __forceinline__ void each_word(const X* row, int V, int rank, int CS, F word) {
-  each_chunk<U>(row, V, rank, CS, [&](int i, uint4 v) { each4(row, v, i, word); }, word);
+  constexpr int E = 16 / static_cast<int>(sizeof(X));
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(X)) % E);
+  const int head = off ? min(V, E - off) : 0, chunks = (V - head) / E, step = CS * STH;
+  const uint4* body = reinterpret_cast<const uint4*>(row + head);
+  int c = rank * STH + static_cast<int>(threadIdx.x);
+  uint4 next;
+  if (c < chunks) next = __ldg(body + c);
+#pragma unroll 1
+  for (; c < chunks; c += step) {
+    const uint4 v = next;
+    if (c + step < chunks) next = __ldg(body + c + step);
+    each4(row, v, head + c * E, word);
+  }
+  each_chunk<0>(row, V, rank, CS, [](int, uint4) {}, word);
 }
 __device__ __forceinline__ float largest(const float*, uint4 v) {
   return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
@@ -564,13 +582,12 @@ struct Bins {
   unsigned long long m[2], pm;
   int c[2], pc;
 };
-// Weights are up to 2^40: three sums of 14 bits each, of at most 2^18 words.
+// A bin's weight in two words; the higher one is added to where the lower one passes 2^32 or the weight does, which is
+// seldom in the rows that come here.
 __device__ __forceinline__ void add_weight(Smem& s, int d, unsigned long long w) {
-  const uint32_t l0 = static_cast<uint32_t>(w) & 0x3FFFu, l1 = static_cast<uint32_t>(w >> 14) & 0x3FFFu,
-                 l2 = static_cast<uint32_t>(w >> 28);
-  if (l0) atomicAdd(&s.limb[0][d], l0);
-  if (l1) atomicAdd(&s.limb[1][d], l1);
-  if (l2) atomicAdd(&s.limb[2][d], l2);
+  const uint32_t lo = static_cast<uint32_t>(w), before = atomicAdd(&s.limb[0][d], lo);
+  const uint32_t hi = static_cast<uint32_t>(w >> 32) + (before + lo < before);
+  if (hi) atomicAdd(&s.limb[1][d], hi);
 }
 // The sum of the cluster's histograms, into the first CTA's `to` (weights) and `to_n` (words).  Each CTA sums its share of the bins: one that
 // read all of them from the others (128 KB) took 8 us.
@@ -584,9 +601,7 @@ __device__ __forceinline__ void share_bins(Smem& s, unsigned long long* to, uint
       const int q = i / share * 2 + k;
       if (q < CS) {
         c += peer32(at_rank(&s.count[b], q));
-        m += static_cast<unsigned long long>(peer32(at_rank(&s.limb[0][b], q))) +
-             (static_cast<unsigned long long>(peer32(at_rank(&s.limb[1][b], q))) << 14) +
-             (static_cast<unsigned long long>(peer32(at_rank(&s.limb[2][b], q))) << 28);
+        m += peer32(at_rank(&s.limb[0][b], q)) + (static_cast<unsigned long long>(peer32(at_rank(&s.limb[1][b], q))) << 32);
       }
     }
     s.cand[i] = m;
@@ -729,6 +744,20 @@ __device__ __forceinline__ void pass_in_list(Smem& s, const Row r, int V, int n,
   }
   __syncthreads();
 }
+// A row's settings: temperature not above 0 is the first word; k = 0: no top_k.
+__device__ __forceinline__ void settings(const SampleArgs& a, int m, float& temp, int& k, float& p, float& mp, float& u) {
+  temp = a.temperature ? __ldg(a.temperature + m) : 1.0f;
+  k = a.top_k ? __ldg(a.top_k + m) : 0;
+  p = a.top_p ? __ldg(a.top_p + m) : 1.0f;
+  mp = a.min_p ? __ldg(a.min_p + m) : 0.0f;
+  u = __ldg(a.u + m);
+  if (!(temp > 0.0f)) {
+    temp = 1.0f;
+    k = 1;
+  }
+  if (k < 0 || k >= a.V) k = 0;
+}
+
 // The weight of the words down to the one with the key `last` that weigh at least `least`, every CTA of the cluster.
 template <class X>
 __device__ __noinline__ void sum_cut(Smem& s, const X* row, int V, int rank, int CS, const Row r, unsigned long long last,
@@ -745,9 +774,8 @@ __device__ __noinline__ void sum_cut(Smem& s, const X* row, int V, int rank, int
 // cluster's barriers is in registers or shared memory: each of them empties the cache that local memory is read through.
 template <class X>
 __device__ __noinline__ void whole_row(Smem& s, const SampleArgs& a, const X* row, int m, int rank, int CS, const Row r_in,
-                                       unsigned long long total, int k, float p, float mp, float u) {
+                                       unsigned long long total) {
   const Row r = r_in;  // a copy that no store can change
-  constexpr int UL = 1;
   enum : int { kCount, kNucleus, kToken };
   const int V = a.V;
   auto cut_total = [&](unsigned long long last, float least) {
@@ -758,23 +786,39 @@ __device__ __noinline__ void whole_row(Smem& s, const SampleArgs& a, const X* ro
     return t;
   };
   if (total == 0) total = cut_total(~0ull, 0.0f);
+  if (threadIdx.x == 0) s.total = total;
   bool have = false;  // the histogram of the whole row
+  int step = -1;      // the one before
 #pragma unroll 1
-  for (int step = k > 0 ? kCount : p < 1.0f ? kNucleus : kToken;;) {
-    if (step == kToken && mp > 0.0f) total = min(total, cut_total(~0ull, fminf(mp, 1.0f)));
+  do {
+    {
+      float temp, p, mp, u;
+      int k;
+      settings(a, m, temp, k, p, mp, u);
+      step = step < kCount && k > 0 ? kCount : step < kNucleus && p < 1.0f ? kNucleus : kToken;
+      unsigned long long t = ~0ull;
+      if (step == kToken && mp > 0.0f) t = cut_total(~0ull, fminf(mp, 1.0f));
+      if (threadIdx.x == 0) {
+        t = min(t, s.total);
+        s.total = t;
+        s.x = step == kCount ? static_cast<unsigned long long>(k) - 1 : step == kNucleus ? nucleus(p, t) : share(u, t);
+        s.base_m = 0;
+        s.base_c = 0;
+      }
+      __syncthreads();
+    }
     const bool by_count = step == kCount;
-    const unsigned long long x = by_count ? static_cast<unsigned long long>(k) - 1 : step == kNucleus ? nucleus(p, total) : share(u, total);
-    unsigned long long base_m = 0, pre = 0;  // before the words that are left, in the first CTA
-    int base_c = 0, what = kAll, shift = 0, bin = 0;
+    unsigned long long pre = 0;
+    int what = kAll, shift = 0, bin = 0;
     auto sums = [&] { return what == kAll ? s.all_m : s.list; };  // of digits: where nothing is listed yet
     auto counts = [&] { return what == kAll ? s.all_c : reinterpret_cast<uint32_t*>(s.list + BINS); };
 #pragma unroll 1
     for (;;) {
       if (have) {
         if (rank == 0) {
-          pick_bin(s, read_bins(s, sums(), counts()), base_m, base_c, x, by_count);
-          if (s.pick >= 0) { base_m = s.pick_m; base_c = s.pick_c; }
+          pick_bin(s, read_bins(s, sums(), counts()), s.base_m, s.base_c, s.x, by_count);
           if (threadIdx.x == 0) {
+            if (s.pick >= 0) { s.base_m = s.pick_m; s.base_c = s.pick_c; }
             const bool fits = s.pick_n <= LIST;
             if (what == kAll) {
               s.cmd.bin = s.pick;
@@ -799,20 +843,19 @@ __device__ __noinline__ void whole_row(Smem& s, const SampleArgs& a, const X* ro
         }
       }
       if (what != kGather) {
-        for (int i = threadIdx.x; i < BINS; i += STH) { s.count[i] = 0; s.limb[0][i] = 0; s.limb[1][i] = 0; s.limb[2][i] = 0; }
+        for (int i = threadIdx.x; i < BINS; i += STH) { s.count[i] = 0; s.limb[0][i] = 0; s.limb[1][i] = 0; }
         __syncthreads();
       }
       if (what == kAll) {
-        each_word<UL>(row, V, rank, CS, [&](int, float l) {
-          int h, g;
-          r.parts(l, h, g);
-          if (!(l > -INFINITY) || !(h | g)) return;
+        each_word(row, V, rank, CS, [&](int, float l) {
+          const unsigned long long w = r.units(l);
+          if (!(l > -INFINITY) || w == 0) return;
           const int d = r.bin(l);
           atomicAdd(&s.count[d], 1u);
-          add_weight(s, d, static_cast<unsigned long long>((static_cast<long long>(h) << 20) + g));
+          add_weight(s, d, w);
         });
       } else {
-        each_word<UL>(row, V, rank, CS, [&](int i, float l) {
+        each_word(row, V, rank, CS, [&](int i, float l) {
           if (!(l > -INFINITY) || r.bin(l) != bin) return;
           const unsigned long long cv = sort_key(l, i), w = r.units(l);
           if (w == 0) return;
@@ -836,7 +879,7 @@ __device__ __noinline__ void whole_row(Smem& s, const SampleArgs& a, const X* ro
         for (int i = threadIdx.x; i < n; i += STH)
           if (s.listed + i < LIST) peer_store64(to + 8 * (s.listed + i), s.cand[i]);
         cluster_sync();
-        if (rank == 0) pass_in_list<X>(s, r, V, min(s.nlist, LIST), base_m, base_c, x, by_count);
+        if (rank == 0) pass_in_list<X>(s, r, V, min(s.nlist, LIST), s.base_m, s.base_c, s.x, by_count);
         break;
       }
       cluster_sync();
@@ -844,33 +887,21 @@ __device__ __noinline__ void whole_row(Smem& s, const SampleArgs& a, const X* ro
       cluster_sync();
       have = true;
     }
-    if (step == kToken) break;
-    if (step == kCount) {
+    if (by_count) {
       cluster_sync();
       const unsigned long long kth = peer64(at_rank(&s.found_cv, 0));
       cluster_sync();
-      if (what != kNone) total = cut_total(kth, 0.0f);  // else fewer words weigh anything
-    } else if (rank == 0) {
-      total = min(total, s.found_before + r.units(logit_of(s.found_cv)));
+      if (what != kNone) {  // else fewer words weigh anything
+        const unsigned long long t = cut_total(kth, 0.0f);
+        if (threadIdx.x == 0) s.total = t;
+      }
+    } else if (step == kNucleus && rank == 0 && threadIdx.x == 0) {
+      s.total = min(s.total, s.found_before + r.units(logit_of(s.found_cv)));
     }
-    step = by_count && p < 1.0f ? kNucleus : kToken;
-  }
-  if (rank == 0 && threadIdx.x == 0) write_row(a, m, r, s.found_cv, total);
+  } while (step != kToken);
+  if (rank == 0 && threadIdx.x == 0) write_row(a, m, r, s.found_cv, s.total);
 }
 
-// A row's settings: temperature not above 0 is the first word; k = 0: no top_k.
-__device__ __forceinline__ void settings(const SampleArgs& a, int m, float& temp, int& k, float& p, float& mp, float& u) {
-  temp = a.temperature ? __ldg(a.temperature + m) : 1.0f;
-  k = a.top_k ? __ldg(a.top_k + m) : 0;
-  p = a.top_p ? __ldg(a.top_p + m) : 1.0f;
-  mp = a.min_p ? __ldg(a.min_p + m) : 0.0f;
-  u = __ldg(a.u + m);
-  if (!(temp > 0.0f)) {
-    temp = 1.0f;
-    k = 1;
-  }
-  if (k < 0 || k >= a.V) k = 0;
-}
 __device__ __forceinline__ Row row_of(float lmax, float temp) {
   Row r;
   r.lmax = lmax;
@@ -1114,7 +1145,7 @@ __global__ void __launch_bounds__(STH, 2) sample_kernel(const __grid_constant__ 
     if (rank == 0 && tid == 0) tail.rows[atomicAdd(tail.count, 1)] = Left{m, r.lmax, sum};
     return;
   }
-  whole_row(s, a, row, m, rank, CS, r, by_top_k ? 0 : cluster_mass(s, CS), k, p, mp, u);
+  whole_row(s, a, row, m, rank, CS, r, by_top_k ? 0 : cluster_mass(s, CS));
 }
 
 // The rows that sample_kernel left, by clusters of eight CTAs in turn; the last CTA to leave clears the count.
@@ -1133,7 +1164,7 @@ __global__ void __launch_bounds__(STH, 2) tail_kernel(const __grid_constant__ Sa
     float temp, p, mp, u;
     int k;
     settings(a, m, temp, k, p, mp, u);
-    whole_row(s, a, row, m, rank, 8, row_of(todo.lmax, temp), todo.total, k, p, mp, u);
+    whole_row(s, a, row, m, rank, 8, row_of(todo.lmax, temp), todo.total);
     cluster_sync();
   }
   if (tid == 0) {
@@ -1163,11 +1194,10 @@ cudaError_t launch_x(const SampleArgs& a, cudaStream_t st) {
     set = true;
   }
   // CTAs per row: as many as the device holds at once, two per SM, with at least 4096 words
-  // each, and at most 2^18, the histograms' room.
+  // each.
   const int sms = num_sms();
   int CS = 1;
   while (CS < 8 && static_cast<int64_t>(a.M) * CS * 2 <= 2 * sms && a.V / (CS * 2) >= 4096) CS *= 2;
-  while (CS < 8 && a.V / CS > (1 << 18)) CS *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.M) * CS);
   cfg.blockDim = dim3(STH);
@@ -1193,7 +1223,7 @@ cudaError_t launch_x(const SampleArgs& a, cudaStream_t st) {
   }
   cudaError_t e = cudaLaunchKernelEx(&cfg, sample_kernel<X>, a, CS, tail);
   if (e == cudaSuccess && second) {
-    cfg.gridDim = dim3(sms / 8 * 8 > 0 ? sms / 8 * 8 : 8);
+    cfg.gridDim = dim3(2 * sms / 8 * 8);
     attr[1].val.clusterDim.x = 8;
     e = cudaLaunchKernelEx(&cfg, tail_kernel<X>, a, tail);
   }

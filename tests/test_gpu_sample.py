@@ -259,3 +259,23 @@ def test_sample_many_rows_some_flat(dtype):
 def test_sample_large_vocabularies(V):
     x = logits(3, V, 11)
     check(x, [1.0, 2.5, 0.8], [0, 0, 50], [("mid", 12), 1.0, ("mid", 20)], [0.0, 0.0, 0.0], [9, 300, 5])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M", [6, 320])
+def test_sample_total_weight_of_odd_rows(dtype, M):
+    """Rows without top_k, whose every word is summed: NaN, infinities, a temperature below fp32's normal numbers, one
+    logit above a flat rest, at row starts off 16 bytes."""
+    V, inf = 40003, float("inf")
+    base = torch.randn((6, V), generator=torch.Generator().manual_seed(12))
+    base[0, ::3] = float("nan")
+    base[1, [7, 39000]] = inf
+    base[2, 5:] = -inf
+    base[3, [11, 20000, 40002]] = 9.0
+    base[4, :] = -3.0
+    base[4, 33333] = 4.0
+    x = base.to(dtype).cuda().repeat(M // 6 + 1, 1)[:M]
+    check(x, [[1.5, 1.0, 0.7, 1e-39, 1.0, 3.0][m % 6] for m in range(M)], [0] * M,
+          [[1.0, 1.0, ("mid", 3), 1.0, ("mid", 20000), 1.0][m % 6] for m in range(M)],
+          [[0.0, 0.0, 0.0, 0.0, 0.0, 0.02][m % 6] for m in range(M)],
+          [[9000, 1, 2, 2, [0, 15000][m // 6 % 2], 700][m % 6] for m in range(M)])

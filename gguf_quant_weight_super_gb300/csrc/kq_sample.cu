@@ -18,7 +18,7 @@
 //    logits each works out its threshold.
 //  * The words above it are listed, in two steps: chunks of 16 bytes that hold
 //    one are noted, then every thread looks at a noted one (a warp that lists
-//    what few of its lanes found, where they found it, took 26 us in place of 8
+//    what few of its lanes found, where they found it, took 27 us in place of 13
 //    for top_k = 1000 in one CTA).  A row without top_k sums its total weight in
 //    the same second pass (from L2), others only look again at the chunks of the
 //    threads whose largest logit is above the threshold.
@@ -406,8 +406,9 @@ __device__ __forceinline__ int push_at(int* counter, bool on) {
   return __shfl_sync(0xFFFFFFFFu, base, 0) + __popc(who & ((1u << lane) - 1u));
 }
 
-// The cuts and the choice on n <= FEW listed words, by one warp, two words per lane.  total: the row's weight where k is 0.  Returns whether the answer lies in the list; then cv_out and the kept weight in `total`.
-// Runs once per row: loops stay rolled, since what it costs is fetching its code.
+// The cuts and the choice on n <= FEW listed words, by one warp, two words per lane.  total: the row's weight where k is 0.
+// Returns whether the answer lies in the list; then the word in cv_out and the kept weight in total.  Runs once per row:
+// loops stay rolled, since what it costs is fetching its code.
 __device__ __noinline__ bool choose_in_warp(const unsigned long long* list, bool sorted, const Row r, int n, bool complete, int k,
                                             float p, float mp, float u, unsigned long long& total, unsigned long long& cv_out) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -589,8 +590,8 @@ __device__ __forceinline__ void add_weight(Smem& s, int d, unsigned long long w)
   const uint32_t hi = static_cast<uint32_t>(w >> 32) + (before + lo < before);
   if (hi) atomicAdd(&s.limb[1][d], hi);
 }
-// The sum of the cluster's histograms, into the first CTA's `to` (weights) and `to_n` (words).  Each CTA sums its share of the bins: one that
-// read all of them from the others (128 KB) took 8 us.
+// The sum of the cluster's histograms, into the first CTA's `to` (weights) and `to_n` (words).  Each CTA sums its share of
+// the bins: one that read all of them from the others (128 KB) took 8 us.
 __device__ __forceinline__ void share_bins(Smem& s, unsigned long long* to, uint32_t* to_n, int rank, int CS) {
   const int share = BINS / CS, each = max(1, CS / 2);  // CTAs are read by `each` groups of threads
   for (int i = threadIdx.x; i < share * each; i += STH) {

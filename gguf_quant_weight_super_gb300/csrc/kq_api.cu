@@ -422,7 +422,7 @@ static kq_status check_attn(const kq_kv_cache* cache, int64_t B, int64_t T, int3
 
 size_t kq_attn_workspace_size(const kq_kv_cache* cache, int64_t B, int64_t T, int32_t n_q_heads) {
   if (check_attn(cache, B, T, n_q_heads) != KQ_OK) return 0;
-  return attn_workspace_bytes(cache->head_dim, cache->n_kv_heads, B, T, n_q_heads);
+  return attn_workspace_bytes(cache->head_dim, cache->n_kv_heads, T, n_q_heads);
 }
 
 kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
@@ -439,7 +439,7 @@ kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, in
       !stride16(q_stride, q_dtype == KQ_BF16 ? 2 : 4))
     return KQ_ERR_ALIGN;
   if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < attn_workspace_bytes(cache->head_dim, cache->n_kv_heads, B, T, n_q_heads))
+      workspace_bytes < attn_workspace_bytes(cache->head_dim, cache->n_kv_heads, T, n_q_heads))
     return KQ_ERR_WORKSPACE;
   AttnArgs a;
   a.c = *cache;

@@ -19,15 +19,17 @@ struct Layout {
   int rows, RT;
   size_t count_off, ml_off, part_off, bytes;
 };
-Layout layout(int head_dim, int Hkv, int64_t B, int64_t T, int Hq, bool to_wide) {
+Layout layout(int head_dim, int Hkv, int64_t T, int Hq, bool to_wide) {
   Layout L;
   const int R = static_cast<int>(T) * (Hq / Hkv);
   L.rows = to_wide ? kWideRows : rows_per_pass(head_dim, R);
   L.RT = R > 0 ? (R + L.rows - 1) / L.rows : 1;
   const size_t slots = 2 * static_cast<size_t>(num_sms()) * (to_wide ? 1 : 3);  // two parts per CTA, at most three CTAs per SM
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  // The counters, which have to be zero when a call begins, lie where no call writes anything else: one per range of the
+  // most that any call cuts, whatever its sizes.  Parts are written before they are read.
   L.count_off = 0;
-  L.ml_off = up(static_cast<size_t>(B) * Hkv * L.RT * sizeof(int));
+  L.ml_off = up(3 * static_cast<size_t>(num_sms()) * sizeof(int));
   L.part_off = L.ml_off + up(slots * L.rows * 2 * sizeof(float));
   L.bytes = L.part_off + up(slots * L.rows * head_dim * sizeof(float));
   return L;
@@ -35,16 +37,16 @@ Layout layout(int head_dim, int Hkv, int64_t B, int64_t T, int Hq, bool to_wide)
 
 }  // namespace
 
-size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t B, int64_t T, int Hq) {
-  const size_t n = layout(head_dim, Hkv, B, T, Hq, false).bytes;
+size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq) {
+  const size_t n = layout(head_dim, Hkv, T, Hq, false).bytes;
   if (!wide(head_dim, static_cast<int>(T) * (Hq / Hkv))) return n;
-  const size_t m = layout(head_dim, Hkv, B, T, Hq, true).bytes;  // the size does not depend on the queries' type
+  const size_t m = layout(head_dim, Hkv, T, Hq, true).bytes;  // the size does not depend on the queries' type
   return n > m ? n : m;
 }
 
 cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st) {
   const bool to_wide = q_bf16 && a.c.dtype == KQ_BF16 && wide(a.c.head_dim, a.T * a.G);
-  const Layout L = layout(a.c.head_dim, a.c.n_kv_heads, a.B, a.T, a.Hq, to_wide);
+  const Layout L = layout(a.c.head_dim, a.c.n_kv_heads, a.T, a.Hq, to_wide);
   // the line of tiles is counted in 31 bits
   const int64_t tiles = ((a.max_pages << a.page_shift) + TK - 1) / TK + 8;  // 8: more than an item's start counts
   if (tiles * a.B > INT32_MAX / (a.c.n_kv_heads * L.RT)) return cudaErrorNotSupported;

@@ -94,7 +94,7 @@ struct Params {
   int RT;          // row tiles per (sequence, head)
   float* part;     // [2 * grid][ROWS][D] sums, then [2 * grid][ROWS][2] maximum and weight sum
   float* part_ml;
-  int* count;      // [items] arrivals
+  int* count;      // [grid] arrivals at the split item whose first tile a range holds
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -671,7 +671,7 @@ __device__ __forceinline__ void join_parts(const Params& p, const Line& line, co
   sync();
   if (tid == 0) {
     __threadfence();  // after the barrier: orders the whole block's stores before the arrival
-    int* cnt = p.count + (it.b * line.HR + it.hr);
+    int* cnt = p.count + ca;  // no two split items begin in one range: the first one goes on past its end
     *s_last = atomicAdd(cnt, 1) == parts - 1;
     if (*s_last) *cnt = 0;
   }

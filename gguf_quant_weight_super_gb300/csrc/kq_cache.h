@@ -51,7 +51,7 @@ struct AttnArgs {
   void* ws;
   int* err;
 };
-size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t B, int64_t T, int Hq);
+size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq);
 cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st);
 
 struct SampleArgs {

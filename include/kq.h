@@ -495,8 +495,10 @@ kq_status kq_kv_append(const kq_kv_cache *cache, const int32_t *page_table, int6
  * identical outputs.
  * workspace: kq_attn_workspace_size bytes, 256-byte aligned, zero-filled once
  * before first use (its counters are zero again after every call); one call at
- * a time per workspace.  q and out 16-byte aligned, q_stride a multiple of 16
- * bytes.  B <= 4096, and B * n_kv_heads * ceil(T * n_q_heads / n_kv_heads / 8)
+ * a time per workspace.  The size depends on neither B nor q's type, and a
+ * workspace serves any calls that it is large enough for, in any order.
+ * q and out 16-byte aligned, q_stride a multiple of 16 bytes.
+ * B <= 4096, and B * n_kv_heads * ceil(T * n_q_heads / n_kv_heads / 8)
  * * (max_pages * page_size / 64 + 8) < 2^31 (else KQ_ERR_UNSUPPORTED).
  */
 size_t kq_attn_workspace_size(const kq_kv_cache *cache, int64_t B, int64_t T, int32_t n_q_heads);

@@ -34,7 +34,10 @@
 // weights 2^(..) as two parts (2^-17) for bf16 q and three for fp32 q.  e4m3
 // cache: its values are fp16 values, so fp16 instructions serve; q is scaled
 // by a power of two per row into fp16's range (bf16: one part; fp32: two, 22
-// bits), weights are two parts.  Accumulation is fp32; the matrix instructions
+// bits), weights are two parts of 2^15 times their value (the sums of weights
+// likewise), which are exact to 2^-22 of a weight or to 2^-40 of the row's
+// largest one: fp16 ends at 2^-24, and the many small weights beside a peak
+// would vanish without the factor.  Accumulation is fp32; the matrix instructions
 // cut what they add to an accumulator instead of rounding it, which over the
 // hundreds of steps of a long range grows to 2^-16, so with fp32 q each step's
 // product is added by rounding fp32 additions.
@@ -71,6 +74,7 @@ struct Cfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int NQ = F8 ? (QF32 ? 2 : 1) : (QF32 ? 3 : 1);  // parts of q
   static constexpr int NP = F8 ? 2 : (QF32 ? 3 : 2);               // parts of the weights
+  static constexpr float LIFT = 32768.0f;                          // of fp16 weights, which reach 65504
   static constexpr int RB = D * static_cast<int>(sizeof(C)) + 16;  // bytes of a cache row in shared memory
   static constexpr int SUB = WT * RB, STAGE = 2 * SUB;
   static constexpr int QB = 2 * D + 16;  // bytes of a q row in shared memory
@@ -343,6 +347,10 @@ struct Warp {
         const float mm = m[n][e] == -INFINITY ? 0.0f : m[n][e];  // nothing seen yet: the weights are 0
         s[n][e] = ex2(s[n][e] - mm);
         s[n][2 + e] = ex2(s[n][2 + e] - mm);
+        if constexpr (K::F8) {
+          s[n][e] *= K::LIFT;
+          s[n][2 + e] *= K::LIFT;
+        }
         l[n][e] += s[n][e] + s[n][2 + e];
       }
     }

@@ -1,11 +1,12 @@
 """kq_kv_append, kq_attn_decode and kq_sample where calls meet: one workspace for many calls, tensors on other streams, and
 arguments at the ends of their types.  The 64-bit definitions and the bounds are test_gpu_cache.py's."""
+import numpy as np
 import pytest
 import torch
 
 from gguf_quant_weight_super_gb300 import kq
 from tests.gpu_util import require_gpu
-from tests.test_gpu_cache import BF16, F8, F32, Paged, rand_q
+from tests.test_gpu_cache import BF16, F8, F32, Paged, f64, rand_q
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,36 @@ def test_attn_one_workspace_for_any_calls():
         kq.attn_decode(P.cache, P.table, P.seq_lens, q, shared, out=got)
         torch.cuda.synchronize()
         assert torch.equal(got, want), call
+
+
+@pytest.mark.parametrize("qt", [BF16, F32])
+@pytest.mark.parametrize("D,T,G", [(64, 1, 1), (128, 1, 8), (128, 8, 4), (256, 1, 2), (256, 3, 4)])
+@pytest.mark.parametrize("n,B", [(200, 1), (3000, 1), (300, 600)])
+def test_attn_8bit_small_weights_beside_a_peak(qt, D, T, G, n, B):
+    """One score 16 to 18.5 above the rest, its value 0: the result is made of weights below 2^-23 of the largest.  The
+    bound of test_gpu_cache.py, and 2^-40 of the largest weight for each position: 2^15 times a weight enters as two fp16
+    parts, whose steps end at 2^-24."""
+    P = Paged([n], 1, D, 64, F8, seed=D + n)
+    g = torch.Generator().manual_seed(n)
+    k, v = torch.zeros(P.k.shape), torch.zeros(P.v.shape)
+    k[..., 0] = 1.5 + 2.5 * torch.rand(P.k.shape[:-1], generator=g)
+    v[:] = 0.5 + torch.rand(P.v.shape, generator=g)
+    first = int(P.table[0, 0])
+    k[first, 0, :, 0], v[first, 0] = 20.0, 0.0
+    P.k.copy_((k / P.k_scale).to(F8)), P.v.copy_((v / P.v_scale).to(F8))
+    q = torch.zeros((B, T, G, D), dtype=qt, device="cuda")
+    q[..., 0] = 1.0
+    table, lens = P.table.expand(B, -1).contiguous(), P.seq_lens.expand(B).contiguous()  # all read the same pages
+    out = kq.attn_decode(P.cache, table, lens, q, kq.attn_workspace(P.cache, B, T, G), scale=1.0)
+    torch.cuda.synchronize()
+    kk, vv = (x[:, 0] for x in P.dense(0))
+    for t in range(T):
+        m = n - T + t + 1
+        s = kk[:m, 0]
+        p = np.exp(s - s.max())
+        ref, sv, lost = p @ vv[:m] / p.sum(), p @ np.abs(vv[:m]) / p.sum(), 2.0 ** -40 * np.abs(vv[:m]).sum(0) / p.sum()
+        part, rnd = (2.0 ** -16, 2.0 ** -8) if qt == BF16 else (2.0 ** -20, 2.0 ** -24)
+        d = 2 * (D + 8) * 2.0 ** -23 * np.abs(kk[:m]).max() + 2.0 ** -20 + part + (n / 8 + 128) * 2.0 ** -23
+        tol = (d * sv + lost) * (1 + rnd) + rnd * np.abs(ref)
+        err = np.abs(f64(out.float())[:, t] - ref)
+        assert np.all(err <= tol), float((err / tol).max())

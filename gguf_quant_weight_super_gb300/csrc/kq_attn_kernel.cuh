@@ -594,10 +594,9 @@ __device__ __forceinline__ void stage_q(const Params& p, uint8_t* qsm, float* rs
 // A sequence's length as its table allows, and the first position that some of its tokens sees.
 __device__ __forceinline__ int length_of(const AttnArgs& a, int b, bool tell) {
   const int n = __ldg(a.seq_lens + b);
-  const int64_t room = a.max_pages << a.page_shift;
-  if (n > room) {
+  if (n > a.room) {
     if (tell) record_error(a.err, DEV_ERR_PAGE);
-    return static_cast<int>(room);
+    return a.room;
   }
   return max(n, 0);
 }

@@ -48,9 +48,12 @@ struct AttnArgs {
   int window;
   int B, T, Hq, G;
   int page_shift;
+  int room;  // positions that a sequence can have
   void* ws;
   int* err;
 };
+// Positions are counted in 32 bits, tiles and copies ahead of the last one included.
+constexpr int64_t kMaxPositions = INT32_MAX - 4095;
 size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq);
 cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st);
 

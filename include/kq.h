@@ -418,9 +418,9 @@ kq_status kq_moe_ffn(const kq_moe_ffn_weights *w, const int32_t *expert_ids, con
  * sequences' lengths, the T newest tokens included, so token t of the T is at
  * position seq_lens[b] - T + t; where that is negative the token is padding.
  * Table entries past a sequence's length are not read.  A length past the
- * table (max_pages*page_size) and a page id outside [0, n_pages) never fault:
- * they are recorded in the device error word (kq_device_error), and what that
- * sequence gets is unspecified.
+ * table (max_pages*page_size, for attention at most 2^31 - 4096 positions) and a
+ * page id outside [0, n_pages) never fault: they are recorded in the device error
+ * word (kq_device_error), and what that sequence gets is unspecified.
  */
 typedef struct kq_kv_cache {
   int32_t dtype;

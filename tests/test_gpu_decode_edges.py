@@ -78,3 +78,25 @@ def test_attn_8bit_small_weights_beside_a_peak(qt, D, T, G, n, B):
         tol = (d * sv + lost) * (1 + rnd) + rnd * np.abs(ref)
         err = np.abs(f64(out.float())[:, t] - ref)
         assert np.all(err <= tol), float((err / tol).max())
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (16, 4)])
+def test_attn_longest_lengths(T, G):
+    """Lengths at the end of 32 bits, all pages of a sequence being one: the last positions as at length 2048, and a
+    length past the limit is recorded and keeps the other sequence as it is."""
+    P = Paged([1024, 500], 1, 64, 1024, BF16, seed=50)
+    q = rand_q(2, T, G, 64, BF16, 51)
+    ws = kq.attn_workspace(P.cache, 2, T, G)
+    table = P.table[:, :1].expand(2, 1 << 21).contiguous()
+
+    def call(n):
+        lens = torch.tensor([n, 500], dtype=torch.int32, device="cuda")
+        out = kq.attn_decode(P.cache, table, lens, q, ws, window=100)
+        torch.cuda.synchronize()
+        return out
+
+    want = call(2048)
+    assert torch.equal(call(2 ** 31 - 4096), want) and kq.kq_device_error() == 0
+    got = call(2 ** 31 - 1)
+    assert kq.kq_device_error(clear=True) == 4
+    assert torch.equal(got[1], want[1])

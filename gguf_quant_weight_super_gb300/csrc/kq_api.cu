@@ -451,13 +451,13 @@ kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, in
   a.out = out;
   a.scale = scale;
   a.softcap = softcap;
-  a.window = window;
   a.B = static_cast<int>(B);
   a.T = static_cast<int>(T);
   a.Hq = n_q_heads;
   a.G = n_q_heads / cache->n_kv_heads;
   a.page_shift = log2_of(cache->page_size);
   a.room = static_cast<int>(min_i64(max_pages << a.page_shift, kMaxPositions));
+  a.window = window < a.room ? window : 0;  // a window of all positions cuts nothing; position - window stays in 32 bits
   a.ws = workspace;
   a.err = device_error_ptr();
   cudaError_t e = launch_attn(a, q_dtype == KQ_BF16, reinterpret_cast<cudaStream_t>(stream));

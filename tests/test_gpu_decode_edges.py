@@ -100,3 +100,18 @@ def test_attn_longest_lengths(T, G):
     got = call(2 ** 31 - 1)
     assert kq.kq_device_error(clear=True) == 4
     assert torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("T,G,Hkv", [(8, 4, 2), (16, 4, 2), (16, 1, 32), (3, 2, 1)])
+def test_attn_largest_windows_are_none(T, G, Hkv):
+    """Windows of the table's positions and more, up to the largest, cut nothing, beside padding tokens too."""
+    P = Paged([1, 500, 1, 1, 37], Hkv, 64, 16, BF16, seed=52)
+    q = rand_q(5, T, G * Hkv, 64, BF16, 53)
+    ws = kq.attn_workspace(P.cache, 5, T, G * Hkv)
+    want = kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws)
+    room = P.table.shape[1] * 16
+    for window in (2 ** 31 - 1, 2 ** 31 - 8, 1 << 30, room + 1, room, room - 1):
+        out = torch.full_like(q, float("nan"))
+        kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws, window=window, out=out)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), window

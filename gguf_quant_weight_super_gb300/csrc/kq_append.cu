@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ App
       x1[i] = load4(src + e1);
     }
   }
-  const int pos = __ldg(a.seq_lens + b) - a.T + t;
+  const int pos = max(__ldg(a.seq_lens + b), 0) - a.T + t;  // below 0, whatever the length: all padding
   bool ok = pos >= 0;
   if (ok && rot > 0 && pos >= a.rope.n_positions) {
     if (l == 0) record_error(a.err, DEV_ERR_POSITION);

@@ -115,3 +115,17 @@ def test_attn_largest_windows_are_none(T, G, Hkv):
         kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws, window=window, out=out)
         torch.cuda.synchronize()
         assert torch.equal(out, want), window
+
+
+@pytest.mark.parametrize("rot", [0, 64])
+def test_append_negative_lengths_are_padding(rot):
+    """A length below 0, down to the lowest, is a sequence of padding tokens: zeros out, nothing stored, no error."""
+    P = Paged([0, 9, 0], 2, 64, 16, BF16, seed=54, fill="zero")
+    lens = torch.tensor([-2 ** 31, 9, -1], dtype=torch.int32, device="cuda")
+    q, kv = rand_q(3, 3, 4, 64, BF16, 55), rand_q(3, 3, 2, 64, BF16, 56)
+    out = kq.kv_append(P.cache, P.table, lens, q, kv, kv, kq.RopeNorm(kq.rope_table(20, 64)) if rot else kq.RopeNorm())
+    torch.cuda.synchronize()
+    assert kq.kq_device_error(clear=True) == 0
+    assert torch.all(out[0] == 0) and torch.all(out[1] != 0) and torch.all(out[2] == 0)
+    stored = (P.k.nan_to_num(0.0) != 0).any(-1).any(-1)
+    assert int(stored.sum()) == 3 and torch.all(stored[int(P.table[1, 0]), 6:9])

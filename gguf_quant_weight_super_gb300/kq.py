@@ -4,6 +4,9 @@ Every function named ``kq_*`` here calls the C function of the same name with
 the device pointers of the given torch tensors and the current CUDA stream;
 all computation happens in libkq's CUDA kernels.  There is no fallback: if
 libkq.so is missing or fails to load, importing the library raises.
+``stream`` (a torch stream or a handle) in place of the current one: the caller
+orders and keeps the tensors it passes; those that the call makes itself are
+made on that stream.
 """
 from __future__ import annotations
 
@@ -148,6 +151,17 @@ def _stream(stream):
     return int(stream)
 
 
+def _new(stream, make, *args, **kw):
+    """make(...), a tensor of the call's own: made on the stream that the call runs on, so that its memory is neither written
+    by earlier work of another stream nor handed on while the call's kernels use it."""
+    if stream is None:
+        return make(*args, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _check(fn: str, status: int):
     if status != KQ_OK:
         raise KQError(fn, status)
@@ -176,8 +190,8 @@ def kq_moe_route(logits, M, n_experts, top_k, expert_ids, gate_w, workspace=None
 def moe_route(logits: torch.Tensor, top_k: int, workspace=None, stream=None):
     """(ids int32 [M, top_k], gate fp32 [M, top_k]) for logits [M, n_experts] (kq_moe_route)."""
     M, E = logits.shape
-    ids = torch.empty((M, top_k), dtype=torch.int32, device=logits.device)
-    gate = torch.empty((M, top_k), dtype=torch.float32, device=logits.device)
+    ids = _new(stream, torch.empty, (M, top_k), dtype=torch.int32, device=logits.device)
+    gate = _new(stream, torch.empty, (M, top_k), dtype=torch.float32, device=logits.device)
     kq_moe_route(logits, M, E, top_k, ids, gate, workspace, stream)
     return ids, gate
 
@@ -544,7 +558,7 @@ def kv_append(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, 
     if rope.norm_dim != 0 and rope.norm_dim != D:
         raise ValueError("norm weights: [head_dim]")
     if q_out is None:
-        q_out = torch.empty(shape, dtype=q_out_dtype, device=q.device)
+        q_out = _new(stream, torch.empty, shape, dtype=q_out_dtype, device=q.device)
     elif q_out.shape != shape or not q_out.is_contiguous():
         raise ValueError("q_out: contiguous, of q's shape")
     out_code = _DTYPE_CODE.get(q_out.dtype)
@@ -588,7 +602,7 @@ def attn_decode(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor
     if code is None:
         raise TypeError("q is float32 or bfloat16")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = _new(stream, torch.empty, shape, dtype=dtype, device=q.device)
     elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
         raise ValueError("out: contiguous, of q's shape and type")
     rows, W = page_table.shape
@@ -631,13 +645,13 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     if one != 1 and V > 1:
         raise ValueError("logits: each row contiguous")
     if workspace is None:
-        workspace = sample_workspace(M, V, logits.device)
+        workspace = _new(stream, sample_workspace, M, V, logits.device)
     elif workspace.dtype is not _u8 or not workspace.is_contiguous():
         raise ValueError("workspace: contiguous uint8")
     if ids is None:
-        ids = torch.empty(M, dtype=_i32, device=logits.device)
+        ids = _new(stream, torch.empty, M, dtype=_i32, device=logits.device)
     if probs is None:
-        probs = torch.empty(M, dtype=_f32, device=logits.device)
+        probs = _new(stream, torch.empty, M, dtype=_f32, device=logits.device)
     cuda = logits.is_cuda and workspace.is_cuda
     at = []
     for t, dtype in ((u, _f32), (temperature, _f32), (top_k, _i32), (top_p, _f32), (min_p, _f32), (ids, _i32), (probs, _f32)):

@@ -129,3 +129,37 @@ def test_append_negative_lengths_are_padding(rot):
     assert torch.all(out[0] == 0) and torch.all(out[1] != 0) and torch.all(out[2] == 0)
     stored = (P.k.nan_to_num(0.0) != 0).any(-1).any(-1)
     assert int(stored.sum()) == 3 and torch.all(stored[int(P.table[1, 0]), 6:9])
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_tensors_of_a_call_on_another_stream(handle):
+    """What a call makes itself (outputs, the sampler's workspace) is ordered with the stream it is given: it is neither a
+    block that pending work of the current stream still writes, nor filled on the current stream."""
+    P = Paged([300, 40], 2, 128, 16, BF16, seed=57)
+    q, kv = rand_q(2, 1, 8, 128, BF16, 58), rand_q(2, 1, 2, 128, BF16, 59)
+    ws = kq.attn_workspace(P.cache, 2, 1, 8)
+    side = torch.cuda.Stream()
+    x, u = torch.randn(40, 40000, device="cuda"), torch.full((40,), 0.5, device="cuda")  # flat: half of them go to the tail
+    k = torch.tensor([5, 3000] * 20, dtype=torch.int32, device="cuda")
+    route = torch.randn(3, 16, device="cuda")
+
+    def calls(stream):
+        yield lambda: [kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws, stream=stream)]
+        yield lambda: [kq.kv_append(P.cache, P.table, P.seq_lens, q, kv, kv, kq.RopeNorm(), stream=stream)]
+        yield lambda: list(kq.sample(x, u, top_k=k, stream=stream))
+        yield lambda: list(kq.moe_route(route, 2, stream=stream))
+
+    for plain, there in zip(calls(None), calls(side.cuda_stream if handle else side)):
+        want = plain()
+        sizes = [t.shape for t in want] + [(2048,)]  # the sampler's workspace is of a few KB
+        torch.cuda.synchronize()
+        torch.cuda._sleep(50_000_000)
+        for shape in sizes:  # written after the sleep, their blocks are free for the current stream at once
+            torch.empty(shape, device="cuda").fill_(1e9)
+        got = there()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    a = kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws, stream=0)  # the default stream's handle
+    b = kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)

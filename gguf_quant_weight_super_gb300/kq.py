@@ -376,7 +376,7 @@ class Chain:
         if n == 0:
             raise KQError("kq_chain_workspace_size", -4)
         dev = device if device is not None else self.ops[0]["y"].device
-        self.workspace = torch.empty(n + 256, dtype=torch.uint8, device=dev)
+        self.workspace = _new(stream, torch.empty, n + 256, dtype=torch.uint8, device=dev)
         off = (-self.workspace.data_ptr()) % 256
         self._ws_ptr = self.workspace.data_ptr() + off
         self._ws_bytes = n

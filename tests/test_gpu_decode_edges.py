@@ -4,8 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from gguf_quant_weight_super_gb300 import kq
-from tests.gpu_util import require_gpu
+from gguf_quant_weight_super_gb300 import kq, synth
+from tests.gpu_util import dev, require_gpu
 from tests.test_gpu_cache import BF16, F8, F32, Paged, f64, rand_q
 
 pytestmark = pytest.mark.gpu
@@ -163,3 +163,22 @@ def test_tensors_of_a_call_on_another_stream(handle):
     b = kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws)
     torch.cuda.synchronize()
     assert torch.equal(a, b)
+
+
+def test_chain_planned_on_another_stream():
+    """A chain's workspace holds its plan: pending work of the current stream does not write over it."""
+    N, K = 64, 512
+    W = dev(synth.gen_matrix(synth.Q4_K, N, K, synth.rng(600)))
+    x, y, want = torch.randn(1, K, device="cuda"), torch.zeros(N, device="cuda"), torch.zeros(N, device="cuda")
+    op = dict(type=synth.Q4_K, x_dtype=kq.KQ_F32, W=W, x=x, N=N, K=K)
+    kq.Chain([dict(op, y=want)]).run()
+    size = kq.kq_chain_workspace_size([dict(op, y=y)]) + 256
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(50_000_000)
+    torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0)
+    chain = kq.Chain([dict(op, y=y)], stream=side)
+    torch.cuda.synchronize()  # whatever was pending has been written
+    chain.run(stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)

@@ -1,5 +1,6 @@
 // kq_api.cu -- the extern "C" entry points of libkq (declared in include/kq.h):
 // argument checks, kernel choice, launch, and the device error word.
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 
@@ -431,7 +432,9 @@ kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, in
                          size_t workspace_bytes, kq_stream_t stream) {
   const kq_status cs = check_attn(cache, B, T, n_q_heads);
   if (cs != KQ_OK) return cs;
-  if (!float_dtype(q_dtype) || max_pages < 0 || window < 0 || !(softcap >= 0.0f) || scale != scale) return KQ_ERR_ARG;
+  if (!float_dtype(q_dtype) || max_pages < 0 || window < 0 || !(softcap == 0.0f || good_scale(softcap)) ||
+      !good_scale(scale == 0.0f ? 1.0f : fabsf(scale)))
+    return KQ_ERR_ARG;
   if (B == 0 || T == 0) return KQ_OK;
   if (max_pages > INT32_MAX) return KQ_ERR_UNSUPPORTED;
   if (!seq_lens || !q || !out || (max_pages > 0 && !page_table)) return KQ_ERR_ARG;

@@ -484,7 +484,7 @@ kq_status kq_kv_append(const kq_kv_cache *cache, const int32_t *page_table, int6
  * where the token at position p sees positions j <= p, with window > 0 only
  * j > p - window.  n_q_heads a multiple of n_kv_heads, at most 16 times it:
  * query head h reads head h / (n_q_heads / n_kv_heads).  A token that sees
- * nothing (padding, an empty sequence) gets zeros.  What lies in slots that no
+ * nothing (padding, an empty sequence) gets zeros.  scale and softcap are finite.  What lies in slots that no
  * token sees has no influence, NaN and infinities included; a slot that only
  * some of the T tokens see has none on the others.
  *   q   [B*T] rows of n_q_heads*head_dim, q_stride elements apart, q_dtype KQ_F32 or KQ_BF16

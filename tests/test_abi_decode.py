@@ -128,3 +128,12 @@ def test_binding_refusals(L):
         kq.sample(torch.zeros(3, 5), torch.zeros(2))
     with pytest.raises(ValueError):
         kq.sample(torch.zeros(5, 3).T, torch.zeros(3))
+
+
+def test_attn_refuses_scales_and_caps_that_are_not_finite(L):
+    """An infinite cap or scale would make every score that is 0 a NaN."""
+    inf = float("inf")
+    for kw in (dict(cap=inf), dict(scale=inf), dict(scale=-inf)):
+        assert attn(L, **kw) == ARG, kw
+    for kw in (dict(cap=30.0), dict(scale=0.0), dict(scale=-0.5), dict(cap=3e38)):
+        assert attn(L, ws=None, **kw) == WORKSPACE, kw  # past these checks

@@ -469,6 +469,24 @@ kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, in
   return cuda_status(e);
 }
 
+kq_status kq_selftest_attn_ctas(const kq_kv_cache* cache, int64_t B, int64_t T, int q_dtype, int32_t n_q_heads,
+                                int* planned, int* resident) {
+  const kq_status cs = check_attn(cache, B, T, n_q_heads);
+  if (cs != KQ_OK) return cs;
+  if (!float_dtype(q_dtype) || B == 0 || T == 0 || !planned || !resident) return KQ_ERR_ARG;
+  AttnArgs a = {};
+  a.c = *cache;
+  a.B = static_cast<int>(B);
+  a.T = static_cast<int>(T);
+  a.Hq = n_q_heads;
+  a.G = n_q_heads / cache->n_kv_heads;
+  AttnShape s = {0, 0};
+  const cudaError_t e = launch_attn(a, q_dtype == KQ_BF16, nullptr, &s);
+  *planned = s.planned;
+  *resident = s.resident;
+  return e == cudaErrorNotSupported ? KQ_ERR_UNSUPPORTED : cuda_status(e);
+}
+
 size_t kq_sample_workspace_size(int64_t M, int64_t V) {
   if (M < 0 || V < 1 || M > (1 << 24) || V > (1 << 20)) return 0;
   return sample_workspace_bytes(M, V);

@@ -44,7 +44,7 @@ size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq) {
   return n > m ? n : m;
 }
 
-cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st) {
+cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st, AttnShape* ask) {
   const bool to_wide = q_bf16 && a.c.dtype == KQ_BF16 && wide(a.c.head_dim, a.T * a.G);
   const Layout L = layout(a.c.head_dim, a.c.n_kv_heads, a.T, a.Hq, to_wide);
   // the line of tiles is counted in 31 bits
@@ -57,9 +57,9 @@ cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st) {
   p.count = reinterpret_cast<int*>(ws + L.count_off);
   p.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
   p.part = reinterpret_cast<float*>(ws + L.part_off);
-  if (to_wide) return launch_attn_wide(p, st);
-  if (a.c.dtype == KQ_BF16) return q_bf16 ? launch_attn_bf16_bf16(p, L.rows, st) : launch_attn_bf16_f32(p, L.rows, st);
-  return q_bf16 ? launch_attn_f8_bf16(p, L.rows, st) : launch_attn_f8_f32(p, L.rows, st);
+  if (to_wide) return launch_attn_wide(p, st, ask);
+  if (a.c.dtype == KQ_BF16) return q_bf16 ? launch_attn_bf16_bf16(p, L.rows, st, ask) : launch_attn_bf16_f32(p, L.rows, st, ask);
+  return q_bf16 ? launch_attn_f8_bf16(p, L.rows, st, ask) : launch_attn_f8_f32(p, L.rows, st, ask);
 }
 
 }  // namespace kq

@@ -3,8 +3,8 @@
 
 namespace kq {
 
-cudaError_t launch_attn_bf16_f32(const attn::Params& p, int rows, cudaStream_t st) {
-  return attn::launch_kind<float, __nv_bfloat16>(p, rows, st);
+cudaError_t launch_attn_bf16_f32(const attn::Params& p, int rows, cudaStream_t st, AttnShape* ask) {
+  return attn::launch_kind<float, __nv_bfloat16>(p, rows, st, ask);
 }
 
 }  // namespace kq

@@ -68,6 +68,11 @@ constexpr int WT = 16;           // positions per warp sub-tile
 constexpr int TK = NW * WT;      // positions per tile
 constexpr int START = 3;         // tiles' time that an item costs besides its tiles
 
+// The attention kernel's static shared memory.
+struct Scratch {
+  int scan[NW], last;
+};
+
 template <class Q, class C, int D, int NT>
 struct Cfg {
   static constexpr bool F8 = sizeof(C) == 1, QF32 = sizeof(Q) == 4;
@@ -82,12 +87,14 @@ struct Cfg {
   static constexpr int HDR = (ROWS * (2 + 2 * NW) * 4 + 127) / 128 * 128;  // row scales, the join's and the warps' statistics
   static constexpr int FIXED = HDR + QBYTES;
   // CTAs per SM: three where the sums take few registers, two where a ring of at least two stages fits beside q in half of
-  // the shared memory (what is left of it is the line of tiles' index, 4 bytes per sequence), else one
+  // the shared memory, else one.  An SM has 228 KB, of which each CTA's static memory and 1 KB of the system's go off; what
+  // the budgets leave is the line of tiles' index, 4 bytes per sequence (large batches have fewer CTAs per SM).
   static constexpr int budget(int ctas) { return (ctas == 3 ? 73 : ctas == 2 ? 110 : 192) * 1024; }
   static constexpr int stages(int ctas) { return (budget(ctas) - FIXED) / (NW * STAGE); }
   static constexpr int CPS = NT * D <= 128 && stages(3) >= 2 ? 3 : stages(2) >= 2 ? 2 : 1;
   static constexpr int S = stages(CPS) < 6 ? stages(CPS) : 6;  // ring stages
-  static constexpr int SMEM = FIXED + S * NW * STAGE;
+  static constexpr int RING = S * NW * STAGE, SMEM = FIXED + RING;
+  static_assert(CPS * (SMEM + 4 * 257 + static_cast<int>(sizeof(Scratch)) + 1024) <= 228 * 1024, "256 sequences: all resident");
   static constexpr bool QREG = NT * NQ * (D / 8) <= 32;  // q's operands stay in registers
   static constexpr int OB = (D + 4) * 4;                 // bytes of a row of the warps' sums in shared memory
   static_assert(S >= 2 && S * STAGE >= ROWS * OB, "the warps' sums take the ring's place");
@@ -766,21 +773,19 @@ template <class Q, class C, int D, int NT>
 __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(const __grid_constant__ Params p) {
   using K = Cfg<Q, C, D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_scan[NW];
-  __shared__ __align__(16) float s_sum[JOIN_SUMS];
-  __shared__ int s_last;
+  __shared__ Scratch scratch;
   float* rscale = reinterpret_cast<float*>(smem);  // [ROWS]
   float* s_i = rscale + K::ROWS;                   // [ROWS] the join's 1 / weight sum
   float* w_ml = s_i + K::ROWS;                     // [NW][ROWS][2] each warp's maximum and weight sum
   uint8_t* qsm = smem + K::HDR;
   uint8_t* ring = smem + K::FIXED;
   const AttnArgs& a = p.a;
-  int* prefix = reinterpret_cast<int*>(ring + K::S * NW * K::STAGE);  // [B + 1] tiles before each sequence
+  int* prefix = reinterpret_cast<int*>(ring + K::RING);  // [B + 1] tiles before each sequence
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
 
-  build_prefix(a, START, prefix, s_scan);
+  build_prefix(a, START, prefix, scratch.scan);
   const Line line(a, p.RT, prefix);
   const int range = blockIdx.x;
   if (range >= line.nc) return;
@@ -877,18 +882,21 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
         if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * K::ROWS + r) * 2) = make_float2(mm, ll);
       }
     }
-    if (!whole)
-      join_parts<D, K::ROWS>(p, line, it, R, threadIdx.x, reinterpret_cast<float*>(ring), K::S * NW * K::STAGE, s_sum, s_i, &s_last,
-                             [] { __syncthreads(); }, write);
+    if (!whole) {  // in the ring's place, too
+      constexpr int ROOM = K::RING - JOIN_SUMS * 4;
+      join_parts<D, K::ROWS>(p, line, it, R, threadIdx.x, reinterpret_cast<float*>(ring), ROOM, reinterpret_cast<float*>(ring + ROOM),
+                             s_i, &scratch.last, [] { __syncthreads(); }, write);
+    }
     __syncthreads();
     u = end;
   }
 }
 
 template <class Q, class C, int D, int NT>
-cudaError_t launch_one(const Params& p, cudaStream_t st) {
+cudaError_t launch_one(const Params& p, cudaStream_t st, AttnShape* ask) {
   using K = Cfg<Q, C, D, NT>;
   const size_t smem = K::SMEM + 4 * (static_cast<size_t>(p.a.B) + 1);
+  static size_t fits[64] = {0};  // shared memory with which CPS CTAs are known to be resident, per device
   static int set[64] = {0};  // shared memory allowed so far, per device
   const int dev = current_device_id();
   if (set[dev] < static_cast<int>(smem)) {
@@ -897,20 +905,32 @@ cudaError_t launch_one(const Params& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set[dev] = static_cast<int>(smem);
   }
-  return launch_pdl(attn_kernel<Q, C, D, NT>, dim3(num_sms() * K::CPS), dim3(NTH), smem, st, p);
+  // one range per CTA, all of them resident: one that waits for another's place would start when that one has ended
+  int ctas = K::CPS;
+  if (K::CPS > 1 && smem > fits[dev]) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, attn_kernel<Q, C, D, NT>, NTH, smem);
+    if (e != cudaSuccess) return e;
+    if (ctas >= K::CPS) fits[dev] = smem;
+    ctas = ctas < 1 ? 1 : ctas < K::CPS ? ctas : K::CPS;
+  }
+  if (ask) {
+    ask->planned = K::CPS;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ask->resident, attn_kernel<Q, C, D, NT>, NTH, smem);
+  }
+  return launch_pdl(attn_kernel<Q, C, D, NT>, dim3(num_sms() * ctas), dim3(NTH), smem, st, p);
 }
 
 template <class Q, class C>
-cudaError_t launch_kind(const Params& p, int rows, cudaStream_t st) {
+cudaError_t launch_kind(const Params& p, int rows, cudaStream_t st, AttnShape* ask) {
   switch (p.a.c.head_dim * 100 + rows) {
-    case 6408: return launch_one<Q, C, 64, 1>(p, st);
-    case 6416: return launch_one<Q, C, 64, 2>(p, st);
-    case 6432: return launch_one<Q, C, 64, 4>(p, st);
-    case 12808: return launch_one<Q, C, 128, 1>(p, st);
-    case 12816: return launch_one<Q, C, 128, 2>(p, st);
-    case 12832: return launch_one<Q, C, 128, 4>(p, st);
-    case 25608: return launch_one<Q, C, 256, 1>(p, st);
-    default: return launch_one<Q, C, 256, 2>(p, st);
+    case 6408: return launch_one<Q, C, 64, 1>(p, st, ask);
+    case 6416: return launch_one<Q, C, 64, 2>(p, st, ask);
+    case 6432: return launch_one<Q, C, 64, 4>(p, st, ask);
+    case 12808: return launch_one<Q, C, 128, 1>(p, st, ask);
+    case 12816: return launch_one<Q, C, 128, 2>(p, st, ask);
+    case 12832: return launch_one<Q, C, 128, 4>(p, st, ask);
+    case 25608: return launch_one<Q, C, 256, 1>(p, st, ask);
+    default: return launch_one<Q, C, 256, 2>(p, st, ask);
   }
 }
 
@@ -918,12 +938,12 @@ cudaError_t launch_kind(const Params& p, int rows, cudaStream_t st) {
 
 // More than 16 rows, bf16 q and cache, heads of 64 or 128 values (kq_attn_wide.cu).
 constexpr int kWideRows = 128;
-cudaError_t launch_attn_wide(const attn::Params& p, cudaStream_t st);
+cudaError_t launch_attn_wide(const attn::Params& p, cudaStream_t st, AttnShape* ask);
 
 // One translation unit per cache and query type (rows: query rows per pass, 8, 16 or 32).
-cudaError_t launch_attn_bf16_bf16(const attn::Params& p, int rows, cudaStream_t st);
-cudaError_t launch_attn_bf16_f32(const attn::Params& p, int rows, cudaStream_t st);
-cudaError_t launch_attn_f8_bf16(const attn::Params& p, int rows, cudaStream_t st);
-cudaError_t launch_attn_f8_f32(const attn::Params& p, int rows, cudaStream_t st);
+cudaError_t launch_attn_bf16_bf16(const attn::Params& p, int rows, cudaStream_t st, AttnShape* ask);
+cudaError_t launch_attn_bf16_f32(const attn::Params& p, int rows, cudaStream_t st, AttnShape* ask);
+cudaError_t launch_attn_f8_bf16(const attn::Params& p, int rows, cudaStream_t st, AttnShape* ask);
+cudaError_t launch_attn_f8_f32(const attn::Params& p, int rows, cudaStream_t st, AttnShape* ask);
 
 }  // namespace kq

@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
 }
 
 template <int D>
-cudaError_t launch_d(const Params& p, cudaStream_t st) {
+cudaError_t launch_d(const Params& p, cudaStream_t st, AttnShape* ask) {
   using W = WCfg<D>;
   const size_t smem = W::SMEM + 4 * (static_cast<size_t>(p.a.B) + 1);
   static int set[64] = {0};
@@ -530,14 +530,18 @@ cudaError_t launch_d(const Params& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set[dev] = static_cast<int>(smem);
   }
+  if (ask) {
+    ask->planned = 1;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ask->resident, wide_kernel<D>, WTH, smem);
+  }
   return launch_pdl(wide_kernel<D>, dim3(num_sms()), dim3(WTH), smem, st, p);
 }
 
 }  // namespace
 }  // namespace attn
 
-cudaError_t launch_attn_wide(const attn::Params& p, cudaStream_t st) {
-  return p.a.c.head_dim == 64 ? attn::launch_d<64>(p, st) : attn::launch_d<128>(p, st);
+cudaError_t launch_attn_wide(const attn::Params& p, cudaStream_t st, AttnShape* ask) {
+  return p.a.c.head_dim == 64 ? attn::launch_d<64>(p, st, ask) : attn::launch_d<128>(p, st, ask);
 }
 
 }  // namespace kq

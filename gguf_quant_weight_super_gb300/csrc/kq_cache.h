@@ -55,7 +55,11 @@ struct AttnArgs {
 // Positions are counted in 32 bits, tiles and copies ahead of the last one included.
 constexpr int64_t kMaxPositions = INT32_MAX - 4095;
 size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq);
-cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st);
+// With `ask`: no launch, but the CTAs per SM that the kernel is laid out for and that the device holds at once.
+struct AttnShape {
+  int planned, resident;
+};
+cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st, AttnShape* ask = nullptr);
 
 struct SampleArgs {
   const void* logits;

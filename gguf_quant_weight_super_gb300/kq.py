@@ -54,6 +54,8 @@ SIGNATURES = {
     "kq_attn_workspace_size": (_SZ, [_P, _I64, _I64, ctypes.c_int32]),
     "kq_attn_decode": (_I, [_P, _P, _I64, _P, _I64, _I64, _P, _I, _I64, ctypes.c_int32, ctypes.c_float,
                             ctypes.c_float, ctypes.c_int32, _P, _P, _SZ, _P]),
+    "kq_selftest_attn_ctas": (_I, [_P, _I64, _I64, _I, ctypes.c_int32, ctypes.POINTER(ctypes.c_int),
+                                   ctypes.POINTER(ctypes.c_int)]),
     "kq_sample_workspace_size": (_SZ, [_I64, _I64]),
     "kq_sample": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "kq_device_error": (_I, [ctypes.POINTER(ctypes.c_int), _I]),
@@ -492,6 +494,13 @@ def kq_attn_decode(cache, page_table, max_pages, seq_lens, B, T, q, q_dtype, q_s
     _check("kq_attn_decode", lib().kq_attn_decode(cache, _ptr(page_table), max_pages, _ptr(seq_lens), B, T, _ptr(q),
                                                   q_dtype, q_stride, n_q_heads, scale, softcap, window, _ptr(out),
                                                   _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def kq_selftest_attn_ctas(cache, B, T, q_dtype, n_q_heads):
+    """(planned, resident) CTAs per SM of an attention call."""
+    n = ctypes.c_int(0), ctypes.c_int(0)
+    _check("kq_selftest_attn_ctas", lib().kq_selftest_attn_ctas(cache, B, T, q_dtype, n_q_heads, *map(ctypes.byref, n)))
+    return n[0].value, n[1].value
 
 
 def kq_sample_workspace_size(M, V) -> int:

@@ -509,6 +509,15 @@ kq_status kq_attn_decode(const kq_kv_cache *cache, const int32_t *page_table, in
                          size_t workspace_bytes, kq_stream_t stream);
 
 /*
+ * Self-test of kq_attn_decode's layout, without a launch: for a call with
+ * these arguments, the CTAs per SM that its kernel is laid out for (*planned)
+ * and that the device holds at once (*resident).  A call's grid is the smaller
+ * of both; up to 256 sequences they are the same.  Errors as kq_attn_decode's.
+ */
+kq_status kq_selftest_attn_ctas(const kq_kv_cache *cache, int64_t B, int64_t T, int q_dtype, int32_t n_q_heads,
+                                int *planned, int *resident);
+
+/*
  * The next token of each of M rows of V logits, from a uniform number per row.
  *   logits [M] rows of V values, row_stride elements apart, KQ_F32 or KQ_BF16
  *   u      [M] fp32 in [0, 1)

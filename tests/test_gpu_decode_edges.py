@@ -182,3 +182,40 @@ def test_chain_planned_on_another_stream():
     chain.run(stream=side)
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF16, F8])
+@pytest.mark.parametrize("qt", [kq.KQ_BF16, kq.KQ_F32])
+def test_attn_ranges_are_all_resident(D, dtype, qt):
+    """The line of tiles is cut for CTAs that run at the same time: the device holds as many as the kernel is laid out for,
+    up to 256 sequences; a large batch's index leaves room for one at least."""
+    c = kq.KVCache(*(torch.zeros((1, 16, 1, D), device="cuda").to(dtype) for _ in range(2)))
+    for rows in (1, 8, 9, 16, 17, 32, 128, 256):
+        T, G = max(1, rows // 16), min(rows, 16)
+        if T * G != rows:
+            T, G = rows, 1
+        if T > 16:
+            T, G = 16, 2
+        planned, resident = kq.kq_selftest_attn_ctas(c._ref, 1, T, qt, G)
+        assert planned == resident >= 1, (rows, planned, resident)
+        assert kq.kq_selftest_attn_ctas(c._ref, 256, T, qt, G) == (planned, planned)
+        assert kq.kq_selftest_attn_ctas(c._ref, 4096, T, qt, G)[1] >= 1
+        if rows <= 8 and dtype == BF16 and qt == kq.KQ_BF16 and D <= 128:
+            assert planned == 3
+
+
+def test_attn_large_batch_with_fewer_ranges():
+    """4096 sequences: the index takes a CTA's place on each SM."""
+    lens = [(i * 37) % 100 for i in range(4096)]
+    P = Paged([99], 1, 128, 16, BF16, seed=60)
+    q = rand_q(4096, 1, 2, 128, BF16, 61)
+    table = P.table.expand(4096, -1).contiguous()
+    out = kq.attn_decode(P.cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), q, kq.attn_workspace(P.cache, 4096, 1, 2))
+    few = list(range(0, 4096, 256))
+    want = kq.attn_decode(P.cache, table[few].contiguous(), torch.tensor([lens[i] for i in few], dtype=torch.int32, device="cuda"),
+                          q[few].contiguous(), kq.attn_workspace(P.cache, len(few), 1, 2))
+    torch.cuda.synchronize()
+    # the same sums in another order and one rounding to bf16
+    assert torch.all((out[few].double() - want.double()).abs() <= 2.0 ** -7 * want.double().abs() + 2.0 ** -14)
+    assert torch.all(out[lens.index(0)] == 0)

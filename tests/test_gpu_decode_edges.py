@@ -219,3 +219,30 @@ def test_attn_large_batch_with_fewer_ranges():
     # the same sums in another order and one rounding to bf16
     assert torch.all((out[few].double() - want.double()).abs() <= 2.0 ** -7 * want.double().abs() + 2.0 ** -14)
     assert torch.all(out[lens.index(0)] == 0)
+
+
+@pytest.mark.parametrize("qt", [BF16, F32])
+@pytest.mark.parametrize("D,Hkv,G", [(64, 2, 1), (128, 2, 4), (256, 1, 2)])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_attn_8bit_nan_in_unseen_positions(qt, D, Hkv, G, what):
+    """As test_attn_unseen_positions_do_not_matter, in an e4m3 cache, whose only special value is NaN."""
+    T, n, window = 8, 200, 64
+    P = Paged([n, 64], Hkv, D, 16, F8, seed=62)
+    q = rand_q(2, T, G * Hkv, D, qt, 63)
+    ws = kq.attn_workspace(P.cache, 2, T, G * Hkv)
+    clean = kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws, window=window)
+    for pos in (n - 3, n - T - window + 3):  # seen by tokens t >= 5; by tokens t <= 2
+        (P.k if what == "k" else P.v).view(torch.uint8)[int(P.table[0, pos // 16]), pos % 16, 0, 5] = 0x7F
+    got = kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws, window=window)
+    torch.cuda.synchronize()
+    for t in range(T):
+        if 2 < t < 5:
+            assert torch.equal(got[0, t], clean[0, t]), t
+            continue
+        assert torch.equal(got[0, t, G:], clean[0, t, G:]), t
+        nan = torch.isnan(got[0, t, :G])
+        assert torch.all(nan if what == "k" else nan[:, 5]), t
+        if what == "v":
+            rest = [d for d in range(D) if d != 5]
+            assert torch.equal(got[0, t, :G][:, rest], clean[0, t, :G][:, rest]), t
+    assert torch.equal(got[1], clean[1])

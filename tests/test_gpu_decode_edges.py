@@ -6,7 +6,7 @@ import torch
 
 from gguf_quant_weight_super_gb300 import kq, synth
 from tests.gpu_util import dev, require_gpu
-from tests.test_gpu_cache import BF16, F8, F32, Paged, f64, rand_q
+from tests.test_gpu_cache import BF16, F8, F32, Paged, check_attn, f64, rand_q
 
 pytestmark = pytest.mark.gpu
 
@@ -199,7 +199,8 @@ def test_attn_ranges_are_all_resident(D, dtype, qt):
             T, G = 16, 2
         planned, resident = kq.kq_selftest_attn_ctas(c._ref, 1, T, qt, G)
         assert planned == resident >= 1, (rows, planned, resident)
-        assert kq.kq_selftest_attn_ctas(c._ref, 256, T, qt, G) == (planned, planned)
+        at_256 = kq.kq_selftest_attn_ctas(c._ref, 256, T, qt, G)  # of more than 16 rows maybe the other kernel's
+        assert at_256[0] == at_256[1] and (rows > 16 or at_256[0] == planned), (rows, at_256)
         assert kq.kq_selftest_attn_ctas(c._ref, 4096, T, qt, G)[1] >= 1
         if rows <= 8 and dtype == BF16 and qt == kq.KQ_BF16 and D <= 128:
             assert planned == 3
@@ -246,3 +247,44 @@ def test_attn_8bit_nan_in_unseen_positions(qt, D, Hkv, G, what):
             rest = [d for d in range(D) if d != 5]
             assert torch.equal(got[0, t, :G][:, rest], clean[0, t, :G][:, rest]), t
     assert torch.equal(got[1], clean[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,T,Hkv,G", [(2, 16, 1, 2), (3, 5, 2, 4), (33, 8, 1, 4), (5, 10, 2, 4), (7, 11, 1, 3), (6, 16, 4, 4),
+                                       (3, 16, 4, 4), (12, 16, 2, 8), (2, 16, 2, 8), (7, 15, 4, 9), (6, 16, 4, 16), (1, 16, 2, 16)])
+def test_attn_blocks_of_few_and_many_heads(D, B, T, Hkv, G):
+    """Blocks of more than 16 rows, on both sides of the choice between the kernels, with a window and without."""
+    lens = [(517, 100, 16, 0, 3, 64, 1030)[i % 7] for i in range(B)]
+    P = Paged(lens, Hkv, D, 32, BF16, seed=T * G + B)
+    q = rand_q(B, T, Hkv * G, D, BF16, 64)
+    check_attn(P, q)
+    check_attn(P, q, cap=20.0, window=70)
+
+
+@pytest.mark.parametrize("what", ["v_nan", "k_nan", "v_inf"])
+@pytest.mark.parametrize("T,G", [(8, 8), (16, 8), (16, 16)])
+def test_attn_unseen_positions_of_many_rows(what, T, G):
+    """As test_attn_unseen_positions_do_not_matter, for blocks of 64 rows and more of many heads."""
+    n, window, Hkv, B = 200, 64, 8, 4
+    P = Paged([n, 64, 300, 17], Hkv, 128, 16, BF16, seed=65)
+    q = rand_q(B, T, G * Hkv, 128, BF16, 66)
+    ws = kq.attn_workspace(P.cache, B, T, G * Hkv)
+    clean = kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws, window=window)
+    bad = float("inf") if what == "v_inf" else float("nan")
+    late, early = n - 3, n - T - window + 3  # seen by tokens from T - 3 on; by tokens up to 2
+    for pos in (late, early):
+        (P.k if what == "k_nan" else P.v)[int(P.table[0, pos // 16]), pos % 16, 0, 3] = bad
+    got = kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws, window=window)
+    torch.cuda.synchronize()
+    rest = [d for d in range(128) if d != 3]
+    for t in range(T):
+        assert torch.equal(got[0, t, G:], clean[0, t, G:]), t
+        mine = got[0, t, :G].float()
+        if 2 < t < T - 3:
+            assert torch.equal(got[0, t, :G], clean[0, t, :G]), t
+        elif what == "k_nan":
+            assert torch.all(torch.isnan(mine)), t
+        else:
+            assert torch.all(torch.isnan(mine[:, 3]) if what == "v_nan" else torch.isinf(mine[:, 3])), t
+            assert torch.equal(mine[:, rest], clean[0, t, :G].float()[:, rest]), t
+    assert torch.equal(got[1:], clean[1:])

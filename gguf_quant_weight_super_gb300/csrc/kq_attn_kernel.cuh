@@ -43,12 +43,13 @@
 // product is added by rounding fp32 additions.
 //
 // Measured on one GB300, calls in a graph: 4 x 131071 positions, 32 heads on 8
-// of 128, bf16, 316-322 us (6.4 TB/s, 94% of the copy rate); 24 sequences of 0
-// to 9001 positions, 71-76 us (5.2-5.5 TB/s: the slower fifth of the SMs ends
-// an eighth later, and an even cut cannot know them); one of 1000 positions,
-// 9.1 us, a chain of length, page, row, sum, partial sums and their join; 16
-// sequences in an e4m3 cache, heads of 256, fp32 q, window 4096, cap, 34 us
-// (3.9 TB/s: two CTAs per SM of 255 registers, and 4 us of joins).
+// of 128, bf16, 308-322 us (6.4-6.6 TB/s, 94-98% of the copy rate); 24 sequences
+// of 0 to 9001 positions, 72.5 us (5.4 TB/s: the median SM has read its ranges
+// after 54 us, the slowest fifth, the same SMs each time, after 60 to 62, and an
+// even cut cannot know them; the joins end at 69); one of 1000 positions, 9.4 us,
+// a chain of length, page, row, sum, partial sums and their join; 16 sequences in
+// an e4m3 cache, heads of 256, fp32 q, window 4096, cap, 34 us (3.9 TB/s: two CTAs
+// per SM of 255 registers, and 4 us of joins).
 //
 // Values that no row sees are never loaded (zeros take their place).  One that
 // some rows of the block see and others do not would reach the others as

@@ -9,10 +9,10 @@
 // Bound: with 32 rows and more the products of mma instructions cost more
 // than the bytes (8 x 16 tokens x 4 heads over 6007 positions: 26 us of their
 // pipe alone and 88 us in all, against 24 us for the bytes); tcgen05 has three
-// times their rate: 54.4 us here, of which the copies alone take 45 (7 us until
-// the first tile is there, 10 us for the parts' join).  20 rows 51 us against
-// 54 with mma, 128 rows 79 against 146; over 700 positions 128 rows take 37
-// against 28, since joining them costs more.  One CTA per SM:
+// times their rate: 54 us here, of which the copies alone take 45 (7 us until
+// the first tile is there, 10 us for the parts' join).  20 rows 49 us against
+// 51 with mma, 128 rows 75 against 139.  Where the joins of 128-row parts outweigh
+// that, with few heads, the host takes mma (kq_attn.cu).  One CTA per SM:
 //  * seven loader warps copy 8 positions at a time into a ring of stages, 16
 //    bytes per lane, where the matrix descriptors' 128-byte swizzle wants them:
 //    64 dims of a position are a line of 128 bytes, its 16-byte chunks c at

@@ -254,8 +254,9 @@ kq_status kq_chain_run(const kq_chain_plan *plan, void *workspace, kq_stream_t s
  * workspace: kq_moe_workspace_size(N, M, top_k, n_experts) bytes of device
  * memory, 256-byte aligned, zero-filled once before first use (arrival
  * counters return to zero after every call); one call at a time per
- * workspace.  After a call it holds the grouping, for inspection: at byte
- * 256, int32 D (distinct experts), expert[Dmax] (ascending ids),
+ * workspace, and calls of one set of these sizes only: where the counters lie
+ * depends on them, so zero it again before other ones.
+ * After a call it holds the grouping, for inspection: at byte 256, int32 D (distinct experts), expert[Dmax] (ascending ids),
  * offset[Dmax + 1], pair[M*top_k] (pair index m*top_k + j, grouped by expert,
  * (m, j) order within an expert), Dmax = min(n_experts, M*top_k).
  *
@@ -366,8 +367,8 @@ kq_status kq_moe_route(const float *logits, int64_t M, int32_t n_experts, int32_
  * workspace error word, read by kq_moe_check).
  * Two launches on stream (programmatic dependent launch); the workspace
  * (kq_moe_ffn_workspace_size bytes, 256-byte aligned, zero-filled once before
- * first use) holds the error word, the grouping plan at byte 256 (as in
- * kq_moe_matvec), arrival counters (back at zero after each call) and the fp32
+ * first use and again before calls of other sizes) holds the error word, the
+ * grouping plan at byte 256 (as in kq_moe_matvec), arrival counters (back at zero after each call) and the fp32
  * intermediates; h [M*top_k][F] and hs [M][SH] start at the offsets
  * kq_moe_ffn_offsets returns (for inspection).
  * Errors: KQ_ERR_ARG, KQ_ERR_TYPE, KQ_ERR_SHAPE (H, F or SH not a multiple of
@@ -484,15 +485,28 @@ kq_status kq_kv_append(const kq_kv_cache *cache, const int32_t *page_table, int6
  * where the token at position p sees positions j <= p, with window > 0 only
  * j > p - window.  n_q_heads a multiple of n_kv_heads, at most 16 times it:
  * query head h reads head h / (n_q_heads / n_kv_heads).  A token that sees
- * nothing (padding, an empty sequence) gets zeros.  scale and softcap are finite.  What lies in slots that no
- * token sees has no influence, NaN and infinities included; a slot that only
- * some of the T tokens see has none on the others.
+ * nothing (padding, an empty sequence) gets zeros.  scale and softcap are
+ * finite.  What lies in slots that no token sees has no influence, NaN and
+ * infinities included; a slot that only some of the T tokens see has none on
+ * the others.
  *   q   [B*T] rows of n_q_heads*head_dim, q_stride elements apart, q_dtype KQ_F32 or KQ_BF16
  *   out [B*T][n_q_heads][head_dim] of q_dtype
- * Scores, softmax and sums are fp32, and so are the partial results that
- * split sequences are joined from; the order of the sums depends on the
- * arguments, the lengths and the device's SM count only: repeated calls give
- * identical outputs.
+ * Scores, softmax statistics and sums are held in fp32, and so are the partial
+ * results that split sequences are joined from.  What has fewer bits:
+ *   - bf16 q over a bf16 cache: the weights multiply the values as two bf16
+ *     parts (2^-17 of a weight); over an e4m3 cache, with either q, as two fp16
+ *     parts (2^-22 of a weight, or 2^-40 of the row's largest if that is more);
+ *     fp32 q over a bf16 cache: three bf16 parts, all 24 bits;
+ *   - fp32 q over an e4m3 cache enters as two fp16 parts (2^-22 of a value, or
+ *     2^-38 of the row's largest);
+ *   - with bf16 q the matrix instructions cut what they add to a sum instead of
+ *     rounding it, up to 2^-16 over a long range; with fp32 q each step's
+ *     product is added by rounded fp32 additions.
+ * So fp32 q and out are as exact as a computation in fp32 but for weights far
+ * below the largest over an e4m3 cache; with bf16 q the error is bf16's rounding
+ * of out, though a few outputs in a thousand may round the other way than those
+ * of an fp32 computation.  The order of the sums depends on the arguments, the
+ * lengths and the device's SM count only: repeated calls give identical outputs.
  * workspace: kq_attn_workspace_size bytes, 256-byte aligned, zero-filled once
  * before first use (its counters are zero again after every call); one call at
  * a time per workspace.  The size depends on neither B nor q's type, and a
@@ -511,8 +525,10 @@ kq_status kq_attn_decode(const kq_kv_cache *cache, const int32_t *page_table, in
 /*
  * Self-test of kq_attn_decode's layout, without a launch: for a call with
  * these arguments, the CTAs per SM that its kernel is laid out for (*planned)
- * and that the device holds at once (*resident).  A call's grid is the smaller
- * of both; up to 256 sequences they are the same.  Errors as kq_attn_decode's.
+ * and that the device holds at once (*resident).  A call's grid has the smaller
+ * of both per SM; up to 256 sequences they are the same.  (A table of more than
+ * 16384 positions can have blocks of many rows go to another kernel.)  Errors as
+ * kq_attn_decode's.
  */
 kq_status kq_selftest_attn_ctas(const kq_kv_cache *cache, int64_t B, int64_t T, int q_dtype, int32_t n_q_heads,
                                 int *planned, int *resident);

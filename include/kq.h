@@ -256,8 +256,8 @@ kq_status kq_chain_run(const kq_chain_plan *plan, void *workspace, kq_stream_t s
  * counters return to zero after every call); one call at a time per
  * workspace, and calls of one set of these sizes only: where the counters lie
  * depends on them, so zero it again before other ones.
- * After a call it holds the grouping, for inspection: at byte 256, int32 D (distinct experts), expert[Dmax] (ascending ids),
- * offset[Dmax + 1], pair[M*top_k] (pair index m*top_k + j, grouped by expert,
+ * After a call it holds the grouping, for inspection: at byte 256, int32 D
+ * (distinct experts), expert[Dmax] (ascending ids), offset[Dmax + 1], pair[M*top_k] (pair index m*top_k + j, grouped by expert,
  * (m, j) order within an expert), Dmax = min(n_experts, M*top_k).
  *
  * Limits: M*top_k <= 512, n_experts <= 4096, K a multiple of 32, 32 rows of
@@ -368,8 +368,8 @@ kq_status kq_moe_route(const float *logits, int64_t M, int32_t n_experts, int32_
  * Two launches on stream (programmatic dependent launch); the workspace
  * (kq_moe_ffn_workspace_size bytes, 256-byte aligned, zero-filled once before
  * first use and again before calls of other sizes) holds the error word, the
- * grouping plan at byte 256 (as in kq_moe_matvec), arrival counters (back at zero after each call) and the fp32
- * intermediates; h [M*top_k][F] and hs [M][SH] start at the offsets
+ * grouping plan at byte 256 (as in kq_moe_matvec), arrival counters (back at
+ * zero after each call) and the fp32 intermediates; h [M*top_k][F] and hs [M][SH] start at the offsets
  * kq_moe_ffn_offsets returns (for inspection).
  * Errors: KQ_ERR_ARG, KQ_ERR_TYPE, KQ_ERR_SHAPE (H, F or SH not a multiple of
  * 32), KQ_ERR_UNSUPPORTED (M*top_k > 512, n_experts > 4096, a K above 16384 or

@@ -371,10 +371,11 @@ static int log2_of(int v) {
   return s;
 }
 
-kq_status kq_kv_append(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
-                       const int32_t* seq_lens, int64_t B, int64_t T, const void* q, const void* k, const void* v,
-                       int x_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t n_q_heads,
-                       const kq_rope* rope, void* q_out, int q_out_dtype, kq_stream_t stream) {
+static kq_status kv_append(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
+                           const int32_t* seq_lens, const uint64_t* tree, int64_t B, int64_t T, const void* q,
+                           const void* k, const void* v, int x_dtype, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, int32_t n_q_heads, const kq_rope* rope, void* q_out, int q_out_dtype,
+                           kq_stream_t stream) {
   const kq_status cs = check_cache(cache);
   if (cs != KQ_OK) return cs;
   if (!rope || !float_dtype(x_dtype) || !float_dtype(q_out_dtype)) return KQ_ERR_ARG;
@@ -408,16 +409,45 @@ kq_status kq_kv_append(const kq_kv_cache* cache, const int32_t* page_table, int6
   a.Hq = n_q_heads;
   a.page_shift = log2_of(cache->page_size);
   a.err = device_error_ptr();
+  a.tree = tree;
   cudaError_t e = launch_kv_append(a, x_dtype == KQ_BF16, q_out_dtype == KQ_BF16, reinterpret_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) e = cudaGetLastError();
   return cuda_status(e);
 }
 
-static kq_status check_attn(const kq_kv_cache* cache, int64_t B, int64_t T, int32_t n_q_heads) {
+kq_status kq_kv_append(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
+                       const int32_t* seq_lens, int64_t B, int64_t T, const void* q, const void* k, const void* v,
+                       int x_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t n_q_heads,
+                       const kq_rope* rope, void* q_out, int q_out_dtype, kq_stream_t stream) {
+  return kv_append(cache, page_table, max_pages, seq_lens, nullptr, B, T, q, k, v, x_dtype, q_stride, k_stride, v_stride,
+                   n_q_heads, rope, q_out, q_out_dtype, stream);
+}
+
+// A tree's masks for T tokens of each of B sequences (either may be 0: nothing to do).
+static kq_status check_tree(const uint64_t* tree, int64_t B, int64_t T) {
+  if (B < 0 || T < 0) return KQ_ERR_ARG;
+  if (T > kMaxTree) return KQ_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return KQ_OK;
+  if (!tree) return KQ_ERR_ARG;
+  return aligned(tree, 8) ? KQ_OK : KQ_ERR_ALIGN;
+}
+
+kq_status kq_kv_append_tree(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
+                            const int32_t* seq_lens, const uint64_t* tree, int64_t B, int64_t T, const void* q,
+                            const void* k, const void* v, int x_dtype, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, int32_t n_q_heads, const kq_rope* rope, void* q_out, int q_out_dtype,
+                            kq_stream_t stream) {
+  const kq_status ts = check_tree(tree, B, T);
+  if (ts != KQ_OK) return ts;
+  return kv_append(cache, page_table, max_pages, seq_lens, tree, B, T, q, k, v, x_dtype, q_stride, k_stride, v_stride,
+                   n_q_heads, rope, q_out, q_out_dtype, stream);
+}
+
+static kq_status check_attn(const kq_kv_cache* cache, int64_t B, int64_t T, int32_t n_q_heads, int most = 16) {
   const kq_status cs = check_cache(cache);
   if (cs != KQ_OK) return cs;
   if (B < 0 || T < 0 || n_q_heads <= 0 || n_q_heads % cache->n_kv_heads) return KQ_ERR_ARG;
-  if (B > 4096 || T > 16 || n_q_heads / cache->n_kv_heads > 16) return KQ_ERR_UNSUPPORTED;
+  if (B > 4096 || T > most || n_q_heads / cache->n_kv_heads > 16) return KQ_ERR_UNSUPPORTED;
   return KQ_OK;
 }
 
@@ -426,11 +456,21 @@ size_t kq_attn_workspace_size(const kq_kv_cache* cache, int64_t B, int64_t T, in
   return attn_workspace_bytes(cache->head_dim, cache->n_kv_heads, T, n_q_heads);
 }
 
-kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
-                         const int32_t* seq_lens, int64_t B, int64_t T, const void* q, int q_dtype, int64_t q_stride,
-                         int32_t n_q_heads, float scale, float softcap, int32_t window, void* out, void* workspace,
-                         size_t workspace_bytes, kq_stream_t stream) {
-  const kq_status cs = check_attn(cache, B, T, n_q_heads);
+size_t kq_attn_tree_workspace_size(const kq_kv_cache* cache, int64_t B, int64_t T, int32_t n_q_heads) {
+  if (check_attn(cache, B, T, n_q_heads, kMaxTree) != KQ_OK) return 0;
+  size_t most = 0;  // which kernel takes a call, and how many rows at a time, depends on T: room for any up to it
+  for (int64_t t = 0; t <= T; ++t) {
+    const size_t n = attn_workspace_bytes(cache->head_dim, cache->n_kv_heads, t, n_q_heads);
+    most = n > most ? n : most;
+  }
+  return most;
+}
+
+static kq_status attn(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages, const int32_t* seq_lens,
+                      const uint64_t* tree, int64_t B, int64_t T, const void* q, int q_dtype, int64_t q_stride,
+                      int32_t n_q_heads, float scale, float softcap, int32_t window, void* out, void* workspace,
+                      size_t workspace_bytes, kq_stream_t stream) {
+  const kq_status cs = check_attn(cache, B, T, n_q_heads, tree ? kMaxTree : 16);
   if (cs != KQ_OK) return cs;
   if (!float_dtype(q_dtype) || max_pages < 0 || window < 0 || !(softcap == 0.0f || good_scale(softcap)) ||
       !good_scale(scale == 0.0f ? 1.0f : fabsf(scale)))
@@ -463,7 +503,231 @@ kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, in
   a.window = window < a.room ? window : 0;  // a window of all positions cuts nothing; position - window stays in 32 bits
   a.ws = workspace;
   a.err = device_error_ptr();
+  a.tree = tree;
   cudaError_t e = launch_attn(a, q_dtype == KQ_BF16, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return KQ_ERR_UNSUPPORTED;
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_status(e);
+}
+
+kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
+                         const int32_t* seq_lens, int64_t B, int64_t T, const void* q, int q_dtype, int64_t q_stride,
+                         int32_t n_q_heads, float scale, float softcap, int32_t window, void* out, void* workspace,
+                         size_t workspace_bytes, kq_stream_t stream) {
+  return attn(cache, page_table, max_pages, seq_lens, nullptr, B, T, q, q_dtype, q_stride, n_q_heads, scale, softcap, window,
+              out, workspace, workspace_bytes, stream);
+}
+
+kq_status kq_attn_tree(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
+                       const int32_t* seq_lens, const uint64_t* tree, int64_t B, int64_t T, const void* q, int q_dtype,
+                       int64_t q_stride, int32_t n_q_heads, float scale, float softcap, int32_t window, void* out,
+                       void* workspace, size_t workspace_bytes, kq_stream_t stream) {
+  const kq_status ts = check_tree(tree, B, T);
+  if (ts != KQ_OK) return ts;
+  return attn(cache, page_table, max_pages, seq_lens, tree, B, T, q, q_dtype, q_stride, n_q_heads, scale, softcap, window,
+              out, workspace, workspace_bytes, stream);
+}
+
+static kq_status check_latent(const kq_latent_cache* c) {
+  if (!c) return KQ_ERR_ARG;
+  if (!cache_dtype(c->dtype) || c->n_pages < 0 || c->page_size <= 0 || !good_scale(c->scale)) return KQ_ERR_ARG;
+  if (c->page_size > 1024 || (c->page_size & (c->page_size - 1)) || (c->latent_dim != 256 && c->latent_dim != 512) ||
+      (c->rope_dim != 32 && c->rope_dim != 64) || c->n_pages > INT32_MAX)
+    return KQ_ERR_UNSUPPORTED;
+  if (c->n_pages > 0 && !c->c) return KQ_ERR_ARG;
+  const int es = c->dtype == KQ_BF16 ? 2 : 1;
+  if (!aligned(c->c, 16) || !stride16(c->page_stride, es) || !stride16(c->slot_stride, es)) return KQ_ERR_ALIGN;
+  return KQ_OK;
+}
+
+// The walk; a: the pools' geometry and addresses.
+static kq_status accept(TreeArgs& a, const int32_t* page_table, int64_t max_pages, const int32_t* seq_lens,
+                        const uint64_t* tree, const int32_t* tokens, const int32_t* ids, int64_t B, int64_t T,
+                        int32_t* path, int32_t* count, int32_t* next, int32_t* new_lens, kq_stream_t stream) {
+  const kq_status ts = check_tree(tree, B, T);
+  if (ts != KQ_OK) return ts;
+  if (max_pages < 0) return KQ_ERR_ARG;
+  if (B > 65535) return KQ_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return KQ_OK;
+  if (!seq_lens || !tokens || !ids || (a.n_pools > 0 && max_pages > 0 && !page_table)) return KQ_ERR_ARG;
+  if (new_lens == seq_lens) return KQ_ERR_ARG;
+  for (const void* p : {static_cast<const void*>(page_table), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(tokens), static_cast<const void*>(ids), static_cast<const void*>(path),
+                        static_cast<const void*>(count), static_cast<const void*>(next), static_cast<const void*>(new_lens)})
+    if (!aligned(p, 4)) return KQ_ERR_ALIGN;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.tree = tree;
+  a.tokens = tokens;
+  a.ids = ids;
+  a.path = path;
+  a.count = count;
+  a.next = next;
+  a.new_lens = new_lens;
+  a.B = static_cast<int>(B);
+  a.T = static_cast<int>(T);
+  a.err = device_error_ptr();
+  cudaError_t e = launch_tree_accept(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_status(e);
+}
+
+kq_status kq_tree_accept(const kq_kv_cache* caches, int32_t n_caches, const int32_t* page_table, int64_t max_pages,
+                         const int32_t* seq_lens, const uint64_t* tree, const int32_t* tokens, const int32_t* ids,
+                         int64_t B, int64_t T, int32_t* path, int32_t* count, int32_t* next, int32_t* new_lens,
+                         kq_stream_t stream) {
+  if (n_caches < 0 || (n_caches > 0 && !caches)) return KQ_ERR_ARG;
+  if (2 * int64_t(n_caches) > kMaxPools) return KQ_ERR_UNSUPPORTED;
+  TreeArgs a = {};
+  for (int i = 0; i < n_caches; ++i) {
+    const kq_kv_cache &c = caches[i], &f = caches[0];
+    const kq_status cs = check_cache(&c);
+    if (cs != KQ_OK) return cs;
+    if (c.dtype != f.dtype || c.n_kv_heads != f.n_kv_heads || c.head_dim != f.head_dim || c.page_size != f.page_size ||
+        c.n_pages != f.n_pages || c.page_stride != f.page_stride || c.slot_stride != f.slot_stride ||
+        c.head_stride != f.head_stride)
+      return KQ_ERR_ARG;
+    a.pool[a.n_pools++] = c.k;
+    a.pool[a.n_pools++] = c.v;
+  }
+  if (n_caches > 0) {
+    const kq_kv_cache& f = caches[0];
+    const int es = f.dtype == KQ_BF16 ? 2 : 1;
+    a.n_pages = f.n_pages;
+    a.page_stride = f.page_stride * es;
+    a.slot_stride = f.slot_stride * es;
+    a.head_stride = f.head_stride * es;
+    a.head_cols = f.head_dim * es / 16;
+    if (int64_t(f.n_kv_heads) * a.head_cols * a.n_pools > INT32_MAX - 4096) return KQ_ERR_UNSUPPORTED;
+    a.cols = f.n_kv_heads * a.head_cols;
+    a.page_shift = log2_of(f.page_size);
+  }
+  return accept(a, page_table, max_pages, seq_lens, tree, tokens, ids, B, T, path, count, next, new_lens, stream);
+}
+
+kq_status kq_latent_accept(const kq_latent_cache* caches, int32_t n_caches, const int32_t* page_table,
+                           int64_t max_pages, const int32_t* seq_lens, const uint64_t* tree, const int32_t* tokens,
+                           const int32_t* ids, int64_t B, int64_t T, int32_t* path, int32_t* count, int32_t* next,
+                           int32_t* new_lens, kq_stream_t stream) {
+  if (n_caches < 0 || (n_caches > 0 && !caches)) return KQ_ERR_ARG;
+  if (n_caches > kMaxPools) return KQ_ERR_UNSUPPORTED;
+  TreeArgs a = {};
+  for (int i = 0; i < n_caches; ++i) {
+    const kq_latent_cache &c = caches[i], &f = caches[0];
+    const kq_status cs = check_latent(&c);
+    if (cs != KQ_OK) return cs;
+    if (c.dtype != f.dtype || c.latent_dim != f.latent_dim || c.rope_dim != f.rope_dim || c.page_size != f.page_size ||
+        c.n_pages != f.n_pages || c.page_stride != f.page_stride || c.slot_stride != f.slot_stride)
+      return KQ_ERR_ARG;
+    a.pool[a.n_pools++] = c.c;
+  }
+  if (n_caches > 0) {
+    const kq_latent_cache& f = caches[0];
+    const int es = f.dtype == KQ_BF16 ? 2 : 1;
+    a.n_pages = f.n_pages;
+    a.page_stride = f.page_stride * es;
+    a.slot_stride = f.slot_stride * es;
+    a.cols = a.head_cols = (f.latent_dim + f.rope_dim) * es / 16;
+    a.page_shift = log2_of(f.page_size);
+  }
+  return accept(a, page_table, max_pages, seq_lens, tree, tokens, ids, B, T, path, count, next, new_lens, stream);
+}
+
+kq_status kq_latent_append(const kq_latent_cache* cache, const int32_t* page_table, int64_t max_pages,
+                           const int32_t* seq_lens, const uint64_t* tree, int64_t B, int64_t T, const void* q_latent,
+                           const void* q_rope, const void* c, int x_dtype, int64_t q_latent_stride,
+                           int64_t q_rope_stride, int64_t q_rope_head_stride, int64_t c_stride, int32_t n_heads,
+                           const kq_rope* rope, void* q_out, kq_stream_t stream) {
+  const kq_status cs = check_latent(cache);
+  if (cs != KQ_OK) return cs;
+  if (!rope || rope->q_norm || !float_dtype(x_dtype)) return KQ_ERR_ARG;
+  if (max_pages < 0 || B < 0 || T < 0 || n_heads <= 0 || rope->n_positions < 0) return KQ_ERR_ARG;
+  if (rope->rot_dim != cache->rope_dim) return KQ_ERR_SHAPE;
+  if (tree) {
+    const kq_status ts = check_tree(tree, B, T);
+    if (ts != KQ_OK) return ts;
+  }
+  if (B == 0 || T == 0) return KQ_OK;
+  if (B > INT32_MAX || T > INT32_MAX || B * T > INT32_MAX / (int64_t(n_heads) + 1)) return KQ_ERR_UNSUPPORTED;
+  if (!seq_lens || !q_latent || !q_rope || !c || !q_out || (max_pages > 0 && !page_table) || !rope->cos_sin) return KQ_ERR_ARG;
+  const int xs = x_dtype == KQ_BF16 ? 2 : 4;
+  if (!aligned(q_latent, 16) || !aligned(q_rope, 16) || !aligned(c, 16) || !aligned(q_out, 16) || !aligned(page_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(rope->k_norm, 16) || !aligned(rope->cos_sin, 16) || !stride16(q_latent_stride, xs) ||
+      !stride16(q_rope_stride, xs) || !stride16(q_rope_head_stride, xs) || !stride16(c_stride, xs))
+    return KQ_ERR_ALIGN;
+  LatentAppendArgs a;
+  a.l = *cache;
+  a.rope = *rope;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.tree = tree;
+  a.q_latent = q_latent;
+  a.q_rope = q_rope;
+  a.c = c;
+  a.q_latent_stride = q_latent_stride;
+  a.q_rope_stride = q_rope_stride;
+  a.q_rope_head_stride = q_rope_head_stride;
+  a.c_stride = c_stride;
+  a.q_out = q_out;
+  a.B = static_cast<int>(B);
+  a.T = static_cast<int>(T);
+  a.H = n_heads;
+  a.page_shift = log2_of(cache->page_size);
+  a.err = device_error_ptr();
+  cudaError_t e = launch_latent_append(a, x_dtype == KQ_BF16, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_status(e);
+}
+
+static kq_status check_latent_attn(const kq_latent_cache* cache, int64_t B, int64_t T, int32_t n_heads) {
+  const kq_status cs = check_latent(cache);
+  if (cs != KQ_OK) return cs;
+  if (B < 0 || T < 0 || n_heads <= 0) return KQ_ERR_ARG;
+  return B > 4096 || T > kMaxTree || n_heads > 256 ? KQ_ERR_UNSUPPORTED : KQ_OK;
+}
+
+size_t kq_latent_attn_workspace_size(const kq_latent_cache* cache, int64_t B, int64_t T, int32_t n_heads) {
+  if (check_latent_attn(cache, B, T, n_heads) != KQ_OK) return 0;
+  return latent_workspace_bytes(*cache, T, n_heads);
+}
+
+kq_status kq_latent_attn(const kq_latent_cache* cache, const int32_t* page_table, int64_t max_pages,
+                         const int32_t* seq_lens, const uint64_t* tree, int64_t B, int64_t T, const void* q,
+                         int64_t q_stride, int32_t n_heads, float scale, void* out, void* workspace,
+                         size_t workspace_bytes, kq_stream_t stream) {
+  const kq_status cs = check_latent_attn(cache, B, T, n_heads);
+  if (cs != KQ_OK) return cs;
+  if (max_pages < 0 || !good_scale(scale == 0.0f ? 1.0f : fabsf(scale))) return KQ_ERR_ARG;
+  if (B == 0 || T == 0) return KQ_OK;
+  if (max_pages > INT32_MAX) return KQ_ERR_UNSUPPORTED;
+  const int64_t tiles = (max_pages * cache->page_size + 63) / 64 + 8;  // the line of tiles is counted in 31 bits
+  if (tiles * B > INT32_MAX / ((T * n_heads + 63) / 64)) return KQ_ERR_UNSUPPORTED;
+  if (!seq_lens || !q || !out || (max_pages > 0 && !page_table)) return KQ_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(tree, 8) ||
+      !stride16(q_stride, 2))
+    return KQ_ERR_ALIGN;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < latent_workspace_bytes(*cache, T, n_heads))
+    return KQ_ERR_WORKSPACE;
+  LatentArgs a;
+  a.l = *cache;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.tree = tree;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.scale = scale;
+  a.B = static_cast<int>(B);
+  a.T = static_cast<int>(T);
+  a.H = n_heads;
+  a.page_shift = log2_of(cache->page_size);
+  a.room = static_cast<int>(min_i64(max_pages << a.page_shift, kMaxPositions));
+  a.ws = workspace;
+  a.err = device_error_ptr();
+  cudaError_t e = launch_latent(a, reinterpret_cast<cudaStream_t>(stream));
   if (e == cudaErrorNotSupported) return KQ_ERR_UNSUPPORTED;
   if (e == cudaSuccess) e = cudaGetLastError();
   return cuda_status(e);

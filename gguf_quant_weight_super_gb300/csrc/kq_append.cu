@@ -26,6 +26,7 @@
 // group 53, with six 58, with 256 threads 55; a CTA per token 48, but then 28917
 // tokens of 6 heads, bf16, 46 in place of 28); one token of 48 heads 2.1 us.
 #include "kq_cache.h"
+#include "kq_vec.cuh"
 
 namespace kq {
 namespace {
@@ -33,33 +34,8 @@ namespace {
 constexpr int ATH = 128;  // threads per CTA
 constexpr int ROWS = 3;   // rows per group of lanes at a time
 
-__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xFFFF0000u));
-}
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
-}
-__device__ __forceinline__ void store4(__nv_fp8_e4m3* p, float4 v) {
-  const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v.x, v.y), __NV_SATFINITE, __NV_E4M3);
-  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v.z, v.w), __NV_SATFINITE, __NV_E4M3);
-  *reinterpret_cast<uint32_t*>(p) = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-}
-__device__ __forceinline__ float sq4(float4 v) { return v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w; }
-__device__ __forceinline__ float4 scale4(float4 v, float s, float4 w, float off) {
-  return make_float4(v.x * s * (w.x + off), v.y * s * (w.y + off), v.z * s * (w.z + off), v.w * s * (w.w + off));
-}
-
 // X: q, k, v; O: q_out; C: the cache.  LG = D / 8 lanes hold one row; U rows per group of lanes.
-template <class X, class O, class C, int LG, int U>
+template <class X, class O, class C, int LG, int U, bool TREE>
 __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int D = 8 * LG, NG = ATH / LG;
   pdl_wait();
@@ -96,7 +72,10 @@ __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ App
       x1[i] = load4(src + e1);
     }
   }
-  const int pos = max(__ldg(a.seq_lens + b), 0) - a.T + t;  // below 0, whatever the length: all padding
+  const int len = max(__ldg(a.seq_lens + b), 0);
+  const int slot = len - a.T + t;  // below 0, whatever the length: all padding
+  int pos = slot;
+  if constexpr (TREE) pos = tree_position(tree_bits(__ldg(a.tree + tok), a.T, t, len), a.T, len);
   bool ok = pos >= 0;
   if (ok && rot > 0 && pos >= a.rope.n_positions) {
     if (l == 0) record_error(a.err, DEV_ERR_POSITION);
@@ -105,7 +84,7 @@ __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ App
   int page = -1;
   float4 c = make_float4(1, 1, 1, 1), s = make_float4(0, 0, 0, 0);
   if (ok) {
-    const int64_t pi = pos >> a.page_shift;
+    const int64_t pi = slot >> a.page_shift;
     if (pi < a.max_pages) page = __ldg(a.page_table + b * a.max_pages + pi);
     if (l < rl) {
       const float* cs = a.rope.cos_sin + static_cast<int64_t>(pos) * rot + 4 * l;
@@ -126,16 +105,7 @@ __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ App
       x0[i] = scale4(x0[i], f, load4(nw + e0), a.rope.norm_offset);
       x1[i] = scale4(x1[i], f, load4(nw + e1), a.rope.norm_offset);
     }
-    if ((isq || isk) && l < rl && ok) {
-      const float4 p = x0[i], q = x1[i];
-      if (a.rope.interleaved) {  // pairs (p.x, p.y), (p.z, p.w), (q.x, q.y), (q.z, q.w)
-        x0[i] = make_float4(p.x * c.x - p.y * s.x, p.y * c.x + p.x * s.x, p.z * c.y - p.w * s.y, p.w * c.y + p.z * s.y);
-        x1[i] = make_float4(q.x * c.z - q.y * s.z, q.y * c.z + q.x * s.z, q.z * c.w - q.w * s.w, q.w * c.w + q.z * s.w);
-      } else {
-        x0[i] = make_float4(p.x * c.x - q.x * s.x, p.y * c.y - q.y * s.y, p.z * c.z - q.z * s.z, p.w * c.w - q.w * s.w);
-        x1[i] = make_float4(q.x * c.x + p.x * s.x, q.y * c.y + p.y * s.y, q.z * c.z + p.z * s.z, q.w * c.w + p.w * s.w);
-      }
-    }
+    if ((isq || isk) && l < rl && ok) rotate8(x0[i], x1[i], c, s, a.rope.interleaved);
     if (h >= H) continue;
     if (isq) {
       if (!ok) x0[i] = x1[i] = make_float4(0, 0, 0, 0);
@@ -149,11 +119,11 @@ __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ App
       }
       const int hk = isk ? h - a.Hq : h - a.Hq - Hkv;
       C* dst = static_cast<C*>(isk ? a.c.k : a.c.v) + page * a.c.page_stride +
-               (pos & (a.c.page_size - 1)) * a.c.slot_stride + hk * a.c.head_stride;
+               (slot & (a.c.page_size - 1)) * a.c.slot_stride + hk * a.c.head_stride;
       const float sc = isk ? a.c.k_scale : a.c.v_scale;
       if (sc != 1.0f) {
-        x0[i] = make_float4(x0[i].x / sc, x0[i].y / sc, x0[i].z / sc, x0[i].w / sc);
-        x1[i] = make_float4(x1[i].x / sc, x1[i].y / sc, x1[i].z / sc, x1[i].w / sc);
+        x0[i] = over4(x0[i], sc);
+        x1[i] = over4(x1[i], sc);
       }
       store4(dst + e0, x0[i]);
       store4(dst + e1, x1[i]);
@@ -161,7 +131,7 @@ __global__ void __launch_bounds__(ATH) append_kernel(const __grid_constant__ App
   }
 }
 
-template <class X, class O, class C, int LG>
+template <class X, class O, class C, int LG, bool TREE>
 cudaError_t launch_d(const AppendArgs& a, cudaStream_t st) {
   constexpr int NG = ATH / LG;
   const int H = a.Hq + 2 * a.c.n_kv_heads;
@@ -169,21 +139,22 @@ cudaError_t launch_d(const AppendArgs& a, cudaStream_t st) {
   // several heads per group once that still fills the device (8 CTAs per SM)
   const int64_t few = (tokens * ((H + ROWS - 1) / ROWS) + NG - 1) / NG, one = (tokens * H + NG - 1) / NG;
   if (few >= 8 * num_sms())
-    return launch_pdl(append_kernel<X, O, C, LG, ROWS>, dim3(static_cast<unsigned>(few)), dim3(ATH), 0, st, a);
-  return launch_pdl(append_kernel<X, O, C, LG, 1>, dim3(static_cast<unsigned>(one)), dim3(ATH), 0, st, a);
+    return launch_pdl(append_kernel<X, O, C, LG, ROWS, TREE>, dim3(static_cast<unsigned>(few)), dim3(ATH), 0, st, a);
+  return launch_pdl(append_kernel<X, O, C, LG, 1, TREE>, dim3(static_cast<unsigned>(one)), dim3(ATH), 0, st, a);
 }
 
-template <class X, class O, class C>
+template <class X, class O, class C, bool TREE>
 cudaError_t launch_dim(const AppendArgs& a, cudaStream_t st) {
   switch (a.c.head_dim) {
-    case 64: return launch_d<X, O, C, 8>(a, st);
-    case 128: return launch_d<X, O, C, 16>(a, st);
-    default: return launch_d<X, O, C, 32>(a, st);
+    case 64: return launch_d<X, O, C, 8, TREE>(a, st);
+    case 128: return launch_d<X, O, C, 16, TREE>(a, st);
+    default: return launch_d<X, O, C, 32, TREE>(a, st);
   }
 }
 template <class X, class O>
 cudaError_t launch_c(const AppendArgs& a, cudaStream_t st) {
-  return a.c.dtype == KQ_BF16 ? launch_dim<X, O, __nv_bfloat16>(a, st) : launch_dim<X, O, __nv_fp8_e4m3>(a, st);
+  if (a.c.dtype == KQ_BF16) return a.tree ? launch_dim<X, O, __nv_bfloat16, true>(a, st) : launch_dim<X, O, __nv_bfloat16, false>(a, st);
+  return a.tree ? launch_dim<X, O, __nv_fp8_e4m3, true>(a, st) : launch_dim<X, O, __nv_fp8_e4m3, false>(a, st);
 }
 
 }  // namespace

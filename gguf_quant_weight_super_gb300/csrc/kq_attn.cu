@@ -77,6 +77,8 @@ cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st, AttnShap
   p.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
   p.part = reinterpret_cast<float*>(ws + L.part_off);
   if (to_wide) return launch_attn_wide(p, st, ask);
+  if (a.tree && a.c.dtype == KQ_BF16) return q_bf16 ? launch_attn_tree_bf16_bf16(p, L.rows, st) : launch_attn_tree_bf16_f32(p, L.rows, st);
+  if (a.tree) return q_bf16 ? launch_attn_tree_f8_bf16(p, L.rows, st) : launch_attn_tree_f8_f32(p, L.rows, st);
   if (a.c.dtype == KQ_BF16) return q_bf16 ? launch_attn_bf16_bf16(p, L.rows, st, ask) : launch_attn_bf16_f32(p, L.rows, st, ask);
   return q_bf16 ? launch_attn_f8_bf16(p, L.rows, st, ask) : launch_attn_f8_f32(p, L.rows, st, ask);
 }

@@ -73,6 +73,12 @@ constexpr int START = 3;         // tiles' time that an item costs besides its t
 struct Scratch {
   int scan[NW], last;
 };
+// Trees: what each query row of a pass sees of the drafted tokens, and its position (-1: padding).
+template <int ROWS>
+struct TreeRows {
+  uint64_t bits[ROWS];
+  int pos[ROWS];
+};
 
 template <class Q, class C, int D, int NT>
 struct Cfg {
@@ -95,7 +101,7 @@ struct Cfg {
   static constexpr int CPS = NT * D <= 128 && stages(3) >= 2 ? 3 : stages(2) >= 2 ? 2 : 1;
   static constexpr int S = stages(CPS) < 6 ? stages(CPS) : 6;  // ring stages
   static constexpr int RING = S * NW * STAGE, SMEM = FIXED + RING;
-  static_assert(CPS * (SMEM + 4 * 257 + static_cast<int>(sizeof(Scratch)) + 1024) <= 228 * 1024, "256 sequences: all resident");
+  static_assert(CPS * (SMEM + 4 * 257 + static_cast<int>(sizeof(Scratch) + sizeof(TreeRows<ROWS>)) + 1024) <= 228 * 1024, "256 sequences: all resident");
   static constexpr bool QREG = NT * NQ * (D / 8) <= 32;  // q's operands stay in registers
   static constexpr int OB = (D + 4) * 4;                 // bytes of a row of the warps' sums in shared memory
   static_assert(S >= 2 && S * STAGE >= ROWS * OB, "the warps' sums take the ring's place");
@@ -183,6 +189,35 @@ __device__ __forceinline__ void add4(float4& a, float f, float4 v) {
 }
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
 
+// ---- trees of drafted tokens
+
+// What token t of a tree sees of the drafted tokens, and its position (-1: padding).  With a window the tokens too far
+// before it in the tree are taken out.
+struct TreeToken {
+  uint64_t bits;
+  int pos;
+  __device__ __forceinline__ TreeToken(const AttnArgs& a, int b, int t, int len) {
+    const uint64_t* masks = a.tree + static_cast<int64_t>(b) * a.T;
+    bits = tree_bits(__ldg(masks + t), a.T, t, len);
+    pos = tree_position(bits, a.T, len);
+    if (a.window > 0 && __popcll(bits) > a.window)
+      for (uint64_t rest = bits; rest != 0; rest &= rest - 1) {
+        const int u = __ffsll(static_cast<long long>(rest)) - 1;
+        if (tree_position(tree_bits(__ldg(masks + u), a.T, u, len), a.T, len) <= pos - a.window) bits &= ~(1ull << u);
+      }
+  }
+};
+
+// Whether a token (its position pos; bits: of a tree) sees the slot of position j, base being the first new token's.
+template <bool TREE>
+__device__ __forceinline__ bool sees(int j, int pos, uint64_t bits, int base, int window) {
+  if constexpr (TREE) {
+    const int u = j - base;
+    if (u >= 0) return u < 64 && (bits >> u & 1);
+  }
+  return j <= pos && (window == 0 || j > pos - window);
+}
+
 // One segment: tiles [t0, t1) of one item, for one warp.
 struct Seg {
   const int32_t* table;  // the sequence's pages
@@ -191,9 +226,11 @@ struct Seg {
   int t0, t1;
 };
 
-template <class Q, class C, int D, int NT>
+template <class Q, class C, int D, int NT, bool TREE>
 struct Warp {
   using K = Cfg<Q, C, D, NT>;
+  const uint64_t* tree;  // trees: the rows' bits, in shared memory
+
   // o[n][d]: dims 16 d + ... (M) of rows 8 n + ... (N): registers 0, 1 of the lane's first dim, 2, 3 of its second, for rows
   // 8 n + 2 (lane & 3) and + 1
   float o[NT][D / 16][4];
@@ -324,8 +361,7 @@ struct Warp {
       if (!all) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int j = j0 + 8 * (e >> 1), ps = pos[n][e & 1];
-          if (!(j <= ps && (a.window == 0 || j > ps - a.window))) s[n][e] = -INFINITY;
+          if (!sees<TREE>(j0 + 8 * (e >> 1), pos[n][e & 1], bits_of(n, e & 1, lane), g.len - a.T, a.window)) s[n][e] = -INFINITY;
         }
       }
       float mx[2];
@@ -362,7 +398,7 @@ struct Warp {
         l[n][e] += s[n][e] + s[n][2 + e];
       }
     }
-    if constexpr (CAREFUL) take_out(p, vrow, base, s, pos, lane);
+    if constexpr (CAREFUL) take_out(p, g.len - a.T, vrow, base, s, pos, lane);
     // ---- sums
     uint32_t w[NT][K::NP][2];  // positions 0-7 and 8-15, as the second operand
 #pragma unroll
@@ -426,8 +462,12 @@ struct Warp {
     if constexpr (K::F8) return static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(row)[d]);
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[d]);
   }
+  __device__ __forceinline__ uint64_t bits_of(int n, int e, int lane) const {
+    if constexpr (TREE) return tree[8 * n + 2 * (lane & 3) + e];
+    else return 0;
+  }
   // Adds the values that are not finite to the rows that see them, and puts zeros in their place.
-  __device__ __noinline__ void take_out(const Params& p, uint8_t* vrow, int base, const float (&s)[NT][4],
+  __device__ __noinline__ void take_out(const Params& p, int first_new, uint8_t* vrow, int base, const float (&s)[NT][4],
                                         const int (&pos)[NT][2], int lane) {
     for (int jj = 0; jj < WT; ++jj) {
       const int j = base + jj, from = (jj & 7) * 4 + (lane & 3);
@@ -436,13 +476,13 @@ struct Warp {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float w = __shfl_sync(0xFFFFFFFFu, jj & 8 ? s[n][2 + e] : s[n][e], from);
-          const bool sees = j <= pos[n][e] && (p.a.window == 0 || j > pos[n][e] - p.a.window);
+          const bool seen = sees<TREE>(j, pos[n][e], bits_of(n, e, lane), first_new, p.a.window);
 #pragma unroll
           for (int d = 0; d < D / 16; ++d)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float v = value_at(vrow + jj * K::RB, dim_of(d, h, lane));
-              if (sees && !finite(v)) o[n][d][2 * h + e] += w * v;
+              if (seen && !finite(v)) o[n][d][2 * h + e] += w * v;
             }
         }
     }
@@ -464,7 +504,11 @@ struct Warp {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) { m[n][e] = -INFINITY; l[n][e] = 0.0f; }
+      for (int e = 0; e < 2; ++e) {
+        // a tree's padding rows: weights of 0 wherever masks are not looked at
+        m[n][e] = TREE && pos[n][e] < 0 ? INFINITY : -INFINITY;
+        l[n][e] = 0.0f;
+      }
 #pragma unroll
       for (int d = 0; d < D / 16; ++d)
 #pragma unroll
@@ -490,7 +534,7 @@ struct Warp {
           for (int k2 = 0; k2 < D / 32; ++k2) load_q4(qreg[(i * K::NQ + t) * (D / 32) + k2], qaddr, t, i, k2, lane);
     }
     // a sub-tile in [all_lo, all_hi] is seen by every row in full
-    const int all_lo = p.a.window > 0 ? g.len - p.a.window : 0, all_hi = g.len - p.a.T;
+    const int all_lo = p.a.window > 0 ? g.len - p.a.window : 0, all_hi = g.len - p.a.T - (TREE ? 1 : 0);
     int slot = 0;
     for (int i = 0; i < n; ++i) {
       const int base = b0 + i * TK;
@@ -515,6 +559,12 @@ struct Warp {
         l[i][e] += __shfl_xor_sync(0xFFFFFFFFu, l[i][e], 4);
         l[i][e] += __shfl_xor_sync(0xFFFFFFFFu, l[i][e], 8);
         l[i][e] += __shfl_xor_sync(0xFFFFFFFFu, l[i][e], 16);
+        if (TREE && pos[i][e] < 0) {  // whatever the keys were
+          m[i][e] = -INFINITY;
+          l[i][e] = 0.0f;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) o[i][d][e] = o[i][d][2 + e] = 0.0f;
+        }
       }
   }
   __device__ __forceinline__ bool all_finite() const {
@@ -770,7 +820,7 @@ __device__ __forceinline__ void join_parts(const Params& p, const Line& line, co
 }
 constexpr int JOIN_SUMS = NW * 4 * 32 * 4;  // floats of s_sum
 
-template <class Q, class C, int D, int NT>
+template <class Q, class C, int D, int NT, bool TREE>
 __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(const __grid_constant__ Params p) {
   using K = Cfg<Q, C, D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -818,6 +868,12 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
     g.t1 = end - it.i0 + g.first / TK;
 
     stage_q<Q, C, D, NT>(p, qsm, rscale, it.b, it.hk, r0, warp, lane);
+    __shared__ TreeRows<TREE ? K::ROWS : 1> rows;
+    if (TREE && threadIdx.x < K::ROWS) {
+      const TreeToken x(a, it.b, min((r0 + static_cast<int>(threadIdx.x)) / a.G, a.T - 1), g.len);
+      rows.bits[threadIdx.x] = x.bits;
+      rows.pos[threadIdx.x] = x.pos;
+    }
     __syncthreads();
     int pos[NT][2];
     float qs[NT][2];
@@ -827,14 +883,17 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * n + 2 * (lane & 3) + e;
-        pos[n][e] = g.len - a.T + min((r0 + r) / a.G, a.T - 1);
+        if constexpr (TREE) pos[n][e] = rows.pos[r];
+        else pos[n][e] = g.len - a.T + min((r0 + r) / a.G, a.T - 1);
         qs[n][e] = f * rscale[r];
       }
-    Warp<Q, C, D, NT> w;
+    Warp<Q, C, D, NT, TREE> w;
+    w.tree = rows.bits;
     uint8_t* mine = ring + warp * (K::S * K::STAGE);
     w.template run<false>(p, g, mine, smem_u32(qsm), pos, qs, warp, lane);
     if (!w.all_finite()) {
-      Warp<Q, C, D, NT> again;  // an object of its own: the call in it keeps this one out of registers
+      Warp<Q, C, D, NT, TREE> again;  // an object of its own: the call in it keeps this one out of registers
+      again.tree = rows.bits;
       again.template run<true>(p, g, mine, smem_u32(qsm), pos, qs, warp, lane);
       w = again;
     }
@@ -893,7 +952,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
   }
 }
 
-template <class Q, class C, int D, int NT>
+template <class Q, class C, int D, int NT, bool TREE>
 cudaError_t launch_one(const Params& p, cudaStream_t st, AttnShape* ask) {
   using K = Cfg<Q, C, D, NT>;
   const size_t smem = K::SMEM + 4 * (static_cast<size_t>(p.a.B) + 1);
@@ -901,7 +960,7 @@ cudaError_t launch_one(const Params& p, cudaStream_t st, AttnShape* ask) {
   static int set[64] = {0};  // shared memory allowed so far, per device
   const int dev = current_device_id();
   if (set[dev] < static_cast<int>(smem)) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_kernel<Q, C, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(attn_kernel<Q, C, D, NT, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     set[dev] = static_cast<int>(smem);
@@ -909,33 +968,33 @@ cudaError_t launch_one(const Params& p, cudaStream_t st, AttnShape* ask) {
   // one range per CTA, all of them resident: one that waits for another's place would start when that one has ended
   int ctas = K::CPS;
   if (K::CPS > 1 && smem > fits[dev]) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, attn_kernel<Q, C, D, NT>, NTH, smem);
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, attn_kernel<Q, C, D, NT, TREE>, NTH, smem);
     if (e != cudaSuccess) return e;
     if (ctas >= K::CPS) fits[dev] = smem;
     ctas = ctas < 1 ? 1 : ctas < K::CPS ? ctas : K::CPS;
   }
   if (ask) {
     ask->planned = K::CPS;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ask->resident, attn_kernel<Q, C, D, NT>, NTH, smem);
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ask->resident, attn_kernel<Q, C, D, NT, TREE>, NTH, smem);
   }
   // no more ranges than units that sequences as long as the table can have: CTAs without one only take their places (one of
   // 1000 positions: 9.4 us in place of 9.6)
   const int64_t units = (START + (static_cast<int64_t>(p.a.room) + TK - 1) / TK) * p.a.B * p.a.c.n_kv_heads * p.RT;
   const int grid = static_cast<int>(min_i64(num_sms() * ctas, units));
-  return launch_pdl(attn_kernel<Q, C, D, NT>, dim3(grid), dim3(NTH), smem, st, p);
+  return launch_pdl(attn_kernel<Q, C, D, NT, TREE>, dim3(grid), dim3(NTH), smem, st, p);
 }
 
-template <class Q, class C>
+template <class Q, class C, bool TREE = false>
 cudaError_t launch_kind(const Params& p, int rows, cudaStream_t st, AttnShape* ask) {
   switch (p.a.c.head_dim * 100 + rows) {
-    case 6408: return launch_one<Q, C, 64, 1>(p, st, ask);
-    case 6416: return launch_one<Q, C, 64, 2>(p, st, ask);
-    case 6432: return launch_one<Q, C, 64, 4>(p, st, ask);
-    case 12808: return launch_one<Q, C, 128, 1>(p, st, ask);
-    case 12816: return launch_one<Q, C, 128, 2>(p, st, ask);
-    case 12832: return launch_one<Q, C, 128, 4>(p, st, ask);
-    case 25608: return launch_one<Q, C, 256, 1>(p, st, ask);
-    default: return launch_one<Q, C, 256, 2>(p, st, ask);
+    case 6408: return launch_one<Q, C, 64, 1, TREE>(p, st, ask);
+    case 6416: return launch_one<Q, C, 64, 2, TREE>(p, st, ask);
+    case 6432: return launch_one<Q, C, 64, 4, TREE>(p, st, ask);
+    case 12808: return launch_one<Q, C, 128, 1, TREE>(p, st, ask);
+    case 12816: return launch_one<Q, C, 128, 2, TREE>(p, st, ask);
+    case 12832: return launch_one<Q, C, 128, 4, TREE>(p, st, ask);
+    case 25608: return launch_one<Q, C, 256, 1, TREE>(p, st, ask);
+    default: return launch_one<Q, C, 256, 2, TREE>(p, st, ask);
   }
 }
 
@@ -950,5 +1009,10 @@ cudaError_t launch_attn_bf16_bf16(const attn::Params& p, int rows, cudaStream_t 
 cudaError_t launch_attn_bf16_f32(const attn::Params& p, int rows, cudaStream_t st, AttnShape* ask);
 cudaError_t launch_attn_f8_bf16(const attn::Params& p, int rows, cudaStream_t st, AttnShape* ask);
 cudaError_t launch_attn_f8_f32(const attn::Params& p, int rows, cudaStream_t st, AttnShape* ask);
+// Trees of drafted tokens (kq_attn_tree_<cache>_<query>.cu).
+cudaError_t launch_attn_tree_bf16_bf16(const attn::Params& p, int rows, cudaStream_t st);
+cudaError_t launch_attn_tree_bf16_f32(const attn::Params& p, int rows, cudaStream_t st);
+cudaError_t launch_attn_tree_f8_bf16(const attn::Params& p, int rows, cudaStream_t st);
+cudaError_t launch_attn_tree_f8_f32(const attn::Params& p, int rows, cudaStream_t st);
 
 }  // namespace kq

@@ -87,7 +87,7 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 2, 256;"
 // The two warps of 32 rows.
 __device__ __forceinline__ void rows_sync(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(3 + quarter) : "memory"); }
 
-template <int D>
+template <int D, bool TREE>
 struct Wide {
   using W = WCfg<D>;
   const Params& p;
@@ -249,11 +249,11 @@ struct Wide {
   }
   // r: the row; f: from the raw product to log2 units, or to the cap's argument; extra [D]: what the careful run adds.
   template <bool CAREFUL>
-  __device__ __forceinline__ void softmax(uint32_t lanes, int r, int half, bool active, int pos, float f, float* extra) {
+  __device__ __forceinline__ void softmax(uint32_t lanes, int r, int half, bool active, int pos, uint64_t bits, float f, float* extra) {
     const AttnArgs& a = p.a;
     const int n = g.t1 - g.t0;
-    const int all_lo = a.window > 0 ? g.len - a.window : 0, all_hi = g.len - a.T;
-    m = -INFINITY;
+    const int all_lo = a.window > 0 ? g.len - a.window : 0, all_hi = g.len - a.T - (TREE ? 1 : 0);
+    m = TREE && pos < 0 ? INFINITY : -INFINITY;  // a tree's padding: weights of 0 wherever masks are not looked at
     l = 0.0f;
     for (int i = 0; i < n; ++i) {
       const int gi = tile0 + i, buf = gi & 1, tile = (g.t0 + i) * TK, base = tile + half * HC;
@@ -283,7 +283,7 @@ struct Wide {
         if (tile < all_lo || tile + TK - 1 > all_hi) {
 #pragma unroll
           for (int e = 0; e < HC; ++e)
-            if (!(base + e <= pos && (a.window == 0 || base + e > pos - a.window))) s[e] = -INFINITY;
+            if (!sees<TREE>(base + e, pos, bits, g.len - a.T, a.window)) s[e] = -INFINITY;
         }
         float top[4];
 #pragma unroll
@@ -320,7 +320,7 @@ struct Wide {
           float weights[HC];  // an array of its own: the call keeps it out of registers
 #pragma unroll
           for (int e = 0; e < HC; ++e) weights[e] = s[e];
-          add_bad(p, g, base, pos, weights, extra);
+          add_bad(p, g, base, pos, bits, weights, extra);
         }
         // (P of two tiles ago, in the same columns, is used up: its product was issued before S of this tile)
         uint32_t hi[16], lo[16];
@@ -344,7 +344,7 @@ struct Wide {
     tc_fence_after();
   }
   // The values of a half tile that are not finite, to the row's extra sums if it sees them (weights w).
-  static __device__ __noinline__ void add_bad(const Params& p, Seg g, int base, int pos, const float* w, float* extra) {
+  static __device__ __noinline__ void add_bad(const Params& p, Seg g, int base, int pos, uint64_t bits, const float* w, float* extra) {
     const AttnArgs& a = p.a;
     const int lane = threadIdx.x & 31;
     for (int e = 0; e < HC; ++e) {
@@ -356,16 +356,16 @@ struct Wide {
       bool bad = false;
       for (int d = lane; d < D; d += 32) bad |= !finite(__bfloat162float(v[d]));
       if (!__any_sync(0xFFFFFFFFu, bad)) continue;
-      const bool sees = j <= pos && (a.window == 0 || j > pos - a.window);
+      const bool seen = sees<TREE>(j, pos, bits, g.len - a.T, a.window);
       for (int d = 0; d < D; ++d) {
         const float x = __bfloat162float(v[d]);
-        if (sees && !finite(x)) extra[d] += w[e] * x;
+        if (seen && !finite(x)) extra[d] += w[e] * x;
       }
     }
   }
 };
 
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Params p) {
   using W = WCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -425,18 +425,25 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
     __syncthreads();  // the ring, the sums and tensor memory are free
 
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    int pos = it.len - a.T + t;
+    uint64_t bits = 0;
+    if constexpr (TREE) {
+      const TreeToken x(a, it.b, t, it.len);
+      pos = x.pos;
+      bits = x.bits;
+    }
+    const bool padding = TREE && pos < 0;
     const bool active = warp < 8 && 32 * (warp & 3) < R;
     const float f = a.scale * a.c.k_scale * (a.softcap > 0.0f ? 1.0f / a.softcap : 1.4426950408889634f);
-    Wide<D> w{p, g, bars, ring, tb, tile0, ok, -INFINITY, 0.0f};
+    Wide<D, TREE> w{p, g, bars, ring, tb, tile0, ok, -INFINITY, 0.0f};
     float extra[D];
     bool careful = false;
     for (;;) {
       if (warp < 8) {
         const auto* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(it.b) * a.T + t) * a.q_stride + static_cast<int64_t>(h) * D;
         w.load_q(r < R ? q : nullptr, lanes, half, active);
-        const int pos = it.len - a.T + t;
         if (!careful) {
-          w.template softmax<false>(lanes, r, half, active, pos, f, nullptr);
+          w.template softmax<false>(lanes, r, half, active, pos, bits, f, nullptr);
           if (active) {
             bool bad = false;
 #pragma unroll 1
@@ -448,11 +455,15 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
 #pragma unroll
               for (int i = 0; i < 16; ++i) bad |= !finite(__uint_as_float(v[i]));
             }
-            if (bad && r < R) bars.bad = 1;
+            if (bad && r < R && !padding) bars.bad = 1;
           }
         } else {
           for (int d = 0; d < D; ++d) extra[d] = 0.0f;
-          w.template softmax<true>(lanes, r, half, active, pos, f, extra);
+          w.template softmax<true>(lanes, r, half, active, pos, bits, f, extra);
+        }
+        if (padding) {  // whatever the keys were
+          w.m = -INFINITY;
+          w.l = 0.0f;
         }
         bars.top[0][half][r] = w.l;  // read after the barrier
       } else if (warp < 8 + NLOAD) {
@@ -494,6 +505,7 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
             float4 x = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
             if (careful)
               for (int e = 0; e < 2; ++e) add4(x, 1.0f, *reinterpret_cast<const float4*>(others + (e * kWideRows + r) * D + d + i));
+            if (padding) x = make_float4(0, 0, 0, 0);
             if (r < R) {
               if (whole) put4(out_row(r) + d + i, x, inv);
               else *reinterpret_cast<float4*>(part + d + i) = x;
@@ -519,29 +531,30 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
   if (warp == 8 + NLOAD) tmem_dealloc(tb, COLS);
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t launch_d(const Params& p, cudaStream_t st, AttnShape* ask) {
   using W = WCfg<D>;
   const size_t smem = W::SMEM + 4 * (static_cast<size_t>(p.a.B) + 1);
   static int set[64] = {0};
   const int dev = current_device_id();
   if (set[dev] < static_cast<int>(smem)) {
-    const cudaError_t e = cudaFuncSetAttribute(wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = cudaFuncSetAttribute(wide_kernel<D, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     set[dev] = static_cast<int>(smem);
   }
   if (ask) {
     ask->planned = 1;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ask->resident, wide_kernel<D>, WTH, smem);
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ask->resident, wide_kernel<D, TREE>, WTH, smem);
   }
-  return launch_pdl(wide_kernel<D>, dim3(num_sms()), dim3(WTH), smem, st, p);
+  return launch_pdl(wide_kernel<D, TREE>, dim3(num_sms()), dim3(WTH), smem, st, p);
 }
 
 }  // namespace
 }  // namespace attn
 
 cudaError_t launch_attn_wide(const attn::Params& p, cudaStream_t st, AttnShape* ask) {
-  return p.a.c.head_dim == 64 ? attn::launch_d<64>(p, st, ask) : attn::launch_d<128>(p, st, ask);
+  if (p.a.tree) return p.a.c.head_dim == 64 ? attn::launch_d<64, true>(p, st, ask) : attn::launch_d<128, true>(p, st, ask);
+  return p.a.c.head_dim == 64 ? attn::launch_d<64, false>(p, st, ask) : attn::launch_d<128, false>(p, st, ask);
 }
 
 }  // namespace kq

@@ -21,6 +21,23 @@ enum : int {
 constexpr int kMaxHeadDim = 256;
 inline bool head_dim_supported(int d) { return d == 64 || d == 128 || d == 256; }
 
+// ---- trees of drafted tokens: the T <= 64 newest slots of a sequence hold a tree, a 64-bit mask per token says which of
+// them it sees.  Slots before the sequence's start hold nothing: their bits do not count, their tokens are padding.
+constexpr int kMaxTree = 64;
+__device__ __forceinline__ uint64_t tree_there(int T, int len) {
+  const uint64_t all = ~0ull >> (64 - T);
+  return len >= T ? all : len > 0 ? all & ~0ull << (T - len) : 0;
+}
+// What token t sees of the drafted tokens (0: it is padding).
+__device__ __forceinline__ uint64_t tree_bits(uint64_t mask, int T, int t, int len) {
+  const uint64_t there = tree_there(T, len);
+  return there >> t & 1 ? mask & there : 0;
+}
+// Its position: the tokens that it sees stand in a row after the context.  -1: padding.
+__device__ __forceinline__ int tree_position(uint64_t bits, int T, int len) {
+  return bits ? max(len - T, 0) + __popcll(bits) - 1 : -1;
+}
+
 struct AppendArgs {
   kq_kv_cache c;
   kq_rope rope;
@@ -33,6 +50,7 @@ struct AppendArgs {
   int B, T, Hq;
   int page_shift;
   int* err;
+  const uint64_t* tree;  // [B][T] masks, or NULL: a chain
 };
 cudaError_t launch_kv_append(const AppendArgs& a, int x_bf16, int out_bf16, cudaStream_t st);
 
@@ -51,6 +69,7 @@ struct AttnArgs {
   int room;  // positions that a sequence can have
   void* ws;
   int* err;
+  const uint64_t* tree;  // [B][T] masks, or NULL: a chain
 };
 // Positions are counted in 32 bits, tiles and copies ahead of the last one included.
 constexpr int64_t kMaxPositions = INT32_MAX - 4095;
@@ -60,6 +79,59 @@ struct AttnShape {
   int planned, resident;
 };
 cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st, AttnShape* ask = nullptr);
+
+// A verified tree's walk, and the accepted branch's slots of up to kMaxPools pools of one geometry (strides in bytes).
+constexpr int kMaxPools = 256;
+struct TreeArgs {
+  const int32_t* page_table;
+  int64_t max_pages;
+  const int32_t* seq_lens;
+  const uint64_t* tree;
+  const int32_t *tokens, *ids;
+  int32_t *path, *count, *next, *new_lens;
+  int B, T;
+  int page_shift;
+  int* err;
+  int64_t n_pages, page_stride, slot_stride, head_stride;
+  int n_pools, cols, head_cols;  // 16-byte columns of a slot, and of one of its heads
+  void* pool[kMaxPools];
+};
+cudaError_t launch_tree_accept(const TreeArgs& a, cudaStream_t st);
+
+struct LatentAppendArgs {
+  kq_latent_cache l;
+  kq_rope rope;
+  const int32_t* page_table;
+  int64_t max_pages;
+  const int32_t* seq_lens;
+  const uint64_t* tree;  // or NULL
+  const void *q_latent, *q_rope, *c;
+  int64_t q_latent_stride, q_rope_stride, q_rope_head_stride, c_stride;
+  void* q_out;
+  int B, T, H;
+  int page_shift;
+  int* err;
+};
+cudaError_t launch_latent_append(const LatentAppendArgs& a, int x_bf16, cudaStream_t st);
+
+struct LatentArgs {
+  kq_latent_cache l;
+  const int32_t* page_table;
+  int64_t max_pages;
+  const int32_t* seq_lens;
+  const uint64_t* tree;  // or NULL
+  const void* q;
+  int64_t q_stride;
+  void* out;
+  float scale;
+  int B, T, H;
+  int page_shift;
+  int room;  // positions that a sequence can have
+  void* ws;
+  int* err;
+};
+size_t latent_workspace_bytes(const kq_latent_cache& l, int64_t T, int H);
+cudaError_t launch_latent(const LatentArgs& a, cudaStream_t st);
 
 struct SampleArgs {
   const void* logits;

@@ -56,6 +56,17 @@ SIGNATURES = {
                             ctypes.c_float, ctypes.c_int32, _P, _P, _SZ, _P]),
     "kq_selftest_attn_ctas": (_I, [_P, _I64, _I64, _I, ctypes.c_int32, ctypes.POINTER(ctypes.c_int),
                                    ctypes.POINTER(ctypes.c_int)]),
+    "kq_kv_append_tree": (_I, [_P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P, _I, _I64, _I64, _I64, ctypes.c_int32, _P, _P,
+                               _I, _P]),
+    "kq_attn_tree_workspace_size": (_SZ, [_P, _I64, _I64, ctypes.c_int32]),
+    "kq_attn_tree": (_I, [_P, _P, _I64, _P, _P, _I64, _I64, _P, _I, _I64, ctypes.c_int32, ctypes.c_float, ctypes.c_float,
+                          ctypes.c_int32, _P, _P, _SZ, _P]),
+    "kq_tree_accept": (_I, [_P, ctypes.c_int32, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P]),
+    "kq_latent_accept": (_I, [_P, ctypes.c_int32, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P]),
+    "kq_latent_append": (_I, [_P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _I64, ctypes.c_int32, _P,
+                              _P, _P]),
+    "kq_latent_attn_workspace_size": (_SZ, [_P, _I64, _I64, ctypes.c_int32]),
+    "kq_latent_attn": (_I, [_P, _P, _I64, _P, _P, _I64, _I64, _P, _I64, ctypes.c_int32, ctypes.c_float, _P, _P, _SZ, _P]),
     "kq_sample_workspace_size": (_SZ, [_I64, _I64]),
     "kq_sample": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "kq_device_error": (_I, [ctypes.POINTER(ctypes.c_int), _I]),
@@ -518,7 +529,7 @@ def kq_sample(logits, dtype, row_stride, M, V, u, temperature, top_k, top_p, min
 # looked up once, in line.
 
 _DTYPE_CODE = {torch.float32: KQ_F32, torch.bfloat16: KQ_BF16}
-_f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
+_f32, _i32, _i64, _u8 = torch.float32, torch.int32, torch.int64, torch.uint8
 
 
 def _row_stride(name: str, x: torch.Tensor, B: int, T: int, heads: int, D: int) -> int:
@@ -629,6 +640,289 @@ def attn_decode(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor
         workspace.data_ptr(), workspace.numel(), _here() if stream is None else _stream(stream))
     if status:
         raise KQError("kq_attn_decode", status)
+    return out
+
+
+# ---- trees of drafted tokens, and latent caches
+
+def kq_kv_append_tree(cache, page_table, max_pages, seq_lens, tree, B, T, q, k, v, x_dtype, q_stride, k_stride, v_stride,
+                      n_q_heads, rope, q_out, q_out_dtype, stream=None):
+    _check("kq_kv_append_tree", lib().kq_kv_append_tree(cache, _ptr(page_table), max_pages, _ptr(seq_lens), _ptr(tree), B, T,
+                                                        _ptr(q), _ptr(k), _ptr(v), x_dtype, q_stride, k_stride, v_stride,
+                                                        n_q_heads, rope, _ptr(q_out), q_out_dtype, _stream(stream)))
+
+
+def kq_attn_tree_workspace_size(cache, B, T, n_q_heads) -> int:
+    return lib().kq_attn_tree_workspace_size(cache, B, T, n_q_heads)
+
+
+def kq_attn_tree(cache, page_table, max_pages, seq_lens, tree, B, T, q, q_dtype, q_stride, n_q_heads, scale, softcap, window,
+                 out, workspace, workspace_bytes, stream=None):
+    _check("kq_attn_tree", lib().kq_attn_tree(cache, _ptr(page_table), max_pages, _ptr(seq_lens), _ptr(tree), B, T, _ptr(q),
+                                              q_dtype, q_stride, n_q_heads, scale, softcap, window, _ptr(out),
+                                              _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def kq_tree_accept(caches, n_caches, page_table, max_pages, seq_lens, tree, tokens, ids, B, T, path, count, next_ids, new_lens,
+                   stream=None):
+    _check("kq_tree_accept", lib().kq_tree_accept(caches, n_caches, _ptr(page_table), max_pages, _ptr(seq_lens), _ptr(tree),
+                                                  _ptr(tokens), _ptr(ids), B, T, _ptr(path), _ptr(count), _ptr(next_ids),
+                                                  _ptr(new_lens), _stream(stream)))
+
+
+def kq_latent_accept(caches, n_caches, page_table, max_pages, seq_lens, tree, tokens, ids, B, T, path, count, next_ids,
+                     new_lens, stream=None):
+    _check("kq_latent_accept", lib().kq_latent_accept(caches, n_caches, _ptr(page_table), max_pages, _ptr(seq_lens),
+                                                      _ptr(tree), _ptr(tokens), _ptr(ids), B, T, _ptr(path), _ptr(count),
+                                                      _ptr(next_ids), _ptr(new_lens), _stream(stream)))
+
+
+def kq_latent_append(cache, page_table, max_pages, seq_lens, tree, B, T, q_latent, q_rope, c, x_dtype, q_latent_stride,
+                     q_rope_stride, q_rope_head_stride, c_stride, n_heads, rope, q_out, stream=None):
+    _check("kq_latent_append", lib().kq_latent_append(cache, _ptr(page_table), max_pages, _ptr(seq_lens), _ptr(tree), B, T,
+                                                      _ptr(q_latent), _ptr(q_rope), _ptr(c), x_dtype, q_latent_stride,
+                                                      q_rope_stride, q_rope_head_stride, c_stride, n_heads, rope,
+                                                      _ptr(q_out), _stream(stream)))
+
+
+def kq_latent_attn_workspace_size(cache, B, T, n_heads) -> int:
+    return lib().kq_latent_attn_workspace_size(cache, B, T, n_heads)
+
+
+def kq_latent_attn(cache, page_table, max_pages, seq_lens, tree, B, T, q, q_stride, n_heads, scale, out, workspace,
+                   workspace_bytes, stream=None):
+    _check("kq_latent_attn", lib().kq_latent_attn(cache, _ptr(page_table), max_pages, _ptr(seq_lens), _ptr(tree), B, T,
+                                                  _ptr(q), q_stride, n_heads, scale, _ptr(out), _ptr(workspace),
+                                                  workspace_bytes, _stream(stream)))
+
+
+class KqLatentCache(ctypes.Structure):
+    """struct kq_latent_cache of include/kq.h."""
+    _fields_ = [("dtype", ctypes.c_int32), ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("c", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
+class LatentCache:
+    """A layer's latent cache: c [n_pages, page_size, latent_dim + rope_dim], bfloat16 or float8_e4m3fn (stored values times
+    scale), of any strides but a contiguous last dimension.  Holds the tensor."""
+
+    def __init__(self, c: torch.Tensor, latent_dim: int, scale: float = 1.0):
+        if c.dim() != 3 or c.stride(2) != 1 or not 0 < latent_dim < c.shape[2]:
+            raise ValueError("c: [n_pages, page_size, latent_dim + rope_dim], last dimension contiguous")
+        if c.dtype not in _CACHE_TYPES:
+            raise TypeError("a cache is bfloat16 or float8_e4m3fn")
+        self.c, self.scale = c, float(scale)
+        self.latent_dim, self.rope_dim = latent_dim, c.shape[2] - latent_dim
+        self.struct = KqLatentCache(_CACHE_TYPES[c.dtype], latent_dim, self.rope_dim, c.shape[1], c.shape[0], c.stride(0),
+                                    c.stride(1), _ptr(c), self.scale)
+        self._ref = ctypes.addressof(self.struct)
+
+
+class CacheSet:
+    """The caches of all layers, all KVCache or all LatentCache, for tree_accept.  Holds them."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        kinds = {type(c) for c in self.caches}
+        if len(kinds) > 1 or not kinds <= {KVCache, LatentCache}:
+            raise TypeError("caches are all KVCache or all LatentCache")
+        self.latent = kinds == {LatentCache}
+        kind = KqLatentCache if self.latent else KqKvCache
+        self._array = (kind * len(self.caches))(*(c.struct for c in self.caches))
+        self._ref, self.n = (ctypes.addressof(self._array) if self.caches else None), len(self.caches)
+
+
+def _tables(page_table, seq_lens, tree, B, T):
+    """Checks the tensors that say where a call's tokens are; whether all are device tensors, and the table's width."""
+    rows, W = page_table.shape
+    if page_table.dtype is not _i32 or rows != B or not page_table.is_contiguous():
+        raise ValueError(f"page_table: contiguous int32 [{B}, max_pages]")
+    if seq_lens.dtype is not _i32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
+        raise ValueError(f"seq_lens: contiguous int32 [{B}]")
+    if tree is not None and (tree.dtype is not _i64 or tree.shape != (B, T) or not tree.is_contiguous()):
+        raise ValueError(f"tree: contiguous int64 [{B}, {T}]")
+    return page_table.is_cuda and seq_lens.is_cuda and (tree is None or tree.is_cuda), W
+
+
+def kv_append_tree(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, tree: torch.Tensor, q: torch.Tensor,
+                   k: torch.Tensor, v: torch.Tensor, rope: RopeNorm, q_out: torch.Tensor | None = None,
+                   q_out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """kv_append of drafted tokens that form a tree (kq_kv_append_tree): tree [B, T] int64, bit u of a token's mask: it sees
+    drafted token u."""
+    shape, kv_shape, D, heads, dtype = q.shape, k.shape, cache.head_dim, cache.n_kv_heads, q.dtype
+    if len(shape) != 4 or shape[3] != D:
+        raise ValueError(f"q: [B, T, heads, {D}], not {list(shape)}")
+    B, T, Hq, _ = shape
+    if kv_shape != (B, T, heads, D) or v.shape != kv_shape or k.dtype is not dtype or v.dtype is not dtype:
+        raise ValueError(f"k and v: [{B}, {T}, {heads}, {D}], of q's type")
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
+        raise TypeError("q, k and v are float32 or bfloat16")
+    if rope.norm_dim != 0 and rope.norm_dim != D:
+        raise ValueError("norm weights: [head_dim]")
+    if q_out is None:
+        q_out = _new(stream, torch.empty, shape, dtype=q_out_dtype, device=q.device)
+    elif q_out.shape != shape or not q_out.is_contiguous():
+        raise ValueError("q_out: contiguous, of q's shape")
+    out_code = _DTYPE_CODE.get(q_out.dtype)
+    if out_code is None:
+        raise TypeError("q_out is float32 or bfloat16")
+    cuda, W = _tables(page_table, seq_lens, tree, B, T)
+    if not (cuda and q.is_cuda and k.is_cuda and v.is_cuda and q_out.is_cuda):
+        raise _host()
+    status = (_lib or lib()).kq_kv_append_tree(
+        cache._ref, page_table.data_ptr(), W, seq_lens.data_ptr(), tree.data_ptr(), B, T, q.data_ptr(), k.data_ptr(),
+        v.data_ptr(), code, Hq * D if q.is_contiguous() else _row_stride("q", q, B, T, Hq, D),
+        heads * D if k.is_contiguous() else _row_stride("k", k, B, T, heads, D),
+        heads * D if v.is_contiguous() else _row_stride("v", v, B, T, heads, D), Hq,
+        rope._ref, q_out.data_ptr(), out_code, _here() if stream is None else _stream(stream))
+    if status:
+        raise KQError("kq_kv_append_tree", status)
+    return q_out
+
+
+def attn_tree_workspace(cache: KVCache, B: int, T: int, n_q_heads: int) -> torch.Tensor:
+    """A zero-filled workspace tensor for attn_tree, with room for smaller T and for attn_decode too."""
+    n = kq_attn_tree_workspace_size(cache._ref, B, T, n_q_heads)
+    if n == 0:
+        raise KQError("kq_attn_tree_workspace_size", -4)
+    return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)
+
+
+def attn_tree(cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, tree: torch.Tensor, q: torch.Tensor,
+              workspace: torch.Tensor, scale: float | None = None, softcap: float = 0.0, window: int = 0,
+              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """attn_decode of drafted tokens that form a tree (kq_attn_tree), tree [B, T] int64 masks, T up to 64."""
+    shape, D, dtype = q.shape, cache.head_dim, q.dtype
+    if len(shape) != 4 or shape[3] != D:
+        raise ValueError(f"q: [B, T, heads, {D}], not {list(shape)}")
+    B, T, Hq, _ = shape
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
+        raise TypeError("q is float32 or bfloat16")
+    if out is None:
+        out = _new(stream, torch.empty, shape, dtype=dtype, device=q.device)
+    elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
+        raise ValueError("out: contiguous, of q's shape and type")
+    cuda, W = _tables(page_table, seq_lens, tree, B, T)
+    if workspace.dtype is not _u8 or not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous uint8")
+    if not (cuda and q.is_cuda and out.is_cuda and workspace.is_cuda):
+        raise _host()
+    status = (_lib or lib()).kq_attn_tree(
+        cache._ref, page_table.data_ptr(), W, seq_lens.data_ptr(), tree.data_ptr(), B, T, q.data_ptr(), code,
+        Hq * D if q.is_contiguous() else _row_stride("q", q, B, T, Hq, D), Hq, D ** -0.5 if scale is None else scale, softcap,
+        window, out.data_ptr(), workspace.data_ptr(), workspace.numel(), _here() if stream is None else _stream(stream))
+    if status:
+        raise KQError("kq_attn_tree", status)
+    return out
+
+
+def tree_accept(caches: CacheSet, page_table: torch.Tensor, seq_lens: torch.Tensor, tree: torch.Tensor, tokens: torch.Tensor,
+                ids: torch.Tensor, path=None, count=None, next_ids=None, new_lens=None, stream=None):
+    """The walk along a verified tree and the accepted branch's slots moved together in all layers' caches (kq_tree_accept,
+    kq_latent_accept): tokens [B, T] int32 the nodes' words, ids [B, T] int32 the model's word after each node.  Returns
+    (path [B, T], count [B], next_ids [B], new_lens [B]), int32."""
+    B, T = shape = tree.shape
+    cuda, W = _tables(page_table, seq_lens, tree, B, T)
+    if path is None:
+        path = _new(stream, torch.empty, (B, T), dtype=_i32, device=tree.device)
+    if count is None:
+        count = _new(stream, torch.empty, B, dtype=_i32, device=tree.device)
+    if next_ids is None:
+        next_ids = _new(stream, torch.empty, B, dtype=_i32, device=tree.device)
+    if new_lens is None:
+        new_lens = _new(stream, torch.empty, B, dtype=_i32, device=tree.device)
+    for x, want in ((tokens, shape), (ids, shape), (path, shape), (count, shape[:1]), (next_ids, shape[:1]), (new_lens, shape[:1])):
+        if x.dtype is not _i32 or x.shape != want or not x.is_contiguous():
+            raise ValueError(f"tokens, ids, path: contiguous int32 [{B}, {T}]; count, next_ids, new_lens: [{B}]")
+        cuda = cuda and x.is_cuda
+    if not cuda:
+        raise _host()
+    name = "kq_latent_accept" if caches.latent else "kq_tree_accept"
+    status = getattr(_lib or lib(), name)(
+        caches._ref, caches.n, page_table.data_ptr(), W, seq_lens.data_ptr(), tree.data_ptr(), tokens.data_ptr(),
+        ids.data_ptr(), B, T, path.data_ptr(), count.data_ptr(), next_ids.data_ptr(), new_lens.data_ptr(),
+        _here() if stream is None else _stream(stream))
+    if status:
+        raise KQError(name, status)
+    return path, count, next_ids, new_lens
+
+
+def latent_append(cache: LatentCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q_latent: torch.Tensor,
+                  q_rope: torch.Tensor, c: torch.Tensor, rope: RopeNorm, tree: torch.Tensor | None = None,
+                  q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kq_latent_append for q_latent [B, T, heads, latent_dim], q_rope [B, T, heads, rope_dim] (a view into the queries'
+    product will do) and c [B, T, latent_dim + rope_dim]; rope's k_norm norms the latent.  Returns q_out
+    [B, T, heads, latent_dim + rope_dim] bfloat16."""
+    shape, C, R, dtype = q_latent.shape, cache.latent_dim, cache.rope_dim, q_latent.dtype
+    if len(shape) != 4 or shape[3] != C:
+        raise ValueError(f"q_latent: [B, T, heads, {C}], not {list(shape)}")
+    B, T, H, _ = shape
+    if q_rope.shape != (B, T, H, R) or c.shape != (B, T, C + R) or q_rope.dtype is not dtype or c.dtype is not dtype:
+        raise ValueError(f"q_rope: [{B}, {T}, {H}, {R}], c: [{B}, {T}, {C + R}], of q_latent's type")
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
+        raise TypeError("q_latent, q_rope and c are float32 or bfloat16")
+    if rope.q_norm is not None or (rope.norm_dim != 0 and rope.norm_dim != C):
+        raise ValueError("norm weights: k_norm [latent_dim]")
+    if q_out is None:
+        q_out = _new(stream, torch.empty, (B, T, H, C + R), dtype=torch.bfloat16, device=c.device)
+    elif q_out.shape != (B, T, H, C + R) or q_out.dtype is not torch.bfloat16 or not q_out.is_contiguous():
+        raise ValueError(f"q_out: contiguous bfloat16 [{B}, {T}, {H}, {C + R}]")
+    s0, s1, s2, s3 = q_rope.stride()
+    if s3 != 1 or (s0 != T * s1 and B > 1 and T > 1):
+        raise ValueError("q_rope: tokens at one stride, values contiguous")
+    cuda, W = _tables(page_table, seq_lens, tree, B, T)
+    if not (cuda and q_latent.is_cuda and q_rope.is_cuda and c.is_cuda and q_out.is_cuda):
+        raise _host()
+    status = (_lib or lib()).kq_latent_append(
+        cache._ref, page_table.data_ptr(), W, seq_lens.data_ptr(), None if tree is None else tree.data_ptr(), B, T,
+        q_latent.data_ptr(), q_rope.data_ptr(), c.data_ptr(), code,
+        H * C if q_latent.is_contiguous() else _row_stride("q_latent", q_latent, B, T, H, C),
+        s1 if T > 1 else s0 if B > 1 else 0, s2 if H > 1 else 0,
+        C + R if c.is_contiguous() else _row_stride("c", c.unsqueeze(2), B, T, 1, C + R), H, rope._ref, q_out.data_ptr(),
+        _here() if stream is None else _stream(stream))
+    if status:
+        raise KQError("kq_latent_append", status)
+    return q_out
+
+
+def latent_attn_workspace(cache: LatentCache, B: int, T: int, n_heads: int) -> torch.Tensor:
+    """A zero-filled workspace tensor for latent_attn."""
+    n = kq_latent_attn_workspace_size(cache._ref, B, T, n_heads)
+    if n == 0:
+        raise KQError("kq_latent_attn_workspace_size", -4)
+    return torch.zeros(n, dtype=torch.uint8, device=cache.c.device)
+
+
+def latent_attn(cache: LatentCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor,
+                workspace: torch.Tensor, scale: float, tree: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """kq_latent_attn for q [B, T, heads, latent_dim + rope_dim] bfloat16; scale: the expanded heads'.  Returns out
+    [B, T, heads, latent_dim] bfloat16."""
+    shape, C, W = q.shape, cache.latent_dim, cache.latent_dim + cache.rope_dim
+    if len(shape) != 4 or shape[3] != W:
+        raise ValueError(f"q: [B, T, heads, {W}], not {list(shape)}")
+    if q.dtype is not torch.bfloat16:
+        raise TypeError("q is bfloat16")
+    B, T, H, _ = shape
+    if out is None:
+        out = _new(stream, torch.empty, (B, T, H, C), dtype=torch.bfloat16, device=q.device)
+    elif out.shape != (B, T, H, C) or out.dtype is not torch.bfloat16 or not out.is_contiguous():
+        raise ValueError(f"out: contiguous bfloat16 [{B}, {T}, {H}, {C}]")
+    cuda, pages = _tables(page_table, seq_lens, tree, B, T)
+    if workspace.dtype is not _u8 or not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous uint8")
+    if not (cuda and q.is_cuda and out.is_cuda and workspace.is_cuda):
+        raise _host()
+    status = (_lib or lib()).kq_latent_attn(
+        cache._ref, page_table.data_ptr(), pages, seq_lens.data_ptr(), None if tree is None else tree.data_ptr(), B, T,
+        q.data_ptr(), H * W if q.is_contiguous() else _row_stride("q", q, B, T, H, W), H, scale, out.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _here() if stream is None else _stream(stream))
+    if status:
+        raise KQError("kq_latent_attn", status)
     return out
 
 

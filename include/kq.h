@@ -534,6 +534,138 @@ kq_status kq_selftest_attn_ctas(const kq_kv_cache *cache, int64_t B, int64_t T, 
                                 int *planned, int *resident);
 
 /*
+ * Trees of drafted tokens.  The T newest tokens of a sequence (1..64) may form a
+ * tree instead of a chain: token t lies in slot seq_lens[b] - T + t as before,
+ * and bit u of tree[b][t] says whether it sees drafted token u.  A node of a tree
+ * sees its ancestors and itself; any other sets of bits are allowed too.  With
+ * base = max(seq_lens[b] - T, 0), the length of the context, a token's position
+ * is base + (the bits set) - 1: what it sees stands in a row after the context.
+ * Bits u >= T, and those of slots before the sequence's start, do not count; a
+ * token without bits, or in such a slot, is padding.  tree [B][T], 8-byte aligned.
+ *
+ * kq_kv_append_tree: kq_kv_append, with the rotation of each token's position.
+ * T in 1..64 (else KQ_ERR_UNSUPPORTED).
+ *
+ * kq_attn_tree: kq_attn_decode, where a token sees the whole context and the
+ * drafted tokens of its bits, with window > 0 those whose position is above its
+ * own less window.  Padding gets zeros.  T in 0..64; kq_attn_tree_workspace_size
+ * has the size for it, in which a call of kq_attn_decode with that T or a smaller
+ * one, and the same heads, has room too.
+ */
+kq_status kq_kv_append_tree(const kq_kv_cache *cache, const int32_t *page_table, int64_t max_pages,
+                            const int32_t *seq_lens, const uint64_t *tree, int64_t B, int64_t T, const void *q,
+                            const void *k, const void *v, int x_dtype, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, int32_t n_q_heads, const kq_rope *rope, void *q_out, int q_out_dtype,
+                            kq_stream_t stream);
+
+size_t kq_attn_tree_workspace_size(const kq_kv_cache *cache, int64_t B, int64_t T, int32_t n_q_heads);
+
+kq_status kq_attn_tree(const kq_kv_cache *cache, const int32_t *page_table, int64_t max_pages,
+                       const int32_t *seq_lens, const uint64_t *tree, int64_t B, int64_t T, const void *q, int q_dtype,
+                       int64_t q_stride, int32_t n_q_heads, float scale, float softcap, int32_t window, void *out,
+                       void *workspace, size_t workspace_bytes, kq_stream_t stream);
+
+/*
+ * A latent cache: one vector per token that serves all heads as key and, but for
+ * its rope part, as value (the absorbed form of attention over keys and values
+ * that are products of that vector).  One pool of n_pages pages; slot s of page p
+ * holds latent_dim + rope_dim values from p*page_stride + s*slot_stride elements
+ * on.  dtype KQ_BF16, or KQ_F8E4M3: a stored value stands for itself times scale.
+ * latent_dim 256 or 512, rope_dim 32 or 64.  Page sizes, alignment, page tables
+ * and lengths as for kq_kv_cache.
+ */
+typedef struct kq_latent_cache {
+  int32_t dtype;
+  int32_t latent_dim;
+  int32_t rope_dim;
+  int32_t page_size;
+  int64_t n_pages;
+  int64_t page_stride, slot_stride;
+  void *c;
+  float scale;
+} kq_latent_cache;
+
+/*
+ * The walk along a verified tree and the move of the accepted branch, in one
+ * launch for the caches of all layers.
+ *   tokens [B][T]  the drafted words of the tree's nodes
+ *   ids    [B][T]  the word that the model chose after each node
+ * Node 0 is the root, a known word.  From it on, the walk goes from a node to its
+ * child with the word that the model chose after the node, the first of them if
+ * there are several, until there is none.  Children come after their parent and
+ * have its bits and their own.
+ *   path     [B][T]  the nodes passed, the root first; -1 behind them
+ *   count    [B]     how many there are; 0 where the root is padding
+ *   next     [B]     the word after the last one: the next step's root; -1 with 0
+ *   new_lens [B]     base + count: the sequences' lengths now (not seq_lens itself)
+ * each int32, NULL for off.  In every cache the nodes' keys and values are moved
+ * from slots base + path[i] to base + i, where a chain's would lie.  n_caches 0
+ * does the walk alone (then page_table may be NULL).
+ * The caches are alike but for their pools (else KQ_ERR_ARG), at most 128 (256
+ * latent ones), B <= 65535, T in 1..64 (else KQ_ERR_UNSUPPORTED).  No two tokens
+ * of a call share a slot.
+ */
+kq_status kq_tree_accept(const kq_kv_cache *caches, int32_t n_caches, const int32_t *page_table, int64_t max_pages,
+                         const int32_t *seq_lens, const uint64_t *tree, const int32_t *tokens, const int32_t *ids,
+                         int64_t B, int64_t T, int32_t *path, int32_t *count, int32_t *next, int32_t *new_lens,
+                         kq_stream_t stream);
+
+kq_status kq_latent_accept(const kq_latent_cache *caches, int32_t n_caches, const int32_t *page_table,
+                           int64_t max_pages, const int32_t *seq_lens, const uint64_t *tree, const int32_t *tokens,
+                           const int32_t *ids, int64_t B, int64_t T, int32_t *path, int32_t *count, int32_t *next,
+                           int32_t *new_lens, kq_stream_t stream);
+
+/*
+ * The write of T new tokens' vectors into a latent cache, and the queries that go
+ * with them, in one launch.  tree NULL: a chain, T of any size; else T in 1..64.
+ *   c        [B*T] rows of latent_dim + rope_dim values, c_stride elements apart:
+ *            the latent gets k_norm's norm (with eps, norm_offset), the rope part
+ *            the rotation of the token's position; then both go to its slot
+ *   q_latent [B*T] rows of n_heads*latent_dim: the queries' products with each
+ *            head's key expansion; they pass as they are
+ *   q_rope   head h of row i starts i*q_rope_stride + h*q_rope_head_stride
+ *            elements in: rope_dim values, which are rotated
+ *   x_dtype  KQ_F32 or KQ_BF16 (all three)
+ *   q_out    [B*T][n_heads][latent_dim + rope_dim] KQ_BF16
+ * rope: k_norm [latent_dim] or NULL, q_norm NULL, rot_dim equal to rope_dim (else
+ * KQ_ERR_ARG; KQ_ERR_SHAPE for rot_dim).  Rounding, padding and positions outside
+ * the table as in kq_kv_append.  Inputs 16-byte aligned, strides multiples of 16
+ * bytes.  B*T*(n_heads + 1) < 2^31.
+ */
+kq_status kq_latent_append(const kq_latent_cache *cache, const int32_t *page_table, int64_t max_pages,
+                           const int32_t *seq_lens, const uint64_t *tree, int64_t B, int64_t T, const void *q_latent,
+                           const void *q_rope, const void *c, int x_dtype, int64_t q_latent_stride,
+                           int64_t q_rope_stride, int64_t q_rope_head_stride, int64_t c_stride, int32_t n_heads,
+                           const kq_rope *rope, void *q_out, kq_stream_t stream);
+
+/*
+ * Attention of the newest T tokens (0..64) of each sequence over a latent cache:
+ *   s_j = scale * q.c_j        over latent_dim + rope_dim values
+ *   out = sum_j softmax(s)_j c_j[0 .. latent_dim)
+ * where the token at position p sees positions j <= p (tree NULL), or what a
+ * tree's token sees.  A token that sees nothing gets zeros.  scale is finite; it
+ * is that of the expanded heads, as the latent's size does not give it.  What a
+ * token gets that sees a vector with values that are not finite is not specified;
+ * tokens that do not see it are not influenced.
+ *   q   [B*T] rows of n_heads*(latent_dim + rope_dim) KQ_BF16, q_stride elements apart
+ *   out [B*T][n_heads][latent_dim] KQ_BF16
+ * Scores, softmax statistics, sums and partial results are held in fp32; the
+ * weights enter their product as bf16 (2^-8 of each), their sum in fp32.
+ * Repeated calls give identical outputs.  workspace: kq_latent_attn_workspace_size
+ * bytes, 256-byte aligned, zero-filled once before first use; one call at a time
+ * per workspace; a workspace serves any calls that it is large enough for.
+ * q and out 16-byte aligned, q_stride a multiple of 16 bytes.  B <= 4096,
+ * n_heads <= 256, and B * ceil(T*n_heads / 64) * (max_pages*page_size / 64 + 8)
+ * < 2^31 (else KQ_ERR_UNSUPPORTED).
+ */
+size_t kq_latent_attn_workspace_size(const kq_latent_cache *cache, int64_t B, int64_t T, int32_t n_heads);
+
+kq_status kq_latent_attn(const kq_latent_cache *cache, const int32_t *page_table, int64_t max_pages,
+                         const int32_t *seq_lens, const uint64_t *tree, int64_t B, int64_t T, const void *q,
+                         int64_t q_stride, int32_t n_heads, float scale, void *out, void *workspace,
+                         size_t workspace_bytes, kq_stream_t stream);
+
+/*
  * The next token of each of M rows of V logits, from a uniform number per row.
  *   logits [M] rows of V values, row_stride elements apart, KQ_F32 or KQ_BF16
  *   u      [M] fp32 in [0, 1)

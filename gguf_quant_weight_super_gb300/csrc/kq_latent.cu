@@ -1,134 +1,839 @@
 // kq_latent.cu -- attention of the newest T tokens of each sequence over its
 // cache of latent vectors c_j, which all heads share, in absorbed form:
-//   s_j = scale q.c_j (latent and rope part),  out = sum_j softmax(s)_j c_j[0 .. C)
-// A CTA takes one token and HEADS of its heads, and goes over the positions in
-// tiles of 32 with a running maximum and running sums, everything in fp32.
-#include "kq_cache.h"
+//   s_j = scale q.c_j (latent and rope part),  o = sum_j softmax(s)_j c_j[0 .. C)
+// in one pass with a running maximum and running sums, on the 5th-generation
+// tensor cores, with up to 128 rows (tokens x heads) as the M.
+//
+// Bound: a vector of 1152 bytes (C = 512, bf16) serves 2 (2 C + 64) flops per
+// row, with 128 rows 242 flops per byte, near the device's 282: bytes and
+// products both have to run at their rate.  What is in the way is the room: the
+// sums of 128 rows, 512 fp32 values each, are all of an SM's tensor memory, and
+// the queries 144 KB of its shared memory.  So two SMs, a cluster, share 128 rows
+// by halves of the latent's dims: each CTA keeps its half of q and of the sums in
+// tensor memory, loads its half of every vector (the first also the rope part)
+// and multiplies it once as keys and once as values,
+//   S  = q_half K_half^T   (A: q in tensor memory; the rope part of q in shared memory)
+//   o += P V_half          (A: P = 2^(s - m) in tensor memory; V: the same lines, N-major)
+// Nothing is loaded or multiplied twice.  The price is S: each CTA has the sum
+// over its half of the dims only, so the CTAs send each other their halves' sums
+// (32 KB per tile of 64 positions and direction, straight from registers into the
+// other's shared memory, which tells the barrier its bytes) and both go through
+// the same softmax, bit for bit, as a + b is b + a.
+//
+// The roles of a CTA, as in kq_attn_wide.cu:
+//  * loader warps copy 8 positions at a time into a ring of stages, 64 dims of a
+//    position a line of 128 bytes in the matrix descriptors' 128-byte swizzle
+//    (e4m3 becomes fp16 on the way, exactly);
+//  * one warp issues S of the next tile and P V of this one, whichever can run;
+//  * eight softmax warps, two threads per row, 32 positions each.  A tile's own
+//    sums are read, and sent, as soon as they are there, while the tile before is
+//    worked on, so that the other CTA's arrive before they are asked for.
+// A row's maximum is raised, and its sums scaled down, only when it grows by more
+// than 2^8.  All tiles of all (sequence, 128 rows) items are one line, cut evenly
+// into one range per cluster; an item that spans ranges is left in parts in the
+// workspace, which a second launch joins in the ranges' order.
+//
+// Precision: q and the cache enter exactly (an e4m3 cache as fp16 values, with q
+// scaled by a power of two per row: 2^-38 of the row's largest).  Weights enter
+// P V as bf16, 2^-8 of each (fp16 beside an e4m3 cache, 2^-11, or 2^-32 of the
+// row's largest): independent errors, that stay below the result's own rounding
+// to bf16 in the sum, while a second part would make the products 1.5 times as
+// much where they bound the call.  Sums, statistics and parts are fp32.
+//
+// Every wait is bounded: one that gives up sets the device error word, after
+// which the CTA's roles run through without waiting.
+//
+// Vectors that some rows see and others do not would reach the others as 0 * NaN
+// if they are not finite: a segment whose sums are not all finite runs again; then
+// each value that is not finite becomes 0 before P V, and a row that sees such a
+// vector (its score is not finite) becomes NaN.
+#include "kq_attn_kernel.cuh"
+#include "kq_vec.cuh"
 
 namespace kq {
+namespace attn {
 namespace {
 
-constexpr int STH = 256, HEADS = 8, KT = 32;
+constexpr int NLOAD = 3;                 // loader warps
+constexpr int LTH = (8 + NLOAD + 1) * 32;  // softmax warps 0-7, loaders, products
+constexpr int HC = TK / 2;               // a softmax thread's positions of a tile
+constexpr int LROWS = 128;               // rows of an item
+constexpr int LSTART = 4;                // tiles' time that an item costs besides its tiles
+constexpr float kGrow = 8.0f;            // log2 units that a row's maximum may lag behind
+constexpr int XCHG = 32 * HC * 4;        // bytes that a warp sends per tile
 
-__device__ __forceinline__ float value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float value(const __nv_fp8_e4m3* p) { return static_cast<float>(*p); }
+template <int C, bool F8>
+struct LCfg {
+  static constexpr int HD = C / 2;                // dims of a CTA's half
+  static constexpr int NB = HD / 64;              // lines of a position, without the rope part's
+  static constexpr int LINES = TK * 128;          // 64 dims of a tile's positions
+  static constexpr int STAGE = (NB + 1) * LINES;  // the last lines: the rope part, in the first CTA
+  static constexpr int S = C == 512 ? 3 : 5;
+  static constexpr int QROPE = LROWS * 128;
+  static constexpr int XBUF = 2 * 8 * XCHG;
+  static constexpr int SMEM = S * STAGE + QROPE + XBUF;
+  // tensor memory columns: q, S, P x 2, o
+  static constexpr int CQ = 0, CS = HD / 2, CP = CS + TK, CO = CP + TK, COLS = 512;
+  static constexpr float LIFT = F8 ? 7.0f : 0.0f;  // log2: fp16 weights, below 2^8, fill fp16's range
+  static_assert(CO + HD <= COLS);
+};
 
-template <class Y>
-__global__ void __launch_bounds__(STH) latent_kernel(const __grid_constant__ LatentArgs a) {
-  extern __shared__ float smem[];
-  const int C = a.l.latent_dim, W = C + a.l.rope_dim;
-  float* tile = smem;               // [KT][W + 1]
-  float* q = tile + KT * (W + 1);   // [HEADS][W]
-  __shared__ float s[HEADS][KT];    // scores, then weights
-  __shared__ float m[HEADS], l[HEADS], fix[HEADS];
-  __shared__ int seen[KT];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
-  const int groups = (a.H + HEADS - 1) / HEADS;
-  const int tok = blockIdx.x / groups, h0 = (blockIdx.x - tok * groups) * HEADS, b = tok / a.T, t = tok - b * a.T;
-  int len = max(__ldg(a.seq_lens + b), 0);
-  if (len > a.room) {
-    if (tid == 0) record_error(a.err, DEV_ERR_PAGE);
-    len = a.room;
-  }
-  const int base = len - a.T;
-  uint64_t bits = 0;
-  int pos = base + t;
-  if (a.tree) {
-    bits = tree_bits(__ldg(a.tree + tok), a.T, t, len);
-    pos = tree_position(bits, a.T, len);
-  }
-  for (int x = tid; x < HEADS * W; x += STH) {
-    const int h = h0 + x / W;
-    q[x] = h < a.H ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[tok * a.q_stride + static_cast<int64_t>(h) * W + x % W]) : 0.0f;
-  }
-  if (tid < HEADS) {
-    m[tid] = -INFINITY;
-    l[tid] = 0.0f;
-  }
-  float o[HEADS][2] = {};
-  for (int j0 = 0; j0 < len && pos >= 0; j0 += KT) {
-    __syncthreads();
-    if (tid < KT) {
-      const int j = j0 + tid, u = j - base;
-      bool see = j < len && (a.tree && u >= 0 ? u < 64 && (bits >> u & 1) : j <= pos);
-      if (see) {
-        const int page = __ldg(a.page_table + b * a.max_pages + (j >> a.page_shift));
-        if (page < 0 || page >= a.l.n_pages) {
-          record_error(a.err, DEV_ERR_PAGE);
-          see = false;
-        }
-      }
-      seen[tid] = see;
-    }
-    __syncthreads();
-    for (int x = tid; x < KT * W; x += STH) {
-      const int k = x / W, d = x - k * W, j = j0 + k;
-      float v = 0.0f;
-      if (seen[k]) {
-        const int page = __ldg(a.page_table + b * a.max_pages + (j >> a.page_shift));
-        v = value(static_cast<const Y*>(a.l.c) + page * a.l.page_stride + (j & (a.l.page_size - 1)) * a.l.slot_stride + d) * a.l.scale;
-      }
-      tile[k * (W + 1) + d] = v;
-    }
-    __syncthreads();
-    for (int x = warp; x < HEADS; x += STH / 32) {  // a lane per position
-      float acc = 0.0f;
-      for (int d = 0; d < W; ++d) acc = fmaf(q[x * W + d], tile[lane * (W + 1) + d], acc);
-      acc = seen[lane] ? acc * a.scale * 1.4426950408889634f : -INFINITY;
-      float top = acc;
-      for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-      const float mm = fmaxf(m[x], top), ref = mm == -INFINITY ? 0.0f : mm;
-      const float w = exp2f(acc - ref);
-      float sum = w;
-      for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
-      s[x][lane] = w;
-      __syncwarp();
-      if (lane == 0) {
-        fix[x] = exp2f(m[x] - ref);
-        l[x] = l[x] * fix[x] + sum;
-        m[x] = mm;
-      }
-    }
-    __syncthreads();
+// A range's item that goes on in the next ranges.
+struct Split {
+  int b, rt, parts, slot;  // parts 0: none
+};
+
+struct LParams {
+  AttnArgs a;  // one key-value head; G: heads
+  const uint8_t* pool;
+  int64_t page_bytes, slot_bytes;
+  float c_scale;
+  int rope, RT, clusters, rows;  // rows: of a part
+  Split* split;
+  float *part_ml, *part;
+};
+
+struct LBars {
+  uint64_t full[5], empty[5], s_full, s_free, p_full[2], pv_done[2], q_full, x_full[2][8];
+  uint32_t tmem;
+  int bad, peer_bad;
+  int scan[NW];
+  float back[LROWS];            // e4m3: the rows' powers of two
+  float top[2][2][LROWS];       // tile parity, half: the rows' largest score; at the end their weight sums
+};
+
+// Shared-memory operand in 128-byte-swizzled groups of 8 lines (1024 bytes apart); mn_step: bytes from 64 values along M or
+// N to the next (N-major operands).
+__device__ __forceinline__ uint64_t line_desc(uint32_t saddr, uint32_t mn_step) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (static_cast<uint64_t>((mn_step >> 4) & 0x3FFF) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+// kind::f16, fp32 accumulator, bf16 or fp16 operands, M = 128; n_major: B's N is contiguous
+__device__ __forceinline__ constexpr uint32_t idesc(bool f16, int n, bool n_major) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t id) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_taddr),
+               "l"(a_desc), "l"(b_desc), "r"(id)
+               : "memory");
+}
+// 16 bytes into the other CTA's shared memory; its barrier there counts them.
+__device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, float a, float b, float c, float d) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+               "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d)), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool phase_done(uint64_t* bar, int phase) {
+  uint32_t done;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(done)
+               : "r"(smem_u32(bar)), "r"(phase & 1)
+               : "memory");
+  return done != 0;
+}
+// After the wait for tensor-memory loads: uses of v stay behind it.
+__device__ __forceinline__ void tie(uint32_t (&v)[16]) {
 #pragma unroll
-    for (int h = 0; h < HEADS; ++h) {
-      o[h][0] *= fix[h];
-      o[h][1] *= fix[h];
-    }
-    for (int k = 0; k < KT; ++k) {
-      if (!seen[k]) continue;
-      for (int i = 0; i < C / STH; ++i) {
-        const float v = tile[k * (W + 1) + tid + i * STH];
-#pragma unroll
-        for (int h = 0; h < HEADS; ++h) o[h][i] = fmaf(s[h][k], v, o[h][i]);
-      }
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int h = 0; h < HEADS; ++h)
-    if (h0 + h < a.H)
-      for (int i = 0; i < C / STH; ++i)
-        static_cast<__nv_bfloat16*>(a.out)[(static_cast<int64_t>(tok) * a.H + h0 + h) * C + tid + i * STH] =
-            __float2bfloat16_rn(l[h] == 0.0f ? 0.0f : o[h][i] / l[h]);
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[i]));
+}
+// The two warps of 32 rows.
+__device__ __forceinline__ void rows_sync(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(3 + quarter) : "memory"); }
+__device__ __forceinline__ bool finite16(uint32_t two, bool f16) {  // both halves
+  const uint32_t e = f16 ? 0x7C00u : 0x7F80u;
+  return (two & e) != e && (two >> 16 & e) != e;
 }
 
-template <class Y>
-cudaError_t launch_y(const LatentArgs& a, cudaStream_t st) {
-  const int W = a.l.latent_dim + a.l.rope_dim, smem = (KT * (W + 1) + HEADS * W) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(latent_kernel<Y>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <int C, bool F8>
+struct Latent {
+  using L = LCfg<C, F8>;
+  const LParams& p;
+  const Seg g;
+  LBars& bars;
+  uint8_t* ring;
+  uint8_t* qrope;
+  uint8_t* xbuf;
+  uint32_t tb;    // tensor memory
+  uint32_t rank;  // the CTA's half
+  int tile0;      // tiles of earlier segments: the barriers' phases and the ring go on
+  int xn;         // a softmax warp's tiles so far, as its exchange counts them
+  bool ok;        // no wait has given up
+
+  __device__ __forceinline__ void wait(uint64_t* bar, int phase) {
+    if (!ok || __all_sync(0xFFFFFFFFu, phase_done(bar, phase))) return;
+    bool done = false;
+    for (uint32_t i = 0; i < kMaxPolls && !done; ++i) {
+      done = mbar_try_wait(bar, static_cast<uint32_t>(phase & 1));
+      done = __all_sync(0xFFFFFFFFu, done || phase_done(bar, phase));
+    }
+    ok = done && __all_sync(0xFFFFFFFFu, phase_done(bar, phase));
+    if (!ok) record_error(p.a.err, DEV_ERR_MBAR_TIMEOUT);
+  }
+
+  // Bytes from the pool's start to position j's vector; -1 where none is to be read.
+  __device__ __forceinline__ int64_t offset_of(int j, int page) const {
+    if (j < 0 || j >= g.len) return -1;
+    if (page < 0 || page >= p.a.c.n_pages) {
+      record_error(p.a.err, DEV_ERR_PAGE);
+      return -1;
+    }
+    return page * p.page_bytes + (j & (p.a.c.page_size - 1)) * p.slot_bytes;
+  }
+
+  // ---- loaders: 8 positions at a time, in turn
+  __device__ __forceinline__ void load(int lw, int lane) {
+    const int n = g.t1 - g.t0, b0 = g.t0 * TK;
+    auto page_of = [&](int x) {  // of this lane's row (lane & 7)
+      const int j = b0 + 8 * x + (lane & 7);
+      return j < g.len ? __ldg(g.table + (j >> p.a.page_shift)) : 0;
+    };
+    int page = lw < 8 * n ? page_of(lw) : 0;
+    for (int x = lw; x < 8 * n; x += NLOAD) {
+      const int gi = tile0 + (x >> 3), st = gi % L::S;
+      const int next = x + NLOAD < 8 * n ? page_of(x + NLOAD) : 0;
+      const int64_t off = offset_of(b0 + 8 * x + (lane & 7), page);  // this lane's row's
+      uint8_t* lines = ring + st * L::STAGE + (x & 7) * 1024;
+      if constexpr (F8) {
+        // 16 values per lane and load; all loads before the stage is waited for
+        constexpr int CH = L::HD / 16, N = 8 * CH / 32;
+        uint4 v[N], vr = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int64_t src = __shfl_sync(0xFFFFFFFFu, off, (i * 32 + lane) / CH);
+          v[i] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.pool + src + rank * L::HD) + lane % CH) : make_uint4(0, 0, 0, 0);
+        }
+        const int rch = p.rope / 16;  // 2 or 4
+        {
+          const int64_t src = __shfl_sync(0xFFFFFFFFu, off, (lane / rch) & 7);
+          if (rank == 0 && lane < 8 * rch && src >= 0) vr = __ldg(reinterpret_cast<const uint4*>(p.pool + src + C) + lane % rch);
+        }
+        if (gi >= L::S) wait(&bars.empty[st], gi / L::S - 1);
+        if (ok) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) put(lines + lane % CH / 4 * L::LINES, (i * 32 + lane) / CH, lane % CH % 4, v[i]);
+          if (rank == 0 && lane < 8 * rch) put(lines + L::NB * L::LINES, lane / rch, lane % rch, vr);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars.full[st]);
+      } else {
+        if (gi >= L::S) wait(&bars.empty[st], gi / L::S - 1);
+        if (ok) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = (lane >> 3) + 4 * i;
+            int64_t src = __shfl_sync(0xFFFFFFFFu, off, r);
+            const bool on = src >= 0;
+            src = (on ? src : 0) + (lane & 7) * 16;
+            const uint32_t to = smem_u32(lines) + r * 128 + ((lane & 7) ^ r) * 16;
+#pragma unroll
+            for (int h = 0; h < L::NB; ++h) copy16(to + h * L::LINES, p.pool + src + rank * (2 * L::HD) + h * 128, on);
+            if (rank == 0 && (lane & 7) < p.rope / 8) copy16(to + L::NB * L::LINES, p.pool + src + 2 * C, on);
+          }
+        }
+        // each thread's arrival, once its copies have landed
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.full[st])) : "memory");
+      }
+      page = next;
+    }
+    copy_commit();
+    copy_wait<0>();
+  }
+  // 16 e4m3 values as fp16: chunks 2 c and 2 c + 1 of row r's line.
+  static __device__ __forceinline__ void put(uint8_t* lines, int r, int c, uint4 v) {
+    uint8_t* row = lines + r * 128;
+    *reinterpret_cast<uint4*>(row + ((2 * c) ^ r) * 16) = make_uint4(f8_pair(v.x), f8_pair(v.x >> 16), f8_pair(v.y), f8_pair(v.y >> 16));
+    *reinterpret_cast<uint4*>(row + ((2 * c + 1) ^ r) * 16) = make_uint4(f8_pair(v.z), f8_pair(v.z >> 16), f8_pair(v.w), f8_pair(v.w >> 16));
+  }
+
+  // ---- products, by one warp (its first lane issues): S of the next tile, P V of the oldest, whichever can run
+  __device__ __forceinline__ void products(int lane, int segment) {
+    const int n = g.t1 - g.t0;
+    const uint32_t rs = smem_u32(ring), qr = smem_u32(qrope);
+    wait(&bars.q_full, segment);
+    uint32_t idle = 0;
+    for (int s = 0, v = 0; v < n && ok;) {
+      bool did = false;
+      const int gs = tile0 + s, gv = tile0 + v;
+      if (s < n && __all_sync(0xFFFFFFFFu, phase_done(&bars.full[gs % L::S], gs / L::S) && (gs == 0 || phase_done(&bars.s_free, gs - 1)))) {
+        fence_proxy_async_smem();  // the copies, which the barrier has put before this, seen by the tensor cores
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t k = rs + gs % L::S * L::STAGE;
+#pragma unroll
+          for (int i = 0; i < L::HD / 16; ++i)
+            tc_mma_ts(tb + L::CS, tb + L::CQ + 8 * i, line_desc(k + i / 4 * L::LINES + i % 4 * 32, 16), idesc(F8, TK, false), i > 0);
+          if (rank == 0)
+            for (int i = 0; i < p.rope / 16; ++i)
+              mma_ss(tb + L::CS, line_desc(qr + i * 32, 16), line_desc(k + L::NB * L::LINES + i * 32, 16), idesc(F8, TK, false));
+          tc_commit(&bars.s_full);
+        }
+        __syncwarp();
+        ++s;
+        did = true;
+      }
+      if (v < s && __all_sync(0xFFFFFFFFu, phase_done(&bars.p_full[gv & 1], gv >> 1))) {
+        fence_proxy_async_smem();
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t c = rs + gv % L::S * L::STAGE;
+#pragma unroll
+          for (int k = 0; k < TK / 16; ++k)
+            tc_mma_ts(tb + L::CO, tb + L::CP + TK / 2 * (gv & 1) + 8 * k, line_desc(c + k * 2048, L::LINES), idesc(F8, L::HD, true), v > 0 || k > 0);
+          tc_commit(&bars.pv_done[gv & 1]);
+          tc_commit(&bars.empty[gv % L::S]);
+        }
+        __syncwarp();
+        ++v;
+        did = true;
+      }
+      idle = did ? 0 : idle + 1;
+      if (idle > (1u << 25)) {
+        ok = false;
+        record_error(p.a.err, DEV_ERR_MBAR_TIMEOUT);
+      }
+    }
+  }
+
+  // ---- softmax: two threads per row, warps w and w + 4 (half 0, 1)
+  float m, l;
+  bool poison;  // the row sees a vector that is not finite (careful run)
+
+  // The row's half of q into tensor memory, its rope part into shared memory; mul: the row's power of two (e4m3 cache).
+  __device__ __forceinline__ void load_q(const __nv_bfloat16* src, int r, uint32_t lanes, int half, bool active, float mul) {
+    if (active) {
+#pragma unroll
+      for (int c = 0; c < L::HD / 4; c += 16) {
+        const int col = half * (L::HD / 4) + c;
+        uint32_t v[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 x = operand(src ? __ldg(reinterpret_cast<const uint4*>(src + rank * L::HD + 2 * col) + i) : make_uint4(0, 0, 0, 0), mul);
+          v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+        }
+        tmem_st16(tb + lanes + L::CQ + col, v);
+      }
+      tmem_wait_st();
+    }
+    if (rank == 0)
+      for (int c = half; c < p.rope / 8; c += 2)
+        *reinterpret_cast<uint4*>(qrope + r * 128 + (c ^ (r & 7)) * 16) =
+            operand(src && active ? __ldg(reinterpret_cast<const uint4*>(src + C) + c) : make_uint4(0, 0, 0, 0), mul);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.q_full);
+  }
+  static __device__ __forceinline__ uint4 operand(uint4 x, float mul) {
+    if constexpr (F8) {
+      auto two = [&](uint32_t v) {
+        const float2 f = unpack2<false>(v);
+        return pack2<true>(f.x * mul, f.y * mul);
+      };
+      return make_uint4(two(x.x), two(x.y), two(x.z), two(x.w));
+    } else {
+      return x;
+    }
+  }
+  // Scales the row's sums in tensor memory, HD / 2 of them from column `sums`, by c.
+  static __device__ __noinline__ void scale_sums(uint32_t sums, float c) {
+#pragma unroll 1
+    for (int d = 0; d < L::HD / 2; d += 16) {
+      uint32_t v[16];
+      tmem_ld16(sums + d, v);
+      tmem_wait_ld();
+      tie(v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
+      tmem_st16(sums + d, v);
+    }
+    tmem_wait_st();
+  }
+  // This CTA's half of the scores of a tile from tensor memory, and to the other CTA.
+  __device__ __forceinline__ void read_and_send(float (&own)[HC], uint32_t lanes, int half, bool active) {
+    tc_fence_after();
+    if (active) {
+      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, buf = xn & 1;
+      uint32_t v[2][16];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld16(tb + lanes + L::CS + HC * half + 16 * c, v[c]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        tie(v[c]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) own[16 * c + e] = __uint_as_float(v[c][e]);
+      }
+      const uint32_t to = cluster_map(smem_u32(xbuf + (buf * 8 + warp) * XCHG + lane * 16), rank ^ 1);
+      const uint32_t bar = cluster_map(smem_u32(&bars.x_full[buf][warp]), rank ^ 1);
+#pragma unroll
+      for (int c = 0; c < HC / 4; ++c) send16(to + c * 512, bar, own[4 * c], own[4 * c + 1], own[4 * c + 2], own[4 * c + 3]);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.s_free);
+  }
+  // The other CTA's half of them, added.
+  __device__ __forceinline__ void receive(float (&s)[HC], const float (&own)[HC]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, buf = xn & 1;
+    if (lane == 0) mbar_arrive_expect_tx(&bars.x_full[buf][warp], XCHG);
+    __syncwarp();
+    wait(&bars.x_full[buf][warp], xn >> 1);
+    ++xn;
+    const float4* x = reinterpret_cast<const float4*>(xbuf + (buf * 8 + warp) * XCHG) + lane;
+#pragma unroll
+    for (int c = 0; c < HC / 4; ++c) {
+      const float4 v = x[32 * c];
+      s[4 * c] = own[4 * c] + v.x;
+      s[4 * c + 1] = own[4 * c + 1] + v.y;
+      s[4 * c + 2] = own[4 * c + 2] + v.z;
+      s[4 * c + 3] = own[4 * c + 3] + v.w;
+    }
+  }
+  // r: the row; f: from the raw product to log2 units.
+  template <bool CAREFUL>
+  __device__ __forceinline__ void softmax(uint32_t lanes, int r, int half, bool active, int pos, uint64_t bits, float f) {
+    const AttnArgs& a = p.a;
+    const int n = g.t1 - g.t0, all_hi = g.len - a.T - 1;
+    m = pos < 0 ? INFINITY : -INFINITY;  // padding: weights of 0 wherever masks are not looked at
+    l = 0.0f;
+    poison = false;
+    float own[HC];
+    wait(&bars.s_full, tile0);
+    read_and_send(own, lanes, half, active);
+    for (int i = 0; i < n; ++i) {
+      const int gi = tile0 + i, buf = gi & 1, tile = (g.t0 + i) * TK, base = tile + half * HC;
+      float s[HC];
+      if (active) receive(s, own);
+      bool ahead = i + 1 < n && __all_sync(0xFFFFFFFFu, phase_done(&bars.s_full, gi + 1));
+      if (ahead) read_and_send(own, lanes, half, active);
+      if (active) {
+        float scale = f;
+        if (!(f > 0.0f)) {  // a factor that turns the order around comes first
+          scale = 1.0f;
+#pragma unroll
+          for (int e = 0; e < HC; ++e) s[e] *= f;
+        }
+        if (tile + TK - 1 > all_hi) {
+#pragma unroll
+          for (int e = 0; e < HC; ++e)
+            if (!sees<true>(base + e, pos, bits, g.len - a.T, 0)) s[e] = -INFINITY;
+        }
+        if constexpr (CAREFUL) {
+#pragma unroll
+          for (int e = 0; e < HC; ++e)
+            if (!finite(s[e])) {
+              poison |= sees<true>(base + e, pos, bits, g.len - a.T, 0);
+              s[e] = -INFINITY;
+            }
+        }
+        float top[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[e] = s[e];
+#pragma unroll
+        for (int e = 4; e < HC; ++e) top[e & 3] = fmaxf(top[e & 3], s[e]);
+        float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+        bars.top[buf][half][r] = mx;
+        rows_sync(r >> 5);
+        mx = fmaxf(mx, bars.top[buf][half ^ 1][r]);
+        const bool grow = mx > (m == -INFINITY ? m : m + kGrow);
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float c = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mx);
+          if (grow) m = mx;
+          l *= c;
+          if (i > 0) {
+            wait(&bars.pv_done[buf ^ 1], (gi - 1) >> 1);
+            tc_fence_after();
+            scale_sums(tb + lanes + L::CO + half * (L::HD / 2), c);
+          }
+        }
+        const float mm = (m == -INFINITY ? 0.0f : m) - L::LIFT;  // nothing seen yet: the weights are 0
+        const float2 sc = make_float2(scale, scale), off = make_float2(-mm, -mm);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < HC; e += 2) {
+          const float2 x = ffma2(make_float2(s[e], s[e + 1]), sc, off);
+          const float2 y = make_float2(ex2(x.x), ex2(x.y));
+          sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], y);
+          w[e / 2] = pack2<F8>(y.x, y.y);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        if (i > 1) wait(&bars.pv_done[buf], (gi - 2) >> 1);  // P of two tiles ago is used up
+        tc_fence_after();
+        tmem_st16(tb + lanes + L::CP + TK / 2 * buf + 16 * half, w);
+        tmem_wait_st();
+      }
+      if constexpr (CAREFUL) clean(gi);
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.p_full[buf]);
+      if (i + 1 < n && !ahead) {
+        wait(&bars.s_full, gi + 1);
+        read_and_send(own, lanes, half, active);
+      }
+    }
+    const int last = tile0 + n - 1;
+    wait(&bars.pv_done[last & 1], last >> 1);
+    tc_fence_after();
+  }
+  // Zeros in the place of a tile's values that are not finite, 8 positions per softmax warp: its scores are done, its sums
+  // not begun.
+  __device__ __noinline__ void clean(int gi) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, st = gi % L::S;
+    wait(&bars.full[st], gi / L::S);
+    for (int h = 0; h < L::NB; ++h) {
+      uint32_t* x = reinterpret_cast<uint32_t*>(ring + st * L::STAGE + h * L::LINES + warp * 1024);
+      for (int i = lane; i < 256; i += 32)
+        if (!finite16(x[i], F8)) {
+          const uint32_t e = F8 ? 0x7C00u : 0x7F80u;
+          x[i] = ((x[i] & e) == e ? 0 : x[i] & 0xFFFFu) | ((x[i] >> 16 & e) == e ? 0 : x[i] & 0xFFFF0000u);
+        }
+    }
+    fence_proxy_async_smem();
+  }
+};
+
+template <int C, bool F8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ LParams p) {
+  using L = LCfg<C, F8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ LBars bars;
+  const AttnArgs& a = p.a;
+  uint8_t* ring = smem;
+  uint8_t* qrope = ring + L::S * L::STAGE;
+  uint8_t* xbuf = qrope + L::QROPE;
+  int* prefix = reinterpret_cast<int*>(xbuf + L::XBUF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int range = blockIdx.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::S; ++i) { mbar_init(&bars.full[i], 256); mbar_init(&bars.empty[i], 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.p_full[i], 8);
+      mbar_init(&bars.pv_done[i], 1);
+      for (int w = 0; w < 8; ++w) mbar_init(&bars.x_full[i][w], 1);
+    }
+    mbar_init(&bars.s_full, 1);
+    mbar_init(&bars.s_free, 8);
+    mbar_init(&bars.q_full, 8);
+    fence_mbar_init();
+  }
+  if (warp == 8 + NLOAD) { tmem_alloc(&bars.tmem, L::COLS); tmem_relinquish(); }
+  pdl_wait();
+  pdl_launch_dependents();
+  build_prefix(a, LSTART, prefix, bars.scan);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the other CTA's barriers are there
+  tc_fence_after();
+  const uint32_t tb = bars.tmem;
+  const Line line(a, p.RT, prefix, p.clusters);
+  const int lo = line.bound(min(range, line.nc)), hi = range < line.nc ? line.bound(range + 1) : lo;
+  Split split = {0, 0, 0, 0};
+  int tile0 = 0, segment = 0, xn = 0;
+  bool ok = true;
+  for (int u = lo; u < hi;) {
+    const Item it(a, line, p.RT, LSTART, u);
+    const int end = min(it.i1, hi);
+    if (u < it.i0) u = it.i0;
+    if (u >= end) {  // none of its tiles is in this range
+      u = end;
+      continue;
+    }
+    const int r0 = it.rt * LROWS, R = min(LROWS, a.T * a.G - r0);
+    auto out_row = [&](int r) {
+      return static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(it.b) * a.T * a.G + r0 + r) * C + rank * L::HD;
+    };
+    if (it.len == 0) {
+      for (int x = threadIdx.x; x < R * (L::HD / 4); x += LTH) store4(out_row(x / (L::HD / 4)) + 4 * (x % (L::HD / 4)), make_float4(0, 0, 0, 0));
+      u = end;
+      continue;
+    }
+    Seg g;
+    g.len = it.len;
+    g.first = 0;
+    g.table = a.page_table + it.b * a.max_pages;
+    g.head_off = 0;
+    g.t0 = u - it.i0;
+    g.t1 = end - it.i0;
+    const int r = threadIdx.x & (LROWS - 1), half = (warp >> 2) & 1;  // softmax warps
+    const bool active = warp < 8 && 32 * (warp & 3) < R;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const int row = min(r0 + r, a.T * a.G - 1), t = row / a.G;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(it.b) * a.T + t) * a.q_stride +
+                             static_cast<int64_t>(row - t * a.G) * (C + p.rope);
+    int pos = -1;
+    uint64_t bits = 0;
+    float f = a.scale * p.c_scale * 1.4426950408889634f, mul = 1.0f;
+    if (warp < 8) {
+      // a chain is a tree whose masks are known
+      bits = tree_bits(a.tree ? __ldg(a.tree + static_cast<int64_t>(it.b) * a.T + t) : (2ull << t) - 1, a.T, t, g.len);
+      pos = tree_position(bits, a.T, g.len);
+    }
+    if (threadIdx.x == 0) bars.bad = bars.peer_bad = 0;
+    if constexpr (F8) {
+      if (warp < 8)  // the rows' largest values: a warp per row
+        for (int rr = warp; rr < R; rr += 8) {
+          const int x = r0 + rr, tt = x / a.G;
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(it.b) * a.T + tt) * a.q_stride +
+                                                            static_cast<int64_t>(x - tt * a.G) * (C + p.rope));
+          float mx = 0.0f;
+          for (int i = lane; i < (C + p.rope) / 8; i += 32) {
+            const uint4 v = __ldg(src + i);
+            for (uint32_t w : {v.x, v.y, v.z, v.w}) {
+              const float2 y = unpack2<false>(w);
+              mx = fmaxf(mx, fmaxf(fabsf(y.x), fabsf(y.y)));
+            }
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+          // largest value into [2^13, 2^14); the factor and its inverse stay normal numbers
+          const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
+          if (lane == 0) bars.back[rr] = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+        }
+    }
+    __syncthreads();  // the ring, the sums and tensor memory are free
+    if constexpr (F8) {
+      if (r < R) {
+        f *= bars.back[r];
+        mul = __uint_as_float((254u << 23) - __float_as_uint(bars.back[r]));  // its inverse
+      }
+    }
+    Latent<C, F8> w{p, g, bars, ring, qrope, xbuf, tb, rank, tile0, xn, ok, 0.0f, 0.0f, false};
+    bool careful = false;
+    for (;;) {
+      if (warp < 8) {
+        w.load_q(r < R ? q : nullptr, r, lanes, half, active, mul);
+        if (!careful) {
+          w.template softmax<false>(lanes, r, half, active, pos, bits, f);
+          if (active) {
+            bool bad = false;
+#pragma unroll 1
+            for (int d = half * (L::HD / 2); d < (half + 1) * (L::HD / 2); d += 16) {
+              uint32_t v[16];
+              tmem_ld16(tb + lanes + L::CO + d, v);
+              tmem_wait_ld();
+              tie(v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) bad |= !finite(__uint_as_float(v[i]));
+            }
+            if (bad && r < R) {
+              bars.bad = 1;
+              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(smem_u32(&bars.peer_bad), rank ^ 1)), "r"(1) : "memory");
+            }
+          }
+        } else {
+          w.template softmax<true>(lanes, r, half, active, pos, bits, f);
+        }
+        if (pos < 0) {  // whatever the keys were
+          w.m = -INFINITY;
+          w.l = 0.0f;
+        } else if (w.poison) {
+          w.l = NAN;
+        }
+        bars.top[0][half][r] = w.l;  // read after the barrier
+      } else if (warp < 8 + NLOAD) {
+        w.load(warp - 8, lane);
+      } else {
+        w.products(lane, segment);
+      }
+      ++segment;
+      w.tile0 += g.t1 - g.t0;
+      tc_fence_before();
+      __syncwarp();
+      cluster_sync();  // both CTAs have read what they were sent
+      tc_fence_after();
+      if (careful || !(bars.bad | bars.peer_bad)) break;
+      careful = true;
+      cluster_sync();
+    }
+    tile0 = w.tile0;
+    xn = w.xn;
+    ok = w.ok;
+
+    const bool whole = u == it.i0 && end == it.i1;
+    const int slot = 2 * range + (lo >= it.i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
+    if (!whole && u == it.i0) split = {it.b, it.rt, line.range_of(it.i1 - 1) - range + 1, slot};
+    if (active) {
+      const float weight = bars.top[0][0][r] + bars.top[0][1][r];
+      const float inv = weight == 0.0f ? 0.0f : p.c_scale / weight;
+      float* part = p.part + (static_cast<int64_t>(slot) * p.rows + r) * C + rank * L::HD;
+#pragma unroll 1
+      for (int d = half * (L::HD / 2); d < (half + 1) * (L::HD / 2); d += 16) {
+        uint32_t v[16];
+        tmem_ld16(tb + lanes + L::CO + d, v);
+        tmem_wait_ld();
+        tie(v);
+        if (r < R) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            float4 x = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+            if (pos < 0) x = make_float4(0, 0, 0, 0);
+            if (whole) put4(out_row(r) + d + i, x, inv);
+            else *reinterpret_cast<float4*>(part + d + i) = x;
+          }
+        }
+      }
+      if (!whole && half == 0 && rank == 0 && r < R)
+        *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * p.rows + r) * 2) = make_float2(w.m, weight);
+    }
+    tc_fence_before();
+    __syncthreads();  // top is read before the next segment writes it
+    tc_fence_after();
+    u = end;
+  }
+  if (threadIdx.x == 0 && rank == 0) p.split[range] = split;
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 8 + NLOAD) tmem_dealloc(tb, L::COLS);
+}
+
+// Joins the parts of the items that span ranges: o = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k, in the ranges' order.
+// A block: a range's item, eight rows of it (a warp each) or, with MANY parts expected, one row, its parts in eight shares.
+constexpr int JTH = 256;
+template <int C, bool MANY>
+__global__ void __launch_bounds__(JTH) latent_join_kernel(const __grid_constant__ LParams p) {
+  constexpr int V = C / 128, JW = JTH / 32, MOST = 160;  // vectors of a row per lane; ranges
+  __shared__ float factor[MANY ? 1 : JW][MOST];
+  __shared__ float4 sums[MANY ? JW : 1][C / 4];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 s4 = __ldcg(reinterpret_cast<const int4*>(p.split) + blockIdx.x);
+  const Split sp = {s4.x, s4.y, s4.z, s4.w};
+  const int r = MANY ? blockIdx.y : blockIdx.y * JW + warp;
+  const int64_t row0 = static_cast<int64_t>(sp.rt) * LROWS;
+  if (sp.parts == 0 || row0 + (MANY ? r : r - warp) >= p.a.T * p.a.G) return;
+  const bool on = row0 + r < p.a.T * p.a.G;
+  auto slot_of = [&](int k) { return k == 0 ? sp.slot : 2 * (static_cast<int>(blockIdx.x) + k) + 1; };
+  float* e = factor[MANY ? 0 : warp];
+  float mm = -INFINITY, ll = 0.0f;
+  if (on) {
+    for (int k = lane; k < sp.parts; k += 32) mm = fmaxf(mm, __ldcg(p.part_ml + (static_cast<int64_t>(slot_of(k)) * p.rows + r) * 2));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+    const float ms = mm == -INFINITY ? 0.0f : mm;
+    for (int k = lane; k < sp.parts; k += 32) {
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (static_cast<int64_t>(slot_of(k)) * p.rows + r) * 2));
+      const float f = ex2(x.x - ms);
+      if (!MANY || warp == 0) e[k] = f;
+      ll += f * x.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o);
+  }
+  if (MANY) __syncthreads();
+  else __syncwarp();
+  float4 acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = make_float4(0, 0, 0, 0);
+  if (on) {
+#pragma unroll 4
+    for (int k = MANY ? warp : 0; k < sp.parts; k += MANY ? JW : 1) {
+      const float4* part = reinterpret_cast<const float4*>(p.part + (static_cast<int64_t>(slot_of(k)) * p.rows + r) * C) + lane;
+#pragma unroll
+      for (int i = 0; i < V; ++i) add4(acc[i], e[k], __ldcg(part + 32 * i));
+    }
+  }
+  const float inv = ll == 0.0f ? 0.0f : p.c_scale / ll;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + (static_cast<int64_t>(sp.b) * p.a.T * p.a.G + row0 + r) * C;
+  if (!MANY) {
+    if (on)
+#pragma unroll
+      for (int i = 0; i < V; ++i) put4(out + 4 * (lane + 32 * i), acc[i], inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) sums[warp][lane + 32 * i] = acc[i];
+    __syncthreads();
+    if (threadIdx.x < C / 4) {
+      float4 x = sums[0][threadIdx.x];
+#pragma unroll
+      for (int k = 1; k < JW; ++k) add4(x, 1.0f, sums[k][threadIdx.x]);
+      put4(out + 4 * threadIdx.x, x, inv);
+    }
+  }
+}
+
+int clusters() { return num_sms() / 2 < 160 ? num_sms() / 2 : 160; }
+
+struct LLayout {
+  int rows;
+  size_t ml_off, part_off, bytes;
+};
+LLayout latent_layout(int C, int64_t T, int H) {
+  LLayout l;
+  l.rows = static_cast<int>(min_i64(LROWS, T * H));
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  const size_t slots = 2 * static_cast<size_t>(clusters());
+  l.ml_off = up(clusters() * sizeof(Split));
+  l.part_off = l.ml_off + up(slots * l.rows * 2 * sizeof(float));
+  l.bytes = l.part_off + up(slots * l.rows * C * sizeof(float));
+  return l;
+}
+
+template <int C, bool F8>
+cudaError_t launch_halves(const LParams& p, cudaStream_t st) {
+  using L = LCfg<C, F8>;
+  const size_t smem = L::SMEM + 4 * (static_cast<size_t>(p.a.B) + 1);
+  static int set[64] = {0};
+  const int dev = current_device_id();
+  if (set[dev] < static_cast<int>(smem)) {
+    const cudaError_t e = cudaFuncSetAttribute(latent_kernel<C, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    set[dev] = static_cast<int>(smem);
+  }
+  cudaError_t e = launch_pdl(latent_kernel<C, F8>, dim3(2 * p.clusters), dim3(LTH), smem, st, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(latent_kernel<Y>, dim3(a.B * a.T * ((a.H + HEADS - 1) / HEADS)), dim3(STH), smem, st, a);
+  // few items: many parts of each
+  const bool many = static_cast<int64_t>(p.a.B) * p.RT * 8 <= p.clusters;
+  if (many) return launch_pdl(latent_join_kernel<C, true>, dim3(p.clusters, p.rows), dim3(JTH), 0, st, p);
+  return launch_pdl(latent_join_kernel<C, false>, dim3(p.clusters, (p.rows + 7) / 8), dim3(JTH), 0, st, p);
 }
 
 }  // namespace
+}  // namespace attn
 
-size_t latent_workspace_bytes(const kq_latent_cache&, int64_t, int) { return 256; }
+size_t latent_workspace_bytes(const kq_latent_cache& l, int64_t T, int H) {
+  return attn::latent_layout(l.latent_dim, T < 1 ? 1 : T, H).bytes;
+}
 
-cudaError_t launch_latent(const LatentArgs& a, cudaStream_t st) {
-  return a.l.dtype == KQ_BF16 ? launch_y<__nv_bfloat16>(a, st) : launch_y<__nv_fp8_e4m3>(a, st);
+cudaError_t launch_latent(const LatentArgs& x, cudaStream_t st) {
+  attn::LParams p = {};
+  p.a.c.dtype = x.l.dtype;
+  p.a.c.n_kv_heads = 1;
+  p.a.c.page_size = x.l.page_size;
+  p.a.c.n_pages = x.l.n_pages;
+  p.a.page_table = x.page_table;
+  p.a.max_pages = x.max_pages;
+  p.a.seq_lens = x.seq_lens;
+  p.a.q = x.q;
+  p.a.q_stride = x.q_stride;
+  p.a.out = x.out;
+  p.a.scale = x.scale;
+  p.a.B = x.B;
+  p.a.T = x.T;
+  p.a.Hq = p.a.G = x.H;
+  p.a.page_shift = x.page_shift;
+  p.a.room = x.room;
+  p.a.err = x.err;
+  p.a.tree = x.tree;
+  const int es = x.l.dtype == KQ_BF16 ? 2 : 1;
+  p.pool = static_cast<const uint8_t*>(x.l.c);
+  p.page_bytes = x.l.page_stride * es;
+  p.slot_bytes = x.l.slot_stride * es;
+  p.c_scale = x.l.scale;
+  p.rope = x.l.rope_dim;
+  p.RT = (x.T * x.H + attn::LROWS - 1) / attn::LROWS;
+  p.clusters = attn::clusters();
+  const attn::LLayout l = attn::latent_layout(x.l.latent_dim, x.T, x.H);
+  p.rows = l.rows;
+  uint8_t* ws = static_cast<uint8_t*>(x.ws);
+  p.split = reinterpret_cast<attn::Split*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + l.ml_off);
+  p.part = reinterpret_cast<float*>(ws + l.part_off);
+  if (x.l.latent_dim == 512) return x.l.dtype == KQ_BF16 ? attn::launch_halves<512, false>(p, st) : attn::launch_halves<512, true>(p, st);
+  return x.l.dtype == KQ_BF16 ? attn::launch_halves<256, false>(p, st) : attn::launch_halves<256, true>(p, st);
 }
 
 }  // namespace kq

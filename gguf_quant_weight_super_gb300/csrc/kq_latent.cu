@@ -350,7 +350,7 @@ struct Latent {
   // This CTA's half of the scores of a tile from tensor memory, and to the other CTA.
   __device__ __forceinline__ void read_and_send(float (&own)[HC], uint32_t lanes, int half, bool active) {
     tc_fence_after();
-    if (active) {
+    if (active && ok) {
       const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, buf = xn & 1;
       uint32_t v[2][16];
 #pragma unroll
@@ -387,6 +387,12 @@ struct Latent {
       s[4 * c + 2] = own[4 * c + 2] + v.z;
       s[4 * c + 3] = own[4 * c + 3] + v.w;
     }
+  }
+  // P of two tiles ago is used up: its columns are free, and so is its barrier, at which warps without rows, whose scores may
+  // be two tiles ahead, must not arrive for this tile before all others have for that one.
+  __device__ __forceinline__ void await_weights(int i, int gi) {
+    if (i > 1) wait(&bars.pv_done[gi & 1], (gi - 2) >> 1);
+    tc_fence_after();
   }
   // r: the row; f: from the raw product to log2 units.
   template <bool CAREFUL>
@@ -457,10 +463,11 @@ struct Latent {
           w[e / 2] = pack2<F8>(y.x, y.y);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        if (i > 1) wait(&bars.pv_done[buf], (gi - 2) >> 1);  // P of two tiles ago is used up
-        tc_fence_after();
+        await_weights(i, gi);
         tmem_st16(tb + lanes + L::CP + TK / 2 * buf + 16 * half, w);
         tmem_wait_st();
+      } else {
+        await_weights(i, gi);
       }
       if constexpr (CAREFUL) clean(gi);
       tc_fence_before();
@@ -638,6 +645,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kerne
       }
       ++segment;
       w.tile0 += g.t1 - g.t0;
+      if (!w.ok)  // what is on its way to or from a CTA that did not wait for it lands before the CTA can end
+        for (int i = 0; i < 100; ++i) __nanosleep(1000);
       tc_fence_before();
       __syncwarp();
       cluster_sync();  // both CTAs have read what they were sent

@@ -126,6 +126,14 @@ def test_latent_attn_pages_strides_and_splits(dtype, page):
     check_latent(P, latent_q(4, 1, 16, 576, page))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F8])
+@pytest.mark.parametrize("T,H,L", [(1, 16, 70001), (9, 16, 30011), (1, 40, 50000), (2, 56, 40000), (1, 128, 40003), (3, 100, 20011)])
+def test_latent_attn_long_segments(dtype, T, H, L):
+    """Every range a dozen tiles, with all rows of a tile, some, few."""
+    P = Latent([L, 77], 512, 64, 64, dtype, seed=T + H)
+    check_latent(P, latent_q(2, T, H, 576, T + H))
+
+
 def test_latent_attn_many_sequences_and_rows():
     lens = [int(x) for x in np.random.default_rng(3).integers(0, 400, 70)]
     P = Latent(lens, 512, 64, 32, BF16, seed=5)

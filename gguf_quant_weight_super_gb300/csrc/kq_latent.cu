@@ -54,23 +54,24 @@ namespace kq {
 namespace attn {
 namespace {
 
-constexpr int NLOAD = 3;                 // loader warps
-constexpr int LTH = (8 + NLOAD + 1) * 32;  // softmax warps 0-7, loaders, products
-constexpr int HC = TK / 2;               // a softmax thread's positions of a tile
 constexpr int LROWS = 128;               // rows of an item
 constexpr int LSTART = 4;                // tiles' time that an item costs besides its tiles
 constexpr float kGrow = 8.0f;            // log2 units that a row's maximum may lag behind
-constexpr int XCHG = 32 * HC * 4;        // bytes that a warp sends per tile
+constexpr int XCHG = 32 * TK * 4;        // bytes that a warp sends per tile
 
 template <int C, bool F8>
 struct LCfg {
+  static constexpr int NLOAD = 3;                 // loader warps
+  static constexpr int TH = (8 + NLOAD + 1) * 32;  // softmax warps 0-7, loaders, products
   static constexpr int HD = C / 2;                // dims of a CTA's half
   static constexpr int NB = HD / 64;              // lines of a position, without the rope part's
   static constexpr int LINES = TK * 128;          // 64 dims of a tile's positions
   static constexpr int STAGE = (NB + 1) * LINES;  // the last lines: the rope part, in the first CTA
   static constexpr int S = C == 512 ? 3 : 5;
   static constexpr int QROPE = LROWS * 128;
-  static constexpr int XBUF = 2 * 8 * XCHG;
+  static constexpr int XBUF = 8 * XCHG;
+  static constexpr int OROW = HD * 4 + 16;        // bytes of a row of sums on its way out, in the ring's and q's place
+  static_assert(S * STAGE + QROPE >= LROWS * OROW);
   static constexpr int SMEM = S * STAGE + QROPE + XBUF;
   // tensor memory columns: q, S, P x 2, o
   static constexpr int CQ = 0, CS = HD / 2, CP = CS + TK, CO = CP + TK, COLS = 512;
@@ -94,12 +95,13 @@ struct LParams {
 };
 
 struct LBars {
-  uint64_t full[5], empty[5], s_full, s_free, p_full[2], pv_done[2], q_full, x_full[2][8];
+  uint64_t full[5], empty[5], s_full[2], s_free, p_full[2], pv_done[2], q_full, x_full[8], x_free[8], decided[2][4];
   uint32_t tmem;
   int bad, peer_bad;
   int scan[NW];
-  float back[LROWS];            // e4m3: the rows' powers of two
-  float top[2][2][LROWS];       // tile parity, half: the rows' largest score; at the end their weight sums
+  float back[LROWS];        // e4m3: the rows' powers of two
+  float m[LROWS];           // the rows' maxima that their sums are relative to, in log2 units
+  float weight[2][LROWS];   // at the end, their weight sums over each warpgroup's tiles
 };
 
 // Shared-memory operand in 128-byte-swizzled groups of 8 lines (1024 bytes apart); mn_step: bytes from 64 values along M or
@@ -125,7 +127,7 @@ __device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, float a, floa
 }
 __device__ __forceinline__ bool phase_done(uint64_t* bar, int phase) {
   uint32_t done;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                : "=r"(done)
                : "r"(smem_u32(bar)), "r"(phase & 1)
                : "memory");
@@ -136,8 +138,15 @@ __device__ __forceinline__ void tie(uint32_t (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[i]));
 }
-// The two warps of 32 rows.
-__device__ __forceinline__ void rows_sync(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(3 + quarter) : "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// A copy of 16 bytes, both addresses with constant offsets.
+template <int TO, int FROM>
+__device__ __forceinline__ void copy16_at(uint32_t dst, const uint8_t* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0), "n"(TO), "n"(FROM) : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ bool finite16(uint32_t two, bool f16) {  // both halves
   const uint32_t e = f16 ? 0x7C00u : 0x7F80u;
   return (two & e) != e && (two >> 16 & e) != e;
@@ -179,54 +188,68 @@ struct Latent {
     return page * p.page_bytes + (j & (p.a.c.page_size - 1)) * p.slot_bytes;
   }
 
-  // ---- loaders: 8 positions at a time, in turn
+  // ---- loaders: 32 positions at a time, in turn, their page ids one turn ahead
   __device__ __forceinline__ void load(int lw, int lane) {
+    constexpr int NLOAD = L::NLOAD;
     const int n = g.t1 - g.t0, b0 = g.t0 * TK;
-    auto page_of = [&](int x) {  // of this lane's row (lane & 7)
-      const int j = b0 + 8 * x + (lane & 7);
-      return j < g.len ? __ldg(g.table + (j >> p.a.page_shift)) : 0;
+    auto page_of = [&](int x) {  // of this lane's position
+      const int j = b0 + 32 * x + lane;
+      return x < 2 * n && j < g.len ? __ldg(g.table + (j >> p.a.page_shift)) : 0;
     };
-    int page = lw < 8 * n ? page_of(lw) : 0;
-    for (int x = lw; x < 8 * n; x += NLOAD) {
-      const int gi = tile0 + (x >> 3), st = gi % L::S;
-      const int next = x + NLOAD < 8 * n ? page_of(x + NLOAD) : 0;
-      const int64_t off = offset_of(b0 + 8 * x + (lane & 7), page);  // this lane's row's
-      uint8_t* lines = ring + st * L::STAGE + (x & 7) * 1024;
+    int page = page_of(lw);
+    for (int x = lw; x < 2 * n; x += NLOAD) {
+      const int gi = tile0 + (x >> 1), st = gi % L::S;
+      const int next = page_of(x + NLOAD);
+      const int64_t off = offset_of(b0 + 32 * x + lane, page);
+      uint8_t* lines = ring + st * L::STAGE + (x & 1) * 4096;
       if constexpr (F8) {
-        // 16 values per lane and load; all loads before the stage is waited for
+        // 16 values per lane and load, 8 positions at a time, two times in flight
         constexpr int CH = L::HD / 16, N = 8 * CH / 32;
-        uint4 v[N], vr = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int64_t src = __shfl_sync(0xFFFFFFFFu, off, (i * 32 + lane) / CH);
-          v[i] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.pool + src + rank * L::HD) + lane % CH) : make_uint4(0, 0, 0, 0);
-        }
         const int rch = p.rope / 16;  // 2 or 4
-        {
-          const int64_t src = __shfl_sync(0xFFFFFFFFu, off, (lane / rch) & 7);
-          if (rank == 0 && lane < 8 * rch && src >= 0) vr = __ldg(reinterpret_cast<const uint4*>(p.pool + src + C) + lane % rch);
-        }
-        if (gi >= L::S) wait(&bars.empty[st], gi / L::S - 1);
-        if (ok) {
+        uint4 v[2][N], vr[2];
+        auto fetch = [&](int u) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) put(lines + lane % CH / 4 * L::LINES, (i * 32 + lane) / CH, lane % CH % 4, v[i]);
-          if (rank == 0 && lane < 8 * rch) put(lines + L::NB * L::LINES, lane / rch, lane % rch, vr);
+          for (int i = 0; i < N; ++i) {
+            const int64_t src = __shfl_sync(0xFFFFFFFFu, off, 8 * u + (i * 32 + lane) / CH);
+            v[u & 1][i] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.pool + src + rank * L::HD) + lane % CH) : make_uint4(0, 0, 0, 0);
+          }
+          const int64_t src = __shfl_sync(0xFFFFFFFFu, off, 8 * u + ((lane / rch) & 7));
+          vr[u & 1] = make_uint4(0, 0, 0, 0);
+          if (rank == 0 && lane < 8 * rch && src >= 0) vr[u & 1] = __ldg(reinterpret_cast<const uint4*>(p.pool + src + C) + lane % rch);
+        };
+        fetch(0);
+        fetch(1);
+        if (gi >= L::S) wait(&bars.empty[st], gi / L::S - 1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (ok) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) put(lines + u * 1024 + lane % CH / 4 * L::LINES, (i * 32 + lane) / CH, lane % CH % 4, v[u & 1][i]);
+            if (rank == 0 && lane < 8 * rch) put(lines + u * 1024 + L::NB * L::LINES, lane / rch, lane % rch, vr[u & 1]);
+          }
+          if (u < 2) fetch(u + 2);
         }
         fence_proxy_async_smem();
         mbar_arrive(&bars.full[st]);
       } else {
         if (gi >= L::S) wait(&bars.empty[st], gi / L::S - 1);
         if (ok) {
+          const bool rope = rank == 0 && (lane & 7) < p.rope / 8;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < 8; ++i) {
             const int r = (lane >> 3) + 4 * i;
             int64_t src = __shfl_sync(0xFFFFFFFFu, off, r);
             const bool on = src >= 0;
-            src = (on ? src : 0) + (lane & 7) * 16;
-            const uint32_t to = smem_u32(lines) + r * 128 + ((lane & 7) ^ r) * 16;
-#pragma unroll
-            for (int h = 0; h < L::NB; ++h) copy16(to + h * L::LINES, p.pool + src + rank * (2 * L::HD) + h * 128, on);
-            if (rank == 0 && (lane & 7) < p.rope / 8) copy16(to + L::NB * L::LINES, p.pool + src + 2 * C, on);
+            const uint8_t* from = p.pool + (on ? src : 0) + (lane & 7) * 16;
+            const uint8_t* half = from + rank * (2 * L::HD);
+            const uint32_t to = smem_u32(lines) + r * 128 + ((lane & 7) ^ (r & 7)) * 16;
+            copy16_at<0, 0>(to, half, on);
+            copy16_at<L::LINES, 128>(to, half, on);
+            if constexpr (L::NB == 4) {
+              copy16_at<2 * L::LINES, 256>(to, half, on);
+              copy16_at<3 * L::LINES, 384>(to, half, on);
+            }
+            if (rope) copy16_at<L::NB * L::LINES, 2 * C>(to, from, on);
           }
         }
         // each thread's arrival, once its copies have landed
@@ -257,14 +280,17 @@ struct Latent {
         fence_proxy_async_smem();  // the copies, which the barrier has put before this, seen by the tensor cores
         tc_fence_after();
         if (lane == 0) {
-          const uint32_t k = rs + gs % L::S * L::STAGE;
+          const uint64_t k = line_desc(rs + gs % L::S * L::STAGE, 16);
 #pragma unroll
           for (int i = 0; i < L::HD / 16; ++i)
-            tc_mma_ts(tb + L::CS, tb + L::CQ + 8 * i, line_desc(k + i / 4 * L::LINES + i % 4 * 32, 16), idesc(F8, TK, false), i > 0);
-          if (rank == 0)
-            for (int i = 0; i < p.rope / 16; ++i)
-              mma_ss(tb + L::CS, line_desc(qr + i * 32, 16), line_desc(k + L::NB * L::LINES + i * 32, 16), idesc(F8, TK, false));
-          tc_commit(&bars.s_full);
+            tc_mma_ts(tb + L::CS, tb + L::CQ + 8 * i, k + (i / 4 * L::LINES + i % 4 * 32) / 16, idesc(F8, TK, false), i > 0);
+          if (rank == 0) {
+            const uint64_t q = line_desc(qr, 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i < p.rope / 16) mma_ss(tb + L::CS, q + i * 2, k + (L::NB * L::LINES + i * 32) / 16, idesc(F8, TK, false));
+          }
+          tc_commit(&bars.s_full[gs & 1]);
         }
         __syncwarp();
         ++s;
@@ -274,10 +300,10 @@ struct Latent {
         fence_proxy_async_smem();
         tc_fence_after();
         if (lane == 0) {
-          const uint32_t c = rs + gv % L::S * L::STAGE;
+          const uint64_t c = line_desc(rs + gv % L::S * L::STAGE, L::LINES);
 #pragma unroll
           for (int k = 0; k < TK / 16; ++k)
-            tc_mma_ts(tb + L::CO, tb + L::CP + TK / 2 * (gv & 1) + 8 * k, line_desc(c + k * 2048, L::LINES), idesc(F8, L::HD, true), v > 0 || k > 0);
+            tc_mma_ts(tb + L::CO, tb + L::CP + TK / 2 * (gv & 1) + 8 * k, c + k * 128, idesc(F8, L::HD, true), v > 0 || k > 0);
           tc_commit(&bars.pv_done[gv & 1]);
           tc_commit(&bars.empty[gv % L::S]);
         }
@@ -293,8 +319,8 @@ struct Latent {
     }
   }
 
-  // ---- softmax: two threads per row, warps w and w + 4 (half 0, 1)
-  float m, l;
+  // ---- softmax: a thread per row; warps 0-3 take the even tiles, warps 4-7 the odd ones
+  float l;
   bool poison;  // the row sees a vector that is not finite (careful run)
 
   // The row's half of q into tensor memory, its rope part into shared memory; mul: the row's power of two (e4m3 cache).
@@ -333,10 +359,10 @@ struct Latent {
       return x;
     }
   }
-  // Scales the row's sums in tensor memory, HD / 2 of them from column `sums`, by c.
+  // Scales the row's sums in tensor memory, from column `sums` on, by c.
   static __device__ __noinline__ void scale_sums(uint32_t sums, float c) {
 #pragma unroll 1
-    for (int d = 0; d < L::HD / 2; d += 16) {
+    for (int d = 0; d < L::HD; d += 16) {
       uint32_t v[16];
       tmem_ld16(sums + d, v);
       tmem_wait_ld();
@@ -347,87 +373,79 @@ struct Latent {
     }
     tmem_wait_st();
   }
-  // This CTA's half of the scores of a tile from tensor memory, and to the other CTA.
-  __device__ __forceinline__ void read_and_send(float (&own)[HC], uint32_t lanes, int half, bool active) {
-    tc_fence_after();
-    if (active && ok) {
-      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, buf = xn & 1;
-      uint32_t v[2][16];
+  // A tile's scores: this CTA's half of the sum from tensor memory, to the other CTA, and with the other's half added.  The
+  // other CTA's warp has a place for one tile, which it says is free.
+  __device__ __forceinline__ void exchange(float (&s)[TK], uint32_t lanes) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t v[4][16];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld16(tb + lanes + L::CS + HC * half + 16 * c, v[c]);
-      tmem_wait_ld();
+    for (int c = 0; c < 4; ++c) tmem_ld16(tb + lanes + L::CS + 16 * c, v[c]);
+    tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        tie(v[c]);
+    for (int c = 0; c < 4; ++c) {
+      tie(v[c]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) own[16 * c + e] = __uint_as_float(v[c][e]);
-      }
-      const uint32_t to = cluster_map(smem_u32(xbuf + (buf * 8 + warp) * XCHG + lane * 16), rank ^ 1);
-      const uint32_t bar = cluster_map(smem_u32(&bars.x_full[buf][warp]), rank ^ 1);
-#pragma unroll
-      for (int c = 0; c < HC / 4; ++c) send16(to + c * 512, bar, own[4 * c], own[4 * c + 1], own[4 * c + 2], own[4 * c + 3]);
+      for (int e = 0; e < 16; ++e) s[16 * c + e] = __uint_as_float(v[c][e]);
     }
     tc_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.s_free);
-  }
-  // The other CTA's half of them, added.
-  __device__ __forceinline__ void receive(float (&s)[HC], const float (&own)[HC]) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, buf = xn & 1;
-    if (lane == 0) mbar_arrive_expect_tx(&bars.x_full[buf][warp], XCHG);
-    __syncwarp();
-    wait(&bars.x_full[buf][warp], xn >> 1);
-    ++xn;
-    const float4* x = reinterpret_cast<const float4*>(xbuf + (buf * 8 + warp) * XCHG) + lane;
-#pragma unroll
-    for (int c = 0; c < HC / 4; ++c) {
-      const float4 v = x[32 * c];
-      s[4 * c] = own[4 * c] + v.x;
-      s[4 * c + 1] = own[4 * c + 1] + v.y;
-      s[4 * c + 2] = own[4 * c + 2] + v.z;
-      s[4 * c + 3] = own[4 * c + 3] + v.w;
+    if (lane == 0) {
+      mbar_arrive(&bars.s_free);
+      mbar_arrive_expect_tx(&bars.x_full[warp], XCHG);
     }
-  }
-  // P of two tiles ago is used up: its columns are free, and so is its barrier, at which warps without rows, whose scores may
-  // be two tiles ahead, must not arrive for this tile before all others have for that one.
-  __device__ __forceinline__ void await_weights(int i, int gi) {
-    if (i > 1) wait(&bars.pv_done[gi & 1], (gi - 2) >> 1);
-    tc_fence_after();
+    __syncwarp();
+    if (xn > 0) wait(&bars.x_free[warp], xn - 1);
+    uint8_t* mine = xbuf + warp * XCHG + lane * 16;
+    if (ok) {
+      const uint32_t to = cluster_map(smem_u32(mine), rank ^ 1), bar = cluster_map(smem_u32(&bars.x_full[warp]), rank ^ 1);
+#pragma unroll
+      for (int c = 0; c < TK / 4; ++c) send16(to + c * 512, bar, s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
+    }
+    wait(&bars.x_full[warp], xn);
+    ++xn;
+#pragma unroll
+    for (int c = 0; c < TK / 4; ++c) {
+      const float4 x = *reinterpret_cast<const float4*>(mine + c * 512);
+      s[4 * c] += x.x;
+      s[4 * c + 1] += x.y;
+      s[4 * c + 2] += x.z;
+      s[4 * c + 3] += x.w;
+    }
+    __syncwarp();
+    if (lane == 0) arrive_remote(cluster_map(smem_u32(&bars.x_free[warp]), rank ^ 1));
   }
   // r: the row; f: from the raw product to log2 units.
   template <bool CAREFUL>
-  __device__ __forceinline__ void softmax(uint32_t lanes, int r, int half, bool active, int pos, uint64_t bits, float f) {
+  __device__ __forceinline__ void softmax(uint32_t lanes, int r, bool active, int pos, uint64_t bits, float f) {
     const AttnArgs& a = p.a;
-    const int n = g.t1 - g.t0, all_hi = g.len - a.T - 1;
-    m = pos < 0 ? INFINITY : -INFINITY;  // padding: weights of 0 wherever masks are not looked at
+    const int n = g.t1 - g.t0, all_hi = g.len - a.T - 1, wg = threadIdx.x >> 7, quarter = (threadIdx.x >> 5) & 3;
+    const bool lead = (threadIdx.x & 31) == 0;
+    float m = pos < 0 ? INFINITY : -INFINITY;  // padding: weights of 0 wherever masks are not looked at
     l = 0.0f;
     poison = false;
-    float own[HC];
-    wait(&bars.s_full, tile0);
-    read_and_send(own, lanes, half, active);
-    for (int i = 0; i < n; ++i) {
-      const int gi = tile0 + i, buf = gi & 1, tile = (g.t0 + i) * TK, base = tile + half * HC;
-      float s[HC];
-      if (active) receive(s, own);
-      bool ahead = i + 1 < n && __all_sync(0xFFFFFFFFu, phase_done(&bars.s_full, gi + 1));
-      if (ahead) read_and_send(own, lanes, half, active);
+    for (int i = (tile0 & 1) ^ wg; i < n; i += 2) {
+      const int gi = tile0 + i, tile = (g.t0 + i) * TK;
+      float s[TK];
+      float scale = f, mx = -INFINITY;
+      wait(&bars.s_full[wg], gi >> 1);
+      tc_fence_after();
       if (active) {
-        float scale = f;
+        exchange(s, lanes);
         if (!(f > 0.0f)) {  // a factor that turns the order around comes first
           scale = 1.0f;
 #pragma unroll
-          for (int e = 0; e < HC; ++e) s[e] *= f;
+          for (int e = 0; e < TK; ++e) s[e] *= f;
         }
         if (tile + TK - 1 > all_hi) {
 #pragma unroll
-          for (int e = 0; e < HC; ++e)
-            if (!sees<true>(base + e, pos, bits, g.len - a.T, 0)) s[e] = -INFINITY;
+          for (int e = 0; e < TK; ++e)
+            if (!sees<true>(tile + e, pos, bits, g.len - a.T, 0)) s[e] = -INFINITY;
         }
         if constexpr (CAREFUL) {
 #pragma unroll
-          for (int e = 0; e < HC; ++e)
+          for (int e = 0; e < TK; ++e)
             if (!finite(s[e])) {
-              poison |= sees<true>(base + e, pos, bits, g.len - a.T, 0);
+              poison |= sees<true>(tile + e, pos, bits, g.len - a.T, 0);
               s[e] = -INFINITY;
             }
         }
@@ -435,61 +453,81 @@ struct Latent {
 #pragma unroll
         for (int e = 0; e < 4; ++e) top[e] = s[e];
 #pragma unroll
-        for (int e = 4; e < HC; ++e) top[e & 3] = fmaxf(top[e & 3], s[e]);
-        float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-        bars.top[buf][half][r] = mx;
-        rows_sync(r >> 5);
-        mx = fmaxf(mx, bars.top[buf][half ^ 1][r]);
+        for (int e = 4; e < TK; ++e) top[e & 3] = fmaxf(top[e & 3], s[e]);
+        mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+      } else {
+        tc_fence_before();
+        __syncwarp();
+        if (lead) mbar_arrive(&bars.s_free);
+      }
+      // P of two tiles ago is used up: its columns are free, and so is its barrier, at which a warp without rows must not
+      // arrive for this tile before all others have for that one.
+      if (i > 1) wait(&bars.pv_done[wg], (gi - 2) >> 1);
+      // The tile before has its maxima; this one's are decided after them.
+      if (gi > 0) wait(&bars.decided[wg ^ 1][quarter], (gi - 1) >> 1);
+      tc_fence_after();
+      if (active) {
+        const float now = bars.m[r];
+        if (now != m) {  // raised by the tile before
+          l *= m == -INFINITY ? 0.0f : ex2(m - now);
+          m = now;
+        }
         const bool grow = mx > (m == -INFINITY ? m : m + kGrow);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float c = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mx);
-          if (grow) m = mx;
+          if (grow) bars.m[r] = m = mx;
           l *= c;
           if (i > 0) {
-            wait(&bars.pv_done[buf ^ 1], (gi - 1) >> 1);
+            wait(&bars.pv_done[wg ^ 1], (gi - 1) >> 1);
             tc_fence_after();
-            scale_sums(tb + lanes + L::CO + half * (L::HD / 2), c);
+            scale_sums(tb + lanes + L::CO, c);
+            tc_fence_before();
           }
         }
+      }
+      __syncwarp();
+      if (lead) mbar_arrive(&bars.decided[wg][quarter]);
+      if (active) {
         const float mm = (m == -INFINITY ? 0.0f : m) - L::LIFT;  // nothing seen yet: the weights are 0
         const float2 sc = make_float2(scale, scale), off = make_float2(-mm, -mm);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-        uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < HC; e += 2) {
-          const float2 x = ffma2(make_float2(s[e], s[e + 1]), sc, off);
-          const float2 y = make_float2(ex2(x.x), ex2(x.y));
-          sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], y);
-          w[e / 2] = pack2<F8>(y.x, y.y);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = ffma2(make_float2(s[32 * c + e], s[32 * c + e + 1]), sc, off);
+            const float2 y = make_float2(ex2(x.x), ex2(x.y));
+            sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], y);
+            w[e / 2] = pack2<F8>(y.x, y.y);
+          }
+          tmem_st16(tb + lanes + L::CP + TK / 2 * wg + 16 * c, w);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        await_weights(i, gi);
-        tmem_st16(tb + lanes + L::CP + TK / 2 * buf + 16 * half, w);
         tmem_wait_st();
-      } else {
-        await_weights(i, gi);
       }
-      if constexpr (CAREFUL) clean(gi);
+      if constexpr (CAREFUL) clean(gi, quarter);
       tc_fence_before();
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.p_full[buf]);
-      if (i + 1 < n && !ahead) {
-        wait(&bars.s_full, gi + 1);
-        read_and_send(own, lanes, half, active);
-      }
+      if (lead) mbar_arrive(&bars.p_full[wg]);
     }
     const int last = tile0 + n - 1;
-    wait(&bars.pv_done[last & 1], last >> 1);
+    if (wg == (last & 1)) wait(&bars.pv_done[wg], last >> 1);
+    softmax_sync();
     tc_fence_after();
+    if (active) {  // relative to the rows' last maxima
+      const float now = bars.m[r];
+      if (now != m) l *= m == -INFINITY ? 0.0f : ex2(m - now);
+    }
   }
-  // Zeros in the place of a tile's values that are not finite, 8 positions per softmax warp: its scores are done, its sums
-  // not begun.
-  __device__ __noinline__ void clean(int gi) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, st = gi % L::S;
+  // Zeros in the place of a tile's values that are not finite, 16 positions per warp of the tile's four: its scores are done,
+  // its sums not begun.
+  __device__ __noinline__ void clean(int gi, int quarter) {
+    const int lane = threadIdx.x & 31, st = gi % L::S;
     wait(&bars.full[st], gi / L::S);
     for (int h = 0; h < L::NB; ++h) {
-      uint32_t* x = reinterpret_cast<uint32_t*>(ring + st * L::STAGE + h * L::LINES + warp * 1024);
-      for (int i = lane; i < 256; i += 32)
+      uint32_t* x = reinterpret_cast<uint32_t*>(ring + st * L::STAGE + h * L::LINES + quarter * 2048);
+      for (int i = lane; i < 512; i += 32)
         if (!finite16(x[i], F8)) {
           const uint32_t e = F8 ? 0x7C00u : 0x7F80u;
           x[i] = ((x[i] & e) == e ? 0 : x[i] & 0xFFFFu) | ((x[i] >> 16 & e) == e ? 0 : x[i] & 0xFFFF0000u);
@@ -500,7 +538,7 @@ struct Latent {
 };
 
 template <int C, bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ LParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1) latent_kernel(const __grid_constant__ LParams p) {
   using L = LCfg<C, F8>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ LBars bars;
@@ -513,18 +551,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kerne
   const uint32_t rank = cluster_rank();
   const int range = blockIdx.x >> 1;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::S; ++i) { mbar_init(&bars.full[i], 256); mbar_init(&bars.empty[i], 1); }
+    for (int i = 0; i < L::S; ++i) { mbar_init(&bars.full[i], 64); mbar_init(&bars.empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.p_full[i], 8);
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_full[i], 4);
       mbar_init(&bars.pv_done[i], 1);
-      for (int w = 0; w < 8; ++w) mbar_init(&bars.x_full[i][w], 1);
+      for (int w = 0; w < 4; ++w) mbar_init(&bars.decided[i][w], 1);
     }
-    mbar_init(&bars.s_full, 1);
-    mbar_init(&bars.s_free, 8);
+    for (int w = 0; w < 8; ++w) { mbar_init(&bars.x_full[w], 1); mbar_init(&bars.x_free[w], 1); }
+    mbar_init(&bars.s_free, 4);
     mbar_init(&bars.q_full, 8);
     fence_mbar_init();
   }
-  if (warp == 8 + NLOAD) { tmem_alloc(&bars.tmem, L::COLS); tmem_relinquish(); }
+  if (warp == 8 + L::NLOAD) { tmem_alloc(&bars.tmem, L::COLS); tmem_relinquish(); }
   pdl_wait();
   pdl_launch_dependents();
   build_prefix(a, LSTART, prefix, bars.scan);
@@ -551,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kerne
       return static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(it.b) * a.T * a.G + r0 + r) * C + rank * L::HD;
     };
     if (it.len == 0) {
-      for (int x = threadIdx.x; x < R * (L::HD / 4); x += LTH) store4(out_row(x / (L::HD / 4)) + 4 * (x % (L::HD / 4)), make_float4(0, 0, 0, 0));
+      for (int x = threadIdx.x; x < R * (L::HD / 4); x += L::TH) store4(out_row(x / (L::HD / 4)) + 4 * (x % (L::HD / 4)), make_float4(0, 0, 0, 0));
       u = end;
       continue;
     }
@@ -562,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kerne
     g.head_off = 0;
     g.t0 = u - it.i0;
     g.t1 = end - it.i0;
-    const int r = threadIdx.x & (LROWS - 1), half = (warp >> 2) & 1;  // softmax warps
+    const int r = threadIdx.x & (LROWS - 1), half = (warp >> 2) & 1;  // softmax warps; half: of q's and the sums' dims
     const bool active = warp < 8 && 32 * (warp & 3) < R;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const int row = min(r0 + r, a.T * a.G - 1), t = row / a.G;
@@ -576,26 +615,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kerne
       bits = tree_bits(a.tree ? __ldg(a.tree + static_cast<int64_t>(it.b) * a.T + t) : (2ull << t) - 1, a.T, t, g.len);
       pos = tree_position(bits, a.T, g.len);
     }
+    if (warp < 4) bars.m[r] = pos < 0 ? INFINITY : -INFINITY;
     if (threadIdx.x == 0) bars.bad = bars.peer_bad = 0;
     if constexpr (F8) {
       if (warp < 8)  // the rows' largest values: a warp per row
-        for (int rr = warp; rr < R; rr += 8) {
-          const int x = r0 + rr, tt = x / a.G;
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(it.b) * a.T + tt) * a.q_stride +
-                                                            static_cast<int64_t>(x - tt * a.G) * (C + p.rope));
-          float mx = 0.0f;
-          for (int i = lane; i < (C + p.rope) / 8; i += 32) {
-            const uint4 v = __ldg(src + i);
-            for (uint32_t w : {v.x, v.y, v.z, v.w}) {
-              const float2 y = unpack2<false>(w);
-              mx = fmaxf(mx, fmaxf(fabsf(y.x), fabsf(y.y)));
-            }
+        for (int r4 = warp * 4; r4 < R; r4 += 32) {
+          uint4 v[4][3];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int x = min(r0 + r4 + k, a.T * a.G - 1), tt = x / a.G;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(it.b) * a.T + tt) * a.q_stride +
+                                                              static_cast<int64_t>(x - tt * a.G) * (C + p.rope));
+#pragma unroll
+            for (int i = 0; i < 3; ++i) v[k][i] = lane + 32 * i < (C + p.rope) / 8 ? __ldg(src + lane + 32 * i) : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-          // largest value into [2^13, 2^14); the factor and its inverse stay normal numbers
-          const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
-          if (lane == 0) bars.back[rr] = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+          for (int k = 0; k < 4; ++k) {
+            float mx = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              for (uint32_t w : {v[k][i].x, v[k][i].y, v[k][i].z, v[k][i].w}) {
+                const float2 y = unpack2<false>(w);
+                mx = fmaxf(mx, fmaxf(fabsf(y.x), fabsf(y.y)));
+              }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+            // largest value into [2^13, 2^14); the factor and its inverse stay normal numbers
+            const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
+            if (lane == 0) bars.back[r4 + k] = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+          }
         }
     }
     __syncthreads();  // the ring, the sums and tensor memory are free
@@ -605,13 +653,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kerne
         mul = __uint_as_float((254u << 23) - __float_as_uint(bars.back[r]));  // its inverse
       }
     }
-    Latent<C, F8> w{p, g, bars, ring, qrope, xbuf, tb, rank, tile0, xn, ok, 0.0f, 0.0f, false};
+    Latent<C, F8> w{p, g, bars, ring, qrope, xbuf, tb, rank, tile0, xn, ok, 0.0f, false};
     bool careful = false;
     for (;;) {
       if (warp < 8) {
         w.load_q(r < R ? q : nullptr, r, lanes, half, active, mul);
         if (!careful) {
-          w.template softmax<false>(lanes, r, half, active, pos, bits, f);
+          w.template softmax<false>(lanes, r, active, pos, bits, f);
           if (active) {
             bool bad = false;
 #pragma unroll 1
@@ -629,16 +677,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kerne
             }
           }
         } else {
-          w.template softmax<true>(lanes, r, half, active, pos, bits, f);
+          w.template softmax<true>(lanes, r, active, pos, bits, f);
         }
-        if (pos < 0) {  // whatever the keys were
-          w.m = -INFINITY;
-          w.l = 0.0f;
-        } else if (w.poison) {
-          w.l = NAN;
-        }
-        bars.top[0][half][r] = w.l;  // read after the barrier
-      } else if (warp < 8 + NLOAD) {
+        bars.weight[half][r] = pos < 0 ? 0.0f : w.poison ? NAN : w.l;  // padding: whatever the keys were
+      } else if (warp < 8 + L::NLOAD) {
         w.load(warp - 8, lane);
       } else {
         w.products(lane, segment);
@@ -653,6 +695,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kerne
       tc_fence_after();
       if (careful || !(bars.bad | bars.peer_bad)) break;
       careful = true;
+      if (warp < 4) bars.m[r] = pos < 0 ? INFINITY : -INFINITY;
       cluster_sync();
     }
     tile0 = w.tile0;
@@ -662,31 +705,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kerne
     const bool whole = u == it.i0 && end == it.i1;
     const int slot = 2 * range + (lo >= it.i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
     if (!whole && u == it.i0) split = {it.b, it.rt, line.range_of(it.i1 - 1) - range + 1, slot};
+    // out through shared memory, in the ring's and q's place, a row of the half at a time
     if (active) {
-      const float weight = bars.top[0][0][r] + bars.top[0][1][r];
+      const float weight = bars.weight[0][r] + bars.weight[1][r];
       const float inv = weight == 0.0f ? 0.0f : p.c_scale / weight;
-      float* part = p.part + (static_cast<int64_t>(slot) * p.rows + r) * C + rank * L::HD;
+      uint8_t* stage = ring + r * L::OROW;
 #pragma unroll 1
       for (int d = half * (L::HD / 2); d < (half + 1) * (L::HD / 2); d += 16) {
         uint32_t v[16];
         tmem_ld16(tb + lanes + L::CO + d, v);
         tmem_wait_ld();
         tie(v);
-        if (r < R) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            float4 x = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-            if (pos < 0) x = make_float4(0, 0, 0, 0);
-            if (whole) put4(out_row(r) + d + i, x, inv);
-            else *reinterpret_cast<float4*>(part + d + i) = x;
-          }
+        for (int i = 0; i < 16; i += 4) {
+          float4 x = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+          if (pos < 0) x = make_float4(0, 0, 0, 0);
+          if (whole) put4(reinterpret_cast<__nv_bfloat16*>(stage) + d + i, x, inv);
+          else *reinterpret_cast<float4*>(stage + (d + i) * 4) = x;
         }
       }
       if (!whole && half == 0 && rank == 0 && r < R)
-        *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * p.rows + r) * 2) = make_float2(w.m, weight);
+        *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * p.rows + r) * 2) = make_float2(pos < 0 ? -INFINITY : bars.m[r], weight);
+      fence_proxy_async_smem();
+    }
+    if (warp < 8) {
+      softmax_sync();
+      if (half == 0 && r < R) {
+        void* dst = whole ? static_cast<void*>(out_row(r)) : p.part + (static_cast<int64_t>(slot) * p.rows + r) * C + rank * L::HD;
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(ring + r * L::OROW)),
+                     "r"(whole ? L::HD * 2 : L::HD * 4)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+      }
     }
     tc_fence_before();
-    __syncthreads();  // top is read before the next segment writes it
+    __syncthreads();  // the copies have read the ring; weights and maxima are read before the next segment writes them
     tc_fence_after();
     u = end;
   }
@@ -695,7 +748,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LTH, 1) latent_kerne
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  if (warp == 8 + NLOAD) tmem_dealloc(tb, L::COLS);
+  if (warp == 8 + L::NLOAD) tmem_dealloc(tb, L::COLS);
 }
 
 // Joins the parts of the items that span ranges: o = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k, in the ranges' order.
@@ -792,7 +845,7 @@ cudaError_t launch_halves(const LParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set[dev] = static_cast<int>(smem);
   }
-  cudaError_t e = launch_pdl(latent_kernel<C, F8>, dim3(2 * p.clusters), dim3(LTH), smem, st, p);
+  cudaError_t e = launch_pdl(latent_kernel<C, F8>, dim3(2 * p.clusters), dim3(L::TH), smem, st, p);
   if (e != cudaSuccess) return e;
   // few items: many parts of each
   const bool many = static_cast<int64_t>(p.a.B) * p.RT * 8 <= p.clusters;

@@ -47,6 +47,8 @@
 // if they are not finite: a segment whose sums are not all finite runs again; then
 // each value that is not finite becomes 0 before P V, and a row that sees such a
 // vector (its score is not finite) becomes NaN.
+#include <utility>
+
 #include "kq_attn_kernel.cuh"
 #include "kq_vec.cuh"
 
@@ -114,15 +116,39 @@ __device__ __forceinline__ uint64_t line_desc(uint32_t saddr, uint32_t mn_step) 
 __device__ __forceinline__ constexpr uint32_t idesc(bool f16, int n, bool n_major) {
   return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t id) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_taddr),
-               "l"(a_desc), "l"(b_desc), "r"(id)
-               : "memory");
+// Products issued by one lane of a converged warp (`on`), so that their operands can stay in uniform registers: moving
+// them there for a lane's branch took twice the products' time.
+__device__ __forceinline__ void mma_ts_on(uint32_t d_taddr, uint32_t a_taddr, uint64_t b_desc, uint32_t id, uint32_t accumulate, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_taddr),
+      "r"(a_taddr), "l"(b_desc), "r"(id), "r"(accumulate), "r"(on)
+      : "memory");
 }
+__device__ __forceinline__ void mma_ss_on(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t id, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.eq.u32 p, 0, 0;\n\tsetp.ne.u32 q, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_taddr),
+      "l"(a_desc), "l"(b_desc), "r"(id), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit_on(uint32_t bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
 // 16 bytes into the other CTA's shared memory; its barrier there counts them.
-__device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, float a, float b, float c, float d) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
-               "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d)), "r"(bar)
+template <int TO>
+__device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, const float* x) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0 + %6], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+               "r"(__float_as_uint(x[0])), "r"(__float_as_uint(x[1])), "r"(__float_as_uint(x[2])), "r"(__float_as_uint(x[3])), "r"(bar), "n"(TO)
                : "memory");
 }
 __device__ __forceinline__ bool phase_done(uint64_t* bar, int phase) {
@@ -145,7 +171,7 @@ __device__ __forceinline__ void copy16_at(uint32_t dst, const uint8_t* src, bool
   asm volatile("cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0), "n"(TO), "n"(FROM) : "memory");
 }
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool finite16(uint32_t two, bool f16) {  // both halves
   const uint32_t e = f16 ? 0x7C00u : 0x7F80u;
@@ -270,7 +296,9 @@ struct Latent {
   // ---- products, by one warp (its first lane issues): S of the next tile, P V of the oldest, whichever can run
   __device__ __forceinline__ void products(int lane, int segment) {
     const int n = g.t1 - g.t0;
-    const uint32_t rs = smem_u32(ring), qr = smem_u32(qrope);
+    const uint32_t rs = smem_u32(ring), t = uniform(tb), on = elect();
+    const uint64_t q = line_desc(smem_u32(qrope), 16);
+    const int rope = rank == 0 ? p.rope / 16 : 0;
     wait(&bars.q_full, segment);
     uint32_t idle = 0;
     for (int s = 0, v = 0; v < n && ok;) {
@@ -279,35 +307,26 @@ struct Latent {
       if (s < n && __all_sync(0xFFFFFFFFu, phase_done(&bars.full[gs % L::S], gs / L::S) && (gs == 0 || phase_done(&bars.s_free, gs - 1)))) {
         fence_proxy_async_smem();  // the copies, which the barrier has put before this, seen by the tensor cores
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t k = line_desc(rs + gs % L::S * L::STAGE, 16);
+        const uint64_t k = line_desc(uniform(rs + gs % L::S * L::STAGE), 16);
 #pragma unroll
-          for (int i = 0; i < L::HD / 16; ++i)
-            tc_mma_ts(tb + L::CS, tb + L::CQ + 8 * i, k + (i / 4 * L::LINES + i % 4 * 32) / 16, idesc(F8, TK, false), i > 0);
-          if (rank == 0) {
-            const uint64_t q = line_desc(qr, 16);
+        for (int i = 0; i < L::HD / 16; ++i)
+          mma_ts_on(t + L::CS, t + L::CQ + 8 * i, k + (i / 4 * L::LINES + i % 4 * 32) / 16, idesc(F8, TK, false), i > 0, on);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (i < p.rope / 16) mma_ss(tb + L::CS, q + i * 2, k + (L::NB * L::LINES + i * 32) / 16, idesc(F8, TK, false));
-          }
-          tc_commit(&bars.s_full[gs & 1]);
-        }
-        __syncwarp();
+        for (int i = 0; i < 4; ++i)
+          if (i < rope) mma_ss_on(t + L::CS, q + i * 2, k + (L::NB * L::LINES + i * 32) / 16, idesc(F8, TK, false), on);
+        commit_on(smem_u32(&bars.s_full[gs & 1]), on);
         ++s;
         did = true;
       }
       if (v < s && __all_sync(0xFFFFFFFFu, phase_done(&bars.p_full[gv & 1], gv >> 1))) {
         fence_proxy_async_smem();
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t c = line_desc(rs + gv % L::S * L::STAGE, L::LINES);
+        const uint64_t c = line_desc(uniform(rs + gv % L::S * L::STAGE), L::LINES);
+        const uint32_t w = uniform(t + L::CP + TK / 2 * (gv & 1));
 #pragma unroll
-          for (int k = 0; k < TK / 16; ++k)
-            tc_mma_ts(tb + L::CO, tb + L::CP + TK / 2 * (gv & 1) + 8 * k, c + k * 128, idesc(F8, L::HD, true), v > 0 || k > 0);
-          tc_commit(&bars.pv_done[gv & 1]);
-          tc_commit(&bars.empty[gv % L::S]);
-        }
-        __syncwarp();
+        for (int k = 0; k < TK / 16; ++k) mma_ts_on(t + L::CO, w + 8 * k, c + k * 128, idesc(F8, L::HD, true), v > 0 || k > 0, on);
+        commit_on(smem_u32(&bars.pv_done[gv & 1]), on);
+        commit_on(smem_u32(&bars.empty[gv % L::S]), on);
         ++v;
         did = true;
       }
@@ -360,7 +379,7 @@ struct Latent {
     }
   }
   // Scales the row's sums in tensor memory, from column `sums` on, by c.
-  static __device__ __noinline__ void scale_sums(uint32_t sums, float c) {
+  static __device__ __forceinline__ void scale_sums(uint32_t sums, float c) {
 #pragma unroll 1
     for (int d = 0; d < L::HD; d += 16) {
       uint32_t v[16];
@@ -372,6 +391,10 @@ struct Latent {
       tmem_st16(sums + d, v);
     }
     tmem_wait_st();
+  }
+  template <int... I>
+  static __device__ __forceinline__ void send_all(uint32_t to, uint32_t bar, const float (&s)[TK], std::integer_sequence<int, I...>) {
+    (send16<I * 512>(to, bar, s + 4 * I), ...);
   }
   // A tile's scores: this CTA's half of the sum from tensor memory, to the other CTA, and with the other's half added.  The
   // other CTA's warp has a place for one tile, which it says is free.
@@ -398,18 +421,16 @@ struct Latent {
     uint8_t* mine = xbuf + warp * XCHG + lane * 16;
     if (ok) {
       const uint32_t to = cluster_map(smem_u32(mine), rank ^ 1), bar = cluster_map(smem_u32(&bars.x_full[warp]), rank ^ 1);
-#pragma unroll
-      for (int c = 0; c < TK / 4; ++c) send16(to + c * 512, bar, s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
+      send_all(to, bar, s, std::make_integer_sequence<int, TK / 4>());
     }
     wait(&bars.x_full[warp], xn);
     ++xn;
 #pragma unroll
     for (int c = 0; c < TK / 4; ++c) {
       const float4 x = *reinterpret_cast<const float4*>(mine + c * 512);
-      s[4 * c] += x.x;
-      s[4 * c + 1] += x.y;
-      s[4 * c + 2] += x.z;
-      s[4 * c + 3] += x.w;
+      const float2 lo = fadd2(make_float2(s[4 * c], s[4 * c + 1]), make_float2(x.x, x.y));
+      const float2 hi = fadd2(make_float2(s[4 * c + 2], s[4 * c + 3]), make_float2(x.z, x.w));
+      s[4 * c] = lo.x, s[4 * c + 1] = lo.y, s[4 * c + 2] = hi.x, s[4 * c + 3] = hi.y;
     }
     __syncwarp();
     if (lane == 0) arrive_remote(cluster_map(smem_u32(&bars.x_free[warp]), rank ^ 1));
@@ -449,11 +470,9 @@ struct Latent {
               s[e] = -INFINITY;
             }
         }
-        float top[4];
+        float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top[e] = s[e];
-#pragma unroll
-        for (int e = 4; e < TK; ++e) top[e & 3] = fmaxf(top[e & 3], s[e]);
+        for (int e = 4; e < TK; e += 2) top[(e >> 1) & 3] = fmaxf(fmaxf(top[(e >> 1) & 3], s[e]), s[e + 1]);
         mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
       } else {
         tc_fence_before();
@@ -506,7 +525,10 @@ struct Latent {
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
       }
-      if constexpr (CAREFUL) clean(gi, quarter);
+      if constexpr (CAREFUL) {  // (static, as is all that is not inlined: an object with an address would live in memory)
+        wait(&bars.full[gi % L::S], gi / L::S);
+        clean(ring + gi % L::S * L::STAGE + quarter * 2048);
+      }
       tc_fence_before();
       __syncwarp();
       if (lead) mbar_arrive(&bars.p_full[wg]);
@@ -522,11 +544,10 @@ struct Latent {
   }
   // Zeros in the place of a tile's values that are not finite, 16 positions per warp of the tile's four: its scores are done,
   // its sums not begun.
-  __device__ __noinline__ void clean(int gi, int quarter) {
-    const int lane = threadIdx.x & 31, st = gi % L::S;
-    wait(&bars.full[st], gi / L::S);
+  static __device__ __noinline__ void clean(uint8_t* lines) {
+    const int lane = threadIdx.x & 31;
     for (int h = 0; h < L::NB; ++h) {
-      uint32_t* x = reinterpret_cast<uint32_t*>(ring + st * L::STAGE + h * L::LINES + quarter * 2048);
+      uint32_t* x = reinterpret_cast<uint32_t*>(lines + h * L::LINES);
       for (int i = lane; i < 512; i += 32)
         if (!finite16(x[i], F8)) {
           const uint32_t e = F8 ? 0x7C00u : 0x7F80u;

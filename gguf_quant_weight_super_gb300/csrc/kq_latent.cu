@@ -59,22 +59,30 @@ namespace {
 constexpr int LROWS = 128;               // rows of an item
 constexpr int LSTART = 4;                // tiles' time that an item costs besides its tiles
 constexpr float kGrow = 8.0f;            // log2 units that a row's maximum may lag behind
-constexpr int XCHG = 32 * TK * 4;        // bytes that a warp sends per tile
+constexpr int SW = 16;                   // softmax warps
+constexpr int HC = TK / 2;               // a softmax thread's positions of a tile
+constexpr int XCHG = 32 * HC * 4;        // bytes that a warp sends per tile
+constexpr int MOST_STAGES = 6;
 
 template <int C, bool F8>
 struct LCfg {
-  static constexpr int NLOAD = 3;                 // loader warps
-  static constexpr int TH = (8 + NLOAD + 1) * 32;  // softmax warps 0-7, loaders, products
-  static constexpr int HD = C / 2;                // dims of a CTA's half
-  static constexpr int NB = HD / 64;              // lines of a position, without the rope part's
-  static constexpr int LINES = TK * 128;          // 64 dims of a tile's positions
-  static constexpr int STAGE = (NB + 1) * LINES;  // the last lines: the rope part, in the first CTA
-  static constexpr int S = C == 512 ? 3 : 5;
+  static constexpr int NLOAD = 3;                     // loader warps
+  static constexpr int TH = (SW + NLOAD + 1) * 32;    // softmax warps, loaders, products
+  static constexpr int HD = C / 2;                    // dims of a CTA's half
+  static constexpr int NB = HD / 64;                  // lines of a position, without the rope part's
+  static constexpr int LINES = TK * 128;              // 64 dims of a tile's positions
+  static constexpr int STAGE = (NB + 1) * LINES;      // the last lines: the rope part, in the first CTA
   static constexpr int QROPE = LROWS * 128;
-  static constexpr int XBUF = 8 * XCHG;
-  static constexpr int OROW = HD * 4 + 16;        // bytes of a row of sums on its way out, in the ring's and q's place
-  static_assert(S * STAGE + QROPE >= LROWS * OROW);
-  static constexpr int SMEM = S * STAGE + QROPE + XBUF;
+  static constexpr int OROW = HD * 4 + 16;            // bytes of a row of sums on its way out, in q's and the ring's place
+  // e4m3: 16 positions as they are in the cache, and how many such pieces a loader warp has on their way
+  static constexpr int RAWROW = HD + 64, RAWS = F8 ? 3 : 0, RAW = RAWS * 16 * RAWROW;
+  // Shared memory: q's rope part, the ring, the exchange (by quarters of the rows), the raw pieces, the line's index.
+  static constexpr int smem(int stages, int quarters, int B) {
+    return QROPE + stages * STAGE + 4 * quarters * XCHG + NLOAD * RAW + 4 * (B + 1);
+  }
+  static constexpr int ROOM = 227 * 1024 - 4096;  // less the static memory
+  static_assert(smem(F8 ? 2 : 3, 4, 4096) <= ROOM, "all rows, the most sequences");
+  static_assert(QROPE + (F8 ? 2 : 3) * STAGE + (F8 ? 4 * XCHG + NLOAD * RAW : 0) >= (F8 ? 32 : 128) * OROW, "and the sums on their way out");
   // tensor memory columns: q, S, P x 2, o
   static constexpr int CQ = 0, CS = HD / 2, CP = CS + TK, CO = CP + TK, COLS = 512;
   static constexpr float LIFT = F8 ? 7.0f : 0.0f;  // log2: fp16 weights, below 2^8, fill fp16's range
@@ -92,18 +100,19 @@ struct LParams {
   int64_t page_bytes, slot_bytes;
   float c_scale;
   int rope, RT, clusters, rows;  // rows: of a part
+  int stages, quarters;          // of the ring; of 32 rows that an item can have
   Split* split;
   float *part_ml, *part;
 };
 
 struct LBars {
-  uint64_t full[5], empty[5], s_full[2], s_free, p_full[2], pv_done[2], q_full, x_full[8], x_free[8], decided[2][4];
+  uint64_t full[MOST_STAGES], empty[MOST_STAGES], s_full[2], s_free, p_full[2], pv_done[2], q_full, x_full[SW], x_free[SW], decided[2][4];
   uint32_t tmem;
   int bad, peer_bad;
   int scan[NW];
-  float back[LROWS];        // e4m3: the rows' powers of two
-  float m[LROWS];           // the rows' maxima that their sums are relative to, in log2 units
-  float weight[2][LROWS];   // at the end, their weight sums over each warpgroup's tiles
+  float back[LROWS];           // e4m3: the rows' powers of two
+  float m[LROWS];              // the rows' maxima that their sums are relative to, in log2 units
+  float top[4][LROWS];         // a warpgroup's half of a tile: the rows' largest score; at the end, its weight sums
 };
 
 // Shared-memory operand in 128-byte-swizzled groups of 8 lines (1024 bytes apart); mn_step: bytes from 64 values along M or
@@ -164,7 +173,9 @@ __device__ __forceinline__ void tie(uint32_t (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[i]));
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+// The two warps of 32 rows that work on one tile.
+__device__ __forceinline__ void rows_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(2 + id) : "memory"); }
 // A copy of 16 bytes, both addresses with constant offsets.
 template <int TO, int FROM>
 __device__ __forceinline__ void copy16_at(uint32_t dst, const uint8_t* src, bool on) {
@@ -186,7 +197,8 @@ struct Latent {
   LBars& bars;
   uint8_t* ring;
   uint8_t* qrope;
-  uint8_t* xbuf;
+  uint8_t* xbuf;  // a softmax warp's place
+  uint8_t* raw;   // a loader warp's
   uint32_t tb;    // tensor memory
   uint32_t rank;  // the CTA's half
   int tile0;      // tiles of earlier segments: the barriers' phases and the ring go on
@@ -204,6 +216,13 @@ struct Latent {
     if (!ok) record_error(p.a.err, DEV_ERR_MBAR_TIMEOUT);
   }
 
+  // Both, which are mostly done already.
+  __device__ __forceinline__ void wait(uint64_t* bar, int phase, uint64_t* bar2, int phase2) {
+    if (!ok || __all_sync(0xFFFFFFFFu, phase_done(bar, phase) && phase_done(bar2, phase2))) return;
+    wait(bar, phase);
+    wait(bar2, phase2);
+  }
+
   // Bytes from the pool's start to position j's vector; -1 where none is to be read.
   __device__ __forceinline__ int64_t offset_of(int j, int page) const {
     if (j < 0 || j >= g.len) return -1;
@@ -214,51 +233,75 @@ struct Latent {
     return page * p.page_bytes + (j & (p.a.c.page_size - 1)) * p.slot_bytes;
   }
 
-  // ---- loaders: 32 positions at a time, in turn, their page ids one turn ahead
+  // ---- loaders: U positions at a time, in turn, their page ids one turn ahead
   __device__ __forceinline__ void load(int lw, int lane) {
-    constexpr int NLOAD = L::NLOAD;
-    const int n = g.t1 - g.t0, b0 = g.t0 * TK;
+    constexpr int NLOAD = L::NLOAD, U = F8 ? 16 : 32, PT = TK / U;
+    const int n = g.t1 - g.t0, b0 = g.t0 * TK, units = PT * n;
     auto page_of = [&](int x) {  // of this lane's position
-      const int j = b0 + 32 * x + lane;
-      return x < 2 * n && j < g.len ? __ldg(g.table + (j >> p.a.page_shift)) : 0;
+      const int j = b0 + U * x + lane % U;
+      return x < units && j < g.len ? __ldg(g.table + (j >> p.a.page_shift)) : 0;
     };
     int page = page_of(lw);
-    for (int x = lw; x < 2 * n; x += NLOAD) {
-      const int gi = tile0 + (x >> 1), st = gi % L::S;
+    auto offset_at = [&](int x) {  // and its offset, the next page on its way
       const int next = page_of(x + NLOAD);
-      const int64_t off = offset_of(b0 + 32 * x + lane, page);
-      uint8_t* lines = ring + st * L::STAGE + (x & 1) * 4096;
-      if constexpr (F8) {
-        // 16 values per lane and load, 8 positions at a time, two times in flight
-        constexpr int CH = L::HD / 16, N = 8 * CH / 32;
-        const int rch = p.rope / 16;  // 2 or 4
-        uint4 v[2][N], vr[2];
-        auto fetch = [&](int u) {
+      const int64_t off = offset_of(b0 + U * x + lane % U, page);
+      page = next;
+      return off;
+    };
+    if constexpr (F8) {
+      // Pieces come as they are, RAWS - 1 ahead, and go into their lines as fp16.
+      constexpr int CH = L::HD / 16;  // 16-byte chunks of a row, without the rope part
+      const int rch = p.rope / 16;    // 2 or 4
+      auto fetch = [&](int x, int slot) {
+        const int64_t off = x < units ? offset_at(x) : 0;
+        const uint32_t to = smem_u32(raw) + slot * (16 * L::RAWROW);
+        if (x < units && ok) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int64_t src = __shfl_sync(0xFFFFFFFFu, off, 8 * u + (i * 32 + lane) / CH);
-            v[u & 1][i] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.pool + src + rank * L::HD) + lane % CH) : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < CH / 2; ++i) {
+            const int r = (i * 32 + lane) / CH;
+            const int64_t src = __shfl_sync(0xFFFFFFFFu, off, r);
+            copy16(to + r * L::RAWROW + lane % CH * 16, p.pool + (src >= 0 ? src : 0) + rank * L::HD + lane % CH * 16, src >= 0);
           }
-          const int64_t src = __shfl_sync(0xFFFFFFFFu, off, 8 * u + ((lane / rch) & 7));
-          vr[u & 1] = make_uint4(0, 0, 0, 0);
-          if (rank == 0 && lane < 8 * rch && src >= 0) vr[u & 1] = __ldg(reinterpret_cast<const uint4*>(p.pool + src + C) + lane % rch);
-        };
-        fetch(0);
-        fetch(1);
-        if (gi >= L::S) wait(&bars.empty[st], gi / L::S - 1);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (ok) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) put(lines + u * 1024 + lane % CH / 4 * L::LINES, (i * 32 + lane) / CH, lane % CH % 4, v[u & 1][i]);
-            if (rank == 0 && lane < 8 * rch) put(lines + u * 1024 + L::NB * L::LINES, lane / rch, lane % rch, vr[u & 1]);
+          for (int i = lane; i < 16 * rch; i += 32) {
+            const int r = i / rch;
+            const int64_t src = __shfl_sync(0xFFFFFFFFu, off, r);
+            if (rank == 0) copy16(to + r * L::RAWROW + L::HD + i % rch * 16, p.pool + (src >= 0 ? src : 0) + C + i % rch * 16, src >= 0);
           }
-          if (u < 2) fetch(u + 2);
+        }
+        copy_commit();
+      };
+#pragma unroll
+      for (int i = 0; i < L::RAWS - 1; ++i) fetch(lw + i * NLOAD, i);
+      int slot = 0;
+      for (int x = lw; x < units; x += NLOAD) {
+        const int gi = tile0 + x / PT, st = gi % p.stages;
+        copy_wait<L::RAWS - 2>();
+        __syncwarp();
+        fetch(x + (L::RAWS - 1) * NLOAD, slot == 0 ? L::RAWS - 1 : slot - 1);
+        if (gi >= p.stages) wait(&bars.empty[st], gi / p.stages - 1);
+        uint8_t* lines = ring + st * L::STAGE + x % PT * (U * 128);
+        const uint8_t* from = raw + slot * (16 * L::RAWROW);
+        if (ok) {
+#pragma unroll 4
+          for (int i = 0; i < CH / 2; ++i) {
+            const int r = (i * 32 + lane) / CH;
+            put(lines + lane % CH / 4 * L::LINES, r, lane % CH % 4, *reinterpret_cast<const uint4*>(from + r * L::RAWROW + lane % CH * 16));
+          }
+          if (rank == 0)
+            for (int i = lane; i < 16 * rch; i += 32)
+              put(lines + L::NB * L::LINES, i / rch, i % rch, *reinterpret_cast<const uint4*>(from + i / rch * L::RAWROW + L::HD + i % rch * 16));
         }
         fence_proxy_async_smem();
         mbar_arrive(&bars.full[st]);
-      } else {
-        if (gi >= L::S) wait(&bars.empty[st], gi / L::S - 1);
+        __syncwarp();  // the piece's place is free
+        slot = slot + 1 == L::RAWS ? 0 : slot + 1;
+      }
+    } else {
+      for (int x = lw; x < units; x += NLOAD) {
+        const int gi = tile0 + x / PT, st = gi % p.stages;
+        const int64_t off = offset_at(x);
+        uint8_t* lines = ring + st * L::STAGE + x % PT * (U * 128);
+        if (gi >= p.stages) wait(&bars.empty[st], gi / p.stages - 1);
         if (ok) {
           const bool rope = rank == 0 && (lane & 7) < p.rope / 8;
 #pragma unroll
@@ -281,7 +324,6 @@ struct Latent {
         // each thread's arrival, once its copies have landed
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.full[st])) : "memory");
       }
-      page = next;
     }
     copy_commit();
     copy_wait<0>();
@@ -289,6 +331,7 @@ struct Latent {
   // 16 e4m3 values as fp16: chunks 2 c and 2 c + 1 of row r's line.
   static __device__ __forceinline__ void put(uint8_t* lines, int r, int c, uint4 v) {
     uint8_t* row = lines + r * 128;
+    r &= 7;
     *reinterpret_cast<uint4*>(row + ((2 * c) ^ r) * 16) = make_uint4(f8_pair(v.x), f8_pair(v.x >> 16), f8_pair(v.y), f8_pair(v.y >> 16));
     *reinterpret_cast<uint4*>(row + ((2 * c + 1) ^ r) * 16) = make_uint4(f8_pair(v.z), f8_pair(v.z >> 16), f8_pair(v.w), f8_pair(v.w >> 16));
   }
@@ -301,13 +344,14 @@ struct Latent {
     const int rope = rank == 0 ? p.rope / 16 : 0;
     wait(&bars.q_full, segment);
     uint32_t idle = 0;
+    int sst = tile0 % p.stages, sph = tile0 / p.stages, vst = sst;  // the stages of both products' tiles
     for (int s = 0, v = 0; v < n && ok;) {
       bool did = false;
       const int gs = tile0 + s, gv = tile0 + v;
-      if (s < n && __all_sync(0xFFFFFFFFu, phase_done(&bars.full[gs % L::S], gs / L::S) && (gs == 0 || phase_done(&bars.s_free, gs - 1)))) {
+      if (s < n && __all_sync(0xFFFFFFFFu, phase_done(&bars.full[sst], sph) && (gs == 0 || phase_done(&bars.s_free, gs - 1)))) {
         fence_proxy_async_smem();  // the copies, which the barrier has put before this, seen by the tensor cores
         tc_fence_after();
-        const uint64_t k = line_desc(uniform(rs + gs % L::S * L::STAGE), 16);
+        const uint64_t k = line_desc(uniform(rs + sst * L::STAGE), 16);
 #pragma unroll
         for (int i = 0; i < L::HD / 16; ++i)
           mma_ts_on(t + L::CS, t + L::CQ + 8 * i, k + (i / 4 * L::LINES + i % 4 * 32) / 16, idesc(F8, TK, false), i > 0, on);
@@ -316,20 +360,23 @@ struct Latent {
           if (i < rope) mma_ss_on(t + L::CS, q + i * 2, k + (L::NB * L::LINES + i * 32) / 16, idesc(F8, TK, false), on);
         commit_on(smem_u32(&bars.s_full[gs & 1]), on);
         ++s;
+        if (++sst == p.stages) sst = 0, ++sph;
         did = true;
       }
       if (v < s && __all_sync(0xFFFFFFFFu, phase_done(&bars.p_full[gv & 1], gv >> 1))) {
         fence_proxy_async_smem();
         tc_fence_after();
-        const uint64_t c = line_desc(uniform(rs + gv % L::S * L::STAGE), L::LINES);
+        const uint64_t c = line_desc(uniform(rs + vst * L::STAGE), L::LINES);
         const uint32_t w = uniform(t + L::CP + TK / 2 * (gv & 1));
 #pragma unroll
         for (int k = 0; k < TK / 16; ++k) mma_ts_on(t + L::CO, w + 8 * k, c + k * 128, idesc(F8, L::HD, true), v > 0 || k > 0, on);
         commit_on(smem_u32(&bars.pv_done[gv & 1]), on);
-        commit_on(smem_u32(&bars.empty[gv % L::S]), on);
+        commit_on(smem_u32(&bars.empty[vst]), on);
         ++v;
+        if (++vst == p.stages) vst = 0;
         did = true;
       }
+      if (!did) __nanosleep(20);  // the slots are for the others
       idle = did ? 0 : idle + 1;
       if (idle > (1u << 25)) {
         ok = false;
@@ -338,16 +385,16 @@ struct Latent {
     }
   }
 
-  // ---- softmax: a thread per row; warps 0-3 take the even tiles, warps 4-7 the odd ones
+  // ---- softmax: two threads per row and tile, half of its positions each; warps 0-7 take the even tiles, warps 8-15 the odd
   float l;
   bool poison;  // the row sees a vector that is not finite (careful run)
 
   // The row's half of q into tensor memory, its rope part into shared memory; mul: the row's power of two (e4m3 cache).
-  __device__ __forceinline__ void load_q(const __nv_bfloat16* src, int r, uint32_t lanes, int half, bool active, float mul) {
+  __device__ __forceinline__ void load_q(const __nv_bfloat16* src, int r, uint32_t lanes, int part, bool active, float mul) {
     if (active) {
 #pragma unroll
-      for (int c = 0; c < L::HD / 4; c += 16) {
-        const int col = half * (L::HD / 4) + c;
+      for (int c = 0; c < L::HD / 8; c += 16) {
+        const int col = part * (L::HD / 8) + c;
         uint32_t v[16];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -359,7 +406,7 @@ struct Latent {
       tmem_wait_st();
     }
     if (rank == 0)
-      for (int c = half; c < p.rope / 8; c += 2)
+      for (int c = part; c < p.rope / 8; c += 4)
         *reinterpret_cast<uint4*>(qrope + r * 128 + (c ^ (r & 7)) * 16) =
             operand(src && active ? __ldg(reinterpret_cast<const uint4*>(src + C) + c) : make_uint4(0, 0, 0, 0), mul);
     fence_proxy_async_smem();
@@ -378,10 +425,10 @@ struct Latent {
       return x;
     }
   }
-  // Scales the row's sums in tensor memory, from column `sums` on, by c.
+  // Scales the row's sums in tensor memory, HD / 2 of them from column `sums` on, by c.
   static __device__ __forceinline__ void scale_sums(uint32_t sums, float c) {
 #pragma unroll 1
-    for (int d = 0; d < L::HD; d += 16) {
+    for (int d = 0; d < L::HD / 2; d += 16) {
       uint32_t v[16];
       tmem_ld16(sums + d, v);
       tmem_wait_ld();
@@ -393,19 +440,19 @@ struct Latent {
     tmem_wait_st();
   }
   template <int... I>
-  static __device__ __forceinline__ void send_all(uint32_t to, uint32_t bar, const float (&s)[TK], std::integer_sequence<int, I...>) {
+  static __device__ __forceinline__ void send_all(uint32_t to, uint32_t bar, const float (&s)[HC], std::integer_sequence<int, I...>) {
     (send16<I * 512>(to, bar, s + 4 * I), ...);
   }
   // A tile's scores: this CTA's half of the sum from tensor memory, to the other CTA, and with the other's half added.  The
   // other CTA's warp has a place for one tile, which it says is free.
-  __device__ __forceinline__ void exchange(float (&s)[TK], uint32_t lanes) {
+  __device__ __forceinline__ void exchange(float (&s)[HC], uint32_t lanes, int half) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t v[4][16];
+    uint32_t v[2][16];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld16(tb + lanes + L::CS + 16 * c, v[c]);
+    for (int c = 0; c < 2; ++c) tmem_ld16(tb + lanes + L::CS + HC * half + 16 * c, v[c]);
     tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 2; ++c) {
       tie(v[c]);
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[16 * c + e] = __uint_as_float(v[c][e]);
@@ -416,17 +463,17 @@ struct Latent {
       mbar_arrive(&bars.s_free);
       mbar_arrive_expect_tx(&bars.x_full[warp], XCHG);
     }
-    __syncwarp();
     if (xn > 0) wait(&bars.x_free[warp], xn - 1);
-    uint8_t* mine = xbuf + warp * XCHG + lane * 16;
+    else __syncwarp();
+    uint8_t* mine = xbuf + lane * 16;
     if (ok) {
       const uint32_t to = cluster_map(smem_u32(mine), rank ^ 1), bar = cluster_map(smem_u32(&bars.x_full[warp]), rank ^ 1);
-      send_all(to, bar, s, std::make_integer_sequence<int, TK / 4>());
+      send_all(to, bar, s, std::make_integer_sequence<int, HC / 4>());
     }
     wait(&bars.x_full[warp], xn);
     ++xn;
 #pragma unroll
-    for (int c = 0; c < TK / 4; ++c) {
+    for (int c = 0; c < HC / 4; ++c) {
       const float4 x = *reinterpret_cast<const float4*>(mine + c * 512);
       const float2 lo = fadd2(make_float2(s[4 * c], s[4 * c + 1]), make_float2(x.x, x.y));
       const float2 hi = fadd2(make_float2(s[4 * c + 2], s[4 * c + 3]), make_float2(x.z, x.w));
@@ -439,40 +486,40 @@ struct Latent {
   template <bool CAREFUL>
   __device__ __forceinline__ void softmax(uint32_t lanes, int r, bool active, int pos, uint64_t bits, float f) {
     const AttnArgs& a = p.a;
-    const int n = g.t1 - g.t0, all_hi = g.len - a.T - 1, wg = threadIdx.x >> 7, quarter = (threadIdx.x >> 5) & 3;
+    const int n = g.t1 - g.t0, all_hi = g.len - a.T - 1, warp = threadIdx.x >> 5, wg = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
     const bool lead = (threadIdx.x & 31) == 0;
     float m = pos < 0 ? INFINITY : -INFINITY;  // padding: weights of 0 wherever masks are not looked at
     l = 0.0f;
     poison = false;
     for (int i = (tile0 & 1) ^ wg; i < n; i += 2) {
-      const int gi = tile0 + i, tile = (g.t0 + i) * TK;
-      float s[TK];
+      const int gi = tile0 + i, tile = (g.t0 + i) * TK, base = tile + HC * half;
+      float s[HC];
       float scale = f, mx = -INFINITY;
       wait(&bars.s_full[wg], gi >> 1);
       tc_fence_after();
       if (active) {
-        exchange(s, lanes);
+        exchange(s, lanes, half);
         if (!(f > 0.0f)) {  // a factor that turns the order around comes first
           scale = 1.0f;
 #pragma unroll
-          for (int e = 0; e < TK; ++e) s[e] *= f;
+          for (int e = 0; e < HC; ++e) s[e] *= f;
         }
         if (tile + TK - 1 > all_hi) {
 #pragma unroll
-          for (int e = 0; e < TK; ++e)
-            if (!sees<true>(tile + e, pos, bits, g.len - a.T, 0)) s[e] = -INFINITY;
+          for (int e = 0; e < HC; ++e)
+            if (!sees<true>(base + e, pos, bits, g.len - a.T, 0)) s[e] = -INFINITY;
         }
         if constexpr (CAREFUL) {
 #pragma unroll
-          for (int e = 0; e < TK; ++e)
+          for (int e = 0; e < HC; ++e)
             if (!finite(s[e])) {
-              poison |= sees<true>(tile + e, pos, bits, g.len - a.T, 0);
+              poison |= sees<true>(base + e, pos, bits, g.len - a.T, 0);
               s[e] = -INFINITY;
             }
         }
         float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int e = 4; e < TK; e += 2) top[(e >> 1) & 3] = fmaxf(fmaxf(top[(e >> 1) & 3], s[e]), s[e + 1]);
+        for (int e = 4; e < HC; e += 2) top[(e >> 1) & 3] = fmaxf(fmaxf(top[(e >> 1) & 3], s[e]), s[e + 1]);
         mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
       } else {
         tc_fence_before();
@@ -480,13 +527,16 @@ struct Latent {
         if (lead) mbar_arrive(&bars.s_free);
       }
       // P of two tiles ago is used up: its columns are free, and so is its barrier, at which a warp without rows must not
-      // arrive for this tile before all others have for that one.
-      if (i > 1) wait(&bars.pv_done[wg], (gi - 2) >> 1);
-      // The tile before has its maxima; this one's are decided after them.
-      if (gi > 0) wait(&bars.decided[wg ^ 1][quarter], (gi - 1) >> 1);
+      // arrive for this tile before all others have for that one.  The tile before has its maxima; this one's are decided
+      // after them.
+      if (i > 1) wait(&bars.pv_done[wg], (gi - 2) >> 1, &bars.decided[wg ^ 1][quarter], (gi - 1) >> 1);
+      else if (gi > 0) wait(&bars.decided[wg ^ 1][quarter], (gi - 1) >> 1);
       tc_fence_after();
       if (active) {
         const float now = bars.m[r];
+        bars.top[2 * wg + half][r] = mx;
+        rows_sync(wg * 4 + quarter);  // both halves know the maximum, old and new
+        mx = fmaxf(mx, bars.top[2 * wg + (half ^ 1)][r]);
         if (now != m) {  // raised by the tile before
           l *= m == -INFINITY ? 0.0f : ex2(m - now);
           m = now;
@@ -494,12 +544,15 @@ struct Latent {
         const bool grow = mx > (m == -INFINITY ? m : m + kGrow);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float c = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mx);
-          if (grow) bars.m[r] = m = mx;
+          if (grow) {
+            m = mx;
+            if (half == 0) bars.m[r] = mx;
+          }
           l *= c;
           if (i > 0) {
             wait(&bars.pv_done[wg ^ 1], (gi - 1) >> 1);
             tc_fence_after();
-            scale_sums(tb + lanes + L::CO, c);
+            scale_sums(tb + lanes + L::CO + half * (L::HD / 2), c);
             tc_fence_before();
           }
         }
@@ -510,24 +563,21 @@ struct Latent {
         const float mm = (m == -INFINITY ? 0.0f : m) - L::LIFT;  // nothing seen yet: the weights are 0
         const float2 sc = make_float2(scale, scale), off = make_float2(-mm, -mm);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 x = ffma2(make_float2(s[32 * c + e], s[32 * c + e + 1]), sc, off);
-            const float2 y = make_float2(ex2(x.x), ex2(x.y));
-            sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], y);
-            w[e / 2] = pack2<F8>(y.x, y.y);
-          }
-          tmem_st16(tb + lanes + L::CP + TK / 2 * wg + 16 * c, w);
+        for (int e = 0; e < HC; e += 2) {
+          const float2 x = ffma2(make_float2(s[e], s[e + 1]), sc, off);
+          const float2 y = make_float2(ex2(x.x), ex2(x.y));
+          sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], y);
+          w[e / 2] = pack2<F8>(y.x, y.y);
         }
+        tmem_st16(tb + lanes + L::CP + TK / 2 * wg + 16 * half, w);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
       }
       if constexpr (CAREFUL) {  // (static, as is all that is not inlined: an object with an address would live in memory)
-        wait(&bars.full[gi % L::S], gi / L::S);
-        clean(ring + gi % L::S * L::STAGE + quarter * 2048);
+        wait(&bars.full[gi % p.stages], gi / p.stages);
+        clean(ring + gi % p.stages * L::STAGE + (warp & 7) * 1024);
       }
       tc_fence_before();
       __syncwarp();
@@ -542,13 +592,13 @@ struct Latent {
       if (now != m) l *= m == -INFINITY ? 0.0f : ex2(m - now);
     }
   }
-  // Zeros in the place of a tile's values that are not finite, 16 positions per warp of the tile's four: its scores are done,
-  // its sums not begun.
+  // Zeros in the place of a tile's values that are not finite, 8 positions per warp of the tile's eight: its scores are
+  // done, its sums not begun.
   static __device__ __noinline__ void clean(uint8_t* lines) {
     const int lane = threadIdx.x & 31;
     for (int h = 0; h < L::NB; ++h) {
       uint32_t* x = reinterpret_cast<uint32_t*>(lines + h * L::LINES);
-      for (int i = lane; i < 512; i += 32)
+      for (int i = lane; i < 256; i += 32)
         if (!finite16(x[i], F8)) {
           const uint32_t e = F8 ? 0x7C00u : 0x7F80u;
           x[i] = ((x[i] & e) == e ? 0 : x[i] & 0xFFFFu) | ((x[i] >> 16 & e) == e ? 0 : x[i] & 0xFFFF0000u);
@@ -564,27 +614,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ LBars bars;
   const AttnArgs& a = p.a;
-  uint8_t* ring = smem;
-  uint8_t* qrope = ring + L::S * L::STAGE;
-  uint8_t* xbuf = qrope + L::QROPE;
-  int* prefix = reinterpret_cast<int*>(xbuf + L::XBUF);
+  uint8_t* qrope = smem;
+  uint8_t* ring = qrope + L::QROPE;
+  uint8_t* xbuf = ring + p.stages * L::STAGE;
+  uint8_t* raw = xbuf + 4 * p.quarters * XCHG;
+  int* prefix = reinterpret_cast<int*>(raw + L::NLOAD * L::RAW);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int range = blockIdx.x >> 1;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::S; ++i) { mbar_init(&bars.full[i], 64); mbar_init(&bars.empty[i], 1); }
+    for (int i = 0; i < p.stages; ++i) { mbar_init(&bars.full[i], 32 * TK / (F8 ? 16 : 32)); mbar_init(&bars.empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i], 4);
+      mbar_init(&bars.p_full[i], 8);
       mbar_init(&bars.pv_done[i], 1);
-      for (int w = 0; w < 4; ++w) mbar_init(&bars.decided[i][w], 1);
+      for (int w = 0; w < 4; ++w) mbar_init(&bars.decided[i][w], 2);
     }
-    for (int w = 0; w < 8; ++w) { mbar_init(&bars.x_full[w], 1); mbar_init(&bars.x_free[w], 1); }
-    mbar_init(&bars.s_free, 4);
-    mbar_init(&bars.q_full, 8);
+    for (int w = 0; w < SW; ++w) { mbar_init(&bars.x_full[w], 1); mbar_init(&bars.x_free[w], 1); }
+    mbar_init(&bars.s_free, 8);
+    mbar_init(&bars.q_full, SW);
     fence_mbar_init();
   }
-  if (warp == 8 + L::NLOAD) { tmem_alloc(&bars.tmem, L::COLS); tmem_relinquish(); }
+  if (warp == SW + L::NLOAD) { tmem_alloc(&bars.tmem, L::COLS); tmem_relinquish(); }
   pdl_wait();
   pdl_launch_dependents();
   build_prefix(a, LSTART, prefix, bars.scan);
@@ -622,8 +673,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
     g.head_off = 0;
     g.t0 = u - it.i0;
     g.t1 = end - it.i0;
-    const int r = threadIdx.x & (LROWS - 1), half = (warp >> 2) & 1;  // softmax warps; half: of q's and the sums' dims
-    const bool active = warp < 8 && 32 * (warp & 3) < R;
+    const int r = threadIdx.x & (LROWS - 1), part = warp >> 2;  // softmax warps; part: of q's and the sums' dims
+    const bool active = warp < SW && 32 * (warp & 3) < R;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const int row = min(r0 + r, a.T * a.G - 1), t = row / a.G;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(it.b) * a.T + t) * a.q_stride +
@@ -631,7 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
     int pos = -1;
     uint64_t bits = 0;
     float f = a.scale * p.c_scale * 1.4426950408889634f, mul = 1.0f;
-    if (warp < 8) {
+    if (warp < SW) {
       // a chain is a tree whose masks are known
       bits = tree_bits(a.tree ? __ldg(a.tree + static_cast<int64_t>(it.b) * a.T + t) : (2ull << t) - 1, a.T, t, g.len);
       pos = tree_position(bits, a.T, g.len);
@@ -639,8 +690,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
     if (warp < 4) bars.m[r] = pos < 0 ? INFINITY : -INFINITY;
     if (threadIdx.x == 0) bars.bad = bars.peer_bad = 0;
     if constexpr (F8) {
-      if (warp < 8)  // the rows' largest values: a warp per row
-        for (int r4 = warp * 4; r4 < R; r4 += 32) {
+      if (warp < SW)  // the rows' largest values: a warp per row
+        for (int r4 = warp * 4; r4 < R; r4 += 4 * SW) {
           uint4 v[4][3];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -674,17 +725,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
         mul = __uint_as_float((254u << 23) - __float_as_uint(bars.back[r]));  // its inverse
       }
     }
-    Latent<C, F8> w{p, g, bars, ring, qrope, xbuf, tb, rank, tile0, xn, ok, 0.0f, false};
+    Latent<C, F8> w{p, g, bars, ring, qrope, xbuf + ((warp >> 2) * p.quarters + (warp & 3)) * XCHG, raw + (warp - SW) * L::RAW, tb, rank, tile0, xn, ok, 0.0f, false};
     bool careful = false;
     for (;;) {
-      if (warp < 8) {
-        w.load_q(r < R ? q : nullptr, r, lanes, half, active, mul);
+      if (warp < SW) {
+        w.load_q(r < R ? q : nullptr, r, lanes, part, active, mul);
         if (!careful) {
           w.template softmax<false>(lanes, r, active, pos, bits, f);
           if (active) {
             bool bad = false;
 #pragma unroll 1
-            for (int d = half * (L::HD / 2); d < (half + 1) * (L::HD / 2); d += 16) {
+            for (int d = part * (L::HD / 4); d < (part + 1) * (L::HD / 4); d += 16) {
               uint32_t v[16];
               tmem_ld16(tb + lanes + L::CO + d, v);
               tmem_wait_ld();
@@ -700,9 +751,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
         } else {
           w.template softmax<true>(lanes, r, active, pos, bits, f);
         }
-        bars.weight[half][r] = pos < 0 ? 0.0f : w.poison ? NAN : w.l;  // padding: whatever the keys were
-      } else if (warp < 8 + L::NLOAD) {
-        w.load(warp - 8, lane);
+        bars.top[part][r] = pos < 0 ? 0.0f : w.poison ? NAN : w.l;  // padding: whatever the keys were
+      } else if (warp < SW + L::NLOAD) {
+        w.load(warp - SW, lane);
       } else {
         w.products(lane, segment);
       }
@@ -726,13 +777,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
     const bool whole = u == it.i0 && end == it.i1;
     const int slot = 2 * range + (lo >= it.i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
     if (!whole && u == it.i0) split = {it.b, it.rt, line.range_of(it.i1 - 1) - range + 1, slot};
-    // out through shared memory, in the ring's and q's place, a row of the half at a time
+    // out through shared memory, in q's and the ring's place, a row of the half at a time
     if (active) {
-      const float weight = bars.weight[0][r] + bars.weight[1][r];
+      const float weight = (bars.top[0][r] + bars.top[1][r]) + (bars.top[2][r] + bars.top[3][r]);
       const float inv = weight == 0.0f ? 0.0f : p.c_scale / weight;
-      uint8_t* stage = ring + r * L::OROW;
+      uint8_t* stage = smem + r * L::OROW;
 #pragma unroll 1
-      for (int d = half * (L::HD / 2); d < (half + 1) * (L::HD / 2); d += 16) {
+      for (int d = part * (L::HD / 4); d < (part + 1) * (L::HD / 4); d += 16) {
         uint32_t v[16];
         tmem_ld16(tb + lanes + L::CO + d, v);
         tmem_wait_ld();
@@ -745,15 +796,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
           else *reinterpret_cast<float4*>(stage + (d + i) * 4) = x;
         }
       }
-      if (!whole && half == 0 && rank == 0 && r < R)
+      if (!whole && part == 0 && rank == 0 && r < R)
         *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * p.rows + r) * 2) = make_float2(pos < 0 ? -INFINITY : bars.m[r], weight);
       fence_proxy_async_smem();
     }
-    if (warp < 8) {
+    if (warp < SW) {
       softmax_sync();
-      if (half == 0 && r < R) {
+      if (part == 0 && r < R) {
         void* dst = whole ? static_cast<void*>(out_row(r)) : p.part + (static_cast<int64_t>(slot) * p.rows + r) * C + rank * L::HD;
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(ring + r * L::OROW)),
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(smem + r * L::OROW)),
                      "r"(whole ? L::HD * 2 : L::HD * 4)
                      : "memory");
         asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
@@ -769,7 +820,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  if (warp == 8 + L::NLOAD) tmem_dealloc(tb, L::COLS);
+  if (warp == SW + L::NLOAD) tmem_dealloc(tb, L::COLS);
 }
 
 // Joins the parts of the items that span ranges: o = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k, in the ranges' order.
@@ -856,9 +907,12 @@ LLayout latent_layout(int C, int64_t T, int H) {
 }
 
 template <int C, bool F8>
-cudaError_t launch_halves(const LParams& p, cudaStream_t st) {
+cudaError_t launch_halves(LParams p, cudaStream_t st) {
   using L = LCfg<C, F8>;
-  const size_t smem = L::SMEM + 4 * (static_cast<size_t>(p.a.B) + 1);
+  p.quarters = (p.rows + 31) / 32;
+  p.stages = F8 ? 2 : 3;  // and as many more as there is room for
+  while (p.stages < MOST_STAGES && L::smem(p.stages + 1, p.quarters, p.a.B) <= L::ROOM) ++p.stages;
+  const size_t smem = L::smem(p.stages, p.quarters, p.a.B);
   static int set[64] = {0};
   const int dev = current_device_id();
   if (set[dev] < static_cast<int>(smem)) {

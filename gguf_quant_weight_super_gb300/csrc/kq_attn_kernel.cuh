@@ -662,18 +662,20 @@ __device__ __forceinline__ int first_of(const AttnArgs& a, int len) {
   return a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0;
 }
 // Units of the line that one item of the sequence takes (an empty sequence has one, so that its rows are written).
+template <int TILE = TK>
 __device__ __forceinline__ int units_of(const AttnArgs& a, int len, int start) {
-  return len > 0 ? start + (len + TK - 1) / TK - first_of(a, len) / TK : 1;
+  return len > 0 ? start + (len + TILE - 1) / TILE - first_of(a, len) / TILE : 1;
 }
 
 // prefix [B + 1]: units (per head and row tile) before each sequence.  Threads 0 .. NTH - 1 work, every thread of the
 // block calls.
+template <int TILE = TK>
 __device__ __forceinline__ void build_prefix(const AttnArgs& a, int start, int* prefix, int* s_scan) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (a.B + NTH - 1) / NTH;
   const int b0 = tid < NTH ? min(a.B, tid * per) : a.B, b1 = tid < NTH ? min(a.B, b0 + per) : a.B;
   int n = 0;
-  for (int b = b0; b < b1; ++b) n += units_of(a, length_of(a, b, blockIdx.x == 0), start);
+  for (int b = b0; b < b1; ++b) n += units_of<TILE>(a, length_of(a, b, blockIdx.x == 0), start);
   int incl = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -686,7 +688,7 @@ __device__ __forceinline__ void build_prefix(const AttnArgs& a, int start, int* 
   for (int w = 0; w < warp && w < NW; ++w) before += s_scan[w];
   for (int b = b0; b < b1; ++b) {
     prefix[b] = before;
-    before += units_of(a, length_of(a, b, false), start);
+    before += units_of<TILE>(a, length_of(a, b, false), start);
     if (b == a.B - 1) prefix[a.B] = before;
   }
   __syncthreads();
@@ -696,11 +698,10 @@ __device__ __forceinline__ void build_prefix(const AttnArgs& a, int start, int* 
 struct Line {
   const int* prefix;
   int HR, nc, share, more;  // heads x row tiles of a sequence; ranges
-  __device__ __forceinline__ Line(const AttnArgs& a, int RT, const int* pre) : Line(a, RT, pre, gridDim.x) {}
-  __device__ __forceinline__ Line(const AttnArgs& a, int RT, const int* pre, int ranges) : prefix(pre) {
+  __device__ __forceinline__ Line(const AttnArgs& a, int RT, const int* pre) : prefix(pre) {
     HR = a.c.n_kv_heads * RT;  // the host has seen to it that the line's units fit 31 bits
     const int total = prefix[a.B] * HR;
-    nc = min(total, ranges);
+    nc = min(total, static_cast<int>(gridDim.x));
     share = total / nc;
     more = total - share * nc;
   }

@@ -2,53 +2,56 @@
 // cache of latent vectors c_j, which all heads share, in absorbed form:
 //   s_j = scale q.c_j (latent and rope part),  o = sum_j softmax(s)_j c_j[0 .. C)
 // in one pass with a running maximum and running sums, on the 5th-generation
-// tensor cores, with up to 128 rows (tokens x heads) as the M.
+// tensor cores.
 //
-// Bound: a vector of 1152 bytes (C = 512, bf16) serves 2 (2 C + 64) flops per
-// row, with 128 rows 242 flops per byte, near the device's 282: bytes and
-// products both have to run at their rate.  What is in the way is the room: the
-// sums of 128 rows, 512 fp32 values each, are all of an SM's tensor memory, and
-// the queries 144 KB of its shared memory.  So two SMs, a cluster, share 128 rows
-// by halves of the latent's dims: each CTA keeps its half of q and of the sums in
-// tensor memory, loads its half of every vector (the first also the rope part)
-// and multiplies it once as keys and once as values,
-//   S  = q_half K_half^T   (A: q in tensor memory; the rope part of q in shared memory)
-//   o += P V_half          (A: P = 2^(s - m) in tensor memory; V: the same lines, N-major)
-// Nothing is loaded or multiplied twice.  The price is S: each CTA has the sum
-// over its half of the dims only, so the CTAs send each other their halves' sums
-// (32 KB per tile of 64 positions and direction, straight from registers into the
-// other's shared memory, which tells the barrier its bytes) and both go through
-// the same softmax, bit for bit, as a + b is b + a.
+// Bound: a vector of 1152 bytes (C = 512, bf16) serves 2 (2 C + 64) flops per row
+// (a token's head): up to 64 rows the bytes bound it, with 128 rows 242 flops per
+// byte stand against the device's 282.  What is in the way is the room.  128 rows'
+// sums, 512 fp32 values each, would be all of an SM's tensor memory and their
+// queries 144 KB of its shared memory; so a CTA, one per SM, takes up to 64 rows.
+// Its products:
+//   S   = Q K^T    rows are the M (128 lanes, the upper ones idle), 48 positions the N;
+//                  Q in tensor memory (64 rows: three of its nine lines of 64 dims in
+//                  shared memory), K lines in shared memory
+//   O^T += V^T P^T dims are the M, 128 at a time, the rows the N: 16, 32 or 64 columns
+//                  of sums per 128 dims.  V^T is the same lines, M-major; P rows lie in
+//                  shared memory as K-major lines, so nothing is transposed
+// With rows as O's M all calls would pay for 128 of them.
 //
-// The roles of a CTA, as in kq_attn_wide.cu:
-//  * loader warps copy 8 positions at a time into a ring of stages, 64 dims of a
-//    position a line of 128 bytes in the matrix descriptors' 128-byte swizzle
-//    (e4m3 becomes fp16 on the way, exactly);
-//  * one warp issues S of the next tile and P V of this one, whichever can run;
-//  * eight softmax warps, two threads per row, 32 positions each.  A tile's own
-//    sums are read, and sent, as soon as they are there, while the tile before is
-//    worked on, so that the other CTA's arrive before they are asked for.
-// A row's maximum is raised, and its sums scaled down, only when it grows by more
-// than 2^8.  All tiles of all (sequence, 128 rows) items are one line, cut evenly
-// into one range per cluster; an item that spans ranges is left in parts in the
-// workspace, which a second launch joins in the ranges' order.
+// (Two CTAs that share 128 rows by halves of the dims load and multiply nothing
+// twice, but have to exchange the scores' halves: 32 KB per 64 positions through
+// the cluster's shared memory took 2000 clocks by itself, the tile 6300: 64
+// sequences of 4096 positions and 128 heads 171 us, and 99 us with 16 heads.)
+//
+// Warps:
+//  * loaders copy 16 positions at a time into a ring of stages of 48, 64 dims of
+//    a position a line of 128 bytes in the matrix descriptors' 128-byte swizzle
+//    (e4m3: 8 positions, as they are, into places of their own, and from there as
+//    fp16, exactly, into the lines);
+//  * one warp issues S of the next tile and O of this one, whichever can run;
+//  * softmax warps, two threads per row and tile, half of its positions each; two
+//    groups of them take every other tile, as a tile's chain of steps is longer
+//    than its share of the time.  A row's maximum is raised only when it grows by
+//    more than 2^8;
+//  * four warps then scale the sums down, before this tile's are added.
+// All tiles of all (sequence, rows) items are one line, cut evenly into one range
+// per CTA; an item that spans ranges is left in parts in the workspace, which a
+// second launch joins in the ranges' order.
 //
 // Precision: q and the cache enter exactly (an e4m3 cache as fp16 values, with q
 // scaled by a power of two per row: 2^-38 of the row's largest).  Weights enter
-// P V as bf16, 2^-8 of each (fp16 beside an e4m3 cache, 2^-11, or 2^-32 of the
-// row's largest): independent errors, that stay below the result's own rounding
-// to bf16 in the sum, while a second part would make the products 1.5 times as
-// much where they bound the call.  Sums, statistics and parts are fp32.
+// the second product as bf16, 2^-8 of each (fp16 beside an e4m3 cache, 2^-11, or
+// 2^-32 of the row's largest): independent errors, which in the sum stay below the
+// result's own rounding to bf16, while a second part would be half as many
+// products again where they bound the call.  Sums, statistics and parts are fp32.
 //
 // Every wait is bounded: one that gives up sets the device error word, after
 // which the CTA's roles run through without waiting.
 //
 // Vectors that some rows see and others do not would reach the others as 0 * NaN
 // if they are not finite: a segment whose sums are not all finite runs again; then
-// each value that is not finite becomes 0 before P V, and a row that sees such a
-// vector (its score is not finite) becomes NaN.
-#include <utility>
-
+// each value that is not finite becomes 0 before the second product, and a row that
+// sees such a vector (its score is not finite) becomes NaN.
 #include "kq_attn_kernel.cuh"
 #include "kq_vec.cuh"
 
@@ -56,37 +59,34 @@ namespace kq {
 namespace attn {
 namespace {
 
-constexpr int LROWS = 128;               // rows of an item
-constexpr int LSTART = 4;                // tiles' time that an item costs besides its tiles
-constexpr float kGrow = 8.0f;            // log2 units that a row's maximum may lag behind
-constexpr int SW = 16;                   // softmax warps
-constexpr int HC = TK / 2;               // a softmax thread's positions of a tile
-constexpr int XCHG = 32 * HC * 4;        // bytes that a warp sends per tile
-constexpr int MOST_STAGES = 6;
+constexpr int LT = 48;                // positions per tile
+constexpr int HC = LT / 2;            // a softmax thread's positions of a tile
+constexpr int LSTART = 4;             // tiles' time that an item costs besides its tiles
+constexpr float kGrow = 8.0f;         // log2 units that a row's maximum may lag behind
+constexpr int MOST_ROWS = 64, MOST_STAGES = 6;
+// Warps 0-15 by four: the first two of each four are softmax warps (their tensor memory lanes are rows 0-31 and 32-63), of
+// the others one issues products and seven load; warps 16-19 scale sums.
+constexpr int LTH = 20 * 32, PRODUCTS = 2, NLOAD = 7;
 
-template <int C, bool F8>
+template <int C, bool F8, int NR>
 struct LCfg {
-  static constexpr int NLOAD = 3;                     // loader warps
-  static constexpr int TH = (SW + NLOAD + 1) * 32;    // softmax warps, loaders, products
-  static constexpr int HD = C / 2;                    // dims of a CTA's half
-  static constexpr int NB = HD / 64;                  // lines of a position, without the rope part's
-  static constexpr int LINES = TK * 128;              // 64 dims of a tile's positions
-  static constexpr int STAGE = (NB + 1) * LINES;      // the last lines: the rope part, in the first CTA
-  static constexpr int QROPE = LROWS * 128;
-  static constexpr int OROW = HD * 4 + 16;            // bytes of a row of sums on its way out, in q's and the ring's place
-  // e4m3: 16 positions as they are in the cache, and how many such pieces a loader warp has on their way
-  static constexpr int RAWROW = HD + 64, RAWS = F8 ? 3 : 0, RAW = RAWS * 16 * RAWROW;
-  // Shared memory: q's rope part, the ring, the exchange (by quarters of the rows), the raw pieces, the line's index.
-  static constexpr int smem(int stages, int quarters, int B) {
-    return QROPE + stages * STAGE + 4 * quarters * XCHG + NLOAD * RAW + 4 * (B + 1);
-  }
-  static constexpr int ROOM = 227 * 1024 - 4096;  // less the static memory
-  static_assert(smem(F8 ? 2 : 3, 4, 4096) <= ROOM, "all rows, the most sequences");
-  static_assert(QROPE + (F8 ? 2 : 3) * STAGE + (F8 ? 4 * XCHG + NLOAD * RAW : 0) >= (F8 ? 32 : 128) * OROW, "and the sums on their way out");
-  // tensor memory columns: q, S, P x 2, o
-  static constexpr int CQ = 0, CS = HD / 2, CP = CS + TK, CO = CP + TK, COLS = 512;
-  static constexpr float LIFT = F8 ? 7.0f : 0.0f;  // log2: fp16 weights, below 2^8, fill fp16's range
-  static_assert(CO + HD <= COLS);
+  static constexpr int NB = C / 64 + 1;               // lines of a position, the rope part's last
+  static constexpr int LINES = LT * 128;              // 64 dims of a tile's positions
+  static constexpr int STAGE = NB * LINES;
+  static constexpr int QT = C == 512 && NR == 64 ? 6 : NB;  // lines of q in tensor memory
+  static constexpr int QS = (NB - QT) * NR * 128;     // the others, in shared memory
+  static constexpr int P = NR * 128;                  // a tile's weights
+  static constexpr int U = F8 ? 8 : 16;               // positions at a time of a loader
+  static constexpr int LOADERS = F8 ? 6 : NLOAD;
+  static constexpr int RAWROW = C + 64, RAWS = F8 ? 2 : 0, RAW = RAWS * U * RAWROW;
+  static constexpr int smem(int stages, int B) { return QS + 2 * P + stages * STAGE + LOADERS * RAW + 4 * (B + 1); }
+  static constexpr int ROOM = 227 * 1024 - 4096;      // less the static memory
+  static constexpr int LEAST = F8 ? 2 : 3;            // stages
+  static_assert(smem(LEAST, 4096) <= ROOM);
+  // tensor memory columns: o, q, S
+  static constexpr int MB = C / 128, CO = 0, CQ = C == 256 ? 256 : NR == 64 ? 256 : 128, CS = 448, COLS = 512;
+  static_assert(MB * NR <= CQ && CQ + 32 * QT <= CS && CS + LT <= COLS);
+  static constexpr float LIFT = F8 ? 7.0f : 0.0f;     // log2: fp16 weights, below 2^8, fill fp16's range
 };
 
 // A range's item that goes on in the next ranges.
@@ -99,31 +99,33 @@ struct LParams {
   const uint8_t* pool;
   int64_t page_bytes, slot_bytes;
   float c_scale;
-  int rope, RT, clusters, rows;  // rows: of a part
-  int stages, quarters;          // of the ring; of 32 rows that an item can have
+  int rope, RT, rows, ranges, stages;  // rows: of a part
   Split* split;
   float *part_ml, *part;
 };
 
 struct LBars {
-  uint64_t full[MOST_STAGES], empty[MOST_STAGES], s_full[2], s_free, p_full[2], pv_done[2], q_full, x_full[SW], x_free[SW], decided[2][4];
+  uint64_t full[MOST_STAGES], empty[MOST_STAGES], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, decided[2][2], grown[2], scaled[2];
   uint32_t tmem;
-  int bad, peer_bad;
+  int bad;
   int scan[NW];
-  float back[LROWS];           // e4m3: the rows' powers of two
-  float m[LROWS];              // the rows' maxima that their sums are relative to, in log2 units
-  float top[4][LROWS];         // a warpgroup's half of a tile: the rows' largest score; at the end, its weight sums
+  int raise[2];                  // a warpgroup's last tile, counted from 1, that raised a maximum
+  float back[MOST_ROWS];         // e4m3: the rows' powers of two
+  float m[MOST_ROWS];            // the rows' maxima that their sums are relative to, in log2 units
+  float factor[2][MOST_ROWS];    // a warpgroup's tile: what the sums are scaled by; at the end [0]: the rows' last factor
+  float top[4][MOST_ROWS];       // a warpgroup's half of a tile: the rows' largest score; at the end, its weight sums
+  int seen[MOST_ROWS];           // 0: padding
 };
 
 // Shared-memory operand in 128-byte-swizzled groups of 8 lines (1024 bytes apart); mn_step: bytes from 64 values along M or
-// N to the next (N-major operands).
+// N to the next (operands whose M or N is contiguous).
 __device__ __forceinline__ uint64_t line_desc(uint32_t saddr, uint32_t mn_step) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (static_cast<uint64_t>((mn_step >> 4) & 0x3FFF) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
-// kind::f16, fp32 accumulator, bf16 or fp16 operands, M = 128; n_major: B's N is contiguous
-__device__ __forceinline__ constexpr uint32_t idesc(bool f16, int n, bool n_major) {
-  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+// kind::f16, fp32 accumulator, bf16 or fp16 operands, M = 128; m_major: A's M is contiguous
+__device__ __forceinline__ constexpr uint32_t idesc(bool f16, int n, bool m_major) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (m_major ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 // Products issued by one lane of a converged warp (`on`), so that their operands can stay in uniform registers: moving
 // them there for a lane's branch took twice the products' time.
@@ -134,11 +136,11 @@ __device__ __forceinline__ void mma_ts_on(uint32_t d_taddr, uint32_t a_taddr, ui
       "r"(a_taddr), "l"(b_desc), "r"(id), "r"(accumulate), "r"(on)
       : "memory");
 }
-__device__ __forceinline__ void mma_ss_on(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t id, uint32_t on) {
+__device__ __forceinline__ void mma_ss_on(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t id, uint32_t accumulate, uint32_t on) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.eq.u32 p, 0, 0;\n\tsetp.ne.u32 q, %4, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_taddr),
-      "l"(a_desc), "l"(b_desc), "r"(id), "r"(on)
+      "l"(a_desc), "l"(b_desc), "r"(id), "r"(accumulate), "r"(on)
       : "memory");
 }
 __device__ __forceinline__ void commit_on(uint32_t bar, uint32_t on) {
@@ -153,13 +155,6 @@ __device__ __forceinline__ uint32_t elect() {
   return r;
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
-// 16 bytes into the other CTA's shared memory; its barrier there counts them.
-template <int TO>
-__device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, const float* x) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0 + %6], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
-               "r"(__float_as_uint(x[0])), "r"(__float_as_uint(x[1])), "r"(__float_as_uint(x[2])), "r"(__float_as_uint(x[3])), "r"(bar), "n"(TO)
-               : "memory");
-}
 __device__ __forceinline__ bool phase_done(uint64_t* bar, int phase) {
   uint32_t done;
   asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
@@ -168,12 +163,19 @@ __device__ __forceinline__ bool phase_done(uint64_t* bar, int phase) {
                : "memory");
   return done != 0;
 }
-// After the wait for tensor-memory loads: uses of v stay behind it.
-__device__ __forceinline__ void tie(uint32_t (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[i]));
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+// After the wait for tensor-memory loads: uses of v stay behind it.
+template <int N>
+__device__ __forceinline__ void tie(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // The two warps of 32 rows that work on one tile.
 __device__ __forceinline__ void rows_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(2 + id) : "memory"); }
 // A copy of 16 bytes, both addresses with constant offsets.
@@ -181,41 +183,26 @@ template <int TO, int FROM>
 __device__ __forceinline__ void copy16_at(uint32_t dst, const uint8_t* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0), "n"(TO), "n"(FROM) : "memory");
 }
-__device__ __forceinline__ void arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ bool finite16(uint32_t two, bool f16) {  // both halves
   const uint32_t e = f16 ? 0x7C00u : 0x7F80u;
   return (two & e) != e && (two >> 16 & e) != e;
 }
 
-template <int C, bool F8>
+template <int C, bool F8, int NR>
 struct Latent {
-  using L = LCfg<C, F8>;
+  using L = LCfg<C, F8, NR>;
   const LParams& p;
   const Seg g;
   LBars& bars;
-  uint8_t* ring;
-  uint8_t* qrope;
-  uint8_t* xbuf;  // a softmax warp's place
-  uint8_t* raw;   // a loader warp's
-  uint32_t tb;    // tensor memory
-  uint32_t rank;  // the CTA's half
-  int tile0;      // tiles of earlier segments: the barriers' phases and the ring go on
-  int xn;         // a softmax warp's tiles so far, as its exchange counts them
-  bool ok;        // no wait has given up
+  uint8_t *qs, *ps, *ring, *raw;
+  uint32_t tb;  // tensor memory
+  int tile0;    // tiles of earlier segments: the barriers' phases and the ring go on
+  bool ok;      // no wait has given up
 
   __device__ __forceinline__ void wait(uint64_t* bar, int phase) {
     if (!ok || __all_sync(0xFFFFFFFFu, phase_done(bar, phase))) return;
-    bool done = false;
-    for (uint32_t i = 0; i < kMaxPolls && !done; ++i) {
-      done = mbar_try_wait(bar, static_cast<uint32_t>(phase & 1));
-      done = __all_sync(0xFFFFFFFFu, done || phase_done(bar, phase));
-    }
-    ok = done && __all_sync(0xFFFFFFFFu, phase_done(bar, phase));
-    if (!ok) record_error(p.a.err, DEV_ERR_MBAR_TIMEOUT);
+    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, static_cast<uint32_t>(phase & 1), p.a.err));
   }
-
   // Both, which are mostly done already.
   __device__ __forceinline__ void wait(uint64_t* bar, int phase, uint64_t* bar2, int phase2) {
     if (!ok || __all_sync(0xFFFFFFFFu, phase_done(bar, phase) && phase_done(bar2, phase2))) return;
@@ -235,90 +222,88 @@ struct Latent {
 
   // ---- loaders: U positions at a time, in turn, their page ids one turn ahead
   __device__ __forceinline__ void load(int lw, int lane) {
-    constexpr int NLOAD = L::NLOAD, U = F8 ? 16 : 32, PT = TK / U;
-    const int n = g.t1 - g.t0, b0 = g.t0 * TK, units = PT * n;
+    constexpr int U = L::U, PT = LT / U, STEP = L::LOADERS;
+    const int n = g.t1 - g.t0, b0 = g.t0 * LT, units = PT * n;
     auto page_of = [&](int x) {  // of this lane's position
       const int j = b0 + U * x + lane % U;
       return x < units && j < g.len ? __ldg(g.table + (j >> p.a.page_shift)) : 0;
     };
     int page = page_of(lw);
     auto offset_at = [&](int x) {  // and its offset, the next page on its way
-      const int next = page_of(x + NLOAD);
+      const int next = page_of(x + STEP);
       const int64_t off = offset_of(b0 + U * x + lane % U, page);
       page = next;
       return off;
     };
     if constexpr (F8) {
-      // Pieces come as they are, RAWS - 1 ahead, and go into their lines as fp16.
-      constexpr int CH = L::HD / 16;  // 16-byte chunks of a row, without the rope part
-      const int rch = p.rope / 16;    // 2 or 4
+      constexpr int CH = C / 16;    // 16-byte chunks of a row, without the rope part
+      const int rch = p.rope / 16;  // 2 or 4
       auto fetch = [&](int x, int slot) {
         const int64_t off = x < units ? offset_at(x) : 0;
-        const uint32_t to = smem_u32(raw) + slot * (16 * L::RAWROW);
+        const uint32_t to = smem_u32(raw) + slot * (U * L::RAWROW);
         if (x < units && ok) {
 #pragma unroll
-          for (int i = 0; i < CH / 2; ++i) {
+          for (int i = 0; i < U * CH / 32; ++i) {
             const int r = (i * 32 + lane) / CH;
             const int64_t src = __shfl_sync(0xFFFFFFFFu, off, r);
-            copy16(to + r * L::RAWROW + lane % CH * 16, p.pool + (src >= 0 ? src : 0) + rank * L::HD + lane % CH * 16, src >= 0);
+            copy16(to + r * L::RAWROW + lane % CH * 16, p.pool + (src >= 0 ? src : 0) + lane % CH * 16, src >= 0);
           }
-          for (int i = lane; i < 16 * rch; i += 32) {
-            const int r = i / rch;
-            const int64_t src = __shfl_sync(0xFFFFFFFFu, off, r);
-            if (rank == 0) copy16(to + r * L::RAWROW + L::HD + i % rch * 16, p.pool + (src >= 0 ? src : 0) + C + i % rch * 16, src >= 0);
-          }
+          const int r = lane / rch & (U - 1);
+          const int64_t src = __shfl_sync(0xFFFFFFFFu, off, r);
+          if (lane < U * rch) copy16(to + r * L::RAWROW + C + lane % rch * 16, p.pool + (src >= 0 ? src : 0) + C + lane % rch * 16, src >= 0);
         }
         copy_commit();
       };
-#pragma unroll
-      for (int i = 0; i < L::RAWS - 1; ++i) fetch(lw + i * NLOAD, i);
+      fetch(lw, 0);
       int slot = 0;
-      for (int x = lw; x < units; x += NLOAD) {
+      for (int x = lw; x < units; x += STEP) {
         const int gi = tile0 + x / PT, st = gi % p.stages;
-        copy_wait<L::RAWS - 2>();
+        copy_wait<0>();
         __syncwarp();
-        fetch(x + (L::RAWS - 1) * NLOAD, slot == 0 ? L::RAWS - 1 : slot - 1);
+        fetch(x + STEP, slot ^ 1);
         if (gi >= p.stages) wait(&bars.empty[st], gi / p.stages - 1);
         uint8_t* lines = ring + st * L::STAGE + x % PT * (U * 128);
-        const uint8_t* from = raw + slot * (16 * L::RAWROW);
+        const uint8_t* from = raw + slot * (U * L::RAWROW);
         if (ok) {
 #pragma unroll 4
-          for (int i = 0; i < CH / 2; ++i) {
+          for (int i = 0; i < U * CH / 32; ++i) {
             const int r = (i * 32 + lane) / CH;
             put(lines + lane % CH / 4 * L::LINES, r, lane % CH % 4, *reinterpret_cast<const uint4*>(from + r * L::RAWROW + lane % CH * 16));
           }
-          if (rank == 0)
-            for (int i = lane; i < 16 * rch; i += 32)
-              put(lines + L::NB * L::LINES, i / rch, i % rch, *reinterpret_cast<const uint4*>(from + i / rch * L::RAWROW + L::HD + i % rch * 16));
+          if (lane < U * rch)
+            put(lines + (L::NB - 1) * L::LINES, lane / rch, lane % rch, *reinterpret_cast<const uint4*>(from + lane / rch * L::RAWROW + C + lane % rch * 16));
         }
         fence_proxy_async_smem();
         mbar_arrive(&bars.full[st]);
         __syncwarp();  // the piece's place is free
-        slot = slot + 1 == L::RAWS ? 0 : slot + 1;
+        slot ^= 1;
       }
     } else {
-      for (int x = lw; x < units; x += NLOAD) {
+      for (int x = lw; x < units; x += STEP) {
         const int gi = tile0 + x / PT, st = gi % p.stages;
         const int64_t off = offset_at(x);
         uint8_t* lines = ring + st * L::STAGE + x % PT * (U * 128);
         if (gi >= p.stages) wait(&bars.empty[st], gi / p.stages - 1);
         if (ok) {
-          const bool rope = rank == 0 && (lane & 7) < p.rope / 8;
+          const bool rope = (lane & 7) < p.rope / 8;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < U / 4; ++i) {
             const int r = (lane >> 3) + 4 * i;
-            int64_t src = __shfl_sync(0xFFFFFFFFu, off, r);
+            const int64_t src = __shfl_sync(0xFFFFFFFFu, off, r);
             const bool on = src >= 0;
             const uint8_t* from = p.pool + (on ? src : 0) + (lane & 7) * 16;
-            const uint8_t* half = from + rank * (2 * L::HD);
             const uint32_t to = smem_u32(lines) + r * 128 + ((lane & 7) ^ (r & 7)) * 16;
-            copy16_at<0, 0>(to, half, on);
-            copy16_at<L::LINES, 128>(to, half, on);
-            if constexpr (L::NB == 4) {
-              copy16_at<2 * L::LINES, 256>(to, half, on);
-              copy16_at<3 * L::LINES, 384>(to, half, on);
+            copy16_at<0, 0>(to, from, on);
+            copy16_at<L::LINES, 128>(to, from, on);
+            copy16_at<2 * L::LINES, 256>(to, from, on);
+            copy16_at<3 * L::LINES, 384>(to, from, on);
+            if constexpr (C == 512) {
+              copy16_at<4 * L::LINES, 512>(to, from, on);
+              copy16_at<5 * L::LINES, 640>(to, from, on);
+              copy16_at<6 * L::LINES, 768>(to, from, on);
+              copy16_at<7 * L::LINES, 896>(to, from, on);
             }
-            if (rope) copy16_at<L::NB * L::LINES, 2 * C>(to, from, on);
+            if (rope) copy16_at<(L::NB - 1) * L::LINES, 2 * C>(to, from, on);
           }
         }
         // each thread's arrival, once its copies have landed
@@ -336,40 +321,45 @@ struct Latent {
     *reinterpret_cast<uint4*>(row + ((2 * c + 1) ^ r) * 16) = make_uint4(f8_pair(v.z), f8_pair(v.z >> 16), f8_pair(v.w), f8_pair(v.w >> 16));
   }
 
-  // ---- products, by one warp (its first lane issues): S of the next tile, P V of the oldest, whichever can run
-  __device__ __forceinline__ void products(int lane, int segment) {
+  // ---- products, by one warp: S of the next tile, O of the oldest, whichever can run
+  __device__ __forceinline__ void products(int segment) {
     const int n = g.t1 - g.t0;
     const uint32_t rs = smem_u32(ring), t = uniform(tb), on = elect();
-    const uint64_t q = line_desc(smem_u32(qrope), 16);
-    const int rope = rank == 0 ? p.rope / 16 : 0;
+    const uint64_t q = line_desc(smem_u32(qs), 16), w0 = line_desc(smem_u32(ps), 16);
+    const int rope = p.rope / 16;
     wait(&bars.q_full, segment);
     uint32_t idle = 0;
     int sst = tile0 % p.stages, sph = tile0 / p.stages, vst = sst;  // the stages of both products' tiles
     for (int s = 0, v = 0; v < n && ok;) {
       bool did = false;
       const int gs = tile0 + s, gv = tile0 + v;
-      if (s < n && __all_sync(0xFFFFFFFFu, phase_done(&bars.full[sst], sph) && (gs == 0 || phase_done(&bars.s_free, gs - 1)))) {
+      if (s < n && __all_sync(0xFFFFFFFFu, phase_done(&bars.full[sst], sph) && (gs == 0 || phase_done(&bars.s_free[(gs - 1) & 1], (gs - 1) >> 1)))) {
         fence_proxy_async_smem();  // the copies, which the barrier has put before this, seen by the tensor cores
         tc_fence_after();
         const uint64_t k = line_desc(uniform(rs + sst * L::STAGE), 16);
 #pragma unroll
-        for (int i = 0; i < L::HD / 16; ++i)
-          mma_ts_on(t + L::CS, t + L::CQ + 8 * i, k + (i / 4 * L::LINES + i % 4 * 32) / 16, idesc(F8, TK, false), i > 0, on);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < rope) mma_ss_on(t + L::CS, q + i * 2, k + (L::NB * L::LINES + i * 32) / 16, idesc(F8, TK, false), on);
+        for (int i = 0; i < 4 * L::NB; ++i) {
+          if (i >= 4 * (L::NB - 1) && i - 4 * (L::NB - 1) >= rope) continue;
+          const uint64_t b = k + (i / 4 * L::LINES + i % 4 * 32) / 16;
+          if (i < 4 * L::QT) mma_ts_on(t + L::CS, t + L::CQ + 8 * i, b, idesc(F8, LT, false), i > 0, on);
+          else mma_ss_on(t + L::CS, q + ((i / 4 - L::QT) * (NR * 128) + i % 4 * 32) / 16, b, idesc(F8, LT, false), 1, on);
+        }
         commit_on(smem_u32(&bars.s_full[gs & 1]), on);
         ++s;
         if (++sst == p.stages) sst = 0, ++sph;
         did = true;
       }
-      if (v < s && __all_sync(0xFFFFFFFFu, phase_done(&bars.p_full[gv & 1], gv >> 1))) {
+      if (v < s && __all_sync(0xFFFFFFFFu, phase_done(&bars.p_full[gv & 1], gv >> 1) && phase_done(&bars.scaled[gv & 1], gv >> 1))) {
         fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t c = line_desc(uniform(rs + vst * L::STAGE), L::LINES);
-        const uint32_t w = uniform(t + L::CP + TK / 2 * (gv & 1));
+        const uint64_t w = w0 + uniform((gv & 1) * L::P / 16);
+        const uint32_t more = v > 0;
 #pragma unroll
-        for (int k = 0; k < TK / 16; ++k) mma_ts_on(t + L::CO, w + 8 * k, c + k * 128, idesc(F8, L::HD, true), v > 0 || k > 0, on);
+        for (int k = 0; k < LT / 16; ++k)
+#pragma unroll
+          for (int mb = 0; mb < L::MB; ++mb)
+            mma_ss_on(t + L::CO + mb * NR, c + (2 * mb * L::LINES + k * 2048) / 16, w + 2 * k, idesc(F8, NR, true), k > 0 ? 1 : more, on);
         commit_on(smem_u32(&bars.pv_done[gv & 1]), on);
         commit_on(smem_u32(&bars.empty[vst]), on);
         ++v;
@@ -385,30 +375,35 @@ struct Latent {
     }
   }
 
-  // ---- softmax: two threads per row and tile, half of its positions each; warps 0-7 take the even tiles, warps 8-15 the odd
+  // ---- softmax: two threads per row and tile, half of its positions each; the first warpgroup takes the even tiles
   float l;
   bool poison;  // the row sees a vector that is not finite (careful run)
 
-  // The row's half of q into tensor memory, its rope part into shared memory; mul: the row's power of two (e4m3 cache).
+  // Part `part` of four of the row's q; mul: the row's power of two (e4m3 cache).
   __device__ __forceinline__ void load_q(const __nv_bfloat16* src, int r, uint32_t lanes, int part, bool active, float mul) {
+    const int W = C + p.rope;
+    auto chunk = [&](int d) {  // 8 dims from d on
+      return operand(src && d < W ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0, 0, 0, 0), mul);
+    };
     if (active) {
 #pragma unroll
-      for (int c = 0; c < L::HD / 8; c += 16) {
-        const int col = part * (L::HD / 8) + c;
-        uint32_t v[16];
+      for (int c = 0; c < (2 * L::QT + 3) / 4; ++c) {
+        const int col = 16 * (part + 4 * c);
+        if (col < 32 * L::QT) {
+          uint32_t v[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 x = operand(src ? __ldg(reinterpret_cast<const uint4*>(src + rank * L::HD + 2 * col) + i) : make_uint4(0, 0, 0, 0), mul);
-          v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+          for (int i = 0; i < 4; ++i) {
+            const uint4 x = chunk(2 * col + 8 * i);
+            v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+          }
+          tmem_st16(tb + lanes + L::CQ + col, v);
         }
-        tmem_st16(tb + lanes + L::CQ + col, v);
       }
       tmem_wait_st();
+      if (r < NR)
+        for (int c = part; c < 8 * (L::NB - L::QT); c += 4)
+          *reinterpret_cast<uint4*>(qs + c / 8 * (NR * 128) + r * 128 + ((c & 7) ^ (r & 7)) * 16) = chunk(64 * L::QT + 8 * c);
     }
-    if (rank == 0)
-      for (int c = part; c < p.rope / 8; c += 4)
-        *reinterpret_cast<uint4*>(qrope + r * 128 + (c ^ (r & 7)) * 16) =
-            operand(src && active ? __ldg(reinterpret_cast<const uint4*>(src + C) + c) : make_uint4(0, 0, 0, 0), mul);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
@@ -425,63 +420,6 @@ struct Latent {
       return x;
     }
   }
-  // Scales the row's sums in tensor memory, HD / 2 of them from column `sums` on, by c.
-  static __device__ __forceinline__ void scale_sums(uint32_t sums, float c) {
-#pragma unroll 1
-    for (int d = 0; d < L::HD / 2; d += 16) {
-      uint32_t v[16];
-      tmem_ld16(sums + d, v);
-      tmem_wait_ld();
-      tie(v);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
-      tmem_st16(sums + d, v);
-    }
-    tmem_wait_st();
-  }
-  template <int... I>
-  static __device__ __forceinline__ void send_all(uint32_t to, uint32_t bar, const float (&s)[HC], std::integer_sequence<int, I...>) {
-    (send16<I * 512>(to, bar, s + 4 * I), ...);
-  }
-  // A tile's scores: this CTA's half of the sum from tensor memory, to the other CTA, and with the other's half added.  The
-  // other CTA's warp has a place for one tile, which it says is free.
-  __device__ __forceinline__ void exchange(float (&s)[HC], uint32_t lanes, int half) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t v[2][16];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) tmem_ld16(tb + lanes + L::CS + HC * half + 16 * c, v[c]);
-    tmem_wait_ld();
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      tie(v[c]);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[16 * c + e] = __uint_as_float(v[c][e]);
-    }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&bars.s_free);
-      mbar_arrive_expect_tx(&bars.x_full[warp], XCHG);
-    }
-    if (xn > 0) wait(&bars.x_free[warp], xn - 1);
-    else __syncwarp();
-    uint8_t* mine = xbuf + lane * 16;
-    if (ok) {
-      const uint32_t to = cluster_map(smem_u32(mine), rank ^ 1), bar = cluster_map(smem_u32(&bars.x_full[warp]), rank ^ 1);
-      send_all(to, bar, s, std::make_integer_sequence<int, HC / 4>());
-    }
-    wait(&bars.x_full[warp], xn);
-    ++xn;
-#pragma unroll
-    for (int c = 0; c < HC / 4; ++c) {
-      const float4 x = *reinterpret_cast<const float4*>(mine + c * 512);
-      const float2 lo = fadd2(make_float2(s[4 * c], s[4 * c + 1]), make_float2(x.x, x.y));
-      const float2 hi = fadd2(make_float2(s[4 * c + 2], s[4 * c + 3]), make_float2(x.z, x.w));
-      s[4 * c] = lo.x, s[4 * c + 1] = lo.y, s[4 * c + 2] = hi.x, s[4 * c + 3] = hi.y;
-    }
-    __syncwarp();
-    if (lane == 0) arrive_remote(cluster_map(smem_u32(&bars.x_free[warp]), rank ^ 1));
-  }
   // r: the row; f: from the raw product to log2 units.
   template <bool CAREFUL>
   __device__ __forceinline__ void softmax(uint32_t lanes, int r, bool active, int pos, uint64_t bits, float f) {
@@ -492,19 +430,31 @@ struct Latent {
     l = 0.0f;
     poison = false;
     for (int i = (tile0 & 1) ^ wg; i < n; i += 2) {
-      const int gi = tile0 + i, tile = (g.t0 + i) * TK, base = tile + HC * half;
+      const int gi = tile0 + i, tile = (g.t0 + i) * LT, base = tile + HC * half;
       float s[HC];
       float scale = f, mx = -INFINITY;
       wait(&bars.s_full[wg], gi >> 1);
       tc_fence_after();
       if (active) {
-        exchange(s, lanes, half);
+        {
+          uint32_t v[16], u[8];
+          tmem_ld16(tb + lanes + L::CS + HC * half, v);
+          tmem_ld8(tb + lanes + L::CS + HC * half + 16, u);
+          tmem_wait_ld();
+          tie(v);
+          tie(u);
+#pragma unroll
+          for (int e = 0; e < HC; ++e) s[e] = __uint_as_float(e < 16 ? v[e] : u[e - 16]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lead) mbar_arrive(&bars.s_free[wg]);
         if (!(f > 0.0f)) {  // a factor that turns the order around comes first
           scale = 1.0f;
 #pragma unroll
           for (int e = 0; e < HC; ++e) s[e] *= f;
         }
-        if (tile + TK - 1 > all_hi) {
+        if (tile + LT - 1 > all_hi) {
 #pragma unroll
           for (int e = 0; e < HC; ++e)
             if (!sees<true>(base + e, pos, bits, g.len - a.T, 0)) s[e] = -INFINITY;
@@ -524,46 +474,45 @@ struct Latent {
       } else {
         tc_fence_before();
         __syncwarp();
-        if (lead) mbar_arrive(&bars.s_free);
+        if (lead) mbar_arrive(&bars.s_free[wg]);
       }
-      // P of two tiles ago is used up: its columns are free, and so is its barrier, at which a warp without rows must not
+      // P of two tiles ago is used up: its place is free, and so are its barriers, at which a warp without rows must not
       // arrive for this tile before all others have for that one.  The tile before has its maxima; this one's are decided
       // after them.
       if (i > 1) wait(&bars.pv_done[wg], (gi - 2) >> 1, &bars.decided[wg ^ 1][quarter], (gi - 1) >> 1);
       else if (gi > 0) wait(&bars.decided[wg ^ 1][quarter], (gi - 1) >> 1);
-      tc_fence_after();
       if (active) {
         const float now = bars.m[r];
         bars.top[2 * wg + half][r] = mx;
-        rows_sync(wg * 4 + quarter);  // both halves know the maximum, old and new
+        rows_sync(wg * 2 + quarter);  // both halves know the maximum, old and new
         mx = fmaxf(mx, bars.top[2 * wg + (half ^ 1)][r]);
         if (now != m) {  // raised by the tile before
           l *= m == -INFINITY ? 0.0f : ex2(m - now);
           m = now;
         }
         const bool grow = mx > (m == -INFINITY ? m : m + kGrow);
+        float c = 1.0f;
         if (__any_sync(0xFFFFFFFFu, grow)) {
-          const float c = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mx);
           if (grow) {
+            c = m == -INFINITY ? 0.0f : ex2(m - mx);
             m = mx;
+            l *= c;
             if (half == 0) bars.m[r] = mx;
-          }
-          l *= c;
-          if (i > 0) {
-            wait(&bars.pv_done[wg ^ 1], (gi - 1) >> 1);
-            tc_fence_after();
-            scale_sums(tb + lanes + L::CO + half * (L::HD / 2), c);
-            tc_fence_before();
+            bars.raise[wg] = gi + 1;
           }
         }
+        if (half == 0 && r < NR) bars.factor[wg][r] = c;
       }
       __syncwarp();
-      if (lead) mbar_arrive(&bars.decided[wg][quarter]);
+      if (lead) {
+        mbar_arrive(&bars.decided[wg][quarter]);
+        mbar_arrive(&bars.grown[wg]);
+      }
       if (active) {
         const float mm = (m == -INFINITY ? 0.0f : m) - L::LIFT;  // nothing seen yet: the weights are 0
         const float2 sc = make_float2(scale, scale), off = make_float2(-mm, -mm);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-        uint32_t w[16];
+        uint32_t w[HC / 2];
 #pragma unroll
         for (int e = 0; e < HC; e += 2) {
           const float2 x = ffma2(make_float2(s[e], s[e + 1]), sc, off);
@@ -571,34 +520,37 @@ struct Latent {
           sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], y);
           w[e / 2] = pack2<F8>(y.x, y.y);
         }
-        tmem_st16(tb + lanes + L::CP + TK / 2 * wg + 16 * half, w);
+        if (r < NR) {
+          uint8_t* line = ps + wg * L::P + r * 128;
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            *reinterpret_cast<uint4*>(line + ((3 * half + c) ^ (r & 7)) * 16) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tmem_wait_st();
+        fence_proxy_async_smem();
       }
       if constexpr (CAREFUL) {  // (static, as is all that is not inlined: an object with an address would live in memory)
         wait(&bars.full[gi % p.stages], gi / p.stages);
-        clean(ring + gi % p.stages * L::STAGE + (warp & 7) * 1024);
+        clean(ring + gi % p.stages * L::STAGE, 2 * half + quarter);
       }
-      tc_fence_before();
       __syncwarp();
       if (lead) mbar_arrive(&bars.p_full[wg]);
     }
     const int last = tile0 + n - 1;
     if (wg == (last & 1)) wait(&bars.pv_done[wg], last >> 1);
     softmax_sync();
-    tc_fence_after();
     if (active) {  // relative to the rows' last maxima
       const float now = bars.m[r];
       if (now != m) l *= m == -INFINITY ? 0.0f : ex2(m - now);
     }
   }
-  // Zeros in the place of a tile's values that are not finite, 8 positions per warp of the tile's eight: its scores are
-  // done, its sums not begun.
-  static __device__ __noinline__ void clean(uint8_t* lines) {
+  // Zeros in the place of a tile's values that are not finite, 12 positions per warp of the tile's four: its scores are done,
+  // its sums not begun.
+  static __device__ __noinline__ void clean(uint8_t* stage, int quarter) {
     const int lane = threadIdx.x & 31;
-    for (int h = 0; h < L::NB; ++h) {
-      uint32_t* x = reinterpret_cast<uint32_t*>(lines + h * L::LINES);
-      for (int i = lane; i < 256; i += 32)
+    for (int h = 0; h < L::NB - 1; ++h) {
+      uint32_t* x = reinterpret_cast<uint32_t*>(stage + h * L::LINES + quarter * (L::LINES / 4));
+      for (int i = lane; i < L::LINES / 16; i += 32)
         if (!finite16(x[i], F8)) {
           const uint32_t e = F8 ? 0x7C00u : 0x7F80u;
           x[i] = ((x[i] & e) == e ? 0 : x[i] & 0xFFFFu) | ((x[i] >> 16 & e) == e ? 0 : x[i] & 0xFFFF0000u);
@@ -606,48 +558,76 @@ struct Latent {
     }
     fence_proxy_async_smem();
   }
+
+  // ---- the sums, of 32 of each 128 dims per warp: scaled when a tile has raised a row's maximum, before its own are added
+  __device__ __forceinline__ void rescale(uint32_t lanes) {
+    const int n = g.t1 - g.t0;
+    for (int i = 0; i < n; ++i) {
+      const int gi = tile0 + i, wg = gi & 1;
+      wait(&bars.grown[wg], gi >> 1);
+      if (i > 0 && bars.raise[wg] == gi + 1) {
+        wait(&bars.pv_done[wg ^ 1], (gi - 1) >> 1);
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < L::MB * NR; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(tb + lanes + L::CO + c, v);
+          tmem_wait_ld();
+          tie(v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * bars.factor[wg][(c & (NR - 1)) + e]);
+          tmem_st16(tb + lanes + L::CO + c, v);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.scaled[wg]);
+    }
+  }
 };
 
-template <int C, bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1) latent_kernel(const __grid_constant__ LParams p) {
-  using L = LCfg<C, F8>;
+template <int C, bool F8, int NR>
+__global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ LParams p) {
+  using L = LCfg<C, F8, NR>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ LBars bars;
   const AttnArgs& a = p.a;
-  uint8_t* qrope = smem;
-  uint8_t* ring = qrope + L::QROPE;
-  uint8_t* xbuf = ring + p.stages * L::STAGE;
-  uint8_t* raw = xbuf + 4 * p.quarters * XCHG;
-  int* prefix = reinterpret_cast<int*>(raw + L::NLOAD * L::RAW);
+  uint8_t* ps = smem + L::QS;
+  uint8_t* ring = ps + 2 * L::P;
+  uint8_t* raw = ring + p.stages * L::STAGE;
+  int* prefix = reinterpret_cast<int*>(raw + L::LOADERS * L::RAW);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int range = blockIdx.x >> 1;
+  const bool softmax = warp < 16 && (warp & 3) < 2, scaler = warp >= 16;
+  const int loader = !softmax && !scaler && warp != PRODUCTS ? (warp >> 2) * 2 + (warp & 3) - 3 : -1;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) { mbar_init(&bars.full[i], 32 * TK / (F8 ? 16 : 32)); mbar_init(&bars.empty[i], 1); }
+    for (int i = 0; i < p.stages; ++i) { mbar_init(&bars.full[i], 32 * LT / L::U); mbar_init(&bars.empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i], 8);
+      mbar_init(&bars.s_free[i], 4);
+      mbar_init(&bars.p_full[i], 4);
       mbar_init(&bars.pv_done[i], 1);
-      for (int w = 0; w < 4; ++w) mbar_init(&bars.decided[i][w], 2);
+      mbar_init(&bars.decided[i][0], 2);
+      mbar_init(&bars.decided[i][1], 2);
+      mbar_init(&bars.grown[i], 4);
+      mbar_init(&bars.scaled[i], 4);
+      bars.raise[i] = 0;
     }
-    for (int w = 0; w < SW; ++w) { mbar_init(&bars.x_full[w], 1); mbar_init(&bars.x_free[w], 1); }
-    mbar_init(&bars.s_free, 8);
-    mbar_init(&bars.q_full, SW);
+    mbar_init(&bars.q_full, 8);
     fence_mbar_init();
   }
-  if (warp == SW + L::NLOAD) { tmem_alloc(&bars.tmem, L::COLS); tmem_relinquish(); }
+  if (warp == PRODUCTS) { tmem_alloc(&bars.tmem, L::COLS); tmem_relinquish(); }
   pdl_wait();
   pdl_launch_dependents();
-  build_prefix(a, LSTART, prefix, bars.scan);
+  build_prefix<LT>(a, LSTART, prefix, bars.scan);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // the other CTA's barriers are there
   tc_fence_after();
-  const uint32_t tb = bars.tmem;
-  const Line line(a, p.RT, prefix, p.clusters);
-  const int lo = line.bound(min(range, line.nc)), hi = range < line.nc ? line.bound(range + 1) : lo;
+  const uint32_t tb = bars.tmem, lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  const Line line(a, p.RT, prefix);
+  const int range = blockIdx.x, lo = line.bound(min(range, line.nc)), hi = range < line.nc ? line.bound(range + 1) : lo;
   Split split = {0, 0, 0, 0};
-  int tile0 = 0, segment = 0, xn = 0;
+  int tile0 = 0, segment = 0;
   bool ok = true;
   for (int u = lo; u < hi;) {
     const Item it(a, line, p.RT, LSTART, u);
@@ -657,12 +637,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
       u = end;
       continue;
     }
-    const int r0 = it.rt * LROWS, R = min(LROWS, a.T * a.G - r0);
-    auto out_row = [&](int r) {
-      return static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(it.b) * a.T * a.G + r0 + r) * C + rank * L::HD;
-    };
+    const int r0 = it.rt * NR, R = min(NR, a.T * a.G - r0);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(it.b) * a.T * a.G + r0) * C;
     if (it.len == 0) {
-      for (int x = threadIdx.x; x < R * (L::HD / 4); x += L::TH) store4(out_row(x / (L::HD / 4)) + 4 * (x % (L::HD / 4)), make_float4(0, 0, 0, 0));
+      for (int x = threadIdx.x; x < R * (C / 4); x += LTH) store4(out + 4 * x, make_float4(0, 0, 0, 0));
       u = end;
       continue;
     }
@@ -673,25 +651,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
     g.head_off = 0;
     g.t0 = u - it.i0;
     g.t1 = end - it.i0;
-    const int r = threadIdx.x & (LROWS - 1), part = warp >> 2;  // softmax warps; part: of q's and the sums' dims
-    const bool active = warp < SW && 32 * (warp & 3) < R;
-    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const int r = 32 * (warp & 3) + lane, part = warp >> 2;  // softmax warps: the row, and which of four parts of the work
+    const bool active = softmax && 32 * (warp & 3) < R;
     const int row = min(r0 + r, a.T * a.G - 1), t = row / a.G;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(it.b) * a.T + t) * a.q_stride +
                              static_cast<int64_t>(row - t * a.G) * (C + p.rope);
     int pos = -1;
     uint64_t bits = 0;
     float f = a.scale * p.c_scale * 1.4426950408889634f, mul = 1.0f;
-    if (warp < SW) {
+    if (softmax) {
       // a chain is a tree whose masks are known
       bits = tree_bits(a.tree ? __ldg(a.tree + static_cast<int64_t>(it.b) * a.T + t) : (2ull << t) - 1, a.T, t, g.len);
       pos = tree_position(bits, a.T, g.len);
+      if (part == 0) {
+        bars.m[r] = pos < 0 ? INFINITY : -INFINITY;
+        bars.seen[r] = r < R && pos >= 0;
+      }
     }
-    if (warp < 4) bars.m[r] = pos < 0 ? INFINITY : -INFINITY;
-    if (threadIdx.x == 0) bars.bad = bars.peer_bad = 0;
+    if (threadIdx.x == 0) bars.bad = 0;
     if constexpr (F8) {
-      if (warp < SW)  // the rows' largest values: a warp per row
-        for (int r4 = warp * 4; r4 < R; r4 += 4 * SW) {
+      if (warp < 16)  // the rows' largest values: a warp per row, four at a time
+        for (int r4 = warp * 4; r4 < R; r4 += 64) {
           uint4 v[4][3];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -720,107 +700,108 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((LCfg<C, F8>::TH), 1
     }
     __syncthreads();  // the ring, the sums and tensor memory are free
     if constexpr (F8) {
-      if (r < R) {
+      if (softmax && r < R) {
         f *= bars.back[r];
         mul = __uint_as_float((254u << 23) - __float_as_uint(bars.back[r]));  // its inverse
       }
     }
-    Latent<C, F8> w{p, g, bars, ring, qrope, xbuf + ((warp >> 2) * p.quarters + (warp & 3)) * XCHG, raw + (warp - SW) * L::RAW, tb, rank, tile0, xn, ok, 0.0f, false};
+    Latent<C, F8, NR> w{p, g, bars, smem, ps, ring, raw + max(loader, 0) * L::RAW, tb, tile0, ok, 0.0f, false};
+    // Which of the sums a warp of the first 16 takes out: of 128 dims 32 (its lanes), of those 128 the part-th, or of the
+    // rows the half.
+    constexpr int SPAN = NR * L::MB / 4;  // columns
+    const int col0 = part * SPAN, mb = col0 / NR, c0 = col0 % NR;
     bool careful = false;
     for (;;) {
-      if (warp < SW) {
+      if (softmax) {
         w.load_q(r < R ? q : nullptr, r, lanes, part, active, mul);
-        if (!careful) {
-          w.template softmax<false>(lanes, r, active, pos, bits, f);
-          if (active) {
-            bool bad = false;
-#pragma unroll 1
-            for (int d = part * (L::HD / 4); d < (part + 1) * (L::HD / 4); d += 16) {
-              uint32_t v[16];
-              tmem_ld16(tb + lanes + L::CO + d, v);
-              tmem_wait_ld();
-              tie(v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) bad |= !finite(__uint_as_float(v[i]));
-            }
-            if (bad && r < R) {
-              bars.bad = 1;
-              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(smem_u32(&bars.peer_bad), rank ^ 1)), "r"(1) : "memory");
-            }
-          }
-        } else {
-          w.template softmax<true>(lanes, r, active, pos, bits, f);
-        }
+        if (!careful) w.template softmax<false>(lanes, r, active, pos, bits, f);
+        else w.template softmax<true>(lanes, r, active, pos, bits, f);
         bars.top[part][r] = pos < 0 ? 0.0f : w.poison ? NAN : w.l;  // padding: whatever the keys were
-      } else if (warp < SW + L::NLOAD) {
-        w.load(warp - SW, lane);
-      } else {
-        w.products(lane, segment);
+      } else if (scaler) {
+        w.rescale(lanes);
+      } else if (warp == PRODUCTS) {
+        w.products(segment);
+      } else if (loader < L::LOADERS) {
+        w.load(loader, lane);
       }
       ++segment;
       w.tile0 += g.t1 - g.t0;
-      if (!w.ok)  // what is on its way to or from a CTA that did not wait for it lands before the CTA can end
-        for (int i = 0; i < 100; ++i) __nanosleep(1000);
-      tc_fence_before();
-      __syncwarp();
-      cluster_sync();  // both CTAs have read what they were sent
+      __syncthreads();
       tc_fence_after();
-      if (careful || !(bars.bad | bars.peer_bad)) break;
+      if (careful) break;
+      if (warp < 16) {
+        bool bad = false;
+#pragma unroll 1
+        for (int c = 0; c < SPAN; c += 8) {
+          uint32_t v[8];
+          tmem_ld8(tb + lanes + L::CO + col0 + c, v);
+          tmem_wait_ld();
+          tie(v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) bad |= !finite(__uint_as_float(v[e])) && bars.seen[c0 + c + e];
+        }
+        if (bad) bars.bad = 1;
+      } else if (threadIdx.x - 512 < R) {  // and the rows' last factors
+        const int rr = threadIdx.x - 512;
+        const float weight = (bars.top[0][rr] + bars.top[1][rr]) + (bars.top[2][rr] + bars.top[3][rr]);
+        bars.factor[0][rr] = weight == 0.0f ? 0.0f : p.c_scale / weight;
+      }
+      tc_fence_before();
+      __syncthreads();
+      if (!bars.bad) break;
       careful = true;
-      if (warp < 4) bars.m[r] = pos < 0 ? INFINITY : -INFINITY;
-      cluster_sync();
+      if (softmax && part == 0) bars.m[r] = pos < 0 ? INFINITY : -INFINITY;
+      __syncthreads();
     }
     tile0 = w.tile0;
-    xn = w.xn;
     ok = w.ok;
+    if (careful) {
+      if (threadIdx.x < R) {
+        const int rr = threadIdx.x;
+        const float weight = (bars.top[0][rr] + bars.top[1][rr]) + (bars.top[2][rr] + bars.top[3][rr]);
+        bars.factor[0][rr] = weight == 0.0f ? 0.0f : p.c_scale / weight;
+      }
+      __syncthreads();
+    }
 
     const bool whole = u == it.i0 && end == it.i1;
     const int slot = 2 * range + (lo >= it.i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
     if (!whole && u == it.i0) split = {it.b, it.rt, line.range_of(it.i1 - 1) - range + 1, slot};
-    // out through shared memory, in q's and the ring's place, a row of the half at a time
-    if (active) {
-      const float weight = (bars.top[0][r] + bars.top[1][r]) + (bars.top[2][r] + bars.top[3][r]);
-      const float inv = weight == 0.0f ? 0.0f : p.c_scale / weight;
-      uint8_t* stage = smem + r * L::OROW;
+    if (warp < 16) {
+      const int d = mb * 128 + r;
+      float* to = p.part + static_cast<int64_t>(slot) * p.rows * C + d;
 #pragma unroll 1
-      for (int d = part * (L::HD / 4); d < (part + 1) * (L::HD / 4); d += 16) {
-        uint32_t v[16];
-        tmem_ld16(tb + lanes + L::CO + d, v);
+      for (int c = 0; c < SPAN && c0 + c < R; c += 8) {
+        uint32_t v[8];
+        tmem_ld8(tb + lanes + L::CO + col0 + c, v);
         tmem_wait_ld();
         tie(v);
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          float4 x = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-          if (pos < 0) x = make_float4(0, 0, 0, 0);
-          if (whole) put4(reinterpret_cast<__nv_bfloat16*>(stage) + d + i, x, inv);
-          else *reinterpret_cast<float4*>(stage + (d + i) * 4) = x;
+        for (int e = 0; e < 8; ++e) {
+          const int rr = c0 + c + e;
+          const float x = bars.seen[rr] ? __uint_as_float(v[e]) : 0.0f;
+          if (rr < R) {
+            if (whole) out[static_cast<int64_t>(rr) * C + d] = __float2bfloat16_rn(x * bars.factor[0][rr]);
+            else to[static_cast<int64_t>(rr) * C] = x;
+          }
         }
+        __syncwarp();
       }
-      if (!whole && part == 0 && rank == 0 && r < R)
-        *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * p.rows + r) * 2) = make_float2(pos < 0 ? -INFINITY : bars.m[r], weight);
-      fence_proxy_async_smem();
-    }
-    if (warp < SW) {
-      softmax_sync();
-      if (part == 0 && r < R) {
-        void* dst = whole ? static_cast<void*>(out_row(r)) : p.part + (static_cast<int64_t>(slot) * p.rows + r) * C + rank * L::HD;
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(smem + r * L::OROW)),
-                     "r"(whole ? L::HD * 2 : L::HD * 4)
-                     : "memory");
-        asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
-      }
+    } else if (!whole && threadIdx.x - 512 < R) {
+      const int rr = threadIdx.x - 512;
+      const float weight = (bars.top[0][rr] + bars.top[1][rr]) + (bars.top[2][rr] + bars.top[3][rr]);
+      *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * p.rows + rr) * 2) = make_float2(bars.seen[rr] ? bars.m[rr] : -INFINITY, weight);
     }
     tc_fence_before();
-    __syncthreads();  // the copies have read the ring; weights and maxima are read before the next segment writes them
+    __syncthreads();  // the sums, weights and maxima are read before the next segment writes them
     tc_fence_after();
     u = end;
   }
-  if (threadIdx.x == 0 && rank == 0) p.split[range] = split;
+  if (threadIdx.x == 0) p.split[range] = split;
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
   tc_fence_after();
-  if (warp == SW + L::NLOAD) tmem_dealloc(tb, L::COLS);
+  if (warp == PRODUCTS) tmem_dealloc(tb, L::COLS);
 }
 
 // Joins the parts of the items that span ranges: o = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k, in the ranges' order.
@@ -837,9 +818,9 @@ __global__ void __launch_bounds__(JTH) latent_join_kernel(const __grid_constant_
   const int4 s4 = __ldcg(reinterpret_cast<const int4*>(p.split) + blockIdx.x);
   const Split sp = {s4.x, s4.y, s4.z, s4.w};
   const int r = MANY ? blockIdx.y : blockIdx.y * JW + warp;
-  const int64_t row0 = static_cast<int64_t>(sp.rt) * LROWS;
+  const int64_t row0 = static_cast<int64_t>(sp.rt) * p.rows;
   if (sp.parts == 0 || row0 + (MANY ? r : r - warp) >= p.a.T * p.a.G) return;
-  const bool on = row0 + r < p.a.T * p.a.G;
+  const bool on = row0 + r < p.a.T * p.a.G && r < p.rows;
   auto slot_of = [&](int k) { return k == 0 ? sp.slot : 2 * (static_cast<int>(blockIdx.x) + k) + 1; };
   float* e = factor[MANY ? 0 : warp];
   float mm = -INFINITY, ll = 0.0f;
@@ -889,7 +870,9 @@ __global__ void __launch_bounds__(JTH) latent_join_kernel(const __grid_constant_
   }
 }
 
-int clusters() { return num_sms() / 2 < 160 ? num_sms() / 2 : 160; }
+int ranges() { return num_sms() < 160 ? num_sms() : 160; }
+// Rows of an item: 16, 32 or 64 columns of sums.
+int rows_of(int64_t all) { return all <= 16 ? 16 : all <= 32 ? 32 : MOST_ROWS; }
 
 struct LLayout {
   int rows;
@@ -897,35 +880,38 @@ struct LLayout {
 };
 LLayout latent_layout(int C, int64_t T, int H) {
   LLayout l;
-  l.rows = static_cast<int>(min_i64(LROWS, T * H));
+  l.rows = rows_of(T * H);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  const size_t slots = 2 * static_cast<size_t>(clusters());
-  l.ml_off = up(clusters() * sizeof(Split));
+  const size_t slots = 2 * static_cast<size_t>(ranges());
+  l.ml_off = up(ranges() * sizeof(Split));
   l.part_off = l.ml_off + up(slots * l.rows * 2 * sizeof(float));
   l.bytes = l.part_off + up(slots * l.rows * C * sizeof(float));
   return l;
 }
 
-template <int C, bool F8>
-cudaError_t launch_halves(LParams p, cudaStream_t st) {
-  using L = LCfg<C, F8>;
-  p.quarters = (p.rows + 31) / 32;
-  p.stages = F8 ? 2 : 3;  // and as many more as there is room for
-  while (p.stages < MOST_STAGES && L::smem(p.stages + 1, p.quarters, p.a.B) <= L::ROOM) ++p.stages;
-  const size_t smem = L::smem(p.stages, p.quarters, p.a.B);
+template <int C, bool F8, int NR>
+cudaError_t launch_rows(LParams p, cudaStream_t st) {
+  using L = LCfg<C, F8, NR>;
+  p.stages = L::LEAST;  // and as many more as there is room for
+  while (p.stages < MOST_STAGES && L::smem(p.stages + 1, p.a.B) <= L::ROOM) ++p.stages;
+  const size_t smem = L::smem(p.stages, p.a.B);
   static int set[64] = {0};
   const int dev = current_device_id();
   if (set[dev] < static_cast<int>(smem)) {
-    const cudaError_t e = cudaFuncSetAttribute(latent_kernel<C, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = cudaFuncSetAttribute(latent_kernel<C, F8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     set[dev] = static_cast<int>(smem);
   }
-  cudaError_t e = launch_pdl(latent_kernel<C, F8>, dim3(2 * p.clusters), dim3(L::TH), smem, st, p);
+  const cudaError_t e = launch_pdl(latent_kernel<C, F8, NR>, dim3(p.ranges), dim3(LTH), smem, st, p);
   if (e != cudaSuccess) return e;
   // few items: many parts of each
-  const bool many = static_cast<int64_t>(p.a.B) * p.RT * 8 <= p.clusters;
-  if (many) return launch_pdl(latent_join_kernel<C, true>, dim3(p.clusters, p.rows), dim3(JTH), 0, st, p);
-  return launch_pdl(latent_join_kernel<C, false>, dim3(p.clusters, (p.rows + 7) / 8), dim3(JTH), 0, st, p);
+  const bool many = static_cast<int64_t>(p.a.B) * p.RT * 8 <= p.ranges;
+  if (many) return launch_pdl(latent_join_kernel<C, true>, dim3(p.ranges, NR), dim3(JTH), 0, st, p);
+  return launch_pdl(latent_join_kernel<C, false>, dim3(p.ranges, (NR + 7) / 8), dim3(JTH), 0, st, p);
+}
+template <int C, bool F8>
+cudaError_t launch_type(const LParams& p, cudaStream_t st) {
+  return p.rows == 16 ? launch_rows<C, F8, 16>(p, st) : p.rows == 32 ? launch_rows<C, F8, 32>(p, st) : launch_rows<C, F8, MOST_ROWS>(p, st);
 }
 
 }  // namespace
@@ -961,16 +947,16 @@ cudaError_t launch_latent(const LatentArgs& x, cudaStream_t st) {
   p.slot_bytes = x.l.slot_stride * es;
   p.c_scale = x.l.scale;
   p.rope = x.l.rope_dim;
-  p.RT = (x.T * x.H + attn::LROWS - 1) / attn::LROWS;
-  p.clusters = attn::clusters();
   const attn::LLayout l = attn::latent_layout(x.l.latent_dim, x.T, x.H);
   p.rows = l.rows;
+  p.RT = (x.T * x.H + p.rows - 1) / p.rows;
+  p.ranges = attn::ranges();
   uint8_t* ws = static_cast<uint8_t*>(x.ws);
   p.split = reinterpret_cast<attn::Split*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + l.ml_off);
   p.part = reinterpret_cast<float*>(ws + l.part_off);
-  if (x.l.latent_dim == 512) return x.l.dtype == KQ_BF16 ? attn::launch_halves<512, false>(p, st) : attn::launch_halves<512, true>(p, st);
-  return x.l.dtype == KQ_BF16 ? attn::launch_halves<256, false>(p, st) : attn::launch_halves<256, true>(p, st);
+  if (x.l.latent_dim == 512) return x.l.dtype == KQ_BF16 ? attn::launch_type<512, false>(p, st) : attn::launch_type<512, true>(p, st);
+  return x.l.dtype == KQ_BF16 ? attn::launch_type<256, false>(p, st) : attn::launch_type<256, true>(p, st);
 }
 
 }  // namespace kq

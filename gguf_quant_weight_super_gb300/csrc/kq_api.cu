@@ -460,7 +460,7 @@ size_t kq_attn_tree_workspace_size(const kq_kv_cache* cache, int64_t B, int64_t 
   if (check_attn(cache, B, T, n_q_heads, kMaxTree) != KQ_OK) return 0;
   size_t most = 0;  // which kernel takes a call, and how many rows at a time, depends on T: room for any up to it
   for (int64_t t = 0; t <= T; ++t) {
-    const size_t n = attn_workspace_bytes(cache->head_dim, cache->n_kv_heads, t, n_q_heads);
+    const size_t n = attn_tree_workspace_bytes(cache->head_dim, cache->n_kv_heads, t, n_q_heads);
     most = n > most ? n : most;
   }
   return most;
@@ -482,7 +482,7 @@ static kq_status attn(const kq_kv_cache* cache, const int32_t* page_table, int64
       !stride16(q_stride, q_dtype == KQ_BF16 ? 2 : 4))
     return KQ_ERR_ALIGN;
   if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < attn_workspace_bytes(cache->head_dim, cache->n_kv_heads, T, n_q_heads))
+      workspace_bytes < (tree ? attn_tree_workspace_bytes : attn_workspace_bytes)(cache->head_dim, cache->n_kv_heads, T, n_q_heads))
     return KQ_ERR_WORKSPACE;
   AttnArgs a;
   a.c = *cache;

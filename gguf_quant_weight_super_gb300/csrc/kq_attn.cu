@@ -1,6 +1,7 @@
 // kq_attn.cu -- host side of kq_attn_decode: the workspace's layout and the
 // choice of the kernel (kq_attn_kernel.cuh).
 #include "kq_attn_kernel.cuh"
+#include "kq_join.cuh"
 
 namespace kq {
 
@@ -36,7 +37,7 @@ bool wide(int head_dim, int rows, int64_t heads, int64_t room) {
 
 struct Layout {
   int rows, RT;
-  size_t count_off, ml_off, part_off, bytes;
+  size_t count_off, ml_off, part_off, bytes;  // trees: and behind them, what the second launch has to join
 };
 Layout layout(int head_dim, int Hkv, int64_t T, int Hq, bool to_wide) {
   Layout L;
@@ -55,6 +56,22 @@ Layout layout(int head_dim, int Hkv, int64_t T, int Hq, bool to_wide) {
 }
 
 }  // namespace
+
+namespace attn {
+
+cudaError_t launch_tree_join(const Params& p, int rows, int D, bool f32, int ranges, cudaStream_t st) {
+  const JoinParams j{p.a, static_cast<const Split*>(p.split), p.part_ml, p.part, p.RT, rows, p.a.c.v_scale};
+  if (D == 64) return f32 ? launch_join<64, float>(j, ranges, st) : launch_join<64, __nv_bfloat16>(j, ranges, st);
+  if (D == 128) return f32 ? launch_join<128, float>(j, ranges, st) : launch_join<128, __nv_bfloat16>(j, ranges, st);
+  return f32 ? launch_join<256, float>(j, ranges, st) : launch_join<256, __nv_bfloat16>(j, ranges, st);
+}
+
+}  // namespace attn
+
+size_t attn_tree_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq) {
+  static_assert(sizeof(Split) == 16);
+  return attn_workspace_bytes(head_dim, Hkv, T, Hq) + 3 * static_cast<size_t>(num_sms()) * sizeof(Split);
+}
 
 size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq) {
   const size_t n = layout(head_dim, Hkv, T, Hq, false).bytes;
@@ -76,6 +93,8 @@ cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st, AttnShap
   p.count = reinterpret_cast<int*>(ws + L.count_off);
   p.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
   p.part = reinterpret_cast<float*>(ws + L.part_off);
+  p.split = ws + L.bytes;
+  if (a.tree && 3 * num_sms() > JOIN_MOST) return cudaErrorNotSupported;
   if (to_wide) return launch_attn_wide(p, st, ask);
   if (a.tree && a.c.dtype == KQ_BF16) return q_bf16 ? launch_attn_tree_bf16_bf16(p, L.rows, st) : launch_attn_tree_bf16_f32(p, L.rows, st);
   if (a.tree) return q_bf16 ? launch_attn_tree_f8_bf16(p, L.rows, st) : launch_attn_tree_f8_f32(p, L.rows, st);

@@ -63,6 +63,10 @@
 namespace kq {
 namespace attn {
 
+struct Params;
+// The second launch of a tree's call (kq_attn.cu): rows of an item's part, heads of D values, fp32 or bf16 out.
+cudaError_t launch_tree_join(const Params& p, int rows, int D, bool f32, int ranges, cudaStream_t st);
+
 constexpr int NW = 4;            // warps per CTA
 constexpr int NTH = NW * 32;
 constexpr int WT = 16;           // positions per warp sub-tile
@@ -113,6 +117,7 @@ struct Params {
   float* part;     // [2 * grid][ROWS][D] sums, then [2 * grid][ROWS][2] maximum and weight sum
   float* part_ml;
   int* count;      // [grid] arrivals at the split item whose first tile a range holds
+  void* split;     // trees: [grid] what is left of a range's last item to a second launch (kq_join.cuh)
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -841,8 +846,12 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
   build_prefix(a, START, prefix, scratch.scan);
   const Line line(a, p.RT, prefix);
   const int range = blockIdx.x;
-  if (range >= line.nc) return;
+  if (range >= line.nc) {
+    if (TREE && threadIdx.x == 0) static_cast<int4*>(p.split)[range] = make_int4(0, 0, 0, 0);
+    return;
+  }
   const int lo = line.bound(range), hi = line.bound(range + 1);
+  int4 split = make_int4(0, 0, 0, 0);
   for (int u = lo; u < hi;) {
     const Item it(a, line, p.RT, START, u);
     const int end = min(it.i1, hi);
@@ -944,7 +953,9 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
         if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * K::ROWS + r) * 2) = make_float2(mm, ll);
       }
     }
-    if (!whole) {  // in the ring's place, too
+    if constexpr (TREE) {
+      if (!whole && u == it.i0) split = make_int4(it.b, it.hr, line.range_of(it.i1 - 1) - range + 1, slot);
+    } else if (!whole) {  // in the ring's place, too
       constexpr int ROOM = K::RING - JOIN_SUMS * 4;
       join_parts<D, K::ROWS>(p, line, it, R, threadIdx.x, reinterpret_cast<float*>(ring), ROOM, reinterpret_cast<float*>(ring + ROOM),
                              s_i, &scratch.last, [] { __syncthreads(); }, write);
@@ -952,6 +963,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
     __syncthreads();
     u = end;
   }
+  if (TREE && threadIdx.x == 0) static_cast<int4*>(p.split)[range] = split;
 }
 
 template <class Q, class C, int D, int NT, bool TREE>
@@ -983,6 +995,10 @@ cudaError_t launch_one(const Params& p, cudaStream_t st, AttnShape* ask) {
   // 1000 positions: 9.4 us in place of 9.6)
   const int64_t units = (START + (static_cast<int64_t>(p.a.room) + TK - 1) / TK) * p.a.B * p.a.c.n_kv_heads * p.RT;
   const int grid = static_cast<int>(min_i64(num_sms() * ctas, units));
+  if constexpr (TREE) {
+    const cudaError_t e = launch_pdl(attn_kernel<Q, C, D, NT, TREE>, dim3(grid), dim3(NTH), smem, st, p);
+    return e != cudaSuccess ? e : launch_tree_join(p, K::ROWS, D, sizeof(Q) == 4, grid, st);
+  }
   return launch_pdl(attn_kernel<Q, C, D, NT, TREE>, dim3(grid), dim3(NTH), smem, st, p);
 }
 

@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
   const int range = blockIdx.x;
   const int lo = line.bound(min(range, line.nc)), hi = range < line.nc ? line.bound(range + 1) : lo;
   int tile0 = 0, segment = 0;
+  int4 split = make_int4(0, 0, 0, 0);
   bool ok = true;
   for (int u = lo; u < hi;) {
     const Item it(a, line, p.RT, WSTART, u);
@@ -483,6 +484,7 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
     ok = w.ok;
 
     const bool whole = u == it.i0 && end == it.i1;
+    if (TREE && !whole && u == it.i0) split = make_int4(it.b, it.hr, line.range_of(it.i1 - 1) - range + 1, 2 * range + (lo >= it.i0 ? 1 : 0));
     if (warp < 8) {
       const int slot = 2 * range + (lo >= it.i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
       const float weight = bars.top[0][0][r] + bars.top[0][1][r];
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
           *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * kWideRows + r) * 2) = make_float2(w.m, weight);
       }
       tc_fence_before();
-      if (!whole) {
+      if (!TREE && !whole) {
         softmax_sync();  // both halves' parts are stored
         if (half == 0)
           join_parts<D, kWideRows>(p, line, it, R, threadIdx.x, reinterpret_cast<float*>(ring), W::S * W::STAGE, s_sum, bars.s_i, &bars.last,
@@ -525,6 +527,7 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
     }
     u = end;
   }
+  if (TREE && threadIdx.x == 0) static_cast<int4*>(p.split)[range] = split;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -546,7 +549,8 @@ cudaError_t launch_d(const Params& p, cudaStream_t st, AttnShape* ask) {
     ask->planned = 1;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ask->resident, wide_kernel<D, TREE>, WTH, smem);
   }
-  return launch_pdl(wide_kernel<D, TREE>, dim3(num_sms()), dim3(WTH), smem, st, p);
+  const cudaError_t e = launch_pdl(wide_kernel<D, TREE>, dim3(num_sms()), dim3(WTH), smem, st, p);
+  return !TREE || e != cudaSuccess ? e : launch_tree_join(p, kWideRows, D, false, num_sms(), st);
 }
 
 }  // namespace

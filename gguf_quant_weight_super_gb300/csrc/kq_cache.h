@@ -74,6 +74,7 @@ struct AttnArgs {
 // Positions are counted in 32 bits, tiles and copies ahead of the last one included.
 constexpr int64_t kMaxPositions = INT32_MAX - 4095;
 size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq);
+size_t attn_tree_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq);
 // With `ask`: no launch, but the CTAs per SM that the kernel is laid out for and that the device holds at once.
 struct AttnShape {
   int planned, resident;

@@ -53,6 +53,7 @@
 // each value that is not finite becomes 0 before the second product, and a row that
 // sees such a vector (its score is not finite) becomes NaN.
 #include "kq_attn_kernel.cuh"
+#include "kq_join.cuh"
 #include "kq_vec.cuh"
 
 namespace kq {
@@ -87,11 +88,6 @@ struct LCfg {
   static constexpr int MB = C / 128, CO = 0, CQ = C == 256 ? 256 : NR == 64 ? 256 : 128, CS = 448, COLS = 512;
   static_assert(MB * NR <= CQ && CQ + 32 * QT <= CS && CS + LT <= COLS);
   static constexpr float LIFT = F8 ? 7.0f : 0.0f;     // log2: fp16 weights, below 2^8, fill fp16's range
-};
-
-// A range's item that goes on in the next ranges.
-struct Split {
-  int b, rt, parts, slot;  // parts 0: none
 };
 
 struct LParams {
@@ -350,7 +346,6 @@ struct Latent {
         did = true;
       }
       if (v < s && __all_sync(0xFFFFFFFFu, phase_done(&bars.p_full[gv & 1], gv >> 1) && phase_done(&bars.scaled[gv & 1], gv >> 1))) {
-        fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t c = line_desc(uniform(rs + vst * L::STAGE), L::LINES);
         const uint64_t w = w0 + uniform((gv & 1) * L::P / 16);
@@ -366,7 +361,6 @@ struct Latent {
         if (++vst == p.stages) vst = 0;
         did = true;
       }
-      if (!did) __nanosleep(20);  // the slots are for the others
       idle = did ? 0 : idle + 1;
       if (idle > (1u << 25)) {
         ok = false;
@@ -804,72 +798,6 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
   if (warp == PRODUCTS) tmem_dealloc(tb, L::COLS);
 }
 
-// Joins the parts of the items that span ranges: o = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k, in the ranges' order.
-// A block: a range's item, eight rows of it (a warp each) or, with MANY parts expected, one row, its parts in eight shares.
-constexpr int JTH = 256;
-template <int C, bool MANY>
-__global__ void __launch_bounds__(JTH) latent_join_kernel(const __grid_constant__ LParams p) {
-  constexpr int V = C / 128, JW = JTH / 32, MOST = 160;  // vectors of a row per lane; ranges
-  __shared__ float factor[MANY ? 1 : JW][MOST];
-  __shared__ float4 sums[MANY ? JW : 1][C / 4];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 s4 = __ldcg(reinterpret_cast<const int4*>(p.split) + blockIdx.x);
-  const Split sp = {s4.x, s4.y, s4.z, s4.w};
-  const int r = MANY ? blockIdx.y : blockIdx.y * JW + warp;
-  const int64_t row0 = static_cast<int64_t>(sp.rt) * p.rows;
-  if (sp.parts == 0 || row0 + (MANY ? r : r - warp) >= p.a.T * p.a.G) return;
-  const bool on = row0 + r < p.a.T * p.a.G && r < p.rows;
-  auto slot_of = [&](int k) { return k == 0 ? sp.slot : 2 * (static_cast<int>(blockIdx.x) + k) + 1; };
-  float* e = factor[MANY ? 0 : warp];
-  float mm = -INFINITY, ll = 0.0f;
-  if (on) {
-    for (int k = lane; k < sp.parts; k += 32) mm = fmaxf(mm, __ldcg(p.part_ml + (static_cast<int64_t>(slot_of(k)) * p.rows + r) * 2));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
-    const float ms = mm == -INFINITY ? 0.0f : mm;
-    for (int k = lane; k < sp.parts; k += 32) {
-      const float2 x = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (static_cast<int64_t>(slot_of(k)) * p.rows + r) * 2));
-      const float f = ex2(x.x - ms);
-      if (!MANY || warp == 0) e[k] = f;
-      ll += f * x.y;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o);
-  }
-  if (MANY) __syncthreads();
-  else __syncwarp();
-  float4 acc[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = make_float4(0, 0, 0, 0);
-  if (on) {
-#pragma unroll 4
-    for (int k = MANY ? warp : 0; k < sp.parts; k += MANY ? JW : 1) {
-      const float4* part = reinterpret_cast<const float4*>(p.part + (static_cast<int64_t>(slot_of(k)) * p.rows + r) * C) + lane;
-#pragma unroll
-      for (int i = 0; i < V; ++i) add4(acc[i], e[k], __ldcg(part + 32 * i));
-    }
-  }
-  const float inv = ll == 0.0f ? 0.0f : p.c_scale / ll;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + (static_cast<int64_t>(sp.b) * p.a.T * p.a.G + row0 + r) * C;
-  if (!MANY) {
-    if (on)
-#pragma unroll
-      for (int i = 0; i < V; ++i) put4(out + 4 * (lane + 32 * i), acc[i], inv);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) sums[warp][lane + 32 * i] = acc[i];
-    __syncthreads();
-    if (threadIdx.x < C / 4) {
-      float4 x = sums[0][threadIdx.x];
-#pragma unroll
-      for (int k = 1; k < JW; ++k) add4(x, 1.0f, sums[k][threadIdx.x]);
-      put4(out + 4 * threadIdx.x, x, inv);
-    }
-  }
-}
-
 int ranges() { return num_sms() < 160 ? num_sms() : 160; }
 // Rows of an item: 16, 32 or 64 columns of sums.
 int rows_of(int64_t all) { return all <= 16 ? 16 : all <= 32 ? 32 : MOST_ROWS; }
@@ -904,10 +832,7 @@ cudaError_t launch_rows(LParams p, cudaStream_t st) {
   }
   const cudaError_t e = launch_pdl(latent_kernel<C, F8, NR>, dim3(p.ranges), dim3(LTH), smem, st, p);
   if (e != cudaSuccess) return e;
-  // few items: many parts of each
-  const bool many = static_cast<int64_t>(p.a.B) * p.RT * 8 <= p.ranges;
-  if (many) return launch_pdl(latent_join_kernel<C, true>, dim3(p.ranges, NR), dim3(JTH), 0, st, p);
-  return launch_pdl(latent_join_kernel<C, false>, dim3(p.ranges, (NR + 7) / 8), dim3(JTH), 0, st, p);
+  return launch_join<C, __nv_bfloat16>(JoinParams{p.a, p.split, p.part_ml, p.part, p.RT, p.rows, p.c_scale}, p.ranges, st);
 }
 template <int C, bool F8>
 cudaError_t launch_type(const LParams& p, cudaStream_t st) {

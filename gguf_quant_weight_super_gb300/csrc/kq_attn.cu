@@ -35,6 +35,19 @@ bool wide(int head_dim, int rows, int64_t heads, int64_t room) {
   return (room > 16384 ? 32 : 16) * tiles >= 3 * (rows < kWideRows ? rows : kWideRows);
 }
 
+// Trees' parts are joined by a launch of their own, so splitting a head costs less.  Up to 32 rows both kernels take the same
+// time, and from 64 heads on this one less.  Above, the other one from eight heads' tiles of 128 rows on (heads of 64: 16; long
+// tables: from a quarter of that).  us, the other's time / this one's, up to 1500 and up to 6007 positions, heads of 128:
+//   heads of 128:  1 head     4         8         16        32        64
+//     64 rows     15/14 24/18  16/15 20/22  17/19 20/27  19/22 28/39  21/27 38/59  29/41 59/94
+//    128 rows     17/14 25/21  18/19 22/27  22/22 25/37  25/27 36/56  25/38 46/93  37/62 72/162
+//    244 rows     18/16 28/22  22/22 25/38  25/27 34/55  25/39 44/91  35/60 72/161 53/106 125/302
+bool wide_tree(int head_dim, int rows, int64_t heads, int64_t room) {
+  if (!could_be_wide(head_dim, rows) || rows <= 32) return false;
+  const int64_t tiles = heads * ((rows + kWideRows - 1) / kWideRows);
+  return (room > 16384 ? 4 : 1) * tiles >= (head_dim == 128 ? 8 : 16);
+}
+
 struct Layout {
   int rows, RT;
   size_t count_off, ml_off, part_off, bytes;  // trees: and behind them, what the second launch has to join
@@ -60,7 +73,7 @@ Layout layout(int head_dim, int Hkv, int64_t T, int Hq, bool to_wide) {
 namespace attn {
 
 cudaError_t launch_tree_join(const Params& p, int rows, int D, bool f32, int ranges, cudaStream_t st) {
-  const JoinParams j{p.a, static_cast<const Split*>(p.split), p.part_ml, p.part, p.RT, rows, p.a.c.v_scale};
+  const JoinParams j{p.a, p.split, p.part_ml, p.part, p.RT, rows, p.by_item, p.a.c.v_scale};
   if (D == 64) return f32 ? launch_join<64, float>(j, ranges, st) : launch_join<64, __nv_bfloat16>(j, ranges, st);
   if (D == 128) return f32 ? launch_join<128, float>(j, ranges, st) : launch_join<128, __nv_bfloat16>(j, ranges, st);
   return f32 ? launch_join<256, float>(j, ranges, st) : launch_join<256, __nv_bfloat16>(j, ranges, st);
@@ -69,7 +82,6 @@ cudaError_t launch_tree_join(const Params& p, int rows, int D, bool f32, int ran
 }  // namespace attn
 
 size_t attn_tree_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq) {
-  static_assert(sizeof(Split) == 16);
   return attn_workspace_bytes(head_dim, Hkv, T, Hq) + 3 * static_cast<size_t>(num_sms()) * sizeof(Split);
 }
 
@@ -81,7 +93,7 @@ size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq) {
 }
 
 cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st, AttnShape* ask) {
-  const bool to_wide = q_bf16 && a.c.dtype == KQ_BF16 && wide(a.c.head_dim, a.T * a.G, static_cast<int64_t>(a.B) * a.c.n_kv_heads, a.room);
+  const bool to_wide = q_bf16 && a.c.dtype == KQ_BF16 && (a.tree ? wide_tree : wide)(a.c.head_dim, a.T * a.G, static_cast<int64_t>(a.B) * a.c.n_kv_heads, a.room);
   const Layout L = layout(a.c.head_dim, a.c.n_kv_heads, a.T, a.Hq, to_wide);
   // the line of tiles is counted in 31 bits
   const int64_t tiles = ((a.max_pages << a.page_shift) + TK - 1) / TK + 8;  // 8: more than an item's start counts
@@ -93,7 +105,8 @@ cudaError_t launch_attn(const AttnArgs& a, int q_bf16, cudaStream_t st, AttnShap
   p.count = reinterpret_cast<int*>(ws + L.count_off);
   p.part_ml = reinterpret_cast<float*>(ws + L.ml_off);
   p.part = reinterpret_cast<float*>(ws + L.part_off);
-  p.split = ws + L.bytes;
+  p.split = reinterpret_cast<Split*>(ws + L.bytes);
+  p.by_item = static_cast<int64_t>(a.B) * a.c.n_kv_heads * L.RT <= num_sms();  // at most as many as any grid of tiles has ranges
   if (a.tree && 3 * num_sms() > JOIN_MOST) return cudaErrorNotSupported;
   if (to_wide) return launch_attn_wide(p, st, ask);
   if (a.tree && a.c.dtype == KQ_BF16) return q_bf16 ? launch_attn_tree_bf16_bf16(p, L.rows, st) : launch_attn_tree_bf16_f32(p, L.rows, st);

@@ -63,6 +63,12 @@
 namespace kq {
 namespace attn {
 
+// What a first launch leaves of an item to a second one (kq_join.cuh): (sequence * heads + head) * RT + row tile, the first
+// range, the parts (0: none), the first one's place.  The other ranges' lie at 2 * range + 1.
+struct Split {
+  int item, range, parts, slot;
+};
+
 struct Params;
 // The second launch of a tree's call (kq_attn.cu): rows of an item's part, heads of D values, fp32 or bf16 out.
 cudaError_t launch_tree_join(const Params& p, int rows, int D, bool f32, int ranges, cudaStream_t st);
@@ -117,7 +123,8 @@ struct Params {
   float* part;     // [2 * grid][ROWS][D] sums, then [2 * grid][ROWS][2] maximum and weight sum
   float* part_ml;
   int* count;      // [grid] arrivals at the split item whose first tile a range holds
-  void* split;     // trees: [grid] what is left of a range's last item to a second launch (kq_join.cuh)
+  Split* split;    // trees: [items] or, if those are more than ranges, [grid]
+  int by_item;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -732,6 +739,13 @@ struct Item {
   }
 };
 
+// By one thread of the range that has the item's first tile.
+__device__ __forceinline__ void note_split(Split* split, int by_item, const Line& line, const Item& it, int range, bool whole, int slot) {
+  const int item = it.b * line.HR + it.hr;
+  if (!whole) split[by_item ? item : range] = {item, range, line.range_of(it.i1 - 1) - range + 1, slot};
+  else if (by_item) split[item].parts = 0;
+}
+
 // The last CTA to arrive with its part of an item joins the ranges' sums: NTH threads (tid) call with their part stored,
 // sync being their barrier.  scratch: `room` bytes of shared memory; s_sum, s_i, s_last: shared.  write(r, d, sum, factor).
 template <int D, int ROWS, class Sync, class Write>
@@ -847,11 +861,11 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
   const Line line(a, p.RT, prefix);
   const int range = blockIdx.x;
   if (range >= line.nc) {
-    if (TREE && threadIdx.x == 0) static_cast<int4*>(p.split)[range] = make_int4(0, 0, 0, 0);
+    if (TREE && threadIdx.x == 0 && !p.by_item) p.split[range].parts = 0;
     return;
   }
   const int lo = line.bound(range), hi = line.bound(range + 1);
-  int4 split = make_int4(0, 0, 0, 0);
+  if (TREE && threadIdx.x == 0 && !p.by_item) p.split[range].parts = 0;
   for (int u = lo; u < hi;) {
     const Item it(a, line, p.RT, START, u);
     const int end = min(it.i1, hi);
@@ -866,6 +880,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
       put4(static_cast<Q*>(a.out) + ((static_cast<int64_t>(it.b) * a.T + t) * a.Hq + h) * D + d, v, inv);
     };
     if (it.len == 0) {
+      if (TREE && threadIdx.x == 0) note_split(p.split, p.by_item, line, it, range, true, 0);
       for (int x = threadIdx.x; x < R * (D / 4); x += NTH) write(x / (D / 4), 4 * (x % (D / 4)), make_float4(0, 0, 0, 0), 0.0f);
       u = end;
       continue;
@@ -954,7 +969,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
       }
     }
     if constexpr (TREE) {
-      if (!whole && u == it.i0) split = make_int4(it.b, it.hr, line.range_of(it.i1 - 1) - range + 1, slot);
+      if (u == it.i0 && threadIdx.x == 0) note_split(p.split, p.by_item, line, it, range, whole, slot);
     } else if (!whole) {  // in the ring's place, too
       constexpr int ROOM = K::RING - JOIN_SUMS * 4;
       join_parts<D, K::ROWS>(p, line, it, R, threadIdx.x, reinterpret_cast<float*>(ring), ROOM, reinterpret_cast<float*>(ring + ROOM),
@@ -963,7 +978,6 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
     __syncthreads();
     u = end;
   }
-  if (TREE && threadIdx.x == 0) static_cast<int4*>(p.split)[range] = split;
 }
 
 template <class Q, class C, int D, int NT, bool TREE>

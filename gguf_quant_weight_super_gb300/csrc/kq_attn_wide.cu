@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
   const int range = blockIdx.x;
   const int lo = line.bound(min(range, line.nc)), hi = range < line.nc ? line.bound(range + 1) : lo;
   int tile0 = 0, segment = 0;
-  int4 split = make_int4(0, 0, 0, 0);
+  if (TREE && threadIdx.x == 0 && !p.by_item) p.split[range].parts = 0;
   bool ok = true;
   for (int u = lo; u < hi;) {
     const Item it(a, line, p.RT, WSTART, u);
@@ -411,6 +411,7 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
       return static_cast<__nv_bfloat16*>(a.out) + ((static_cast<int64_t>(it.b) * a.T + tt) * a.Hq + hh) * D;
     };
     if (it.len == 0) {
+      if (TREE && threadIdx.x == 0) note_split(p.split, p.by_item, line, it, range, true, 0);
       for (int x = threadIdx.x; x < R * (D / 4); x += WTH) put4(out_row(x / (D / 4)) + 4 * (x % (D / 4)), make_float4(0, 0, 0, 0), 0.0f);
       u = end;
       continue;
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
     ok = w.ok;
 
     const bool whole = u == it.i0 && end == it.i1;
-    if (TREE && !whole && u == it.i0) split = make_int4(it.b, it.hr, line.range_of(it.i1 - 1) - range + 1, 2 * range + (lo >= it.i0 ? 1 : 0));
+    if (TREE && u == it.i0 && threadIdx.x == 0) note_split(p.split, p.by_item, line, it, range, whole, 2 * range + (lo >= it.i0 ? 1 : 0));
     if (warp < 8) {
       const int slot = 2 * range + (lo >= it.i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
       const float weight = bars.top[0][0][r] + bars.top[0][1][r];
@@ -527,7 +528,6 @@ __global__ void __launch_bounds__(WTH, 1) wide_kernel(const __grid_constant__ Pa
     }
     u = end;
   }
-  if (TREE && threadIdx.x == 0) static_cast<int4*>(p.split)[range] = split;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

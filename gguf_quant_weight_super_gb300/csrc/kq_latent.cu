@@ -79,6 +79,7 @@ struct LCfg {
   static constexpr int P = NR * 128;                  // a tile's weights
   static constexpr int U = F8 ? 8 : 16;               // positions at a time of a loader
   static constexpr int LOADERS = F8 ? 6 : NLOAD;
+  // e4m3: the places of a loader's pieces, as they are in the cache; all but one are on their way
   static constexpr int RAWROW = C + 64, RAWS = F8 ? 2 : 0, RAW = RAWS * U * RAWROW;
   static constexpr int smem(int stages, int B) { return QS + 2 * P + stages * STAGE + LOADERS * RAW + 4 * (B + 1); }
   static constexpr int ROOM = 227 * 1024 - 4096;      // less the static memory
@@ -96,6 +97,7 @@ struct LParams {
   int64_t page_bytes, slot_bytes;
   float c_scale;
   int rope, RT, rows, ranges, stages;  // rows: of a part
+  int by_item;                         // split [items] instead of [ranges]
   Split* split;
   float *part_ml, *part;
 };
@@ -106,10 +108,9 @@ struct LBars {
   int bad;
   int scan[NW];
   int raise[2];                  // a warpgroup's last tile, counted from 1, that raised a maximum
-  float back[MOST_ROWS];         // e4m3: the rows' powers of two
   float m[MOST_ROWS];            // the rows' maxima that their sums are relative to, in log2 units
   float factor[2][MOST_ROWS];    // a warpgroup's tile: what the sums are scaled by; at the end [0]: the rows' last factor
-  float top[4][MOST_ROWS];       // a warpgroup's half of a tile: the rows' largest score; at the end, its weight sums
+  float top[4][MOST_ROWS];       // a warpgroup's half of a tile: the rows' largest score; at the end, its weight sums (e4m3, before: q's largest values)
   int seen[MOST_ROWS];           // 0: padding
 };
 
@@ -184,6 +185,11 @@ __device__ __forceinline__ bool finite16(uint32_t two, bool f16) {  // both halv
   return (two & e) != e && (two >> 16 & e) != e;
 }
 
+__device__ __forceinline__ float largest(uint32_t two) {  // of two bf16 values, by size
+  const float2 y = unpack2<false>(two);
+  return fmaxf(fabsf(y.x), fabsf(y.y));
+}
+
 template <int C, bool F8, int NR>
 struct Latent {
   using L = LCfg<C, F8, NR>;
@@ -250,13 +256,14 @@ struct Latent {
         }
         copy_commit();
       };
-      fetch(lw, 0);
+#pragma unroll
+      for (int i = 0; i < L::RAWS - 1; ++i) fetch(lw + i * STEP, i);
       int slot = 0;
       for (int x = lw; x < units; x += STEP) {
         const int gi = tile0 + x / PT, st = gi % p.stages;
-        copy_wait<0>();
+        copy_wait<L::RAWS - 2>();
         __syncwarp();
-        fetch(x + STEP, slot ^ 1);
+        fetch(x + (L::RAWS - 1) * STEP, slot == 0 ? L::RAWS - 1 : slot - 1);
         if (gi >= p.stages) wait(&bars.empty[st], gi / p.stages - 1);
         uint8_t* lines = ring + st * L::STAGE + x % PT * (U * 128);
         const uint8_t* from = raw + slot * (U * L::RAWROW);
@@ -272,7 +279,7 @@ struct Latent {
         fence_proxy_async_smem();
         mbar_arrive(&bars.full[st]);
         __syncwarp();  // the piece's place is free
-        slot ^= 1;
+        slot = slot + 1 == L::RAWS ? 0 : slot + 1;
       }
     } else {
       for (int x = lw; x < units; x += STEP) {
@@ -326,9 +333,28 @@ struct Latent {
     wait(&bars.q_full, segment);
     uint32_t idle = 0;
     int sst = tile0 % p.stages, sph = tile0 / p.stages, vst = sst;  // the stages of both products' tiles
-    for (int s = 0, v = 0; v < n && ok;) {
+    int s = 0, v = 0;
+    auto sums = [&] {  // of the oldest tile whose scores are under way
+      const int gv = tile0 + v;
+      if (v >= s || !__all_sync(0xFFFFFFFFu, phase_done(&bars.p_full[gv & 1], gv >> 1) && phase_done(&bars.scaled[gv & 1], gv >> 1))) return false;
+      tc_fence_after();
+      const uint64_t c = line_desc(uniform(rs + vst * L::STAGE), L::LINES);
+      const uint64_t w = w0 + uniform((gv & 1) * L::P / 16);
+      const uint32_t more = v > 0;
+#pragma unroll
+      for (int k = 0; k < LT / 16; ++k)
+#pragma unroll
+        for (int mb = 0; mb < L::MB; ++mb)
+          mma_ss_on(t + L::CO + mb * NR, c + (2 * mb * L::LINES + k * 2048) / 16, w + 2 * k, idesc(F8, NR, true), k > 0 ? 1 : more, on);
+      commit_on(smem_u32(&bars.pv_done[gv & 1]), on);
+      commit_on(smem_u32(&bars.empty[vst]), on);
+      ++v;
+      if (++vst == p.stages) vst = 0;
+      return true;
+    };
+    while (v < n && ok) {
       bool did = false;
-      const int gs = tile0 + s, gv = tile0 + v;
+      const int gs = tile0 + s;
       if (s < n && __all_sync(0xFFFFFFFFu, phase_done(&bars.full[sst], sph) && (gs == 0 || phase_done(&bars.s_free[(gs - 1) & 1], (gs - 1) >> 1)))) {
         fence_proxy_async_smem();  // the copies, which the barrier has put before this, seen by the tensor cores
         tc_fence_after();
@@ -345,22 +371,7 @@ struct Latent {
         if (++sst == p.stages) sst = 0, ++sph;
         did = true;
       }
-      if (v < s && __all_sync(0xFFFFFFFFu, phase_done(&bars.p_full[gv & 1], gv >> 1) && phase_done(&bars.scaled[gv & 1], gv >> 1))) {
-        tc_fence_after();
-        const uint64_t c = line_desc(uniform(rs + vst * L::STAGE), L::LINES);
-        const uint64_t w = w0 + uniform((gv & 1) * L::P / 16);
-        const uint32_t more = v > 0;
-#pragma unroll
-        for (int k = 0; k < LT / 16; ++k)
-#pragma unroll
-          for (int mb = 0; mb < L::MB; ++mb)
-            mma_ss_on(t + L::CO + mb * NR, c + (2 * mb * L::LINES + k * 2048) / 16, w + 2 * k, idesc(F8, NR, true), k > 0 ? 1 : more, on);
-        commit_on(smem_u32(&bars.pv_done[gv & 1]), on);
-        commit_on(smem_u32(&bars.empty[vst]), on);
-        ++v;
-        if (++vst == p.stages) vst = 0;
-        did = true;
-      }
+      did |= sums();
       idle = did ? 0 : idle + 1;
       if (idle > (1u << 25)) {
         ok = false;
@@ -620,7 +631,7 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
   const uint32_t tb = bars.tmem, lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
   const Line line(a, p.RT, prefix);
   const int range = blockIdx.x, lo = line.bound(min(range, line.nc)), hi = range < line.nc ? line.bound(range + 1) : lo;
-  Split split = {0, 0, 0, 0};
+  if (threadIdx.x == 0 && !p.by_item) p.split[range].parts = 0;
   int tile0 = 0, segment = 0;
   bool ok = true;
   for (int u = lo; u < hi;) {
@@ -634,6 +645,7 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
     const int r0 = it.rt * NR, R = min(NR, a.T * a.G - r0);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(it.b) * a.T * a.G + r0) * C;
     if (it.len == 0) {
+      if (threadIdx.x == 0) note_split(p.split, p.by_item, line, it, range, true, 0);
       for (int x = threadIdx.x; x < R * (C / 4); x += LTH) store4(out + 4 * x, make_float4(0, 0, 0, 0));
       u = end;
       continue;
@@ -663,40 +675,23 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
       }
     }
     if (threadIdx.x == 0) bars.bad = 0;
-    if constexpr (F8) {
-      if (warp < 16)  // the rows' largest values: a warp per row, four at a time
-        for (int r4 = warp * 4; r4 < R; r4 += 64) {
-          uint4 v[4][3];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int x = min(r0 + r4 + k, a.T * a.G - 1), tt = x / a.G;
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(it.b) * a.T + tt) * a.q_stride +
-                                                              static_cast<int64_t>(x - tt * a.G) * (C + p.rope));
-#pragma unroll
-            for (int i = 0; i < 3; ++i) v[k][i] = lane + 32 * i < (C + p.rope) / 8 ? __ldg(src + lane + 32 * i) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float mx = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-              for (uint32_t w : {v[k][i].x, v[k][i].y, v[k][i].z, v[k][i].w}) {
-                const float2 y = unpack2<false>(w);
-                mx = fmaxf(mx, fmaxf(fabsf(y.x), fabsf(y.y)));
-              }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-            // largest value into [2^13, 2^14); the factor and its inverse stay normal numbers
-            const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
-            if (lane == 0) bars.back[r4 + k] = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
-          }
-        }
-    }
     __syncthreads();  // the ring, the sums and tensor memory are free
     if constexpr (F8) {
-      if (softmax && r < R) {
-        f *= bars.back[r];
-        mul = __uint_as_float((254u << 23) - __float_as_uint(bars.back[r]));  // its inverse
+      if (softmax) {  // the row's largest value into [2^13, 2^14); the factor and its inverse stay normal numbers
+        float mx = 0.0f;
+        if (r < R)
+#pragma unroll 6
+          for (int c = part; c < (C + p.rope) / 8; c += 4) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(q) + c);
+            mx = fmaxf(mx, fmaxf(fmaxf(largest(x.x), largest(x.y)), fmaxf(largest(x.z), largest(x.w))));
+          }
+        bars.top[part][r] = mx;
+        softmax_sync();
+        mx = fmaxf(fmaxf(bars.top[0][r], bars.top[1][r]), fmaxf(bars.top[2][r], bars.top[3][r]));
+        const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
+        f *= __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+        mul = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+        softmax_sync();
       }
     }
     Latent<C, F8, NR> w{p, g, bars, smem, ps, ring, raw + max(loader, 0) * L::RAW, tb, tile0, ok, 0.0f, false};
@@ -760,7 +755,7 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
 
     const bool whole = u == it.i0 && end == it.i1;
     const int slot = 2 * range + (lo >= it.i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
-    if (!whole && u == it.i0) split = {it.b, it.rt, line.range_of(it.i1 - 1) - range + 1, slot};
+    if (u == it.i0 && threadIdx.x == 0) note_split(p.split, p.by_item, line, it, range, whole, slot);
     if (warp < 16) {
       const int d = mb * 128 + r;
       float* to = p.part + static_cast<int64_t>(slot) * p.rows * C + d;
@@ -791,7 +786,6 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
     tc_fence_after();
     u = end;
   }
-  if (threadIdx.x == 0) p.split[range] = split;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -832,7 +826,7 @@ cudaError_t launch_rows(LParams p, cudaStream_t st) {
   }
   const cudaError_t e = launch_pdl(latent_kernel<C, F8, NR>, dim3(p.ranges), dim3(LTH), smem, st, p);
   if (e != cudaSuccess) return e;
-  return launch_join<C, __nv_bfloat16>(JoinParams{p.a, p.split, p.part_ml, p.part, p.RT, p.rows, p.c_scale}, p.ranges, st);
+  return launch_join<C, __nv_bfloat16>(JoinParams{p.a, p.split, p.part_ml, p.part, p.RT, p.rows, p.by_item, p.c_scale}, p.ranges, st);
 }
 template <int C, bool F8>
 cudaError_t launch_type(const LParams& p, cudaStream_t st) {
@@ -876,6 +870,7 @@ cudaError_t launch_latent(const LatentArgs& x, cudaStream_t st) {
   p.rows = l.rows;
   p.RT = (x.T * x.H + p.rows - 1) / p.rows;
   p.ranges = attn::ranges();
+  p.by_item = static_cast<int64_t>(x.B) * p.RT <= p.ranges;
   uint8_t* ws = static_cast<uint8_t*>(x.ws);
   p.split = reinterpret_cast<attn::Split*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + l.ml_off);

@@ -10,7 +10,7 @@
 // sums, 512 fp32 values each, would be all of an SM's tensor memory and their
 // queries 144 KB of its shared memory; so a CTA, one per SM, takes up to 64 rows.
 // Its products:
-//   S   = Q K^T    rows are the M (128 lanes, the upper ones idle), 48 positions the N;
+//   S   = Q K^T    rows are the M (128 lanes, the upper ones idle), 32 positions the N;
 //                  Q in tensor memory (64 rows: three of its nine lines of 64 dims in
 //                  shared memory), K lines in shared memory
 //   O^T += V^T P^T dims are the M, 128 at a time, the rows the N: 16, 32 or 64 columns
@@ -24,7 +24,7 @@
 // sequences of 4096 positions and 128 heads 171 us, and 99 us with 16 heads.)
 //
 // Warps:
-//  * loaders copy 16 positions at a time into a ring of stages of 48, 64 dims of
+//  * loaders copy 16 positions at a time into a ring of stages of 32, 64 dims of
 //    a position a line of 128 bytes in the matrix descriptors' 128-byte swizzle
 //    (e4m3: 8 positions, as they are, into places of their own, and from there as
 //    fp16, exactly, into the lines);
@@ -60,11 +60,11 @@ namespace kq {
 namespace attn {
 namespace {
 
-constexpr int LT = 48;                // positions per tile
+constexpr int LT = 32;                // positions per tile
 constexpr int HC = LT / 2;            // a softmax thread's positions of a tile
 constexpr int LSTART = 4;             // tiles' time that an item costs besides its tiles
 constexpr float kGrow = 8.0f;         // log2 units that a row's maximum may lag behind
-constexpr int MOST_ROWS = 64, MOST_STAGES = 6;
+constexpr int MOST_ROWS = 64, MOST_STAGES = 8;
 // Warps 0-15 by four: the first two of each four are softmax warps (their tensor memory lanes are rows 0-31 and 32-63), of
 // the others one issues products and seven load; warps 16-19 scale sums.
 constexpr int LTH = 20 * 32, PRODUCTS = 2, NLOAD = 7;
@@ -83,7 +83,7 @@ struct LCfg {
   static constexpr int RAWROW = C + 64, RAWS = F8 ? 2 : 0, RAW = RAWS * U * RAWROW;
   static constexpr int smem(int stages, int B) { return QS + 2 * P + stages * STAGE + LOADERS * RAW + 4 * (B + 1); }
   static constexpr int ROOM = 227 * 1024 - 4096;      // less the static memory
-  static constexpr int LEAST = F8 ? 2 : 3;            // stages
+  static constexpr int LEAST = F8 ? 3 : 4;            // stages
   static_assert(smem(LEAST, 4096) <= ROOM);
   // tensor memory columns: o, q, S
   static constexpr int MB = C / 128, CO = 0, CQ = C == 256 ? 256 : NR == 64 ? 256 : 128, CS = 448, COLS = 512;
@@ -110,7 +110,8 @@ struct LBars {
   int raise[2];                  // a warpgroup's last tile, counted from 1, that raised a maximum
   float m[MOST_ROWS];            // the rows' maxima that their sums are relative to, in log2 units
   float factor[2][MOST_ROWS];    // a warpgroup's tile: what the sums are scaled by; at the end [0]: the rows' last factor
-  float top[4][MOST_ROWS];       // a warpgroup's half of a tile: the rows' largest score; at the end, its weight sums (e4m3, before: q's largest values)
+  float top[4][MOST_ROWS];       // a warpgroup's half of a tile: the rows' largest score; at the end, weight sums (e4m3, before: q's largest values)
+  float weight[MOST_ROWS];
   int seen[MOST_ROWS];           // 0: padding
 };
 
@@ -442,14 +443,12 @@ struct Latent {
       tc_fence_after();
       if (active) {
         {
-          uint32_t v[16], u[8];
+          uint32_t v[HC];
           tmem_ld16(tb + lanes + L::CS + HC * half, v);
-          tmem_ld8(tb + lanes + L::CS + HC * half + 16, u);
           tmem_wait_ld();
           tie(v);
-          tie(u);
 #pragma unroll
-          for (int e = 0; e < HC; ++e) s[e] = __uint_as_float(e < 16 ? v[e] : u[e - 16]);
+          for (int e = 0; e < HC; ++e) s[e] = __uint_as_float(v[e]);
         }
         tc_fence_before();
         __syncwarp();
@@ -528,8 +527,8 @@ struct Latent {
         if (r < NR) {
           uint8_t* line = ps + wg * L::P + r * 128;
 #pragma unroll
-          for (int c = 0; c < 3; ++c)
-            *reinterpret_cast<uint4*>(line + ((3 * half + c) ^ (r & 7)) * 16) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4*>(line + ((2 * half + c) ^ (r & 7)) * 16) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         fence_proxy_async_smem();
@@ -548,8 +547,16 @@ struct Latent {
       const float now = bars.m[r];
       if (now != m) l *= m == -INFINITY ? 0.0f : ex2(m - now);
     }
+    // the rows' weight sums, and what their sums are multiplied by (padding: nothing, whatever the keys were)
+    bars.top[2 * wg + half][r] = pos < 0 ? 0.0f : poison ? NAN : l;
+    softmax_sync();
+    if (wg == 0 && half == 0) {
+      const float weight = (bars.top[0][r] + bars.top[1][r]) + (bars.top[2][r] + bars.top[3][r]);
+      bars.weight[r] = weight;
+      bars.factor[0][r] = weight == 0.0f ? 0.0f : p.c_scale / weight;
+    }
   }
-  // Zeros in the place of a tile's values that are not finite, 12 positions per warp of the tile's four: its scores are done,
+  // Zeros in the place of a tile's values that are not finite, 8 positions per warp of the tile's four: its scores are done,
   // its sums not begun.
   static __device__ __noinline__ void clean(uint8_t* stage, int quarter) {
     const int lane = threadIdx.x & 31;
@@ -618,6 +625,7 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
       mbar_init(&bars.scaled[i], 4);
       bars.raise[i] = 0;
     }
+    bars.bad = 0;
     mbar_init(&bars.q_full, 8);
     fence_mbar_init();
   }
@@ -674,8 +682,6 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
         bars.seen[r] = r < R && pos >= 0;
       }
     }
-    if (threadIdx.x == 0) bars.bad = 0;
-    __syncthreads();  // the ring, the sums and tensor memory are free
     if constexpr (F8) {
       if (softmax) {  // the row's largest value into [2^13, 2^14); the factor and its inverse stay normal numbers
         float mx = 0.0f;
@@ -691,7 +697,6 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
         const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
         f *= __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
         mul = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
-        softmax_sync();
       }
     }
     Latent<C, F8, NR> w{p, g, bars, smem, ps, ring, raw + max(loader, 0) * L::RAW, tb, tile0, ok, 0.0f, false};
@@ -699,13 +704,15 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
     // rows the half.
     constexpr int SPAN = NR * L::MB / 4;  // columns
     const int col0 = part * SPAN, mb = col0 / NR, c0 = col0 % NR;
-    bool careful = false;
-    for (;;) {
+    const bool whole = u == it.i0 && end == it.i1;
+    const int slot = 2 * range + (lo >= it.i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
+    if (u == it.i0 && threadIdx.x == 0) note_split(p.split, p.by_item, line, it, range, whole, slot);
+    for (bool careful = false;; careful = true) {
       if (softmax) {
+        softmax_sync();  // the rows' maxima are there
         w.load_q(r < R ? q : nullptr, r, lanes, part, active, mul);
         if (!careful) w.template softmax<false>(lanes, r, active, pos, bits, f);
         else w.template softmax<true>(lanes, r, active, pos, bits, f);
-        bars.top[part][r] = pos < 0 ? 0.0f : w.poison ? NAN : w.l;  // padding: whatever the keys were
       } else if (scaler) {
         w.rescale(lanes);
       } else if (warp == PRODUCTS) {
@@ -715,75 +722,46 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
       }
       ++segment;
       w.tile0 += g.t1 - g.t0;
-      __syncthreads();
+      __syncthreads();  // the sums are complete, and the rows' factors there
       tc_fence_after();
-      if (careful) break;
       if (warp < 16) {
+        const int d = mb * 128 + r;
+        float* to = p.part + static_cast<int64_t>(slot) * p.rows * C + d;
         bool bad = false;
 #pragma unroll 1
-        for (int c = 0; c < SPAN; c += 8) {
+        for (int c = 0; c < SPAN && c0 + c < R; c += 8) {
           uint32_t v[8];
           tmem_ld8(tb + lanes + L::CO + col0 + c, v);
           tmem_wait_ld();
           tie(v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) bad |= !finite(__uint_as_float(v[e])) && bars.seen[c0 + c + e];
+          for (int e = 0; e < 8; ++e) {
+            const int rr = c0 + c + e;
+            if (rr < R) {
+              const float x = bars.seen[rr] ? __uint_as_float(v[e]) : 0.0f;
+              bad |= !finite(x);
+              if (whole) out[rr * C + d] = __float2bfloat16_rn(x * bars.factor[0][rr]);
+              else to[rr * C] = x;
+            }
+          }
+          __syncwarp();
         }
-        if (bad) bars.bad = 1;
-      } else if (threadIdx.x - 512 < R) {  // and the rows' last factors
+        if (bad && !careful) bars.bad = 1;
+      } else if (!whole && threadIdx.x - 512 < R) {
         const int rr = threadIdx.x - 512;
-        const float weight = (bars.top[0][rr] + bars.top[1][rr]) + (bars.top[2][rr] + bars.top[3][rr]);
-        bars.factor[0][rr] = weight == 0.0f ? 0.0f : p.c_scale / weight;
+        *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * p.rows + rr) * 2) =
+            make_float2(bars.seen[rr] ? bars.m[rr] : -INFINITY, bars.weight[rr]);
       }
       tc_fence_before();
-      __syncthreads();
-      if (!bars.bad) break;
-      careful = true;
+      __syncthreads();  // what lies in shared and tensor memory is read
+      tc_fence_after();
+      if (careful || !bars.bad) break;
       if (softmax && part == 0) bars.m[r] = pos < 0 ? INFINITY : -INFINITY;
       __syncthreads();
+      if (threadIdx.x == 0) bars.bad = 0;
     }
     tile0 = w.tile0;
     ok = w.ok;
-    if (careful) {
-      if (threadIdx.x < R) {
-        const int rr = threadIdx.x;
-        const float weight = (bars.top[0][rr] + bars.top[1][rr]) + (bars.top[2][rr] + bars.top[3][rr]);
-        bars.factor[0][rr] = weight == 0.0f ? 0.0f : p.c_scale / weight;
-      }
-      __syncthreads();
-    }
-
-    const bool whole = u == it.i0 && end == it.i1;
-    const int slot = 2 * range + (lo >= it.i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
-    if (u == it.i0 && threadIdx.x == 0) note_split(p.split, p.by_item, line, it, range, whole, slot);
-    if (warp < 16) {
-      const int d = mb * 128 + r;
-      float* to = p.part + static_cast<int64_t>(slot) * p.rows * C + d;
-#pragma unroll 1
-      for (int c = 0; c < SPAN && c0 + c < R; c += 8) {
-        uint32_t v[8];
-        tmem_ld8(tb + lanes + L::CO + col0 + c, v);
-        tmem_wait_ld();
-        tie(v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int rr = c0 + c + e;
-          const float x = bars.seen[rr] ? __uint_as_float(v[e]) : 0.0f;
-          if (rr < R) {
-            if (whole) out[static_cast<int64_t>(rr) * C + d] = __float2bfloat16_rn(x * bars.factor[0][rr]);
-            else to[static_cast<int64_t>(rr) * C] = x;
-          }
-        }
-        __syncwarp();
-      }
-    } else if (!whole && threadIdx.x - 512 < R) {
-      const int rr = threadIdx.x - 512;
-      const float weight = (bars.top[0][rr] + bars.top[1][rr]) + (bars.top[2][rr] + bars.top[3][rr]);
-      *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * p.rows + rr) * 2) = make_float2(bars.seen[rr] ? bars.m[rr] : -INFINITY, weight);
-    }
-    tc_fence_before();
-    __syncthreads();  // the sums, weights and maxima are read before the next segment writes them
-    tc_fence_after();
     u = end;
   }
   tc_fence_before();

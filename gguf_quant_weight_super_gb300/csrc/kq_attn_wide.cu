@@ -45,7 +45,9 @@ constexpr int NLOAD = 7;        // loader warps
 constexpr int WTH = (8 + NLOAD + 1) * 32;  // softmax warps 0-7, loaders 8-14, products 15
 constexpr int HC = TK / 2;      // a softmax thread's positions of a tile
 constexpr int WSTART = 6;       // tiles' time that an item costs besides its tiles
-constexpr float kGrow = 8.0f;   // log2 units that a row's maximum may lag behind
+// log2 units that a row's maximum may lag behind.  (Trees' blocks have up to 128 rows, of which with 8 units one grows often.)
+template <bool TREE>
+constexpr float kGrow = TREE ? 24.0f : 8.0f;
 // tensor memory columns: q, S x 2, P x 2 (high parts, low parts), o
 constexpr int CQ = 0, CS = 64, CP = 192, CO = 320, COLS = 512;
 
@@ -294,7 +296,7 @@ struct Wide {
         bars.top[buf][half][r] = mx;
         rows_sync(r >> 5);
         mx = fmaxf(mx, bars.top[buf][half ^ 1][r]);
-        const bool grow = mx > (m == -INFINITY ? m : m + kGrow);
+        const bool grow = mx > (m == -INFINITY ? m : m + kGrow<TREE>);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float c = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mx);
           if (grow) m = mx;

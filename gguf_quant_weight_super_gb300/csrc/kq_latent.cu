@@ -28,11 +28,11 @@
 //    a position a line of 128 bytes in the matrix descriptors' 128-byte swizzle
 //    (e4m3: 8 positions, as they are, into places of their own, and from there as
 //    fp16, exactly, into the lines);
-//  * one warp issues S of the next tile and O of this one, whichever can run;
+//  * two warps issue the products, S of the next tiles and O of the oldest;
 //  * softmax warps, two threads per row and tile, half of its positions each; two
 //    groups of them take every other tile, as a tile's chain of steps is longer
 //    than its share of the time.  A row's maximum is raised only when it grows by
-//    more than 2^8;
+//    more than 2^24 (e4m3 cache: 2^11);
 //  * four warps then scale the sums down, before this tile's are added.
 // All tiles of all (sequence, rows) items are one line, cut evenly into one range
 // per CTA; an item that spans ranges is left in parts in the workspace, which a
@@ -41,7 +41,7 @@
 // Precision: q and the cache enter exactly (an e4m3 cache as fp16 values, with q
 // scaled by a power of two per row: 2^-38 of the row's largest).  Weights enter
 // the second product as bf16, 2^-8 of each (fp16 beside an e4m3 cache, 2^-11, or
-// 2^-32 of the row's largest): independent errors, which in the sum stay below the
+// 2^-29 of the row's largest): independent errors, which in the sum stay below the
 // result's own rounding to bf16, while a second part would be half as many
 // products again where they bound the call.  Sums, statistics and parts are fp32.
 //
@@ -63,11 +63,11 @@ namespace {
 constexpr int LT = 32;                // positions per tile
 constexpr int HC = LT / 2;            // a softmax thread's positions of a tile
 constexpr int LSTART = 4;             // tiles' time that an item costs besides its tiles
-constexpr float kGrow = 8.0f;         // log2 units that a row's maximum may lag behind
 constexpr int MOST_ROWS = 64, MOST_STAGES = 8;
 // Warps 0-15 by four: the first two of each four are softmax warps (their tensor memory lanes are rows 0-31 and 32-63), of
-// the others one issues products and seven load; warps 16-19 scale sums.
-constexpr int LTH = 20 * 32, PRODUCTS = 2, NLOAD = 7;
+// the others one each issues the two products, and six load; warps 16-19 scale sums.  (One warp that issued whichever
+// product could run saw both late: 64 sequences of 4096 positions, 128 heads, KQ_ONE in place of KQ_TWO us.)
+constexpr int LTH = 20 * 32, SCORES = 2, SUMS = 3, NLOAD = 6;
 
 template <int C, bool F8, int NR>
 struct LCfg {
@@ -78,17 +78,19 @@ struct LCfg {
   static constexpr int QS = (NB - QT) * NR * 128;     // the others, in shared memory
   static constexpr int P = NR * 128;                  // a tile's weights
   static constexpr int U = F8 ? 8 : 16;               // positions at a time of a loader
-  static constexpr int LOADERS = F8 ? 6 : NLOAD;
   // e4m3: the places of a loader's pieces, as they are in the cache; all but one are on their way
   static constexpr int RAWROW = C + 64, RAWS = F8 ? 2 : 0, RAW = RAWS * U * RAWROW;
-  static constexpr int smem(int stages, int B) { return QS + 2 * P + stages * STAGE + LOADERS * RAW + 4 * (B + 1); }
+  static constexpr int smem(int stages, int B) { return QS + 2 * P + stages * STAGE + NLOAD * RAW + 4 * (B + 1); }
   static constexpr int ROOM = 227 * 1024 - 4096;      // less the static memory
   static constexpr int LEAST = F8 ? 3 : 4;            // stages
   static_assert(smem(LEAST, 4096) <= ROOM);
   // tensor memory columns: o, q, S
   static constexpr int MB = C / 128, CO = 0, CQ = C == 256 ? 256 : NR == 64 ? 256 : 128, CS = 448, COLS = 512;
   static_assert(MB * NR <= CQ && CQ + 32 * QT <= CS && CS + LT <= COLS);
-  static constexpr float LIFT = F8 ? 7.0f : 0.0f;     // log2: fp16 weights, below 2^8, fill fp16's range
+  // log2 units that a row's maximum may lag behind, so that sums are seldom scaled (a scaling is a tile's time, and with 8
+  // units 64 rows of random scores took 160 us in place of KQ_GROW_US): bf16 weights have fp32's range; fp16 ones, which end
+  // at 2^16, are lifted so far that what is left below reaches 2^-28 of the maximum
+  static constexpr float GROW = F8 ? 11.0f : 24.0f, LIFT = F8 ? 4.0f : 0.0f;
 };
 
 struct LParams {
@@ -225,7 +227,7 @@ struct Latent {
 
   // ---- loaders: U positions at a time, in turn, their page ids one turn ahead
   __device__ __forceinline__ void load(int lw, int lane) {
-    constexpr int U = L::U, PT = LT / U, STEP = L::LOADERS;
+    constexpr int U = L::U, PT = LT / U, STEP = NLOAD;
     const int n = g.t1 - g.t0, b0 = g.t0 * LT, units = PT * n;
     auto page_of = [&](int x) {  // of this lane's position
       const int j = b0 + U * x + lane % U;
@@ -325,59 +327,57 @@ struct Latent {
     *reinterpret_cast<uint4*>(row + ((2 * c + 1) ^ r) * 16) = make_uint4(f8_pair(v.z), f8_pair(v.z >> 16), f8_pair(v.w), f8_pair(v.w >> 16));
   }
 
-  // ---- products, by one warp: S of the next tile, O of the oldest, whichever can run
-  __device__ __forceinline__ void products(int segment) {
+  // ---- products, each by a warp of its own
+  __device__ __forceinline__ void scores(int segment) {
     const int n = g.t1 - g.t0;
     const uint32_t rs = smem_u32(ring), t = uniform(tb), on = elect();
-    const uint64_t q = line_desc(smem_u32(qs), 16), w0 = line_desc(smem_u32(ps), 16);
+    const uint64_t q = line_desc(smem_u32(qs), 16);
     const int rope = p.rope / 16;
     wait(&bars.q_full, segment);
-    uint32_t idle = 0;
-    int sst = tile0 % p.stages, sph = tile0 / p.stages, vst = sst;  // the stages of both products' tiles
-    int s = 0, v = 0;
-    auto sums = [&] {  // of the oldest tile whose scores are under way
-      const int gv = tile0 + v;
-      if (v >= s || !__all_sync(0xFFFFFFFFu, phase_done(&bars.p_full[gv & 1], gv >> 1) && phase_done(&bars.scaled[gv & 1], gv >> 1))) return false;
+    int st = tile0 % p.stages, ph = tile0 / p.stages;
+    for (int i = 0; i < n; ++i) {
+      const int gi = tile0 + i;
+      wait(&bars.full[st], ph);
+      if (gi > 0) wait(&bars.s_free[(gi - 1) & 1], (gi - 1) >> 1);
+      fence_proxy_async_smem();  // the copies, which the barrier has put before this, seen by the tensor cores
       tc_fence_after();
-      const uint64_t c = line_desc(uniform(rs + vst * L::STAGE), L::LINES);
-      const uint64_t w = w0 + uniform((gv & 1) * L::P / 16);
-      const uint32_t more = v > 0;
+      if (ok) {
+        const uint64_t k = line_desc(uniform(rs + st * L::STAGE), 16);
 #pragma unroll
-      for (int k = 0; k < LT / 16; ++k)
-#pragma unroll
-        for (int mb = 0; mb < L::MB; ++mb)
-          mma_ss_on(t + L::CO + mb * NR, c + (2 * mb * L::LINES + k * 2048) / 16, w + 2 * k, idesc(F8, NR, true), k > 0 ? 1 : more, on);
-      commit_on(smem_u32(&bars.pv_done[gv & 1]), on);
-      commit_on(smem_u32(&bars.empty[vst]), on);
-      ++v;
-      if (++vst == p.stages) vst = 0;
-      return true;
-    };
-    while (v < n && ok) {
-      bool did = false;
-      const int gs = tile0 + s;
-      if (s < n && __all_sync(0xFFFFFFFFu, phase_done(&bars.full[sst], sph) && (gs == 0 || phase_done(&bars.s_free[(gs - 1) & 1], (gs - 1) >> 1)))) {
-        fence_proxy_async_smem();  // the copies, which the barrier has put before this, seen by the tensor cores
-        tc_fence_after();
-        const uint64_t k = line_desc(uniform(rs + sst * L::STAGE), 16);
-#pragma unroll
-        for (int i = 0; i < 4 * L::NB; ++i) {
-          if (i >= 4 * (L::NB - 1) && i - 4 * (L::NB - 1) >= rope) continue;
-          const uint64_t b = k + (i / 4 * L::LINES + i % 4 * 32) / 16;
-          if (i < 4 * L::QT) mma_ts_on(t + L::CS, t + L::CQ + 8 * i, b, idesc(F8, LT, false), i > 0, on);
-          else mma_ss_on(t + L::CS, q + ((i / 4 - L::QT) * (NR * 128) + i % 4 * 32) / 16, b, idesc(F8, LT, false), 1, on);
+        for (int j = 0; j < 4 * L::NB; ++j) {
+          if (j >= 4 * (L::NB - 1) && j - 4 * (L::NB - 1) >= rope) continue;
+          const uint64_t b = k + (j / 4 * L::LINES + j % 4 * 32) / 16;
+          if (j < 4 * L::QT) mma_ts_on(t + L::CS, t + L::CQ + 8 * j, b, idesc(F8, LT, false), j > 0, on);
+          else mma_ss_on(t + L::CS, q + ((j / 4 - L::QT) * (NR * 128) + j % 4 * 32) / 16, b, idesc(F8, LT, false), 1, on);
         }
-        commit_on(smem_u32(&bars.s_full[gs & 1]), on);
-        ++s;
-        if (++sst == p.stages) sst = 0, ++sph;
-        did = true;
+        commit_on(smem_u32(&bars.s_full[gi & 1]), on);
       }
-      did |= sums();
-      idle = did ? 0 : idle + 1;
-      if (idle > (1u << 25)) {
-        ok = false;
-        record_error(p.a.err, DEV_ERR_MBAR_TIMEOUT);
+      if (++st == p.stages) st = 0, ++ph;
+    }
+  }
+  __device__ __forceinline__ void sums() {
+    const int n = g.t1 - g.t0;
+    const uint32_t rs = smem_u32(ring), t = uniform(tb), on = elect();
+    const uint64_t w0 = line_desc(smem_u32(ps), 16);
+    int st = tile0 % p.stages;
+    for (int i = 0; i < n; ++i) {
+      const int gi = tile0 + i;
+      wait(&bars.scaled[gi & 1], gi >> 1);
+      wait(&bars.p_full[gi & 1], gi >> 1);
+      tc_fence_after();
+      if (ok) {
+        const uint64_t c = line_desc(uniform(rs + st * L::STAGE), L::LINES);
+        const uint64_t w = w0 + uniform((gi & 1) * L::P / 16);
+        const uint32_t more = i > 0;
+#pragma unroll
+        for (int k = 0; k < LT / 16; ++k)
+#pragma unroll
+          for (int mb = 0; mb < L::MB; ++mb)
+            mma_ss_on(t + L::CO + mb * NR, c + (2 * mb * L::LINES + k * 2048) / 16, w + 2 * k, idesc(F8, NR, true), k > 0 ? 1 : more, on);
+        commit_on(smem_u32(&bars.pv_done[gi & 1]), on);
+        commit_on(smem_u32(&bars.empty[st]), on);
       }
+      if (++st == p.stages) st = 0;
     }
   }
 
@@ -494,7 +494,7 @@ struct Latent {
           l *= m == -INFINITY ? 0.0f : ex2(m - now);
           m = now;
         }
-        const bool grow = mx > (m == -INFINITY ? m : m + kGrow);
+        const bool grow = mx > (m == -INFINITY ? m : m + L::GROW);
         float c = 1.0f;
         if (__any_sync(0xFFFFFFFFu, grow)) {
           if (grow) {
@@ -608,10 +608,10 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
   uint8_t* ps = smem + L::QS;
   uint8_t* ring = ps + 2 * L::P;
   uint8_t* raw = ring + p.stages * L::STAGE;
-  int* prefix = reinterpret_cast<int*>(raw + L::LOADERS * L::RAW);
+  int* prefix = reinterpret_cast<int*>(raw + NLOAD * L::RAW);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool softmax = warp < 16 && (warp & 3) < 2, scaler = warp >= 16;
-  const int loader = !softmax && !scaler && warp != PRODUCTS ? (warp >> 2) * 2 + (warp & 3) - 3 : -1;
+  const int loader = !softmax && !scaler && warp > 3 ? (warp >> 2) * 2 + (warp & 3) - 4 : -1;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) { mbar_init(&bars.full[i], 32 * LT / L::U); mbar_init(&bars.empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
     mbar_init(&bars.q_full, 8);
     fence_mbar_init();
   }
-  if (warp == PRODUCTS) { tmem_alloc(&bars.tmem, L::COLS); tmem_relinquish(); }
+  if (warp == SCORES) { tmem_alloc(&bars.tmem, L::COLS); tmem_relinquish(); }
   pdl_wait();
   pdl_launch_dependents();
   build_prefix<LT>(a, LSTART, prefix, bars.scan);
@@ -715,9 +715,11 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
         else w.template softmax<true>(lanes, r, active, pos, bits, f);
       } else if (scaler) {
         w.rescale(lanes);
-      } else if (warp == PRODUCTS) {
-        w.products(segment);
-      } else if (loader < L::LOADERS) {
+      } else if (warp == SCORES) {
+        w.scores(segment);
+      } else if (warp == SUMS) {
+        w.sums();
+      } else {
         w.load(loader, lane);
       }
       ++segment;
@@ -767,7 +769,7 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == PRODUCTS) tmem_dealloc(tb, L::COLS);
+  if (warp == SCORES) tmem_dealloc(tb, L::COLS);
 }
 
 int ranges() { return num_sms() < 160 ? num_sms() : 160; }

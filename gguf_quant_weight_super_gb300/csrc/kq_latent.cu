@@ -84,9 +84,9 @@ struct LCfg {
   static constexpr int ROOM = 227 * 1024 - 4096;      // less the static memory
   static constexpr int LEAST = F8 ? 3 : 4;            // stages
   static_assert(smem(LEAST, 4096) <= ROOM);
-  // tensor memory columns: o, q, S
+  // tensor memory columns: o, q, S x 2
   static constexpr int MB = C / 128, CO = 0, CQ = C == 256 ? 256 : NR == 64 ? 256 : 128, CS = 448, COLS = 512;
-  static_assert(MB * NR <= CQ && CQ + 32 * QT <= CS && CS + LT <= COLS);
+  static_assert(MB * NR <= CQ && CQ + 32 * QT <= CS && CS + 2 * LT <= COLS);
   // log2 units that a row's maximum may lag behind, so that sums are seldom scaled (a scaling is a tile's time, and with 8
   // units 64 rows of random scores took 160 us in place of KQ_GROW_US): bf16 weights have fp32's range; fp16 ones, which end
   // at 2^16, are lifted so far that what is left below reaches 2^-28 of the maximum
@@ -338,17 +338,18 @@ struct Latent {
     for (int i = 0; i < n; ++i) {
       const int gi = tile0 + i;
       wait(&bars.full[st], ph);
-      if (gi > 0) wait(&bars.s_free[(gi - 1) & 1], (gi - 1) >> 1);
+      if (gi > 1) wait(&bars.s_free[gi & 1], (gi - 2) >> 1);
       fence_proxy_async_smem();  // the copies, which the barrier has put before this, seen by the tensor cores
       tc_fence_after();
       if (ok) {
         const uint64_t k = line_desc(uniform(rs + st * L::STAGE), 16);
+        const uint32_t to = uniform(t + L::CS + LT * (gi & 1));
 #pragma unroll
         for (int j = 0; j < 4 * L::NB; ++j) {
           if (j >= 4 * (L::NB - 1) && j - 4 * (L::NB - 1) >= rope) continue;
           const uint64_t b = k + (j / 4 * L::LINES + j % 4 * 32) / 16;
-          if (j < 4 * L::QT) mma_ts_on(t + L::CS, t + L::CQ + 8 * j, b, idesc(F8, LT, false), j > 0, on);
-          else mma_ss_on(t + L::CS, q + ((j / 4 - L::QT) * (NR * 128) + j % 4 * 32) / 16, b, idesc(F8, LT, false), 1, on);
+          if (j < 4 * L::QT) mma_ts_on(to, t + L::CQ + 8 * j, b, idesc(F8, LT, false), j > 0, on);
+          else mma_ss_on(to, q + ((j / 4 - L::QT) * (NR * 128) + j % 4 * 32) / 16, b, idesc(F8, LT, false), 1, on);
         }
         commit_on(smem_u32(&bars.s_full[gi & 1]), on);
       }
@@ -444,7 +445,7 @@ struct Latent {
       if (active) {
         {
           uint32_t v[HC];
-          tmem_ld16(tb + lanes + L::CS + HC * half, v);
+          tmem_ld16(tb + lanes + L::CS + LT * wg + HC * half, v);
           tmem_wait_ld();
           tie(v);
 #pragma unroll

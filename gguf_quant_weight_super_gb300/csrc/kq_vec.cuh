@@ -31,6 +31,26 @@ __device__ __forceinline__ uint32_t e4m3x4(float4 v) {
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 __device__ __forceinline__ void store4(__nv_fp8_e4m3* p, float4 v) { *reinterpret_cast<uint32_t*>(p) = e4m3x4(v); }
+// Eight neighbouring values.
+struct F8 {
+  float4 a, b;
+};
+__device__ __forceinline__ F8 load8(const float* p) { return {load4(p), load4(p + 4)}; }
+__device__ __forceinline__ F8 load8(const __nv_bfloat16* p) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+  return {bf16x4(make_uint2(u.x, u.y)), bf16x4(make_uint2(u.z, u.w))};
+}
+__device__ __forceinline__ void store8(float* p, F8 v) {
+  store4(p, v.a);
+  store4(p + 4, v.b);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, F8 v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(bf16_pair(v.a.x, v.a.y), bf16_pair(v.a.z, v.a.w), bf16_pair(v.b.x, v.b.y),
+                                            bf16_pair(v.b.z, v.b.w));
+}
+__device__ __forceinline__ void store8(__nv_fp8_e4m3* p, F8 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x4(v.a), e4m3x4(v.b));
+}
 __device__ __forceinline__ float sq4(float4 v) { return v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w; }
 __device__ __forceinline__ float4 scale4(float4 v, float s, float4 w, float off) {
   return make_float4(v.x * s * (w.x + off), v.y * s * (w.y + off), v.z * s * (w.z + off), v.w * s * (w.w + off));

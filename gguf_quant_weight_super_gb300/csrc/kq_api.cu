@@ -702,7 +702,7 @@ kq_status kq_latent_attn(const kq_latent_cache* cache, const int32_t* page_table
   if (max_pages < 0 || !good_scale(scale == 0.0f ? 1.0f : fabsf(scale))) return KQ_ERR_ARG;
   if (B == 0 || T == 0) return KQ_OK;
   if (max_pages > INT32_MAX) return KQ_ERR_UNSUPPORTED;
-  const int64_t tiles = (max_pages * cache->page_size + 31) / 32 + 16;  // the line of tiles is counted in 31 bits
+  const int64_t tiles = (max_pages * cache->page_size + 31) / 32 + 24;  // the line of tiles is counted in 31 bits
   if (tiles * B > INT32_MAX / ((T * n_heads + 63) / 64)) return KQ_ERR_UNSUPPORTED;
   if (!seq_lens || !q || !out || (max_pages > 0 && !page_table)) return KQ_ERR_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(tree, 8) ||

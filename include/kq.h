@@ -655,7 +655,7 @@ kq_status kq_latent_append(const kq_latent_cache *cache, const int32_t *page_tab
  * bytes, 256-byte aligned, zero-filled once before first use; one call at a time
  * per workspace; a workspace serves any calls that it is large enough for.
  * q and out 16-byte aligned, q_stride a multiple of 16 bytes.  B <= 4096,
- * n_heads <= 256, and B * ceil(T*n_heads / 64) * (max_pages*page_size / 32 + 16)
+ * n_heads <= 256, and B * ceil(T*n_heads / 64) * (max_pages*page_size / 32 + 24)
  * < 2^31 (else KQ_ERR_UNSUPPORTED).
  */
 size_t kq_latent_attn_workspace_size(const kq_latent_cache *cache, int64_t B, int64_t T, int32_t n_heads);

@@ -550,11 +550,18 @@ static kq_status accept(TreeArgs& a, const int32_t* page_table, int64_t max_page
   if (B > 65535) return KQ_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return KQ_OK;
   if (!seq_lens || !tokens || !ids || (a.n_pools > 0 && max_pages > 0 && !page_table)) return KQ_ERR_ARG;
-  if (new_lens == seq_lens) return KQ_ERR_ARG;
   for (const void* p : {static_cast<const void*>(page_table), static_cast<const void*>(seq_lens),
                         static_cast<const void*>(tokens), static_cast<const void*>(ids), static_cast<const void*>(path),
                         static_cast<const void*>(count), static_cast<const void*>(next), static_cast<const void*>(new_lens)})
     if (!aligned(p, 4)) return KQ_ERR_ALIGN;
+  // every block walks by itself, whatever another has written; and moves by itself
+  for (const int32_t* out : {path, count, next, new_lens})
+    if (out && (out == seq_lens || out == tokens || out == ids || out == page_table || static_cast<const void*>(out) == tree))
+      return KQ_ERR_ARG;
+  bool twice = false;
+  for (int i = 1; i < a.n_pools; ++i)
+    for (int j = 0; j < i; ++j) twice |= a.pool[i] == a.pool[j];
+  if (twice && a.n_pages > 0) return KQ_ERR_ARG;
   a.page_table = page_table;
   a.max_pages = max_pages;
   a.seq_lens = seq_lens;

@@ -601,9 +601,10 @@ typedef struct kq_latent_cache {
  * each int32, NULL for off.  In every cache the nodes' keys and values are moved
  * from slots base + path[i] to base + i, where a chain's would lie.  n_caches 0
  * does the walk alone (then page_table may be NULL).
- * The caches are alike but for their pools (else KQ_ERR_ARG), at most 128 (256
- * latent ones), B <= 65535, T in 1..64 (else KQ_ERR_UNSUPPORTED).  No two tokens
- * of a call share a slot.
+ * The caches are alike but for their pools, which are all different ones (else
+ * KQ_ERR_ARG), at most 128 (256 latent ones), B <= 65535, T in 1..64 (else
+ * KQ_ERR_UNSUPPORTED).  No two tokens of a call share a slot, no two pools a slot's
+ * bytes, and no output lies in an input (KQ_ERR_ARG where they start together).
  */
 kq_status kq_tree_accept(const kq_kv_cache *caches, int32_t n_caches, const int32_t *page_table, int64_t max_pages,
                          const int32_t *seq_lens, const uint64_t *tree, const int32_t *tokens, const int32_t *ids,
@@ -650,10 +651,12 @@ kq_status kq_latent_append(const kq_latent_cache *cache, const int32_t *page_tab
  *   q   [B*T] rows of n_heads*(latent_dim + rope_dim) KQ_BF16, q_stride elements apart
  *   out [B*T][n_heads][latent_dim] KQ_BF16
  * Scores, softmax statistics, sums and partial results are held in fp32; the
- * weights enter their product as bf16 (2^-8 of each), their sum in fp32.
+ * weights enter their product as bf16 (2^-8 of each; beside an e4m3 cache as fp16,
+ * 2^-11 of each or 2^-29 of the row's largest), their sum in fp32.
  * Repeated calls give identical outputs.  workspace: kq_latent_attn_workspace_size
  * bytes, 256-byte aligned, zero-filled once before first use; one call at a time
- * per workspace; a workspace serves any calls that it is large enough for.
+ * per workspace; a workspace serves any calls of kq_latent_attn that it is large
+ * enough for (not one of kq_attn_decode too).
  * q and out 16-byte aligned, q_stride a multiple of 16 bytes.  B <= 4096,
  * n_heads <= 256, and B * ceil(T*n_heads / 64) * (max_pages*page_size / 32 + 24)
  * < 2^31 (else KQ_ERR_UNSUPPORTED).

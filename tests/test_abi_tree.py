@@ -88,6 +88,19 @@ def test_accept_refusals(L):  # noqa: F811
     assert call(L.kq_latent_accept, [latent(), latent(slot_stride=592)]) == ARG
 
 
+def test_accept_refuses_overlaps(L):  # noqa: F811
+    """Blocks walk and move by themselves: outputs over inputs, and one pool twice, would depend on their order."""
+    ins = dict(table=F + 1024, W=4, lens=F + 2048, tree=F + 3328, tokens=F + 4096, ids=F + 5120, B=2, T=3)
+    outs = dict(path=F + 6144, count=F + 7168, next=F + 8192, new=F + 9216)
+    two = (kq.KqKvCache * 2)(cache(k=F, v=F + (1 << 20)), cache(k=F + (2 << 20), v=F + (1 << 20)))
+    assert L.kq_tree_accept(ctypes.addressof(two), 2, *ins.values(), *outs.values(), None) == ARG
+    two = (kq.KqLatentCache * 2)(latent(), latent())
+    assert L.kq_latent_accept(ctypes.addressof(two), 2, *ins.values(), *outs.values(), None) == ARG
+    for o in outs:
+        for i in ("table", "lens", "tree", "tokens", "ids"):
+            assert L.kq_tree_accept(None, 0, *ins.values(), *{**outs, o: ins[i]}.values(), None) == ARG, (o, i)
+
+
 def test_latent_refusals(L):  # noqa: F811
     def append(c=None, r=None, **kw):
         a = dict(table=F, W=4, lens=F, tree=F, B=2, T=3, ql=F, qr=F, rows=F, xd=1, ls=512, rs=64, hs=64, cs=576, H=8)

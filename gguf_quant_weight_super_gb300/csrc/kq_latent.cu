@@ -808,12 +808,12 @@ cudaError_t launch_rows(LParams p, cudaStream_t st) {
   p.stages = L::LEAST;  // and as many more as there is room for
   while (p.stages < MOST_STAGES && L::smem(p.stages + 1, p.a.B) <= L::ROOM) ++p.stages;
   const size_t smem = L::smem(p.stages, p.a.B);
-  static int set[64] = {0};
+  static bool set[64] = {false};
   const int dev = current_device_id();
-  if (set[dev] < static_cast<int>(smem)) {
-    const cudaError_t e = cudaFuncSetAttribute(latent_kernel<C, F8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (!set[dev]) {  // for all calls: one at the same time may want less
+    const cudaError_t e = cudaFuncSetAttribute(latent_kernel<C, F8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ROOM);
     if (e != cudaSuccess) return e;
-    set[dev] = static_cast<int>(smem);
+    set[dev] = true;
   }
   const cudaError_t e = launch_pdl(latent_kernel<C, F8, NR>, dim3(p.ranges), dim3(LTH), smem, st, p);
   if (e != cudaSuccess) return e;

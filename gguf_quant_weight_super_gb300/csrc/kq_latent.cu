@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
         bars.top[part][r] = mx;
         softmax_sync();
         mx = fmaxf(fmaxf(bars.top[0][r], bars.top[1][r]), fmaxf(bars.top[2][r], bars.top[3][r]));
-        const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
+        const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 127);
         f *= __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
         mul = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
       }

@@ -368,3 +368,11 @@ def test_a_latent_layer_step_by_step_equals_its_prompt():
             # each is within 2^-8 (sum p|c| + |out|) and a little of the same value; sum p|c| is below 4 here
             assert bool((d <= 2 * 2.0 ** -8 * (4 + all_at_once[:, t].float().abs()) + 2.0 ** -10).all())
     assert torch.equal(P.c.nan_to_num(5.0), Q.c.nan_to_num(5.0))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F8])
+@pytest.mark.parametrize("power", [-108, 108])
+def test_latent_attn_queries_far_from_one(dtype, power):
+    """Queries and a scale whose product is an ordinary one's."""
+    P = Latent([700, 64, 5], 512, 64, 16, dtype, seed=2)
+    check_latent(P, latent_q(3, 2, 16, 576, 3, mul=1.4 * 2.0 ** power), scale=0.07 * 2.0 ** -power)

@@ -370,6 +370,68 @@ def test_a_latent_layer_step_by_step_equals_its_prompt():
     assert torch.equal(P.c.nan_to_num(5.0), Q.c.nan_to_num(5.0))
 
 
+# ---- many items, shared workspaces, long pools, other streams
+
+@pytest.mark.parametrize("dtype", [BF16, F8])
+def test_latent_attn_more_sequences_than_ranges_and_one_split(dtype):
+    """Parts joined range by range: 330 short sequences beside two that many ranges share."""
+    lens = [int(x) for x in np.random.default_rng(4).integers(0, 70, 332)]
+    lens[100], lens[331] = 9000, 5003
+    P = Latent(lens, 256, 32, 16, dtype, seed=9)
+    check_latent(P, latent_q(332, 1, 8, 288, 6))
+    check_latent(P, latent_q(332, 2, 8, 288, 7), [trees(1, 2, b)[0] for b in range(332)])
+
+
+def test_latent_attn_one_workspace_for_calls_of_all_shapes():
+    """In turn, on one stream, what the largest call asked for: with and without a tree, few and many rows, splits or none."""
+    P = Latent([3000, 5, 0, 64, 900, 17], 512, 64, 16, BF16, seed=5)
+    F = Latent([5000, 70], 512, 64, 32, F8, seed=6)
+    shapes = [(P, 6, 7, 64), (P, 6, 1, 16), (F, 2, 1, 3), (P, 6, 2, 100), (F, 2, 33, 16), (P, 6, 1, 1)]
+    ws = torch.zeros(max(kq.latent_attn_workspace(p.cache, b, t, h).numel() for p, b, t, h in shapes), dtype=torch.uint8,
+                     device="cuda")
+    for rep in range(2):
+        for p, b, t, h in shapes:
+            check_latent(p, latent_q(b, t, h, 576, t + h + rep), trees(b, t, h) if t > 2 else None, ws=ws)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F8])
+def test_latent_ops_in_pages_past_2_to_the_32_bytes_and_elements(dtype):
+    T, lens, page = 5, [5, 700, 33], 64
+    P = Latent(lens, 512, 64, page, dtype, seed=3)
+    n = P.c.shape[0]
+    far = -(-(2 ** 32 + 4096) // (page * 576))
+    pool = torch.empty((far + n, page, 576), dtype=dtype, device="cuda")
+    pool[:far].view(torch.uint8).fill_(0xff)  # NaN
+    pool[far:] = P.c
+    table = torch.where(P.table >= 0, P.table + far, P.table)
+    big = kq.LatentCache(pool, 512, P.scale)
+    q, masks = latent_q(3, T, 16, 576, 4), trees(3, T, 5)
+    ws = kq.latent_attn_workspace(P.cache, 3, T, 16)
+    g = torch.Generator().manual_seed(5)
+    c, ql, qr = (torch.randn(s, generator=g).to(BF16).cuda() for s in ((3, T, 576), (3, T, 16, 512), (3, T, 16, 64)))
+    rope = kq.RopeNorm(kq.rope_table(800, 64))
+    words, ids = (torch.randint(0, 2, (3, T), generator=g).int().cuda() for _ in range(2))
+    outs = []
+    for cache, tab in ((P.cache, P.table), (big, table)):
+        a = kq.latent_append(cache, tab, P.seq_lens, ql, qr, c, rope, tree=to_tensor(masks))
+        o = kq.latent_attn(cache, tab, P.seq_lens, q, ws, 0.07, tree=to_tensor(masks))
+        outs.append([a, o, *kq.tree_accept(kq.CacheSet([cache]), tab, P.seq_lens, to_tensor(masks), words, ids)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+    assert torch.equal(pool[far:].view(torch.uint8), P.c.view(torch.uint8))
+    assert bool((pool[:far].view(torch.int64) == -1).all())
+
+
+def test_latent_attn_rows_with_strides_on_another_stream():
+    """Queries that are a slice of a wider tensor; a stream that waits for nothing else."""
+    P = Latent([900, 40, 0], 512, 64, 16, BF16, seed=2)
+    wide = latent_q(3, 4, 24, 576, 3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    check_latent(P, wide[:, :, 5:21], stream=side)
+    check_latent(P, wide[:, :, 8:12], trees(3, 4, 1), stream=side)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F8])
 @pytest.mark.parametrize("power", [-108, 108])
 def test_latent_attn_queries_far_from_one(dtype, power):

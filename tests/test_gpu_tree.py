@@ -410,3 +410,78 @@ def test_a_verified_tree_step_equals_the_chain_of_its_branch():
             d = (ac[0].float() - outs["a"][b, pick].float()).abs()
             # both are within one bf16 rounding and 2^-15 of sum p|v| (below 4) of the same value
             assert bool((d <= 2 * 2.0 ** -8 * ac[0].float().abs() + 2.0 ** -12).all())
+
+
+# ---- many items, shared workspaces, long pools, other streams
+
+@pytest.mark.parametrize("q_dtype,dtype,G,T", [(BF16, BF16, 4, 3), (F32, F8, 1, 2), (BF16, BF16, 8, 24)])
+def test_attn_tree_more_sequences_than_ranges_and_one_split(q_dtype, dtype, G, T):
+    """Parts joined range by range: 330 short sequences beside two that many ranges share."""
+    lens = [int(x) for x in np.random.default_rng(4).integers(0, 60, 332)]
+    lens[100], lens[331] = 9000, 5003
+    P = Paged(lens, 1, 128, 16, dtype, seed=9)
+    check_tree(P, trees(332, T, 3), rand_q(332, T, G, 128, q_dtype, 6))
+
+
+def test_attn_tree_and_attn_decode_share_a_workspace():
+    """In turn, on one stream, what the largest call asked for: splits or none, wide and narrow, trees and chains."""
+    P = Paged([3000, 5, 0, 64, 900, 17], 2, 128, 16, BF16, seed=5)
+    shapes = [(7, 8, BF16), (1, 2, BF16), (24, 16, BF16), (3, 4, F32), (64, 8, BF16), (2, 16, BF16)]
+    ws = torch.zeros(max(kq.attn_tree_workspace(P.cache, 6, t, h).numel() for t, h, _ in shapes), dtype=torch.uint8, device="cuda")
+    for rep in range(2):
+        for t, h, d in shapes:
+            q, tree = rand_q(6, t, h, 128, d, t + h + rep), to_tensor(trees(6, t, t))
+            # a workspace of its own gives the same bits
+            one = kq.attn_tree(P.cache, P.table, P.seq_lens, tree, q, ws)
+            own = kq.attn_tree(P.cache, P.table, P.seq_lens, tree, q, kq.attn_tree_workspace(P.cache, 6, t, h))
+            assert torch.equal(one, own), (rep, t, h)
+            if t <= 16:  # chains of more are refused
+                two = kq.attn_decode(P.cache, P.table, P.seq_lens, q, ws)
+                own = kq.attn_decode(P.cache, P.table, P.seq_lens, q, kq.attn_workspace(P.cache, 6, t, h))
+                assert torch.equal(two, own), (rep, t, h)
+
+
+@pytest.mark.parametrize("q_dtype,dtype,G", [(BF16, BF16, 8), (F32, F8, 2)])
+def test_tree_ops_in_pages_past_2_to_the_32_bytes_and_elements(q_dtype, dtype, G):
+    T, lens, page, D = 9, [9, 700, 33], 32, 128
+    P = Paged(lens, 2, D, page, dtype, seed=3)
+    n = P.k.shape[0]
+    far = -(-(2 ** 32 + 4096) // (page * 2 * D))
+    pools = []
+    for x in (P.k, P.v):
+        pool = torch.empty((far + n, page, 2, D), dtype=dtype, device="cuda")
+        pool[:far].view(torch.uint8).fill_(0xff)  # NaN
+        pool[far:] = x
+        pools.append(pool)
+    table = torch.where(P.table >= 0, P.table + far, P.table)
+    big = kq.KVCache(*pools, P.k_scale, P.v_scale)
+    q, k, v = (rand_q(3, T, h, D, q_dtype, h) for h in (2 * G, 2, 2))
+    tree, rope, ws = to_tensor(trees(3, T, 5)), kq.RopeNorm(kq.rope_table(800, D)), kq.attn_tree_workspace(P.cache, 3, T, 2 * G)
+    g = torch.Generator().manual_seed(5)
+    words, ids = (torch.randint(0, 2, (3, T), generator=g).int().cuda() for _ in range(2))
+    outs = []
+    for cache, tab in ((P.cache, P.table), (big, table)):
+        a = kq.kv_append_tree(cache, tab, P.seq_lens, tree, q, k, v, rope, q_out_dtype=q_dtype)
+        o = kq.attn_tree(cache, tab, P.seq_lens, tree, a, ws)
+        outs.append([a, o, *kq.tree_accept(kq.CacheSet([cache]), tab, P.seq_lens, tree, words, ids)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+    for pool, x in zip(pools, (P.k, P.v)):
+        assert torch.equal(pool[far:].view(torch.uint8), x.view(torch.uint8))
+        assert bool((pool[:far].view(torch.int64) == -1).all())
+
+
+def test_attn_tree_rows_with_strides_on_another_stream():
+    """Queries inside a fused projection; a stream that waits for nothing else."""
+    P = Paged([900, 40, 0], 2, 128, 16, BF16, seed=2)
+    for T, Hq in ((4, 4), (24, 16)):
+        masks = trees(3, T, 1)
+        fused = rand_q(3, T, Hq + 5, 128, BF16, 3)
+        q = fused[:, :, 2:2 + Hq]
+        want = check_tree(P, masks, q)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = kq.attn_tree(P.cache, P.table, P.seq_lens, to_tensor(masks), q, kq.attn_tree_workspace(P.cache, 3, T, Hq),
+                           stream=side)
+        side.synchronize()
+        assert torch.equal(got, want)

@@ -710,10 +710,11 @@ __device__ __forceinline__ void build_prefix(const AttnArgs& a, int start, int* 
 struct Line {
   const int* prefix;
   int HR, nc, share, more;  // heads x row tiles of a sequence; ranges
-  __device__ __forceinline__ Line(const AttnArgs& a, int RT, const int* pre) : prefix(pre) {
+  __device__ __forceinline__ Line(const AttnArgs& a, int RT, const int* pre) : Line(a, RT, pre, gridDim.x) {}
+  __device__ __forceinline__ Line(const AttnArgs& a, int RT, const int* pre, int most) : prefix(pre) {
     HR = a.c.n_kv_heads * RT;  // the host has seen to it that the line's units fit 31 bits
     const int total = prefix[a.B] * HR;
-    nc = min(total, static_cast<int>(gridDim.x));
+    nc = min(total, most);
     share = total / nc;
     more = total - share * nc;
   }

@@ -35,8 +35,12 @@
 //    more than 2^24 (e4m3 cache: 2^11);
 //  * four warps then scale the sums down, before this tile's are added.
 // All tiles of all (sequence, rows) items are one line, cut evenly into one range
-// per CTA; an item that spans ranges is left in parts in the workspace, which a
-// second launch joins in the ranges' order.
+// per CTA (row tiles of a sequence side by side where that leaves no SM over: a
+// line of sequences, which neighbouring CTAs walk together); an item that spans
+// ranges is left in parts in the workspace, which a second launch joins in the
+// ranges' order.  The loaders do not wait for a segment's end: the next one's first
+// tiles are there when its queries are (64 sequences of 4096 positions, 128 heads
+// 145 -> 140 us, e4m3, 16 heads, 96 -> 90).
 //
 // Precision: q and the cache enter exactly (an e4m3 cache as fp16 values, with q
 // scaled by a power of two per row: 2^-38 of the row's largest).  Weights enter
@@ -46,20 +50,21 @@
 // products again where they bound the call.  Sums, statistics and parts are fp32.
 //
 // Measured on one GB300, calls in a graph: 64 sequences of 4096 positions, 16
-// heads, bf16, 70 us (4.4 TB/s; a tile is 1700 clocks, at the memory's rate, but the
-// first one comes 18000 clocks after the start); 128 heads 149 us (490 TFLOP/s; two
-// CTAs read each vector, and a stage is held for 4000 clocks from its scores to its
-// sums); in an e4m3 cache 95 and 199 us (four or three stages beside the raw
-// pieces); one of 131071 positions, 16 heads, 48 us, of which the join takes 8; one
-// of 1000, 15 us.
+// heads, bf16, 68 us (4.5 TB/s; a tile is 1600 clocks, at the memory's rate, but the
+// first one comes 18000 clocks after the start); 128 heads 140 us (520 TFLOP/s; a
+// tile is 1800 clocks: of a stage's 8700 from one load to the next, 4000 pass until
+// its copies are there and 4500 until its sums are done, and five stages are all that
+// fits); in an e4m3 cache 90 and 196 us (four or three stages beside the raw pieces);
+// one of 131071 positions, 16 heads, 47 us, of which the join takes 8; one of 1000,
+// 15 us.
 //
 // Every wait is bounded: one that gives up sets the device error word, after
 // which the CTA's roles run through without waiting.
 //
 // Vectors that some rows see and others do not would reach the others as 0 * NaN
-// if they are not finite: a segment whose sums are not all finite runs again; then
-// each value that is not finite becomes 0 before the second product, and a row that
-// sees such a vector (its score is not finite) becomes NaN.
+// if they are not finite: segments whose sums are not all finite run again once the
+// range is through; then each value that is not finite becomes 0 before the second
+// product, and a row that sees such a vector (its score is not finite) becomes NaN.
 #include "kq_attn_kernel.cuh"
 #include "kq_join.cuh"
 #include "kq_vec.cuh"
@@ -109,15 +114,18 @@ struct LParams {
   int64_t page_bytes, slot_bytes;
   float c_scale;
   int rope, RT, rows, ranges, stages;  // rows: of a part
+  int abreast;                         // row tiles of a sequence that go side by side: RT, or 1
   int by_item;                         // split [items] instead of [ranges]
   Split* split;
   float *part_ml, *part;
 };
 
+constexpr int FLAGS = 32;
 struct LBars {
   uint64_t full[MOST_STAGES], empty[MOST_STAGES], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, decided[2][2], grown[2], scaled[2];
   uint32_t tmem;
-  int bad;
+  int bad;                       // a segment's sums are not all finite; which segments of the range's (the last: and all behind it)
+  uint32_t flags[FLAGS];
   int scan[NW];
   int raise[2];                  // a warpgroup's last tile, counted from 1, that raised a maximum
   float m[MOST_ROWS];            // the rows' maxima that their sums are relative to, in log2 units
@@ -186,6 +194,8 @@ __device__ __forceinline__ void tie(uint32_t (&v)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// All but the loaders, which run ahead.
+__device__ __forceinline__ void others_sync() { asm volatile("bar.sync 6, %0;" ::"n"(LTH - 32 * NLOAD) : "memory"); }
 // The two warps of 32 rows that work on one tile.
 __device__ __forceinline__ void rows_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(2 + id) : "memory"); }
 // A copy of 16 bytes, both addresses with constant offsets.
@@ -238,12 +248,16 @@ struct Latent {
   // ---- loaders: U positions at a time, in turn, their page ids one turn ahead
   __device__ __forceinline__ void load(int lw, int lane) {
     constexpr int U = L::U, PT = LT / U, STEP = NLOAD;
+    static_assert(STEP <= 3 * PT && L::LEAST >= 3);
+    // A loader's turns go on from segment to segment, at most three tiles apart: one that stood out a few short segments could
+    // come to a barrier two phases early, and take the phase before the last for the last.
+    const int first = (lw + STEP - tile0 % STEP * PT % STEP) % STEP;
     const int n = g.t1 - g.t0, b0 = g.t0 * LT, units = PT * n;
     auto page_of = [&](int x) {  // of this lane's position
       const int j = b0 + U * x + lane % U;
       return x < units && j < g.len ? __ldg(g.table + (j >> p.a.page_shift)) : 0;
     };
-    int page = page_of(lw);
+    int page = page_of(first);
     auto offset_at = [&](int x) {  // and its offset, the next page on its way
       const int next = page_of(x + STEP);
       const int64_t off = offset_of(b0 + U * x + lane % U, page);
@@ -270,9 +284,9 @@ struct Latent {
         copy_commit();
       };
 #pragma unroll
-      for (int i = 0; i < L::RAWS - 1; ++i) fetch(lw + i * STEP, i);
+      for (int i = 0; i < L::RAWS - 1; ++i) fetch(first + i * STEP, i);
       int slot = 0;
-      for (int x = lw; x < units; x += STEP) {
+      for (int x = first; x < units; x += STEP) {
         const int gi = tile0 + x / PT, st = gi % p.stages;
         copy_wait<L::RAWS - 2>();
         __syncwarp();
@@ -295,7 +309,7 @@ struct Latent {
         slot = slot + 1 == L::RAWS ? 0 : slot + 1;
       }
     } else {
-      for (int x = lw; x < units; x += STEP) {
+      for (int x = first; x < units; x += STEP) {
         const int gi = tile0 + x / PT, st = gi % p.stages;
         const int64_t off = offset_at(x);
         uint8_t* lines = ring + st * L::STAGE + x % PT * (U * 128);
@@ -326,8 +340,7 @@ struct Latent {
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.full[st])) : "memory");
       }
     }
-    copy_commit();
-    copy_wait<0>();
+    if constexpr (F8) copy_wait<0>();
   }
   // 16 e4m3 values as fp16: chunks 2 c and 2 c + 1 of row r's line.
   static __device__ __forceinline__ void put(uint8_t* lines, int r, int c, uint4 v) {
@@ -637,6 +650,7 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
       bars.raise[i] = 0;
     }
     bars.bad = 0;
+    for (int i = 0; i < FLAGS; ++i) bars.flags[i] = 0;
     mbar_init(&bars.q_full, 8);
     fence_mbar_init();
   }
@@ -648,24 +662,46 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = bars.tmem, lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-  const Line line(a, p.RT, prefix);
-  const int range = blockIdx.x, lo = line.bound(min(range, line.nc)), hi = range < line.nc ? line.bound(range + 1) : lo;
+  // row tiles abreast: neighbouring CTAs take the same range of a line of sequences, each for its row tile, and the ranges
+  // of one row tile are numbered in a row
+  const int most = gridDim.x / p.abreast, at = blockIdx.x / p.abreast, side = blockIdx.x - at * p.abreast, RT = p.RT / p.abreast;
+  const Line line(a, RT, prefix, most);
+  const int range = side * most + at, lo = line.bound(min(at, line.nc)), hi = at < line.nc ? line.bound(at + 1) : lo;
+  auto note = [&](const Item& it, bool whole, int slot) {
+    const int item = (it.b * line.HR + it.hr) * p.abreast + side;
+    if (!whole) p.split[p.by_item ? item : range] = {item, range, line.range_of(it.i1 - 1) - at + 1, slot};
+    else if (p.by_item) p.split[item].parts = 0;
+  };
   if (threadIdx.x == 0 && !p.by_item) p.split[range].parts = 0;
-  int tile0 = 0, segment = 0;
+  int tile0 = 0, segment = 0, pass = 0, u = lo, number = 0;  // segment: that ran; number: in this pass
   bool ok = true;
-  for (int u = lo; u < hi;) {
-    const Item it(a, line, p.RT, LSTART, u);
+  for (;;) {
+    if (u >= hi) {  // the segments whose sums are not all finite run again
+      if (pass++ > 0) break;
+      __syncthreads();
+      if (!bars.bad) break;
+      u = lo;
+      number = 0;
+      continue;
+    }
+    const Item it(a, line, RT, LSTART, u);
     const int end = min(it.i1, hi);
     if (u < it.i0) u = it.i0;
     if (u >= end) {  // none of its tiles is in this range
       u = end;
       continue;
     }
-    const int r0 = it.rt * NR, R = min(NR, a.T * a.G - r0);
+    const int r0 = (it.rt + side) * NR, R = min(NR, a.T * a.G - r0);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<int64_t>(it.b) * a.T * a.G + r0) * C;
     if (it.len == 0) {
-      if (threadIdx.x == 0) note_split(p.split, p.by_item, line, it, range, true, 0);
-      for (int x = threadIdx.x; x < R * (C / 4); x += LTH) store4(out + 4 * x, make_float4(0, 0, 0, 0));
+      if (threadIdx.x == 0) note(it, true, 0);
+      if (scaler)
+        for (int x = threadIdx.x - 512; x < R * (C / 4); x += LTH - 512) store4(out + 4 * x, make_float4(0, 0, 0, 0));
+      u = end;
+      continue;
+    }
+    const int name = min(number++, 32 * FLAGS - 1);
+    if (pass > 0 && !(bars.flags[name >> 5] >> (name & 31) & 1)) {
       u = end;
       continue;
     }
@@ -711,45 +747,46 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
       }
     }
     Latent<C, F8, NR> w{p, g, bars, smem, ps, ring, raw + max(loader, 0) * L::RAW, tb, tile0, ok, 0.0f, false};
-    // Which of the sums a warp of the first 16 takes out: of 128 dims 32 (its lanes), of those 128 the part-th, or of the
-    // rows the half.
-    constexpr int SPAN = NR * L::MB / 4;  // columns
-    const int col0 = part * SPAN, mb = col0 / NR, c0 = col0 % NR;
     const bool whole = u == it.i0 && end == it.i1;
     const int slot = 2 * range + (lo >= it.i0 ? 1 : 0);  // the range starts in these tiles (1), or before them
-    if (u == it.i0 && threadIdx.x == 0) note_split(p.split, p.by_item, line, it, range, whole, slot);
-    for (bool careful = false;; careful = true) {
+    if (u == it.i0 && threadIdx.x == 0) note(it, whole, slot);
+    if (loader >= 0) {  // on to the next segment as soon as there is room
+      w.load(loader, lane);
+      w.tile0 += g.t1 - g.t0;
+    } else {
       if (softmax) {
         softmax_sync();  // the rows' maxima are there
         w.load_q(r < R ? q : nullptr, r, lanes, part, active, mul);
-        if (!careful) w.template softmax<false>(lanes, r, active, pos, bits, f);
+        if (pass == 0) w.template softmax<false>(lanes, r, active, pos, bits, f);
         else w.template softmax<true>(lanes, r, active, pos, bits, f);
       } else if (scaler) {
         w.rescale(lanes);
       } else if (warp == SCORES) {
         w.scores(segment);
-      } else if (warp == SUMS) {
-        w.sums();
       } else {
-        w.load(loader, lane);
+        w.sums();
       }
       ++segment;
       w.tile0 += g.t1 - g.t0;
-      __syncthreads();  // the sums are complete, and the rows' factors there
+      others_sync();  // the sums are complete, and the rows' factors there
       tc_fence_after();
-      if (warp < 16) {
-        const int d = mb * 128 + r;
-        float* to = p.part + static_cast<int64_t>(slot) * p.rows * C + d;
+      if (warp != 16 && warp != 17) {
+        // a warp's lanes are 32 of each 128 dims; loaders are not there, so of the upper ones two warps each take half of the
+        // columns, of the lower ones the softmax warps a quarter
+        const int of = (warp & 2) ? 2 : 4, span = NR * L::MB / of, col0 = ((warp & 2) ? warp >> 4 : part) * span;
         bool bad = false;
 #pragma unroll 1
-        for (int c = 0; c < SPAN && c0 + c < R; c += 8) {
+        for (int c = col0; c < col0 + span; c += 8) {
+          const int c0 = c % NR, d = c / NR * 128 + r;
+          if (c0 >= R) continue;
+          float* to = p.part + static_cast<int64_t>(slot) * p.rows * C + d;
           uint32_t v[8];
-          tmem_ld8(tb + lanes + L::CO + col0 + c, v);
+          tmem_ld8(tb + lanes + L::CO + c, v);
           tmem_wait_ld();
           tie(v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int rr = c0 + c + e;
+            const int rr = c0 + e;
             if (rr < R) {
               const float x = bars.seen[rr] ? __uint_as_float(v[e]) : 0.0f;
               bad |= !finite(x);
@@ -759,24 +796,26 @@ __global__ void __launch_bounds__(LTH, 1) latent_kernel(const __grid_constant__ 
           }
           __syncwarp();
         }
-        if (bad && !careful) bars.bad = 1;
-      } else if (!whole && threadIdx.x - 512 < R) {
+        if (bad && pass == 0) {
+          bars.bad = 1;
+          atomicOr(&bars.flags[name >> 5], 1u << (name & 31));
+        }
+      }
+      if (scaler && !whole && threadIdx.x - 512 < R) {
         const int rr = threadIdx.x - 512;
         *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * p.rows + rr) * 2) =
             make_float2(bars.seen[rr] ? bars.m[rr] : -INFINITY, bars.weight[rr]);
       }
       tc_fence_before();
-      __syncthreads();  // what lies in shared and tensor memory is read
+      others_sync();  // what lies in shared and tensor memory is read
       tc_fence_after();
-      if (careful || !bars.bad) break;
-      if (softmax && part == 0) bars.m[r] = pos < 0 ? INFINITY : -INFINITY;
-      __syncthreads();
-      if (threadIdx.x == 0) bars.bad = 0;
     }
     tile0 = w.tile0;
     ok = w.ok;
     u = end;
   }
+  copy_commit();
+  copy_wait<0>();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -861,6 +900,11 @@ cudaError_t launch_latent(const LatentArgs& x, cudaStream_t st) {
   p.rows = l.rows;
   p.RT = (x.T * x.H + p.rows - 1) / p.rows;
   p.ranges = attn::ranges();
+  // Row tiles side by side read the same vectors at the same time, so the second one finds them in L2 (64 sequences of 4096
+  // positions, 128 heads, bf16: 140 us; one after the other 145), but only where next to no SM is left over by it (8 x 16
+  // tokens of 64 heads, 16 row tiles on 144 of 152 SMs: 248 us; one after the other 240).
+  p.abreast = p.ranges % p.RT <= 2 ? p.RT : 1;
+  p.ranges -= p.ranges % p.abreast;
   p.by_item = static_cast<int64_t>(x.B) * p.RT <= p.ranges;
   uint8_t* ws = static_cast<uint8_t*>(x.ws);
   p.split = reinterpret_cast<attn::Split*>(ws);

@@ -382,6 +382,32 @@ def test_latent_attn_more_sequences_than_ranges_and_one_split(dtype):
     check_latent(P, latent_q(332, 2, 8, 288, 7), [trees(1, 2, b)[0] for b in range(332)])
 
 
+@pytest.mark.parametrize("dtype,every,longer", [(BF16, 7, 400), (F8, 13, 90)])
+def test_latent_attn_many_short_segments_between_longer_ones(dtype, every, longer):
+    """Ranges of a dozen segments, most of one tile."""
+    lens = [longer + b % 40 if b % every == 0 else 1 + b % 45 for b in range(1500)]
+    P = Latent(lens, 256, 32, 16, dtype, seed=every)
+    check_latent(P, latent_q(1500, 1, 3, 288, every))
+
+
+def test_latent_attn_bad_vectors_in_some_of_many_segments():
+    """Sequences with a vector that is not finite, which their newest token alone sees: their segments run twice, and the others
+    of the range are as they are without."""
+    lens = [2 + b % 70 for b in range(1100)]
+    P = Latent(lens, 256, 32, 16, BF16, seed=3)
+    q = latent_q(1100, 2, 3, 288, 4)
+    clean = check_latent(P, q)
+    hit = [b for b in range(1100) if b % 5 == 0 or 600 < b < 630]
+    for b in hit:
+        j = lens[b] - 1
+        P.c[int(P.table[b, j // 16]), j % 16, b % 256] = float("nan")
+    ws = kq.latent_attn_workspace(P.cache, 1100, 2, 3)
+    out = kq.latent_attn(P.cache, P.table, P.seq_lens, q, ws, (128 + 32) ** -0.5)
+    keep = torch.ones((1100, 2), dtype=torch.bool, device="cuda")
+    keep[hit, 1] = False
+    assert torch.equal(out[keep], clean[keep]) and out[~keep].isnan().all()
+
+
 def test_latent_attn_one_workspace_for_calls_of_all_shapes():
     """In turn, on one stream, what the largest call asked for: with and without a tree, few and many rows, splits or none."""
     P = Latent([3000, 5, 0, 64, 900, 17], 512, 64, 16, BF16, seed=5)

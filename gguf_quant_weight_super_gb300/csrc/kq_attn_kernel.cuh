@@ -56,6 +56,13 @@
 // 0 * NaN if it is not finite: a warp whose sums are not all finite runs its
 // part again, taking those values out of the product and adding each to the
 // rows that see it.
+//
+// TREE: the newest tokens are a tree, whose masks say what a row sees of them;
+// tiles that end before them are as above.  Parts then stay in the workspace for
+// a second launch (kq_join.cuh), since a tree's rows are many and one SM's time to
+// join them showed: 16 nodes of 4 heads a group over 1000 positions, 8 heads of
+// 128, 15 us in place of 30.  4 x 24 nodes, window 4096, e4m3, heads of 256, fp32
+// q: 43 us.
 #pragma once
 
 #include "kq_cache.h"

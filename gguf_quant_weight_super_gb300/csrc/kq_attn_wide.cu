@@ -28,6 +28,12 @@
 //    A row's maximum is raised, and its sums in tensor memory scaled down, only
 //    when it grows by more than 2^8 (the weights stay below 2^8 and the sums
 //    exact); warps without rows pass.
+// TREE: masks, and parts joined by a second launch, as in kq_attn_kernel.cuh; a
+// row's maximum may lag by 2^24, since of 128 rows one grows by 2^8 in every
+// fourth tile, and a scaling takes a tile's time (weights have bf16's range, their
+// parts and sums fp32's).  8 x 61 nodes of 4 heads a group, 0 to 6007 positions, 8
+// heads of 128: 72 us, of which the join is 9.
+//
 // Every wait is bounded: one that gives up sets the device error word, after
 // which the CTA's roles run through without waiting.
 //

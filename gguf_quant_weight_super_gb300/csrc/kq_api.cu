@@ -501,7 +501,9 @@ static kq_status attn(const kq_kv_cache* cache, const int32_t* page_table, int64
   a.G = n_q_heads / cache->n_kv_heads;
   a.page_shift = log2_of(cache->page_size);
   a.room = static_cast<int>(min_i64(max_pages << a.page_shift, kMaxPositions));
-  a.window = window < a.room ? window : 0;  // a window of all positions cuts nothing; position - window stays in 32 bits
+  // a window of all positions cuts nothing (of a tree: one of more, as padding stands before them); position - window stays in
+  // 32 bits
+  a.window = window < a.room + (tree ? 1 : 0) ? window : 0;
   a.ws = workspace;
   a.err = device_error_ptr();
   a.tree = tree;

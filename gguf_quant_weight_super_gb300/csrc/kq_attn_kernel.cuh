@@ -210,20 +210,34 @@ __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0
 
 // ---- trees of drafted tokens
 
-// What token t of a tree sees of the drafted tokens, and its position (-1: padding).  With a window the tokens too far
-// before it in the tree are taken out.
+// What token t of a tree sees of the drafted tokens, and its position (-1: padding).  With a window the tokens behind it are
+// taken out: padding, which stands at -1 wherever a bit names it, and tokens too far up the tree.  Whole warps call: which
+// tokens are padding their lanes find together, in the time of the token's own mask (each token's masks by itself: 4 x 24
+// nodes, window 4096, 0.6 us of 43).
 struct TreeToken {
   uint64_t bits;
   int pos;
   __device__ __forceinline__ TreeToken(const AttnArgs& a, int b, int t, int len) {
     const uint64_t* masks = a.tree + static_cast<int64_t>(b) * a.T;
-    bits = tree_bits(__ldg(masks + t), a.T, t, len);
+    auto bits_of = [&](int u) { return tree_bits(__ldg(masks + u), a.T, u, len); };
+    uint64_t token = ~0ull;  // those that are no padding
+    if (a.window > 0) {
+      const int lane = threadIdx.x & 31;
+      const uint32_t lower = __ballot_sync(0xFFFFFFFFu, lane < a.T && bits_of(min(lane, a.T - 1)) != 0);
+      const uint32_t upper = __ballot_sync(0xFFFFFFFFu, lane + 32 < a.T && bits_of(min(lane + 32, a.T - 1)) != 0);
+      token = static_cast<uint64_t>(upper) << 32 | lower;
+    }
+    bits = bits_of(t);
     pos = tree_position(bits, a.T, len);
-    if (a.window > 0 && __popcll(bits) > a.window)
-      for (uint64_t rest = bits; rest != 0; rest &= rest - 1) {
-        const int u = __ffsll(static_cast<long long>(rest)) - 1;
-        if (tree_position(tree_bits(__ldg(masks + u), a.T, u, len), a.T, len) <= pos - a.window) bits &= ~(1ull << u);
-      }
+    if (a.window > 0 && pos - a.window >= -1) {
+      const int n = __popcll(bits);
+      bits &= token;
+      if (n > a.window)  // (as many tokens as the window has can stand after the context)
+        for (uint64_t rest = bits; rest != 0; rest &= rest - 1) {
+          const int u = __ffsll(static_cast<long long>(rest)) - 1;
+          if (tree_position(bits_of(u), a.T, len) <= pos - a.window) bits &= ~(1ull << u);
+        }
+    }
   }
 };
 
@@ -903,10 +917,12 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
 
     stage_q<Q, C, D, NT>(p, qsm, rscale, it.b, it.hk, r0, warp, lane);
     __shared__ TreeRows<TREE ? K::ROWS : 1> rows;
-    if (TREE && threadIdx.x < K::ROWS) {
-      const TreeToken x(a, it.b, min((r0 + static_cast<int>(threadIdx.x)) / a.G, a.T - 1), g.len);
-      rows.bits[threadIdx.x] = x.bits;
-      rows.pos[threadIdx.x] = x.pos;
+    if (TREE && warp == 0) {
+      const TreeToken x(a, it.b, min((r0 + lane) / a.G, a.T - 1), g.len);
+      if (lane < K::ROWS) {
+        rows.bits[lane] = x.bits;
+        rows.pos[lane] = x.pos;
+      }
     }
     __syncthreads();
     int pos[NT][2];

@@ -542,6 +542,9 @@ kq_status kq_selftest_attn_ctas(const kq_kv_cache *cache, int64_t B, int64_t T, 
  * is base + (the bits set) - 1: what it sees stands in a row after the context.
  * Bits u >= T, and those of slots before the sequence's start, do not count; a
  * token without bits, or in such a slot, is padding.  tree [B][T], 8-byte aligned.
+ * Padding stands before all positions, at -1.  A bit that names padding counts as
+ * any other and shows what its slot holds, which kq_kv_append_tree did not write;
+ * with a window, only if that reaches to before the sequence's start.
  *
  * kq_kv_append_tree: kq_kv_append, with the rotation of each token's position.
  * T in 1..64 (else KQ_ERR_UNSUPPORTED).

@@ -189,6 +189,30 @@ def test_attn_tree_sets_of_bits_that_are_no_ancestors():
     check_tree(P, masks, rand_q(4, T, 8, 64, BF16, 3))
 
 
+def padded_masks(r, T):
+    """Any bits, few or many of them, a third of the tokens padding that others' bits name."""
+    few = r.integers(0, 2, T)
+    m = [int(r.integers(0, 2 ** 63) & (r.integers(0, 2 ** 63) if f else 2 ** 63 - 1)) & (1 << T) - 1 for f in few]
+    return [0 if r.random() < 0.33 else x for x in m]
+
+
+@pytest.mark.parametrize("q_dtype,dtype,D,G", [(BF16, BF16, 64, 1), (F32, F8, 128, 2), (BF16, BF16, 128, 4)])
+@pytest.mark.parametrize("window", [1, 2, 3, 9, 16, 20, 21, 40, 57, 60, 61, 300, 319, 320, 1000])
+def test_attn_tree_windows_and_bits_that_name_padding(q_dtype, dtype, D, G, window):
+    """Padding stands at position -1: behind every window that ends after the sequence's start, however many bits a mask has.
+    With four heads a group the call goes to the kernel of 128 rows."""
+    r, T, lens = np.random.default_rng(window + G), 20, [60, 20, 19, 320]
+    masks = [padded_masks(r, T) for _ in lens]
+    masks[0][:6] = [1, 3, 0, 7, 0b10111, 0b101]
+    masks[1][:3] = [0, 3, 7]
+    masks[3][5] = (1 << T) - 1  # the newest position that there can be
+    P = Paged(lens, 2, D, 16, dtype, seed=window)
+    q = rand_q(4, T, 2 * G, D, q_dtype, window)
+    check_tree(P, masks, q, window=window)
+    P.table = P.table[:, :-1].contiguous()  # room for 320 positions, and no more
+    check_tree(P, masks, q, window=window)
+
+
 # ---- append
 
 def append_ref(P, masks, q, k, v, cs, rot, inter, wq, wk, off, eps):

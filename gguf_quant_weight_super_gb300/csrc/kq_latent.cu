@@ -45,16 +45,20 @@
 // Precision: q and the cache enter exactly (an e4m3 cache as fp16 values, with q
 // scaled by a power of two per row: 2^-38 of the row's largest).  Weights enter
 // the second product as bf16, 2^-8 of each (fp16 beside an e4m3 cache, 2^-11, or
-// 2^-29 of the row's largest): independent errors, which in the sum stay below the
-// result's own rounding to bf16, while a second part would be half as many
-// products again where they bound the call.  Sums, statistics and parts are fp32.
+// 2^-29 of the row's largest), and the rounded weights are the ones that are
+// summed: with p_j (1 + e_j) in both sums the result is off by
+// sum_j p_j e_j (c_j - o).  That is next to nothing for a row that one position
+// dominates (as the maximum may lag, its weight is any number, not 1: summed before
+// the rounding, it had an error of the whole row), and where many count, the e_j are
+// independent.  A second part of the weights would be half as many products again
+// where they bound the call.  Sums, statistics and parts are fp32.
 //
 // Measured on one GB300, calls in a graph: 64 sequences of 4096 positions, 16
-// heads, bf16, 68 us (4.5 TB/s; a tile is 1600 clocks, at the memory's rate, but the
+// heads, bf16, 69 us (4.4 TB/s; a tile is 1600 clocks, at the memory's rate, but the
 // first one comes 18000 clocks after the start); 128 heads 140 us (520 TFLOP/s; a
 // tile is 1800 clocks: of a stage's 8700 from one load to the next, 4000 pass until
 // its copies are there and 4500 until its sums are done, and five stages are all that
-// fits); in an e4m3 cache 90 and 196 us (four or three stages beside the raw pieces);
+// fits); in an e4m3 cache 90 and 198 us (four or three stages beside the raw pieces);
 // one of 131071 positions, 16 heads, 47 us, of which the join takes 8; one of 1000,
 // 15 us.
 //
@@ -544,9 +548,8 @@ struct Latent {
 #pragma unroll
         for (int e = 0; e < HC; e += 2) {
           const float2 x = ffma2(make_float2(s[e], s[e + 1]), sc, off);
-          const float2 y = make_float2(ex2(x.x), ex2(x.y));
-          sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], y);
-          w[e / 2] = pack2<F8>(y.x, y.y);
+          w[e / 2] = pack2<F8>(ex2(x.x), ex2(x.y));
+          sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], unpack2<F8>(w[e / 2]));  // of the weights as they are multiplied
         }
         if (r < NR) {
           uint8_t* line = ps + wg * L::P + r * 128;

@@ -655,7 +655,9 @@ kq_status kq_latent_append(const kq_latent_cache *cache, const int32_t *page_tab
  *   out [B*T][n_heads][latent_dim] KQ_BF16
  * Scores, softmax statistics, sums and partial results are held in fp32; the
  * weights enter their product as bf16 (2^-8 of each; beside an e4m3 cache as fp16,
- * 2^-11 of each or 2^-29 of the row's largest), their sum in fp32.
+ * 2^-11 of each or 2^-29 of the row's largest), and the fp32 sum that they are
+ * divided by is that of the rounded ones: with p_j (1 + e_j) in place of p_j, out is
+ * off by sum p_j e_j (c_j - out).
  * Repeated calls give identical outputs.  workspace: kq_latent_attn_workspace_size
  * bytes, 256-byte aligned, zero-filled once before first use; one call at a time
  * per workspace; a workspace serves any calls of kq_latent_attn that it is large

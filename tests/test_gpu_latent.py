@@ -464,3 +464,65 @@ def test_latent_attn_queries_far_from_one(dtype, power):
     """Queries and a scale whose product is an ordinary one's."""
     P = Latent([700, 64, 5], 512, 64, 16, dtype, seed=2)
     check_latent(P, latent_q(3, 2, 16, 576, 3, mul=1.4 * 2.0 ** power), scale=0.07 * 2.0 ** -power)
+
+
+# ---- the weights' rounding
+
+def closely(P, q, masks=None, scale=None):
+    """Weights are rounded once, and it is the rounded ones that are summed: with p_j (1 + e_j) in both sums the result is off
+    by sum_j p_j e_j (c_j - out), |e_j| <= 2^-8 as bf16, 2^-11 (or 2^-29 of the row's largest weight) as fp16 beside an e4m3
+    cache.  The rest as above, and the weights' fp32 sum, (n/64 + 32) 2^-24."""
+    B, T, H, W = q.shape
+    scale = (128 + P.R) ** -0.5 if scale is None else scale
+    f8 = P.c.dtype == F8
+    unit, least = (2.0 ** -11, 2.0 ** -29) if f8 else (2.0 ** -8, 0.0)
+    out = kq.latent_attn(P.cache, P.table, P.seq_lens, q, kq.latent_attn_workspace(P.cache, B, T, H), scale,
+                         tree=None if masks is None else to_tensor(masks))
+    got, qn, square, bound = f64(out.float()), f64(q.float()), 0.0, 0.0
+    for b in range(B):
+        c = P.dense(b)
+        for t, cols in enumerate(columns(None if masks is None else masks[b], P.lens[b], T)):
+            if not cols:
+                continue
+            k, n = c[cols], len(cols)
+            s = qn[b, t] @ k.T * scale
+            ds = (W + 8) * 2.0 ** -23 * abs(scale) * np.max(np.abs(qn[b, t]) @ np.abs(k).T, axis=1)[:, None]
+            p = np.exp(s - s.max(1, keepdims=True))
+            weights = p.sum(1, keepdims=True)
+            v = k[:, :P.C]
+            ref, sv = p @ v / weights, p @ np.abs(v) / weights
+            off = np.abs(v[None] - ref[:, None])  # |c_j - out|
+            spread = (np.einsum("hj,hjd->hd", p, off) * unit + least * off.sum(1)) / weights
+            rest = 2 * ds + 2.0 ** -20 + (n / 8 + 128) * 2.0 ** -23 + (n / 64 + 32) * 2.0 ** -24
+            err = np.abs(got[b, t] - ref)
+            tol = (spread + rest * sv) * (1 + 2.0 ** -7) + 2.0 ** -8 * np.abs(ref)
+            assert np.all(np.isfinite(err)) and np.all(err <= tol), (b, t, float(np.nanmax(err / tol)))
+            square += (err ** 2).sum()
+            # of a rounding to bf16, a step of up to 2^-7 of the value: step / sqrt(12) in the mean square
+            bound += ((2.0 ** -8 / 3 ** 0.5 * np.abs(ref) + spread + rest * sv) ** 2).sum()
+    assert square <= bound, (square / bound) ** 0.5
+
+
+@pytest.mark.parametrize("dtype", [BF16, F8])
+@pytest.mark.parametrize("C,R,T,H,tree", [(512, 64, 1, 16, False), (256, 32, 1, 40, False), (512, 64, 9, 16, True), (512, 32, 3, 5, False)])
+def test_latent_attn_rounds_each_weight_once(dtype, C, R, T, H, tree):
+    lens = [700, T, 90, 0, 333]
+    P = Latent(lens, C, R, 16, dtype, seed=C + H)
+    closely(P, latent_q(5, T, H, C + R, T + H), trees(5, T, T + 2) if tree else None)
+
+
+@pytest.mark.parametrize("dtype,n,per_sm", [(BF16, 64, 2), (BF16, 500, 1), (F8, 64, 2)])
+@pytest.mark.parametrize("late", [33, 50, 63])
+def test_latent_attn_a_late_position_that_dominates(dtype, n, per_sm, late):
+    """A position behind the first tile, by powers of two (that are not whole numbers) which do not raise the row's maximum: its
+    weight is any number, and that number's rounding is not the result's.  As many sequences as leave each one whole."""
+    B = per_sm * torch.cuda.get_device_properties(0).multi_processor_count
+    P = Latent([n] * B, 512, 64, 16, dtype, seed=late)
+    j = torch.arange(n, device="cuda")
+    pages = P.table.long()[:, j // 16]
+    P.c[pages, j % 16, 512] = torch.zeros((B, n), device="cuda").to(dtype)
+    P.c[pages[:, late], late % 16, 512] = torch.full((B,), 1 / P.scale, device="cuda").to(dtype)
+    most = 10.9 if dtype == F8 else 23.9
+    q = torch.zeros((B, 1, 6, 576), device="cuda")
+    q[..., 512] = (torch.linspace(0.5, 1.0, 6 * B, device="cuda") * most * 0.6931471805599453).view(B, 1, 6)
+    closely(P, q.to(BF16), scale=1.0)

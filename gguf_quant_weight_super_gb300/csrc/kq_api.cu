@@ -467,11 +467,12 @@ size_t kq_attn_tree_workspace_size(const kq_kv_cache* cache, int64_t B, int64_t 
   return most;
 }
 
+// most: tokens of a sequence that the call takes.  (An empty batch's tree may be NULL, so tree does not say which call it is.)
 static kq_status attn(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages, const int32_t* seq_lens,
-                      const uint64_t* tree, int64_t B, int64_t T, const void* q, int q_dtype, int64_t q_stride,
+                      const uint64_t* tree, int most, int64_t B, int64_t T, const void* q, int q_dtype, int64_t q_stride,
                       int32_t n_q_heads, float scale, float softcap, int32_t window, void* out, void* workspace,
                       size_t workspace_bytes, kq_stream_t stream) {
-  const kq_status cs = check_attn(cache, B, T, n_q_heads, tree ? kMaxTree : 16);
+  const kq_status cs = check_attn(cache, B, T, n_q_heads, most);
   if (cs != KQ_OK) return cs;
   if (!float_dtype(q_dtype) || max_pages < 0 || window < 0 || !(softcap == 0.0f || good_scale(softcap)) ||
       !good_scale(scale == 0.0f ? 1.0f : fabsf(scale)))
@@ -517,8 +518,8 @@ kq_status kq_attn_decode(const kq_kv_cache* cache, const int32_t* page_table, in
                          const int32_t* seq_lens, int64_t B, int64_t T, const void* q, int q_dtype, int64_t q_stride,
                          int32_t n_q_heads, float scale, float softcap, int32_t window, void* out, void* workspace,
                          size_t workspace_bytes, kq_stream_t stream) {
-  return attn(cache, page_table, max_pages, seq_lens, nullptr, B, T, q, q_dtype, q_stride, n_q_heads, scale, softcap, window,
-              out, workspace, workspace_bytes, stream);
+  return attn(cache, page_table, max_pages, seq_lens, nullptr, 16, B, T, q, q_dtype, q_stride, n_q_heads, scale, softcap,
+              window, out, workspace, workspace_bytes, stream);
 }
 
 kq_status kq_attn_tree(const kq_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
@@ -527,8 +528,8 @@ kq_status kq_attn_tree(const kq_kv_cache* cache, const int32_t* page_table, int6
                        void* workspace, size_t workspace_bytes, kq_stream_t stream) {
   const kq_status ts = check_tree(tree, B, T);
   if (ts != KQ_OK) return ts;
-  return attn(cache, page_table, max_pages, seq_lens, tree, B, T, q, q_dtype, q_stride, n_q_heads, scale, softcap, window,
-              out, workspace, workspace_bytes, stream);
+  return attn(cache, page_table, max_pages, seq_lens, tree, kMaxTree, B, T, q, q_dtype, q_stride, n_q_heads, scale, softcap,
+              window, out, workspace, workspace_bytes, stream);
 }
 
 static kq_status check_latent(const kq_latent_cache* c) {

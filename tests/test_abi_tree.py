@@ -161,3 +161,16 @@ def test_binding_refusals(L):  # noqa: F811
         kq.tree_accept(kq.CacheSet([]), table, lens, tree, words.long(), words)
     with pytest.raises(ValueError):
         kq.tree_accept(kq.CacheSet([]), table, lens, tree, words, words)  # host tensors
+
+
+def test_an_empty_batch_takes_every_length_that_a_tree_can_have(L):  # noqa: F811
+    """An empty tensor's address is NULL."""
+    c, r = cache(), rope()
+    c_ref, r_ref = ctypes.addressof(c), ctypes.addressof(r)
+    for tree in (None, F):
+        for T in (0, 1, 16, 17, 61, 64):
+            assert L.kq_attn_tree(c_ref, F, 4, F, tree, 0, T, F, 1, 1024, 8, 0.1, 0.0, 0, F, F, 1 << 40, None) == 0, (tree, T)
+            assert L.kq_kv_append_tree(c_ref, F, 4, F, tree, 0, T, F, F, F, 1, 1024, 256, 256, 8, r_ref, F, 1, None) == 0
+            assert L.kq_tree_accept(c_ref, 1, F, 4, F, tree, F, F, 0, T, F, F, F, F + 64, None) == 0
+        assert L.kq_attn_tree(c_ref, F, 4, F, tree, 0, 65, F, 1, 1024, 8, 0.1, 0.0, 0, F, F, 1 << 40, None) == UNSUPPORTED
+    assert L.kq_attn_decode(c_ref, F, 4, F, 0, 17, F, 1, 1024, 8, 0.1, 0.0, 0, F, F, 1 << 40, None) == UNSUPPORTED

@@ -448,7 +448,7 @@ static kq_status check_attn(const kq_kv_cache* cache, int64_t B, int64_t T, int3
   const kq_status cs = check_cache(cache);
   if (cs != KQ_OK) return cs;
   if (B < 0 || T < 0 || n_q_heads <= 0 || n_q_heads % cache->n_kv_heads) return KQ_ERR_ARG;
-  if (B > 4096 || T > most || n_q_heads / cache->n_kv_heads > 16) return KQ_ERR_UNSUPPORTED;
+  if (B > kMaxSeqs || T > most || n_q_heads / cache->n_kv_heads > 16) return KQ_ERR_UNSUPPORTED;
   return KQ_OK;
 }
 
@@ -707,7 +707,7 @@ static kq_status check_latent_attn(const kq_latent_cache* cache, int64_t B, int6
   const kq_status cs = check_latent(cache);
   if (cs != KQ_OK) return cs;
   if (B < 0 || T < 0 || n_heads <= 0) return KQ_ERR_ARG;
-  return B > 4096 || T > kMaxTree || n_heads > 256 ? KQ_ERR_UNSUPPORTED : KQ_OK;
+  return B > kMaxSeqs || T > kMaxTree || n_heads > 256 ? KQ_ERR_UNSUPPORTED : KQ_OK;
 }
 
 size_t kq_latent_attn_workspace_size(const kq_latent_cache* cache, int64_t B, int64_t T, int32_t n_heads) {

@@ -1009,13 +1009,14 @@ cudaError_t launch_one(const Params& p, cudaStream_t st, AttnShape* ask) {
   using K = Cfg<Q, C, D, NT>;
   const size_t smem = K::SMEM + 4 * (static_cast<size_t>(p.a.B) + 1);
   static size_t fits[64] = {0};  // shared memory with which CPS CTAs are known to be resident, per device
-  static int set[64] = {0};  // shared memory allowed so far, per device
+  static bool set[64] = {false};
   const int dev = current_device_id();
-  if (set[dev] < static_cast<int>(smem)) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_kernel<Q, C, D, NT, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+  if (!set[dev]) {  // for all calls: one at the same time may want less
+    constexpr int most = K::SMEM + 4 * (kMaxSeqs + 1);
+    static_assert(most + 2048 <= kMaxSmemPerBlock, "beside the static memory");
+    const cudaError_t e = cudaFuncSetAttribute(attn_kernel<Q, C, D, NT, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
-    set[dev] = static_cast<int>(smem);
+    set[dev] = true;
   }
   // one range per CTA, all of them resident: one that waits for another's place would start when that one has ended
   int ctas = K::CPS;

@@ -546,12 +546,14 @@ template <int D, bool TREE>
 cudaError_t launch_d(const Params& p, cudaStream_t st, AttnShape* ask) {
   using W = WCfg<D>;
   const size_t smem = W::SMEM + 4 * (static_cast<size_t>(p.a.B) + 1);
-  static int set[64] = {0};
+  static bool set[64] = {false};
   const int dev = current_device_id();
-  if (set[dev] < static_cast<int>(smem)) {
-    const cudaError_t e = cudaFuncSetAttribute(wide_kernel<D, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (!set[dev]) {  // for all calls: one at the same time may want less
+    constexpr int most = W::SMEM + 4 * (kMaxSeqs + 1);
+    static_assert(most + 14 * 1024 <= kMaxSmemPerBlock, "beside the static memory");
+    const cudaError_t e = cudaFuncSetAttribute(wide_kernel<D, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
-    set[dev] = static_cast<int>(smem);
+    set[dev] = true;
   }
   if (ask) {
     ask->planned = 1;

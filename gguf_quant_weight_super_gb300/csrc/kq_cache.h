@@ -71,6 +71,7 @@ struct AttnArgs {
   int* err;
   const uint64_t* tree;  // [B][T] masks, or NULL: a chain
 };
+constexpr int kMaxSeqs = 4096;  // sequences of an attention call, whose place in the line of tiles lies in shared memory
 // Positions are counted in 32 bits, tiles and copies ahead of the last one included.
 constexpr int64_t kMaxPositions = INT32_MAX - 4095;
 size_t attn_workspace_bytes(int head_dim, int Hkv, int64_t T, int Hq);

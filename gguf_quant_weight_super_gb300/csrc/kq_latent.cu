@@ -102,7 +102,7 @@ struct LCfg {
   static constexpr int smem(int stages, int B) { return QS + 2 * P + stages * STAGE + NLOAD * RAW + 4 * (B + 1); }
   static constexpr int ROOM = 227 * 1024 - 4096;      // less the static memory
   static constexpr int LEAST = F8 ? 3 : 4;            // stages
-  static_assert(smem(LEAST, 4096) <= ROOM);
+  static_assert(smem(LEAST, kMaxSeqs) <= ROOM);
   // tensor memory columns: o, q, S x 2
   static constexpr int MB = C / 128, CO = 0, CQ = C == 256 ? 256 : NR == 64 ? 256 : 128, CS = 448, COLS = 512;
   static_assert(MB * NR <= CQ && CQ + 32 * QT <= CS && CS + 2 * LT <= COLS);

@@ -259,11 +259,19 @@ struct Seg {
   int t0, t1;
 };
 
-template <class Q, class C, int D, int NT, bool TREE>
-struct Warp {
-  using K = Cfg<Q, C, D, NT>;
-  const uint64_t* tree;  // trees: the rows' bits, in shared memory
+// What a warp keeps of a tree: the rows' bits, in shared memory, and the position of the first new token's slot.  (Nothing in
+// a chain's warps, whose values the careful run holds in memory.)
+template <bool TREE>
+struct WarpTree {
+  const uint64_t* tree;
+  int first_new;
+};
+template <>
+struct WarpTree<false> {};
 
+template <class Q, class C, int D, int NT, bool TREE>
+struct Warp : WarpTree<TREE> {
+  using K = Cfg<Q, C, D, NT>;
   // o[n][d]: dims 16 d + ... (M) of rows 8 n + ... (N): registers 0, 1 of the lane's first dim, 2, 3 of its second, for rows
   // 8 n + 2 (lane & 3) and + 1
   float o[NT][D / 16][4];
@@ -431,7 +439,7 @@ struct Warp {
         l[n][e] += s[n][e] + s[n][2 + e];
       }
     }
-    if constexpr (CAREFUL) take_out(p, g.len - a.T, vrow, base, s, pos, lane);
+    if constexpr (CAREFUL) take_out(p, vrow, base, s, pos, lane);
     // ---- sums
     uint32_t w[NT][K::NP][2];  // positions 0-7 and 8-15, as the second operand
 #pragma unroll
@@ -496,11 +504,15 @@ struct Warp {
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[d]);
   }
   __device__ __forceinline__ uint64_t bits_of(int n, int e, int lane) const {
-    if constexpr (TREE) return tree[8 * n + 2 * (lane & 3) + e];
+    if constexpr (TREE) return this->tree[8 * n + 2 * (lane & 3) + e];
+    else return 0;
+  }
+  __device__ __forceinline__ int new_from() const {
+    if constexpr (TREE) return this->first_new;
     else return 0;
   }
   // Adds the values that are not finite to the rows that see them, and puts zeros in their place.
-  __device__ __noinline__ void take_out(const Params& p, int first_new, uint8_t* vrow, int base, const float (&s)[NT][4],
+  __device__ __noinline__ void take_out(const Params& p, uint8_t* vrow, int base, const float (&s)[NT][4],
                                         const int (&pos)[NT][2], int lane) {
     for (int jj = 0; jj < WT; ++jj) {
       const int j = base + jj, from = (jj & 7) * 4 + (lane & 3);
@@ -509,7 +521,7 @@ struct Warp {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float w = __shfl_sync(0xFFFFFFFFu, jj & 8 ? s[n][2 + e] : s[n][e], from);
-          const bool seen = sees<TREE>(j, pos[n][e], bits_of(n, e, lane), first_new, p.a.window);
+          const bool seen = sees<TREE>(j, pos[n][e], bits_of(n, e, lane), new_from(), p.a.window);
 #pragma unroll
           for (int d = 0; d < D / 16; ++d)
 #pragma unroll
@@ -916,7 +928,7 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
     g.t1 = end - it.i0 + g.first / TK;
 
     stage_q<Q, C, D, NT>(p, qsm, rscale, it.b, it.hk, r0, warp, lane);
-    __shared__ TreeRows<TREE ? K::ROWS : 1> rows;
+    __shared__ TreeRows<TREE ? K::ROWS : 1> rows;  // (a chain's kernels have none)
     if (TREE && warp == 0) {
       const TreeToken x(a, it.b, min((r0 + lane) / a.G, a.T - 1), g.len);
       if (lane < K::ROWS) {
@@ -938,12 +950,12 @@ __global__ void __launch_bounds__(NTH, (Cfg<Q, C, D, NT>::CPS)) attn_kernel(cons
         qs[n][e] = f * rscale[r];
       }
     Warp<Q, C, D, NT, TREE> w;
-    w.tree = rows.bits;
+    if constexpr (TREE) w.tree = rows.bits, w.first_new = g.len - a.T;
     uint8_t* mine = ring + warp * (K::S * K::STAGE);
     w.template run<false>(p, g, mine, smem_u32(qsm), pos, qs, warp, lane);
     if (!w.all_finite()) {
       Warp<Q, C, D, NT, TREE> again;  // an object of its own: the call in it keeps this one out of registers
-      again.tree = rows.bits;
+      if constexpr (TREE) again.tree = rows.bits, again.first_new = g.len - a.T;
       again.template run<true>(p, g, mine, smem_u32(qsm), pos, qs, warp, lane);
       w = again;
     }

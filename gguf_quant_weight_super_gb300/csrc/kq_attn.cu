@@ -36,16 +36,31 @@ bool wide(int head_dim, int rows, int64_t heads, int64_t room) {
 }
 
 // Trees' parts are joined by a launch of their own, so splitting a head costs less.  Up to 32 rows both kernels take the same
-// time, and from 64 heads on this one less.  Above, the other one from eight heads' tiles of 128 rows on (heads of 64: 16; long
-// tables: from a quarter of that).  us, the other's time / this one's, up to 1500 and up to 6007 positions, heads of 128:
-//   heads of 128:  1 head     4         8         16        32        64
-//     64 rows     15/14 24/18  16/15 20/22  17/19 20/27  19/22 28/39  21/27 38/59  29/41 59/94
-//    128 rows     17/14 25/21  18/19 22/27  22/22 25/37  25/27 36/56  25/38 46/93  37/62 72/162
-//    244 rows     18/16 28/22  22/22 25/38  25/27 34/55  25/39 44/91  35/60 72/161 53/106 125/302
+// time, and from 64 heads on this one less.  Above, the other one from four heads' tiles of 128 rows on (heads of 64: eight),
+// and any number where the table has room for long caches.  us, the other's time / this one's, lengths from half of 1500,
+// 6007, 24000 to all of it:
+//   heads of 128:   1 head   2        4        8        16       32       64
+//   1500   64 rows  13/14    13/14    14/15    15/18    19/22    19/25    25/36
+//         128 rows  16/14    16/14    17/18    20/22    25/25    23/33    33/56
+//         244 rows  16/14    17/18    21/22    26/25    22/33    31/51    50/94
+//   6007   64 rows  15/15    15/17    16/18    18/22    24/33    32/49    50/79
+//         128 rows  17/17    18/18    18/22    23/33    32/44    40/76    64/139
+//         244 rows  18/19    19/23    23/33    33/45    36/71    61/130   108/253
+//  24000   64 rows  18/20    19/23    22/32    32/48    48/72
+//         244 rows  22/32    24/46    38/74    63/125   90/213
+//   heads of 64:
+//   1500   64 rows  12/11    12/12    13/12    14/15    17/18    19/21    24/28
+//         128 rows  13/12    14/12    14/14    18/18    23/21    21/26    27/39
+//         244 rows  14/12    14/15    19/18    23/21    21/27    27/39    40/65
+//   6007   64 rows  13/12    14/14    14/15    16/18    22/25    29/36    44/59
+//         128 rows  15/14    15/15    16/18    20/25    28/34    33/55    52/98
+//         244 rows  15/15    17/18    21/25    30/36    32/52    50/93    89/181
+//  24000   64 rows  16/17    16/18    19/23    26/34    40/53    68/93    122/170
+//         244 rows  18/24    21/34    32/54    52/90    76/157   142/306  277/615
 bool wide_tree(int head_dim, int rows, int64_t heads, int64_t room) {
   if (!could_be_wide(head_dim, rows) || rows <= 32) return false;
   const int64_t tiles = heads * ((rows + kWideRows - 1) / kWideRows);
-  return (room > 16384 ? 4 : 1) * tiles >= (head_dim == 128 ? 8 : 16);
+  return room > 16384 || tiles >= (head_dim == 128 ? 4 : 8);
 }
 
 struct Layout {

@@ -903,9 +903,13 @@ cudaError_t launch_latent(const LatentArgs& x, cudaStream_t st) {
   p.rows = l.rows;
   p.RT = (x.T * x.H + p.rows - 1) / p.rows;
   p.ranges = attn::ranges();
-  // Row tiles side by side read the same vectors at the same time, so the second one finds them in L2 (64 sequences of 4096
-  // positions, 128 heads, bf16: 140 us; one after the other 145), but only where next to no SM is left over by it (8 x 16
-  // tokens of 64 heads, 16 row tiles on 144 of 152 SMs: 248 us; one after the other 240).
+  // Row tiles side by side read the same vectors at the same time, so the second one finds them in L2, but only where next to
+  // no SM is left over by it.  us, side by side / one after the other, bf16:
+  //   no SM over    2 row tiles: 1000 positions 22.6/22.9, 131071 70.9/73.1, 64 x 4096 141/147, 256 x 500 138/141
+  //                 4: 16 x 8192 124.5/129.3   8: 8 x 8192 123.8/126.7   19: 4 x 8192 142.2/142.4
+  //   2 SMs over    3: 16 x 8192 100.4/102.5   5: 8 x 8192 86.7/88.7   6: 99.3/101.4   10: 150.6/153.0   15: 118.6/119.9
+  //   more          7 (5 over): 113.5/113.6    9 (8): 141.4/139.7      16 (8): 235.5/228.8
+  // and beside an e4m3 cache, where the conversion is what takes time, within 1% of each other up to 2 SMs over.
   p.abreast = p.ranges % p.RT <= 2 ? p.RT : 1;
   p.ranges -= p.ranges % p.abreast;
   p.by_item = static_cast<int64_t>(x.B) * p.RT <= p.ranges;

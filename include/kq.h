@@ -626,7 +626,10 @@ kq_status kq_latent_accept(const kq_latent_cache *caches, int32_t n_caches, cons
  *            the latent gets k_norm's norm (with eps, norm_offset), the rope part
  *            the rotation of the token's position; then both go to its slot
  *   q_latent [B*T] rows of n_heads*latent_dim: the queries' products with each
- *            head's key expansion; they pass as they are
+ *            head's key expansion; they pass as they are.  (kq_moe_matvec makes
+ *            them: the heads are its experts, expert_ids 0 .. n_heads - 1 for each
+ *            row, x_per_slot 1, gate_w NULL, up to 512 (row, head) pairs a call;
+ *            and so each head's values from kq_latent_attn's out.)
  *   q_rope   head h of row i starts i*q_rope_stride + h*q_rope_head_stride
  *            elements in: rope_dim values, which are rotated
  *   x_dtype  KQ_F32 or KQ_BF16 (all three)

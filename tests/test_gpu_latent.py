@@ -15,7 +15,8 @@ import numpy as np
 import pytest
 import torch
 
-from gguf_quant_weight_super_gb300 import kq
+from gguf_quant_weight_super_gb300 import kq, synth
+from tests.gpu_util import TOL
 from tests.test_gpu_cache import BF16, F8, F32, _setup, f64  # noqa: F401
 from tests.test_gpu_tree import chain, masks_of, rounded, to_tensor, tree_columns, tree_tokens, trees, walk
 
@@ -526,3 +527,63 @@ def test_latent_attn_a_late_position_that_dominates(dtype, n, per_sm, late):
     q = torch.zeros((B, 1, 6, 576), device="cuda")
     q[..., 512] = (torch.linspace(0.5, 1.0, 6 * B, device="cuda") * most * 0.6931471805599453).view(B, 1, 6)
     closely(P, q.to(BF16), scale=1.0)
+
+
+# ---- from the products on
+
+@pytest.mark.parametrize("qtype,T,H", [(1, 1, 16), (3, 4, 20), (1, 4, 128)])
+def test_a_latent_layer_from_its_quantized_products(qtype, T, H):
+    """Queries absorbed by kq_moe_matvec, whose experts are the heads, then append, attention and each head's values by
+    kq_moe_matvec again: against attention over expanded keys and values in 64 bits.  An absorbed query is off by 2^-8 of
+    itself (its bf16) and a product's bound (tests/gpu_util.py); a score so by scale times that over sum |c|, twice that in
+    the weights, with 2^-8 for their rounding; then the result's bf16 and the values' product."""
+    C, R, N, B, page = 512, 64, 128, 512 // (T * H) if T * H > 64 else 2, 16
+    g, t = synth.rng(77, qtype, T, H), torch.Generator().manual_seed(H)
+    up, down = synth.gen_matrix(qtype, H * C, N, g), synth.gen_matrix(qtype, H * N, C, g)  # [C, N] and [N, C] per head
+    dense = []
+    for w, rows, cols in ((up, H * C, N), (down, H * N, C)):
+        full = -(-cols // 256) * 256
+        y = torch.empty(rows * full, device="cuda")
+        w = torch.from_numpy(w).cuda()
+        kq.kq_dequant(qtype, w, y, rows * full)
+        dense.append((w, f64(y.view(rows, full)[:, :cols]).reshape(H, -1, cols)))
+    lens = [T + 57 * b for b in range(B)]
+    P = Latent(lens, C, R, page, BF16, seed=H)
+    ids = torch.arange(H, dtype=torch.int32, device="cuda").repeat(B * T, 1)
+
+    def heads(w, x, n, k):
+        y = torch.empty((B * T, H, n), device="cuda")
+        ws = kq.moe_workspace(n, B * T, H, H)
+        kq.kq_moe_matvec(qtype, w, H, ids, None, x.reshape(B * T, H, k).contiguous(), kq.KQ_BF16, True, y, n, k, B * T, H, ws, ws.numel())
+        kq.kq_moe_check(ws)
+        return y.view(B, T, H, n)
+    q = torch.randn((B, T, H, N + R), generator=t).to(BF16).cuda()  # a query product's rows
+    c = torch.randn((B, T, C + R), generator=t).cuda()
+    rope = kq.RopeNorm(kq.rope_table(max(lens) + 1, R), k_norm=torch.ones(C, device="cuda"))
+    absorbed = heads(dense[0][0], q[..., :N], C, N)
+    a = kq.latent_append(P.cache, P.table, P.seq_lens, absorbed, q[..., N:].float(), c, rope)
+    size = float(absorbed.square().mean().sqrt())
+    scale = 1.0 / (size * C ** 0.5)  # scores about one
+    o = kq.latent_attn(P.cache, P.table, P.seq_lens, a, kq.latent_attn_workspace(P.cache, B, T, H), scale)
+    y = f64(heads(dense[1][0], o, N, C))
+    A, V, qn, an = dense[0][1], dense[1][1], f64(q[..., :N].float()), f64(a.float())
+    for b in range(B):
+        cc = P.dense(b)
+        for i in range(T):
+            k = cc[:lens[b] - T + i + 1]
+            lat, rot = k[:, :C], an[b, i, :, C:] @ k[:, C:].T      # (the rotated part is tested above)
+            keys = np.einsum("hcn,jc->hjn", A, lat)                # expanded
+            s = (np.einsum("hn,hjn->hj", qn[b, i], keys) + rot) * scale
+            p = np.exp(s - s.max(1, keepdims=True))
+            p /= p.sum(1, keepdims=True)
+            latents = p @ lat
+            ref = np.einsum("hnc,hc->hn", V, latents)
+            dq = 2.0 ** -8 * np.abs(an[b, i, :, :C]) * (1 + 2.0 ** -8) + TOL["bf16"] * np.einsum("hcn,hn->hc", np.abs(A), np.abs(qn[b, i]))
+            ds = scale * (dq @ np.abs(lat).T).max(1)[:, None] + 2.0 ** -12
+            sv = p @ np.abs(lat)
+            do = (np.expm1(2 * ds) + 2.0 ** -7) * sv + 2.0 ** -8 * np.abs(latents)
+            tol = np.einsum("hnc,hc->hn", np.abs(V), do + TOL["bf16"] * (np.abs(latents) + do))
+            err = np.abs(y[b, i] - ref)
+            assert np.all(err <= tol), (b, i, float((err / tol).max()))
+            # far within it, as the errors are independent: their root mean square is below a tenth of the values'
+            assert (err ** 2).mean() <= 0.01 * (ref ** 2).mean(), (b, i)

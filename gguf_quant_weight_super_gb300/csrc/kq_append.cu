@@ -26,8 +26,9 @@
 // group 53, with six 58, with 256 threads 55; a CTA per token 48, but then 28917
 // tokens of 6 heads, bf16, 46 in place of 28); one token of 48 heads 2.1 us.
 // TREE: the position that a token is rotated by comes from its mask, its slot as
-// before: 48 x 63 nodes of 48 heads of 128, bf16 into e4m3, 26 us (2.7 TB/s: 700
-// instructions a warp, issued at 62%); 16 nodes 2.4 us.
+// before: 48 x 63 nodes of 48 heads of 128, bf16 into e4m3, 26 us (2.7 TB/s; 700
+// instructions a warp, issued at 62%, and accesses of 4 and 8 bytes: neither by
+// itself is the bound); 16 nodes 2.4 us.
 #include "kq_cache.h"
 #include "kq_vec.cuh"
 

@@ -32,7 +32,7 @@
 // row's maximum may lag by 2^24, since of 128 rows one grows by 2^8 in every
 // fourth tile, and a scaling takes a tile's time (weights have bf16's range, their
 // parts and sums fp32's).  8 x 61 nodes of 4 heads a group, 0 to 6007 positions, 8
-// heads of 128: 72 us, of which the join is 9.
+// heads of 128: 72 us, of which the join is 8.
 //
 // Every wait is bounded: one that gives up sets the device error word, after
 // which the CTA's roles run through without waiting.

@@ -59,7 +59,7 @@
 // tile is 1800 clocks: of a stage's 8700 from one load to the next, 4000 pass until
 // its copies are there and 4500 until its sums are done, and five stages are all that
 // fits); in an e4m3 cache 90 and 198 us (four or three stages beside the raw pieces);
-// one of 131071 positions, 16 heads, 47 us, of which the join takes 8; one of 1000,
+// one of 131071 positions, 16 heads, 47 us, of which the join takes 10; one of 1000,
 // 15 us.
 //
 // Every wait is bounded: one that gives up sets the device error word, after

@@ -529,6 +529,16 @@ def test_latent_attn_a_late_position_that_dominates(dtype, n, per_sm, late):
     closely(P, q.to(BF16), scale=1.0)
 
 
+# ---- as many rows as a call takes
+
+@pytest.mark.parametrize("dtype,T,H", [(BF16, 64, 256), (F8, 64, 256), (BF16, 38, 256), (BF16, 59, 163), (F8, 19, 256), (BF16, 64, 119)])
+def test_latent_attn_as_many_row_tiles_as_sms_and_more(dtype, T, H):
+    """256, 152, 151 (no tile, or next to none, is left over by all of them side by side), 76 and 119 row tiles."""
+    lens = [T + 45, T, 3]
+    P = Latent(lens, 256, 32, 16, dtype, seed=T)
+    check_latent(P, latent_q(3, T, H, 288, T), [chain(T), trees(1, T, T)[0], trees(1, T, T + 1)[0]])
+
+
 # ---- from the products on
 
 @pytest.mark.parametrize("qtype,T,H", [(1, 1, 16), (3, 4, 20), (1, 4, 128)])

@@ -213,6 +213,16 @@ def test_attn_tree_windows_and_bits_that_name_padding(q_dtype, dtype, D, G, wind
     check_tree(P, masks, q, window=window)
 
 
+@pytest.mark.parametrize("q_dtype,dtype,D,G", [(F32, BF16, 128, 1), (BF16, F8, 64, 3), (BF16, BF16, 64, 4)])
+@pytest.mark.parametrize("T,window", [(33, 5), (50, 17), (50, 60), (64, 33), (64, 90)])
+def test_attn_tree_windows_and_padding_among_more_than_32_tokens(q_dtype, dtype, D, G, T, window):
+    r, lens = np.random.default_rng(window + T), [T + 40, T, T - 1, 500]
+    masks = [padded_masks(r, min(T, 62)) + [0, 5][:max(0, T - 62)] for _ in lens]
+    masks[3][T - 1] = (1 << T) - 1
+    P = Paged(lens, 2, D, 16, dtype, seed=window)
+    check_tree(P, masks, rand_q(4, T, 2 * G, D, q_dtype, window), window=window)
+
+
 # ---- append
 
 def append_ref(P, masks, q, k, v, cs, rot, inter, wq, wk, off, eps):
